@@ -17,6 +17,7 @@ FA_ERR_UNSUPPORTED = 2
 FA_ERR_WORKSPACE = 3
 FA_ERR_CUDA = 4
 FA_ERR_TIMEOUT = 5
+FA_ERR_PAGE = 6
 
 # (name, restype, argtypes) for every entry point declared in include/fa.h
 _P = ctypes.c_void_p
@@ -24,6 +25,20 @@ _I = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
 _ULL = ctypes.c_ulonglong
+
+
+class PagedCache(ctypes.Structure):
+    """fa_paged_cache."""
+    _fields_ = [("K", _P), ("V", _P), ("k_scale", _P), ("v_scale", _P), ("page_table", _P),
+                ("lens", _P), ("B", _I), ("H_kv", _I), ("d", _I), ("num_pages", _I),
+                ("page_size", _I), ("max_pages", _I)]
+
+
+_C = ctypes.POINTER(PagedCache)
+_LL2 = ctypes.c_longlong * 2   # (token, head) strides
+_LL3 = ctypes.c_longlong * 3   # (sequence, head, row) strides
+_APPEND = [_C, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _P, _I, _I, _P]
+_PAGED = [_C, _P, _P, _P, _P, _P, _I, _I, _F, _I, _I, _P, _SZ, _P]
 SIGNATURES = {
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P]),
     "fa_fwd_o32": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P]),
@@ -36,10 +51,18 @@ SIGNATURES = {
     "fa_set_timing_events": (_I, [_P, _P]),
     "fa_fwd_window": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P]),
     "fa_bwd_window": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _I, _I, _I, _I, _F, _I, _P]),
+    "fa_fwd_sinks": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _I, _P]),
+    "fa_bwd_sinks": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _I, _I, _I, _I, _F, _I, _I,
+                          _P]),
     "fa_bwd_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P]),
     "fa_fwd_fp8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _F, _F, _F, _P]),
     "fa_decode_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "fa_fwd_decode": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P]),
+    "fa_kv_append": (_I, _APPEND),
+    "fa_kv_append_fp8": (_I, _APPEND),
+    "fa_paged_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "fa_fwd_paged": (_I, _PAGED),
+    "fa_fwd_paged_fp8": (_I, _PAGED),
     "fa_fwd_blocks": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P, _I, _P]),
     "fa_bwd_blocks": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _I, _I, _I, _I, _F, _I,
                            _P, _I, _P]),
@@ -112,6 +135,16 @@ def fa_bwd_window(Q, K, V, O, dO, LSE, dQ, dK, dV, workspace, workspace_bytes, B
                  H, N, d, tau, window, stream)
 
 
+def fa_fwd_sinks(Q, K, V, O, LSE, B, H, N, d, tau, window, sinks, stream) -> int:
+    return _call("fa_fwd_sinks", Q, K, V, O, LSE, B, H, N, d, tau, window, sinks, stream)
+
+
+def fa_bwd_sinks(Q, K, V, O, dO, LSE, dQ, dK, dV, workspace, workspace_bytes, B, H, N, d, tau,
+                 window, sinks, stream) -> int:
+    return _call("fa_bwd_sinks", Q, K, V, O, dO, LSE, dQ, dK, dV, workspace, workspace_bytes, B, H,
+                 N, d, tau, window, sinks, stream)
+
+
 def fa_fwd_fp8(Q, K, V, O, LSE, B, H, N, d, tau, causal, q_scale, k_scale, v_scale, stream) -> int:
     return _call("fa_fwd_fp8", Q, K, V, O, LSE, B, H, N, d, tau, causal, q_scale, k_scale, v_scale,
                  stream)
@@ -125,6 +158,41 @@ def fa_fwd_decode(Q, K, V, O, LSE, B, H, Nq, Nk, d, tau, causal, workspace, work
                   stream) -> int:
     return _call("fa_fwd_decode", Q, K, V, O, LSE, B, H, Nq, Nk, d, tau, causal, workspace,
                  workspace_bytes, stream)
+
+
+def _strides(t, n):
+    """A host array of strides, or None."""
+    return None if t is None else (_LL2 if n == 2 else _LL3)(*t)
+
+
+def fa_kv_append(cache, k, k_strides, v, v_strides, T, cu_new, q, q_strides, q_out, q_out_strides,
+                 H, inv_freq, rot, interleaved, stream) -> int:
+    return _call("fa_kv_append", cache, k, _strides(k_strides, 2), v, _strides(v_strides, 2), T,
+                 cu_new, q, _strides(q_strides, 2), q_out, _strides(q_out_strides, 2), H, inv_freq,
+                 rot, interleaved, stream)
+
+
+def fa_kv_append_fp8(cache, k, k_strides, v, v_strides, T, cu_new, q, q_strides, q_out,
+                     q_out_strides, H, inv_freq, rot, interleaved, stream) -> int:
+    return _call("fa_kv_append_fp8", cache, k, _strides(k_strides, 2), v, _strides(v_strides, 2),
+                 T, cu_new, q, _strides(q_strides, 2), q_out, _strides(q_out_strides, 2), H,
+                 inv_freq, rot, interleaved, stream)
+
+
+def fa_paged_workspace_size(B, H, H_kv, Nq, d, fp8) -> int:
+    return int(_call("fa_paged_workspace_size", B, H, H_kv, Nq, d, fp8))
+
+
+def fa_fwd_paged(cache, Q, q_strides, O, o_strides, LSE, H, Nq, tau, window, sinks, workspace,
+                 workspace_bytes, stream) -> int:
+    return _call("fa_fwd_paged", cache, Q, _strides(q_strides, 3), O, _strides(o_strides, 3), LSE,
+                 H, Nq, tau, window, sinks, workspace, workspace_bytes, stream)
+
+
+def fa_fwd_paged_fp8(cache, Q, q_strides, O, o_strides, LSE, H, Nq, tau, window, sinks, workspace,
+                     workspace_bytes, stream) -> int:
+    return _call("fa_fwd_paged_fp8", cache, Q, _strides(q_strides, 3), O, _strides(o_strides, 3),
+                 LSE, H, Nq, tau, window, sinks, workspace, workspace_bytes, stream)
 
 
 def fa_fwd_blocks(Q, K, V, O, LSE, B, H, N, d, tau, causal, block_mask, mask_heads, stream) -> int:

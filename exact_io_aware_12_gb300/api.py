@@ -18,6 +18,11 @@ def _stream_handle(device: torch.device) -> int:
     return torch.cuda.current_stream(device).cuda_stream
 
 
+def _on(device: torch.device):
+    """The tensors' device as the current one: the library launches there."""
+    return torch.cuda.device(device)
+
+
 def _check_inputs(*ts: torch.Tensor) -> Tuple[int, int, int, int]:
     ref = ts[0]
     if ref.dim() != 4:
@@ -54,11 +59,14 @@ def _check_blocks(blocks: torch.Tensor, ref: torch.Tensor) -> int:
 def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool,
         tau: Optional[float] = None, out: Optional[torch.Tensor] = None,
         lse: Optional[torch.Tensor] = None, o_fp32: bool = False, window: Optional[int] = None,
-        blocks: Optional[torch.Tensor] = None):
+        blocks: Optional[torch.Tensor] = None, sinks: int = 0):
     """Forward pass.  Returns (O, LSE): O bf16 (fp32 with ``o_fp32``) and LSE
     fp32 [B, H, N].  ``window`` (with ``causal``): each query sees only its
-    ``window`` most recent keys (fa_fwd_window).  ``blocks``: a block mask
-    over 128 x 128 blocks (fa_fwd_blocks)."""
+    ``window`` most recent keys (fa_fwd_window), and with ``sinks`` also the
+    first ``sinks`` keys of the sequence (fa_fwd_sinks).  ``blocks``: a block
+    mask over 128 x 128 blocks (fa_fwd_blocks)."""
+    if sinks and window is None:
+        raise ValueError("sinks need a window")
     if window is not None and (not causal or o_fp32):
         raise ValueError("a window needs causal=True and a bf16 O")
     if blocks is not None and (o_fp32 or window is not None):
@@ -76,6 +84,12 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool,
                                   lse.data_ptr(), B, H, N, d, tau, int(bool(causal)),
                                   blocks.data_ptr(), heads, _stream_handle(q.device))
         _lib.check(code, "fa_fwd_blocks")
+        return out, lse
+    if sinks:
+        code = _lib.fa_fwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                 lse.data_ptr(), B, H, N, d, tau, int(window), int(sinks),
+                                 _stream_handle(q.device))
+        _lib.check(code, "fa_fwd_sinks")
         return out, lse
     if window is not None:
         code = _lib.fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -97,10 +111,12 @@ def workspace_bytes(B: int, H: int, N: int, d: int) -> int:
 def bwd(q, k, v, o, do, lse, causal: bool, tau: Optional[float] = None,
         dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
         dv: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-        window: Optional[int] = None, blocks: Optional[torch.Tensor] = None):
+        window: Optional[int] = None, blocks: Optional[torch.Tensor] = None, sinks: int = 0):
     """Backward pass.  Returns (dQ, dK, dV), bf16.  ``workspace`` (a byte
     tensor of at least ``workspace_bytes`` bytes) is allocated with torch when
     not given, so the library itself allocates nothing."""
+    if sinks and window is None:
+        raise ValueError("sinks need a window")
     B, H, N, d = _check_inputs(q, k, v, o, do)
     if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (B, H, N):
         raise ValueError("lse must be contiguous fp32 [B, H, N]")
@@ -125,6 +141,13 @@ def bwd(q, k, v, o, do, lse, causal: bool, tau: Optional[float] = None,
     if window is not None:
         if not causal:
             raise ValueError("a window needs causal=True")
+        if sinks:
+            code = _lib.fa_bwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
+                                     do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
+                                     dv.data_ptr(), workspace.data_ptr(), workspace.numel(), B, H,
+                                     N, d, tau, int(window), int(sinks), _stream_handle(q.device))
+            _lib.check(code, "fa_bwd_sinks")
+            return dq, dk, dv
         code = _lib.fa_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                   do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                                   dv.data_ptr(), workspace.data_ptr(), workspace.numel(), B, H, N,
@@ -201,6 +224,153 @@ def fwd_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool,
     return out, lse
 
 
+def _paged_cache(k_cache, v_cache, page_table, lens, k_scale, v_scale):
+    """Checks a paged cache's tensors; returns (its description for the C ABI, whether 8-bit)."""
+    fp8 = k_scale is not None
+    if (v_scale is not None) != fp8:
+        raise ValueError("an 8-bit cache has both scales, a bf16 cache none")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("caches must be [num_pages, H_kv, page_size, d], alike")
+    if (k_cache.dtype not in (torch.uint8, torch.float8_e4m3fn)) if fp8 else (k_cache.dtype != torch.bfloat16):
+        raise ValueError("a cache is bf16, or with scales e4m3 (uint8 or float8_e4m3fn)")
+    P, Hkv, page, d = k_cache.shape
+    if page_table.dim() != 2 or lens.shape != page_table.shape[:1]:
+        raise ValueError("page_table must be [B, max_pages] and lens [B]")
+    if page_table.dtype != torch.int32 or lens.dtype != torch.int32:
+        raise ValueError("page_table and lens must be int32")
+    ts = (k_cache, v_cache, page_table, lens)
+    if fp8:
+        if k_scale.shape != (P, Hkv) or v_scale.shape != (P, Hkv) or \
+                k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+            raise ValueError("scales must be fp32 [num_pages, H_kv]")
+        ts += (k_scale, v_scale)
+    dev = k_cache.device
+    for t in ts:
+        if not t.is_cuda or t.device != dev or not t.is_contiguous():
+            raise ValueError("cache, scales, page_table and lens must be contiguous, on one CUDA device")
+    c = _lib.PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr() if fp8 else None,
+                        v_scale.data_ptr() if fp8 else None, page_table.data_ptr(), lens.data_ptr(),
+                        page_table.shape[0], Hkv, d, P, page, page_table.shape[1])
+    return c, fp8
+
+
+def _check_rows(t, shape, dev, what):
+    if tuple(t.shape) != shape or t.dtype != torch.bfloat16 or t.device != dev or \
+            (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{what} must be bf16 {list(shape)} on the cache's device, columns contiguous")
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              page_table: torch.Tensor, lens: torch.Tensor, cu_new: Optional[torch.Tensor] = None,
+              q: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
+              interleaved: bool = False, k_scale: Optional[torch.Tensor] = None,
+              v_scale: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None):
+    """Appends new tokens' k, v [T, H_kv, d] (any token and head strides that are
+    multiples of 8) to the paged cache k_cache, v_cache [num_pages, H_kv,
+    page_size, d] (fa_kv_append; with ``k_scale`` and ``v_scale`` [num_pages,
+    H_kv] the cache is e4m3: fa_kv_append_fp8).  Sequence b's tokens are rows
+    cu_new[b] .. cu_new[b + 1] - 1 (int32 [B + 1]; None: T / B each), placed
+    behind the lens[b] keys that it has; add the new tokens to ``lens``
+    afterwards.  ``inv_freq`` (float64 [rot / 2], radians per position) turns
+    the first rot columns of the keys, and of ``q`` [T, H, d] where given, by
+    their position; ``interleaved`` pairs neighbouring columns.  Returns the
+    rotated queries (``q_out``, or a new tensor), or None without ``q``."""
+    c, fp8 = _paged_cache(k_cache, v_cache, page_table, lens, k_scale, v_scale)
+    dev = k_cache.device
+    if k.dim() != 3:
+        raise ValueError("k and v must be [T, H_kv, d]")
+    T = k.shape[0]
+    _check_rows(k, (T, c.H_kv, c.d), dev, "k")
+    _check_rows(v, (T, c.H_kv, c.d), dev, "v")
+    if cu_new is not None and (cu_new.shape != (c.B + 1,) or cu_new.dtype != torch.int32 or
+                               cu_new.device != dev or not cu_new.is_contiguous()):
+        raise ValueError("cu_new must be contiguous int32 [B + 1] on the cache's device")
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or inv_freq.device != dev or \
+                not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be contiguous float64 [rot / 2] on the cache's device")
+        rot = 2 * inv_freq.shape[0]
+        if rot == 0:
+            raise ValueError("inv_freq is empty")
+    H, qp, qs, op, os_ = 0, None, None, None, None
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        if q.dim() != 3:
+            raise ValueError("q must be [T, H, d]")
+        H = q.shape[1]
+        _check_rows(q, (T, H, c.d), dev, "q")
+        if q_out is None:
+            q_out = torch.empty((T, H, c.d), dtype=torch.bfloat16, device=dev)
+        else:
+            _check_rows(q_out, (T, H, c.d), dev, "q_out")
+        qp, qs, op, os_ = q.data_ptr(), q.stride()[:2], q_out.data_ptr(), q_out.stride()[:2]
+        if H == 0:
+            qp = qs = op = os_ = None
+    fn = _lib.fa_kv_append_fp8 if fp8 else _lib.fa_kv_append
+    with _on(dev):
+        code = fn(c, k.data_ptr(), k.stride()[:2], v.data_ptr(), v.stride()[:2], T,
+                  None if cu_new is None else cu_new.data_ptr(), qp, qs, op, os_, H,
+                  None if inv_freq is None else inv_freq.data_ptr(), rot, int(bool(interleaved)),
+                  _stream_handle(dev))
+    _lib.check(code, "fa_kv_append_fp8" if fp8 else "fa_kv_append")
+    return q_out
+
+
+def paged_workspace_bytes(B: int, H: int, H_kv: int, Nq: int, d: int, fp8: bool = False) -> int:
+    return _lib.fa_paged_workspace_size(B, H, H_kv, Nq, d, int(bool(fp8)))
+
+
+def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              page_table: torch.Tensor, lens: torch.Tensor, tau: Optional[float] = None,
+              window: Optional[int] = None, sinks: int = 0, k_scale: Optional[torch.Tensor] = None,
+              v_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+              lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """Attention of a decode step over a paged cache (fa_fwd_paged; with scales
+    the cache is e4m3: fa_fwd_paged_fp8).  q [B, H, Nq, d] (1 <= Nq <= 8, any
+    strides that are multiples of 8) holds each sequence's last Nq positions,
+    which ``lens`` counts; query head h reads key head h // (H // H_kv).
+    ``window`` and ``sinks`` as in ``fwd``.  Returns (O bf16 [B, H, Nq, d], LSE
+    fp32 [B, H, Nq]); a row without keys gives 0 and -inf.  The workspace is
+    allocated with torch when not given."""
+    c, fp8 = _paged_cache(k_cache, v_cache, page_table, lens, k_scale, v_scale)
+    dev = k_cache.device
+    if q.dim() != 4:
+        raise ValueError("expected [B, H, Nq, d] queries")
+    if window is not None and window < 1:
+        raise ValueError("a window holds at least one key")
+    if sinks and window is None:
+        raise ValueError("sinks need a window")
+    _, H, Nq, _ = q.shape
+    shape = (c.B, H, Nq, c.d)
+    _check_rows(q, shape, dev, "q")
+    tau = 1.0 / math.sqrt(c.d) if tau is None else float(tau)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    else:
+        _check_rows(out, shape, dev, "out")
+    if lse is None:
+        lse = torch.empty(shape[:3], dtype=torch.float32, device=dev)
+    elif lse.shape != shape[:3] or lse.dtype != torch.float32 or lse.device != dev or \
+            not lse.is_contiguous():
+        raise ValueError("lse must be contiguous fp32 [B, H, Nq] on the cache's device")
+    if workspace is None:
+        workspace = torch.empty(max(1, _lib.fa_paged_workspace_size(c.B, H, c.H_kv, Nq, c.d, int(fp8))),
+                                dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on the cache's device")
+    fn = _lib.fa_fwd_paged_fp8 if fp8 else _lib.fa_fwd_paged
+    with _on(dev):
+        code = fn(c, q.data_ptr(), q.stride()[:3], out.data_ptr(), out.stride()[:3], lse.data_ptr(),
+                  H, Nq, tau, 0 if window is None else int(window), int(sinks),
+                  workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                  _stream_handle(dev))
+    _lib.check(code, "fa_fwd_paged_fp8" if fp8 else "fa_fwd_paged")
+    return out, lse
+
+
 def last_device_error(device: Optional[torch.device] = None) -> int:
     device = device or torch.device("cuda", torch.cuda.current_device())
     return _lib.fa_last_device_error(_stream_handle(device))
@@ -208,22 +378,25 @@ def last_device_error(device: Optional[torch.device] = None) -> int:
 
 class _Attention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, causal, tau):
-        o, lse = fwd(q, k, v, causal, tau)
+    def forward(ctx, q, k, v, causal, tau, window, sinks):
+        o, lse = fwd(q, k, v, causal, tau, window=window, sinks=sinks)
         ctx.save_for_backward(q, k, v, o, lse)
-        ctx.causal, ctx.tau = causal, tau
+        ctx.causal, ctx.tau, ctx.window, ctx.sinks = causal, tau, window, sinks
         return o
 
     @staticmethod
     def backward(ctx, do):
         q, k, v, o, lse = ctx.saved_tensors
-        dq, dk, dv = bwd(q, k, v, o, do.contiguous(), lse, ctx.causal, ctx.tau)
-        return dq, dk, dv, None, None
+        dq, dk, dv = bwd(q, k, v, o, do.contiguous(), lse, ctx.causal, ctx.tau, window=ctx.window,
+                         sinks=ctx.sinks)
+        return dq, dk, dv, None, None, None, None
 
 
-def attention(q, k, v, causal: bool = False, tau: Optional[float] = None) -> torch.Tensor:
-    """O = softmax(tau Q K^T [causal]) V with autograd support."""
-    return _Attention.apply(q, k, v, causal, tau)
+def attention(q, k, v, causal: bool = False, tau: Optional[float] = None,
+              window: Optional[int] = None, sinks: int = 0) -> torch.Tensor:
+    """O = softmax(tau Q K^T [causal]) V with autograd support; ``window`` and
+    ``sinks`` as in ``fwd``."""
+    return _Attention.apply(q, k, v, causal, tau, window, sinks)
 
 
 class HostPipeline:

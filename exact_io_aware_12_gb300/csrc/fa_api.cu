@@ -10,6 +10,7 @@
 
 #include "../../include/fa.h"
 #include "fa_internal.h"
+#include "fa_paged.h"
 #include "ptx.cuh"
 
 // One error word per device (each device holds its own copy of this
@@ -125,7 +126,7 @@ fa_status check_blocks(const uint8_t* blocks, int mask_heads, int B, int H, int 
 
 fa_status fwd_common(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int H,
                      int N, int d, float tau, int causal, void* stream, bool o32, int window = 0,
-                     const uint8_t* blocks = nullptr, int mask_heads = 0) {
+                     const uint8_t* blocks = nullptr, int mask_heads = 0, int sinks = 0) {
     bool empty = false;
     fa_status s = check_shape(B, H, N, d, tau, causal, &empty);
     if (s != FA_OK || empty) return s;
@@ -161,6 +162,7 @@ fa_status fwd_common(const void* Q, const void* K, const void* V, void* O, float
     a.tau = tau;
     a.causal = causal != 0;
     a.window = window;
+    a.sinks = sinks;
     a.blocks = blocks;
     a.blocks_head_stride = mask_stride;
     a.o32 = o32;
@@ -284,7 +286,7 @@ static fa_status bwd_common(const void* Q, const void* K, const void* V, const v
                             const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
                             void* workspace, size_t workspace_bytes, int B, int H, int N, int d,
                             float tau, int causal, int window, void* stream,
-                            const uint8_t* blocks = nullptr, int mask_heads = 0) {
+                            const uint8_t* blocks = nullptr, int mask_heads = 0, int sinks = 0) {
     bool empty = false;
     fa_status s = check_shape(B, H, N, d, tau, causal, &empty);
     if (s != FA_OK || empty) return s;
@@ -347,6 +349,7 @@ static fa_status bwd_common(const void* Q, const void* K, const void* V, const v
     a.tau = tau;
     a.causal = causal != 0;
     a.window = window;
+    a.sinks = sinks;
     a.blocks = blocks;
     a.blocks_head_stride = mask_stride;
     a.err = di->err_word;
@@ -379,6 +382,21 @@ fa_status fa_bwd_window(const void* Q, const void* K, const void* V, const void*
     if (window < 1) return FA_ERR_INVALID_ARG;
     return bwd_common(Q, K, V, O, dO, LSE, dQ, dK, dV, workspace, workspace_bytes, B, H, N, d, tau,
                       1, window, stream);
+}
+
+fa_status fa_fwd_sinks(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int H,
+                       int N, int d, float tau, int window, int sinks, void* stream) {
+    if (window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+    return fwd_common(Q, K, V, O, LSE, B, H, N, d, tau, 1, stream, false, window, nullptr, 0, sinks);
+}
+
+fa_status fa_bwd_sinks(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                       const float* LSE, void* dQ, void* dK, void* dV, void* workspace,
+                       size_t workspace_bytes, int B, int H, int N, int d, float tau, int window,
+                       int sinks, void* stream) {
+    if (window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+    return bwd_common(Q, K, V, O, dO, LSE, dQ, dK, dV, workspace, workspace_bytes, B, H, N, d, tau,
+                      1, window, stream, nullptr, 0, sinks);
 }
 
 fa_status fa_fwd_blocks(const void* Q, const void* K, const void* V, void* O, float* LSE, int B,
@@ -519,6 +537,253 @@ fa_status fa_fwd_fp8(const void* Q, const void* K, const void* V, void* O, float
     return map_cuda(launch_fwd_fp8(a, static_cast<cudaStream_t>(stream)));
 }
 
+// --- paged key/value cache ---
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Elements from the first to one past the last of a strided [n0][n1][n2][d] tensor, or
+// -1 for strides that the kernels do not take: negative ones, and any that is no multiple
+// of 8 elements (16 bytes) where its dimension has more than one entry.
+static long long strided_span(const long long n[3], const long long st[3], int d) {
+    long long span = d;
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] <= 1) continue;
+        if (st[i] < 0 || (st[i] & 7) != 0 || st[i] > (1ll << 60) / n[i]) return -1;
+        span += (n[i] - 1) * st[i];
+    }
+    return span;
+}
+// Whether no two entries of such a tensor share memory (sorted by stride, each dimension
+// steps over all that the smaller ones span).
+static bool strided_distinct(const long long n[3], const long long st[3], int d) {
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if (st[order[j]] < st[order[i]]) {
+                const int t = order[i];
+                order[i] = order[j];
+                order[j] = t;
+            }
+    long long inner = d;
+    for (int i : order) {
+        if (n[i] <= 1) continue;
+        if (st[i] < inner) return false;
+        inner = st[i] * (n[i] - 1) + inner;
+    }
+    return true;
+}
+
+// Checks a cache's description and fills the internal form.  fp8 says what the entry
+// point takes.  Sets *bytes (of K, and of V).
+static fa_status check_cache(const fa_paged_cache* c, bool fp8, PagedCache* out, size_t* bytes) {
+    if (c == nullptr) return FA_ERR_INVALID_ARG;
+    if (c->B < 0 || c->H_kv < 0 || c->d < 0 || c->num_pages < 0 || c->page_size < 0 || c->max_pages < 0)
+        return FA_ERR_INVALID_ARG;
+    out->B = c->B;
+    out->H_kv = c->H_kv;
+    out->d = c->d;
+    out->num_pages = c->num_pages;
+    out->max_pages = c->max_pages;
+    if (c->B == 0 || c->H_kv == 0) return FA_OK;  // empty: the caller returns
+    if (c->d != 64 && c->d != 128) return FA_ERR_UNSUPPORTED;
+    if (c->page_size < kPagedMinPage || c->page_size > kPagedMaxPage || (c->page_size & (c->page_size - 1)) != 0)
+        return FA_ERR_UNSUPPORTED;
+    if (c->num_pages == 0 || c->max_pages == 0) return FA_ERR_INVALID_ARG;
+    if (static_cast<long long>(c->max_pages) * c->page_size > kPagedMaxKeys) return FA_ERR_UNSUPPORTED;
+    if (c->K == nullptr || c->V == nullptr || c->page_table == nullptr || c->lens == nullptr) return FA_ERR_INVALID_ARG;
+    if (!aligned16(c->K) || !aligned16(c->V) || !aligned4(c->page_table) || !aligned4(c->lens)) return FA_ERR_INVALID_ARG;
+    if ((c->k_scale != nullptr) != fp8 || (c->v_scale != nullptr) != fp8) return FA_ERR_INVALID_ARG;
+    if (!aligned4(c->k_scale) || !aligned4(c->v_scale)) return FA_ERR_INVALID_ARG;
+    const double elems = static_cast<double>(c->num_pages) * c->H_kv * c->page_size * c->d;
+    if (elems > 1e15) return FA_ERR_UNSUPPORTED;
+    *bytes = static_cast<size_t>(c->num_pages) * c->H_kv * c->page_size * c->d * (fp8 ? 1 : 2);
+    if (overlaps(c->K, *bytes, c->V, *bytes)) return FA_ERR_INVALID_ARG;
+    out->K = c->K;
+    out->V = c->V;
+    out->k_scale = c->k_scale;
+    out->v_scale = c->v_scale;
+    out->page_table = c->page_table;
+    out->lens = c->lens;
+    out->shift = 0;
+    while ((1 << out->shift) < c->page_size) ++out->shift;
+    return FA_OK;
+}
+
+static fa_status append_common(const fa_paged_cache* c, bool fp8, const void* k, const long long* k_strides,
+                               const void* v, const long long* v_strides, int T, const int* cu_new,
+                               const void* q, const long long* q_strides, void* q_out,
+                               const long long* q_out_strides, int H, const double* inv_freq, int rot,
+                               int interleaved, void* stream) {
+    AppendArgs a;
+    size_t cache_bytes = 0;
+    fa_status s = check_cache(c, fp8, &a.cache, &cache_bytes);
+    if (s != FA_OK) return s;
+    if (T < 0 || H < 0 || rot < 0 || (interleaved != 0 && interleaved != 1)) return FA_ERR_INVALID_ARG;
+    if (c->B == 0 || c->H_kv == 0 || T == 0) return FA_OK;
+    if (rot > c->d || rot % 16 != 0) return FA_ERR_INVALID_ARG;
+    if ((rot > 0) != (inv_freq != nullptr) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0) return FA_ERR_INVALID_ARG;
+    if (cu_new == nullptr ? T % c->B != 0 : !aligned4(cu_new)) return FA_ERR_INVALID_ARG;
+    if (k == nullptr || v == nullptr || k_strides == nullptr || v_strides == nullptr) return FA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v)) return FA_ERR_INVALID_ARG;
+    const bool has_q = q != nullptr;
+    if (has_q != (q_out != nullptr) || has_q != (H > 0)) return FA_ERR_INVALID_ARG;
+    if (has_q && (rot == 0 || q_strides == nullptr || q_out_strides == nullptr || !aligned16(q) || !aligned16(q_out)))
+        return FA_ERR_INVALID_ARG;
+    // (token, head) as a [T][heads][1][d] tensor
+    const long long nk[3] = {T, c->H_kv, 1}, nq[3] = {T, H, 1};
+    const auto span = [&](const long long* n, const long long* st) {
+        const long long s3[3] = {st[0], st[1], 0};
+        return strided_span(n, s3, c->d);
+    };
+    const long long ks = span(nk, k_strides), vs = span(nk, v_strides);
+    if (ks < 0 || vs < 0) return FA_ERR_INVALID_ARG;
+    const void* caches[] = {c->K, c->V};
+    for (const void* x : caches)
+        if (overlaps(x, cache_bytes, k, ks * 2) || overlaps(x, cache_bytes, v, vs * 2)) return FA_ERR_INVALID_ARG;
+    if (has_q) {
+        const long long qs = span(nq, q_strides), os = span(nq, q_out_strides);
+        if (qs < 0 || os < 0) return FA_ERR_INVALID_ARG;
+        const long long o3[3] = {q_out_strides[0], q_out_strides[1], 0};
+        if (!strided_distinct(nq, o3, c->d)) return FA_ERR_INVALID_ARG;
+        // in place (the same rows) or apart from everything else
+        const bool in_place = q == q_out && (T == 1 || q_strides[0] == q_out_strides[0]) &&
+                              (H == 1 || q_strides[1] == q_out_strides[1]);
+        for (const void* x : caches)
+            if (overlaps(x, cache_bytes, q, qs * 2) || overlaps(x, cache_bytes, q_out, os * 2)) return FA_ERR_INVALID_ARG;
+        if (!in_place && (overlaps(q_out, os * 2, q, qs * 2) || overlaps(q_out, os * 2, k, ks * 2) ||
+                          overlaps(q_out, os * 2, v, vs * 2)))
+            return FA_ERR_INVALID_ARG;
+        a.q_st = q_strides[0];
+        a.q_sh = q_strides[1];
+        a.o_st = q_out_strides[0];
+        a.o_sh = q_out_strides[1];
+    } else {
+        a.q_st = a.q_sh = a.o_st = a.o_sh = 0;
+    }
+    DeviceInfo* di = current_device(&s);
+    if (!di) return s;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.cu_new = cu_new;
+    a.inv_freq = inv_freq;
+    a.k_st = k_strides[0];
+    a.k_sh = k_strides[1];
+    a.v_st = v_strides[0];
+    a.v_sh = v_strides[1];
+    a.T = T;
+    a.H = H;
+    a.rot = rot;
+    a.interleaved = interleaved;
+    a.err = di->err_word;
+    return map_cuda(launch_kv_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+fa_status fa_kv_append(const fa_paged_cache* cache, const void* k, const long long* k_strides,
+                       const void* v, const long long* v_strides, int T, const int* cu_new,
+                       const void* q, const long long* q_strides, void* q_out,
+                       const long long* q_out_strides, int H, const double* inv_freq, int rot,
+                       int interleaved, void* stream) {
+    return append_common(cache, false, k, k_strides, v, v_strides, T, cu_new, q, q_strides, q_out,
+                         q_out_strides, H, inv_freq, rot, interleaved, stream);
+}
+
+fa_status fa_kv_append_fp8(const fa_paged_cache* cache, const void* k, const long long* k_strides,
+                           const void* v, const long long* v_strides, int T, const int* cu_new,
+                           const void* q, const long long* q_strides, void* q_out,
+                           const long long* q_out_strides, int H, const double* inv_freq, int rot,
+                           int interleaved, void* stream) {
+    return append_common(cache, true, k, k_strides, v, v_strides, T, cu_new, q, q_strides, q_out,
+                         q_out_strides, H, inv_freq, rot, interleaved, stream);
+}
+
+size_t fa_paged_workspace_size(int B, int H, int H_kv, int Nq, int d, int fp8) {
+    if (B <= 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 || Nq <= 0 || Nq > 8 || (d != 64 && d != 128)) return 0;
+    if (H / H_kv > (1 << 20)) return 0;
+    return paged_workspace(B, H, H_kv, Nq, d, fp8 != 0);
+}
+
+static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, const long long* q_strides,
+                              void* O, const long long* o_strides, float* LSE, int H, int Nq, float tau,
+                              int window, int sinks, void* workspace, size_t workspace_bytes, void* stream) {
+    PagedArgs a;
+    size_t cache_bytes = 0;
+    fa_status s = check_cache(c, fp8, &a.cache, &cache_bytes);
+    if (s != FA_OK) return s;
+    if (H < 0 || Nq < 0 || window < 0 || sinks < 0 || (sinks > 0 && window == 0)) return FA_ERR_INVALID_ARG;
+    if (!(std::isfinite(tau) && tau > 0.f)) return FA_ERR_INVALID_ARG;
+    if (c->B == 0 || c->H_kv == 0 || H == 0 || Nq == 0) return FA_OK;
+    if (H % c->H_kv != 0) return FA_ERR_INVALID_ARG;
+    if (Nq > 8 || H / c->H_kv > (1 << 20)) return FA_ERR_UNSUPPORTED;
+    if (paged_max_steps(c->B, H, c->H_kv, Nq, c->max_pages, a.cache.shift) > INT_MAX) return FA_ERR_UNSUPPORTED;
+    if (Q == nullptr || O == nullptr || LSE == nullptr || q_strides == nullptr || o_strides == nullptr)
+        return FA_ERR_INVALID_ARG;
+    if (!aligned16(Q) || !aligned16(O) || !aligned16(LSE)) return FA_ERR_INVALID_ARG;
+    if (workspace != nullptr && !aligned16(workspace)) return FA_ERR_INVALID_ARG;
+    const long long n[3] = {c->B, H, Nq};
+    const long long qs = strided_span(n, q_strides, c->d), os = strided_span(n, o_strides, c->d);
+    if (qs < 0 || os < 0 || !strided_distinct(n, o_strides, c->d)) return FA_ERR_INVALID_ARG;
+    const size_t need = fa_paged_workspace_size(c->B, H, c->H_kv, Nq, c->d, fp8);
+    if (workspace != nullptr && workspace_bytes < need) return FA_ERR_WORKSPACE;
+    const size_t lb = static_cast<size_t>(c->B) * H * Nq * 4, tb = static_cast<size_t>(c->B) * c->max_pages * 4;
+    const size_t sb = fp8 ? static_cast<size_t>(c->num_pages) * c->H_kv * 4 : 0;
+    const void* ins[] = {Q, c->K, c->V, c->page_table, c->lens, c->k_scale, c->v_scale};
+    const size_t in_bytes[] = {static_cast<size_t>(qs) * 2, cache_bytes, cache_bytes, tb,
+                               static_cast<size_t>(c->B) * 4, sb, sb};
+    const void* outs[] = {O, LSE, workspace};
+    const size_t out_bytes[] = {static_cast<size_t>(os) * 2, lb, need};
+    for (int o = 0; o < (workspace ? 3 : 2); ++o) {
+        for (int i = 0; i < (fp8 ? 7 : 5); ++i)
+            if (overlaps(outs[o], out_bytes[o], ins[i], in_bytes[i])) return FA_ERR_INVALID_ARG;
+        for (int o2 = 0; o2 < o; ++o2)
+            if (overlaps(outs[o], out_bytes[o], outs[o2], out_bytes[o2])) return FA_ERR_INVALID_ARG;
+    }
+    DeviceInfo* di = current_device(&s);
+    if (!di) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    void* ws = workspace;
+    if (ws == nullptr && cudaMallocAsync(&ws, need, st) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_CUDA;
+    }
+    a.Q = Q;
+    a.O = O;
+    a.LSE = LSE;
+    a.workspace = ws;
+    a.q_sb = q_strides[0];
+    a.q_sh = q_strides[1];
+    a.q_sn = q_strides[2];
+    a.o_sb = o_strides[0];
+    a.o_sh = o_strides[1];
+    a.o_sn = o_strides[2];
+    a.H = H;
+    a.Nq = Nq;
+    a.window = window < (1 << 30) ? window : (1 << 30);  // (a length is below 2^31: the same keys)
+    a.sinks = sinks < (1 << 30) ? sinks : (1 << 30);
+    a.tau = tau;
+    a.err = di->err_word;
+    a.ev_start = t_ev_start;
+    a.ev_stop = t_ev_stop;
+    const cudaError_t e = launch_fwd_paged(a, st);
+    if (workspace == nullptr) cudaFreeAsync(ws, st);
+    return map_cuda(e);
+}
+
+fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* Q, const long long* q_strides, void* O,
+                       const long long* o_strides, float* LSE, int H, int Nq, float tau, int window,
+                       int sinks, void* workspace, size_t workspace_bytes, void* stream) {
+    return paged_common(cache, false, Q, q_strides, O, o_strides, LSE, H, Nq, tau, window, sinks,
+                        workspace, workspace_bytes, stream);
+}
+
+fa_status fa_fwd_paged_fp8(const fa_paged_cache* cache, const void* Q, const long long* q_strides,
+                           void* O, const long long* o_strides, float* LSE, int H, int Nq, float tau,
+                           int window, int sinks, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+    return paged_common(cache, true, Q, q_strides, O, o_strides, LSE, H, Nq, tau, window, sinks,
+                        workspace, workspace_bytes, stream);
+}
+
 const char* fa_status_string(fa_status s) {
     switch (s) {
         case FA_OK: return "FA_OK";
@@ -527,6 +792,7 @@ const char* fa_status_string(fa_status s) {
         case FA_ERR_WORKSPACE: return "FA_ERR_WORKSPACE: workspace too small";
         case FA_ERR_CUDA: return "FA_ERR_CUDA: CUDA runtime or launch error";
         case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT: a kernel pipeline wait timed out";
+        case FA_ERR_PAGE: return "FA_ERR_PAGE: a cache length, token count or page number out of bounds";
     }
     return "unknown fa_status";
 }
@@ -550,7 +816,7 @@ fa_status fa_last_device_error(void* stream) {
             cudaGetLastError();
             return FA_ERR_CUDA;
         }
-        return FA_ERR_TIMEOUT;
+        return (word & 1u) != 0 ? FA_ERR_TIMEOUT : FA_ERR_PAGE;
     }
     return FA_OK;
 }

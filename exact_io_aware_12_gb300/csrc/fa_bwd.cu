@@ -59,7 +59,7 @@ constexpr int kBK = 128;  // keys per CTA
 constexpr int bwd_threads(int nwg) { return 32 * (4 * nwg + 3); }
 constexpr float kLog2e = 1.44269504088896341f;
 // Which query tiles a key tile visits beyond causality.
-enum : int { kMaskNone = 0, kMaskWindow = 1, kMaskBlocks = 2 };
+enum : int { kMaskNone = 0, kMaskWindow = 1, kMaskBlocks = 2, kMaskSinks = 3 };
 constexpr int kMaskWords = kMaxMaskBlocks / 32;
 constexpr int kBwdPersistMaxN = 2048;  // d = 64, no mask, up to this length: the persistent kernel
 
@@ -161,6 +161,7 @@ struct BwdParams {
     int N;
     int n_kv;
     int window;        // causal sliding window in keys (0 = none)
+    int sinks;         // kMaskSinks: keys [0, sinks) stay visible behind the window
     float scale_log2;  // tau * log2(e)
     float tau;
     unsigned int* err;
@@ -240,7 +241,8 @@ __device__ __forceinline__ void mma_mn_mn(uint32_t tmem_d, uint32_t a_lo, uint32
 }
 
 // MASK: kMaskNone; kMaskWindow, a causal sliding window of p.window keys (only
-// with CAUSAL); kMaskBlocks, the block mask p.blocks.  PERSIST: one CTA per SM
+// with CAUSAL); kMaskSinks, such a window beside p.sinks first keys that stay
+// visible; kMaskBlocks, the block mask p.blocks.  PERSIST: one CTA per SM
 // walks a list of (key tile, batch*head) work items (no mask).
 template <int D, bool CAUSAL, int MASK, int NWG, bool PERSIST = false, bool SPLIT = false>
 __global__ void __launch_bounds__(bwd_threads(NWG), 1)
@@ -258,7 +260,8 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     constexpr int kQC = 128 / NWG;      // query columns of P^T / dS^T per warpgroup
     constexpr int kDC = D / NWG;        // d-columns of dQ, dK, dV per warpgroup
     constexpr int kEW = 128 * NWG;      // elementwise threads
-    constexpr bool LOCAL = MASK == kMaskWindow;
+    constexpr bool SINKS = MASK == kMaskSinks;
+    constexpr bool LOCAL = MASK == kMaskWindow || SINKS;
     constexpr bool SPARSE = MASK == kMaskBlocks;
     // a block mask with a split plan (its own instance: the plan's code stays out of
     // the plain block-mask kernel)
@@ -332,10 +335,12 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     const int kv_start = kv_tile * kBK;
     const int n_q = (N + kBQ - 1) / kBQ;
     // Query tiles that see this key tile: from the diagonal when causal, and with
-    // a sliding window only up to the tile holding query (last key + window - 1).
+    // a sliding window only up to the tile holding query (last key + window - 1);
+    // a tile that holds sinks is seen by every later query tile.
     const int window = (CAUSAL && LOCAL) ? p.window : 0;
+    const int sinks = SINKS ? p.sinks : 0;
     const int first = CAUSAL ? kv_tile : 0;
-    const int last = window > 0 ? min(n_q - 1, (kv_start + kBK - 1 + window - 1) / kBQ) : n_q - 1;
+    const int last = window > 0 && (!SINKS || kv_start >= sinks) ? min(n_q - 1, (kv_start + kBK - 1 + window - 1) / kBQ) : n_q - 1;
     int n_steps = last - first + 1;  // with a block mask: counted below
     // an item's first query tile and step count (item 0: first and n_steps)
     auto first_of = [&](int ikv) { return PERSIST ? (CAUSAL ? ikv : 0) : first; };
@@ -750,7 +755,8 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     // past the window edge q >= kg + window - qh, and a key row past a
                     // ragged end sees none
                     const int lo = kg >= N ? (1 << 30) : (diag ? kg - qh : -(1 << 30));
-                    const int hi = (LOCAL && wedge) ? kg + window - qh : (1 << 30);
+                    // (a sink has no such edge)
+                    const int hi = (LOCAL && wedge && (!SINKS || kg >= sinks)) ? kg + window - qh : (1 << 30);
 #pragma unroll
                     for (int c = 0; c < kQC / 32; ++c) {
                         uint32_t sv[32];
@@ -1345,6 +1351,7 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
         p.scale_log2 = a.tau * kLog2e;
         p.tau = a.tau;
         p.window = (a.window > 0 && a.window < a.N) ? a.window : 0;
+        p.sinks = a.sinks;
         p.blocks = a.blocks;
         p.blocks_head_stride = a.blocks_head_stride;
         p.head_group = bwd_head_group(a.BH, a.N, D, CAUSAL, MASK);
@@ -1396,9 +1403,13 @@ cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t stream) {
         return a.causal ? launch_bwd_t<128, true, kMaskBlocks>(a, stream)
                         : launch_bwd_t<128, false, kMaskBlocks>(a, stream);
     }
-    if (a.causal && a.window > 0 && a.window < a.N)
+    if (a.causal && window_hides(a.N, a.window, a.sinks)) {
+        if (a.sinks > 0)
+            return a.d == 64 ? launch_bwd_t<64, true, kMaskSinks>(a, stream)
+                             : launch_bwd_t<128, true, kMaskSinks>(a, stream);
         return a.d == 64 ? launch_bwd_t<64, true, kMaskWindow>(a, stream)
                          : launch_bwd_t<128, true, kMaskWindow>(a, stream);
+    }
     if (a.d == 64) return a.causal ? launch_bwd_t<64, true>(a, stream) : launch_bwd_t<64, false>(a, stream);
     return a.causal ? launch_bwd_t<128, true>(a, stream) : launch_bwd_t<128, false>(a, stream);
 }

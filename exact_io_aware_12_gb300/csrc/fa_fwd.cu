@@ -59,7 +59,7 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8
 // Which keys a query tile visits beyond causality.
-enum : int { kMaskNone = 0, kMaskWindow = 1, kMaskBlocks = 2 };
+enum : int { kMaskNone = 0, kMaskWindow = 1, kMaskBlocks = 2, kMaskSinks = 3 };
 constexpr int kMaskWords = kMaxMaskBlocks / 32;
 constexpr int kSingleTileMaxN = 2048;  // d = 64 up to this length: one tile per CTA
 constexpr int kPersistMaxN128 = 4096;  // d = 128 without a mask up to this length: the persistent pairs
@@ -97,6 +97,7 @@ struct FwdParams {
     unsigned int* err;
     unsigned long long wait_limit_ns;
     int window;  // causal sliding window in keys (0 = none)
+    int sinks;   // kMaskSinks: keys [0, sinks) stay visible behind the window
     const uint8_t* blocks;          // block mask [heads][n_kv][n_kv] (kMaskBlocks)
     long long blocks_head_stride;   // bytes between heads' masks (0: one mask)
     int BH;                         // PERSIST: batch*heads
@@ -159,12 +160,22 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem_o, uint32_t tmem_p, uint3
 // diagonal when causal, and from the block holding key (first row - window + 1)
 // with a sliding window.  The two ranges overlap or touch, so the loaders walk
 // [jlo, jlo + nb) without gaps.  (A block mask recounts n_blk0, n_blk1 and nb.)
+// With sinks both tiles first take the ns key blocks that hold sinks and lie
+// before jlo: step u of the walk is block u for u < ns, then jlo + u - ns.  A
+// block jlo that itself holds sinks is taken by tile 1 too, whose window may
+// begin one block later.
 struct FwdItem {
-    int bh, q_start0, q_start1, lo0, lo1, hi0, hi1, n_blk0, n_blk1, jlo, nb;
+    int bh, q_start0, q_start1, lo0, lo1, hi0, hi1, n_blk0, n_blk1, jlo, nb, ns;
+    // kMaskSinks: whether tile t (its block range [lo, hi)) takes step u, and u's key block
+    __device__ __forceinline__ int block(int u) const { return u < ns ? u : jlo + u - ns; }
+    __device__ __forceinline__ bool takes(int u, int lo, int hi) const {
+        const int j = jlo + u - ns;
+        return u < ns ? hi > 0 : (j >= lo && j < hi);
+    }
 };
 
 template <bool CAUSAL, int TILES>
-__device__ __forceinline__ FwdItem fwd_item(int bh, int pair, int N, int n_kv, int window) {
+__device__ __forceinline__ FwdItem fwd_item(int bh, int pair, int N, int n_kv, int window, int sinks = 0) {
     FwdItem it;
     it.bh = bh;
     it.q_start0 = pair * TILES * kBM;
@@ -173,15 +184,19 @@ __device__ __forceinline__ FwdItem fwd_item(int bh, int pair, int N, int n_kv, i
     it.hi1 = it.q_start1 < N ? (CAUSAL ? min(n_kv, it.q_start1 / kBN + 1) : n_kv) : 0;
     it.lo0 = window > 0 ? max(0, it.q_start0 - window + 1) / kBN : 0;
     it.lo1 = window > 0 ? max(0, it.q_start1 - window + 1) / kBN : 0;
-    it.n_blk0 = it.hi0 - it.lo0;
-    it.n_blk1 = it.hi1 > 0 ? it.hi1 - it.lo1 : 0;
+    const int n_sink = (sinks + kBN - 1) / kBN;  // key blocks that hold sinks
     it.jlo = it.lo0;
-    it.nb = max(it.hi0, it.hi1) - it.jlo;
+    it.ns = min(n_sink, it.jlo);
+    if (it.jlo < n_sink) it.lo1 = it.jlo;
+    it.n_blk0 = it.ns + it.hi0 - it.lo0;
+    it.n_blk1 = it.hi1 > 0 ? it.ns + it.hi1 - it.lo1 : 0;
+    it.nb = it.ns + max(it.hi0, it.hi1) - it.jlo;
     return it;
 }
 
 // MASK: kMaskNone; kMaskWindow, a causal sliding window of p.window keys (only
-// with CAUSAL); kMaskBlocks, the block mask p.blocks (bf16 O only).  PERSIST:
+// with CAUSAL); kMaskSinks, such a window beside p.sinks first keys that stay
+// visible; kMaskBlocks, the block mask p.blocks (bf16 O only).  PERSIST:
 // one CTA per SM walks a list of (batch*head, pair) items (two tiles, bf16 O,
 // no block mask).
 template <int D, bool CAUSAL, bool O32, int MASK, int TILES, bool PERSIST = false>
@@ -191,7 +206,8 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
               const FwdParams p) {
     using L = FwdLayout<D, TILES>;
     constexpr int kProducerWarp = 4 * TILES, kMmaWarp = 4 * TILES + 1;
-    constexpr bool LOCAL = MASK == kMaskWindow;
+    constexpr bool SINKS = MASK == kMaskSinks;
+    constexpr bool LOCAL = MASK == kMaskWindow || SINKS;
     constexpr bool SPARSE = MASK == kMaskBlocks;
     // d = 64 without a mask: P has its own tensor-memory columns, so S of block
     // j + 1 is issued as soon as the softmax has read S of block j, and the
@@ -219,6 +235,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     const int N = p.N;
     const int n_kv = (N + kBN - 1) / kBN;
     const int window = (CAUSAL && LOCAL) ? p.window : 0;
+    const int sinks = SINKS ? p.sinks : 0;
     // Work items in launch order (x, the batch*head, fastest; the pair index y
     // from the heaviest pair down): i = y BH + x.  Without PERSIST a CTA has one
     // item, its launch position.  With PERSIST, CTA c of G takes items c,
@@ -227,11 +244,11 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     auto item_of = [&](long long i) {
         const int y = static_cast<int>(i / p.BH);
         return fwd_item<CAUSAL, TILES>(static_cast<int>(i - static_cast<long long>(y) * p.BH),
-                                       p.n_pairs - 1 - y, N, n_kv, window);
+                                       p.n_pairs - 1 - y, N, n_kv, window, sinks);
     };
     FwdItem it0 = PERSIST ? item_of(blockIdx.x)
                           : fwd_item<CAUSAL, TILES>(blockIdx.x, p.n_pairs - 1 - static_cast<int>(blockIdx.y),
-                                                    N, n_kv, window);
+                                                    N, n_kv, window, sinks);
     const int bh = it0.bh;
     const int q_start0 = it0.q_start0, q_start1 = it0.q_start1;
     [[maybe_unused]] const int hi0 = it0.hi0, hi1 = it0.hi1, lo0 = it0.lo0, lo1 = it0.lo1, jlo = it0.jlo;
@@ -386,7 +403,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                             break;
                         }
                         bool is_k = (ld & 1) == 0;
-                        int blk = it.jlo + (ld >> 1);
+                        int blk = SINKS ? it.block(ld >> 1) : it.jlo + (ld >> 1);
                         if constexpr (PIPE) {
                             // the MMA warp's order: K0 K1 V0 K2 V1 ... K(nb-1) V(nb-2) V(nb-1)
                             is_k = ld == 0 || ((ld & 1) && ld < 2 * it.nb - 1);
@@ -574,7 +591,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                         if (ok) {
                             tc_fence_after();
                             for (int t = 0; t < 2; ++t) {
-                                if (lo[t] == it.jlo && hi[t] > it.jlo) {
+                                if (SINKS ? it.takes(0, lo[t], hi[t]) : lo[t] == it.jlo && hi[t] > it.jlo) {
                                     issue_s<D>(tS[t], qlo[t], klo0 + s0 * kSlot);
                                     mma_commit_warp(bar_s + 8 * t);
                                 }
@@ -636,8 +653,10 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                                 if (k_ready) mma_commit_warp(bar_kv_empty + 8 * sk);
                             }
                         } else {
-                            // tile t takes blocks [lo[t], hi[t]); S of a tile's first block may
-                            // be issued while the other tile is still in its leading blocks
+                            // tile t takes blocks [lo[t], hi[t]) (with sinks: the steps that it.takes
+                            // says); S of a tile's first block may be issued while the other tile is
+                            // still in its leading blocks
+                            [[maybe_unused]] int cnt[2] = {0, 0};  // SINKS: P V products issued per tile
                             for (int u = 0; ok && u < it.nb; ++u) {
                                 const int j = it.jlo + u;  // key block
                                 const int lv = g0 + 2 * u + 1, lk = g0 + 2 * u + 2;
@@ -652,19 +671,21 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                                 // fully unrolled over the two tiles so the per-tile arrays stay in registers
 #pragma unroll
                                 for (int t = 0; t < 2; ++t) {
-                                    if (ok && j >= lo[t] && j < hi[t]) {
-                                        if (j == lo[t]) ok = o_free_wait(t);
+                                    const int done = SINKS ? cnt[t] : j - lo[t];  // P V products of the item before this
+                                    if (ok && (SINKS ? it.takes(u, lo[t], hi[t]) : j >= lo[t] && j < hi[t])) {
+                                        if (done == 0) ok = o_free_wait(t);
                                         if (ok)
                                             ok = __all_sync(0xffffffffu,
-                                                            mbar_wait(bar_p + 8 * t, (cb[t] + j - lo[t]) & 1, wd,
+                                                            mbar_wait(bar_p + 8 * t, (cb[t] + done) & 1, wd,
                                                                       kSiteMmaP));
                                         if (ok) {
                                             tc_fence_after();
-                                            issue_pv<D>(tO[t], tS[t], vlo0 + sv * kSlot, j > lo[t]);
+                                            issue_pv<D>(tO[t], tS[t], vlo0 + sv * kSlot, done > 0);
                                             mma_commit_warp(bar_o + 8 * t);
                                         }
+                                        if constexpr (SINKS) ++cnt[t];
                                     }
-                                    if (ok && j + 1 >= lo[t] && j + 1 < hi[t]) {
+                                    if (ok && (SINKS ? it.takes(u + 1, lo[t], hi[t]) : j + 1 >= lo[t] && j + 1 < hi[t])) {
                                         if (!k_ready) {
                                             ok = __all_sync(0xffffffffu,
                                                             mbar_wait(bar_kv_full + 8 * sk, (lk / L::kStages) & 1,
@@ -720,6 +741,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             int jsp = -1;  // block mask: the last key block visited
             for (int jj = 0; jj < nbt; ++jj) {
                 int j = lot + jj;  // key block
+                if constexpr (SINKS) j = jj < it.ns ? jj : lot + jj - it.ns;
                 if constexpr (SPARSE) {
                     jsp = next_set_bit(sh.use[t], nullptr, jsp + 1, n_kv);
                     j = jsp;
@@ -746,7 +768,8 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 
                 const int kbase = j * kBN;
                 const bool need_mask = (CAUSAL && kbase + kBN - 1 > q_start) || (kbase + kBN > N) ||
-                                       (window > 0 && kbase <= q_start + kBM - 1 - window);
+                                       (window > 0 && kbase <= q_start + kBM - 1 - window &&
+                                        (!SINKS || kbase + kBN > sinks));
                 if (need_mask) {
                     const int last = CAUSAL ? min(row, N - 1) : N - 1;  // last visible key
                     if constexpr (LOCAL) {
@@ -755,8 +778,14 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                         // window's lower edge) or, with a short window, both: one compare per
                         // score unless both
                         const bool upper = (kbase + kBN - 1 > q_start) || (kbase + kBN > N);
-                        const bool lower = kbase <= q_start + kBM - 1 - window;
-                        if (upper && lower) {
+                        const bool lower = kbase <= q_start + kBM - 1 - window && (!SINKS || kbase + kBN > sinks);
+                        if (SINKS && lower && kbase < sinks) {
+                            // the block in which the sinks end: hidden from there up to the window
+#pragma unroll
+                            for (int c = 0; c < 128; ++c)
+                                if (kbase + c > last || (kbase + c < first && kbase + c >= sinks))
+                                    s[c >> 5][c & 31] = f2u(-INFINITY);
+                        } else if (upper && lower) {
 #pragma unroll
                             for (int c = 0; c < 128; ++c)
                                 if (kbase + c > last || kbase + c < first) s[c >> 5][c & 31] = f2u(-INFINITY);
@@ -1062,6 +1091,7 @@ cudaError_t launch_fwd_t(const FwdArgs& a, cudaStream_t stream) {
     p.items = static_cast<int>(items);
     p.N = a.N;
     p.window = (a.window > 0 && a.window < a.N) ? a.window : 0;
+    p.sinks = a.sinks;
     p.blocks = a.blocks;
     p.blocks_head_stride = a.blocks_head_stride;
     p.n_pairs = n_pairs;
@@ -1088,9 +1118,13 @@ cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t stream) {
                             : launch_fwd_t<64, false, false, kMaskBlocks, 1>(a, stream);
         return launch_fwd_sparse(a, stream);  // persistent, fa_fwd_sparse.cu
     }
-    if (a.causal && !a.o32 && a.window > 0 && a.window < a.N)
+    if (a.causal && !a.o32 && window_hides(a.N, a.window, a.sinks)) {
+        if (a.sinks > 0)
+            return a.d == 64 ? launch_fwd_t<64, true, false, kMaskSinks>(a, stream)
+                             : launch_fwd_t<128, true, false, kMaskSinks>(a, stream);
         return a.d == 64 ? launch_fwd_t<64, true, false, kMaskWindow>(a, stream)
                          : launch_fwd_t<128, true, false, kMaskWindow>(a, stream);
+    }
     if (a.d == 64) {
         if (!a.o32 && a.N <= kSingleTileMaxN) return launch_fwd_short(a, stream);
         if (a.causal) return a.o32 ? launch_fwd_t<64, true, true>(a, stream) : launch_fwd_t<64, true, false>(a, stream);

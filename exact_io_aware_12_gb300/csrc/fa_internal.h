@@ -26,6 +26,7 @@ struct FwdArgs {
     float tau;
     bool causal;
     int window;       // causal sliding window in keys (0 = none)
+    int sinks = 0;    // keys [0, sinks) that stay visible behind the window
     const uint8_t* blocks = nullptr;  // block mask [heads][nb][nb] (device) or null
     long long blocks_head_stride = 0;  // bytes between heads' masks (0: one mask)
     bool o32;
@@ -52,6 +53,7 @@ struct BwdArgs {
     float tau;
     bool causal;
     int window;     // causal sliding window in keys (0 = none)
+    int sinks = 0;  // keys [0, sinks) that stay visible behind the window
     const uint8_t* blocks = nullptr;  // block mask [heads][nb][nb] (device) or null
     long long blocks_head_stride = 0;  // bytes between heads' masks (0: one mask)
     unsigned int* err;
@@ -94,6 +96,64 @@ struct DecArgs {
     cudaEvent_t ev_start;  // optional: recorded around the two kernels
     cudaEvent_t ev_stop;
 };
+
+// A paged key/value cache: K, V [num_pages][H_kv][1 << shift][d], bf16, or e4m3 with
+// scales [num_pages][H_kv] (null for bf16); page_table [B][max_pages], lens [B].
+struct PagedCache {
+    void* K;
+    void* V;
+    float* k_scale;
+    float* v_scale;
+    const int* page_table;
+    const int* lens;
+    int B, H_kv, d, num_pages, max_pages, shift;
+};
+
+// Error-word value of a length, token count or page number out of bounds (bit 0 is a
+// timeout's).
+constexpr unsigned int kErrPage = 2u;
+
+// Arguments of one append.  Strides in elements: token, head.
+struct AppendArgs {
+    PagedCache cache;
+    const void* q;       // bf16 [T][H][d], or null
+    const void* k;       // bf16 [T][H_kv][d]
+    const void* v;
+    void* q_out;
+    const int* cu_new;   // [B + 1], or null: T / B tokens each
+    const double* inv_freq;  // [rot / 2]
+    long long q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh;
+    int T, H, rot, interleaved;
+    unsigned int* err;
+};
+
+// Arguments of one attention step over a paged cache.  Strides in elements: sequence,
+// head, row.
+struct PagedArgs {
+    PagedCache cache;
+    const void* Q;     // bf16 [B][H][Nq][d]
+    void* O;
+    float* LSE;        // fp32 [B][H][Nq]
+    void* workspace;
+    long long q_sb, q_sh, q_sn, o_sb, o_sh, o_sn;
+    int H, Nq, window, sinks;
+    float tau;
+    unsigned int* err;
+    cudaEvent_t ev_start;  // optional: recorded around the two kernels
+    cudaEvent_t ev_stop;
+};
+// Bytes of workspace one such step takes, whatever the sequences' lengths.
+size_t paged_workspace(int B, int H, int H_kv, int Nq, int d, bool fp8);
+// Block steps that a full table holds: the launcher's 32-bit step counts must not pass.
+long long paged_max_steps(int B, int H, int H_kv, int Nq, int max_pages, int shift);
+
+// Whether a causal window of `window` keys (0: none) beside `sinks` first keys hides
+// anything that the causal mask shows: the last query, N - 1, sees neither the keys
+// from `sinks` on nor those within its window.  Where it hides nothing the kernels
+// without a window run.
+inline bool window_hides(int N, int window, int sinks) {
+    return window > 0 && static_cast<long long>(window) + sinks < N;
+}
 
 // How the decode forward cuts the KV cache: `splits` chunks of `chunk` keys
 // (a multiple of 64).  Depends only on its arguments.
@@ -148,6 +208,8 @@ cudaError_t launch_fwd_short(const FwdArgs& a, cudaStream_t stream);
 cudaError_t launch_fwd_sparse(const FwdArgs& a, cudaStream_t stream);
 cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t stream);
 cudaError_t launch_decode(const DecArgs& a, cudaStream_t stream);
+cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream);
 cudaError_t launch_fwd_fp8(const Fp8Args& a, cudaStream_t stream);
 cudaError_t launch_watchdog_selftest(unsigned int* err, unsigned long long limit_ns,
                                      cudaStream_t stream);

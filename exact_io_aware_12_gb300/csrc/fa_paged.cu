@@ -1,0 +1,848 @@
+// Attention of a decode step over a paged key/value cache (bf16, or e4m3 with a scale
+// per page and head), for sm_103a.
+//
+// Mathematics: the Nq <= 8 query rows of a sequence are its last positions; row i of
+// len keys sees key j iff j <= len - Nq + i and, with a window, j > len - Nq + i - window
+// or j < sinks.  O = sum_j softmax_j(tau q.k_j) v_j by the online recurrence of
+// fa_decode.cu, each H / H_kv query heads reading one key head.  A step reads each
+// visible K and V once, so HBM bounds it.
+//
+// Design:
+//   - Work is cut evenly whatever the lengths: the 64-key steps of all (sequence, key
+//     head, row block) segments form one list, and each of the resident CTAs takes an
+//     equal contiguous share of it, found from a prefix sum of the lengths, which stay
+//     on the device.  A segment that several shares cut leaves one partial result per
+//     piece (normalised, with its log-sum), which the combine kernel adds.
+//   - The four warps of a CTA take one 16-key tile each per step and share nothing until
+//     the segment ends: no block barrier in the loop.  A warp streams its own tiles
+//     through its own ring of shared memory with 16-byte cp.async, written in the XOR
+//     order that makes the 16-byte fragment loads below free of bank conflicts.
+//   - Both products run on warp matrix instructions with the keys (and the columns of
+//     V) as the 16-row operand and 8 query rows as the narrow one: S^T = K Q^T and
+//     O^T = V^T P^T, so grouped heads fill a tile with little padding.  At 16 query rows
+//     a step's 512 bytes per bf16 key feed 8192 multiply-adds: the tensor cores idle on
+//     the memory either way, and a 128-row tcgen05 tile would be 87-94% padding.
+//   - The order of the summed index is free as long as both operands agree: a thread
+//     takes the 16 bytes of a key row that it can load at once, so K needs no transposing
+//     load.  V^T pairs neighbouring keys with a byte permute; P^T changes from the
+//     accumulator's layout to the operand's with movmatrix.
+//   - The running max is moved only when some score passes it by 2^8 (one vote per
+//     tile); row sums stay per thread until the segment ends.
+//   - e4m3 keys and values are widened to fp16, which holds every code exactly; queries
+//     enter as fp16 with a power of two per row, so bf16's 8 bits stay exact down to
+//     2^-31 of the row's largest.  The page's K scale multiplies the scores in fp32; its
+//     V scale enters the weights, which keep a running max of their own (log2 P + log2
+//     scale), so pages of very different scale lose nothing in fp16.
+//   - P is rounded to bf16 (fp16 for 8-bit pages) for the second product, relative error
+//     at most 2^-9 (2^-12) per weight, no more than O's own rounding; statistics, scores
+//     and sums stay in fp32.
+//   - Rows past a sequence's end are never read: the copy fills them with zeros, so what
+//     a page holds there, NaN included, does not matter; the same goes for keys hidden
+//     from all of the step's rows.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "fa_internal.h"
+#include "fa_paged.h"
+#include "ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kSms = 152;  // of a GB300
+constexpr int kThreads = 32 * kPagedWarps;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kGrow = 8.0f;  // log2 units: weights stay <= 2^8
+
+// Ring slots per warp and CTAs per SM: about 128 KB in flight per SM, as much as the
+// copy bandwidth times the memory's latency asks for (45 GB/s x ~1.5 us per SM).
+template <int D, int NT, bool F8>
+struct PagedLayout {
+    static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a key row
+    static constexpr int kTile = kPagedTile * kRow;     // K or V of one tile
+    static constexpr int kSlot = 2 * kTile;
+    static constexpr int kCtas = NT == 4 ? 2 : kSlot == 8192 ? 2 : NT == 2 ? 3 : 4;
+    static constexpr int kStages = kSlot == 8192 ? 3 : kSlot == 4096 ? (NT == 1 ? 3 : NT == 2 ? 4 : 6) : 6;
+    static constexpr int kWarpRing = kStages * kSlot;
+    static constexpr int kRing = kPagedWarps * kWarpRing;
+    static constexpr int kRed = kPagedWarps * 8 * D * 4;  // merge buffer over the idle ring
+    static constexpr int kBytes = kRing > kRed ? kRing : kRed;
+};
+
+struct PagedParams {
+    const __nv_bfloat16* Q;
+    const uint8_t* K;
+    const uint8_t* V;
+    const float* k_scale;
+    const float* v_scale;
+    const int* table;
+    const int* lens;
+    __nv_bfloat16* O;
+    float* LSE;
+    int2* seg;       // [segments]: (first share, pieces) of a segment in several pieces
+    float* part_o;   // [2 shares][8 NT][D]
+    float* part_l;   // [2 shares][8 NT], log2 of the piece's sum
+    long long q_sb, q_sh, q_sn, o_sb, o_sh, o_sn;
+    int B, H, H_kv, G, Nq, rblocks, num_pages, max_pages, shift, window, sinks;
+    float scale_log2;  // tau * log2(e)
+    unsigned int* err;
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+// d += A B: A 16 x 16 (rows keys or V columns), B 16 x 8 (query rows), fp32 accumulation.
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8 x 8 transpose of 16-bit values across the warp.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// Four e4m3 codes -> two fp16 pairs (exact): a = codes 0, 1; b = codes 2, 3.
+__device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(a), "=r"(b) : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float lg2(float x) {  // log2, -inf at 0
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile.  K: eight threads read four chunks
+// of two neighbouring rows; V: two chunks of every other row of eight.  Either set
+// covers all 32 banks.
+template <int ROW>
+__device__ __forceinline__ int k_off(int r, int c) {
+    if constexpr (ROW >= 128) return r * ROW + ((c ^ ((r & 1) << 2)) << 4);
+    else return r * ROW + (c << 4);
+}
+template <int ROW>
+__device__ __forceinline__ int v_off(int r, int c) {
+    if constexpr (ROW >= 128) return r * ROW + ((c ^ (((r >> 1) & 3) << 1)) << 4);
+    else return ((r >> 1) << 7) + (((r ^ (r >> 2)) & 1) << 6) + ((c ^ (((r >> 1) & 1) << 1)) << 4);
+}
+
+// max over the lanes that share lane % 4
+__device__ __forceinline__ float max_over_g(float x) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+__device__ __forceinline__ float sum_over_g(float x) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+__device__ __forceinline__ int clamp_len(const PagedParams& p, int b) {
+    const int len = __ldg(p.lens + b);
+    const long long cap = static_cast<long long>(p.max_pages) << p.shift;
+    if (len < 0 || len > cap) {
+        atomicCAS(p.err, 0u, kErrPage);
+        return len < 0 ? 0 : static_cast<int>(cap);
+    }
+    return len;
+}
+
+struct PagedShared {
+    int key0[kPagedWarps][8];     // per ring slot: first key of the tile (a bad page: past every row)
+    float ks[kPagedWarps][8], vs[kPagedWarps][8];  // 8-bit: the page's scales
+    float m[kPagedWarps][32], l[kPagedWarps][32], mv[kPagedWarps][32];
+    int scan[kPagedWarps];
+    int at_b, at_before;  // the share's first sequence, steps of the sequences before it
+};
+
+template <int D, int NT, bool F8>
+__global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_paged_kernel(const PagedParams p) {
+    using L = PagedLayout<D, NT, F8>;
+    constexpr int ROW = L::kRow, CH = ROW / 16, S = L::kStages;
+    constexpr int R = 8 * NT;           // query rows of a segment
+    constexpr int MT = D / 16;          // 16-column tiles of V^T
+    constexpr int KS = D / 16;          // 16-element steps of q.k
+    constexpr int kChunksK = D / (F8 ? 64 : 32);  // 16-byte pieces of a key row per thread
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ PagedShared sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const uint32_t ring = smem_addr(smem) + warp * L::kWarpRing;
+    griddep_launch_dependents();
+
+    // ---- this CTA's share of the steps ----
+    const int segs_per_b = p.H_kv * p.rblocks;
+    const int per = (p.B + kThreads - 1) / kThreads;
+    int mine = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = tid * per + i;
+        if (b < p.B) mine += paged_steps(paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks));
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) sh.scan[warp] = incl;
+    __syncthreads();
+    int total_b = 0, before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kPagedWarps; ++w) {
+        if (w < warp) before += sh.scan[w];
+        total_b += sh.scan[w];
+    }
+    // (no share is empty: with fewer steps than CTAs the last CTAs have none)
+    const long long total = static_cast<long long>(total_b) * segs_per_b;
+    const long long shares = min(static_cast<long long>(gridDim.x), total);
+    if (blockIdx.x >= shares) return;
+    long long x = share_start(blockIdx.x, total, shares);
+    const long long x_end = share_start(blockIdx.x + 1ll, total, shares);
+    {
+        const int xs = static_cast<int>(x / segs_per_b);  // steps of whole sequences before x, rounded down
+        if (xs >= before && xs < before + mine) {
+            int b = tid * per, at = before;
+            for (;; ++b) {
+                const int n = paged_steps(paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks));
+                if (xs < at + n) break;
+                at += n;
+            }
+            sh.at_b = b;
+            sh.at_before = at;
+        }
+    }
+    __syncthreads();
+    int b = sh.at_b;
+    long long b_first = static_cast<long long>(sh.at_before) * segs_per_b;  // first step of sequence b
+    PagedRange rg = paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks);
+    int steps = paged_steps(rg);
+
+    while (true) {
+        // ---- one piece: steps [u0, u1) of segment (b, hk, rb) ----
+        const int in_b = static_cast<int>((x - b_first) / steps);
+        const long long seg_first = b_first + static_cast<long long>(in_b) * steps;
+        const int hk = in_b / p.rblocks, rb = in_b - hk * p.rblocks;
+        const int u0 = static_cast<int>(x - seg_first);
+        const int u1 = static_cast<int>(min(static_cast<long long>(steps), x_end - seg_first));
+        const int len = rg.len;
+        const int row0 = rb * R, rows = min(R, p.G * p.Nq - row0);
+        // row r of the segment: head hk G + (row0 + r) / Nq, position (row0 + r) % Nq
+        // tiles of this warp: list entries 4 (u0 + i) + warp
+        const int nv = max(0, min(u1 - u0, (rg.n - warp + kPagedWarps - 1) / kPagedWarps - u0));
+        const auto entry = [&](int i) { return kPagedWarps * (u0 + i) + warp; };
+        const int* table = p.table + static_cast<long long>(b) * p.max_pages;
+
+        // pages of 32 tiles at a time, one per lane; the next 32 are fetched halfway
+        int pg = -1, pg_next = -1;
+        float ks = 0.f, vs = 0.f, ks_next = 0.f, vs_next = 0.f;
+        const auto fetch = [&](int base, int& page, float& k_s, float& v_s) {
+            const int i = base + lane;
+            page = -1;
+            if (i < nv) {
+                page = page_of(table, p.max_pages, p.num_pages, p.shift, rg.key0(entry(i)));
+                if (page < 0) atomicCAS(p.err, 0u, kErrPage);
+                if constexpr (F8) {
+                    if (page >= 0) {
+                        const long long ph = static_cast<long long>(page) * p.H_kv + hk;
+                        k_s = __ldg(p.k_scale + ph);
+                        v_s = __ldg(p.v_scale + ph);
+                    }
+                }
+            }
+        };
+        // first key that any row sees behind the sinks
+        const int low = p.window > 0 ? max(0, len - p.Nq - p.window + 1) : 0;
+        const auto issue = [&](int i) {
+            if (i >= nv) return;
+            if ((i & 31) == 0 && i > 0) {
+                pg = pg_next;
+                ks = ks_next;
+                vs = vs_next;
+            }
+            if ((i & 31) == 16) fetch((i & ~31) + 32, pg_next, ks_next, vs_next);
+            const int slot = i % S;
+            const int key0 = rg.key0(entry(i));
+            const int page = __shfl_sync(0xffffffffu, pg, i & 31);
+            const long long off =
+                page < 0 ? 0
+                         : (((static_cast<long long>(page) * p.H_kv + hk) << p.shift) + (key0 & ((1 << p.shift) - 1))) * ROW;
+            const uint32_t dst = ring + slot * L::kSlot;
+            const bool whole = page >= 0 && key0 + kPagedTile <= len &&
+                               (key0 >= low || key0 + kPagedTile <= p.sinks);
+            const uint8_t* ksrc = p.K + off + lane * 16;
+            const uint8_t* vsrc = p.V + off + lane * 16;
+#pragma unroll
+            for (int j = 0; j < CH / 2; ++j) {
+                const int idx = j * 32 + lane, r = idx / CH, c = idx % CH;
+                int bytes = 16;
+                if (!whole) {
+                    const int key = key0 + r;
+                    bytes = page >= 0 && key < len && (key >= low || key < p.sinks) ? 16 : 0;
+                }
+                cp_async16(dst + k_off<ROW>(r, c), ksrc + j * 512, bytes);
+                cp_async16(dst + L::kTile + v_off<ROW>(r, c), vsrc + j * 512, bytes);
+            }
+            if constexpr (F8) {
+                const float k1 = __shfl_sync(0xffffffffu, ks, i & 31), v1 = __shfl_sync(0xffffffffu, vs, i & 31);
+                if (lane == 0) {
+                    sh.ks[warp][slot] = k1;
+                    sh.vs[warp][slot] = v1;
+                }
+            }
+            if (lane == 0) sh.key0[warp][slot] = page < 0 ? 0x7fffff00 : key0;
+        };
+        fetch(0, pg, ks, vs);
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) {
+            issue(i);
+            cp_commit();
+        }
+
+        // ---- queries: the narrow operand, in the order of the key pieces ----
+        uint32_t q[NT][KS][2];
+        float rs[NT][2];  // 8-bit: 2^x that row (2 t4, 2 t4 + 1) was divided by, times tau log2 e
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = nt * 8 + g;
+            const bool in = r < rows;
+            const int rr = row0 + (in ? r : 0), hh = rr / p.Nq, qi = rr - hh * p.Nq;
+            const __nv_bfloat16* src =
+                p.Q + b * p.q_sb + static_cast<long long>(hk * p.G + hh) * p.q_sh + qi * p.q_sn;
+            if constexpr (!F8) {
+#pragma unroll
+                for (int c = 0; c < kChunksK; ++c) {
+                    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                    if (in) w = __ldg(reinterpret_cast<const uint4*>(src) + t4 + 4 * c);
+                    q[nt][2 * c][0] = w.x;
+                    q[nt][2 * c][1] = w.y;
+                    q[nt][2 * c + 1][0] = w.z;
+                    q[nt][2 * c + 1][1] = w.w;
+                }
+                rs[nt][0] = rs[nt][1] = p.scale_log2;
+            } else {
+                // key piece c of this thread holds columns 16 (t4 + 4 c) .. + 15
+                uint4 w[2 * kChunksK];
+                float m = 0.f;
+#pragma unroll
+                for (int c = 0; c < 2 * kChunksK; ++c) {
+                    w[c] = make_uint4(0u, 0u, 0u, 0u);
+                    if (in) w[c] = __ldg(reinterpret_cast<const uint4*>(src) + 2 * (t4 + 4 * (c >> 1)) + (c & 1));
+                    const uint32_t e[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        m = fmaxf(m, fmaxf(fabsf(__uint_as_float(e[i] << 16)), fabsf(__uint_as_float(e[i] & 0xffff0000u))));
+                }
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                // largest magnitude to [2^14, 2^15); a row of zeros, or with infinities, as it is
+                int ex = static_cast<int>(__float_as_uint(m) >> 23) - 127 - 14;
+                if (m == 0.f || m > 3.4e38f) ex = 0;
+                ex = max(-126, min(112, ex));
+                const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+                const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+#pragma unroll
+                for (int c = 0; c < 2 * kChunksK; ++c) {
+                    const uint32_t e[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        q[nt][2 * c + (i >> 1)][i & 1] =
+                            pack_f16(__uint_as_float(e[i] << 16) * down, __uint_as_float(e[i] & 0xffff0000u) * down);
+                }
+                rs[nt][0] = p.scale_log2 * __shfl_sync(0xffffffffu, up, 8 * t4);
+                rs[nt][1] = p.scale_log2 * __shfl_sync(0xffffffffu, up, 8 * t4 + 4);
+            }
+        }
+        int last[NT][2];  // last visible key of rows 2 t4, 2 t4 + 1 of each tile (-1: no such row)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = nt * 8 + 2 * t4 + e;
+                last[nt][e] = r < rows ? len - p.Nq + (row0 + r) % p.Nq : -1;
+            }
+
+        float acc[NT][MT][4];
+        float m_run[NT][2], l_run[NT][2], mv_run[NT][2], fac[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][j][e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                m_run[nt][e] = mv_run[nt][e] = -INFINITY;
+                l_run[nt][e] = 0.f;
+                fac[nt][e] = 0.f;
+            }
+        }
+        float vs_fac = -1.f;  // the V scale that fac was formed for
+
+        for (int i = 0; i < nv; ++i) {
+            cp_wait<S - 2>();
+            __syncwarp();
+            issue(i + S - 1);
+            cp_commit();
+            const int slot = i % S;
+            const uint32_t kt = ring + slot * L::kSlot, vt = kt + L::kTile;
+            const int key0 = sh.key0[warp][slot];
+
+            // S^T = K Q^T
+            float s[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < kChunksK; ++c) {
+                const uint4 ka = lds128(kt + k_off<ROW>(g, t4 + 4 * c)), kb = lds128(kt + k_off<ROW>(g + 8, t4 + 4 * c));
+                const uint32_t a[4] = {ka.x, ka.y, ka.z, ka.w}, bb[4] = {kb.x, kb.y, kb.z, kb.w};
+                if constexpr (!F8) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<false>(s[nt], a[2 * h], bb[2 * h], a[2 * h + 1], bb[2 * h + 1], q[nt][2 * c + h][0],
+                                            q[nt][2 * c + h][1]);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t a0, a2, a1, a3;
+                        widen4(a[h], a0, a2);
+                        widen4(bb[h], a1, a3);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<true>(s[nt], a0, a1, a2, a3, q[nt][4 * c + h][0], q[nt][4 * c + h][1]);
+                    }
+                }
+            }
+
+            // scale, mask, running max
+            const float ksc = F8 ? sh.ks[warp][slot] : 1.f;
+            const float vsc = F8 ? sh.vs[warp][slot] : 1.f;
+            const bool whole = key0 + kPagedTile <= len - p.Nq + 1 &&
+                               (p.window == 0 || key0 >= len - p.window || key0 + kPagedTile <= p.sinks);
+            bool grow = false;
+            const float lvs = F8 ? lg2(vsc) : 0.f;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[nt][e] *= F8 ? rs[nt][e & 1] * ksc : rs[nt][e & 1];
+                    if (!whole) {
+                        const int key = key0 + g + (e & 2 ? 8 : 0), la = last[nt][e & 1];
+                        const bool see = key <= la && (p.window == 0 || key > la - p.window || key < p.sinks);
+                        if (!see) s[nt][e] = -INFINITY;
+                    }
+                    grow |= s[nt][e] > m_run[nt][e & 1] + kGrow;
+                    if (F8) grow |= s[nt][e] + lvs > mv_run[nt][e & 1] + kGrow;
+                }
+            bool refac = F8 && vsc != vs_fac;
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float mx = max_over_g(fmaxf(s[nt][e], s[nt][e + 2]));
+                        const float m_new = fmaxf(m_run[nt][e], mx);
+                        const float alpha = m_new == -INFINITY ? 1.f : ex2(m_run[nt][e] - m_new);
+                        l_run[nt][e] *= alpha;
+                        float beta = alpha;
+                        if constexpr (F8) {
+                            const float mv_new = fmaxf(mv_run[nt][e], mx + lvs);
+                            beta = mv_new == -INFINITY ? 1.f : ex2(mv_run[nt][e] - mv_new);
+                            mv_run[nt][e] = mv_new;
+                        }
+                        m_run[nt][e] = m_new;
+#pragma unroll
+                        for (int j = 0; j < MT; ++j) {
+                            acc[nt][j][e] *= beta;
+                            acc[nt][j][e + 2] *= beta;
+                        }
+                    }
+                refac = true;
+            }
+            if (F8 && refac) {
+                vs_fac = vsc;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        fac[nt][e] = mv_run[nt][e] == -INFINITY ? 0.f : vsc * ex2(m_run[nt][e] - mv_run[nt][e]);
+            }
+
+            // P^T, from the accumulator's layout to the operand's
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float mm = m_run[nt][e & 1];
+                    w[e] = ex2(s[nt][e] - (mm == -INFINITY ? 0.f : mm));
+                }
+                l_run[nt][0] += w[0] + w[2];
+                l_run[nt][1] += w[1] + w[3];
+                if constexpr (F8) {
+                    pb[nt][0] = movmatrix(pack_f16(w[0] * fac[nt][0], w[1] * fac[nt][1]));
+                    pb[nt][1] = movmatrix(pack_f16(w[2] * fac[nt][0], w[3] * fac[nt][1]));
+                } else {
+                    pb[nt][0] = movmatrix(pack_bf16(w[0], w[1]));
+                    pb[nt][1] = movmatrix(pack_bf16(w[2], w[3]));
+                }
+            }
+
+            // O^T += V^T P^T: element e of this thread's columns of rows 2 t4, 2 t4 + 1 (lo)
+            // and 2 t4 + 8, 2 t4 + 9 (hi); tile j takes elements 2 j and 2 j + 1
+            if constexpr (!F8) {
+#pragma unroll
+                for (int c = 0; c < CH / 8; ++c) {
+                    const int ch = g + 8 * c;
+                    const uint4 x0 = lds128(vt + v_off<ROW>(2 * t4, ch)), x1 = lds128(vt + v_off<ROW>(2 * t4 + 1, ch));
+                    const uint4 y0 = lds128(vt + v_off<ROW>(2 * t4 + 8, ch)), y1 = lds128(vt + v_off<ROW>(2 * t4 + 9, ch));
+                    const uint32_t a[4] = {x0.x, x0.y, x0.z, x0.w}, a1[4] = {x1.x, x1.y, x1.z, x1.w};
+                    const uint32_t bb[4] = {y0.x, y0.y, y0.z, y0.w}, b1[4] = {y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t lo0 = __byte_perm(a[j], a1[j], 0x5410), lo1 = __byte_perm(a[j], a1[j], 0x7632);
+                        const uint32_t hi0 = __byte_perm(bb[j], b1[j], 0x5410), hi1 = __byte_perm(bb[j], b1[j], 0x7632);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<false>(acc[nt][4 * c + j], lo0, lo1, hi0, hi1, pb[nt][0], pb[nt][1]);
+                    }
+                }
+            } else {
+                constexpr int W = D / 32;  // words of a row per thread (16 columns at d = 128, 8 at 64)
+                uint32_t a[4][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = 2 * t4 + (k & 1) + (k >> 1) * 8;
+                    if constexpr (D == 128) {
+                        const uint4 w = lds128(vt + v_off<ROW>(r, g));
+                        a[k][0] = w.x;
+                        a[k][1] = w.y;
+                        a[k][2] = w.z;
+                        a[k][3] = w.w;
+                    } else {
+                        const uint2 w = lds64(vt + v_off<ROW>(r, g >> 1) + (g & 1) * 8);
+                        a[k][0] = w.x;
+                        a[k][1] = w.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < W; ++j) {
+                    uint32_t f[8];  // [lo: elements 4 j .. 4 j + 3, hi: the same]
+                    widen4(__byte_perm(a[0][j], a[1][j], 0x5140), f[0], f[1]);
+                    widen4(__byte_perm(a[0][j], a[1][j], 0x7362), f[2], f[3]);
+                    widen4(__byte_perm(a[2][j], a[3][j], 0x5140), f[4], f[5]);
+                    widen4(__byte_perm(a[2][j], a[3][j], 0x7362), f[6], f[7]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma16816<true>(acc[nt][2 * j], f[0], f[1], f[4], f[5], pb[nt][0], pb[nt][1]);
+                        mma16816<true>(acc[nt][2 * j + 1], f[2], f[3], f[6], f[7], pb[nt][0], pb[nt][1]);
+                    }
+                }
+            }
+        }
+        cp_wait<0>();
+
+        // ---- join the four warps ----
+        // (row sums and weights: over the lanes that share t4)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l_run[nt][e] = sum_over_g(l_run[nt][e]);
+                if (g == 0) {
+                    sh.m[warp][nt * 8 + 2 * t4 + e] = m_run[nt][e];
+                    sh.l[warp][nt * 8 + 2 * t4 + e] = l_run[nt][e];
+                    if (F8) sh.mv[warp][nt * 8 + 2 * t4 + e] = mv_run[nt][e];
+                }
+            }
+        __syncthreads();
+        const bool final_piece = u0 == 0 && u1 == steps;
+        const long long slot = 2ll * blockIdx.x + (u0 == 0 ? 1 : 0);
+        float* red = reinterpret_cast<float*>(smem);  // [warp][8 rows][D]
+        const auto log_sum = [&](int r, float& m_all) {  // log2 of the row's sum, and its max
+            m_all = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]), fmaxf(sh.m[2][r], sh.m[3][r]));
+            const float ref = m_all == -INFINITY ? 0.f : m_all;
+            float sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kPagedWarps; ++w) sum += sh.l[w][r] * ex2(sh.m[w][r] - ref);
+            return ref + lg2(sum);  // -inf for a row that sees nothing, NaN where a score was
+        };
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = nt * 8 + 2 * t4 + e;
+                float m_all;
+                const float ls = log_sum(r, m_all);
+                const float ref = F8 ? mv_run[nt][e] : m_run[nt][e];
+                const float f = ls == -INFINITY || (ref == -INFINITY && ls == ls) ? 0.f : ex2(ref - ls);
+                float* dst = red + (warp * 8 + 2 * t4 + e) * D;
+#pragma unroll
+                for (int j = 0; j < MT; ++j) {
+                    // columns of elements 2 j and 2 j + 1
+                    const int col = F8 ? (D / 8) * g + 2 * j : 64 * (j / 4) + 8 * g + 2 * (j % 4);
+                    *reinterpret_cast<float2*>(dst + col) = make_float2(acc[nt][j][e] * f, acc[nt][j][e + 2] * f);
+                }
+            }
+            __syncthreads();
+            for (int e = tid; e < 8 * (D / 4); e += kThreads) {
+                const int rl = e / (D / 4), col = (e % (D / 4)) * 4, r = nt * 8 + rl;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kPagedWarps; ++w) {
+                    const float4 y = *reinterpret_cast<const float4*>(red + (w * 8 + rl) * D + col);
+                    o.x += y.x;
+                    o.y += y.y;
+                    o.z += y.z;
+                    o.w += y.w;
+                }
+                if (r < rows) {
+                    if (final_piece) {
+                        const int hh = (row0 + r) / p.Nq, qi = (row0 + r) - hh * p.Nq;
+                        __nv_bfloat16* dst = p.O + b * p.o_sb + static_cast<long long>(hk * p.G + hh) * p.o_sh + qi * p.o_sn + col;
+                        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+                    } else {
+                        *reinterpret_cast<float4*>(p.part_o + (slot * R + r) * D + col) = o;
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        if (tid < rows) {
+            float m_all;
+            const float ls = log_sum(tid, m_all);
+            if (final_piece) {
+                const int hh = (row0 + tid) / p.Nq, qi = (row0 + tid) - hh * p.Nq;
+                p.LSE[(static_cast<long long>(b) * p.H + hk * p.G + hh) * p.Nq + qi] = ls * kLn2;
+            } else {
+                p.part_l[slot * R + tid] = ls;
+            }
+        }
+        if (u0 == 0 && tid == 0) {
+            const int pieces =
+                final_piece ? 1 : static_cast<int>(share_of(seg_first + steps - 1, total, shares) - blockIdx.x) + 1;
+            p.seg[static_cast<long long>(b) * segs_per_b + in_b] = make_int2(static_cast<int>(blockIdx.x), pieces);
+        }
+        x = seg_first + u1;
+        if (x >= x_end) return;
+        __syncthreads();  // (sh.m, sh.l are read above)
+        if (x >= b_first + static_cast<long long>(steps) * segs_per_b) {
+            b_first += static_cast<long long>(steps) * segs_per_b;
+            ++b;
+            rg = paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks);
+            steps = paged_steps(rg);
+        }
+    }
+}
+
+// Adds a segment's pieces: O = sum_s 2^(l_s - L) O_s, L = log2 sum_s 2^(l_s).  One block
+// per segment and eight rows, one warp per row.
+template <int D, int NT>
+__global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams p) {
+    constexpr int R = 8 * NT, PER = D / 32;
+    griddep_wait();
+    const int segs_per_b = p.H_kv * p.rblocks;
+    const int2 sg = p.seg[blockIdx.x];
+    if (sg.y <= 1) return;
+    const int b = static_cast<int>(blockIdx.x) / segs_per_b, in_b = static_cast<int>(blockIdx.x) - b * segs_per_b;
+    const int hk = in_b / p.rblocks, rb = in_b - hk * p.rblocks;
+    const int row0 = rb * R, rows = min(R, p.G * p.Nq - row0);
+    const int r = static_cast<int>(blockIdx.y) * 8 + static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (r >= rows) return;
+    // piece 0 lies in its share's second slot (it ends the share), the others in their first
+    const auto at = [&](int s) { return (2ll * (sg.x + s) + (s == 0 ? 1 : 0)) * R + r; };
+    float m = -INFINITY;
+    for (int s = lane; s < sg.y; s += 32) m = fmaxf(m, p.part_l[at(s)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+    float sum = 0.f;
+    float acc[PER];
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    for (int s0 = 0; s0 < sg.y; s0 += 32) {
+        const float w = s0 + lane < sg.y ? ex2(p.part_l[at(s0 + lane)] - ref) : 0.f;
+        sum += w;
+        const int n = min(32, sg.y - s0);
+#pragma unroll 8
+        for (int s = 0; s < n; ++s) {
+            const float ws = __shfl_sync(0xffffffffu, w, s);
+            const float* src = p.part_o + at(s0 + s) * D + lane * PER;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] = fmaf(ws, src[e], acc[e]);
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int hh = (row0 + r) / p.Nq, qi = (row0 + r) - hh * p.Nq, h = hk * p.G + hh;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (0: the row sees nothing)
+    __nv_bfloat16* dst = p.O + b * p.o_sb + static_cast<long long>(h) * p.o_sh + qi * p.o_sn + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; e += 2)
+        *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    if (lane == 0)
+        p.LSE[(static_cast<long long>(b) * p.H + h) * p.Nq + qi] = (ref + lg2(sum)) * kLn2;
+}
+
+// Query rows per segment: 8 for up to 8 rows, 16 for up to 16, else 32 (more row blocks
+// read the keys again, from L2).
+int row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+
+template <int D, int NT, bool F8>
+constexpr int ctas_per_sm() { return PagedLayout<D, NT, F8>::kCtas; }
+
+int ctas_for(int d, int nt, bool fp8) {
+    if (d == 64) {
+        if (nt == 1) return fp8 ? ctas_per_sm<64, 1, true>() : ctas_per_sm<64, 1, false>();
+        if (nt == 2) return fp8 ? ctas_per_sm<64, 2, true>() : ctas_per_sm<64, 2, false>();
+        return fp8 ? ctas_per_sm<64, 4, true>() : ctas_per_sm<64, 4, false>();
+    }
+    if (nt == 1) return fp8 ? ctas_per_sm<128, 1, true>() : ctas_per_sm<128, 1, false>();
+    if (nt == 2) return fp8 ? ctas_per_sm<128, 2, true>() : ctas_per_sm<128, 2, false>();
+    return fp8 ? ctas_per_sm<128, 4, true>() : ctas_per_sm<128, 4, false>();
+}
+
+// Workspace: segment headers, then the pieces' sums and outputs, each 256-aligned.
+struct PagedPlan {
+    int nt, rblocks, shares;
+    long long segs;
+    size_t part_l, part_o, bytes;
+};
+PagedPlan paged_plan(int B, int H, int H_kv, int Nq, int d, bool fp8) {
+    const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    PagedPlan pl;
+    const int rows = H / H_kv * Nq;
+    pl.nt = row_tiles(rows);
+    pl.rblocks = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
+    pl.shares = kSms * ctas_for(d, pl.nt, fp8);
+    pl.segs = static_cast<long long>(B) * H_kv * pl.rblocks;
+    const size_t part_rows = static_cast<size_t>(2) * pl.shares * 8 * pl.nt;
+    pl.part_l = up(static_cast<size_t>(pl.segs) * sizeof(int2));
+    pl.part_o = pl.part_l + up(part_rows * sizeof(float));
+    pl.bytes = pl.part_o + part_rows * d * sizeof(float);
+    return pl;
+}
+
+template <int D, int NT, bool F8>
+cudaError_t launch_paged_t(const PagedArgs& a, const PagedPlan& pl, PagedParams& p, cudaStream_t stream) {
+    using L = PagedLayout<D, NT, F8>;
+    constexpr auto kern = &fa_paged_kernel<D, NT, F8>;
+    cudaError_t e = set_max_dyn_smem_once<kern>(L::kBytes);
+    if (e != cudaSuccess) return e;
+    if (a.ev_start) cudaEventRecord(a.ev_start, stream);
+    kern<<<static_cast<unsigned>(pl.shares), kThreads, L::kBytes, stream>>>(p);
+    e = cudaGetLastError();
+    if (e == cudaSuccess)
+        e = launch_dependent(fa_paged_combine_kernel<D, NT>, dim3(static_cast<unsigned>(pl.segs), NT), dim3(256), 0,
+                             stream, p);
+    if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
+    return e;
+}
+
+}  // namespace
+
+size_t paged_workspace(int B, int H, int H_kv, int Nq, int d, bool fp8) {
+    return paged_plan(B, H, H_kv, Nq, d, fp8).bytes;
+}
+
+long long paged_max_steps(int B, int H, int H_kv, int Nq, int max_pages, int shift) {
+    const int rows = H / H_kv * Nq, nt = row_tiles(rows);
+    const long long rblocks = (rows + 8 * nt - 1) / (8 * nt);
+    const long long steps = ((static_cast<long long>(max_pages) << shift) + 63) / 64 + 1;
+    return rblocks * H_kv * B * steps;
+}
+
+cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream) {
+    const bool fp8 = a.cache.k_scale != nullptr;
+    const PagedPlan pl = paged_plan(a.cache.B, a.H, a.cache.H_kv, a.Nq, a.cache.d, fp8);
+    PagedParams p;
+    p.Q = static_cast<const __nv_bfloat16*>(a.Q);
+    p.K = static_cast<const uint8_t*>(a.cache.K);
+    p.V = static_cast<const uint8_t*>(a.cache.V);
+    p.k_scale = a.cache.k_scale;
+    p.v_scale = a.cache.v_scale;
+    p.table = a.cache.page_table;
+    p.lens = a.cache.lens;
+    p.O = static_cast<__nv_bfloat16*>(a.O);
+    p.LSE = a.LSE;
+    uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+    p.seg = reinterpret_cast<int2*>(ws);
+    p.part_l = reinterpret_cast<float*>(ws + pl.part_l);
+    p.part_o = reinterpret_cast<float*>(ws + pl.part_o);
+    p.q_sb = a.q_sb;
+    p.q_sh = a.q_sh;
+    p.q_sn = a.q_sn;
+    p.o_sb = a.o_sb;
+    p.o_sh = a.o_sh;
+    p.o_sn = a.o_sn;
+    p.B = a.cache.B;
+    p.H = a.H;
+    p.H_kv = a.cache.H_kv;
+    p.G = a.H / a.cache.H_kv;
+    p.Nq = a.Nq;
+    p.rblocks = pl.rblocks;
+    p.num_pages = a.cache.num_pages;
+    p.max_pages = a.cache.max_pages;
+    p.shift = a.cache.shift;
+    p.window = a.window;
+    p.sinks = a.window > 0 ? a.sinks : 0;
+    p.scale_log2 = a.tau * kLog2e;
+    p.err = a.err;
+    const int key = (a.cache.d == 128 ? 8 : 0) + (fp8 ? 4 : 0) + (pl.nt == 1 ? 0 : pl.nt == 2 ? 1 : 2);
+    switch (key) {
+        case 0: return launch_paged_t<64, 1, false>(a, pl, p, stream);
+        case 1: return launch_paged_t<64, 2, false>(a, pl, p, stream);
+        case 2: return launch_paged_t<64, 4, false>(a, pl, p, stream);
+        case 4: return launch_paged_t<64, 1, true>(a, pl, p, stream);
+        case 5: return launch_paged_t<64, 2, true>(a, pl, p, stream);
+        case 6: return launch_paged_t<64, 4, true>(a, pl, p, stream);
+        case 8: return launch_paged_t<128, 1, false>(a, pl, p, stream);
+        case 9: return launch_paged_t<128, 2, false>(a, pl, p, stream);
+        case 10: return launch_paged_t<128, 4, false>(a, pl, p, stream);
+        case 12: return launch_paged_t<128, 1, true>(a, pl, p, stream);
+        case 13: return launch_paged_t<128, 2, true>(a, pl, p, stream);
+        default: return launch_paged_t<128, 4, true>(a, pl, p, stream);
+    }
+}
+
+}  // namespace fa

@@ -53,10 +53,11 @@ extern "C" {
 typedef enum fa_status {
     FA_OK = 0,
     FA_ERR_INVALID_ARG = 1,  /* null/misaligned pointer, negative size, bad tau, overlap */
-    FA_ERR_UNSUPPORTED = 2,  /* d not in {64, 128}, or no sm_103a device */
+    FA_ERR_UNSUPPORTED = 2,  /* d not in {64, 128}, a size limit, or no sm_103a device */
     FA_ERR_WORKSPACE = 3,    /* workspace given but smaller than fa_bwd_workspace_size */
     FA_ERR_CUDA = 4,         /* a CUDA runtime call or kernel launch failed */
-    FA_ERR_TIMEOUT = 5       /* a kernel's bounded pipeline wait ran out */
+    FA_ERR_TIMEOUT = 5,      /* a kernel's bounded pipeline wait ran out */
+    FA_ERR_PAGE = 6          /* a cache length, token count or page number out of bounds */
 } fa_status;
 
 /*
@@ -110,8 +111,9 @@ FA_API const char* fa_status_string(fa_status s);
 /*
  * Synchronises `stream`, then reads and clears the library's device error
  * word for the current device.  FA_ERR_TIMEOUT if some kernel launched since
- * the last call gave up on a bounded wait, FA_ERR_CUDA if the stream reports
- * an error, else FA_OK.
+ * the last call gave up on a bounded wait, FA_ERR_PAGE if one met a cache
+ * length, token count or page number out of bounds (see fa_paged_cache),
+ * FA_ERR_CUDA if the stream reports an error, else FA_OK.
  */
 FA_API fa_status fa_last_device_error(void* stream);
 
@@ -151,6 +153,30 @@ FA_API fa_status fa_bwd_window(const void* Q, const void* K, const void* V, cons
                                const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
                                void* workspace, size_t workspace_bytes, int B, int H, int N, int d,
                                float tau, int window, void* stream);
+
+/*
+ * Sliding-window attention with sinks, forward: a causal window beside the first
+ * `sinks` keys of the sequence, which every later query goes on seeing ("Atencao
+ * eficiente - FlashAttention, sparse e hibrida", section "Sparse e hibrida": a
+ * local window plus global anchor tokens; here element by element).  Key j is
+ * visible from query i iff j <= i and (j > i - window or j < sinks).  Same buffers
+ * and conventions as fa_fwd_window; key blocks that hold neither a sink nor a key
+ * of some row's window are never loaded.  window >= 1 and sinks >= 0 (else
+ * FA_ERR_INVALID_ARG); sinks = 0 is fa_fwd_window, and window + sinks >= N plain
+ * causal attention.
+ */
+FA_API fa_status fa_fwd_sinks(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                              int B, int H, int N, int d, float tau, int window, int sinks,
+                              void* stream);
+
+/*
+ * Backward for the mask of fa_fwd_sinks (LSE must come from fa_fwd_sinks with the
+ * same window and sinks).  Same workspace rules as fa_bwd.
+ */
+FA_API fa_status fa_bwd_sinks(const void* Q, const void* K, const void* V, const void* O,
+                              const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
+                              void* workspace, size_t workspace_bytes, int B, int H, int N, int d,
+                              float tau, int window, int sinks, void* stream);
 
 /*
  * Block-sparse attention, forward ("FlashAttention e o gargalo real de
@@ -213,6 +239,112 @@ FA_API size_t fa_decode_workspace_size(int B, int H, int Nq, int Nk, int d);
 FA_API fa_status fa_fwd_decode(const void* Q, const void* K, const void* V, void* O, float* LSE,
                                int B, int H, int Nq, int Nk, int d, float tau, int causal,
                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A paged key/value cache: sequence b's key j lies in page
+ * page_table[b][j / page_size], row j % page_size ("Atencao eficiente -
+ * FlashAttention, sparse e hibrida", box "FlashAttention nao acelera o decode
+ * token a token": the cache that each decode step reads and extends).
+ *   K, V            [num_pages][H_kv][page_size][d], bf16, or e4m3 bytes for the
+ *                   _fp8 entry points; 16-byte aligned, contiguous
+ *   k_scale,v_scale fp32 [num_pages][H_kv], finite and > 0: the value of a code is
+ *                   code * scale of its page and head.  NULL for a bf16 cache.
+ *   page_table      int [B][max_pages]; lens: int [B] (4-byte aligned)
+ * page_size is a power of two from 16 to 256, max_pages * page_size at most 2^30 and
+ * d 64 or 128 (else FA_ERR_UNSUPPORTED).  Table and lengths are device data, read on the stream, so a
+ * captured call can be replayed while they change.  Entries behind a sequence's
+ * pages are not read.  A length below 0 or above max_pages * page_size, a page number
+ * outside [0, num_pages) that is needed, and token counts that do not ascend within
+ * [0, T] are not followed: fa_last_device_error then returns FA_ERR_PAGE, and each
+ * entry point says what it did instead.  The description itself is host memory and
+ * only read during the call; the caller owns all buffers.
+ */
+typedef struct fa_paged_cache {
+    void* K;
+    void* V;
+    float* k_scale;
+    float* v_scale;
+    const int* page_table;
+    const int* lens;
+    int B, H_kv, d, num_pages, page_size, max_pages;
+} fa_paged_cache;
+
+/*
+ * Appends the keys and values of T new tokens to a bf16 paged cache, rotating the
+ * keys (and, given q, the same tokens' queries) by their position on the way.
+ * Sequence b brings the rows cu_new[b] <= t < cu_new[b + 1] (device int [B + 1],
+ * ascending; NULL: T / B rows each, T a multiple of B); row t stands at position
+ * p = lens[b] + t - cu_new[b], where lens[b] keys are in the cache already (the
+ * caller adds the new tokens to lens afterwards).  Rows from cu_new[B] on are
+ * ignored: nothing of them is written, q_out included.
+ *
+ * k, v: bf16 [T][H_kv][d] and q, q_out: bf16 [T][H][d] with the given (token, head)
+ * strides in elements, columns contiguous, 16-byte aligned, strides multiples of 8
+ * and not negative: slices of one projection's output pass as they are.  q_out may be
+ * q itself with the same strides.  q NULL: H = 0, no queries.
+ * The first rot columns (a multiple of 16, at most d) turn: pair c, columns (c,
+ * c + rot / 2) or with interleaved = 1 (2c, 2c + 1), goes from (x, y) to
+ * (x cos a - y sin a, y cos a + x sin a), a = p * inv_freq[c] (device double
+ * [rot / 2], radians per position), exact at any position and rounded once to bf16.
+ * rot = 0 with inv_freq NULL (and no q): nothing turns.
+ * A token whose position or page is out of bounds is not stored (FA_ERR_PAGE); its
+ * query is rotated all the same.  No two sequences may append to the same page.
+ */
+FA_API fa_status fa_kv_append(const fa_paged_cache* cache, const void* k, const long long* k_strides,
+                              const void* v, const long long* v_strides, int T, const int* cu_new,
+                              const void* q, const long long* q_strides, void* q_out,
+                              const long long* q_out_strides, int H, const double* inv_freq, int rot,
+                              int interleaved, void* stream);
+
+/*
+ * fa_kv_append into an e4m3 cache.  Each page has one scale per head for K and one
+ * for V, set here: the smallest power of two s (2^-100 at least) with bound <= 448 s,
+ * where bound is the largest magnitude of the page's new values, and for rotated keys
+ * 1.5 times their largest magnitude before the rotation (a turned pair is at most
+ * sqrt(2) times its larger half).  Values are rounded once, from fp32, to the nearest
+ * e4m3 (ties to even; infinities become +-448 s, NaN stays NaN).  A page that held
+ * keys before the call keeps the larger of its scale and the new one, and where that
+ * grows its codes are rescaled, rounded to nearest even.  A page whose first row is
+ * new takes the new scale.
+ */
+FA_API fa_status fa_kv_append_fp8(const fa_paged_cache* cache, const void* k,
+                                  const long long* k_strides, const void* v,
+                                  const long long* v_strides, int T, const int* cu_new, const void* q,
+                                  const long long* q_strides, void* q_out,
+                                  const long long* q_out_strides, int H, const double* inv_freq,
+                                  int rot, int interleaved, void* stream);
+
+/*
+ * Attention of a decode step over a bf16 paged cache: fa_fwd_decode for sequences of
+ * uneven length in pages, with grouped heads and, if asked for, a window with sinks.
+ * The Nq (1..8, else FA_ERR_UNSUPPORTED) query rows of sequence b are the last Nq of
+ * its lens[b] positions (lens counts them): row i sees key j iff
+ *   j <= lens[b] - Nq + i, and with window > 0 also
+ *   j > lens[b] - Nq + i - window or j < sinks.
+ * Query head h reads key head h / (H / H_kv); H is a multiple of H_kv.  A row that
+ * sees no key (lens[b] < Nq, or 0) is the empty sum: O = 0 and LSE = -inf.
+ * Q, O: bf16 [B][H][Nq][d] with the given (sequence, head, row) strides in elements,
+ * columns contiguous, 16-byte aligned, strides multiples of 8 and not negative; O's
+ * rows must not overlap.  LSE: fp32 [B][H][Nq] contiguous.  window = 0: none;
+ * sinks > 0 needs a window.  Rows of a page behind a sequence's end, and keys hidden
+ * from every row of the call, are never read.
+ * workspace: fa_paged_workspace_size bytes (it does not depend on the lengths); NULL:
+ * taken with cudaMallocAsync and given back.  Two calls that may run at the same time
+ * need two workspaces.  A length out of bounds is cut to the table's, and keys on a
+ * page out of bounds are hidden (FA_ERR_PAGE).  More than 2^31 64-key steps in a full
+ * table are FA_ERR_UNSUPPORTED.
+ */
+FA_API size_t fa_paged_workspace_size(int B, int H, int H_kv, int Nq, int d, int fp8);
+FA_API fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* Q, const long long* q_strides,
+                              void* O, const long long* o_strides, float* LSE, int H, int Nq,
+                              float tau, int window, int sinks, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* fa_fwd_paged over an e4m3 cache (workspace: fa_paged_workspace_size with fp8 = 1). */
+FA_API fa_status fa_fwd_paged_fp8(const fa_paged_cache* cache, const void* Q,
+                                  const long long* q_strides, void* O, const long long* o_strides,
+                                  float* LSE, int H, int Nq, float tau, int window, int sinks,
+                                  void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * FP8 forward ("Atencao eficiente - FlashAttention, sparse e hibrida", the

@@ -1,0 +1,408 @@
+"""GPU parity of fa_fwd_paged and fa_fwd_paged_fp8 with the plain 64-bit form.
+
+Tolerances, per element, from the exact weights P and scores s (natural units):
+  scores  fp32 sums of d exact products and two scalings: off by ds <= (d + 4) 2^-24 tau sum_c |q_c k_c|;
+  weights off by e^(2 ds) - 1 (numerator and sum) plus 2^-20 for the exponentials and logarithms,
+          and rounded to bf16 (2^-8; fp16 for 8-bit pages: 2^-11) in the numerator only;
+  O       rounded once more (2^-8 |O|); fp32 sums over n keys in pieces: at most 2^-24 * 64 + 2^-18 in all;
+  LSE     2 ds + 2^-19 + 2^-23 |LSE|."""
+import math
+
+import pytest
+import torch
+
+from exact_io_aware_12_gb300 import api, _lib
+from tests import _plain
+from tests._plain import BF16_HALF, FP16_HALF, FP32_HALF
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def build(lens, H, Hkv, Nq, d, page, fp8, seed, poison=True, q_gain=1.0, one_scale=False):
+    g = torch.Generator().manual_seed(seed)
+    P, table = _plain.make_pages(lens, page, g)
+    s = dict(table=table, lens=torch.tensor(lens, dtype=torch.int32),
+             q=(q_gain * torch.randn(len(lens), H, Nq, d, generator=g)).to(torch.bfloat16))
+    for n in "kv":
+        x = torch.randn(P, Hkv, page, d, generator=g)
+        if fp8:
+            sc = 2.0 ** torch.randint(-9, -6, (P, Hkv), generator=g).float()
+            if not one_scale:   # (any positive scale is allowed)
+                sc = sc * (1 + torch.rand(P, Hkv, generator=g))
+            x = (x / sc[:, :, None, None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+            s[n + "_scale"] = sc
+        else:
+            x = x.to(torch.bfloat16)
+            s[n + "_scale"] = None
+        if poison:
+            # rows behind a sequence's end, and pages of no sequence, hold NaN
+            raw = x.view(torch.uint8) if fp8 else x.view(torch.int16)
+            used = torch.zeros(P, page, dtype=torch.bool)
+            for b, ln in enumerate(lens):
+                j = torch.arange(ln)
+                used[table[b, j // page].long(), j % page] = True
+            raw[~used[:, None].expand(P, Hkv, page)] = 0x7F if fp8 else 0x7FC0
+        s[n + "c"] = x
+    return s
+
+
+def run(s, window=None, sinks=0, **kw):
+    dev = {n: (t.to(DEV) if t is not None else None) for n, t in s.items()}
+    o, lse = api.fwd_paged(dev["q"], dev["kc"], dev["vc"], dev["table"], dev["lens"], window=window, sinks=sinks,
+                           k_scale=dev["k_scale"], v_scale=dev["v_scale"], **kw)
+    torch.cuda.synchronize()
+    return o.cpu(), lse.cpu()
+
+
+def check(s, window=None, sinks=0, got=None, tau=None, seqs=None):
+    """Compares with the plain form, sequence by sequence."""
+    o, lse = got if got is not None else run(s, window, sinks, **({} if tau is None else dict(tau=tau)))
+    B, H, Nq, d = s["q"].shape
+    fp8 = s["k_scale"] is not None
+    Hkv = s["kc"].shape[1]
+    tau = 1 / math.sqrt(d) if tau is None else tau
+    for b in (range(B) if seqs is None else seqs):
+        n = int(s["lens"][b])
+        k, v = (_plain.gather(s[c + "c"], s["table"][b], n, s[c + "_scale"]) for c in "kv")
+        k, v = (x.repeat_interleave(H // Hkv, 0) for x in (k, v))
+        see = _plain.visible(Nq, n, window or 0, sinks)
+        any_row = see.any(0)
+        k, v = (torch.where(any_row[None, :, None], x, torch.zeros_like(x)) for x in (k, v))
+        q = s["q"][b].double()
+        ref, l_ref, p = _plain.attention(q, k, v, tau, see)
+        ds = (d + 4) * FP32_HALF * tau * (q.abs() @ k.abs().transpose(-1, -2))
+        ds = torch.where(see, ds, torch.zeros_like(ds)).amax(-1, keepdim=True) if n else torch.zeros(H, Nq, 1)
+        spread = p @ v.abs()                    # sum_j P |v|
+        w = torch.expm1(2 * ds) + 2.0 ** -20 + (FP16_HALF if fp8 else BF16_HALF)
+        tol = w * spread + BF16_HALF * ref.abs() + (64 * FP32_HALF + 2.0 ** -18) * spread + 1e-30
+        off = (o[b].double() - ref).abs()
+        assert bool((off <= tol).all()), f"sequence {b} (len {n}): O off by {float(off.max())}, {float((off - tol).max())} over"
+        fin = torch.isfinite(l_ref)
+        assert torch.equal(fin, torch.isfinite(lse[b])) and bool((lse[b][~fin] == -math.inf).all())
+        l_tol = 2 * ds[..., 0] + 2.0 ** -19 + 2 * FP32_HALF * l_ref.abs()
+        assert bool(((lse[b].double() - l_ref).abs()[fin] <= l_tol[fin]).all()), f"sequence {b}: LSE"
+        assert bool((o[b][~fin] == 0).all())
+    return o, lse
+
+
+# lengths 0 and 1, fewer keys than rows, page and tile borders, several shares
+LENS = [0, 1, 2, 7, 15, 16, 17, 63, 64, 65, 127, 130, 300, 1000, 4097]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hkv,Nq,page", [(1, 1, 1, 16), (4, 4, 1, 32), (8, 1, 1, 64), (12, 4, 2, 64), (16, 2, 1, 128),
+                                           (6, 2, 5, 16), (8, 2, 8, 256), (20, 1, 2, 32), (24, 3, 8, 64), (3, 1, 7, 64)])
+def test_paged_matches_plain(H, Hkv, Nq, page, d, fp8):
+    s = build(LENS, H, Hkv, Nq, d, page, fp8, seed=H + Hkv + Nq + d)
+    check(s)
+    assert api.last_device_error() == _lib.FA_OK
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 3), (16, 16), (64, 0), (100, 17), (128, 200), (5000, 4)])
+def test_window_and_sinks(window, sinks, fp8):
+    for H, Hkv, Nq, d, page in ((4, 2, 1, 128, 64), (6, 3, 4, 64, 16), (16, 1, 8, 128, 32)):
+        s = build(LENS, H, Hkv, Nq, d, page, fp8, seed=window + sinks + Nq)
+        check(s, window, sinks)
+    assert api.last_device_error() == _lib.FA_OK
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_random_batches(fp8):
+    g = torch.Generator().manual_seed(4)
+    r = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))
+    for i in range(30):
+        Hkv, G, Nq = r(1, 5), r(1, 9), r(1, 8)
+        lens = [r(0, 10 ** r(1, 3) * 3) for _ in range(r(1, 40))]
+        window = r(1, 700) if r(0, 1) else None
+        check(build(lens, Hkv * G, Hkv, Nq, 64 * r(1, 2), 16 << r(0, 4), fp8, seed=i), window, r(0, 90) if window else 0)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_long_and_many(fp8):
+    """One long cache cut into a piece per resident CTA, and many short ones (whole segments)."""
+    check(build([70001], 8, 2, 1, 128, 64, fp8, seed=1))
+    check(build([40000, 3], 2, 1, 4, 64, 16, fp8, seed=2))
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 200, (700,), generator=g).tolist()
+    check(build(lens, 4, 2, 1, 64, 32, fp8, seed=4), seqs=list(range(0, 700, 37)) + [699])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_peaked_and_flat_scores(fp8):
+    """One dominant key, equal scores, and scores that rise along the keys by far more than the
+    running max's slack."""
+    s = build([500], 4, 2, 1, 128, 32, fp8, seed=5, q_gain=30.0)
+    check(s)
+    s = build([500], 4, 2, 2, 128, 32, fp8, seed=6)
+    s["q"].zero_()
+    check(s)
+    s = build([600], 2, 1, 1, 64, 16, fp8, seed=7, one_scale=True)
+    ids = s["table"][0].long()
+    for j in range(600):
+        row = torch.full((64,), (j - 300) / 300.0)
+        at = (ids[j // 16], 0, j % 16)
+        if fp8:
+            s["kc"].view(torch.uint8)[at] = (row / s["k_scale"][at[0], 0]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        else:
+            s["kc"][at] = row.bfloat16()
+    s["q"].fill_(40.0)
+    check(s)
+
+
+def test_8_bit_pages_of_very_different_scales():
+    """V scales from 2^-60 to 2^60 page by page, the large ones under small weights and the other way
+    round: each row's error stays relative to what it sums."""
+    for up in (True, False):
+        s = build([320], 4, 2, 1, 128, 16, True, seed=8, one_scale=True)
+        ids = s["table"][0, :20].long()
+        e = torch.linspace(-60, 60, 20).round()
+        s["v_scale"][ids] = (2.0 ** (e if up else -e))[:, None].float().expand(20, 2).contiguous()
+        check(s)
+        s["k_scale"][ids] = (2.0 ** torch.linspace(-14, -7, 20).round())[:, None].expand(20, 2).contiguous()
+        check(s)
+    # rows of large and tiny queries
+    s = build([100], 4, 2, 2, 64, 16, True, seed=9, one_scale=True)
+    s["q"][:, 0] *= 2.0 ** 100
+    s["k_scale"] *= 2.0 ** -100
+    check(s, seqs=[0])
+    s = build([100], 4, 2, 2, 64, 16, True, seed=9)
+    s["q"][0, 0, 0, 1:] *= 2.0 ** -20   # (one large column, the rest far below it)
+    s["q"][0, 1] *= 2.0 ** -60
+    check(s)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_strides_orders_and_given_buffers(fp8):
+    s = build([40, 0, 77], 4, 2, 3, 64, 16, fp8, seed=10)
+    want = check(s)
+    B, H, Nq, d = s["q"].shape
+    for perm in ((0, 2, 1, 3), (1, 0, 2, 3), (2, 1, 0, 3)):
+        inv = [perm.index(i) for i in range(4)]
+        wide = torch.zeros([s["q"].shape[i] for i in perm[:3]] + [d + 8], dtype=torch.bfloat16)
+        view = wide[..., :d].permute(inv)
+        view.copy_(s["q"])
+        dev = wide.to(DEV)[..., :d].permute(inv)
+        out = torch.full(wide.shape, 3.0, dtype=torch.bfloat16, device=DEV)
+        lse = torch.empty(B, H, Nq, device=DEV)
+        ws = torch.empty(api.paged_workspace_bytes(B, H, 2, Nq, d, fp8), dtype=torch.uint8, device=DEV)
+        d2 = {n: (t.to(DEV) if t is not None else None) for n, t in s.items()}
+        o, l = api.fwd_paged(dev, d2["kc"], d2["vc"], d2["table"], d2["lens"], k_scale=d2["k_scale"],
+                             v_scale=d2["v_scale"], out=out[..., :d].permute(inv), lse=lse, workspace=ws)
+        assert l is lse and torch.equal(o.cpu(), want[0]) and torch.equal(lse.cpu(), want[1])
+        assert bool((out[..., d:] == 3).all())   # what lies between the rows stays
+    # one query broadcast over rows (stride 0)
+    q1 = s["q"][:, :, :1].expand(B, H, Nq, d)
+    check(dict(s, q=q1.contiguous()), got=run(dict(s, q=s["q"][:, :, :1].to(DEV).expand(B, H, Nq, d))))
+
+
+def test_workspace_given_or_taken_by_the_library():
+    s = build([900, 5], 4, 2, 1, 64, 16, False, seed=11)
+    want = run(s)
+    dev = {n: t.to(DEV) for n, t in s.items() if t is not None}
+    c, _ = api._paged_cache(dev["kc"], dev["vc"], dev["table"], dev["lens"], None, None)
+    o, lse = torch.empty_like(dev["q"]), torch.empty(2, 4, 1, device=DEV)
+    code = _lib.fa_fwd_paged(c, dev["q"].data_ptr(), dev["q"].stride()[:3], o.data_ptr(), o.stride()[:3], lse.data_ptr(),
+                             4, 1, 0.125, 0, 0, None, 0, torch.cuda.current_stream().cuda_stream)
+    assert code == _lib.FA_OK
+    torch.cuda.synchronize()
+    assert torch.equal(o.cpu(), want[0]) and torch.equal(lse.cpu(), want[1])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_nan_and_infinity_in_hidden_keys(fp8):
+    """Keys that no row of the call sees - behind the window, past the sinks - may hold anything."""
+    s = build([300], 4, 2, 3, 128, 16, fp8, seed=12)
+    window, sinks = 60, 5
+    j = torch.arange(300)
+    hidden = ~_plain.visible(3, 300, window, sinks).any(0)
+    j = j[hidden]
+    at = (s["table"][0, j // 16].long(), slice(None), j % 16)
+    for n in "kv":
+        if fp8:
+            s[n + "c"].view(torch.uint8)[at] = 0x7F
+        else:
+            s[n + "c"][at] = math.inf if n == "k" else math.nan
+    check(s, window, sinks)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_nan_that_is_seen_shows(fp8):
+    s = build([100, 100], 2, 1, 1, 64, 16, fp8, seed=13)
+    page = int(s["table"][0, 3])
+    if fp8:
+        s["kc"].view(torch.uint8)[page, 0, 2] = 0x7F
+    else:
+        s["kc"][page, 0, 2] = math.nan
+    o, lse = run(s)
+    assert bool(torch.isnan(o[0]).all()) and bool(torch.isnan(lse[0]).all())
+    check(s, got=(o, lse), seqs=[1])
+    # every key NaN
+    s = build([40], 2, 1, 1, 64, 16, fp8, seed=14)
+    (s["kc"].view(torch.uint8) if fp8 else s["kc"]).fill_(0x7F if fp8 else math.nan)
+    o, lse = run(s)
+    assert bool(torch.isnan(o).all()) and bool(torch.isnan(lse).all())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_bad_pages_are_hidden_and_reported(fp8):
+    s = build([100, 50, 64, 30], 4, 2, 1, 64, 16, fp8, seed=15)
+    s2 = dict(s, table=s["table"].clone(), lens=s["lens"].clone())
+    s2["table"][0, 2] = s["kc"].shape[0]
+    s2["table"][0, 4] = -7
+    s2["lens"][1] = -3
+    s2["lens"][2] = 10 ** 6       # cut to the table's 7 pages, of which this sequence has 4
+    o, lse = run(s2)
+    assert api.last_device_error() == _lib.FA_ERR_PAGE
+    assert api.last_device_error() == _lib.FA_OK
+    # the plain form of what is left: sequence 0 without keys 32-47 and 64-79
+    j = torch.arange(100)
+    keep = j[~((j // 16 == 2) | (j // 16 == 4))]
+    k, v = (_plain.gather(s[c + "c"], s["table"][0], 100, s[c + "_scale"])[:, keep].repeat_interleave(2, 0) for c in "kv")
+    ref, l_ref, _ = _plain.attention(s["q"][0], k, v, 0.125, torch.ones(1, len(keep), dtype=torch.bool))
+    assert float((o[0].double() - ref).abs().max()) <= 1e-2 and float((lse[0].double() - l_ref).abs().max()) <= 1e-4
+    assert bool((o[1] == 0).all()) and bool((lse[1] == -math.inf).all())
+    check(s, got=(o, lse), seqs=[2, 3])
+
+
+def test_two_streams_two_workspaces():
+    a, b = build([3000, 10, 500], 8, 2, 1, 128, 64, False, seed=16), build([2500], 8, 2, 2, 128, 64, True, seed=17)
+    dev = [{n: (t.to(DEV) if t is not None else None) for n, t in s.items()} for s in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [None, None]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                x = dev[i]
+                outs[i] = api.fwd_paged(x["q"], x["kc"], x["vc"], x["table"], x["lens"], k_scale=x["k_scale"],
+                                        v_scale=x["v_scale"])
+    torch.cuda.synchronize()
+    for s, got in zip((a, b), outs):
+        check(s, got=tuple(t.cpu() for t in got))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_runs_are_bitwise_alike(fp8):
+    s = build([5000, 1, 777, 64], 8, 2, 3, 128, 64, fp8, seed=18)
+    a = run(s)
+    for _ in range(3):
+        b = run(s)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_equals_the_contiguous_decode():
+    """A full batch of equal lengths in pages against fa_fwd_decode on the same keys."""
+    B, H, Nq, Nk, d = 2, 4, 4, 1000, 128
+    s = build([Nk] * B, H, H, Nq, d, 64, False, seed=19)
+    o, lse = run(s)
+    k, v = (torch.stack([_plain.gather(s[c + "c"], s["table"][b], Nk) for b in range(B)]).to(torch.bfloat16).to(DEV) for c in "kv")
+    od, ld = api.fwd_decode(s["q"].to(DEV), k, v, True)
+    assert float((o.float() - od.cpu().float()).abs().max()) <= 1e-2
+    assert float((lse - ld.cpu()).abs().max()) <= 1e-4
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_generation_append_then_attend(fp8):
+    """As a server uses them: a prompt appended in two chunks, then tokens one at a time in a captured
+    graph (append, lengths, attention with window and sinks), each step against the plain form on the
+    cache as it then is, and the cache against all the keys at the end."""
+    B, H, Hkv, d, page, window, sinks = 3, 8, 2, 128, 16, 70, 4
+    g = torch.Generator().manual_seed(20)
+    prompt, gen = [50, 7, 33], 40
+    P, table = _plain.make_pages([n + gen for n in prompt], page, g)
+    dt = torch.uint8 if fp8 else torch.bfloat16
+    kc, vc = (torch.zeros(P, Hkv, page, d, dtype=dt, device=DEV) for _ in "kv")
+    ks, vs = (torch.ones(P, Hkv, device=DEV) if fp8 else None for _ in "kv")
+    table, lens = table.to(DEV), torch.zeros(B, dtype=torch.int32, device=DEV)
+    f = (10000.0 ** (-2.0 * torch.arange(d // 2, dtype=torch.float64) / d)).to(DEV)
+    sc = dict(k_scale=ks, v_scale=vs)
+    keys = [[] for _ in range(B)]
+    for part in (0, 1):
+        n = [p - p // 2 if part else p // 2 for p in prompt]
+        x = torch.randn(sum(n), 2 * Hkv, d, generator=g).to(torch.bfloat16)
+        cu = torch.tensor([0, n[0], n[0] + n[1], sum(n)], dtype=torch.int32, device=DEV)
+        xd = x.to(DEV)
+        api.kv_append(xd[:, :Hkv], xd[:, Hkv:], kc, vc, table, lens, cu_new=cu, inv_freq=f, **sc)
+        lens.add_(cu[1:] - cu[:-1])
+        for b in range(B):
+            keys[b].append(x[int(cu[b]):int(cu[b + 1])])
+    x = torch.zeros(B, H + 2 * Hkv, d, dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(api.paged_workspace_bytes(B, H, Hkv, 1, d, fp8), dtype=torch.uint8, device=DEV)
+
+    def step():
+        q = api.kv_append(x[:, H:H + Hkv], x[:, H + Hkv:], kc, vc, table, lens, q=x[:, :H], inv_freq=f, **sc)
+        lens.add_(1)
+        return (q,) + api.fwd_paged(q[:, :, None], kc, vc, table, lens, window=window, sinks=sinks, workspace=ws, **sc)
+    saved = [t.clone() if t is not None else None for t in (kc, vc, lens, ks, vs)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    for t, o in zip((kc, vc, lens, ks, vs), saved):
+        if t is not None:
+            t.copy_(o)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q, o, lse = step()
+    for i in range(gen):
+        rows = torch.randn(B, H + 2 * Hkv, d, generator=g).to(torch.bfloat16)
+        x.copy_(rows)
+        graph.replay()
+        torch.cuda.synchronize()
+        for b in range(B):
+            keys[b].append(rows[b:b + 1, H:])
+        if i % 6 == 0 or i == gen - 1:
+            view = lambda c: c.cpu().view(torch.float8_e4m3fn) if fp8 else c.cpu()
+            s = dict(q=q.cpu()[:, :, None], kc=view(kc), vc=view(vc), table=table.cpu(), lens=lens.cpu(),
+                     k_scale=ks.cpu() if fp8 else None, v_scale=vs.cpu() if fp8 else None)
+            check(s, window, sinks, got=(o.cpu(), lse.cpu()))
+    assert lens.tolist() == [n + gen for n in prompt] and api.last_device_error() == _lib.FA_OK
+    for b in range(B):
+        x = torch.cat(keys[b])
+        pos = torch.arange(len(x))
+        k_ref = _plain.rotate(x[:, :Hkv], pos, f.cpu(), False).transpose(0, 1)
+        v_ref = x[:, Hkv:].double().transpose(0, 1)
+        view = lambda c: c.cpu().view(torch.float8_e4m3fn) if fp8 else c.cpu()
+        k_got = _plain.gather(view(kc), table[b].cpu(), len(x), ks.cpu() if fp8 else None)
+        v_got = _plain.gather(view(vc), table[b].cpu(), len(x), vs.cpu() if fp8 else None)
+        if fp8:
+            # one rounding, and for held codes rescaling that is exact above the subnormals: half a
+            # step, plus half the subnormals' step per rescaling (a page of 16 grows fewer than 16 times)
+            for got, ref, scale in ((k_got, k_ref, ks), (v_got, v_ref, vs)):
+                ids = table[b, :-(-len(x) // page)].long().cpu()
+                step_ = scale.cpu().double()[ids].repeat_interleave(page, 0)[:len(x)].T[..., None]
+                assert bool(((got - ref).abs() <= _plain.E4M3_HALF * ref.abs() + 16 * 2.0 ** -10 * step_ + 1e-5).all())
+        else:
+            assert bool(((k_got - k_ref).abs() <= BF16_HALF * k_ref.abs() + 2.0 ** -18).all())
+            assert torch.equal(v_got, v_ref)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_offsets_past_32_bits(fp8):
+    """A cache of more than 2^32 bytes (and, in bf16, elements): pages at its far end."""
+    Hkv, page, d = 16, 256, 128
+    P = 2 ** 33 // (Hkv * page * d) + 8
+    kc = torch.zeros(P, Hkv, page, d, dtype=torch.uint8 if fp8 else torch.bfloat16, device=DEV)
+    vc = torch.zeros_like(kc)
+    ids = [P - 1, 3, P - 2]
+    table = torch.tensor([ids], dtype=torch.int32, device=DEV)
+    lens = torch.zeros(1, dtype=torch.int32, device=DEV)
+    sc = dict(k_scale=torch.ones(P, Hkv, device=DEV), v_scale=torch.ones(P, Hkv, device=DEV)) if fp8 else {}
+    g = torch.Generator().manual_seed(21)
+    x = torch.randn(700, 2 * Hkv, d, generator=g).to(torch.bfloat16).to(DEV)
+    api.kv_append(x[:, :Hkv], x[:, Hkv:], kc, vc, table, lens, **sc)
+    lens.fill_(700)
+    q = torch.randn(1, Hkv, 1, d, generator=g).to(torch.bfloat16)
+    o, lse = api.fwd_paged(q.to(DEV), kc, vc, table, lens, **sc)
+    torch.cuda.synchronize()
+    assert api.last_device_error() == _lib.FA_OK
+    view = lambda c: c[ids].cpu().view(torch.float8_e4m3fn) if fp8 else c[ids].cpu()
+    s = dict(q=q, kc=view(kc), vc=view(vc), table=torch.tensor([[0, 1, 2]]), lens=lens.cpu(),
+             k_scale=sc["k_scale"][ids].cpu() if fp8 else None, v_scale=sc["v_scale"][ids].cpu() if fp8 else None)
+    check(s, got=(o.cpu(), lse.cpu()))
+    if not fp8:
+        assert torch.equal(_plain.gather(s["vc"], s["table"][0], 700).float(), x[:, Hkv:].cpu().transpose(0, 1).float())

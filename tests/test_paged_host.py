@@ -1,0 +1,326 @@
+"""The paged cache without a GPU: the index arithmetic that its kernels share (compiled here as
+plain C++), refusals of the entry points, and checks of the Python ones."""
+import ctypes
+import math
+import os
+import struct
+import subprocess
+
+import pytest
+import torch
+
+from exact_io_aware_12_gb300 import _lib, api
+from tests import _plain
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 0x7F0000000000
+GB = 1 << 30
+
+SHIM = r'''
+#include "fa_paged.h"
+using namespace fa;
+extern "C" {
+int t_page_of(const int* t, int mp, int np, int sh, long long k) { return page_of(t, mp, np, sh, k); }
+void t_range(int len, int nq, int w, int s, int* o) {
+    const PagedRange r = paged_range(len, nq, w, s);
+    o[0] = r.lo; o[1] = r.ns; o[2] = r.n; o[3] = paged_steps(r);
+}
+int t_key0(int len, int nq, int w, int s, int i) { return paged_range(len, nq, w, s).key0(i); }
+long long t_start(long long c, long long t, long long s) { return share_start(c, t, s); }
+long long t_share(long long x, long long t, long long s) { return share_of(x, t, s); }
+uint64_t t_turn(uint64_t b) { return turn_fraction(b); }
+int t_exp(uint32_t b) { return page_scale_exp(b); }
+int t_reached(long long p, int n, int sh) { return pages_reached(p, n, sh); }
+long long t_unit(long long c, int b, int sh) { return first_unit(c, b, sh); }
+}
+'''
+
+
+@pytest.fixture(scope="module")
+def shim(tmp_path_factory):
+    d = tmp_path_factory.mktemp("paged")
+    src, lib = d / "shim.cpp", d / "shim.so"
+    src.write_text(SHIM)
+    subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-fsanitize=undefined",
+                    "-fno-sanitize-recover=undefined", "-static-libubsan",
+                    "-I", os.path.join(ROOT, "exact_io_aware_12_gb300", "csrc"), str(src), "-o", str(lib)], check=True)
+    L = ctypes.CDLL(str(lib))
+    LL, I = ctypes.c_longlong, ctypes.c_int
+    L.t_page_of.argtypes = [ctypes.POINTER(I), I, I, I, LL]
+    L.t_start.argtypes = L.t_share.argtypes = [LL, LL, LL]
+    L.t_start.restype = L.t_share.restype = L.t_unit.restype = LL
+    L.t_turn.argtypes, L.t_turn.restype = [ctypes.c_uint64], ctypes.c_uint64
+    L.t_exp.argtypes = [ctypes.c_uint32]
+    L.t_reached.argtypes = [LL, I, I]
+    L.t_unit.argtypes = [LL, I, I]
+    return L
+
+
+def test_bad_pages_and_positions_name_no_page(shim):
+    t = (ctypes.c_int * 4)(2, -1, 7, 2 ** 31 - 1)
+    at = lambda key, pages=7, shift=4: shim.t_page_of(t, 4, pages, shift, key)
+    assert at(0) == 2 and at(15) == 2
+    assert at(16) == -1                    # entry -1
+    assert at(32) == -1 and at(32, pages=8) == 7   # entry == num_pages, and just inside
+    assert at(48) == -1                    # entry far outside
+    assert at(64) == -1 and at(2 ** 40) == -1 and at(-1) == -1 and at(-2 ** 40) == -1  # outside the table
+    assert at(2 ** 31 + 5) == -1
+
+
+@pytest.mark.parametrize("nq,window,sinks", [(1, 0, 0), (4, 0, 0), (1, 1, 0), (1, 40, 5), (4, 64, 17), (8, 100, 130), (3, 16, 16)])
+def test_tile_lists_hold_every_visible_key_once(shim, nq, window, sinks):
+    o = (ctypes.c_int * 4)()
+    for length in list(range(0, 200)) + [511, 512, 513, 1000]:
+        shim.t_range(length, nq, window, sinks, o)
+        lo, ns, n, steps = o
+        starts = [shim.t_key0(length, nq, window, sinks, i) for i in range(n)]
+        assert len(set(starts)) == n and all(k % 16 == 0 and 0 <= k < max(length, 1) for k in starts)
+        assert steps == max(1, -(-n // 4))
+        see = _plain.visible(min(nq, length), length, window, sinks).any(0) if length else torch.zeros(0)
+        held = {k + i for k in starts for i in range(16)}
+        assert all(int(j) in held for j in see.nonzero().flatten())
+        # and no tile without a visible key, but where the window's first row looks further back than row 0 can
+        if length >= nq:
+            assert all(any(k + i < length and see[k + i] for i in range(16)) for k in starts)
+
+
+def test_extreme_lengths_and_windows_do_not_overflow(shim):
+    o = (ctypes.c_int * 4)()
+    for length in (0, 1, 2 ** 31 - 1, 2 ** 31 - 17):
+        for window in (0, 1, 2 ** 30):
+            for sinks in (0, 1, 2 ** 30):
+                shim.t_range(length, 8, window, sinks, o)
+                assert o[2] >= 0 and o[3] >= 1
+
+
+@pytest.mark.parametrize("total,shares", [(1, 1), (10, 3), (1000, 608), (607, 607), (12345, 304), (2 ** 31 - 1, 608)])
+def test_shares_cover_every_step_once(shim, total, shares):
+    assert shim.t_start(0, total, shares) == 0 and shim.t_start(shares, total, shares) == total
+    for c in range(shares):
+        a, b = shim.t_start(c, total, shares), shim.t_start(c + 1, total, shares)
+        assert a < b
+        for x in {a, (a + b) // 2, b - 1}:
+            assert shim.t_share(x, total, shares) == c
+
+
+def test_turns_are_exact_far_out(shim):
+    from fractions import Fraction
+    # pi to 40 digits
+    pi = Fraction(31415926535897932384626433832795028841972, 10 ** 40)
+    for f in [1.0, 0.5, 10000.0 ** (-2 / 128), 1e-4, 3.7e-9, 2.5, 1234.5, -0.3, 5e-324, 0.0, 1e-30, 2.0 ** 60]:
+        got = shim.t_turn(struct.unpack("<Q", struct.pack("<d", f))[0])
+        for p in (1, 131072, 2 ** 24, 2 ** 31 - 1):
+            want = Fraction(f) * p / (2 * pi)
+            want -= math.floor(want)
+            have = Fraction(got * p % 2 ** 64, 2 ** 64)
+            off = abs(want - have)
+            off = min(off, 1 - off)
+            # 2 / pi is held to 2^-64 of itself, the turns to 2^-64, both times the position
+            assert off <= abs(Fraction(f)) * p * Fraction(1, 2 ** 64) + Fraction(p, 2 ** 63), (f, p, float(off))
+    for bits in (0x7FF0000000000000, 0xFFF0000000000000, 0x7FF8000000000000):
+        assert shim.t_turn(bits) == 0
+
+
+def test_page_scales(shim):
+    bits = lambda x: struct.unpack("<I", struct.pack("<f", x))[0]
+    for x in [0.0, 1e-45, 1e-30, 1.0, 447.9, 448.0, 448.00003, 449.0, 896.0, 896.1, 1.75, 1.7500001, 3e38, 3.4e38]:
+        x32 = struct.unpack("<f", struct.pack("<f", x))[0]
+        assert 2.0 ** shim.t_exp(bits(x)) == _plain.scale_of(x32), x
+    assert shim.t_exp(bits(math.inf)) == 121
+
+
+def test_units_fit_every_split_of_tokens(shim):
+    """Each sequence's pages fit the units it is given, whatever its lengths and the others'."""
+    g = torch.Generator().manual_seed(3)
+    for shift in (4, 6):
+        for _ in range(300):
+            n = torch.randint(0, 100, (6,), generator=g).tolist()
+            cu = [0]
+            for x in n:
+                cu.append(cu[-1] + x)
+            for b in range(6):
+                room = shim.t_unit(cu[b + 1], b + 1, shift) - shim.t_unit(cu[b], b, shift)
+                for past in (0, 1, 15, 16, 63, 2 ** 31 - 60):
+                    used = shim.t_reached(past, n[b], shift)
+                    assert used <= room
+                    assert used == len({(past + i) >> shift for i in range(n[b])})
+            assert shim.t_unit(cu[6], 6, shift) <= (cu[6] >> shift) + 12
+
+
+def cache(fp8=False, **kw):
+    c = dict(K=FAKE, V=FAKE + GB, k_scale=FAKE + 2 * GB if fp8 else None, v_scale=FAKE + 3 * GB if fp8 else None,
+             page_table=FAKE + 4 * GB, lens=FAKE + 5 * GB, B=2, H_kv=2, d=64, num_pages=8, page_size=16, max_pages=4)
+    c.update(kw)
+    return _lib.PagedCache(*(c[n] for n, _ in _lib.PagedCache._fields_))
+
+
+BAD_CACHES = [
+    (dict(K=None), _lib.FA_ERR_INVALID_ARG),
+    (dict(V=FAKE + GB + 8), _lib.FA_ERR_INVALID_ARG),
+    (dict(V=FAKE + 64), _lib.FA_ERR_INVALID_ARG),               # V overlaps K
+    (dict(page_table=None), _lib.FA_ERR_INVALID_ARG),
+    (dict(lens=FAKE + 5 * GB + 2), _lib.FA_ERR_INVALID_ARG),
+    (dict(B=-1), _lib.FA_ERR_INVALID_ARG),
+    (dict(max_pages=0), _lib.FA_ERR_INVALID_ARG),
+    (dict(num_pages=0), _lib.FA_ERR_INVALID_ARG),
+    (dict(d=96), _lib.FA_ERR_UNSUPPORTED),
+    (dict(page_size=8), _lib.FA_ERR_UNSUPPORTED),
+    (dict(page_size=48), _lib.FA_ERR_UNSUPPORTED),
+    (dict(page_size=512), _lib.FA_ERR_UNSUPPORTED),
+    (dict(max_pages=2 ** 26 + 1), _lib.FA_ERR_UNSUPPORTED),
+    (dict(k_scale=FAKE + 6 * GB, v_scale=None), _lib.FA_ERR_INVALID_ARG),
+    (dict(B=0), _lib.FA_OK),
+]
+
+
+def append(c, fp8=False, **kw):
+    a = dict(k=FAKE + 8 * GB, k_strides=(128, 64), v=FAKE + 9 * GB, v_strides=(128, 64), T=4, cu_new=FAKE + 10 * GB,
+             q=FAKE + 11 * GB, q_strides=(256, 64), q_out=FAKE + 12 * GB, q_out_strides=(256, 64), H=4,
+             inv_freq=FAKE + 13 * GB, rot=64, interleaved=0, stream=None)
+    a.update(kw)
+    return (_lib.fa_kv_append_fp8 if fp8 else _lib.fa_kv_append)(c, *a.values())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kw,code", BAD_CACHES)
+def test_append_refuses_bad_caches(kw, code, fp8):
+    assert append(cache(fp8, **kw), fp8) == code
+
+
+NO_Q = dict(q=None, q_strides=None, q_out=None, q_out_strides=None, H=0)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(k=None), _lib.FA_ERR_INVALID_ARG),
+    (dict(v=FAKE + 9 * GB + 2), _lib.FA_ERR_INVALID_ARG),
+    (dict(k_strides=(128, 60)), _lib.FA_ERR_INVALID_ARG),       # not a multiple of 8
+    (dict(k_strides=(-128, 64)), _lib.FA_ERR_INVALID_ARG),
+    (dict(k_strides=(2 ** 62, 64)), _lib.FA_ERR_INVALID_ARG),   # beyond any address
+    (dict(v_strides=None), _lib.FA_ERR_INVALID_ARG),
+    (dict(k=FAKE + 16), _lib.FA_ERR_INVALID_ARG),               # inside the cache
+    (dict(T=-1), _lib.FA_ERR_INVALID_ARG),
+    (dict(T=3, cu_new=None), _lib.FA_ERR_INVALID_ARG),          # no even split over two sequences
+    (dict(cu_new=FAKE + 10 * GB + 1), _lib.FA_ERR_INVALID_ARG),
+    (dict(rot=24), _lib.FA_ERR_INVALID_ARG),
+    (dict(rot=80), _lib.FA_ERR_INVALID_ARG),                    # wider than the head
+    (dict(rot=0), _lib.FA_ERR_INVALID_ARG),                     # frequencies without rotation
+    (dict(inv_freq=None), _lib.FA_ERR_INVALID_ARG),
+    (dict(inv_freq=None, rot=0), _lib.FA_ERR_INVALID_ARG),      # queries without rotation
+    (dict(inv_freq=FAKE + 13 * GB + 4), _lib.FA_ERR_INVALID_ARG),
+    (dict(interleaved=2), _lib.FA_ERR_INVALID_ARG),
+    (dict(q_out=None), _lib.FA_ERR_INVALID_ARG),
+    (dict(H=0), _lib.FA_ERR_INVALID_ARG),
+    (dict(q_out=FAKE + 11 * GB + 32), _lib.FA_ERR_INVALID_ARG),  # neither in place nor apart
+    (dict(q_out=FAKE + 11 * GB, q_out_strides=(512, 64)), _lib.FA_ERR_INVALID_ARG),
+    (dict(q_out_strides=(0, 64)), _lib.FA_ERR_INVALID_ARG),     # rows on top of each other
+    (dict(q_out=FAKE + 8 * GB), _lib.FA_ERR_INVALID_ARG),       # over k
+    (dict(T=0), _lib.FA_OK),
+    (dict(T=0, k=None, v=None, **NO_Q), _lib.FA_OK),
+])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_append_refuses(kw, code, fp8):
+    assert append(cache(fp8), fp8, **kw) == code
+
+
+def test_a_cache_of_the_other_kind_is_refused():
+    assert append(cache(True), False) == _lib.FA_ERR_INVALID_ARG
+    assert append(cache(False), True) == _lib.FA_ERR_INVALID_ARG
+    assert paged(cache(True), False) == _lib.FA_ERR_INVALID_ARG
+    assert paged(cache(False), True) == _lib.FA_ERR_INVALID_ARG
+    assert paged(None) == _lib.FA_ERR_INVALID_ARG
+
+
+def paged(c, fp8=False, **kw):
+    a = dict(Q=FAKE + 8 * GB, q_strides=(256, 64, 64), O=FAKE + 9 * GB, o_strides=(256, 64, 64), LSE=FAKE + 10 * GB,
+             H=4, Nq=1, tau=0.125, window=0, sinks=0, workspace=FAKE + 11 * GB, workspace_bytes=GB, stream=None)
+    a.update(kw)
+    return (_lib.fa_fwd_paged_fp8 if fp8 else _lib.fa_fwd_paged)(c, *a.values())
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("kw,code", BAD_CACHES)
+def test_paged_refuses_bad_caches(kw, code, fp8):
+    assert paged(cache(fp8, **kw), fp8) == code
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(Q=None), _lib.FA_ERR_INVALID_ARG),
+    (dict(O=FAKE + 9 * GB + 4), _lib.FA_ERR_INVALID_ARG),
+    (dict(q_strides=(256, 63, 64)), _lib.FA_ERR_INVALID_ARG),
+    (dict(o_strides=None), _lib.FA_ERR_INVALID_ARG),
+    (dict(o_strides=(256, 0, 64)), _lib.FA_ERR_INVALID_ARG),        # heads on top of each other
+    (dict(o_strides=(128, 64, 64)), _lib.FA_ERR_INVALID_ARG),       # sequences overlap
+    (dict(H=3), _lib.FA_ERR_INVALID_ARG),                           # not a multiple of H_kv
+    (dict(H=-4), _lib.FA_ERR_INVALID_ARG),
+    (dict(Nq=9), _lib.FA_ERR_UNSUPPORTED),
+    (dict(tau=0.0), _lib.FA_ERR_INVALID_ARG),
+    (dict(tau=math.nan), _lib.FA_ERR_INVALID_ARG),
+    (dict(window=-1), _lib.FA_ERR_INVALID_ARG),
+    (dict(sinks=4), _lib.FA_ERR_INVALID_ARG),                       # sinks without a window
+    (dict(window=4, sinks=-1), _lib.FA_ERR_INVALID_ARG),
+    (dict(workspace_bytes=1000), _lib.FA_ERR_WORKSPACE),
+    (dict(workspace=FAKE + 11 * GB + 8), _lib.FA_ERR_INVALID_ARG),
+    (dict(workspace=FAKE + 9 * GB), _lib.FA_ERR_INVALID_ARG),       # over O
+    (dict(O=FAKE + 8 * GB), _lib.FA_ERR_INVALID_ARG),               # over Q
+    (dict(LSE=FAKE + 5 * GB), _lib.FA_ERR_INVALID_ARG),             # over lens
+    (dict(O=FAKE), _lib.FA_ERR_INVALID_ARG),                        # over the cache
+    (dict(Nq=0), _lib.FA_OK),
+    (dict(H=0), _lib.FA_OK),
+])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_paged_refuses(kw, code, fp8):
+    assert paged(cache(fp8), fp8, **kw) == code
+
+
+def test_too_many_steps_are_refused():
+    assert paged(cache(B=4096, H_kv=2, max_pages=2 ** 22)) == _lib.FA_ERR_UNSUPPORTED
+
+
+def test_workspace_size_does_not_depend_on_lengths():
+    a = _lib.fa_paged_workspace_size(4, 8, 2, 1, 128, 0)
+    assert a > 0 and a % 256 == 0
+    assert _lib.fa_paged_workspace_size(4, 8, 3, 1, 128, 0) == 0
+    assert _lib.fa_paged_workspace_size(4, 8, 2, 9, 128, 0) == 0
+    assert _lib.fa_paged_workspace_size(0, 8, 2, 1, 128, 0) == 0
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(window=0), _lib.FA_ERR_INVALID_ARG),
+    (dict(window=-3), _lib.FA_ERR_INVALID_ARG),
+    (dict(sinks=-1), _lib.FA_ERR_INVALID_ARG),
+    (dict(d=96), _lib.FA_ERR_UNSUPPORTED),
+    (dict(N=0), _lib.FA_OK),
+])
+def test_sinks_argument_checks(kw, code):
+    a = dict(B=1, H=1, N=128, d=64, tau=0.125, window=8, sinks=2)
+    a.update(kw)
+    p = [FAKE + i * GB for i in range(10)]
+    assert _lib.fa_fwd_sinks(*p[:5], *a.values(), None) == code
+    assert _lib.fa_bwd_sinks(*p[:6], *p[6:9], p[9], GB, *a.values(), None) == code
+
+
+def test_python_checks():
+    x = torch.zeros(1, 1, 128, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="sinks need a window"):
+        api.fwd(x, x, x, True, sinks=4)
+    with pytest.raises(ValueError, match="sinks need a window"):
+        api.bwd(x, x, x, x, x, x, True, sinks=4)
+    kc = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    tb, ln = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    q = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16)
+    new = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    sc = torch.ones(4, 2)
+    for args, kw, what in [
+        ((q, kc, kc, tb, ln), {}, "CUDA"),
+        ((q, kc, kc, tb.long(), ln), {}, "int32"),
+        ((q, kc, kc, tb, ln[:1]), {}, "lens"),
+        ((q, kc, kc[:2], tb, ln), {}, "alike"),
+        ((q, kc, kc, tb, ln), dict(k_scale=sc), "both scales"),
+        ((q, kc, kc, tb, ln), dict(k_scale=sc, v_scale=sc), "e4m3"),
+        ((q, kc.view(torch.uint8), kc.view(torch.uint8), tb, ln), {}, "bf16"),
+        ((q, kc.to(torch.uint8), kc.to(torch.uint8), tb, ln), dict(k_scale=sc[:2], v_scale=sc[:2]), "scales"),
+    ]:
+        with pytest.raises(ValueError, match=what):
+            api.fwd_paged(*args, **kw)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.kv_append(new, new, kc, kc, tb, ln)
