@@ -35,10 +35,9 @@ class PagedCache(ctypes.Structure):
 
 
 _C = ctypes.POINTER(PagedCache)
-_LL2 = ctypes.c_longlong * 2   # (token, head) strides
-_LL3 = ctypes.c_longlong * 3   # (sequence, head, row) strides
-_APPEND = [_C, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _P, _I, _I, _P]
-_PAGED = [_C, _P, _P, _P, _P, _P, _I, _I, _F, _I, _I, _P, _SZ, _P]
+_LL = ctypes.c_longlong
+_APPEND = [_C, _P, _LL, _LL, _P, _LL, _LL, _I, _P, _P, _LL, _LL, _P, _LL, _LL, _I, _P, _I, _I, _P]
+_PAGED = [_C, _P, _LL, _LL, _LL, _P, _LL, _LL, _LL, _P, _I, _I, _F, _I, _I, _P, _SZ, _P]
 SIGNATURES = {
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P]),
     "fa_fwd_o32": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P]),
@@ -114,7 +113,10 @@ def status_string(code: int) -> str:
 
 
 def _call(name: str, *args) -> int:
-    return getattr(load(), name)(*args)
+    lib = _lib
+    if lib is None:
+        lib = load()
+    return getattr(lib, name)(*args)
 
 
 def fa_fwd(Q, K, V, O, LSE, B, H, N, d, tau, causal, stream) -> int:
@@ -160,39 +162,32 @@ def fa_fwd_decode(Q, K, V, O, LSE, B, H, Nq, Nk, d, tau, causal, workspace, work
                  workspace_bytes, stream)
 
 
-def _strides(t, n):
-    """A host array of strides, or None."""
-    return None if t is None else (_LL2 if n == 2 else _LL3)(*t)
-
-
-def fa_kv_append(cache, k, k_strides, v, v_strides, T, cu_new, q, q_strides, q_out, q_out_strides,
+def fa_kv_append(cache, k, k_st, k_sh, v, v_st, v_sh, T, cu_new, q, q_st, q_sh, q_out, qo_st, qo_sh,
                  H, inv_freq, rot, interleaved, stream) -> int:
-    return _call("fa_kv_append", cache, k, _strides(k_strides, 2), v, _strides(v_strides, 2), T,
-                 cu_new, q, _strides(q_strides, 2), q_out, _strides(q_out_strides, 2), H, inv_freq,
-                 rot, interleaved, stream)
+    return _call("fa_kv_append", cache, k, k_st, k_sh, v, v_st, v_sh, T, cu_new, q, q_st, q_sh,
+                 q_out, qo_st, qo_sh, H, inv_freq, rot, interleaved, stream)
 
 
-def fa_kv_append_fp8(cache, k, k_strides, v, v_strides, T, cu_new, q, q_strides, q_out,
-                     q_out_strides, H, inv_freq, rot, interleaved, stream) -> int:
-    return _call("fa_kv_append_fp8", cache, k, _strides(k_strides, 2), v, _strides(v_strides, 2),
-                 T, cu_new, q, _strides(q_strides, 2), q_out, _strides(q_out_strides, 2), H,
-                 inv_freq, rot, interleaved, stream)
+def fa_kv_append_fp8(cache, k, k_st, k_sh, v, v_st, v_sh, T, cu_new, q, q_st, q_sh, q_out, qo_st,
+                     qo_sh, H, inv_freq, rot, interleaved, stream) -> int:
+    return _call("fa_kv_append_fp8", cache, k, k_st, k_sh, v, v_st, v_sh, T, cu_new, q, q_st, q_sh,
+                 q_out, qo_st, qo_sh, H, inv_freq, rot, interleaved, stream)
 
 
 def fa_paged_workspace_size(B, H, H_kv, Nq, d, fp8) -> int:
     return int(_call("fa_paged_workspace_size", B, H, H_kv, Nq, d, fp8))
 
 
-def fa_fwd_paged(cache, Q, q_strides, O, o_strides, LSE, H, Nq, tau, window, sinks, workspace,
-                 workspace_bytes, stream) -> int:
-    return _call("fa_fwd_paged", cache, Q, _strides(q_strides, 3), O, _strides(o_strides, 3), LSE,
-                 H, Nq, tau, window, sinks, workspace, workspace_bytes, stream)
+def fa_fwd_paged(cache, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq, tau, window, sinks,
+                 workspace, workspace_bytes, stream) -> int:
+    return _call("fa_fwd_paged", cache, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq, tau,
+                 window, sinks, workspace, workspace_bytes, stream)
 
 
-def fa_fwd_paged_fp8(cache, Q, q_strides, O, o_strides, LSE, H, Nq, tau, window, sinks, workspace,
-                     workspace_bytes, stream) -> int:
-    return _call("fa_fwd_paged_fp8", cache, Q, _strides(q_strides, 3), O, _strides(o_strides, 3),
-                 LSE, H, Nq, tau, window, sinks, workspace, workspace_bytes, stream)
+def fa_fwd_paged_fp8(cache, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq, tau, window,
+                     sinks, workspace, workspace_bytes, stream) -> int:
+    return _call("fa_fwd_paged_fp8", cache, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq,
+                 tau, window, sinks, workspace, workspace_bytes, stream)
 
 
 def fa_fwd_blocks(Q, K, V, O, LSE, B, H, N, d, tau, causal, block_mask, mask_heads, stream) -> int:

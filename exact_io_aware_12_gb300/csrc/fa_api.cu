@@ -608,11 +608,11 @@ static fa_status check_cache(const fa_paged_cache* c, bool fp8, PagedCache* out,
     return FA_OK;
 }
 
-static fa_status append_common(const fa_paged_cache* c, bool fp8, const void* k, const long long* k_strides,
-                               const void* v, const long long* v_strides, int T, const int* cu_new,
-                               const void* q, const long long* q_strides, void* q_out,
-                               const long long* q_out_strides, int H, const double* inv_freq, int rot,
-                               int interleaved, void* stream) {
+static fa_status append_common(const fa_paged_cache* c, bool fp8, const void* k, long long k_st,
+                               long long k_sh, const void* v, long long v_st, long long v_sh, int T,
+                               const int* cu_new, const void* q, long long q_st, long long q_sh,
+                               void* q_out, long long qo_st, long long qo_sh, int H,
+                               const double* inv_freq, int rot, int interleaved, void* stream) {
     AppendArgs a;
     size_t cache_bytes = 0;
     fa_status s = check_cache(c, fp8, &a.cache, &cache_bytes);
@@ -622,40 +622,38 @@ static fa_status append_common(const fa_paged_cache* c, bool fp8, const void* k,
     if (rot > c->d || rot % 16 != 0) return FA_ERR_INVALID_ARG;
     if ((rot > 0) != (inv_freq != nullptr) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0) return FA_ERR_INVALID_ARG;
     if (cu_new == nullptr ? T % c->B != 0 : !aligned4(cu_new)) return FA_ERR_INVALID_ARG;
-    if (k == nullptr || v == nullptr || k_strides == nullptr || v_strides == nullptr) return FA_ERR_INVALID_ARG;
+    if (k == nullptr || v == nullptr) return FA_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v)) return FA_ERR_INVALID_ARG;
     const bool has_q = q != nullptr;
     if (has_q != (q_out != nullptr) || has_q != (H > 0)) return FA_ERR_INVALID_ARG;
-    if (has_q && (rot == 0 || q_strides == nullptr || q_out_strides == nullptr || !aligned16(q) || !aligned16(q_out)))
-        return FA_ERR_INVALID_ARG;
+    if (has_q && (rot == 0 || !aligned16(q) || !aligned16(q_out))) return FA_ERR_INVALID_ARG;
     // (token, head) as a [T][heads][1][d] tensor
     const long long nk[3] = {T, c->H_kv, 1}, nq[3] = {T, H, 1};
-    const auto span = [&](const long long* n, const long long* st) {
-        const long long s3[3] = {st[0], st[1], 0};
+    const auto span = [&](const long long* n, long long st, long long sh) {
+        const long long s3[3] = {st, sh, 0};
         return strided_span(n, s3, c->d);
     };
-    const long long ks = span(nk, k_strides), vs = span(nk, v_strides);
+    const long long ks = span(nk, k_st, k_sh), vs = span(nk, v_st, v_sh);
     if (ks < 0 || vs < 0) return FA_ERR_INVALID_ARG;
     const void* caches[] = {c->K, c->V};
     for (const void* x : caches)
         if (overlaps(x, cache_bytes, k, ks * 2) || overlaps(x, cache_bytes, v, vs * 2)) return FA_ERR_INVALID_ARG;
     if (has_q) {
-        const long long qs = span(nq, q_strides), os = span(nq, q_out_strides);
+        const long long qs = span(nq, q_st, q_sh), os = span(nq, qo_st, qo_sh);
         if (qs < 0 || os < 0) return FA_ERR_INVALID_ARG;
-        const long long o3[3] = {q_out_strides[0], q_out_strides[1], 0};
+        const long long o3[3] = {qo_st, qo_sh, 0};
         if (!strided_distinct(nq, o3, c->d)) return FA_ERR_INVALID_ARG;
         // in place (the same rows) or apart from everything else
-        const bool in_place = q == q_out && (T == 1 || q_strides[0] == q_out_strides[0]) &&
-                              (H == 1 || q_strides[1] == q_out_strides[1]);
+        const bool in_place = q == q_out && (T == 1 || q_st == qo_st) && (H == 1 || q_sh == qo_sh);
         for (const void* x : caches)
             if (overlaps(x, cache_bytes, q, qs * 2) || overlaps(x, cache_bytes, q_out, os * 2)) return FA_ERR_INVALID_ARG;
         if (!in_place && (overlaps(q_out, os * 2, q, qs * 2) || overlaps(q_out, os * 2, k, ks * 2) ||
                           overlaps(q_out, os * 2, v, vs * 2)))
             return FA_ERR_INVALID_ARG;
-        a.q_st = q_strides[0];
-        a.q_sh = q_strides[1];
-        a.o_st = q_out_strides[0];
-        a.o_sh = q_out_strides[1];
+        a.q_st = q_st;
+        a.q_sh = q_sh;
+        a.o_st = qo_st;
+        a.o_sh = qo_sh;
     } else {
         a.q_st = a.q_sh = a.o_st = a.o_sh = 0;
     }
@@ -667,10 +665,10 @@ static fa_status append_common(const fa_paged_cache* c, bool fp8, const void* k,
     a.q_out = q_out;
     a.cu_new = cu_new;
     a.inv_freq = inv_freq;
-    a.k_st = k_strides[0];
-    a.k_sh = k_strides[1];
-    a.v_st = v_strides[0];
-    a.v_sh = v_strides[1];
+    a.k_st = k_st;
+    a.k_sh = k_sh;
+    a.v_st = v_st;
+    a.v_sh = v_sh;
     a.T = T;
     a.H = H;
     a.rot = rot;
@@ -679,22 +677,22 @@ static fa_status append_common(const fa_paged_cache* c, bool fp8, const void* k,
     return map_cuda(launch_kv_append(a, static_cast<cudaStream_t>(stream)));
 }
 
-fa_status fa_kv_append(const fa_paged_cache* cache, const void* k, const long long* k_strides,
-                       const void* v, const long long* v_strides, int T, const int* cu_new,
-                       const void* q, const long long* q_strides, void* q_out,
-                       const long long* q_out_strides, int H, const double* inv_freq, int rot,
-                       int interleaved, void* stream) {
-    return append_common(cache, false, k, k_strides, v, v_strides, T, cu_new, q, q_strides, q_out,
-                         q_out_strides, H, inv_freq, rot, interleaved, stream);
+fa_status fa_kv_append(const fa_paged_cache* cache, const void* k, long long k_st, long long k_sh,
+                       const void* v, long long v_st, long long v_sh, int T, const int* cu_new,
+                       const void* q, long long q_st, long long q_sh, void* q_out, long long qo_st,
+                       long long qo_sh, int H, const double* inv_freq, int rot, int interleaved,
+                       void* stream) {
+    return append_common(cache, false, k, k_st, k_sh, v, v_st, v_sh, T, cu_new, q, q_st, q_sh, q_out,
+                         qo_st, qo_sh, H, inv_freq, rot, interleaved, stream);
 }
 
-fa_status fa_kv_append_fp8(const fa_paged_cache* cache, const void* k, const long long* k_strides,
-                           const void* v, const long long* v_strides, int T, const int* cu_new,
-                           const void* q, const long long* q_strides, void* q_out,
-                           const long long* q_out_strides, int H, const double* inv_freq, int rot,
-                           int interleaved, void* stream) {
-    return append_common(cache, true, k, k_strides, v, v_strides, T, cu_new, q, q_strides, q_out,
-                         q_out_strides, H, inv_freq, rot, interleaved, stream);
+fa_status fa_kv_append_fp8(const fa_paged_cache* cache, const void* k, long long k_st, long long k_sh,
+                       const void* v, long long v_st, long long v_sh, int T, const int* cu_new,
+                       const void* q, long long q_st, long long q_sh, void* q_out, long long qo_st,
+                       long long qo_sh, int H, const double* inv_freq, int rot, int interleaved,
+                       void* stream) {
+    return append_common(cache, true, k, k_st, k_sh, v, v_st, v_sh, T, cu_new, q, q_st, q_sh, q_out,
+                         qo_st, qo_sh, H, inv_freq, rot, interleaved, stream);
 }
 
 size_t fa_paged_workspace_size(int B, int H, int H_kv, int Nq, int d, int fp8) {
@@ -703,9 +701,10 @@ size_t fa_paged_workspace_size(int B, int H, int H_kv, int Nq, int d, int fp8) {
     return paged_workspace(B, H, H_kv, Nq, d, fp8 != 0);
 }
 
-static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, const long long* q_strides,
-                              void* O, const long long* o_strides, float* LSE, int H, int Nq, float tau,
-                              int window, int sinks, void* workspace, size_t workspace_bytes, void* stream) {
+static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, long long q_sb,
+                              long long q_sh, long long q_sn, void* O, long long o_sb, long long o_sh,
+                              long long o_sn, float* LSE, int H, int Nq, float tau, int window, int sinks,
+                              void* workspace, size_t workspace_bytes, void* stream) {
     PagedArgs a;
     size_t cache_bytes = 0;
     fa_status s = check_cache(c, fp8, &a.cache, &cache_bytes);
@@ -716,11 +715,10 @@ static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, 
     if (H % c->H_kv != 0) return FA_ERR_INVALID_ARG;
     if (Nq > 8 || H / c->H_kv > (1 << 20)) return FA_ERR_UNSUPPORTED;
     if (paged_max_steps(c->B, H, c->H_kv, Nq, c->max_pages, a.cache.shift) > INT_MAX) return FA_ERR_UNSUPPORTED;
-    if (Q == nullptr || O == nullptr || LSE == nullptr || q_strides == nullptr || o_strides == nullptr)
-        return FA_ERR_INVALID_ARG;
+    if (Q == nullptr || O == nullptr || LSE == nullptr) return FA_ERR_INVALID_ARG;
     if (!aligned16(Q) || !aligned16(O) || !aligned16(LSE)) return FA_ERR_INVALID_ARG;
     if (workspace != nullptr && !aligned16(workspace)) return FA_ERR_INVALID_ARG;
-    const long long n[3] = {c->B, H, Nq};
+    const long long n[3] = {c->B, H, Nq}, q_strides[3] = {q_sb, q_sh, q_sn}, o_strides[3] = {o_sb, o_sh, o_sn};
     const long long qs = strided_span(n, q_strides, c->d), os = strided_span(n, o_strides, c->d);
     if (qs < 0 || os < 0 || !strided_distinct(n, o_strides, c->d)) return FA_ERR_INVALID_ARG;
     const size_t need = fa_paged_workspace_size(c->B, H, c->H_kv, Nq, c->d, fp8);
@@ -750,12 +748,12 @@ static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, 
     a.O = O;
     a.LSE = LSE;
     a.workspace = ws;
-    a.q_sb = q_strides[0];
-    a.q_sh = q_strides[1];
-    a.q_sn = q_strides[2];
-    a.o_sb = o_strides[0];
-    a.o_sh = o_strides[1];
-    a.o_sn = o_strides[2];
+    a.q_sb = q_sb;
+    a.q_sh = q_sh;
+    a.q_sn = q_sn;
+    a.o_sb = o_sb;
+    a.o_sh = o_sh;
+    a.o_sn = o_sn;
     a.H = H;
     a.Nq = Nq;
     a.window = window < (1 << 30) ? window : (1 << 30);  // (a length is below 2^31: the same keys)
@@ -769,19 +767,20 @@ static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, 
     return map_cuda(e);
 }
 
-fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* Q, const long long* q_strides, void* O,
-                       const long long* o_strides, float* LSE, int H, int Nq, float tau, int window,
-                       int sinks, void* workspace, size_t workspace_bytes, void* stream) {
-    return paged_common(cache, false, Q, q_strides, O, o_strides, LSE, H, Nq, tau, window, sinks,
-                        workspace, workspace_bytes, stream);
+fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* Q, long long q_sb, long long q_sh,
+                       long long q_sn, void* O, long long o_sb, long long o_sh, long long o_sn,
+                       float* LSE, int H, int Nq, float tau, int window, int sinks, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    return paged_common(cache, false, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq, tau, window,
+                        sinks, workspace, workspace_bytes, stream);
 }
 
-fa_status fa_fwd_paged_fp8(const fa_paged_cache* cache, const void* Q, const long long* q_strides,
-                           void* O, const long long* o_strides, float* LSE, int H, int Nq, float tau,
-                           int window, int sinks, void* workspace, size_t workspace_bytes,
-                           void* stream) {
-    return paged_common(cache, true, Q, q_strides, O, o_strides, LSE, H, Nq, tau, window, sinks,
-                        workspace, workspace_bytes, stream);
+fa_status fa_fwd_paged_fp8(const fa_paged_cache* cache, const void* Q, long long q_sb, long long q_sh,
+                       long long q_sn, void* O, long long o_sb, long long o_sh, long long o_sn,
+                       float* LSE, int H, int Nq, float tau, int window, int sinks, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    return paged_common(cache, true, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq, tau, window,
+                        sinks, workspace, workspace_bytes, stream);
 }
 
 const char* fa_status_string(fa_status s) {

@@ -278,9 +278,9 @@ typedef struct fa_paged_cache {
  * caller adds the new tokens to lens afterwards).  Rows from cu_new[B] on are
  * ignored: nothing of them is written, q_out included.
  *
- * k, v: bf16 [T][H_kv][d] and q, q_out: bf16 [T][H][d] with the given (token, head)
- * strides in elements, columns contiguous, 16-byte aligned, strides multiples of 8
- * and not negative: slices of one projection's output pass as they are.  q_out may be
+ * k, v: bf16 [T][H_kv][d] and q, q_out: bf16 [T][H][d] with the given token (_st) and
+ * head (_sh) strides in elements, columns contiguous, 16-byte aligned, strides multiples
+ * of 8 and not negative: slices of one projection's output pass as they are.  q_out may be
  * q itself with the same strides.  q NULL: H = 0, no queries.
  * The first rot columns (a multiple of 16, at most d) turn: pair c, columns (c,
  * c + rot / 2) or with interleaved = 1 (2c, 2c + 1), goes from (x, y) to
@@ -290,11 +290,11 @@ typedef struct fa_paged_cache {
  * A token whose position or page is out of bounds is not stored (FA_ERR_PAGE); its
  * query is rotated all the same.  No two sequences may append to the same page.
  */
-FA_API fa_status fa_kv_append(const fa_paged_cache* cache, const void* k, const long long* k_strides,
-                              const void* v, const long long* v_strides, int T, const int* cu_new,
-                              const void* q, const long long* q_strides, void* q_out,
-                              const long long* q_out_strides, int H, const double* inv_freq, int rot,
-                              int interleaved, void* stream);
+FA_API fa_status fa_kv_append(const fa_paged_cache* cache, const void* k, long long k_st,
+                              long long k_sh, const void* v, long long v_st, long long v_sh, int T,
+                              const int* cu_new, const void* q, long long q_st, long long q_sh,
+                              void* q_out, long long qo_st, long long qo_sh, int H,
+                              const double* inv_freq, int rot, int interleaved, void* stream);
 
 /*
  * fa_kv_append into an e4m3 cache.  Each page has one scale per head for K and one
@@ -307,12 +307,12 @@ FA_API fa_status fa_kv_append(const fa_paged_cache* cache, const void* k, const 
  * grows its codes are rescaled, rounded to nearest even.  A page whose first row is
  * new takes the new scale.
  */
-FA_API fa_status fa_kv_append_fp8(const fa_paged_cache* cache, const void* k,
-                                  const long long* k_strides, const void* v,
-                                  const long long* v_strides, int T, const int* cu_new, const void* q,
-                                  const long long* q_strides, void* q_out,
-                                  const long long* q_out_strides, int H, const double* inv_freq,
-                                  int rot, int interleaved, void* stream);
+FA_API fa_status fa_kv_append_fp8(const fa_paged_cache* cache, const void* k, long long k_st,
+                                  long long k_sh, const void* v, long long v_st, long long v_sh,
+                                  int T, const int* cu_new, const void* q, long long q_st,
+                                  long long q_sh, void* q_out, long long qo_st, long long qo_sh,
+                                  int H, const double* inv_freq, int rot, int interleaved,
+                                  void* stream);
 
 /*
  * Attention of a decode step over a bf16 paged cache: fa_fwd_decode for sequences of
@@ -323,8 +323,8 @@ FA_API fa_status fa_kv_append_fp8(const fa_paged_cache* cache, const void* k,
  *   j > lens[b] - Nq + i - window or j < sinks.
  * Query head h reads key head h / (H / H_kv); H is a multiple of H_kv.  A row that
  * sees no key (lens[b] < Nq, or 0) is the empty sum: O = 0 and LSE = -inf.
- * Q, O: bf16 [B][H][Nq][d] with the given (sequence, head, row) strides in elements,
- * columns contiguous, 16-byte aligned, strides multiples of 8 and not negative; O's
+ * Q, O: bf16 [B][H][Nq][d] with the given sequence (_sb), head (_sh) and row (_sn)
+ * strides in elements, columns contiguous, 16-byte aligned, strides multiples of 8 and not negative; O's
  * rows must not overlap.  LSE: fp32 [B][H][Nq] contiguous.  window = 0: none;
  * sinks > 0 needs a window.  Rows of a page behind a sequence's end, and keys hidden
  * from every row of the call, are never read.
@@ -335,16 +335,17 @@ FA_API fa_status fa_kv_append_fp8(const fa_paged_cache* cache, const void* k,
  * table are FA_ERR_UNSUPPORTED.
  */
 FA_API size_t fa_paged_workspace_size(int B, int H, int H_kv, int Nq, int d, int fp8);
-FA_API fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* Q, const long long* q_strides,
-                              void* O, const long long* o_strides, float* LSE, int H, int Nq,
-                              float tau, int window, int sinks, void* workspace,
-                              size_t workspace_bytes, void* stream);
+FA_API fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* Q, long long q_sb,
+                              long long q_sh, long long q_sn, void* O, long long o_sb, long long o_sh,
+                              long long o_sn, float* LSE, int H, int Nq, float tau, int window,
+                              int sinks, void* workspace, size_t workspace_bytes, void* stream);
 
 /* fa_fwd_paged over an e4m3 cache (workspace: fa_paged_workspace_size with fp8 = 1). */
-FA_API fa_status fa_fwd_paged_fp8(const fa_paged_cache* cache, const void* Q,
-                                  const long long* q_strides, void* O, const long long* o_strides,
-                                  float* LSE, int H, int Nq, float tau, int window, int sinks,
-                                  void* workspace, size_t workspace_bytes, void* stream);
+FA_API fa_status fa_fwd_paged_fp8(const fa_paged_cache* cache, const void* Q, long long q_sb,
+                                  long long q_sh, long long q_sn, void* O, long long o_sb,
+                                  long long o_sh, long long o_sn, float* LSE, int H, int Nq,
+                                  float tau, int window, int sinks, void* workspace,
+                                  size_t workspace_bytes, void* stream);
 
 /*
  * FP8 forward ("Atencao eficiente - FlashAttention, sparse e hibrida", the

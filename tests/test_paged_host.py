@@ -174,8 +174,8 @@ BAD_CACHES = [
 
 
 def append(c, fp8=False, **kw):
-    a = dict(k=FAKE + 8 * GB, k_strides=(128, 64), v=FAKE + 9 * GB, v_strides=(128, 64), T=4, cu_new=FAKE + 10 * GB,
-             q=FAKE + 11 * GB, q_strides=(256, 64), q_out=FAKE + 12 * GB, q_out_strides=(256, 64), H=4,
+    a = dict(k=FAKE + 8 * GB, k_st=128, k_sh=64, v=FAKE + 9 * GB, v_st=128, v_sh=64, T=4, cu_new=FAKE + 10 * GB,
+             q=FAKE + 11 * GB, q_st=256, q_sh=64, q_out=FAKE + 12 * GB, qo_st=256, qo_sh=64, H=4,
              inv_freq=FAKE + 13 * GB, rot=64, interleaved=0, stream=None)
     a.update(kw)
     return (_lib.fa_kv_append_fp8 if fp8 else _lib.fa_kv_append)(c, *a.values())
@@ -187,16 +187,16 @@ def test_append_refuses_bad_caches(kw, code, fp8):
     assert append(cache(fp8, **kw), fp8) == code
 
 
-NO_Q = dict(q=None, q_strides=None, q_out=None, q_out_strides=None, H=0)
+NO_Q = dict(q=None, q_out=None, H=0)
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(k=None), _lib.FA_ERR_INVALID_ARG),
     (dict(v=FAKE + 9 * GB + 2), _lib.FA_ERR_INVALID_ARG),
-    (dict(k_strides=(128, 60)), _lib.FA_ERR_INVALID_ARG),       # not a multiple of 8
-    (dict(k_strides=(-128, 64)), _lib.FA_ERR_INVALID_ARG),
-    (dict(k_strides=(2 ** 62, 64)), _lib.FA_ERR_INVALID_ARG),   # beyond any address
-    (dict(v_strides=None), _lib.FA_ERR_INVALID_ARG),
+    (dict(k_sh=60), _lib.FA_ERR_INVALID_ARG),       # not a multiple of 8
+    (dict(k_st=-128), _lib.FA_ERR_INVALID_ARG),
+    (dict(k_st=2 ** 62), _lib.FA_ERR_INVALID_ARG),   # beyond any address
+    (dict(v_st=4), _lib.FA_ERR_INVALID_ARG),
     (dict(k=FAKE + 16), _lib.FA_ERR_INVALID_ARG),               # inside the cache
     (dict(T=-1), _lib.FA_ERR_INVALID_ARG),
     (dict(T=3, cu_new=None), _lib.FA_ERR_INVALID_ARG),          # no even split over two sequences
@@ -211,8 +211,8 @@ NO_Q = dict(q=None, q_strides=None, q_out=None, q_out_strides=None, H=0)
     (dict(q_out=None), _lib.FA_ERR_INVALID_ARG),
     (dict(H=0), _lib.FA_ERR_INVALID_ARG),
     (dict(q_out=FAKE + 11 * GB + 32), _lib.FA_ERR_INVALID_ARG),  # neither in place nor apart
-    (dict(q_out=FAKE + 11 * GB, q_out_strides=(512, 64)), _lib.FA_ERR_INVALID_ARG),
-    (dict(q_out_strides=(0, 64)), _lib.FA_ERR_INVALID_ARG),     # rows on top of each other
+    (dict(q_out=FAKE + 11 * GB, qo_st=512), _lib.FA_ERR_INVALID_ARG),
+    (dict(qo_st=0), _lib.FA_ERR_INVALID_ARG),     # rows on top of each other
     (dict(q_out=FAKE + 8 * GB), _lib.FA_ERR_INVALID_ARG),       # over k
     (dict(T=0), _lib.FA_OK),
     (dict(T=0, k=None, v=None, **NO_Q), _lib.FA_OK),
@@ -231,8 +231,8 @@ def test_a_cache_of_the_other_kind_is_refused():
 
 
 def paged(c, fp8=False, **kw):
-    a = dict(Q=FAKE + 8 * GB, q_strides=(256, 64, 64), O=FAKE + 9 * GB, o_strides=(256, 64, 64), LSE=FAKE + 10 * GB,
-             H=4, Nq=1, tau=0.125, window=0, sinks=0, workspace=FAKE + 11 * GB, workspace_bytes=GB, stream=None)
+    a = dict(Q=FAKE + 8 * GB, q_sb=256, q_sh=64, q_sn=64, O=FAKE + 9 * GB, o_sb=256, o_sh=64, o_sn=64,
+             LSE=FAKE + 10 * GB, H=4, Nq=1, tau=0.125, window=0, sinks=0, workspace=FAKE + 11 * GB, workspace_bytes=GB, stream=None)
     a.update(kw)
     return (_lib.fa_fwd_paged_fp8 if fp8 else _lib.fa_fwd_paged)(c, *a.values())
 
@@ -246,10 +246,10 @@ def test_paged_refuses_bad_caches(kw, code, fp8):
 @pytest.mark.parametrize("kw,code", [
     (dict(Q=None), _lib.FA_ERR_INVALID_ARG),
     (dict(O=FAKE + 9 * GB + 4), _lib.FA_ERR_INVALID_ARG),
-    (dict(q_strides=(256, 63, 64)), _lib.FA_ERR_INVALID_ARG),
-    (dict(o_strides=None), _lib.FA_ERR_INVALID_ARG),
-    (dict(o_strides=(256, 0, 64)), _lib.FA_ERR_INVALID_ARG),        # heads on top of each other
-    (dict(o_strides=(128, 64, 64)), _lib.FA_ERR_INVALID_ARG),       # sequences overlap
+    (dict(q_sh=63), _lib.FA_ERR_INVALID_ARG),
+    (dict(LSE=None), _lib.FA_ERR_INVALID_ARG),
+    (dict(o_sh=0), _lib.FA_ERR_INVALID_ARG),        # heads on top of each other
+    (dict(o_sb=128), _lib.FA_ERR_INVALID_ARG),       # sequences overlap
     (dict(H=3), _lib.FA_ERR_INVALID_ARG),                           # not a multiple of H_kv
     (dict(H=-4), _lib.FA_ERR_INVALID_ARG),
     (dict(Nq=9), _lib.FA_ERR_UNSUPPORTED),
