@@ -81,6 +81,7 @@ constexpr int kSplitMaxChunks = 8;
 constexpr int kSplitMinSteps = 16;     // a chunk of fewer query tiles is not worth a CTA
 constexpr int kSplitCtaSteps = 2;      // a CTA's set-up and epilogue cost about two steps
 constexpr int kPlanThreads = 1024;
+constexpr int kSinkMinSteps = 4;       // sinks: the same
 // The plan's arrays in its buffer (byte offsets, each 256-aligned): the number of
 // helper chunks in use (u32); per key tile in launch order kt * BH + bh its chunk
 // count (u8, 1: not split), first partial slot (u32) and finished chunks (u32);
@@ -101,6 +102,15 @@ __host__ __device__ __forceinline__ SplitPlan split_layout(int n_tiles, int n_he
     s.part = s.arrive + up(4 * static_cast<size_t>(n_tiles));
     return s;
 }
+
+// Windows with sinks: a key tile that holds sinks is seen by every later query tile,
+// where a window tile has a few.  Those tiles of all heads come first in launch order,
+// and where one alone would be longer than an SM's share of the work its query list is
+// cut the same way, by arithmetic instead of a plan kernel, into `plan_chunks` chunks.
+// The buffer (dQ again) holds an arrival counter per tile, then the slots, a tile's
+// chunks in a row.  Measured with launch_bwd's rule: one head of 8k tokens, window
+// 1024: 160 -> 40 us (8 chunks); 16 heads of 16k, window 4096: 1114 -> 1097 us (the
+// order alone).
 
 template <int D>
 struct BwdLayout {
@@ -172,8 +182,10 @@ struct BwdParams {
     int BH;                         // persistent: batch*heads
     int items;                      // persistent: work items (BH key tiles each)
     uint8_t* plan;                  // block mask: the split plan's buffer (layout: split_layout)
-    int plan_tiles;                 // its key tiles (BH * n_kv), 0: no plan
+    int plan_tiles;                 // its key tiles (BH * n_kv; sinks: those that hold them, per head), 0: no plan
     int plan_help;                  // its helper CTAs, launched first
+    int plan_chunks;                // sinks: chunks of each tile that holds sinks
+    size_t plan_part;               // sinks: the slots' offset in the buffer
 };
 
 enum : uint32_t {
@@ -266,7 +278,9 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     // a block mask with a split plan (its own instance: the plan's code stays out of
     // the plain block-mask kernel)
     constexpr bool SPLIT_ = SPARSE && SPLIT;
-    static_assert(!SPLIT || SPARSE, "a split plan needs a block mask");
+    // sinks with their key tiles split
+    constexpr bool SINK_SPLIT = SINKS && SPLIT;
+    static_assert(!SPLIT || SPARSE || SINKS, "a split needs a block mask or sinks");
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_addr(smem);
     BwdBarriers& sh = *reinterpret_cast<BwdBarriers*>(smem + L::kBars);
@@ -295,6 +309,27 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             sp_tile = e - p.plan_help;
         }
     }
+    // Sinks: first every head's tiles that hold them, their chunks in a row, then the
+    // others in the order below.
+    int sink_bh = 0, sink_kv = 0;
+    if constexpr (SINK_SPLIT) {
+        const int n_first = p.BH * p.plan_tiles * p.plan_chunks;
+        int i = static_cast<int>(blockIdx.x);
+        if (i < n_first) {
+            sp_chunk = i % p.plan_chunks;
+            i /= p.plan_chunks;
+            sink_kv = i / p.BH;
+            sink_bh = i - sink_kv * p.BH;
+        } else {
+            i -= n_first;
+            const int per_group = p.head_group * (p.n_kv - p.plan_tiles);
+            const int g = i / per_group, j = i - g * per_group;
+            const int heads = min(p.head_group, p.BH - g * p.head_group);
+            sink_kv = j / heads;
+            sink_bh = g * p.head_group + (j - sink_kv * heads);
+            sink_kv += p.plan_tiles;
+        }
+    }
     // Work item k of this CTA: (batch*head, key tile), or false past the last.
     // Without PERSIST a CTA has one item, set by its launch position: the launch
     // order (x fastest) walks groups of p.head_group heads; inside a group the key
@@ -320,6 +355,11 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             ibh = sp_tile - ikv * p.BH;
             return true;
         }
+        if (SINK_SPLIT) {
+            ikv = sink_kv;
+            ibh = sink_bh;
+            return true;
+        }
         const long long i = blockIdx.x + static_cast<long long>(gridDim.x) * blockIdx.y;
         const long long per_group = static_cast<long long>(p.head_group) * p.n_kv;
         const int g = static_cast<int>(i / per_group);
@@ -339,9 +379,19 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     // a tile that holds sinks is seen by every later query tile.
     const int window = (CAUSAL && LOCAL) ? p.window : 0;
     const int sinks = SINKS ? p.sinks : 0;
-    const int first = CAUSAL ? kv_tile : 0;
+    int first = CAUSAL ? kv_tile : 0;
     const int last = window > 0 && (!SINKS || kv_start >= sinks) ? min(n_q - 1, (kv_start + kBK - 1 + window - 1) / kBQ) : n_q - 1;
     int n_steps = last - first + 1;  // with a block mask: counted below
+    int sink_chunks = 1;
+    if constexpr (SINK_SPLIT) {
+        if (kv_start < sinks) {
+            sink_chunks = p.plan_chunks;
+            sp_tile = kv_tile * p.BH + bh;
+            const int lo = sp_chunk * n_steps / sink_chunks;
+            n_steps = (sp_chunk + 1) * n_steps / sink_chunks - lo;
+            first += lo;
+        }
+    }
     // an item's first query tile and step count (item 0: first and n_steps)
     auto first_of = [&](int ikv) { return PERSIST ? (CAUSAL ? ikv : 0) : first; };
     auto steps_of = [&](int ikv) { return PERSIST ? n_q - (CAUSAL ? ikv : 0) : n_steps; };
@@ -904,18 +954,21 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
             // in chunk order.  (Each chunk writes its slot, fences, then counts itself in;
             // the last one fences again before it reads the others' slots.)
             bool store = true;
-            const int nchunks = SPLIT_ ? sh.sp_nchunk : 1;
-            const bool split = SPLIT_ && nchunks > 1;
-            const int tile = SPLIT_ ? sh.sp_tile : 0;
+            const int nchunks = SPLIT_ ? sh.sp_nchunk : SINK_SPLIT ? sink_chunks : 1;
+            const bool split = SPLIT && nchunks > 1;
+            const int tile = SPLIT_ ? sh.sp_tile : sp_tile;
+            const int chunk = SPLIT_ ? sh.sp_chunk : sp_chunk;
             const SplitPlan pl = split_layout(p.plan_tiles, p.plan_help);
-            float* part = split ? reinterpret_cast<float*>(p.plan + pl.part) +
-                                      static_cast<size_t>(reinterpret_cast<const uint32_t*>(p.plan + pl.slot)[tile]) *
-                                          2 * 128 * D
-                                : nullptr;
+            float* part = nullptr;
+            if (split)
+                part = reinterpret_cast<float*>(p.plan + (SINK_SPLIT ? p.plan_part : pl.part)) +
+                       static_cast<size_t>(SINK_SPLIT ? static_cast<uint32_t>(tile * nchunks)
+                                                      : reinterpret_cast<const uint32_t*>(p.plan + pl.slot)[tile]) *
+                           2 * 128 * D;
             if (split) {
                 if (ok) {
                     tc_fence_after();
-                    float* mine = part + static_cast<size_t>(sh.sp_chunk) * 2 * 128 * D;
+                    float* mine = part + static_cast<size_t>(chunk) * 2 * 128 * D;
 #pragma unroll
                     for (int which = 0; which < 2; ++which) {
                         const uint32_t src = tmem + lane_off + (which ? L::kTmDK : L::kTmDV);
@@ -940,7 +993,7 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 named_bar_sync(4, kEW);
                 if (threadIdx.x == 0)
                     sh.last_chunk =
-                        ok && atomicAdd(reinterpret_cast<unsigned int*>(p.plan + pl.arrive) + tile, 1u) ==
+                        ok && atomicAdd(reinterpret_cast<unsigned int*>(p.plan + (SINK_SPLIT ? 0 : pl.arrive)) + tile, 1u) ==
                                   static_cast<unsigned>(nchunks - 1);
                 named_bar_sync(4, kEW);
                 store = sh.last_chunk != 0;
@@ -1199,11 +1252,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) fa_bwd_plan_kernel(const Plan
 
 // D_i = dO_i . O_i in fp32 and a zeroed dQ accumulator row; D/8 threads per row,
 // each handling 8 bf16 of both inputs (16-byte loads).
-template <int D>
+// COUNTERS: block 0 also zeroes the n_count arrival counters of a sink split.
+template <int D, bool COUNTERS>
 __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const __nv_bfloat16* __restrict__ O,
                                                          const __nv_bfloat16* __restrict__ dO,
                                                          float* __restrict__ Dvec,
-                                                         float* __restrict__ dQacc, int64_t rows) {
+                                                         float* __restrict__ dQacc, int64_t rows,
+                                                         unsigned int* counters, int n_count) {
     // launched as a dependent of the previous kernel on the stream (usually the
     // forward, which writes O): wait for it
     griddep_wait();
@@ -1228,6 +1283,8 @@ __global__ void __launch_bounds__(256) fa_bwd_pre_kernel(const __nv_bfloat16* __
 #pragma unroll
     for (int off = TPR / 2; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
     if (row < rows && sub == 0) Dvec[row] = acc;
+    if (COUNTERS && blockIdx.x == 0)
+        for (int i = threadIdx.x; i < n_count; i += blockDim.x) counters[i] = 0u;
     // the main kernel may be scheduled once every CTA of this one is here: its
     // set-up and K, V loads overlap this kernel's last CTAs (it waits for this
     // kernel to finish before reading D or reducing into the accumulator)
@@ -1269,6 +1326,30 @@ int bwd_head_group(int BH, int N, int D, bool causal, int mask) {
     return max(1, min(BH, g));
 }
 
+// How a backward with sinks splits the key tiles that hold them.
+struct SinkPlan {
+    int tiles = 0;    // key tiles that hold sinks, per head
+    int chunks = 1;   // of each (1: no split)
+    size_t part = 0;  // offset of the partial slots in dQ
+};
+SinkPlan sink_plan(const BwdArgs& a, int n_kv, int D, int sms) {
+    SinkPlan s;
+    s.tiles = (std::min(a.sinks, a.N) - 1) / kBK + 1;
+    const int window_steps = std::min((std::min(a.window, a.N) + kBK - 2) / kBK + 1, n_kv);
+    // an SM's share of all query tiles' visits; chunks no shorter than that, than a
+    // window tile's list, or than four steps (their partial sums cost as much)
+    const long long share = (static_cast<long long>(a.BH) *
+                             (static_cast<long long>(n_kv) * window_steps + static_cast<long long>(s.tiles) * n_kv)) / sms;
+    const long long len = std::max<long long>(share, std::max(window_steps, kSinkMinSteps));
+    s.chunks = static_cast<int>(std::min<long long>(kSplitMaxChunks, (n_kv + len - 1) / len));
+    s.part = (static_cast<size_t>(a.BH) * s.tiles * 4 + 255) / 256 * 256;
+    const size_t dq_bytes = static_cast<size_t>(a.BH) * a.N * D * 2, slot = static_cast<size_t>(2) * 128 * D * 4;
+    const size_t room = s.part < dq_bytes ? (dq_bytes - s.part) / slot : 0;
+    s.chunks = static_cast<int>(std::min<size_t>(s.chunks, room / (static_cast<size_t>(a.BH) * s.tiles)));
+    if (s.chunks < 2) s.chunks = 1;
+    return s;
+}
+
 template <int D, bool CAUSAL, int MASK = kMaskNone>
 cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
     using L = BwdLayout<D>;
@@ -1281,7 +1362,7 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
     // overlap the next's
     constexpr bool kCanPersist = D == 64 && MASK == kMaskNone;
     int sms = 0;
-    if (kCanPersist || MASK == kMaskBlocks) {
+    if (kCanPersist || MASK == kMaskBlocks || MASK == kMaskSinks) {
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
@@ -1312,14 +1393,17 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
             pa.causal = CAUSAL;
         }
     }
+    SinkPlan sp{};
+    if (MASK == kMaskSinks) sp = sink_plan(a, n_kv, D, sms);
     // 1. D and a zeroed accumulator
     {
         constexpr int TPR = D / 8;
         const int64_t threads = rows * TPR;
         const unsigned blocks = static_cast<unsigned>((threads + 255) / 256);
-        cudaError_t e = launch_dependent(fa_bwd_pre_kernel<D>, dim3(blocks), dim3(256), 0, stream,
+        cudaError_t e = launch_dependent(fa_bwd_pre_kernel<D, MASK == kMaskSinks>, dim3(blocks), dim3(256), 0, stream,
                                          static_cast<const __nv_bfloat16*>(a.O),
-                                         static_cast<const __nv_bfloat16*>(a.dO), a.D, a.dQacc, rows);
+                                         static_cast<const __nv_bfloat16*>(a.dO), a.D, a.dQacc, rows,
+                                         static_cast<unsigned int*>(a.dQ), sp.chunks > 1 ? a.BH * sp.tiles : 0);
         if (e != cudaSuccess) return e;
     }
     // 2. main kernel
@@ -1336,11 +1420,13 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
             return cudaErrorInvalidValue;
         const long long items = static_cast<long long>(a.BH) * ((a.N + kBK - 1) / kBK);
         const bool persist = kCanPersist && a.N <= kBwdPersistMaxN && items > sms;
-        constexpr auto kern = &fa_bwd_main_kernel<D, CAUSAL, MASK, NWG>;
-        constexpr auto kern_p = &fa_bwd_main_kernel<D, CAUSAL, MASK, NWG, kCanPersist>;
-        constexpr auto kern_s = &fa_bwd_main_kernel<D, CAUSAL, MASK, NWG, false, MASK == kMaskBlocks>;
+        constexpr auto kern = &fa_bwd_main_kernel<D, CAUSAL, MASK, NWG, false, MASK == kMaskSinks>;
+        constexpr auto kern_p = &fa_bwd_main_kernel<D, CAUSAL, MASK, NWG, kCanPersist, MASK == kMaskSinks>;
+        constexpr auto kern_s =
+            &fa_bwd_main_kernel<D, CAUSAL, MASK, NWG, false, MASK == kMaskBlocks || MASK == kMaskSinks>;
+        const bool split = pa.base != nullptr || MASK == kMaskSinks;
         cudaError_t e = persist   ? set_max_dyn_smem_once<kern_p>(L::kBytesPersist)
-                        : pa.base ? set_max_dyn_smem_once<kern_s>(L::kBytes)
+                        : split   ? set_max_dyn_smem_once<kern_s>(L::kBytes)
                                   : set_max_dyn_smem_once<kern>(L::kBytes);
         if (e != cudaSuccess) return e;
         BwdParams p;
@@ -1361,7 +1447,8 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
         if (items > (1ll << 30)) return cudaErrorInvalidValue;
         p.items = static_cast<int>(items);
         p.plan = nullptr;
-        p.plan_tiles = p.plan_help = 0;
+        p.plan_tiles = p.plan_help = p.plan_chunks = 0;
+        p.plan_part = 0;
         dim3 grid(static_cast<unsigned>(a.BH), static_cast<unsigned>(p.n_kv));
         if (persist) grid = dim3(static_cast<unsigned>(sms));
         if (a.ev_start) cudaEventRecord(a.ev_start, stream);
@@ -1373,9 +1460,16 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
             p.plan_help = pa.n_help;
             grid = dim3(static_cast<unsigned>(n_tiles + pa.n_help));
         }
+        if (MASK == kMaskSinks) {
+            p.plan = static_cast<uint8_t*>(a.dQ);
+            p.plan_chunks = sp.chunks;
+            p.plan_tiles = sp.tiles;
+            p.plan_part = sp.part;
+            grid = dim3(static_cast<unsigned>(items + static_cast<long long>(a.BH) * sp.tiles * (sp.chunks - 1)));
+        }
         e = persist   ? launch_dependent(kern_p, grid, dim3(bwd_threads(NWG)), L::kBytesPersist, stream, tq, tk,
                                          tv, tdo, tacc, tdk, tdv, p)
-            : pa.base ? launch_dependent(kern_s, grid, dim3(bwd_threads(NWG)), L::kBytes, stream, tq, tk, tv, tdo,
+            : split   ? launch_dependent(kern_s, grid, dim3(bwd_threads(NWG)), L::kBytes, stream, tq, tk, tv, tdo,
                                          tacc, tdk, tdv, p)
                       : launch_dependent(kern, grid, dim3(bwd_threads(NWG)), L::kBytes, stream, tq, tk, tv, tdo,
                                          tacc, tdk, tdv, p);

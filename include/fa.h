@@ -171,7 +171,9 @@ FA_API fa_status fa_fwd_sinks(const void* Q, const void* K, const void* V, void*
 
 /*
  * Backward for the mask of fa_fwd_sinks (LSE must come from fa_fwd_sinks with the
- * same window and sinks).  Same workspace rules as fa_bwd.
+ * same window and sinks).  Same workspace rules as fa_bwd.  Until its last kernel
+ * writes dQ, the call keeps in dQ's memory the partial dK, dV of the key tiles that
+ * hold sinks, whose query lists extra CTAs share.
  */
 FA_API fa_status fa_bwd_sinks(const void* Q, const void* K, const void* V, const void* O,
                               const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
