@@ -221,14 +221,9 @@ __device__ __forceinline__ float amax8(const uint4& w, float m) {
 
 // Four e4m3 codes rescaled by r (rounded to nearest even).
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
-    float2 a, b;
     uint32_t lo, hi;
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(lo), "=r"(hi) : "r"(w));
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-        : "=f"(a.x), "=f"(a.y) : "r"(lo));
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
-        : "=f"(b.x), "=f"(b.y) : "r"(hi));
+    widen_e4m3x4(w, lo, hi);
+    const float2 a = unpack_f16(lo), b = unpack_f16(hi);
     return pack_e4m3x4(a.x * r, a.y * r, b.x * r, b.y * r);
 }
 

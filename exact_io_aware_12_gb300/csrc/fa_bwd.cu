@@ -278,6 +278,13 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     // a block mask with a split plan (its own instance: the plan's code stays out of
     // the plain block-mask kernel)
     constexpr bool SPLIT_ = SPARSE && SPLIT;
+    // With sinks dS is formed from P before its rounding to bf16 and rounded once,
+    // where the other masks multiply two rounded factors (dQ, dK rel-L2 3.4e-3 ->
+    // 2.5e-3): kept in fp32 at d = 64 (no slower), as fp16 pairs at d = 128, where fp32
+    // spills (10% slower; the pairs cost 1.7%).  P <= 1, so fp16 is off by 2^-12 of it,
+    // or 2^-25 in all below 2^-14.
+    constexpr bool DS_FP32 = SINKS && D == 64, DS_FP16 = SINKS && D == 128;
+    static_assert(!DS_FP16 || kQC == 32, "one chunk per warpgroup");
     // sinks with their key tiles split
     constexpr bool SINK_SPLIT = SINKS && SPLIT;
     static_assert(!SPLIT || SPARSE || SINKS, "a split needs a block mask or sinks");
@@ -784,6 +791,7 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 const ulonglong2* nl4 = reinterpret_cast<const ulonglong2*>(lse2_s + st * 128 + kQC * h);
                 ulonglong2 nl0[8];
                 uint32_t pkeep[16];  // the first chunk's packed P^T, reused by dS^T below
+                [[maybe_unused]] float pf[DS_FP32 ? kQC : 1];  // P^T before its rounding
                 if (ok) ok = __all_sync(FULL, mbar_wait_sleep(bar_qf + 8 * st, (gs >> 1) & 1, wd, kSiteDsQ));
                 if (ok) {
 #pragma unroll
@@ -830,12 +838,17 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                                     if (q + 1 < lo || q + 1 >= hi) p1 = 0.f;
                                 }
                                 pk[i] = pack_bf16(p0, p1);
+                                if constexpr (DS_FP32) {
+                                    pf[32 * c + 2 * i] = p0;
+                                    pf[32 * c + 2 * i + 1] = p1;
+                                }
+                                if constexpr (DS_FP16) pkeep[i] = pack_f16(p0, p1);
                             }
                         };
                         if (masked) p_pairs(std::true_type{});
                         else p_pairs(std::false_type{});
                         tmem_st16(tS + 16 * c, pk);
-                        if (c == 0) {
+                        if (c == 0 && !DS_FP16) {
 #pragma unroll
                             for (int i = 0; i < 16; ++i) pkeep[i] = pk[i];
                         }
@@ -866,12 +879,14 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     for (int c = 0; c < kQC / 32; ++c) {
                         uint32_t dp[32], pk[16];
                         tmem_ld32(tDP + 32 * c, dp);
-                        if (c == 0) {
+                        if constexpr (!SINKS) {
+                            if (c == 0) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) pk[i] = pkeep[i];
-                        } else {
-                            tmem_ld16(tS + 16 * c, pk);
-                            tmem_ld_wait(pk);
+                                for (int i = 0; i < 16; ++i) pk[i] = pkeep[i];
+                            } else {
+                                tmem_ld16(tS + 16 * c, pk);
+                                tmem_ld_wait(pk);
+                            }
                         }
                         tmem_ld_wait(dp);
                         uint32_t ds[16];
@@ -881,10 +896,18 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             const uint64_t ndq = (i & 1) ? nd[i >> 1].y : nd[i >> 1].x;
-                            // dP - D in fp32, rounded to bf16, times the bf16 P
+                            // dP - D in fp32, rounded to bf16, times the bf16 P (sinks: P
+                            // as kept, the product rounded once)
                             const float2 t = f2_unpack(
                                 fadd2(f2_pack(u2f(dp[2 * i]), u2f(dp[2 * i + 1])), ndq));
-                            ds[i] = mul_bf16x2(pk[i], pack_bf16(t.x, t.y));
+                            if constexpr (DS_FP16) {
+                                const float2 pp = unpack_f16(pkeep[i]);
+                                ds[i] = pack_bf16(pp.x * t.x, pp.y * t.y);
+                            } else if constexpr (DS_FP32) {
+                                ds[i] = pack_bf16(pf[32 * c + 2 * i] * t.x, pf[32 * c + 2 * i + 1] * t.y);
+                            } else {
+                                ds[i] = mul_bf16x2(pk[i], pack_bf16(t.x, t.y));
+                            }
                         }
                         if constexpr (L::kDSInTmem) tmem_st16(tS + kQC / 2 + 16 * c, ds);
 #pragma unroll

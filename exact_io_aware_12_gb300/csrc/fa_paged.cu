@@ -130,18 +130,6 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
     return r;
 }
 
-// Four e4m3 codes -> two fp16 pairs (exact): a = codes 0, 1; b = codes 2, 3.
-__device__ __forceinline__ void widen4(uint32_t w, uint32_t& a, uint32_t& b) {
-    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(a), "=r"(b) : "r"(w));
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
 __device__ __forceinline__ float lg2(float x) {  // log2, -inf at 0
     float y;
     asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -444,8 +432,8 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         uint32_t a0, a2, a1, a3;
-                        widen4(a[h], a0, a2);
-                        widen4(bb[h], a1, a3);
+                        widen_e4m3x4(a[h], a0, a2);
+                        widen_e4m3x4(bb[h], a1, a3);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt)
                             mma16816<true>(s[nt], a0, a1, a2, a3, q[nt][4 * c + h][0], q[nt][4 * c + h][1]);
@@ -568,10 +556,10 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
 #pragma unroll
                 for (int j = 0; j < W; ++j) {
                     uint32_t f[8];  // [lo: elements 4 j .. 4 j + 3, hi: the same]
-                    widen4(__byte_perm(a[0][j], a[1][j], 0x5140), f[0], f[1]);
-                    widen4(__byte_perm(a[0][j], a[1][j], 0x7362), f[2], f[3]);
-                    widen4(__byte_perm(a[2][j], a[3][j], 0x5140), f[4], f[5]);
-                    widen4(__byte_perm(a[2][j], a[3][j], 0x7362), f[6], f[7]);
+                    widen_e4m3x4(__byte_perm(a[0][j], a[1][j], 0x5140), f[0], f[1]);
+                    widen_e4m3x4(__byte_perm(a[0][j], a[1][j], 0x7362), f[2], f[3]);
+                    widen_e4m3x4(__byte_perm(a[2][j], a[3][j], 0x5140), f[4], f[5]);
+                    widen_e4m3x4(__byte_perm(a[2][j], a[3][j], 0x7362), f[6], f[7]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         mma16816<true>(acc[nt][2 * j], f[0], f[1], f[4], f[5], pb[nt][0], pb[nt][1]);
