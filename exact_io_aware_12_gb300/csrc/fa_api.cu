@@ -714,7 +714,7 @@ static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, 
     if (c->B == 0 || c->H_kv == 0 || H == 0 || Nq == 0) return FA_OK;
     if (H % c->H_kv != 0) return FA_ERR_INVALID_ARG;
     if (Nq > 8 || H / c->H_kv > (1 << 20)) return FA_ERR_UNSUPPORTED;
-    if (paged_max_steps(c->B, H, c->H_kv, Nq, c->max_pages, a.cache.shift) > INT_MAX) return FA_ERR_UNSUPPORTED;
+    if (paged_max_tiles(c->B, H, c->H_kv, Nq, c->max_pages, a.cache.shift) > INT_MAX) return FA_ERR_UNSUPPORTED;
     if (Q == nullptr || O == nullptr || LSE == nullptr) return FA_ERR_INVALID_ARG;
     if (!aligned16(Q) || !aligned16(O) || !aligned16(LSE)) return FA_ERR_INVALID_ARG;
     if (workspace != nullptr && !aligned16(workspace)) return FA_ERR_INVALID_ARG;

@@ -144,8 +144,8 @@ struct PagedArgs {
 };
 // Bytes of workspace one such step takes, whatever the sequences' lengths.
 size_t paged_workspace(int B, int H, int H_kv, int Nq, int d, bool fp8);
-// Block steps that a full table holds: the launcher's 32-bit step counts must not pass.
-long long paged_max_steps(int B, int H, int H_kv, int Nq, int max_pages, int shift);
+// 16-key tiles that full tables hold, which 32-bit counts must not pass.
+long long paged_max_tiles(int B, int H, int H_kv, int Nq, int max_pages, int shift);
 
 // Whether a causal window of `window` keys (0: none) beside `sinks` first keys hides
 // anything that the causal mask shows: the last query, N - 1, sees neither the keys

@@ -8,15 +8,19 @@
 // visible K and V once, so HBM bounds it.
 //
 // Design:
-//   - Work is cut evenly whatever the lengths: the 64-key steps of all (sequence, key
-//     head, row block) segments form one list, and each of the resident CTAs takes an
-//     equal contiguous share of it, found from a prefix sum of the lengths, which stay
-//     on the device.  A segment that several shares cut leaves one partial result per
-//     piece (normalised, with its log-sum), which the combine kernel adds.
-//   - The four warps of a CTA take one 16-key tile each per step and share nothing until
-//     the segment ends: no block barrier in the loop.  A warp streams its own tiles
-//     through its own ring of shared memory with 16-byte cp.async, written in the XOR
-//     order that makes the 16-byte fragment loads below free of bank conflicts.
+//   - Work is cut evenly whatever the lengths: the 16-key tiles of all (sequence, key
+//     head) segments form one list, and every resident warp takes an equal contiguous
+//     share of it, found from a prefix sum of the lengths, which stay on the device.  A
+//     segment that several shares cut leaves one partial result per piece (normalised,
+//     with its log-sum), which the combine kernel adds.  Shares are per warp, not per
+//     CTA: warps share nothing and never wait for one another, and a warp meets fewer
+//     segment borders (1 + segments / warps), where its pipeline drains.
+//   - A warp holds 8 or 16 query rows.  With more rows, 2 or 4 warps of a CTA take the
+//     same share for 16 rows each and read the same keys at about the same time, all but
+//     one of them from L2.
+//   - A warp streams its tiles through its own ring of shared memory with 16-byte
+//     cp.async, written in the XOR order that makes the 16-byte fragment loads below
+//     free of bank conflicts.
 //   - Both products run on warp matrix instructions with the keys (and the columns of
 //     V) as the 16-row operand and 8 query rows as the narrow one: S^T = K Q^T and
 //     O^T = V^T P^T, so grouped heads fill a tile with little padding.  At 16 query rows
@@ -64,13 +68,13 @@ struct PagedLayout {
     static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a key row
     static constexpr int kTile = kPagedTile * kRow;     // K or V of one tile
     static constexpr int kSlot = 2 * kTile;
-    static constexpr int kCtas = NT == 4 ? 2 : kSlot == 8192 ? 2 : NT == 2 ? 3 : 4;
-    static constexpr int kStages = kSlot == 8192 ? 3 : kSlot == 4096 ? (NT == 1 ? 3 : NT == 2 ? 4 : 6) : 6;
+    static constexpr int kCtas = kSlot == 8192 ? 2 : NT == 2 ? 3 : 4;
+    static constexpr int kStages = kSlot == 8192 ? 3 : kSlot == 4096 ? (NT == 1 ? 3 : 4) : 6;
     static constexpr int kWarpRing = kStages * kSlot;
-    static constexpr int kRing = kPagedWarps * kWarpRing;
-    static constexpr int kRed = kPagedWarps * 8 * D * 4;  // merge buffer over the idle ring
-    static constexpr int kBytes = kRing > kRed ? kRing : kRed;
+    static constexpr int kBytes = kPagedWarps * kWarpRing;
 };
+constexpr int kMinTiles = 2;  // per warp: below, its start and end cost more than they save
+constexpr int kMaxResults = 512;  // pieces of a segment: more cost the combine kernel more than they save
 
 struct PagedParams {
     const __nv_bfloat16* Q;
@@ -82,11 +86,13 @@ struct PagedParams {
     const int* lens;
     __nv_bfloat16* O;
     float* LSE;
-    int2* seg;       // [segments]: (first share, pieces) of a segment in several pieces
-    float* part_o;   // [2 shares][8 NT][D]
-    float* part_l;   // [2 shares][8 NT], log2 of the piece's sum
+    int2* seg;       // [segments]: a segment's first share and number of pieces
+    float* part_o;   // [2 per warp][8 NT][D]
+    float* part_l;   // [2 per warp][8 NT], log2 of the piece's sum
     long long q_sb, q_sh, q_sn, o_sb, o_sh, o_sn;
-    int B, H, H_kv, G, Nq, rblocks, num_pages, max_pages, shift, window, sinks;
+    int B, H, H_kv, G, Nq, num_pages, max_pages, shift, window, sinks;
+    int rwarps;        // warps that share a share, 8 NT query rows each (1, 2 or 4)
+    int rgroups;       // segments per (sequence, key head): rwarps * 8 NT query rows each
     float scale_log2;  // tau * log2(e)
     unsigned int* err;
 };
@@ -175,9 +181,8 @@ __device__ __forceinline__ int clamp_len(const PagedParams& p, int b) {
 struct PagedShared {
     int key0[kPagedWarps][8];     // per ring slot: first key of the tile (a bad page: past every row)
     float ks[kPagedWarps][8], vs[kPagedWarps][8];  // 8-bit: the page's scales
-    float m[kPagedWarps][32], l[kPagedWarps][32], mv[kPagedWarps][32];
     int scan[kPagedWarps];
-    int at_b, at_before;  // the share's first sequence, steps of the sequences before it
+    int at_b[kPagedWarps], at_before[kPagedWarps];  // a share's first sequence, tiles of those before it
 };
 
 template <int D, int NT, bool F8>
@@ -194,13 +199,13 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
     const uint32_t ring = smem_addr(smem) + warp * L::kWarpRing;
     griddep_launch_dependents();
 
-    // ---- this CTA's share of the steps ----
-    const int segs_per_b = p.H_kv * p.rblocks;
+    // ---- this warp's share of the tiles ----
+    const int segs_per_b = p.H_kv * p.rgroups;
     const int per = (p.B + kThreads - 1) / kThreads;
     int mine = 0;
     for (int i = 0; i < per; ++i) {
         const int b = tid * per + i;
-        if (b < p.B) mine += paged_steps(paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks));
+        if (b < p.B) mine += paged_tiles(paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks));
     }
     int incl = mine;
 #pragma unroll
@@ -216,44 +221,65 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
         if (w < warp) before += sh.scan[w];
         total_b += sh.scan[w];
     }
-    // (no share is empty: with fewer steps than CTAs the last CTAs have none)
-    const long long total = static_cast<long long>(total_b) * segs_per_b;
-    const long long shares = min(static_cast<long long>(gridDim.x), total);
-    if (blockIdx.x >= shares) return;
-    long long x = share_start(blockIdx.x, total, shares);
-    const long long x_end = share_start(blockIdx.x + 1ll, total, shares);
-    {
-        const int xs = static_cast<int>(x / segs_per_b);  // steps of whole sequences before x, rounded down
+    const uint32_t total = static_cast<uint32_t>(total_b) * segs_per_b, segs = static_cast<uint32_t>(p.B) * segs_per_b;
+    const int per_cta = kPagedWarps / p.rwarps;  // shares of a CTA
+    // (no share is empty: with few tiles the last warps have none)
+    const uint32_t shares = max(1u, min(min(gridDim.x * per_cta, total / kMinTiles), segs * kMaxResults));
+    const Shares cut(total, shares);
+    for (int w = 0; w < per_cta; ++w) {
+        const uint32_t c = blockIdx.x * per_cta + w;
+        if (c >= shares) break;
+        // the whole sequences' tiles before the share's first, rounded down
+        const int xs = static_cast<int>(cut.start(c) / segs_per_b);
         if (xs >= before && xs < before + mine) {
             int b = tid * per, at = before;
             for (;; ++b) {
-                const int n = paged_steps(paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks));
+                const int n = paged_tiles(paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks));
                 if (xs < at + n) break;
                 at += n;
             }
-            sh.at_b = b;
-            sh.at_before = at;
+            sh.at_b[w] = b;
+            sh.at_before[w] = at;
         }
     }
     __syncthreads();
-    int b = sh.at_b;
-    long long b_first = static_cast<long long>(sh.at_before) * segs_per_b;  // first step of sequence b
+    const int wshare = warp / p.rwarps, rw = warp - wshare * p.rwarps;
+    const uint32_t share = blockIdx.x * per_cta + wshare;
+    if (share >= shares) return;  // (from here on the warps go their own ways)
+    uint32_t x = cut.start(share);
+    const uint32_t x_end = cut.start(share + 1);
+    int b = sh.at_b[wshare];
+    uint32_t b_first = static_cast<uint32_t>(sh.at_before[wshare]) * segs_per_b;  // first tile of sequence b
     PagedRange rg = paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks);
-    int steps = paged_steps(rg);
+    uint32_t tiles = paged_tiles(rg);
 
     while (true) {
-        // ---- one piece: steps [u0, u1) of segment (b, hk, rb) ----
-        const int in_b = static_cast<int>((x - b_first) / steps);
-        const long long seg_first = b_first + static_cast<long long>(in_b) * steps;
-        const int hk = in_b / p.rblocks, rb = in_b - hk * p.rblocks;
+        // ---- one piece: tiles [u0, u1) of segment (b, hk, rb group) ----
+        const int in_b = static_cast<int>((x - b_first) / tiles);
+        const uint32_t seg_first = b_first + in_b * tiles;
+        const int hk = in_b / p.rgroups;
         const int u0 = static_cast<int>(x - seg_first);
-        const int u1 = static_cast<int>(min(static_cast<long long>(steps), x_end - seg_first));
+        const int u1 = static_cast<int>(min(tiles, x_end - seg_first));
+        const auto next = [&]() {  // on to the next segment; false at the share's end
+            x = seg_first + u1;
+            if (x >= x_end) return false;
+            if (x >= b_first + tiles * segs_per_b) {
+                b_first += tiles * segs_per_b;
+                ++b;
+                rg = paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks);
+                tiles = paged_tiles(rg);
+            }
+            return true;
+        };
+        if (u0 > 0 && u0 >= rg.n) {  // only a segment's empty tiles
+            if (!next()) return;
+            continue;
+        }
         const int len = rg.len;
-        const int row0 = rb * R, rows = min(R, p.G * p.Nq - row0);
-        // row r of the segment: head hk G + (row0 + r) / Nq, position (row0 + r) % Nq
-        // tiles of this warp: list entries 4 (u0 + i) + warp
-        const int nv = max(0, min(u1 - u0, (rg.n - warp + kPagedWarps - 1) / kPagedWarps - u0));
-        const auto entry = [&](int i) { return kPagedWarps * (u0 + i) + warp; };
+        // row r of this warp: head hk G + (row0 + r) / Nq, position (row0 + r) % Nq
+        const int row0 = ((in_b - hk * p.rgroups) * p.rwarps + rw) * R;
+        const int rows = min(R, p.G * p.Nq - row0);  // (none for the last warps of a share)
+        const int nv = rows > 0 ? max(0, min(u1, rg.n) - u0) : 0;
         const int* table = p.table + static_cast<long long>(b) * p.max_pages;
 
         // pages of 32 tiles at a time, one per lane; the next 32 are fetched halfway
@@ -263,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
             const int i = base + lane;
             page = -1;
             if (i < nv) {
-                page = page_of(table, p.max_pages, p.num_pages, p.shift, rg.key0(entry(i)));
+                page = page_of(table, p.max_pages, p.num_pages, p.shift, rg.key0(u0 + i));
                 if (page < 0) atomicCAS(p.err, 0u, kErrPage);
                 if constexpr (F8) {
                     if (page >= 0) {
@@ -285,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
             }
             if ((i & 31) == 16) fetch((i & ~31) + 32, pg_next, ks_next, vs_next);
             const int slot = i % S;
-            const int key0 = rg.key0(entry(i));
+            const int key0 = rg.key0(u0 + i);
             const int page = __shfl_sync(0xffffffffu, pg, i & 31);
             const long long off =
                 page < 0 ? 0
@@ -570,151 +596,182 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
         }
         cp_wait<0>();
 
-        // ---- join the four warps ----
-        // (row sums and weights: over the lanes that share t4)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                l_run[nt][e] = sum_over_g(l_run[nt][e]);
-                if (g == 0) {
-                    sh.m[warp][nt * 8 + 2 * t4 + e] = m_run[nt][e];
-                    sh.l[warp][nt * 8 + 2 * t4 + e] = l_run[nt][e];
-                    if (F8) sh.mv[warp][nt * 8 + 2 * t4 + e] = mv_run[nt][e];
-                }
-            }
-        __syncthreads();
-        const bool final_piece = u0 == 0 && u1 == steps;
-        const long long slot = 2ll * blockIdx.x + (u0 == 0 ? 1 : 0);
-        float* red = reinterpret_cast<float*>(smem);  // [warp][8 rows][D]
-        const auto log_sum = [&](int r, float& m_all) {  // log2 of the row's sum, and its max
-            m_all = fmaxf(fmaxf(sh.m[0][r], sh.m[1][r]), fmaxf(sh.m[2][r], sh.m[3][r]));
-            const float ref = m_all == -INFINITY ? 0.f : m_all;
-            float sum = 0.f;
-#pragma unroll
-            for (int w = 0; w < kPagedWarps; ++w) sum += sh.l[w][r] * ex2(sh.m[w][r] - ref);
-            return ref + lg2(sum);  // -inf for a row that sees nothing, NaN where a score was
-        };
+        // ---- this piece's result ----
+        const bool final_piece = u0 == 0 && u1 >= rg.n;
+        const long long slot = 2ll * (static_cast<long long>(blockIdx.x) * kPagedWarps + warp) + (u0 == 0 ? 1 : 0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = nt * 8 + 2 * t4 + e;
-                float m_all;
-                const float ls = log_sum(r, m_all);
-                const float ref = F8 ? mv_run[nt][e] : m_run[nt][e];
-                const float f = ls == -INFINITY || (ref == -INFINITY && ls == ls) ? 0.f : ex2(ref - ls);
-                float* dst = red + (warp * 8 + 2 * t4 + e) * D;
+                const float l = sum_over_g(l_run[nt][e]), m = m_run[nt][e];
+                // (a row that sees nothing: l = 0 and O = 0, LSE = -inf; NaN where a score was)
+                float f = l == 0.f ? 0.f : 1.f / l;
+                if (F8 && l != 0.f) f *= ex2(mv_run[nt][e] - m);
+                const float ls = (m == -INFINITY ? 0.f : m) + lg2(l);
+                if (r >= rows) continue;
+                constexpr int RUN = F8 ? D / 8 : 8;  // columns that lie together
+                if (final_piece) {
+                    const int hh = (row0 + r) / p.Nq, qi = (row0 + r) - hh * p.Nq, h = hk * p.G + hh;
+                    __nv_bfloat16* dst = p.O + b * p.o_sb + static_cast<long long>(h) * p.o_sh + qi * p.o_sn;
 #pragma unroll
-                for (int j = 0; j < MT; ++j) {
-                    // columns of elements 2 j and 2 j + 1
-                    const int col = F8 ? (D / 8) * g + 2 * j : 64 * (j / 4) + 8 * g + 2 * (j % 4);
-                    *reinterpret_cast<float2*>(dst + col) = make_float2(acc[nt][j][e] * f, acc[nt][j][e + 2] * f);
+                    for (int j = 0; j < MT; j += 4) {
+                        const int col = (2 * j / RUN) * (8 * RUN) + RUN * g + 2 * j % RUN;
+                        *reinterpret_cast<uint4*>(dst + col) =
+                            make_uint4(pack_bf16(acc[nt][j][e] * f, acc[nt][j][e + 2] * f),
+                                       pack_bf16(acc[nt][j + 1][e] * f, acc[nt][j + 1][e + 2] * f),
+                                       pack_bf16(acc[nt][j + 2][e] * f, acc[nt][j + 2][e + 2] * f),
+                                       pack_bf16(acc[nt][j + 3][e] * f, acc[nt][j + 3][e + 2] * f));
+                    }
+                    if (g == 0) p.LSE[(static_cast<long long>(b) * p.H + h) * p.Nq + qi] = ls * kLn2;
+                } else {
+                    float* dst = p.part_o + (slot * R + r) * D;
+#pragma unroll
+                    for (int j = 0; j < MT; j += 2) {
+                        const int col = (2 * j / RUN) * (8 * RUN) + RUN * g + 2 * j % RUN;
+                        *reinterpret_cast<float4*>(dst + col) =
+                            make_float4(acc[nt][j][e] * f, acc[nt][j][e + 2] * f, acc[nt][j + 1][e] * f,
+                                        acc[nt][j + 1][e + 2] * f);
+                    }
+                    if (g == 0) p.part_l[slot * R + r] = ls;
                 }
             }
-            __syncthreads();
-            for (int e = tid; e < 8 * (D / 4); e += kThreads) {
-                const int rl = e / (D / 4), col = (e % (D / 4)) * 4, r = nt * 8 + rl;
-                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (u0 == 0 && rw == 0 && lane == 0) {
+            const int pieces = static_cast<int>(cut.of(seg_first + max(1, rg.n) - 1) - share) + 1;
+            p.seg[static_cast<long long>(b) * segs_per_b + in_b] =
+                make_int2(static_cast<int>(share), pieces);
+        }
+        if (!next()) return;
+        __syncwarp();  // (the ring's last slots have been read)
+    }
+}
+
+// Adds a segment's pieces: O = sum_s 2^(l_s - L) O_s, L = log2 sum_s 2^(l_s).  Block
+// (segment, y) takes the rows y, y + gridDim.y, ...  With few pieces a warp adds a row by
+// itself, its loads all in flight at once; with many, the block's warps take them in turn,
+// eight at a time, and are added in warp order.
+constexpr int kFewPieces = 16;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(1024) fa_paged_combine_kernel(const PagedParams p) {
+    constexpr int R = 8 * NT, PER = D / 32, kBatch = 8;
+    __shared__ float red[32][D];
+    __shared__ float red_l[32];
+    const int segs_per_b = p.H_kv * p.rgroups;
+    const int b = static_cast<int>(blockIdx.x) / segs_per_b, in_b = static_cast<int>(blockIdx.x) - b * segs_per_b;
+    const int hk = in_b / p.rgroups, row0 = (in_b - hk * p.rgroups) * p.rwarps * R;
+    const int rows = min(p.rwarps * R, p.G * p.Nq - row0);
+    const int per_cta = kPagedWarps / p.rwarps, warps = static_cast<int>(blockDim.x >> 5);
+    const int warp = static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    griddep_wait();
+    const int2 sg = p.seg[blockIdx.x];
+    const int n = sg.y;
+    if (n <= 1) return;
+    const bool few = n <= kFewPieces;
+    const int rstep = static_cast<int>(gridDim.y) * (few ? warps : 1);
+    for (int row = static_cast<int>(blockIdx.y) + (few ? warp * static_cast<int>(gridDim.y) : 0); row < rows; row += rstep) {
+        const int rw = row / R, r = row - rw * R;
+        // piece 0 lies in its warp's second slot (it ends the share), the others in their first
+        const auto at = [&](int s) {
+            const int share = sg.x + s;
+            const long long w = static_cast<long long>(share / per_cta) * kPagedWarps + share % per_cta * p.rwarps + rw;
+            return (2 * w + (s == 0 ? 1 : 0)) * R + r;
+        };
+        float sum = 0.f, ref;
+        float acc[PER];
 #pragma unroll
-                for (int w = 0; w < kPagedWarps; ++w) {
-                    const float4 y = *reinterpret_cast<const float4*>(red + (w * 8 + rl) * D + col);
-                    o.x += y.x;
-                    o.y += y.y;
-                    o.z += y.z;
-                    o.w += y.w;
-                }
-                if (r < rows) {
-                    if (final_piece) {
-                        const int hh = (row0 + r) / p.Nq, qi = (row0 + r) - hh * p.Nq;
-                        __nv_bfloat16* dst = p.O + b * p.o_sb + static_cast<long long>(hk * p.G + hh) * p.o_sh + qi * p.o_sn + col;
-                        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+        for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+        // pieces s0 .. s0 + 7 (below n), their weights in w of lanes 0 .. 7
+        float v[kBatch][PER];
+        const auto load = [&](int s0) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (s0 + k < n) {
+                    const float* src = p.part_o + at(s0 + k) * D + lane * PER;
+                    if constexpr (PER == 4) {
+                        const float4 y = *reinterpret_cast<const float4*>(src);
+                        v[k][0] = y.x;
+                        v[k][1] = y.y;
+                        v[k][2] = y.z;
+                        v[k][3] = y.w;
                     } else {
-                        *reinterpret_cast<float4*>(p.part_o + (slot * R + r) * D + col) = o;
+                        const float2 y = *reinterpret_cast<const float2*>(src);
+                        v[k][0] = y.x;
+                        v[k][1] = y.y;
                     }
                 }
             }
+        };
+        const auto add = [&](int s0, float w) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, w, k);
+                if (s0 + k < n) {
+#pragma unroll
+                    for (int e = 0; e < PER; ++e) acc[e] = fmaf(wk, v[k][e], acc[e]);
+                }
+            }
+        };
+        if (few) {
+            load(0);
+            const float l = lane < n ? p.part_l[at(lane)] : -INFINITY;
+            float m = l;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            ref = m == -INFINITY ? 0.f : m;
+            const float w = ex2(l - ref);
+            sum = w;
+            add(0, w);
+            if (n > kBatch) {
+                load(kBatch);
+                add(kBatch, __shfl_down_sync(0xffffffffu, w, kBatch));
+            }
+        } else {
+            float m = -INFINITY;
+            for (int s = threadIdx.x; s < n; s += blockDim.x) m = fmaxf(m, p.part_l[at(s)]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            __syncthreads();  // (the row before has been written)
+            if (lane == 0) red_l[warp] = m;
             __syncthreads();
-        }
-        if (tid < rows) {
-            float m_all;
-            const float ls = log_sum(tid, m_all);
-            if (final_piece) {
-                const int hh = (row0 + tid) / p.Nq, qi = (row0 + tid) - hh * p.Nq;
-                p.LSE[(static_cast<long long>(b) * p.H + hk * p.G + hh) * p.Nq + qi] = ls * kLn2;
-            } else {
-                p.part_l[slot * R + tid] = ls;
+            for (int k = 0; k < warps; ++k) m = fmaxf(m, red_l[k]);
+            __syncthreads();
+            ref = m == -INFINITY ? 0.f : m;
+            for (int s0 = warp * kBatch; s0 < n; s0 += warps * kBatch) {
+                load(s0);
+                const float w = lane < min(kBatch, n - s0) ? ex2(p.part_l[at(s0 + lane)] - ref) : 0.f;
+                sum += w;
+                add(s0, w);
             }
         }
-        if (u0 == 0 && tid == 0) {
-            const int pieces =
-                final_piece ? 1 : static_cast<int>(share_of(seg_first + steps - 1, total, shares) - blockIdx.x) + 1;
-            p.seg[static_cast<long long>(b) * segs_per_b + in_b] = make_int2(static_cast<int>(blockIdx.x), pieces);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (!few) {
+#pragma unroll
+            for (int e = 0; e < PER; ++e) red[warp][lane * PER + e] = acc[e];
+            if (lane == 0) red_l[warp] = sum;
+            __syncthreads();
+            if (warp > 0) continue;
+            for (int k = 1; k < warps; ++k) {
+                sum += red_l[k];
+#pragma unroll
+                for (int e = 0; e < PER; ++e) acc[e] += red[k][lane * PER + e];
+            }
         }
-        x = seg_first + u1;
-        if (x >= x_end) return;
-        __syncthreads();  // (sh.m, sh.l are read above)
-        if (x >= b_first + static_cast<long long>(steps) * segs_per_b) {
-            b_first += static_cast<long long>(steps) * segs_per_b;
-            ++b;
-            rg = paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks);
-            steps = paged_steps(rg);
-        }
+        const int hh = (row0 + row) / p.Nq, qi = (row0 + row) - hh * p.Nq, h = hk * p.G + hh;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (0: the row sees nothing)
+        __nv_bfloat16* dst = p.O + b * p.o_sb + static_cast<long long>(h) * p.o_sh + qi * p.o_sn + lane * PER;
+        if constexpr (PER == 4)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+        else
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
+        if (lane == 0) p.LSE[(static_cast<long long>(b) * p.H + h) * p.Nq + qi] = (ref + lg2(sum)) * kLn2;
     }
 }
 
-// Adds a segment's pieces: O = sum_s 2^(l_s - L) O_s, L = log2 sum_s 2^(l_s).  One block
-// per segment and eight rows, one warp per row.
-template <int D, int NT>
-__global__ void __launch_bounds__(256) fa_paged_combine_kernel(const PagedParams p) {
-    constexpr int R = 8 * NT, PER = D / 32;
-    griddep_wait();
-    const int segs_per_b = p.H_kv * p.rblocks;
-    const int2 sg = p.seg[blockIdx.x];
-    if (sg.y <= 1) return;
-    const int b = static_cast<int>(blockIdx.x) / segs_per_b, in_b = static_cast<int>(blockIdx.x) - b * segs_per_b;
-    const int hk = in_b / p.rblocks, rb = in_b - hk * p.rblocks;
-    const int row0 = rb * R, rows = min(R, p.G * p.Nq - row0);
-    const int r = static_cast<int>(blockIdx.y) * 8 + static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (r >= rows) return;
-    // piece 0 lies in its share's second slot (it ends the share), the others in their first
-    const auto at = [&](int s) { return (2ll * (sg.x + s) + (s == 0 ? 1 : 0)) * R + r; };
-    float m = -INFINITY;
-    for (int s = lane; s < sg.y; s += 32) m = fmaxf(m, p.part_l[at(s)]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float sum = 0.f;
-    float acc[PER];
-#pragma unroll
-    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-    for (int s0 = 0; s0 < sg.y; s0 += 32) {
-        const float w = s0 + lane < sg.y ? ex2(p.part_l[at(s0 + lane)] - ref) : 0.f;
-        sum += w;
-        const int n = min(32, sg.y - s0);
-#pragma unroll 8
-        for (int s = 0; s < n; ++s) {
-            const float ws = __shfl_sync(0xffffffffu, w, s);
-            const float* src = p.part_o + at(s0 + s) * D + lane * PER;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) acc[e] = fmaf(ws, src[e], acc[e]);
-        }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const int hh = (row0 + r) / p.Nq, qi = (row0 + r) - hh * p.Nq, h = hk * p.G + hh;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (0: the row sees nothing)
-    __nv_bfloat16* dst = p.O + b * p.o_sb + static_cast<long long>(h) * p.o_sh + qi * p.o_sn + lane * PER;
-#pragma unroll
-    for (int e = 0; e < PER; e += 2)
-        *reinterpret_cast<uint32_t*>(dst + e) = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
-    if (lane == 0)
-        p.LSE[(static_cast<long long>(b) * p.H + h) * p.Nq + qi] = (ref + lg2(sum)) * kLn2;
-}
-
-// Query rows per segment: 8 for up to 8 rows, 16 for up to 16, else 32 (more row blocks
-// read the keys again, from L2).
-int row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
+// Query rows per warp: 8 for up to 8 rows of a key head, else 16.
+int row_tiles(int rows) { return rows <= 8 ? 1 : 2; }
 
 template <int D, int NT, bool F8>
 constexpr int ctas_per_sm() { return PagedLayout<D, NT, F8>::kCtas; }
@@ -722,17 +779,15 @@ constexpr int ctas_per_sm() { return PagedLayout<D, NT, F8>::kCtas; }
 int ctas_for(int d, int nt, bool fp8) {
     if (d == 64) {
         if (nt == 1) return fp8 ? ctas_per_sm<64, 1, true>() : ctas_per_sm<64, 1, false>();
-        if (nt == 2) return fp8 ? ctas_per_sm<64, 2, true>() : ctas_per_sm<64, 2, false>();
-        return fp8 ? ctas_per_sm<64, 4, true>() : ctas_per_sm<64, 4, false>();
+        return fp8 ? ctas_per_sm<64, 2, true>() : ctas_per_sm<64, 2, false>();
     }
     if (nt == 1) return fp8 ? ctas_per_sm<128, 1, true>() : ctas_per_sm<128, 1, false>();
-    if (nt == 2) return fp8 ? ctas_per_sm<128, 2, true>() : ctas_per_sm<128, 2, false>();
-    return fp8 ? ctas_per_sm<128, 4, true>() : ctas_per_sm<128, 4, false>();
+    return fp8 ? ctas_per_sm<128, 2, true>() : ctas_per_sm<128, 2, false>();
 }
 
 // Workspace: segment headers, then the pieces' sums and outputs, each 256-aligned.
 struct PagedPlan {
-    int nt, rblocks, shares;
+    int nt, rwarps, rgroups, ctas;
     long long segs;
     size_t part_l, part_o, bytes;
 };
@@ -741,10 +796,12 @@ PagedPlan paged_plan(int B, int H, int H_kv, int Nq, int d, bool fp8) {
     PagedPlan pl;
     const int rows = H / H_kv * Nq;
     pl.nt = row_tiles(rows);
-    pl.rblocks = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
-    pl.shares = kSms * ctas_for(d, pl.nt, fp8);
-    pl.segs = static_cast<long long>(B) * H_kv * pl.rblocks;
-    const size_t part_rows = static_cast<size_t>(2) * pl.shares * 8 * pl.nt;
+    const int rblocks = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
+    pl.rwarps = rblocks == 1 ? 1 : rblocks == 2 ? 2 : 4;
+    pl.rgroups = (rblocks + pl.rwarps - 1) / pl.rwarps;
+    pl.segs = static_cast<long long>(B) * H_kv * pl.rgroups;
+    pl.ctas = kSms * ctas_for(d, pl.nt, fp8);
+    const size_t part_rows = static_cast<size_t>(2) * kPagedWarps * pl.ctas * 8 * pl.nt;
     pl.part_l = up(static_cast<size_t>(pl.segs) * sizeof(int2));
     pl.part_o = pl.part_l + up(part_rows * sizeof(float));
     pl.bytes = pl.part_o + part_rows * d * sizeof(float);
@@ -758,11 +815,19 @@ cudaError_t launch_paged_t(const PagedArgs& a, const PagedPlan& pl, PagedParams&
     cudaError_t e = set_max_dyn_smem_once<kern>(L::kBytes);
     if (e != cudaSuccess) return e;
     if (a.ev_start) cudaEventRecord(a.ev_start, stream);
-    kern<<<static_cast<unsigned>(pl.shares), kThreads, L::kBytes, stream>>>(p);
+    // (no more CTAs than a full table gives kMinTiles per warp)
+    const long long most = pl.segs * ((static_cast<long long>(p.max_pages) << p.shift) / kPagedTile) * pl.rwarps;
+    const int ctas = static_cast<int>(std::min<long long>(pl.ctas, most / (kMinTiles * kPagedWarps) + 1));
+    kern<<<static_cast<unsigned>(ctas), kThreads, L::kBytes, stream>>>(p);
     e = cudaGetLastError();
+    // pieces of an average segment: few, a block with a warp per row; many, a block per row
+    const long long pieces = static_cast<long long>(ctas) * kPagedWarps / (pl.segs * pl.rwarps) + 1;
+    const long long rows = std::min(p.G * p.Nq, 8 * NT * pl.rwarps);
+    const unsigned threads = pieces > 128 ? 1024 : pieces > kFewPieces ? 256 : static_cast<unsigned>(32 * std::min(8ll, rows));
+    const long long y = pieces > kFewPieces ? rows : (rows + 7) / 8;
     if (e == cudaSuccess)
-        e = launch_dependent(fa_paged_combine_kernel<D, NT>, dim3(static_cast<unsigned>(pl.segs), NT), dim3(256), 0,
-                             stream, p);
+        e = launch_dependent(fa_paged_combine_kernel<D, NT>, dim3(static_cast<unsigned>(pl.segs), static_cast<unsigned>(y)),
+                             dim3(threads), 0, stream, p);
     if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
     return e;
 }
@@ -773,11 +838,9 @@ size_t paged_workspace(int B, int H, int H_kv, int Nq, int d, bool fp8) {
     return paged_plan(B, H, H_kv, Nq, d, fp8).bytes;
 }
 
-long long paged_max_steps(int B, int H, int H_kv, int Nq, int max_pages, int shift) {
-    const int rows = H / H_kv * Nq, nt = row_tiles(rows);
-    const long long rblocks = (rows + 8 * nt - 1) / (8 * nt);
-    const long long steps = ((static_cast<long long>(max_pages) << shift) + 63) / 64 + 1;
-    return rblocks * H_kv * B * steps;
+long long paged_max_tiles(int B, int H, int H_kv, int Nq, int max_pages, int shift) {
+    const long long groups = (static_cast<long long>(H / H_kv) * Nq + 63) / 64;
+    return groups * H_kv * B * ((static_cast<long long>(max_pages) << shift) / kPagedTile + 1);
 }
 
 cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream) {
@@ -808,7 +871,8 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream) {
     p.H_kv = a.cache.H_kv;
     p.G = a.H / a.cache.H_kv;
     p.Nq = a.Nq;
-    p.rblocks = pl.rblocks;
+    p.rwarps = pl.rwarps;
+    p.rgroups = pl.rgroups;
     p.num_pages = a.cache.num_pages;
     p.max_pages = a.cache.max_pages;
     p.shift = a.cache.shift;
@@ -816,20 +880,16 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream) {
     p.sinks = a.window > 0 ? a.sinks : 0;
     p.scale_log2 = a.tau * kLog2e;
     p.err = a.err;
-    const int key = (a.cache.d == 128 ? 8 : 0) + (fp8 ? 4 : 0) + (pl.nt == 1 ? 0 : pl.nt == 2 ? 1 : 2);
+    const int key = (a.cache.d == 128 ? 4 : 0) + (fp8 ? 2 : 0) + (pl.nt - 1);
     switch (key) {
         case 0: return launch_paged_t<64, 1, false>(a, pl, p, stream);
         case 1: return launch_paged_t<64, 2, false>(a, pl, p, stream);
-        case 2: return launch_paged_t<64, 4, false>(a, pl, p, stream);
-        case 4: return launch_paged_t<64, 1, true>(a, pl, p, stream);
-        case 5: return launch_paged_t<64, 2, true>(a, pl, p, stream);
-        case 6: return launch_paged_t<64, 4, true>(a, pl, p, stream);
-        case 8: return launch_paged_t<128, 1, false>(a, pl, p, stream);
-        case 9: return launch_paged_t<128, 2, false>(a, pl, p, stream);
-        case 10: return launch_paged_t<128, 4, false>(a, pl, p, stream);
-        case 12: return launch_paged_t<128, 1, true>(a, pl, p, stream);
-        case 13: return launch_paged_t<128, 2, true>(a, pl, p, stream);
-        default: return launch_paged_t<128, 4, true>(a, pl, p, stream);
+        case 2: return launch_paged_t<64, 1, true>(a, pl, p, stream);
+        case 3: return launch_paged_t<64, 2, true>(a, pl, p, stream);
+        case 4: return launch_paged_t<128, 1, false>(a, pl, p, stream);
+        case 5: return launch_paged_t<128, 2, false>(a, pl, p, stream);
+        case 6: return launch_paged_t<128, 1, true>(a, pl, p, stream);
+        default: return launch_paged_t<128, 2, true>(a, pl, p, stream);
     }
 }
 

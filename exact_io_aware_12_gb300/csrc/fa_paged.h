@@ -18,7 +18,7 @@ namespace fa {
 
 constexpr int kPagedMinPage = 16, kPagedMaxPage = 256;
 constexpr long long kPagedMaxKeys = 1ll << 30;  // of one sequence: key numbers plus a tile fit an int
-// Keys per warp tile, and tiles (one per warp) per block step of the attention kernel.
+// Keys per tile of the attention kernel, and warps of a block.
 constexpr int kPagedTile = 16, kPagedWarps = 4;
 
 // The page of key `key`, or -1 where the key lies outside the table or the table
@@ -52,18 +52,23 @@ FA_HD PagedRange paged_range(int len, int nq, int window, int sinks) {
     return r;
 }
 
-// Block steps of a sequence: at least one, so that an empty sequence is written too.
-FA_HD int paged_steps(const PagedRange& r) {
-    const int t = (r.n + kPagedWarps - 1) / kPagedWarps;
-    return t > 0 ? t : 1;
-}
+// Tiles counted for a segment: its own and, behind them, kSegmentTiles that stand for the
+// time in which a warp changes segments (and make an empty sequence count too).
+constexpr int kSegmentTiles = 3;
+FA_HD int paged_tiles(const PagedRange& r) { return r.n + kSegmentTiles; }
 
-// Of `total` steps cut into `shares` even shares, share c takes [share_start(c),
-// share_start(c + 1)); share_of(x) is the share that takes step x.
-FA_HD long long share_start(long long c, long long total, long long shares) { return c * total / shares; }
-FA_HD long long share_of(long long x, long long total, long long shares) {
-    return ((x + 1) * shares + total - 1) / total - 1;
-}
+// `total` tiles cut into `shares` shares that differ by at most one tile, the longer ones
+// first: share c takes [start(c), start(c + 1)); of(x) is the share that takes tile x.
+// 32-bit throughout: a 64-bit division costs a warp a few hundred cycles.
+struct Shares {
+    uint32_t base, rem;
+    FA_HD Shares(uint32_t total, uint32_t shares) : base(total / shares), rem(total % shares) {}
+    FA_HD uint32_t start(uint32_t c) const { return c * base + (c < rem ? c : rem); }
+    FA_HD uint32_t of(uint32_t x) const {
+        const uint32_t longer = rem * (base + 1);
+        return x < longer ? x / (base + 1) : rem + (x - longer) / base;
+    }
+};
 
 // A frequency (radians per position, the bits of a double) as turns per position: the
 // fractional part in units of 2^-64, so that position * result mod 2^64 is the angle's

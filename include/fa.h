@@ -333,8 +333,8 @@ FA_API fa_status fa_kv_append_fp8(const fa_paged_cache* cache, const void* k, lo
  * workspace: fa_paged_workspace_size bytes (it does not depend on the lengths); NULL:
  * taken with cudaMallocAsync and given back.  Two calls that may run at the same time
  * need two workspaces.  A length out of bounds is cut to the table's, and keys on a
- * page out of bounds are hidden (FA_ERR_PAGE).  More than 2^31 64-key steps in a full
- * table are FA_ERR_UNSUPPORTED.
+ * page out of bounds are hidden (FA_ERR_PAGE).  More than 2^31 16-key tiles in full
+ * tables (of all sequences, key heads and 64 query rows) are FA_ERR_UNSUPPORTED.
  */
 FA_API size_t fa_paged_workspace_size(int B, int H, int H_kv, int Nq, int d, int fp8);
 FA_API fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* Q, long long q_sb,

@@ -23,11 +23,11 @@ extern "C" {
 int t_page_of(const int* t, int mp, int np, int sh, long long k) { return page_of(t, mp, np, sh, k); }
 void t_range(int len, int nq, int w, int s, int* o) {
     const PagedRange r = paged_range(len, nq, w, s);
-    o[0] = r.lo; o[1] = r.ns; o[2] = r.n; o[3] = paged_steps(r);
+    o[0] = r.lo; o[1] = r.ns; o[2] = r.n; o[3] = paged_tiles(r);
 }
 int t_key0(int len, int nq, int w, int s, int i) { return paged_range(len, nq, w, s).key0(i); }
-long long t_start(long long c, long long t, long long s) { return share_start(c, t, s); }
-long long t_share(long long x, long long t, long long s) { return share_of(x, t, s); }
+long long t_start(long long c, long long t, long long s) { return Shares(t, s).start(c); }
+long long t_share(long long x, long long t, long long s) { return Shares(t, s).of(x); }
 uint64_t t_turn(uint64_t b) { return turn_fraction(b); }
 int t_exp(uint32_t b) { return page_scale_exp(b); }
 int t_reached(long long p, int n, int sh) { return pages_reached(p, n, sh); }
@@ -72,10 +72,10 @@ def test_tile_lists_hold_every_visible_key_once(shim, nq, window, sinks):
     o = (ctypes.c_int * 4)()
     for length in list(range(0, 200)) + [511, 512, 513, 1000]:
         shim.t_range(length, nq, window, sinks, o)
-        lo, ns, n, steps = o
+        lo, ns, n, tiles = o
         starts = [shim.t_key0(length, nq, window, sinks, i) for i in range(n)]
         assert len(set(starts)) == n and all(k % 16 == 0 and 0 <= k < max(length, 1) for k in starts)
-        assert steps == max(1, -(-n // 4))
+        assert tiles > n
         see = _plain.visible(min(nq, length), length, window, sinks).any(0) if length else torch.zeros(0)
         held = {k + i for k in starts for i in range(16)}
         assert all(int(j) in held for j in see.nonzero().flatten())
@@ -272,7 +272,7 @@ def test_paged_refuses(kw, code, fp8):
     assert paged(cache(fp8), fp8, **kw) == code
 
 
-def test_too_many_steps_are_refused():
+def test_too_many_tiles_are_refused():
     assert paged(cache(B=4096, H_kv=2, max_pages=2 ** 22)) == _lib.FA_ERR_UNSUPPORTED
 
 
