@@ -60,6 +60,7 @@ constexpr int kThreads = 32 * kPagedWarps;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kGrow = 8.0f;  // log2 units: weights stay <= 2^8
+enum : uint32_t { kSitePagedSmem = 51 };
 
 // Ring slots per warp and CTAs per SM: about 128 KB in flight per SM, as much as the
 // copy bandwidth times the memory's latency asks for (45 GB/s x ~1.5 us per SM).
@@ -71,7 +72,7 @@ struct PagedLayout {
     static constexpr int kCtas = kSlot == 8192 ? 2 : NT == 2 ? 3 : 4;
     static constexpr int kStages = kSlot == 8192 ? 3 : kSlot == 4096 ? (NT == 1 ? 3 : 4) : 6;
     static constexpr int kWarpRing = kStages * kSlot;
-    static constexpr int kBytes = kPagedWarps * kWarpRing;
+    static constexpr int kBytes = kPagedWarps * kWarpRing + 1024;  // + PagedShared
 };
 constexpr int kMinTiles = 2;  // per warp: below, its start and end cost more than they save
 constexpr int kMaxResults = 512;  // pieces of a segment: more cost the combine kernel more than they save
@@ -99,6 +100,9 @@ struct PagedParams {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -142,19 +146,41 @@ __device__ __forceinline__ float lg2(float x) {  // log2, -inf at 0
     return y;
 }
 
-// Byte offset of 16-byte chunk c of row r in a tile.  K: eight threads read four chunks
-// of two neighbouring rows; V: two chunks of every other row of eight.  Either set
-// covers all 32 banks.
+// A tile in shared memory: row r's 16-byte chunks in an XOR order, so that the fragment
+// loads touch all 32 banks once.  K: eight threads read four chunks of two neighbouring
+// rows; V: two chunks of every other row of eight.  Rows of 64 bytes lie two to a line.
+//   rows >= 128 bytes:  K  r ROW + ((c ^ 4 (r & 1)) << 4)
+//                       V  r ROW + ((c ^ 2 ((r >> 1) & 3)) << 4)
+//   rows of 64 bytes:   K  64 r + (c << 4)
+//                       V  128 (r >> 1) + 64 ((r ^ (r >> 2)) & 1) + ((c ^ 2 ((r >> 1) & 1)) << 4)
+// A copy instruction j of 32 lanes fills 512 bytes, chunk idx = 32 j + lane (row idx / CH,
+// chunk idx % CH).  Only the XOR terms that change with j are left for the loop; the
+// lane's part is computed once.
 template <int ROW>
-__device__ __forceinline__ int k_off(int r, int c) {
-    if constexpr (ROW >= 128) return r * ROW + ((c ^ ((r & 1) << 2)) << 4);
-    else return r * ROW + (c << 4);
-}
-template <int ROW>
-__device__ __forceinline__ int v_off(int r, int c) {
-    if constexpr (ROW >= 128) return r * ROW + ((c ^ (((r >> 1) & 3) << 1)) << 4);
-    else return ((r >> 1) << 7) + (((r ^ (r >> 2)) & 1) << 6) + ((c ^ (((r >> 1) & 1) << 1)) << 4);
-}
+struct Swizzle {
+    static constexpr int CH = ROW / 16;
+    // destination of copy j: 512 j + k_dst(lane), 512 j + (v_dst(lane) ^ v_dst_x(j))
+    static __device__ __forceinline__ uint32_t k_dst(int lane) {
+        const int r = lane / CH, c = lane % CH;
+        return ROW >= 128 ? r * ROW + ((c ^ ((r & 1) << 2)) << 4) : lane * 16;
+    }
+    static __device__ __forceinline__ uint32_t v_dst(int lane) {
+        const int r = lane / CH, c = lane % CH;
+        return ROW >= 128 ? r * ROW + ((c ^ (((r >> 1) & 3) << 1)) << 4)
+                          : ((r >> 1) << 7) + (((r ^ (r >> 2)) & 1) << 6) + ((c ^ (((r >> 1) & 1) << 1)) << 4);
+    }
+    static constexpr uint32_t v_dst_x(int j) { return ROW == 256 ? (j & 3) << 5 : ROW == 128 ? (j & 1) << 6 : 0; }
+    // K fragment: chunk t4 + 4 c of row g at k_src ^ (c << 6), row g + 8 8 ROW further
+    static __device__ __forceinline__ uint32_t k_src(int g, int t4) {
+        return g * ROW + (t4 << 4) + (ROW >= 128 ? (g & 1) << 6 : 0);
+    }
+    // V fragment of rows 2 t4, 2 t4 + 1 (at v_row1) and these + 8 (8 ROW further)
+    static __device__ __forceinline__ uint32_t v_src(int g, int t4) {
+        return ROW >= 128 ? 2 * t4 * ROW + ((g ^ (t4 << 1)) << 4)
+                          : (t4 << 7) + ((t4 >> 1) << 6) + (((g >> 1) ^ ((t4 & 1) << 1)) << 4) + ((g & 1) << 3);
+    }
+    static __device__ __forceinline__ uint32_t v_row1(uint32_t a) { return ROW >= 128 ? a + ROW : a ^ 64; }
+};
 
 // max over the lanes that share lane % 4
 __device__ __forceinline__ float max_over_g(float x) {
@@ -179,24 +205,35 @@ __device__ __forceinline__ int clamp_len(const PagedParams& p, int b) {
 }
 
 struct PagedShared {
-    int key0[kPagedWarps][8];     // per ring slot: first key of the tile (a bad page: past every row)
-    float ks[kPagedWarps][8], vs[kPagedWarps][8];  // 8-bit: the page's scales
+    // per ring slot: first key of the tile (a bad page: past every row); 8-bit: the page's scales
+    struct __align__(16) Slot {
+        int key0;
+        float ks, vs, pad;
+    } slot[kPagedWarps][8];
     int scan[kPagedWarps];
     int at_b[kPagedWarps], at_before[kPagedWarps];  // a share's first sequence, tiles of those before it
 };
+
+static_assert(sizeof(PagedShared) <= 1024, "the shared block fits its place");
 
 template <int D, int NT, bool F8>
 __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_paged_kernel(const PagedParams p) {
     using L = PagedLayout<D, NT, F8>;
     constexpr int ROW = L::kRow, CH = ROW / 16, S = L::kStages;
+    using W = Swizzle<ROW>;
     constexpr int R = 8 * NT;           // query rows of a segment
     constexpr int MT = D / 16;          // 16-column tiles of V^T
     constexpr int KS = D / 16;          // 16-element steps of q.k
     constexpr int kChunksK = D / (F8 ? 64 : 32);  // 16-byte pieces of a key row per thread
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ PagedShared sh;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    PagedShared& sh = *reinterpret_cast<PagedShared*>(smem + kPagedWarps * L::kWarpRing);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const uint32_t ring = smem_addr(smem) + warp * L::kWarpRing;
+    if ((smem_addr(smem) & 255u) != 0u) {  // (the XOR orders count on tiles at multiples of 256 bytes)
+        if (tid == 0) atomicCAS(p.err, 0u, 1u | (kSitePagedSmem << 8));
+        return;
+    }
+    const uint32_t k_dst = W::k_dst(lane), v_dst = W::v_dst(lane), k_src = W::k_src(g, t4), v_src = W::v_src(g, t4);
     griddep_launch_dependents();
 
     // ---- this warp's share of the tiles ----
@@ -302,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
         };
         // first key that any row sees behind the sinks
         const int low = p.window > 0 ? max(0, len - p.Nq - p.window + 1) : 0;
+        int in_slot = 0;  // ring slot of the next tile to load
         const auto issue = [&](int i) {
             if (i >= nv) return;
             if ((i & 31) == 0 && i > 0) {
@@ -310,36 +348,39 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
                 vs = vs_next;
             }
             if ((i & 31) == 16) fetch((i & ~31) + 32, pg_next, ks_next, vs_next);
-            const int slot = i % S;
             const int key0 = rg.key0(u0 + i);
             const int page = __shfl_sync(0xffffffffu, pg, i & 31);
-            const long long off =
-                page < 0 ? 0
-                         : (((static_cast<long long>(page) * p.H_kv + hk) << p.shift) + (key0 & ((1 << p.shift) - 1))) * ROW;
-            const uint32_t dst = ring + slot * L::kSlot;
-            const bool whole = page >= 0 && key0 + kPagedTile <= len &&
-                               (key0 >= low || key0 + kPagedTile <= p.sinks);
-            const uint8_t* ksrc = p.K + off + lane * 16;
-            const uint8_t* vsrc = p.V + off + lane * 16;
-#pragma unroll
-            for (int j = 0; j < CH / 2; ++j) {
-                const int idx = j * 32 + lane, r = idx / CH, c = idx % CH;
-                int bytes = 16;
-                if (!whole) {
-                    const int key = key0 + r;
-                    bytes = page >= 0 && key < len && (key >= low || key < p.sinks) ? 16 : 0;
-                }
-                cp_async16(dst + k_off<ROW>(r, c), ksrc + j * 512, bytes);
-                cp_async16(dst + L::kTile + v_off<ROW>(r, c), vsrc + j * 512, bytes);
-            }
+            const uint32_t dst = ring + in_slot * L::kSlot;
+            typename PagedShared::Slot sl;
+            sl.key0 = page < 0 ? 0x7fffff00 : key0;
             if constexpr (F8) {
-                const float k1 = __shfl_sync(0xffffffffu, ks, i & 31), v1 = __shfl_sync(0xffffffffu, vs, i & 31);
-                if (lane == 0) {
-                    sh.ks[warp][slot] = k1;
-                    sh.vs[warp][slot] = v1;
+                sl.ks = __shfl_sync(0xffffffffu, ks, i & 31);
+                sl.vs = __shfl_sync(0xffffffffu, vs, i & 31);
+            }
+            if (lane == 0) sh.slot[warp][in_slot] = sl;
+            in_slot = in_slot + 1 == S ? 0 : in_slot + 1;
+            // (a page is at least one tile: a tile's rows lie together)
+            const long long off =
+                (((static_cast<long long>(max(page, 0)) * p.H_kv + hk) << p.shift) + (key0 & ((1 << p.shift) - 1))) * ROW +
+                lane * 16;
+            const uint8_t* ksrc = p.K + off;
+            const uint8_t* vsrc = p.V + off;
+            if (page >= 0 && key0 + kPagedTile <= len && (key0 >= low || key0 + kPagedTile <= p.sinks)) {
+#pragma unroll
+                for (int j = 0; j < CH / 2; ++j) {
+                    cp_async16(dst + j * 512 + k_dst, ksrc + j * 512);
+                    cp_async16(dst + L::kTile + j * 512 + (v_dst ^ W::v_dst_x(j)), vsrc + j * 512);
+                }
+            } else {
+                // rows that no row of the call sees become zeros
+#pragma unroll
+                for (int j = 0; j < CH / 2; ++j) {
+                    const int key = key0 + (j * 32 + lane) / CH;
+                    const int bytes = page >= 0 && key < len && (key >= low || key < p.sinks) ? 16 : 0;
+                    cp_async16(dst + j * 512 + k_dst, ksrc + j * 512, bytes);
+                    cp_async16(dst + L::kTile + j * 512 + (v_dst ^ W::v_dst_x(j)), vsrc + j * 512, bytes);
                 }
             }
-            if (lane == 0) sh.key0[warp][slot] = page < 0 ? 0x7fffff00 : key0;
         };
         fetch(0, pg, ks, vs);
 #pragma unroll
@@ -428,14 +469,16 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
         }
         float vs_fac = -1.f;  // the V scale that fac was formed for
 
+        int slot_at = 0;
         for (int i = 0; i < nv; ++i) {
             cp_wait<S - 2>();
             __syncwarp();
             issue(i + S - 1);
             cp_commit();
-            const int slot = i % S;
-            const uint32_t kt = ring + slot * L::kSlot, vt = kt + L::kTile;
-            const int key0 = sh.key0[warp][slot];
+            const uint32_t kt = ring + slot_at * L::kSlot, vt = kt + L::kTile;
+            const typename PagedShared::Slot sl = sh.slot[warp][slot_at];
+            const int key0 = sl.key0;
+            slot_at = slot_at + 1 == S ? 0 : slot_at + 1;
 
             // S^T = K Q^T
             float s[NT][4];
@@ -445,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
                 for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
 #pragma unroll
             for (int c = 0; c < kChunksK; ++c) {
-                const uint4 ka = lds128(kt + k_off<ROW>(g, t4 + 4 * c)), kb = lds128(kt + k_off<ROW>(g + 8, t4 + 4 * c));
+                const uint32_t at = (kt + k_src) ^ (c << 6);
+                const uint4 ka = lds128(at), kb = lds128(at + 8 * ROW);
                 const uint32_t a[4] = {ka.x, ka.y, ka.z, ka.w}, bb[4] = {kb.x, kb.y, kb.z, kb.w};
                 if constexpr (!F8) {
 #pragma unroll
@@ -467,43 +511,60 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
                 }
             }
 
-            // scale, mask, running max
-            const float ksc = F8 ? sh.ks[warp][slot] : 1.f;
-            const float vsc = F8 ? sh.vs[warp][slot] : 1.f;
+            // scale, mask; s becomes the score less the running max (log2 units)
+            const float ksc = F8 ? sl.ks : 1.f;
+            const float vsc = F8 ? sl.vs : 1.f;
+            const float lvs = F8 ? lg2(vsc) : 0.f;
             const bool whole = key0 + kPagedTile <= len - p.Nq + 1 &&
                                (p.window == 0 || key0 >= len - p.window || key0 + kPagedTile <= p.sinks);
             bool grow = false;
-            const float lvs = F8 ? lg2(vsc) : 0.f;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                float scale[2], ref[2], most[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[nt][e] *= F8 ? rs[nt][e & 1] * ksc : rs[nt][e & 1];
-                    if (!whole) {
+                for (int e = 0; e < 2; ++e) {
+                    const float m = m_run[nt][e];  // -inf until the row has seen a key
+                    scale[e] = F8 ? rs[nt][e] * ksc : rs[nt][e];
+                    ref[e] = m == -INFINITY ? 0.f : m;
+                    // the largest that the running maxima allow (8-bit: that of P vs, too)
+                    most[e] = F8 ? kGrow + fminf(0.f, mv_run[nt][e] - lvs - m) : kGrow;
+                    if (m == -INFINITY) most[e] = -INFINITY;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[nt][e] = fmaf(s[nt][e], scale[e & 1], -ref[e & 1]);
+                if (!whole) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
                         const int key = key0 + g + (e & 2 ? 8 : 0), la = last[nt][e & 1];
                         const bool see = key <= la && (p.window == 0 || key > la - p.window || key < p.sinks);
                         if (!see) s[nt][e] = -INFINITY;
                     }
-                    grow |= s[nt][e] > m_run[nt][e & 1] + kGrow;
-                    if (F8) grow |= s[nt][e] + lvs > mv_run[nt][e & 1] + kGrow;
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) grow |= s[nt][e] > most[e & 1];
+            }
             bool refac = F8 && vsc != vs_fac;
             if (__any_sync(0xffffffffu, grow)) {
+                // (rare: on a piece's first tile, and where scores rise by more than 2^8)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float mx = max_over_g(fmaxf(s[nt][e], s[nt][e + 2]));
-                        const float m_new = fmaxf(m_run[nt][e], mx);
-                        const float alpha = m_new == -INFINITY ? 1.f : ex2(m_run[nt][e] - m_new);
+                        const float m = m_run[nt][e], ref = m == -INFINITY ? 0.f : m;
+                        const float mx = ref + max_over_g(fmaxf(s[nt][e], s[nt][e + 2]));
+                        const float m_new = fmaxf(m, mx);
+                        const float alpha = m == -INFINITY ? 1.f : ex2(m - m_new);
+                        const float down = m_new == -INFINITY ? 0.f : m_new - ref;
+                        m_run[nt][e] = m_new;
                         l_run[nt][e] *= alpha;
+                        s[nt][e] -= down;
+                        s[nt][e + 2] -= down;
                         float beta = alpha;
                         if constexpr (F8) {
                             const float mv_new = fmaxf(mv_run[nt][e], mx + lvs);
                             beta = mv_new == -INFINITY ? 1.f : ex2(mv_run[nt][e] - mv_new);
                             mv_run[nt][e] = mv_new;
                         }
-                        m_run[nt][e] = m_new;
 #pragma unroll
                         for (int j = 0; j < MT; ++j) {
                             acc[nt][j][e] *= beta;
@@ -527,10 +588,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
             for (int nt = 0; nt < NT; ++nt) {
                 float w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float mm = m_run[nt][e & 1];
-                    w[e] = ex2(s[nt][e] - (mm == -INFINITY ? 0.f : mm));
-                }
+                for (int e = 0; e < 4; ++e) w[e] = ex2(s[nt][e]);
                 l_run[nt][0] += w[0] + w[2];
                 l_run[nt][1] += w[1] + w[3];
                 if constexpr (F8) {
@@ -547,9 +605,8 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
             if constexpr (!F8) {
 #pragma unroll
                 for (int c = 0; c < CH / 8; ++c) {
-                    const int ch = g + 8 * c;
-                    const uint4 x0 = lds128(vt + v_off<ROW>(2 * t4, ch)), x1 = lds128(vt + v_off<ROW>(2 * t4 + 1, ch));
-                    const uint4 y0 = lds128(vt + v_off<ROW>(2 * t4 + 8, ch)), y1 = lds128(vt + v_off<ROW>(2 * t4 + 9, ch));
+                    const uint32_t at = vt + v_src + c * 128, at1 = W::v_row1(at);
+                    const uint4 x0 = lds128(at), x1 = lds128(at1), y0 = lds128(at + 8 * ROW), y1 = lds128(at1 + 8 * ROW);
                     const uint32_t a[4] = {x0.x, x0.y, x0.z, x0.w}, a1[4] = {x1.x, x1.y, x1.z, x1.w};
                     const uint32_t bb[4] = {y0.x, y0.y, y0.z, y0.w}, b1[4] = {y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
@@ -562,25 +619,26 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
                     }
                 }
             } else {
-                constexpr int W = D / 32;  // words of a row per thread (16 columns at d = 128, 8 at 64)
+                constexpr int kWords = D / 32;  // of a row per thread (16 columns at d = 128, 8 at 64)
+                const uint32_t at = vt + v_src, at1 = W::v_row1(at);
                 uint32_t a[4][4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int r = 2 * t4 + (k & 1) + (k >> 1) * 8;
+                    const uint32_t from = (k & 1 ? at1 : at) + (k >> 1) * 8 * ROW;
                     if constexpr (D == 128) {
-                        const uint4 w = lds128(vt + v_off<ROW>(r, g));
+                        const uint4 w = lds128(from);
                         a[k][0] = w.x;
                         a[k][1] = w.y;
                         a[k][2] = w.z;
                         a[k][3] = w.w;
                     } else {
-                        const uint2 w = lds64(vt + v_off<ROW>(r, g >> 1) + (g & 1) * 8);
+                        const uint2 w = lds64(from);
                         a[k][0] = w.x;
                         a[k][1] = w.y;
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < W; ++j) {
+                for (int j = 0; j < kWords; ++j) {
                     uint32_t f[8];  // [lo: elements 4 j .. 4 j + 3, hi: the same]
                     widen_e4m3x4(__byte_perm(a[0][j], a[1][j], 0x5140), f[0], f[1]);
                     widen_e4m3x4(__byte_perm(a[0][j], a[1][j], 0x7362), f[2], f[3]);
