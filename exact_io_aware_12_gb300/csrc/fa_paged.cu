@@ -68,9 +68,10 @@ template <int D, int NT, bool F8>
 struct PagedLayout {
     static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a key row
     static constexpr int kTile = kPagedTile * kRow;     // K or V of one tile
-    static constexpr int kSlot = 2 * kTile;
-    static constexpr int kCtas = kSlot == 8192 ? 2 : NT == 2 ? 3 : 4;
-    static constexpr int kStages = kSlot == 8192 ? 3 : kSlot == 4096 ? (NT == 1 ? 3 : 4) : 6;
+    static constexpr int TP = kTile == 4096 ? 1 : 2;    // tiles per slot and loop iteration
+    static constexpr int kSlot = 2 * TP * kTile;
+    static constexpr int kCtas = kSlot == 8192 ? 2 : 3;
+    static constexpr int kStages = kSlot == 8192 ? 3 : 4;
     static constexpr int kWarpRing = kStages * kSlot;
     static constexpr int kBytes = kPagedWarps * kWarpRing + 1024;  // + PagedShared
 };
@@ -209,7 +210,7 @@ struct PagedShared {
     struct __align__(16) Slot {
         int key0;
         float ks, vs, pad;
-    } slot[kPagedWarps][8];
+    } slot[kPagedWarps][4][2];  // [warp][ring slot][tile]
     int scan[kPagedWarps];
     int at_b[kPagedWarps], at_before[kPagedWarps];  // a share's first sequence, tiles of those before it
 };
@@ -219,7 +220,7 @@ static_assert(sizeof(PagedShared) <= 1024, "the shared block fits its place");
 template <int D, int NT, bool F8>
 __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_paged_kernel(const PagedParams p) {
     using L = PagedLayout<D, NT, F8>;
-    constexpr int ROW = L::kRow, CH = ROW / 16, S = L::kStages;
+    constexpr int ROW = L::kRow, CH = ROW / 16, S = L::kStages, TP = L::TP;
     using W = Swizzle<ROW>;
     constexpr int R = 8 * NT;           // query rows of a segment
     constexpr int MT = D / 16;          // 16-column tiles of V^T
@@ -339,48 +340,53 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
         };
         // first key that any row sees behind the sinks
         const int low = p.window > 0 ? max(0, len - p.Nq - p.window + 1) : 0;
-        int in_slot = 0;  // ring slot of the next tile to load
-        const auto issue = [&](int i) {
-            if (i >= nv) return;
-            if ((i & 31) == 0 && i > 0) {
-                pg = pg_next;
-                ks = ks_next;
-                vs = vs_next;
+        const int nu = (nv + TP - 1) / TP;  // slots' worth
+        int in_slot = 0;                    // ring slot to fill next
+        const auto issue = [&](int u) {
+            if (u >= nu) return;
+#pragma unroll
+            for (int tp = 0; tp < TP; ++tp) {
+                const int i = u * TP + tp;
+                if ((i & 31) == 0 && i > 0) {
+                    pg = pg_next;
+                    ks = ks_next;
+                    vs = vs_next;
+                }
+                if ((i & 31) == 16) fetch((i & ~31) + 32, pg_next, ks_next, vs_next);
+                const int key0 = rg.key0(u0 + i);
+                const int page = __shfl_sync(0xffffffffu, pg, i & 31);  // (-1 behind the piece's last tile, too)
+                const uint32_t dst = ring + in_slot * L::kSlot + tp * 2 * L::kTile;
+                typename PagedShared::Slot sl;
+                sl.key0 = page < 0 ? 0x7fffff00 : key0;
+                if constexpr (F8) {
+                    sl.ks = __shfl_sync(0xffffffffu, ks, i & 31);
+                    sl.vs = __shfl_sync(0xffffffffu, vs, i & 31);
+                }
+                if (lane == 0) sh.slot[warp][in_slot][tp] = sl;
+                // (a page is at least one tile: a tile's rows lie together)
+                const long long off =
+                    (((static_cast<long long>(max(page, 0)) * p.H_kv + hk) << p.shift) + (key0 & ((1 << p.shift) - 1))) * ROW +
+                    lane * 16;
+                const uint8_t* ksrc = p.K + off;
+                const uint8_t* vsrc = p.V + off;
+                if (page >= 0 && key0 + kPagedTile <= len && (key0 >= low || key0 + kPagedTile <= p.sinks)) {
+#pragma unroll
+                    for (int j = 0; j < CH / 2; ++j) {
+                        cp_async16(dst + j * 512 + k_dst, ksrc + j * 512);
+                        cp_async16(dst + L::kTile + j * 512 + (v_dst ^ W::v_dst_x(j)), vsrc + j * 512);
+                    }
+                } else {
+                    // rows that no row of the call sees become zeros
+#pragma unroll
+                    for (int j = 0; j < CH / 2; ++j) {
+                        const int key = key0 + (j * 32 + lane) / CH;
+                        const int bytes = page >= 0 && key < len && (key >= low || key < p.sinks) ? 16 : 0;
+                        cp_async16(dst + j * 512 + k_dst, ksrc + j * 512, bytes);
+                        cp_async16(dst + L::kTile + j * 512 + (v_dst ^ W::v_dst_x(j)), vsrc + j * 512, bytes);
+                    }
+                }
             }
-            if ((i & 31) == 16) fetch((i & ~31) + 32, pg_next, ks_next, vs_next);
-            const int key0 = rg.key0(u0 + i);
-            const int page = __shfl_sync(0xffffffffu, pg, i & 31);
-            const uint32_t dst = ring + in_slot * L::kSlot;
-            typename PagedShared::Slot sl;
-            sl.key0 = page < 0 ? 0x7fffff00 : key0;
-            if constexpr (F8) {
-                sl.ks = __shfl_sync(0xffffffffu, ks, i & 31);
-                sl.vs = __shfl_sync(0xffffffffu, vs, i & 31);
-            }
-            if (lane == 0) sh.slot[warp][in_slot] = sl;
             in_slot = in_slot + 1 == S ? 0 : in_slot + 1;
-            // (a page is at least one tile: a tile's rows lie together)
-            const long long off =
-                (((static_cast<long long>(max(page, 0)) * p.H_kv + hk) << p.shift) + (key0 & ((1 << p.shift) - 1))) * ROW +
-                lane * 16;
-            const uint8_t* ksrc = p.K + off;
-            const uint8_t* vsrc = p.V + off;
-            if (page >= 0 && key0 + kPagedTile <= len && (key0 >= low || key0 + kPagedTile <= p.sinks)) {
-#pragma unroll
-                for (int j = 0; j < CH / 2; ++j) {
-                    cp_async16(dst + j * 512 + k_dst, ksrc + j * 512);
-                    cp_async16(dst + L::kTile + j * 512 + (v_dst ^ W::v_dst_x(j)), vsrc + j * 512);
-                }
-            } else {
-                // rows that no row of the call sees become zeros
-#pragma unroll
-                for (int j = 0; j < CH / 2; ++j) {
-                    const int key = key0 + (j * 32 + lane) / CH;
-                    const int bytes = page >= 0 && key < len && (key >= low || key < p.sinks) ? 16 : 0;
-                    cp_async16(dst + j * 512 + k_dst, ksrc + j * 512, bytes);
-                    cp_async16(dst + L::kTile + j * 512 + (v_dst ^ W::v_dst_x(j)), vsrc + j * 512, bytes);
-                }
-            }
         };
         fetch(0, pg, ks, vs);
 #pragma unroll
@@ -453,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
             }
 
         float acc[NT][MT][4];
-        float m_run[NT][2], l_run[NT][2], mv_run[NT][2], fac[NT][2];
+        float m_run[NT][2], l_run[NT][2], mv_run[NT][2], fac[NT][2];  // fac: 2^(m - mv)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -467,103 +473,122 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
                 fac[nt][e] = 0.f;
             }
         }
-        float vs_fac = -1.f;  // the V scale that fac was formed for
-
         int slot_at = 0;
-        for (int i = 0; i < nv; ++i) {
+        for (int u = 0; u < nu; ++u) {
             cp_wait<S - 2>();
             __syncwarp();
-            issue(i + S - 1);
+            issue(u + S - 1);
             cp_commit();
-            const uint32_t kt = ring + slot_at * L::kSlot, vt = kt + L::kTile;
-            const typename PagedShared::Slot sl = sh.slot[warp][slot_at];
-            const int key0 = sl.key0;
+            const uint32_t ks_at = ring + slot_at * L::kSlot + k_src, vs_at = ring + slot_at * L::kSlot + L::kTile + v_src;
+            typename PagedShared::Slot sl[TP];
+#pragma unroll
+            for (int tp = 0; tp < TP; ++tp) sl[tp] = sh.slot[warp][slot_at][tp];
             slot_at = slot_at + 1 == S ? 0 : slot_at + 1;
 
             // S^T = K Q^T
-            float s[NT][4];
+            float s[TP][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int tp = 0; tp < TP; ++tp)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[tp][nt][e] = 0.f;
 #pragma unroll
             for (int c = 0; c < kChunksK; ++c) {
-                const uint32_t at = (kt + k_src) ^ (c << 6);
-                const uint4 ka = lds128(at), kb = lds128(at + 8 * ROW);
-                const uint32_t a[4] = {ka.x, ka.y, ka.z, ka.w}, bb[4] = {kb.x, kb.y, kb.z, kb.w};
-                if constexpr (!F8) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                for (int tp = 0; tp < TP; ++tp) {
+                    const uint32_t at = (ks_at + tp * 2 * L::kTile) ^ (c << 6);
+                    const uint4 ka = lds128(at), kb = lds128(at + 8 * ROW);
+                    const uint32_t a[4] = {ka.x, ka.y, ka.z, ka.w}, bb[4] = {kb.x, kb.y, kb.z, kb.w};
+                    if constexpr (!F8) {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816<false>(s[nt], a[2 * h], bb[2 * h], a[2 * h + 1], bb[2 * h + 1], q[nt][2 * c + h][0],
-                                            q[nt][2 * c + h][1]);
-                } else {
+                        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t a0, a2, a1, a3;
-                        widen_e4m3x4(a[h], a0, a2);
-                        widen_e4m3x4(bb[h], a1, a3);
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<false>(s[tp][nt], a[2 * h], bb[2 * h], a[2 * h + 1], bb[2 * h + 1],
+                                                q[nt][2 * c + h][0], q[nt][2 * c + h][1]);
+                    } else {
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816<true>(s[nt], a0, a1, a2, a3, q[nt][4 * c + h][0], q[nt][4 * c + h][1]);
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t a0, a2, a1, a3;
+                            widen_e4m3x4(a[h], a0, a2);
+                            widen_e4m3x4(bb[h], a1, a3);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<true>(s[tp][nt], a0, a1, a2, a3, q[nt][4 * c + h][0], q[nt][4 * c + h][1]);
+                        }
                     }
                 }
             }
 
             // scale, mask; s becomes the score less the running max (log2 units)
-            const float ksc = F8 ? sl.ks : 1.f;
-            const float vsc = F8 ? sl.vs : 1.f;
-            const float lvs = F8 ? lg2(vsc) : 0.f;
-            const bool whole = key0 + kPagedTile <= len - p.Nq + 1 &&
-                               (p.window == 0 || key0 >= len - p.window || key0 + kPagedTile <= p.sinks);
             bool grow = false;
+            float vsc[TP], lvs[TP];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float scale[2], ref[2], most[2];
+            for (int tp = 0; tp < TP; ++tp) {
+                const int key0 = sl[tp].key0;
+                const float ksc = F8 ? sl[tp].ks : 1.f;
+                vsc[tp] = F8 ? sl[tp].vs : 1.f;
+                lvs[tp] = F8 ? lg2(vsc[tp]) : 0.f;
+                const bool whole = key0 + kPagedTile <= len - p.Nq + 1 &&
+                                   (p.window == 0 || key0 >= len - p.window || key0 + kPagedTile <= p.sinks);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float m = m_run[nt][e];  // -inf until the row has seen a key
-                    scale[e] = F8 ? rs[nt][e] * ksc : rs[nt][e];
-                    ref[e] = m == -INFINITY ? 0.f : m;
-                    // the largest that the running maxima allow (8-bit: that of P vs, too)
-                    most[e] = F8 ? kGrow + fminf(0.f, mv_run[nt][e] - lvs - m) : kGrow;
-                    if (m == -INFINITY) most[e] = -INFINITY;
-                }
+                for (int nt = 0; nt < NT; ++nt) {
+                    float(&x)[4] = s[tp][nt];
+                    float scale[2], ref[2], most[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[nt][e] = fmaf(s[nt][e], scale[e & 1], -ref[e & 1]);
-                if (!whole) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + g + (e & 2 ? 8 : 0), la = last[nt][e & 1];
-                        const bool see = key <= la && (p.window == 0 || key > la - p.window || key < p.sinks);
-                        if (!see) s[nt][e] = -INFINITY;
+                    for (int e = 0; e < 2; ++e) {
+                        const float m = m_run[nt][e];  // -inf until the row has seen a key
+                        scale[e] = F8 ? rs[nt][e] * ksc : rs[nt][e];
+                        ref[e] = m == -INFINITY ? 0.f : m;
+                        // the largest that the running maxima allow (8-bit: that of P vs, too)
+                        most[e] = F8 ? kGrow + fminf(0.f, mv_run[nt][e] - lvs[tp] - m) : kGrow;
+                        if (m == -INFINITY) most[e] = -INFINITY;
                     }
-                }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) grow |= s[nt][e] > most[e & 1];
+                    for (int e = 0; e < 4; ++e) x[e] = fmaf(x[e], scale[e & 1], -ref[e & 1]);
+                    if (!whole) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = key0 + g + (e & 2 ? 8 : 0), la = last[nt][e & 1];
+                            const bool see = key <= la && (p.window == 0 || key > la - p.window || key < p.sinks);
+                            if (!see) x[e] = -INFINITY;
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) grow |= x[e] > most[e & 1];
+                }
             }
-            bool refac = F8 && vsc != vs_fac;
             if (__any_sync(0xffffffffu, grow)) {
-                // (rare: on a piece's first tile, and where scores rise by more than 2^8)
+                // (rare: on a piece's first tiles, and where scores rise by more than 2^8)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float m = m_run[nt][e], ref = m == -INFINITY ? 0.f : m;
-                        const float mx = ref + max_over_g(fmaxf(s[nt][e], s[nt][e + 2]));
-                        const float m_new = fmaxf(m, mx);
+                        float mx[TP], m_new = m;
+#pragma unroll
+                        for (int tp = 0; tp < TP; ++tp) {
+                            mx[tp] = ref + max_over_g(fmaxf(s[tp][nt][e], s[tp][nt][e + 2]));
+                            m_new = fmaxf(m_new, mx[tp]);
+                        }
                         const float alpha = m == -INFINITY ? 1.f : ex2(m - m_new);
                         const float down = m_new == -INFINITY ? 0.f : m_new - ref;
                         m_run[nt][e] = m_new;
                         l_run[nt][e] *= alpha;
-                        s[nt][e] -= down;
-                        s[nt][e + 2] -= down;
                         float beta = alpha;
                         if constexpr (F8) {
-                            const float mv_new = fmaxf(mv_run[nt][e], mx + lvs);
+                            float mv_new = mv_run[nt][e];
+#pragma unroll
+                            for (int tp = 0; tp < TP; ++tp) mv_new = fmaxf(mv_new, mx[tp] + lvs[tp]);
                             beta = mv_new == -INFINITY ? 1.f : ex2(mv_run[nt][e] - mv_new);
                             mv_run[nt][e] = mv_new;
+                            fac[nt][e] = mv_new == -INFINITY ? 0.f : ex2(m_new - mv_new);
+                        }
+#pragma unroll
+                        for (int tp = 0; tp < TP; ++tp) {
+                            s[tp][nt][e] -= down;
+                            s[tp][nt][e + 2] -= down;
                         }
 #pragma unroll
                         for (int j = 0; j < MT; ++j) {
@@ -571,83 +596,79 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
                             acc[nt][j][e + 2] *= beta;
                         }
                     }
-                refac = true;
-            }
-            if (F8 && refac) {
-                vs_fac = vsc;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        fac[nt][e] = mv_run[nt][e] == -INFINITY ? 0.f : vsc * ex2(m_run[nt][e] - mv_run[nt][e]);
             }
 
-            // P^T, from the accumulator's layout to the operand's
-            uint32_t pb[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float w[4];
+            for (int tp = 0; tp < TP; ++tp) {
+                // P^T, from the accumulator's layout to the operand's
+                uint32_t pb[NT][2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = ex2(s[nt][e]);
-                l_run[nt][0] += w[0] + w[2];
-                l_run[nt][1] += w[1] + w[3];
-                if constexpr (F8) {
-                    pb[nt][0] = movmatrix(pack_f16(w[0] * fac[nt][0], w[1] * fac[nt][1]));
-                    pb[nt][1] = movmatrix(pack_f16(w[2] * fac[nt][0], w[3] * fac[nt][1]));
-                } else {
-                    pb[nt][0] = movmatrix(pack_bf16(w[0], w[1]));
-                    pb[nt][1] = movmatrix(pack_bf16(w[2], w[3]));
-                }
-            }
-
-            // O^T += V^T P^T: element e of this thread's columns of rows 2 t4, 2 t4 + 1 (lo)
-            // and 2 t4 + 8, 2 t4 + 9 (hi); tile j takes elements 2 j and 2 j + 1
-            if constexpr (!F8) {
+                for (int nt = 0; nt < NT; ++nt) {
+                    float w[4];
 #pragma unroll
-                for (int c = 0; c < CH / 8; ++c) {
-                    const uint32_t at = vt + v_src + c * 128, at1 = W::v_row1(at);
-                    const uint4 x0 = lds128(at), x1 = lds128(at1), y0 = lds128(at + 8 * ROW), y1 = lds128(at1 + 8 * ROW);
-                    const uint32_t a[4] = {x0.x, x0.y, x0.z, x0.w}, a1[4] = {x1.x, x1.y, x1.z, x1.w};
-                    const uint32_t bb[4] = {y0.x, y0.y, y0.z, y0.w}, b1[4] = {y1.x, y1.y, y1.z, y1.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t lo0 = __byte_perm(a[j], a1[j], 0x5410), lo1 = __byte_perm(a[j], a1[j], 0x7632);
-                        const uint32_t hi0 = __byte_perm(bb[j], b1[j], 0x5410), hi1 = __byte_perm(bb[j], b1[j], 0x7632);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma16816<false>(acc[nt][4 * c + j], lo0, lo1, hi0, hi1, pb[nt][0], pb[nt][1]);
-                    }
-                }
-            } else {
-                constexpr int kWords = D / 32;  // of a row per thread (16 columns at d = 128, 8 at 64)
-                const uint32_t at = vt + v_src, at1 = W::v_row1(at);
-                uint32_t a[4][4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t from = (k & 1 ? at1 : at) + (k >> 1) * 8 * ROW;
-                    if constexpr (D == 128) {
-                        const uint4 w = lds128(from);
-                        a[k][0] = w.x;
-                        a[k][1] = w.y;
-                        a[k][2] = w.z;
-                        a[k][3] = w.w;
+                    for (int e = 0; e < 4; ++e) w[e] = ex2(s[tp][nt][e]);
+                    l_run[nt][0] += w[0] + w[2];
+                    l_run[nt][1] += w[1] + w[3];
+                    if constexpr (F8) {
+                        const float f0 = fac[nt][0] * vsc[tp], f1 = fac[nt][1] * vsc[tp];
+                        pb[nt][0] = movmatrix(pack_f16(w[0] * f0, w[1] * f1));
+                        pb[nt][1] = movmatrix(pack_f16(w[2] * f0, w[3] * f1));
                     } else {
-                        const uint2 w = lds64(from);
-                        a[k][0] = w.x;
-                        a[k][1] = w.y;
+                        pb[nt][0] = movmatrix(pack_bf16(w[0], w[1]));
+                        pb[nt][1] = movmatrix(pack_bf16(w[2], w[3]));
                     }
                 }
+
+                // O^T += V^T P^T: element e of this thread's columns of rows 2 t4, 2 t4 + 1 (lo)
+                // and 2 t4 + 8, 2 t4 + 9 (hi); tile j takes elements 2 j and 2 j + 1
+                const uint32_t v_at = vs_at + tp * 2 * L::kTile;
+                if constexpr (!F8) {
 #pragma unroll
-                for (int j = 0; j < kWords; ++j) {
-                    uint32_t f[8];  // [lo: elements 4 j .. 4 j + 3, hi: the same]
-                    widen_e4m3x4(__byte_perm(a[0][j], a[1][j], 0x5140), f[0], f[1]);
-                    widen_e4m3x4(__byte_perm(a[0][j], a[1][j], 0x7362), f[2], f[3]);
-                    widen_e4m3x4(__byte_perm(a[2][j], a[3][j], 0x5140), f[4], f[5]);
-                    widen_e4m3x4(__byte_perm(a[2][j], a[3][j], 0x7362), f[6], f[7]);
+                    for (int c = 0; c < CH / 8; ++c) {
+                        const uint32_t at = v_at + c * 128, at1 = W::v_row1(at);
+                        const uint4 x0 = lds128(at), x1 = lds128(at1), y0 = lds128(at + 8 * ROW), y1 = lds128(at1 + 8 * ROW);
+                        const uint32_t a[4] = {x0.x, x0.y, x0.z, x0.w}, a1[4] = {x1.x, x1.y, x1.z, x1.w};
+                        const uint32_t bb[4] = {y0.x, y0.y, y0.z, y0.w}, b1[4] = {y1.x, y1.y, y1.z, y1.w};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma16816<true>(acc[nt][2 * j], f[0], f[1], f[4], f[5], pb[nt][0], pb[nt][1]);
-                        mma16816<true>(acc[nt][2 * j + 1], f[2], f[3], f[6], f[7], pb[nt][0], pb[nt][1]);
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t lo0 = __byte_perm(a[j], a1[j], 0x5410), lo1 = __byte_perm(a[j], a1[j], 0x7632);
+                            const uint32_t hi0 = __byte_perm(bb[j], b1[j], 0x5410), hi1 = __byte_perm(bb[j], b1[j], 0x7632);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816<false>(acc[nt][4 * c + j], lo0, lo1, hi0, hi1, pb[nt][0], pb[nt][1]);
+                        }
+                    }
+                } else {
+                    constexpr int kWords = D / 32;  // of a row per thread (16 columns at d = 128, 8 at 64)
+                    const uint32_t at = v_at, at1 = W::v_row1(at);
+                    uint32_t a[4][4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t from = (k & 1 ? at1 : at) + (k >> 1) * 8 * ROW;
+                        if constexpr (D == 128) {
+                            const uint4 w = lds128(from);
+                            a[k][0] = w.x;
+                            a[k][1] = w.y;
+                            a[k][2] = w.z;
+                            a[k][3] = w.w;
+                        } else {
+                            const uint2 w = lds64(from);
+                            a[k][0] = w.x;
+                            a[k][1] = w.y;
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < kWords; ++j) {
+                        uint32_t f[8];  // [lo: elements 4 j .. 4 j + 3, hi: the same]
+                        widen_e4m3x4(__byte_perm(a[0][j], a[1][j], 0x5140), f[0], f[1]);
+                        widen_e4m3x4(__byte_perm(a[0][j], a[1][j], 0x7362), f[2], f[3]);
+                        widen_e4m3x4(__byte_perm(a[2][j], a[3][j], 0x5140), f[4], f[5]);
+                        widen_e4m3x4(__byte_perm(a[2][j], a[3][j], 0x7362), f[6], f[7]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816<true>(acc[nt][2 * j], f[0], f[1], f[4], f[5], pb[nt][0], pb[nt][1]);
+                            mma16816<true>(acc[nt][2 * j + 1], f[2], f[3], f[6], f[7], pb[nt][0], pb[nt][1]);
+                        }
                     }
                 }
             }
