@@ -17,8 +17,9 @@
 //
 // Both kernels only move bytes: each input is read and each output written once (the
 // 8-bit kernel reads its rows twice, the second time from L1/L2).  A thread owns 16
-// columns of a token (two 16-byte pieces that rotate into each other) and one token's
-// eight (cos, sin) stay in registers while it walks heads.
+// columns of a token (two 16-byte pieces that rotate into each other) and walks heads;
+// what a token costs besides (its sequence, page, sines and cosines) is found once per
+// block or held in registers over the heads.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -45,8 +46,9 @@ struct AppendParams {
     const uint64_t* inv_freq; // [rot / 2] (the bits of doubles)
     long long q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh;  // elements
     int T, B, H, H_kv, rot, interleaved, num_pages, max_pages, shift;
-    int groups;               // head groups (grid.y)
-    int kv_blocks;            // 8-bit: blocks (x) of the pages, the rest rotate queries
+    int groups;               // head groups (bf16: grid y)
+    int kv_blocks, q_groups;  // 8-bit: kv_blocks * groups blocks for the pages, then q_groups
+                              // per block of rows for the queries
     unsigned int* err;
 };
 
@@ -78,19 +80,22 @@ __device__ __forceinline__ int last_not_above(int B, long long x, Key key) {
     return lo;
 }
 
-// One token's eight (cos, sin): pairs [8 u, 8 u + 8).
-struct Turn {
-    float c[8], s[8];
-};
-__device__ __forceinline__ void turn_at(const AppendParams& p, int u, int pos, Turn& t) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint64_t turns = turn_fraction(__ldg(p.inv_freq + 8 * u + i)) * static_cast<uint64_t>(pos);
-        // half turns in [-1, 1): the top 32 bits
-        const float half = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f;
-        sincospif(half, &t.s[i], &t.c[i]);
-    }
+// (cos, sin) of position pos at a frequency given as a turn fraction.
+__device__ __forceinline__ float2 turn_at(uint64_t freq, int pos) {
+    // half turns in [-1, 1): the top 32 bits
+    const uint64_t turns = freq * static_cast<uint64_t>(pos);
+    float2 t;
+    sincospif(static_cast<float>(static_cast<int32_t>(turns >> 32)) * 0x1p-31f, &t.y, &t.x);
+    return t;
 }
+
+// A thread's eight (cos, sin), pairs [8 u, 8 u + 8) of its unit u, lie in shared memory (in
+// registers they would halve the threads that an SM holds): pairs 2 i and 2 i + 1 as the
+// float4 at turn[i * stride].
+struct Turn {
+    const float4* at;
+    int stride;
+};
 
 // The two 16-byte pieces of 8 columns that unit u of a row owns.
 __device__ __forceinline__ void pieces(const AppendParams& p, int u, int& a, int& b) {
@@ -115,19 +120,22 @@ __device__ __forceinline__ void rotate(const AppendParams& p, const uint4& wa, c
         x[8 + 2 * i] = lo_f(b[i]);
         x[8 + 2 * i + 1] = hi_f(b[i]);
     }
-    if (p.interleaved) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float e = x[2 * i], o = x[2 * i + 1];
-            x[2 * i] = e * t.c[i] - o * t.s[i];
-            x[2 * i + 1] = o * t.c[i] + e * t.s[i];
-        }
-    } else {
+    for (int i = 0; i < 4; ++i) {
+        const float4 cs = t.at[i * t.stride];  // cos, sin, cos, sin
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float e = x[i], o = x[8 + i];
-            x[i] = e * t.c[i] - o * t.s[i];
-            x[8 + i] = o * t.c[i] + e * t.s[i];
+        for (int k = 0; k < 2; ++k) {
+            const float c = k ? cs.z : cs.x, s = k ? cs.w : cs.y;
+            const int j = 2 * i + k;
+            if (p.interleaved) {
+                const float e = x[2 * j], o = x[2 * j + 1];
+                x[2 * j] = e * c - o * s;
+                x[2 * j + 1] = o * c + e * s;
+            } else {
+                const float e = x[j], o = x[8 + j];
+                x[j] = e * c - o * s;
+                x[8 + j] = o * c + e * s;
+            }
         }
     }
 }
@@ -136,49 +144,95 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
     return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// Rows (tokens) of a block are consecutive; heads [h0, h1) of the list [Q heads | K
-// heads | V heads] are walked by every row.  Used by both kernels (the 8-bit kernel
-// sends its queries here).  Measured: see fa_kv_append_kernel.
+constexpr int kAppendThreads = 256;
+constexpr int kHeadGroups = 4;  // of a block: threads that share a token's angles
+constexpr int kMaxRot = 128;
+constexpr long long kWantBlocks = 4 * 152;  // as many as are resident
+
+// What the tokens of a block share.
 template <int D>
-__device__ __forceinline__ void append_rows(const AppendParams& p, int t_first, int h0, int h1) {
-    constexpr int U = D / 16;  // units per row
-    const int u = threadIdx.x % U;
-    const int warp_t = t_first + static_cast<int>(threadIdx.x & ~31u) / U;  // the warp's first token
-    if (warp_t >= p.T) return;  // warp-uniform
-    const int t = t_first + static_cast<int>(threadIdx.x) / U;
-    int b = last_not_above(p.B, warp_t, [&](int i) { return static_cast<long long>(cu_of(p, i)); });
-    if (t >= p.T) return;
-    while (b + 1 < p.B && cu_of(p, b + 1) <= t) ++b;
-    const int c0 = cu_of(p, b), c1 = cu_of(p, b + 1);
-    if (t < c0 || t >= c1) return;  // a row behind the last sequence: left as it is
-    const int past = __ldg(p.lens + b);
-    const long long pos = static_cast<long long>(past) + (t - c0);
-    const int pg = past < 0 ? -1 : page_of(p.table + static_cast<long long>(b) * p.max_pages, p.max_pages,
-                                           p.num_pages, p.shift, pos);
-    if (pg < 0 && h1 > p.H) page_error(p.err);
+struct RowShared {
+    static constexpr int U = D / 16;                                   // units per row
+    static constexpr int kTokens = kAppendThreads / (U * kHeadGroups);  // 8 at d = 128, 16 at 64
+    float4 turn[kTokens][4][U];  // [token][pairs 2 i, 2 i + 1][unit]
+    int pos[kTokens], page[kTokens];
+    int live[kTokens];  // the token belongs to a sequence
+};
+
+// kTokens consecutive tokens, the heads [h0, h1) of the list [Q heads | K heads | V heads]
+// in four groups of threads.  Used by both kernels (the 8-bit one sends its queries here).
+template <int D>
+__device__ __forceinline__ void append_rows(const AppendParams& p, RowShared<D>& sh, int t_first, int h0, int h1) {
+    using S = RowShared<D>;
+    constexpr int U = S::U, TOK = S::kTokens;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int u = tid % U, k = tid / U % TOK, hg = tid / (U * TOK);
+    const int t = t_first + k;
+    if (tid < 32) {
+        // the sequence of each token: that of the first, and the next 32 sequences' starts
+        const int b0 = last_not_above(p.B, t_first, [&](int i) { return static_cast<long long>(cu_of(p, i)); });
+        const int cuv = b0 + 1 + lane < p.B ? cu_of(p, b0 + 1 + lane) : 0x7fffffff;
+        int b = b0;
+#pragma unroll
+        for (int i = 0; i < TOK; ++i) {
+            const int n = __popc(__ballot_sync(0xffffffffu, cuv <= t_first + i));
+            if (lane == i) b += n;
+        }
+        if (lane < TOK) {
+            const int tt = t_first + lane;
+            if (b == b0 + 32)  // (32 sequences begin at or before the token: go on one by one)
+                while (b + 1 < p.B && cu_of(p, b + 1) <= tt) ++b;
+            const int c0 = cu_of(p, b), c1 = cu_of(p, b + 1), past = __ldg(p.lens + b);
+            const long long pos = static_cast<long long>(past) + (tt - c0);
+            const bool live = tt < p.T && tt >= c0 && tt < c1;
+            int pg = -1;
+            if (live && h1 > p.H) {
+                if (past >= 0)
+                    pg = page_of(p.table + static_cast<long long>(b) * p.max_pages, p.max_pages, p.num_pages, p.shift, pos);
+                if (pg < 0) page_error(p.err);
+            }
+            sh.pos[lane] = static_cast<int>(pos);
+            sh.page[lane] = pg;
+            sh.live[lane] = live;
+        }
+    }
+    __syncthreads();
+    const int half = p.rot / 2;
+    if (half > 0 && h0 < p.H + p.H_kv) {
+        // freq ascends with idx % half, so neighbouring threads read neighbouring entries
+        for (int idx = tid; idx < TOK * half; idx += kAppendThreads) {
+            const int i = idx / half, c = idx - i * half;
+            reinterpret_cast<float2*>(&sh.turn[i][c % 8 / 2][c / 8])[c & 1] =
+                turn_at(turn_fraction(__ldg(p.inv_freq + c)), sh.pos[i]);
+        }
+        __syncthreads();
+    }
+    if (!sh.live[k]) return;  // a row behind the last sequence: left as it is
+    const int pg = sh.page[k], off = sh.pos[k] & ((1 << p.shift) - 1);
     const bool turns = u < p.rot / 16;
-    Turn tr;
-    if (turns && h0 < p.H + p.H_kv) turn_at(p, u, static_cast<int>(pos), tr);
+    const Turn tr{&sh.turn[k][0][u], U};
     int a, c;
     pieces(p, u, a, c);
-    const int off = static_cast<int>(pos) & ((1 << p.shift) - 1);
     constexpr int kBatch = 4;  // heads whose loads are in flight together
-    for (int hb = h0; hb < h1; hb += kBatch) {
+    const __nv_bfloat16* qrow = p.q + t * p.q_st;
+    const __nv_bfloat16* krow = p.k + t * p.k_st - p.H * p.k_sh;
+    const __nv_bfloat16* vrow = p.v + t * p.v_st - (p.H + p.H_kv) * p.v_sh;
+    for (int hb = h0 + hg; hb < h1; hb += kBatch * kHeadGroups) {
         uint4 wa[kBatch], wb[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const int h = hb + i;
-            if (h >= h1) break;
-            const __nv_bfloat16* src =
-                h < p.H            ? p.q + t * p.q_st + h * p.q_sh
-                : h < p.H + p.H_kv ? p.k + t * p.k_st + (h - p.H) * p.k_sh
-                                   : p.v + t * p.v_st + (h - p.H - p.H_kv) * p.v_sh;
-            wa[i] = __ldg(reinterpret_cast<const uint4*>(src) + a);
-            wb[i] = __ldg(reinterpret_cast<const uint4*>(src) + c);
+            const int h = hb + i * kHeadGroups;
+            if (h < h1) {
+                const __nv_bfloat16* src = h < p.H            ? qrow + h * p.q_sh
+                                           : h < p.H + p.H_kv ? krow + h * p.k_sh
+                                                              : vrow + h * p.v_sh;
+                wa[i] = __ldg(reinterpret_cast<const uint4*>(src) + a);
+                wb[i] = __ldg(reinterpret_cast<const uint4*>(src) + c);
+            }
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const int h = hb + i;
+            const int h = hb + i * kHeadGroups;
             if (h >= h1) break;
             if (turns && h < p.H + p.H_kv) {
                 float x[16];
@@ -202,14 +256,13 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int t_first, 
     }
 }
 
-constexpr int kAppendThreads = 256;
-
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) fa_kv_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const AppendParams p) {
+    __shared__ RowShared<D> sh;
     const int n = p.H + 2 * p.H_kv;
     const int per = (n + p.groups - 1) / p.groups;
     const int h0 = static_cast<int>(blockIdx.y) * per;
-    append_rows<D>(p, static_cast<int>(blockIdx.x) * (kAppendThreads / (D / 16)), h0, min(n, h0 + per));
+    append_rows<D>(p, sh, static_cast<int>(blockIdx.x) * RowShared<D>::kTokens, h0, min(n, h0 + per));
 }
 
 __device__ __forceinline__ float amax8(const uint4& w, float m) {
@@ -227,35 +280,58 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
     return pack_e4m3x4(a.x * r, a.y * r, b.x * r, b.y * r);
 }
 
-constexpr int kMaxGroupHeads = 64;  // heads (of the list [K | V]) that one block walks
+constexpr int kMaxGroupHeads = 16;  // heads (of the list [K | V]) that one team walks
 
-// One block per (sequence, page reached, head group): it alone writes that page's heads,
-// so the scale needs no communication.  Two passes over the page's new rows, the second
-// from L1/L2: the largest magnitude per head, then rotate, scale, round and store.
-template <int D>
-__global__ void __launch_bounds__(256) fa_kv_append_fp8_kernel(const AppendParams p) {
-    constexpr int U = D / 16;
-    __shared__ uint32_t amax_s[kMaxGroupHeads];
-    __shared__ float scale_s[kMaxGroupHeads], inv_s[kMaxGroupHeads];
-    const int rows = static_cast<int>(blockDim.x) / U;
-    const int bx = static_cast<int>(blockIdx.x);
-    if (bx >= p.kv_blocks) {
-        const int per = (p.H + p.groups - 1) / p.groups;
-        const int h0 = static_cast<int>(blockIdx.y) * per;
-        if (h0 < p.H) append_rows<D>(p, (bx - p.kv_blocks) * rows, h0, min(p.H, h0 + per));
+struct PageShared {
+    float4 turn[4][kAppendThreads];  // each thread's own
+    uint64_t freq[kMaxRot / 2];
+    uint32_t amax[kAppendThreads / 32][kMaxGroupHeads];
+    float scale[kAppendThreads / 32][kMaxGroupHeads], inv[kAppendThreads / 32][kMaxGroupHeads];
+};
+
+// One team of threads (a block, or with few new tokens per sequence a warp) per (sequence,
+// page reached, head group): it alone writes that page's heads, so the scale needs no
+// communication.  Two passes over the page's new rows, the second from L1/L2: the largest
+// magnitude per head, then rotate, scale, round and store.
+template <int D, int TEAM>
+__global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_fp8_kernel(const AppendParams p) {
+    constexpr int U = D / 16, ROWS = TEAM / U, TEAMS = kAppendThreads / TEAM;
+    __shared__ union {
+        PageShared page;
+        RowShared<D> row;
+    } sh;
+    int bx = static_cast<int>(blockIdx.x);
+    if (bx >= p.kv_blocks * p.groups) {
+        bx -= p.kv_blocks * p.groups;
+        const int rb = bx / p.q_groups, per = (p.H + p.q_groups - 1) / p.q_groups, h0 = (bx - rb * p.q_groups) * per;
+        if (h0 < p.H) append_rows<D>(p, sh.row, rb * RowShared<D>::kTokens, h0, min(p.H, h0 + per));
         return;
     }
+    const int group = bx % p.groups;
+    bx /= p.groups;
+    const int team = static_cast<int>(threadIdx.x) / TEAM, tid = static_cast<int>(threadIdx.x) % TEAM;
+    const auto sync = [] {
+        if constexpr (TEAM == 32) __syncwarp();
+        else __syncthreads();
+    };
+    if (p.rot > 0) {
+        for (int i = threadIdx.x; i < p.rot / 2; i += kAppendThreads) sh.page.freq[i] = turn_fraction(__ldg(p.inv_freq + i));
+        __syncthreads();
+    }
+    uint32_t* amax_s = sh.page.amax[team];
+    float* scale_s = sh.page.scale[team];
+    float* inv_s = sh.page.inv[team];
     const int n_list = 2 * p.H_kv;
     const int per = (n_list + p.groups - 1) / p.groups;
-    const int h0 = static_cast<int>(blockIdx.y) * per, h1 = min(n_list, h0 + per);
+    const int h0 = group * per, h1 = min(n_list, h0 + per);
     if (h0 >= h1) return;
-    // this block's sequence and page
-    const int b = last_not_above(p.B, bx, [&](int i) { return first_unit(cu_of(p, i), i, p.shift); });
-    const int c0 = cu_of(p, b), c1 = cu_of(p, b + 1);
-    const int i = static_cast<int>(bx - first_unit(c0, b, p.shift));
-    const int past = __ldg(p.lens + b);
+    // this team's sequence and page
+    const int unit = bx * TEAMS + team;
+    const int b = last_not_above(p.B, unit, [&](int i) { return first_unit(cu_of(p, i), i, p.shift); });
+    const int c0 = cu_of(p, b), c1 = cu_of(p, b + 1), past = __ldg(p.lens + b);
+    const int i = static_cast<int>(unit - first_unit(c0, b, p.shift));
     if (c0 < 0 || c1 > p.T || c1 <= c0 || past < 0 || i < 0) {
-        if (c1 != c0 && threadIdx.x == 0) page_error(p.err);
+        if (c1 != c0 && tid == 0) page_error(p.err);
         return;
     }
     if (i >= pages_reached(past, c1 - c0, p.shift)) return;
@@ -266,96 +342,122 @@ __global__ void __launch_bounds__(256) fa_kv_append_fp8_kernel(const AppendParam
     const int t0 = c0 + static_cast<int>(page0 + r0 - past);  // the token of row r0
     const int pg = page_of(p.table + static_cast<long long>(b) * p.max_pages, p.max_pages, p.num_pages, p.shift, page0);
     if (pg < 0) {
-        if (threadIdx.x == 0) page_error(p.err);
+        if (tid == 0) page_error(p.err);
         return;
     }
-    const int u = threadIdx.x % U, tr = threadIdx.x / U;
+    const int u = tid % U, tr = tid / U;
     int a, c;
     pieces(p, u, a, c);
-    for (int h = threadIdx.x; h < h1 - h0; h += blockDim.x) amax_s[h] = 0u;
-    __syncthreads();
+    for (int h = tid; h < h1 - h0; h += TEAM) amax_s[h] = 0u;
+    sync();
     const auto row_of = [&](int h, int r) {
         const long long t = t0 + (r - r0);
-        return h < p.H_kv ? p.k + t * p.k_st + h * p.k_sh : p.v + t * p.v_st + (h - p.H_kv) * p.v_sh;
+        return reinterpret_cast<const uint4*>(h < p.H_kv ? p.k + t * p.k_st + h * p.k_sh
+                                                         : p.v + t * p.v_st + (h - p.H_kv) * p.v_sh);
     };
-    // 1. the largest magnitude of each head's new rows
-    for (int h = h0; h < h1; ++h) {
-        float m = 0.f;
-        for (int r = r0 + tr; r < r1; r += rows) {
-            const uint4* src = reinterpret_cast<const uint4*>(row_of(h, r));
-            m = amax8(__ldg(src + a), m);
-            m = amax8(__ldg(src + c), m);
+    // this thread's items: (row, head), rows r0 + tr, + ROWS, ... below r1
+    const int n_rows = tr < r1 - r0 ? (r1 - r0 - tr + ROWS - 1) / ROWS : 0, nh = h1 - h0;
+    // 1. the largest magnitude of each head's new rows; four items' loads in flight
+    const int most = (r1 - r0 + ROWS - 1) / ROWS * nh;  // (the same for the whole team)
+    constexpr int kBatch = 4;
+    for (int ib = 0; ib < most; ib += kBatch) {
+        uint4 wa[kBatch], wb[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int rr = (ib + k) / nh, h = h0 + (ib + k) - rr * nh;
+            if (rr < n_rows) {
+                const uint4* src = row_of(h, r0 + tr + rr * ROWS);
+                wa[k] = __ldg(src + a);
+                wb[k] = __ldg(src + c);
+            }
         }
-        const uint32_t mw = __reduce_max_sync(0xffffffffu, __float_as_uint(m));  // (non-negative: bits keep the order)
-        if ((threadIdx.x & 31) == 0 && mw != 0u) atomicMax(&amax_s[h - h0], mw);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int rr = (ib + k) / nh, h = (ib + k) - rr * nh;
+            const float m = rr < n_rows ? amax8(wb[k], amax8(wa[k], 0.f)) : 0.f;
+            // (non-negative: the bits keep the order)
+            const uint32_t mw = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+            if ((threadIdx.x & 31) == 0 && mw != 0u) atomicMax(&amax_s[h], mw);
+        }
     }
-    __syncthreads();
+    sync();
     // 2. the scales; a page begun earlier keeps the larger one, its codes rescaled
-    for (int h = h0; h < h1; ++h) {
+    const auto place = [&](int h, bool is_k) { return static_cast<long long>(pg) * p.H_kv + (is_k ? h : h - p.H_kv); };
+    for (int h = h0 + tid; h < h1; h += TEAM) {
         const bool is_k = h < p.H_kv;
-        const int hk = is_k ? h : h - p.H_kv;
-        const long long ph = static_cast<long long>(pg) * p.H_kv + hk;
-        float* scale = (is_k ? p.k_scale : p.v_scale) + ph;
         float bound = __uint_as_float(amax_s[h - h0]);
         if (is_k && p.rot > 0) bound *= 1.5f;
         const float need = __uint_as_float(static_cast<uint32_t>(page_scale_exp(__float_as_uint(bound)) + 127) << 23);
-        float s = need;
-        if (r0 > 0) {
-            const float old = *scale;
-            s = fmaxf(old, need);
-            if (s > old) {
-                const float ratio = old / s;
-                uint4* codes = reinterpret_cast<uint4*>((is_k ? p.kc : p.vc) + ((ph << p.shift) * D));
-                for (int e = threadIdx.x; e < r0 * (D / 16); e += blockDim.x) {
-                    uint4 w = codes[e];
-                    w.x = rescale4(w.x, ratio);
-                    w.y = rescale4(w.y, ratio);
-                    w.z = rescale4(w.z, ratio);
-                    w.w = rescale4(w.w, ratio);
-                    codes[e] = w;
-                }
-            }
-        }
-        if (threadIdx.x == 0) {
-            scale_s[h - h0] = s;
-            inv_s[h - h0] = 1.f / s;  // exact for a power of two
-        }
+        float* scale = (is_k ? p.k_scale : p.v_scale) + place(h, is_k);
+        const float old = r0 > 0 ? *scale : need, s = fmaxf(old, need);
+        scale_s[h - h0] = s > old ? old / s : 1.f;  // what held codes are multiplied by
+        inv_s[h - h0] = 1.f / s;                    // (exact for a power of two)
+        if (r0 == 0 || s != old) *scale = s;
     }
-    __syncthreads();  // every thread has read the old scales
-    for (int h = h0 + static_cast<int>(threadIdx.x); h < h1; h += blockDim.x) {
-        const bool is_k = h < p.H_kv;
-        (is_k ? p.k_scale : p.v_scale)[static_cast<long long>(pg) * p.H_kv + (is_k ? h : h - p.H_kv)] = scale_s[h - h0];
-    }
-    // 3. rotate, scale, round, store
-    const bool turns = u < p.rot / 16;
-    for (int r = r0 + tr; r < r1; r += rows) {
-        Turn t;
-        if (turns && h0 < p.H_kv) turn_at(p, u, static_cast<int>(page0 + r), t);
+    sync();
+    if (r0 > 0) {
         for (int h = h0; h < h1; ++h) {
+            const float ratio = scale_s[h - h0];
+            if (ratio == 1.f) continue;
             const bool is_k = h < p.H_kv;
-            const uint4* src = reinterpret_cast<const uint4*>(row_of(h, r));
-            const uint4 wa = __ldg(src + a), wb = __ldg(src + c);
-            float x[16];
-            if (turns && is_k) {
-                rotate(p, wa, wb, t, x);
-            } else {
-                const uint32_t w[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[2 * e] = lo_f(w[e]);
-                    x[2 * e + 1] = hi_f(w[e]);
-                }
+            uint4* codes = reinterpret_cast<uint4*>((is_k ? p.kc : p.vc) + ((place(h, is_k) << p.shift) * D));
+            for (int e = tid; e < r0 * (D / 16); e += TEAM) {
+                uint4 w = codes[e];
+                w.x = rescale4(w.x, ratio);
+                w.y = rescale4(w.y, ratio);
+                w.z = rescale4(w.z, ratio);
+                w.w = rescale4(w.w, ratio);
+                codes[e] = w;
             }
-            const float inv = inv_s[h - h0];
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[e] = pack_e4m3x4(x[4 * e] * inv, x[4 * e + 1] * inv, x[4 * e + 2] * inv, x[4 * e + 3] * inv);
-            uint8_t* dst = (is_k ? p.kc : p.vc) +
-                           (((static_cast<long long>(pg) * p.H_kv + (is_k ? h : h - p.H_kv)) << p.shift) + r) * D;
-            reinterpret_cast<uint2*>(dst)[a] = make_uint2(o[0], o[1]);
-            reinterpret_cast<uint2*>(dst)[c] = make_uint2(o[2], o[3]);
         }
+    }
+    // 3. rotate, scale, round, store; the next item's loads in flight
+    const bool turns = u < p.rot / 16;
+    const Turn t{&sh.page.turn[0][threadIdx.x], kAppendThreads};
+    const int n_items = n_rows * nh;
+    uint4 wa, wb;
+    if (n_items > 0) {
+        const uint4* src = row_of(h0, r0 + tr);
+        wa = __ldg(src + a);
+        wb = __ldg(src + c);
+    }
+    int h = h0, r = r0 + tr;
+    for (int it = 0; it < n_items; ++it) {
+        const uint4 xa = wa, xb = wb;
+        const int hn = h + 1 < h1 ? h + 1 : h0, rn = h + 1 < h1 ? r : r + ROWS;
+        if (it + 1 < n_items) {
+            const uint4* src = row_of(hn, rn);
+            wa = __ldg(src + a);
+            wb = __ldg(src + c);
+        }
+        if (turns && h == h0 && h0 < p.H_kv) {  // a new row
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                reinterpret_cast<float2*>(&sh.page.turn[e / 2][threadIdx.x])[e & 1] =
+                    turn_at(sh.page.freq[8 * u + e], static_cast<int>(page0 + r));
+        }
+        const bool is_k = h < p.H_kv;
+        float x[16];
+        if (turns && is_k) {
+            rotate(p, xa, xb, t, x);
+        } else {
+            const uint32_t w[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[2 * e] = lo_f(w[e]);
+                x[2 * e + 1] = hi_f(w[e]);
+            }
+        }
+        const float inv = inv_s[h - h0];
+        uint32_t o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            o[e] = pack_e4m3x4(x[4 * e] * inv, x[4 * e + 1] * inv, x[4 * e + 2] * inv, x[4 * e + 3] * inv);
+        uint8_t* dst = (is_k ? p.kc : p.vc) + ((place(h, is_k) << p.shift) + r) * D;
+        reinterpret_cast<uint2*>(dst)[a] = make_uint2(o[0], o[1]);
+        reinterpret_cast<uint2*>(dst)[c] = make_uint2(o[2], o[3]);
+        h = hn;
+        r = rn;
     }
 }
 
@@ -393,35 +495,41 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
     p.max_pages = a.cache.max_pages;
     p.shift = a.cache.shift;
     p.err = a.err;
-    const int d = a.cache.d, units = d / 16;
-    // Heads are cut into groups so that about two full machines of threads exist: with
-    // few tokens each thread takes one head (latency), with many it walks several on one
-    // set of angles.
-    const long long threads = static_cast<long long>(a.T) * units;
-    const long long want = (2ll * 152 * 2048 + threads - 1) / threads;
+    const int d = a.cache.d;
+    // Heads are cut into groups (grid y) only as far as the tokens alone do not fill the
+    // machine: each group finds its tokens' pages and angles again.
+    const int tokens = d == 64 ? RowShared<64>::kTokens : RowShared<128>::kTokens;
+    const long long row_blocks = (static_cast<long long>(a.T) + tokens - 1) / tokens;
     if (a.cache.k_scale == nullptr) {
         const int n = p.H + 2 * p.H_kv;
-        p.groups = static_cast<int>(std::min<long long>(want, n));
-        p.kv_blocks = 0;
-        const int rows = kAppendThreads / units;
-        const dim3 grid(static_cast<unsigned>((a.T + rows - 1) / rows), static_cast<unsigned>(p.groups));
+        p.groups = static_cast<int>(std::max(1ll, std::min<long long>((kWantBlocks + row_blocks - 1) / row_blocks,
+                                                                      (n + kHeadGroups - 1) / kHeadGroups)));
+        p.kv_blocks = p.q_groups = 0;
+        const dim3 grid(static_cast<unsigned>(row_blocks), static_cast<unsigned>(p.groups));
         if (d == 64) fa_kv_append_kernel<64><<<grid, kAppendThreads, 0, stream>>>(p);
         else fa_kv_append_kernel<128><<<grid, kAppendThreads, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    const int n = std::max(p.H, 2 * p.H_kv);
-    p.groups = static_cast<int>(std::max<long long>(std::min<long long>(want, n),
-                                                    (2 * p.H_kv + kMaxGroupHeads - 1) / kMaxGroupHeads));
-    // one warp per block where the sequences bring a token or a few each
-    const int block = static_cast<long long>(a.T) <= 4ll * p.B ? 32 : 256;
-    const int rows = block / units;
-    const long long kv_blocks = (static_cast<long long>(a.T) >> p.shift) + 2ll * p.B;
-    const long long q_blocks = p.H > 0 ? (a.T + rows - 1) / rows : 0;
-    if (kv_blocks + q_blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+    // a warp per page where the sequences bring a token or a few each, else a block
+    const bool warps = static_cast<long long>(a.T) <= 4ll * p.B;
+    const long long units = (static_cast<long long>(a.T) >> p.shift) + 2ll * p.B;
+    const long long kv_blocks = warps ? (units + kAppendThreads / 32 - 1) / (kAppendThreads / 32) : units;
+    const int n = 2 * p.H_kv;
+    p.groups = static_cast<int>(std::max<long long>((n + kMaxGroupHeads - 1) / kMaxGroupHeads,
+                                                    std::min<long long>((kWantBlocks + kv_blocks - 1) / kv_blocks, n)));
+    p.q_groups = static_cast<int>(std::max(1ll, std::min<long long>((kWantBlocks + row_blocks - 1) / row_blocks,
+                                                                    (p.H + kHeadGroups - 1) / kHeadGroups)));
+    const long long blocks = kv_blocks * p.groups + (p.H > 0 ? row_blocks * p.q_groups : 0);
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
     p.kv_blocks = static_cast<int>(kv_blocks);
-    const dim3 grid(static_cast<unsigned>(kv_blocks + q_blocks), static_cast<unsigned>(p.groups));
-    if (d == 64) fa_kv_append_fp8_kernel<64><<<grid, block, 0, stream>>>(p);
-    else fa_kv_append_fp8_kernel<128><<<grid, block, 0, stream>>>(p);
+    const dim3 grid(static_cast<unsigned>(blocks));
+    if (d == 64) {
+        if (warps) fa_kv_append_fp8_kernel<64, 32><<<grid, kAppendThreads, 0, stream>>>(p);
+        else fa_kv_append_fp8_kernel<64, 256><<<grid, kAppendThreads, 0, stream>>>(p);
+    } else {
+        if (warps) fa_kv_append_fp8_kernel<128, 32><<<grid, kAppendThreads, 0, stream>>>(p);
+        else fa_kv_append_fp8_kernel<128, 256><<<grid, kAppendThreads, 0, stream>>>(p);
+    }
     return cudaGetLastError();
 }
 
