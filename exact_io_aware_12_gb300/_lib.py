@@ -104,6 +104,29 @@ def load() -> ctypes.CDLL:
         return _lib
 
 
+_binding = None
+
+
+def binding():
+    """The torch binding of the paged entry points (csrc/torch_binding.cpp), built first
+    if it is missing or stale, with the library behind it."""
+    global _binding
+    if _binding is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch
+        load()
+        with _lock:
+            if _binding is None:
+                loader = importlib.machinery.ExtensionFileLoader("fa_binding", _build.build_binding())
+                mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("fa_binding", loader))
+                loader.exec_module(mod)
+                mod.load(library_path(), FAError, torch.OutOfMemoryError)
+                _binding = mod
+    return _binding
+
+
 def library_path() -> str:
     return _build.LIB_PATH
 

@@ -2,11 +2,12 @@
 
 PyTorch only supplies device memory and the current stream; the tensors'
 data pointers go straight to ``fa_fwd`` / ``fa_bwd``.  Inputs must be CUDA
-bf16 tensors, contiguous, shaped [B, H, N, d].
+bf16 tensors, contiguous, shaped [B, H, N, d].  The paged entry points
+(``kv_append``, ``fwd_paged``) check and call in a small extension module
+(csrc/torch_binding.cpp), for their kernels take little longer than a call.
 """
 from __future__ import annotations
 
-import functools
 import math
 from typing import Optional, Tuple
 
@@ -222,68 +223,6 @@ def fwd_decode(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool,
     return out, lse
 
 
-# The paged entry points take microseconds on the GPU, so the host's share counts: the
-# checks below touch each tensor once, and the device is switched only when it differs.
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
-_E4M3 = (torch.float8_e4m3fn, torch.uint8)
-
-
-def _paged_cache(k_cache, v_cache, page_table, lens, k_scale, v_scale):
-    """Checks a paged cache's tensors; returns its description for the C ABI."""
-    shape, dtype, dev = k_cache.shape, k_cache.dtype, k_cache.device
-    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != dtype:
-        raise ValueError("caches must be [num_pages, H_kv, page_size, d], alike")
-    P, Hkv, page, d = shape
-    if k_scale is None:
-        if v_scale is not None:
-            raise ValueError("an 8-bit cache has both scales, a bf16 cache none")
-        if dtype != _BF16:
-            raise ValueError("a cache is bf16, or with scales e4m3 (uint8 or float8_e4m3fn)")
-        ks = vs = None
-    else:
-        if v_scale is None:
-            raise ValueError("an 8-bit cache has both scales, a bf16 cache none")
-        if dtype not in _E4M3:
-            raise ValueError("a cache is bf16, or with scales e4m3 (uint8 or float8_e4m3fn)")
-        if k_scale.shape != (P, Hkv) or v_scale.shape != (P, Hkv) or k_scale.dtype != _F32 or \
-                v_scale.dtype != _F32:
-            raise ValueError("scales must be fp32 [num_pages, H_kv]")
-        if k_scale.device != dev or v_scale.device != dev or not k_scale.is_contiguous() or \
-                not v_scale.is_contiguous():
-            raise ValueError("scales must be contiguous, on the cache's device")
-        ks, vs = k_scale.data_ptr(), v_scale.data_ptr()
-    ts = page_table.shape
-    if len(ts) != 2 or lens.shape != ts[:1]:
-        raise ValueError("page_table must be [B, max_pages] and lens [B]")
-    if page_table.dtype != _I32 or lens.dtype != _I32:
-        raise ValueError("page_table and lens must be int32")
-    if not k_cache.is_cuda or v_cache.device != dev or page_table.device != dev or \
-            lens.device != dev or not (k_cache.is_contiguous() and v_cache.is_contiguous() and
-                                       page_table.is_contiguous() and lens.is_contiguous()):
-        raise ValueError("caches, page_table and lens must be contiguous, on one CUDA device")
-    return _lib.PagedCache(k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, page_table.data_ptr(),
-                           lens.data_ptr(), ts[0], Hkv, d, P, page, ts[1])
-
-
-def _rows(t, shape, dev, what):
-    """Checks a bf16 tensor of rows with contiguous columns; returns its strides."""
-    st = t.stride()
-    if t.shape != shape or t.dtype != _BF16 or t.device != dev or st[-1] != 1:
-        raise ValueError(f"{what} must be bf16 {list(shape)} on the cache's device, columns contiguous")
-    return st
-
-
-def _launch(dev, name, *args):
-    """Calls an entry point with the tensors' device current, on its current stream."""
-    if dev.index == torch.cuda.current_device():
-        code = _lib._call(name, *args, _stream_handle(dev))
-    else:
-        with torch.cuda.device(dev):
-            code = _lib._call(name, *args, _stream_handle(dev))
-    if code:
-        _lib.check(code, name)
-
-
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
               page_table: torch.Tensor, lens: torch.Tensor, cu_new: Optional[torch.Tensor] = None,
               q: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
@@ -299,49 +238,10 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     the first rot columns of the keys, and of ``q`` [T, H, d] where given, by
     their position; ``interleaved`` pairs neighbouring columns.  Returns the
     rotated queries (``q_out``, or a new tensor), or None without ``q``."""
-    c = _paged_cache(k_cache, v_cache, page_table, lens, k_scale, v_scale)
-    dev, d = k_cache.device, c.d
-    if k.dim() != 3:
-        raise ValueError("k and v must be [T, H_kv, d]")
-    T = k.shape[0]
-    shape = (T, c.H_kv, d)
-    ks, vs = _rows(k, shape, dev, "k"), _rows(v, shape, dev, "v")
-    cu = None
-    if cu_new is not None:
-        if cu_new.shape != (c.B + 1,) or cu_new.dtype != _I32 or cu_new.device != dev or \
-                not cu_new.is_contiguous():
-            raise ValueError("cu_new must be contiguous int32 [B + 1] on the cache's device")
-        cu = cu_new.data_ptr()
-    rot, fp = 0, None
-    if inv_freq is not None:
-        if inv_freq.dim() != 1 or inv_freq.dtype != torch.float64 or inv_freq.device != dev or \
-                not inv_freq.is_contiguous():
-            raise ValueError("inv_freq must be contiguous float64 [rot / 2] on the cache's device")
-        rot, fp = 2 * inv_freq.shape[0], inv_freq.data_ptr()
-        if rot == 0:
-            raise ValueError("inv_freq is empty")
-    H, qp, op, qs, os_ = 0, None, None, (0, 0), (0, 0)
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q must be [T, H, d]")
-        H = q.shape[1]
-        qs = _rows(q, (T, H, d), dev, "q")
-        if q_out is None:
-            q_out = torch.empty((T, H, d), dtype=_BF16, device=dev)
-            os_ = (H * d, d)
-        else:
-            os_ = _rows(q_out, (T, H, d), dev, "q_out")
-        if H:
-            qp, op = q.data_ptr(), q_out.data_ptr()
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    _launch(dev, "fa_kv_append" if k_scale is None else "fa_kv_append_fp8", c, k.data_ptr(), ks[0],
-            ks[1], v.data_ptr(), vs[0], vs[1], T, cu, qp, qs[0], qs[1], op, os_[0], os_[1], H, fp, rot,
-            1 if interleaved else 0)
-    return q_out
+    return _lib.binding().kv_append(k, v, k_cache, v_cache, page_table, lens, cu_new, q, inv_freq,
+                                    interleaved, k_scale, v_scale, q_out)
 
 
-@functools.lru_cache(maxsize=256)
 def paged_workspace_bytes(B: int, H: int, H_kv: int, Nq: int, d: int, fp8: bool = False) -> int:
     return _lib.fa_paged_workspace_size(B, H, H_kv, Nq, d, int(bool(fp8)))
 
@@ -358,40 +258,8 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     ``window`` and ``sinks`` as in ``fwd``.  Returns (O bf16 [B, H, Nq, d], LSE
     fp32 [B, H, Nq]); a row without keys gives 0 and -inf.  The workspace is
     allocated with torch when not given."""
-    c = _paged_cache(k_cache, v_cache, page_table, lens, k_scale, v_scale)
-    dev, B, d = k_cache.device, c.B, c.d
-    if q.dim() != 4:
-        raise ValueError("expected [B, H, Nq, d] queries")
-    if window is None:
-        if sinks:
-            raise ValueError("sinks need a window")
-        window = 0
-    elif window < 1:
-        raise ValueError("a window holds at least one key")
-    _, H, Nq, _ = q.shape
-    shape = (B, H, Nq, d)
-    qs = _rows(q, shape, dev, "q")
-    if out is None:
-        out = torch.empty(shape, dtype=_BF16, device=dev)
-        os_ = (H * Nq * d, Nq * d, d)
-    else:
-        os_ = _rows(out, shape, dev, "out")
-    if lse is None:
-        lse = torch.empty((B, H, Nq), dtype=_F32, device=dev)
-    elif lse.shape != shape[:3] or lse.dtype != _F32 or lse.device != dev or not lse.is_contiguous():
-        raise ValueError("lse must be contiguous fp32 [B, H, Nq] on the cache's device")
-    if workspace is None:
-        size = paged_workspace_bytes(B, H, c.H_kv, Nq, d, k_scale is not None)
-        workspace = torch.empty(max(1, size), dtype=torch.uint8, device=dev)
-    else:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be contiguous, on the cache's device")
-        size = workspace.numel() * workspace.element_size()
-    _launch(dev, "fa_fwd_paged" if k_scale is None else "fa_fwd_paged_fp8", c, q.data_ptr(), qs[0],
-            qs[1], qs[2], out.data_ptr(), os_[0], os_[1], os_[2], lse.data_ptr(), H, Nq,
-            1.0 / math.sqrt(d) if tau is None else float(tau), int(window), int(sinks),
-            workspace.data_ptr(), size)
-    return out, lse
+    return _lib.binding().fwd_paged(q, k_cache, v_cache, page_table, lens, tau, window, sinks, k_scale,
+                                    v_scale, out, lse, workspace)
 
 
 def last_device_error(device: Optional[torch.device] = None) -> int:

@@ -2,8 +2,9 @@
 
 nvcc compiles each translation unit for sm_103a in parallel and links them
 into ``_build/libfa_gb300.so`` inside the package (kept out of version
-control).  No cmake; a rebuild happens only when a source or header is newer
-than the library.
+control).  Beside it g++ compiles the torch binding of the paged entry points
+(csrc/torch_binding.cpp) against the running torch.  No cmake; a rebuild
+happens only when a source or header is newer than what was built.
 """
 from __future__ import annotations
 
@@ -31,6 +32,43 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found")
+
+
+BINDING_SRC = os.path.join(CSRC, "torch_binding.cpp")
+
+
+def binding_path() -> str:
+    """The binding's module file; a module built against one torch version does not
+    load in another, so the version is part of its name."""
+    import torch
+    return os.path.join(BUILD, f"fa_binding-{torch.__version__}.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """Compiles the torch binding (g++, about ten seconds)."""
+    import sysconfig
+
+    import torch
+    path = binding_path()
+    deps = [BINDING_SRC, os.path.join(INCLUDE, "fa.h")]
+    if not force and os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in deps):
+        return path
+    os.makedirs(BUILD, exist_ok=True)
+    root = os.path.join(os.path.dirname(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = f"{path}.tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    cmd += [f"-I{p}" for p in include]
+    cmd += [BINDING_SRC, "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_python", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{r.stderr}")
+    os.replace(tmp, path)
+    return path
 
 
 def _sources():

@@ -202,7 +202,9 @@ def test_workspace_given_or_taken_by_the_library():
     s = build([900, 5], 4, 2, 1, 64, 16, False, seed=11)
     want = run(s)
     dev = {n: t.to(DEV) for n, t in s.items() if t is not None}
-    c = api._paged_cache(dev["kc"], dev["vc"], dev["table"], dev["lens"], None, None)
+    P, Hkv, page, d = dev["kc"].shape
+    c = _lib.PagedCache(dev["kc"].data_ptr(), dev["vc"].data_ptr(), None, None, dev["table"].data_ptr(),
+                        dev["lens"].data_ptr(), 2, Hkv, d, P, page, dev["table"].shape[1])
     o, lse = torch.empty_like(dev["q"]), torch.empty(2, 4, 1, device=DEV)
     code = _lib.fa_fwd_paged(c, dev["q"].data_ptr(), *dev["q"].stride()[:3], o.data_ptr(), *o.stride()[:3], lse.data_ptr(),
                              4, 1, 0.125, 0, 0, None, 0, torch.cuda.current_stream().cuda_stream)
