@@ -59,7 +59,7 @@ SIGNATURES = {
     "fa_fwd_decode": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P]),
     "fa_kv_append": (_I, _APPEND),
     "fa_kv_append_fp8": (_I, _APPEND),
-    "fa_paged_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "fa_paged_workspace_size": (_SZ, [_C, _I, _I, _I, _I]),
     "fa_fwd_paged": (_I, _PAGED),
     "fa_fwd_paged_fp8": (_I, _PAGED),
     "fa_fwd_blocks": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P, _I, _P]),
@@ -197,8 +197,8 @@ def fa_kv_append_fp8(cache, k, k_st, k_sh, v, v_st, v_sh, T, cu_new, q, q_st, q_
                  q_out, qo_st, qo_sh, H, inv_freq, rot, interleaved, stream)
 
 
-def fa_paged_workspace_size(B, H, H_kv, Nq, d, fp8) -> int:
-    return int(_call("fa_paged_workspace_size", B, H, H_kv, Nq, d, fp8))
+def fa_paged_workspace_size(cache, H, Nq, window, sinks) -> int:
+    return int(_call("fa_paged_workspace_size", cache, H, Nq, window, sinks))
 
 
 def fa_fwd_paged(cache, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq, tau, window, sinks,

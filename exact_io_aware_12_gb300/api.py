@@ -242,8 +242,15 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
                                     interleaved, k_scale, v_scale, q_out)
 
 
-def paged_workspace_bytes(B: int, H: int, H_kv: int, Nq: int, d: int, fp8: bool = False) -> int:
-    return _lib.fa_paged_workspace_size(B, H, H_kv, Nq, d, int(bool(fp8)))
+def paged_workspace_bytes(q: torch.Tensor, k_cache: torch.Tensor, page_table: torch.Tensor,
+                          window: Optional[int] = None, sinks: int = 0) -> int:
+    """Bytes of workspace that ``fwd_paged`` takes for tensors of these sizes."""
+    B, H, Nq, d = q.shape
+    P, Hkv, page, _ = k_cache.shape
+    fp8 = k_cache.dtype != torch.bfloat16
+    c = _lib.PagedCache(None, None, 1 if fp8 else None, None, None, None, B, Hkv, d, P, page,
+                        page_table.shape[1])
+    return _lib.fa_paged_workspace_size(c, H, Nq, window or 0, sinks)
 
 
 def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,

@@ -572,6 +572,13 @@ static bool strided_distinct(const long long n[3], const long long st[3], int d)
     return true;
 }
 
+// log2 of a page size that the kernels take.
+static bool page_shift(int page_size, int* shift) {
+    *shift = 0;
+    while ((1 << *shift) < page_size && *shift < 30) ++*shift;
+    return page_size == 1 << *shift && page_size >= kPagedMinPage && page_size <= kPagedMaxPage;
+}
+
 // Checks a cache's description and fills the internal form.  fp8 says what the entry
 // point takes.  Sets *bytes (of K, and of V).
 static fa_status check_cache(const fa_paged_cache* c, bool fp8, PagedCache* out, size_t* bytes) {
@@ -585,8 +592,7 @@ static fa_status check_cache(const fa_paged_cache* c, bool fp8, PagedCache* out,
     out->max_pages = c->max_pages;
     if (c->B == 0 || c->H_kv == 0) return FA_OK;  // empty: the caller returns
     if (c->d != 64 && c->d != 128) return FA_ERR_UNSUPPORTED;
-    if (c->page_size < kPagedMinPage || c->page_size > kPagedMaxPage || (c->page_size & (c->page_size - 1)) != 0)
-        return FA_ERR_UNSUPPORTED;
+    if (!page_shift(c->page_size, &out->shift)) return FA_ERR_UNSUPPORTED;
     if (c->num_pages == 0 || c->max_pages == 0) return FA_ERR_INVALID_ARG;
     if (static_cast<long long>(c->max_pages) * c->page_size > kPagedMaxKeys) return FA_ERR_UNSUPPORTED;
     if (c->K == nullptr || c->V == nullptr || c->page_table == nullptr || c->lens == nullptr) return FA_ERR_INVALID_ARG;
@@ -603,8 +609,6 @@ static fa_status check_cache(const fa_paged_cache* c, bool fp8, PagedCache* out,
     out->v_scale = c->v_scale;
     out->page_table = c->page_table;
     out->lens = c->lens;
-    out->shift = 0;
-    while ((1 << out->shift) < c->page_size) ++out->shift;
     return FA_OK;
 }
 
@@ -695,10 +699,21 @@ fa_status fa_kv_append_fp8(const fa_paged_cache* cache, const void* k, long long
                          qo_st, qo_sh, H, inv_freq, rot, interleaved, stream);
 }
 
-size_t fa_paged_workspace_size(int B, int H, int H_kv, int Nq, int d, int fp8) {
-    if (B <= 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 || Nq <= 0 || Nq > 8 || (d != 64 && d != 128)) return 0;
-    if (H / H_kv > (1 << 20)) return 0;
-    return paged_workspace(B, H, H_kv, Nq, d, fp8 != 0);
+// A window or a number of sinks beyond any length, cut to what the kernels' integers hold
+// (the same keys are visible).
+static int cut_keys(int x) { return x < (1 << 30) ? x : (1 << 30); }
+
+size_t fa_paged_workspace_size(const fa_paged_cache* cache, int H, int Nq, int window, int sinks) {
+    if (cache == nullptr || H <= 0 || Nq <= 0 || Nq > 8 || window < 0 || sinks < 0) return 0;
+    if (cache->B <= 0 || cache->H_kv <= 0 || H % cache->H_kv != 0 || H / cache->H_kv > (1 << 20)) return 0;
+    if ((cache->d != 64 && cache->d != 128) || cache->max_pages <= 0) return 0;
+    PagedCache c;
+    if (!page_shift(cache->page_size, &c.shift)) return 0;
+    c.B = cache->B;
+    c.H_kv = cache->H_kv;
+    c.d = cache->d;
+    c.max_pages = cache->max_pages;
+    return paged_workspace(c, H, Nq, cut_keys(window), cut_keys(sinks), cache->k_scale != nullptr);
 }
 
 static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, long long q_sb,
@@ -721,7 +736,7 @@ static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, 
     const long long n[3] = {c->B, H, Nq}, q_strides[3] = {q_sb, q_sh, q_sn}, o_strides[3] = {o_sb, o_sh, o_sn};
     const long long qs = strided_span(n, q_strides, c->d), os = strided_span(n, o_strides, c->d);
     if (qs < 0 || os < 0 || !strided_distinct(n, o_strides, c->d)) return FA_ERR_INVALID_ARG;
-    const size_t need = fa_paged_workspace_size(c->B, H, c->H_kv, Nq, c->d, fp8);
+    const size_t need = fa_paged_workspace_size(c, H, Nq, window, sinks);
     if (workspace != nullptr && workspace_bytes < need) return FA_ERR_WORKSPACE;
     const size_t lb = static_cast<size_t>(c->B) * H * Nq * 4, tb = static_cast<size_t>(c->B) * c->max_pages * 4;
     const size_t sb = fp8 ? static_cast<size_t>(c->num_pages) * c->H_kv * 4 : 0;
@@ -730,7 +745,7 @@ static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, 
                                static_cast<size_t>(c->B) * 4, sb, sb};
     const void* outs[] = {O, LSE, workspace};
     const size_t out_bytes[] = {static_cast<size_t>(os) * 2, lb, need};
-    for (int o = 0; o < (workspace ? 3 : 2); ++o) {
+    for (int o = 0; o < (workspace && need > 0 ? 3 : 2); ++o) {
         for (int i = 0; i < (fp8 ? 7 : 5); ++i)
             if (overlaps(outs[o], out_bytes[o], ins[i], in_bytes[i])) return FA_ERR_INVALID_ARG;
         for (int o2 = 0; o2 < o; ++o2)
@@ -739,8 +754,9 @@ static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, 
     DeviceInfo* di = current_device(&s);
     if (!di) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    void* ws = workspace;
-    if (ws == nullptr && cudaMallocAsync(&ws, need, st) != cudaSuccess) {
+    void* ws = need > 0 ? workspace : nullptr;
+    const bool own = need > 0 && workspace == nullptr;
+    if (own && cudaMallocAsync(&ws, need, st) != cudaSuccess) {
         cudaGetLastError();
         return FA_ERR_CUDA;
     }
@@ -756,14 +772,14 @@ static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, 
     a.o_sn = o_sn;
     a.H = H;
     a.Nq = Nq;
-    a.window = window < (1 << 30) ? window : (1 << 30);  // (a length is below 2^31: the same keys)
-    a.sinks = sinks < (1 << 30) ? sinks : (1 << 30);
+    a.window = cut_keys(window);
+    a.sinks = cut_keys(sinks);
     a.tau = tau;
     a.err = di->err_word;
     a.ev_start = t_ev_start;
     a.ev_stop = t_ev_stop;
     const cudaError_t e = launch_fwd_paged(a, st);
-    if (workspace == nullptr) cudaFreeAsync(ws, st);
+    if (own) cudaFreeAsync(ws, st);
     return map_cuda(e);
 }
 

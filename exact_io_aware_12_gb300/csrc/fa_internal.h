@@ -142,8 +142,9 @@ struct PagedArgs {
     cudaEvent_t ev_start;  // optional: recorded around the two kernels
     cudaEvent_t ev_stop;
 };
-// Bytes of workspace one such step takes, whatever the sequences' lengths.
-size_t paged_workspace(int B, int H, int H_kv, int Nq, int d, bool fp8);
+// Bytes of workspace one such step takes, whatever the sequences' lengths (only the
+// cache's sizes are looked at).
+size_t paged_workspace(const PagedCache& c, int H, int Nq, int window, int sinks, bool fp8);
 // 16-key tiles that full tables hold, which 32-bit counts must not pass.
 long long paged_max_tiles(int B, int H, int H_kv, int Nq, int max_pages, int shift);
 

@@ -64,16 +64,16 @@ enum : uint32_t { kSitePagedSmem = 51 };
 
 // Ring slots per warp and CTAs per SM: about 128 KB in flight per SM, as much as the
 // copy bandwidth times the memory's latency asks for (45 GB/s x ~1.5 us per SM).
-template <int D, int NT, bool F8>
+template <int D, int NT, bool F8, bool WHOLE = false>
 struct PagedLayout {
     static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a key row
     static constexpr int kTile = kPagedTile * kRow;     // K or V of one tile
     static constexpr int TP = kTile == 4096 ? 1 : 2;    // tiles per slot and loop iteration
     static constexpr int kSlot = 2 * TP * kTile;
-    static constexpr int kCtas = kSlot == 8192 ? 2 : 3;
-    static constexpr int kStages = kSlot == 8192 ? 3 : 4;
+    static constexpr int kCtas = WHOLE && NT == 1 ? (kSlot == 8192 ? 3 : 4) : kSlot == 8192 ? 2 : 3;
+    static constexpr int kStages = WHOLE && NT == 1 ? (kSlot == 8192 ? 2 : 3) : kSlot == 8192 ? 3 : 4;
     static constexpr int kWarpRing = kStages * kSlot;
-    static constexpr int kBytes = kPagedWarps * kWarpRing + 1024;  // + PagedShared
+    static constexpr int kBytes = kPagedWarps * kWarpRing + 2048;  // + PagedShared
 };
 constexpr int kMinTiles = 2;  // per warp: below, its start and end cost more than they save
 constexpr int kMaxResults = 512;  // pieces of a segment: more cost the combine kernel more than they save
@@ -213,13 +213,16 @@ struct PagedShared {
     } slot[kPagedWarps][4][2];  // [warp][ring slot][tile]
     int scan[kPagedWarps];
     int at_b[kPagedWarps], at_before[kPagedWarps];  // a share's first sequence, tiles of those before it
+    float m[kPagedWarps][16], l[kPagedWarps][16];   // WHOLE: each warp's running max and sum
 };
+constexpr int kSharedBytes = 2048;
+static_assert(sizeof(PagedShared) <= kSharedBytes, "the shared block fits its place");
 
-static_assert(sizeof(PagedShared) <= 1024, "the shared block fits its place");
-
-template <int D, int NT, bool F8>
-__global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_paged_kernel(const PagedParams p) {
-    using L = PagedLayout<D, NT, F8>;
+// WHOLE: a block takes one segment, its warps the tiles in turn, and joins their results
+// in shared memory: no partial results, no second kernel.  For short segments.
+template <int D, int NT, bool F8, bool WHOLE>
+__global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8, WHOLE>::kCtas) fa_paged_kernel(const PagedParams p) {
+    using L = PagedLayout<D, NT, F8, WHOLE>;
     constexpr int ROW = L::kRow, CH = ROW / 16, S = L::kStages, TP = L::TP;
     using W = Swizzle<ROW>;
     constexpr int R = 8 * NT;           // query rows of a segment
@@ -235,70 +238,82 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
         return;
     }
     const uint32_t k_dst = W::k_dst(lane), v_dst = W::v_dst(lane), k_src = W::k_src(g, t4), v_src = W::v_src(g, t4);
-    griddep_launch_dependents();
-
-    // ---- this warp's share of the tiles ----
     const int segs_per_b = p.H_kv * p.rgroups;
-    const int per = (p.B + kThreads - 1) / kThreads;
-    int mine = 0;
-    for (int i = 0; i < per; ++i) {
-        const int b = tid * per + i;
-        if (b < p.B) mine += paged_tiles(paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks));
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    if (lane == 31) sh.scan[warp] = incl;
-    __syncthreads();
-    int total_b = 0, before = incl - mine;
-#pragma unroll
-    for (int w = 0; w < kPagedWarps; ++w) {
-        if (w < warp) before += sh.scan[w];
-        total_b += sh.scan[w];
-    }
-    const uint32_t total = static_cast<uint32_t>(total_b) * segs_per_b, segs = static_cast<uint32_t>(p.B) * segs_per_b;
-    const int per_cta = kPagedWarps / p.rwarps;  // shares of a CTA
-    // (no share is empty: with few tiles the last warps have none)
-    const uint32_t shares = max(1u, min(min(gridDim.x * per_cta, total / kMinTiles), segs * kMaxResults));
-    const Shares cut(total, shares);
-    for (int w = 0; w < per_cta; ++w) {
-        const uint32_t c = blockIdx.x * per_cta + w;
-        if (c >= shares) break;
-        // the whole sequences' tiles before the share's first, rounded down
-        const int xs = static_cast<int>(cut.start(c) / segs_per_b);
-        if (xs >= before && xs < before + mine) {
-            int b = tid * per, at = before;
-            for (;; ++b) {
-                const int n = paged_tiles(paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks));
-                if (xs < at + n) break;
-                at += n;
-            }
-            sh.at_b[w] = b;
-            sh.at_before[w] = at;
+    // what this warp works on: its share of the tiles [x, x_end), from sequence b on, or (WHOLE)
+    // every iw-th tile of one segment, from `turn` on; rows of row warp rw
+    uint32_t share = 0, x = 0, x_end = 0, b_first = 0;
+    int b = 0, rw = 0, turn = 0, iw = 1;
+    Shares cut(1u, 1u);
+    if constexpr (WHOLE) {
+        b = static_cast<int>(blockIdx.x) / segs_per_b;
+        iw = kPagedWarps / p.rwarps;
+        rw = warp % p.rwarps;
+        turn = warp / p.rwarps;
+    } else {
+        griddep_launch_dependents();
+        // ---- this warp's share of the tiles ----
+        const int per = (p.B + kThreads - 1) / kThreads;
+        int mine = 0;
+        for (int i = 0; i < per; ++i) {
+            const int b = tid * per + i;
+            if (b < p.B) mine += paged_tiles(paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks));
         }
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) sh.scan[warp] = incl;
+        __syncthreads();
+        int total_b = 0, before = incl - mine;
+#pragma unroll
+        for (int w = 0; w < kPagedWarps; ++w) {
+            if (w < warp) before += sh.scan[w];
+            total_b += sh.scan[w];
+        }
+        const uint32_t total = static_cast<uint32_t>(total_b) * segs_per_b, segs = static_cast<uint32_t>(p.B) * segs_per_b;
+        const int per_cta = kPagedWarps / p.rwarps;  // shares of a CTA
+        // (no share is empty: with few tiles the last warps have none)
+        const uint32_t shares = max(1u, min(min(gridDim.x * per_cta, total / kMinTiles), segs * kMaxResults));
+        cut = Shares(total, shares);
+        for (int w = 0; w < per_cta; ++w) {
+            const uint32_t c = blockIdx.x * per_cta + w;
+            if (c >= shares) break;
+            // the whole sequences' tiles before the share's first, rounded down
+            const int xs = static_cast<int>(cut.start(c) / segs_per_b);
+            if (xs >= before && xs < before + mine) {
+                int b = tid * per, at = before;
+                for (;; ++b) {
+                    const int n = paged_tiles(paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks));
+                    if (xs < at + n) break;
+                    at += n;
+                }
+                sh.at_b[w] = b;
+                sh.at_before[w] = at;
+            }
+        }
+        __syncthreads();
+        const int wshare = warp / p.rwarps;
+        rw = warp - wshare * p.rwarps;
+        share = blockIdx.x * per_cta + wshare;
+        if (share >= shares) return;  // (from here on the warps go their own ways)
+        x = cut.start(share);
+        x_end = cut.start(share + 1);
+        b = sh.at_b[wshare];
+        b_first = static_cast<uint32_t>(sh.at_before[wshare]) * segs_per_b;  // first tile of sequence b
     }
-    __syncthreads();
-    const int wshare = warp / p.rwarps, rw = warp - wshare * p.rwarps;
-    const uint32_t share = blockIdx.x * per_cta + wshare;
-    if (share >= shares) return;  // (from here on the warps go their own ways)
-    uint32_t x = cut.start(share);
-    const uint32_t x_end = cut.start(share + 1);
-    int b = sh.at_b[wshare];
-    uint32_t b_first = static_cast<uint32_t>(sh.at_before[wshare]) * segs_per_b;  // first tile of sequence b
     PagedRange rg = paged_range(clamp_len(p, b), p.Nq, p.window, p.sinks);
     uint32_t tiles = paged_tiles(rg);
 
     while (true) {
         // ---- one piece: tiles [u0, u1) of segment (b, hk, rb group) ----
-        const int in_b = static_cast<int>((x - b_first) / tiles);
-        const uint32_t seg_first = b_first + in_b * tiles;
+        const int in_b = WHOLE ? static_cast<int>(blockIdx.x) - b * segs_per_b : static_cast<int>((x - b_first) / tiles);
+        [[maybe_unused]] const uint32_t seg_first = b_first + in_b * tiles;
         const int hk = in_b / p.rgroups;
-        const int u0 = static_cast<int>(x - seg_first);
-        const int u1 = static_cast<int>(min(tiles, x_end - seg_first));
-        const auto next = [&]() {  // on to the next segment; false at the share's end
+        const int u0 = WHOLE ? 0 : static_cast<int>(x - seg_first);
+        const int u1 = WHOLE ? rg.n : static_cast<int>(min(tiles, x_end - seg_first));
+        [[maybe_unused]] const auto next = [&]() {  // on to the next segment; false at the share's end
             x = seg_first + u1;
             if (x >= x_end) return false;
             if (x >= b_first + tiles * segs_per_b) {
@@ -309,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
             }
             return true;
         };
-        if (u0 > 0 && u0 >= rg.n) {  // only a segment's empty tiles
+        if (!WHOLE && u0 > 0 && u0 >= rg.n) {  // only a segment's empty tiles
             if (!next()) return;
             continue;
         }
@@ -317,7 +332,9 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
         // row r of this warp: head hk G + (row0 + r) / Nq, position (row0 + r) % Nq
         const int row0 = ((in_b - hk * p.rgroups) * p.rwarps + rw) * R;
         const int rows = min(R, p.G * p.Nq - row0);  // (none for the last warps of a share)
-        const int nv = rows > 0 ? max(0, min(u1, rg.n) - u0) : 0;
+        // this warp's tiles: entries entry(0) .. entry(nv - 1) of the sequence's list
+        const int nv = rows <= 0 ? 0 : WHOLE ? max(0, (rg.n - turn + iw - 1) / iw) : max(0, min(u1, rg.n) - u0);
+        const auto entry = [&](int i) { return WHOLE ? turn + i * iw : u0 + i; };
         const int* table = p.table + static_cast<long long>(b) * p.max_pages;
 
         // pages of 32 tiles at a time, one per lane; the next 32 are fetched halfway
@@ -327,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
             const int i = base + lane;
             page = -1;
             if (i < nv) {
-                page = page_of(table, p.max_pages, p.num_pages, p.shift, rg.key0(u0 + i));
+                page = page_of(table, p.max_pages, p.num_pages, p.shift, rg.key0(entry(i)));
                 if (page < 0) atomicCAS(p.err, 0u, kErrPage);
                 if constexpr (F8) {
                     if (page >= 0) {
@@ -353,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
                     vs = vs_next;
                 }
                 if ((i & 31) == 16) fetch((i & ~31) + 32, pg_next, ks_next, vs_next);
-                const int key0 = rg.key0(u0 + i);
+                const int key0 = rg.key0(entry(i));
                 const int page = __shfl_sync(0xffffffffu, pg, i & 31);  // (-1 behind the piece's last tile, too)
                 const uint32_t dst = ring + in_slot * L::kSlot + tp * 2 * L::kTile;
                 typename PagedShared::Slot sl;
@@ -675,6 +692,66 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
         }
         cp_wait<0>();
 
+        if constexpr (WHOLE) {
+            // ---- join the warps of the same rows ----
+            // factor of this warp's sums: 2^(its reference - the joint max) / the joint sum
+            float f[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float l = sum_over_g(l_run[nt][e]);
+                    if (g == 0) {
+                        sh.m[warp][nt * 8 + 2 * t4 + e] = m_run[nt][e];
+                        sh.l[warp][nt * 8 + 2 * t4 + e] = l;
+                    }
+                }
+            __syncthreads();  // (and every warp is done with its ring)
+            float* red = reinterpret_cast<float*>(smem);  // [warp][R][D]
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = nt * 8 + 2 * t4 + e;
+                    float m = -INFINITY, l = 0.f;
+                    for (int k = 0; k < iw; ++k) m = fmaxf(m, sh.m[k * p.rwarps + rw][r]);
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    for (int k = 0; k < iw; ++k) l += sh.l[k * p.rwarps + rw][r] * ex2(sh.m[k * p.rwarps + rw][r] - ref);
+                    // (a row that sees nothing: l = 0 and O = 0, LSE = -inf; NaN where a score was)
+                    for (int k = 0; m == -INFINITY && k < iw; ++k) l += sh.l[k * p.rwarps + rw][r];
+                    f[nt][e] = l == 0.f ? 0.f : ex2((F8 ? mv_run[nt][e] : m_run[nt][e]) - ref) / l;
+                    if (turn == 0 && g == 0 && r < rows) {
+                        const int hh = (row0 + r) / p.Nq, qi = (row0 + r) - hh * p.Nq, h = hk * p.G + hh;
+                        p.LSE[(static_cast<long long>(b) * p.H + h) * p.Nq + qi] = (ref + lg2(l)) * kLn2;
+                    }
+                    constexpr int RUN = F8 ? D / 8 : 8;  // columns that lie together
+                    float* dst = red + (warp * R + r) * D;
+#pragma unroll
+                    for (int j = 0; j < MT; j += 2) {
+                        const int col = (2 * j / RUN) * (8 * RUN) + RUN * g + 2 * j % RUN;
+                        *reinterpret_cast<float4*>(dst + col) =
+                            make_float4(acc[nt][j][e] * f[nt][e], acc[nt][j][e + 2] * f[nt][e],
+                                        acc[nt][j + 1][e] * f[nt][e], acc[nt][j + 1][e + 2] * f[nt][e]);
+                    }
+                }
+            __syncthreads();
+            // the iw warps of row warp rw write its rows
+            for (int i = turn * 32 + lane; i < rows * (D / 4); i += iw * 32) {
+                const int r = i / (D / 4), col = i % (D / 4) * 4;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < iw; ++k) {
+                    const float4 y = *reinterpret_cast<const float4*>(red + ((k * p.rwarps + rw) * R + r) * D + col);
+                    o.x += y.x;
+                    o.y += y.y;
+                    o.z += y.z;
+                    o.w += y.w;
+                }
+                const int hh = (row0 + r) / p.Nq, qi = (row0 + r) - hh * p.Nq, h = hk * p.G + hh;
+                *reinterpret_cast<uint2*>(p.O + b * p.o_sb + static_cast<long long>(h) * p.o_sh + qi * p.o_sn + col) =
+                    make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+            }
+            return;
+        }
         // ---- this piece's result ----
         const bool final_piece = u0 == 0 && u1 >= rg.n;
         const long long slot = 2ll * (static_cast<long long>(blockIdx.x) * kPagedWarps + warp) + (u0 == 0 ? 1 : 0);
@@ -864,39 +941,59 @@ int ctas_for(int d, int nt, bool fp8) {
     return fp8 ? ctas_per_sm<128, 2, true>() : ctas_per_sm<128, 2, false>();
 }
 
-// Workspace: segment headers, then the pieces' sums and outputs, each 256-aligned.
+// Whole segments up to this many tiles (of a full table, within the window; the row warps
+// share a block's four): ten per warp.
+constexpr int kWholeTiles = 40;
+
+// Workspace: segment headers, then the pieces' sums and outputs, each 256-aligned; none
+// for whole segments.
 struct PagedPlan {
     int nt, rwarps, rgroups, ctas;
-    long long segs;
+    bool whole;
+    long long segs, tiles;  // tiles: of a full table, all segments
     size_t part_l, part_o, bytes;
 };
-PagedPlan paged_plan(int B, int H, int H_kv, int Nq, int d, bool fp8) {
+PagedPlan paged_plan(const PagedCache& c, int H, int Nq, int window, int sinks, bool fp8) {
     const auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     PagedPlan pl;
-    const int rows = H / H_kv * Nq;
+    const int rows = H / c.H_kv * Nq;
     pl.nt = row_tiles(rows);
     const int rblocks = (rows + 8 * pl.nt - 1) / (8 * pl.nt);
     pl.rwarps = rblocks == 1 ? 1 : rblocks == 2 ? 2 : 4;
     pl.rgroups = (rblocks + pl.rwarps - 1) / pl.rwarps;
-    pl.segs = static_cast<long long>(B) * H_kv * pl.rgroups;
-    pl.ctas = kSms * ctas_for(d, pl.nt, fp8);
-    const size_t part_rows = static_cast<size_t>(2) * kPagedWarps * pl.ctas * 8 * pl.nt;
-    pl.part_l = up(static_cast<size_t>(pl.segs) * sizeof(int2));
+    pl.segs = static_cast<long long>(c.B) * c.H_kv * pl.rgroups;
+    pl.ctas = kSms * ctas_for(c.d, pl.nt, fp8);
+    // a full table's tiles, or with a window those of a long sequence (its ends may cut tiles)
+    long long most = (static_cast<long long>(c.max_pages) << c.shift) / kPagedTile;
+    if (window > 0)
+        most = std::min(most, (static_cast<long long>(window) + Nq) / kPagedTile + 2 + (sinks + kPagedTile - 1ll) / kPagedTile);
+    pl.tiles = pl.segs * most;
+    pl.whole = most * pl.rwarps <= kWholeTiles;
+    const size_t part_rows = pl.whole ? 0 : static_cast<size_t>(2) * kPagedWarps * pl.ctas * 8 * pl.nt;
+    pl.part_l = pl.whole ? 0 : up(static_cast<size_t>(pl.segs) * sizeof(int2));
     pl.part_o = pl.part_l + up(part_rows * sizeof(float));
-    pl.bytes = pl.part_o + part_rows * d * sizeof(float);
+    pl.bytes = pl.part_o + part_rows * c.d * sizeof(float);
     return pl;
 }
 
 template <int D, int NT, bool F8>
 cudaError_t launch_paged_t(const PagedArgs& a, const PagedPlan& pl, PagedParams& p, cudaStream_t stream) {
     using L = PagedLayout<D, NT, F8>;
-    constexpr auto kern = &fa_paged_kernel<D, NT, F8>;
-    cudaError_t e = set_max_dyn_smem_once<kern>(L::kBytes);
+    constexpr auto kern = &fa_paged_kernel<D, NT, F8, false>;
+    constexpr auto kern_w = &fa_paged_kernel<D, NT, F8, true>;
+    using LW = PagedLayout<D, NT, F8, true>;
+    cudaError_t e = pl.whole ? set_max_dyn_smem_once<kern_w>(LW::kBytes) : set_max_dyn_smem_once<kern>(L::kBytes);
     if (e != cudaSuccess) return e;
+    if (pl.whole) {
+        if (a.ev_start) cudaEventRecord(a.ev_start, stream);
+        kern_w<<<static_cast<unsigned>(pl.segs), kThreads, LW::kBytes, stream>>>(p);
+        e = cudaGetLastError();
+        if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
+        return e;
+    }
     if (a.ev_start) cudaEventRecord(a.ev_start, stream);
     // (no more CTAs than a full table gives kMinTiles per warp)
-    const long long most = pl.segs * ((static_cast<long long>(p.max_pages) << p.shift) / kPagedTile) * pl.rwarps;
-    const int ctas = static_cast<int>(std::min<long long>(pl.ctas, most / (kMinTiles * kPagedWarps) + 1));
+    const int ctas = static_cast<int>(std::min<long long>(pl.ctas, pl.tiles * pl.rwarps / (kMinTiles * kPagedWarps) + 1));
     kern<<<static_cast<unsigned>(ctas), kThreads, L::kBytes, stream>>>(p);
     e = cudaGetLastError();
     // pieces of an average segment: few, a block with a warp per row; many, a block per row
@@ -913,8 +1010,8 @@ cudaError_t launch_paged_t(const PagedArgs& a, const PagedPlan& pl, PagedParams&
 
 }  // namespace
 
-size_t paged_workspace(int B, int H, int H_kv, int Nq, int d, bool fp8) {
-    return paged_plan(B, H, H_kv, Nq, d, fp8).bytes;
+size_t paged_workspace(const PagedCache& c, int H, int Nq, int window, int sinks, bool fp8) {
+    return paged_plan(c, H, Nq, window, sinks, fp8).bytes;
 }
 
 long long paged_max_tiles(int B, int H, int H_kv, int Nq, int max_pages, int shift) {
@@ -924,7 +1021,7 @@ long long paged_max_tiles(int B, int H, int H_kv, int Nq, int max_pages, int shi
 
 cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream) {
     const bool fp8 = a.cache.k_scale != nullptr;
-    const PagedPlan pl = paged_plan(a.cache.B, a.H, a.cache.H_kv, a.Nq, a.cache.d, fp8);
+    const PagedPlan pl = paged_plan(a.cache, a.H, a.Nq, a.window, a.sinks, fp8);
     PagedParams p;
     p.Q = static_cast<const __nv_bfloat16*>(a.Q);
     p.K = static_cast<const uint8_t*>(a.cache.K);

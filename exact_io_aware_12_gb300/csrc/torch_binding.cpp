@@ -230,12 +230,12 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
             require(ws->device() == c.dev && ws->is_contiguous(), "workspace must be contiguous, on the cache's device");
             bytes = ws->nbytes();
         } else {
-            bytes = g_workspace(c.c.B, to_int(H), c.c.H_kv, to_int(Nq), c.c.d, c.fp8);
-            ws = &made_ws.emplace(at::empty({static_cast<int64_t>(bytes ? bytes : 1)}, q.options().dtype(at::kByte)));
+            bytes = g_workspace(&c.c, to_int(H), to_int(Nq), window, sinks);
+            if (bytes) ws = &made_ws.emplace(at::empty({static_cast<int64_t>(bytes)}, q.options().dtype(at::kByte)));
         }
         check_status(g_paged[c.fp8](&c.c, q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), out->data_ptr(),
                                     out->stride(0), out->stride(1), out->stride(2), static_cast<float*>(lse->data_ptr()),
-                                    to_int(H), to_int(Nq), static_cast<float>(tau), window, sinks, ws->data_ptr(), bytes,
+                                    to_int(H), to_int(Nq), static_cast<float>(tau), window, sinks, ws ? ws->data_ptr() : nullptr, bytes,
                                     c10::cuda::getCurrentCUDAStream(c.dev.index()).stream()),
                      c.fp8 ? "fa_fwd_paged_fp8" : "fa_fwd_paged");
         PyObject* o = made_out ? THPVariable_Wrap(*made_out) : Py_NewRef(a[10]);

@@ -330,19 +330,20 @@ FA_API fa_status fa_kv_append_fp8(const fa_paged_cache* cache, const void* k, lo
  * rows must not overlap.  LSE: fp32 [B][H][Nq] contiguous.  window = 0: none;
  * sinks > 0 needs a window.  Rows of a page behind a sequence's end, and keys hidden
  * from every row of the call, are never read.
- * workspace: fa_paged_workspace_size bytes (it does not depend on the lengths); NULL:
- * taken with cudaMallocAsync and given back.  Two calls that may run at the same time
+ * workspace: fa_paged_workspace_size bytes (from the sizes alone, not the lengths; 0 for
+ * small tables); NULL: taken with cudaMallocAsync and given back.  Two calls that may run at the same time
  * need two workspaces.  A length out of bounds is cut to the table's, and keys on a
  * page out of bounds are hidden (FA_ERR_PAGE).  More than 2^31 16-key tiles in full
  * tables (of all sequences, key heads and 64 query rows) are FA_ERR_UNSUPPORTED.
  */
-FA_API size_t fa_paged_workspace_size(int B, int H, int H_kv, int Nq, int d, int fp8);
+FA_API size_t fa_paged_workspace_size(const fa_paged_cache* cache, int H, int Nq, int window,
+                                      int sinks);
 FA_API fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* Q, long long q_sb,
                               long long q_sh, long long q_sn, void* O, long long o_sb, long long o_sh,
                               long long o_sn, float* LSE, int H, int Nq, float tau, int window,
                               int sinks, void* workspace, size_t workspace_bytes, void* stream);
 
-/* fa_fwd_paged over an e4m3 cache (workspace: fa_paged_workspace_size with fp8 = 1). */
+/* fa_fwd_paged over an e4m3 cache. */
 FA_API fa_status fa_fwd_paged_fp8(const fa_paged_cache* cache, const void* Q, long long q_sb,
                                   long long q_sh, long long q_sn, void* O, long long o_sb,
                                   long long o_sh, long long o_sn, float* LSE, int H, int Nq,

@@ -187,7 +187,7 @@ def test_strides_orders_and_given_buffers(fp8):
         dev = wide.to(DEV)[..., :d].permute(inv)
         out = torch.full(wide.shape, 3.0, dtype=torch.bfloat16, device=DEV)
         lse = torch.empty(B, H, Nq, device=DEV)
-        ws = torch.empty(api.paged_workspace_bytes(B, H, 2, Nq, d, fp8), dtype=torch.uint8, device=DEV)
+        ws = torch.empty(max(1, api.paged_workspace_bytes(s["q"], s["kc"], s["table"])), dtype=torch.uint8, device=DEV)
         d2 = {n: (t.to(DEV) if t is not None else None) for n, t in s.items()}
         o, l = api.fwd_paged(dev, d2["kc"], d2["vc"], d2["table"], d2["lens"], k_scale=d2["k_scale"],
                              v_scale=d2["v_scale"], out=out[..., :d].permute(inv), lse=lse, workspace=ws)
@@ -332,7 +332,8 @@ def test_generation_append_then_attend(fp8):
         for b in range(B):
             keys[b].append(x[int(cu[b]):int(cu[b + 1])])
     x = torch.zeros(B, H + 2 * Hkv, d, dtype=torch.bfloat16, device=DEV)
-    ws = torch.empty(api.paged_workspace_bytes(B, H, Hkv, 1, d, fp8), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(max(1, api.paged_workspace_bytes(torch.empty(B, H, 1, d), kc, table, window, sinks)),
+                     dtype=torch.uint8, device=DEV)
 
     def step():
         q = api.kv_append(x[:, H:H + Hkv], x[:, H + Hkv:], kc, vc, table, lens, q=x[:, :H], inv_freq=f, **sc)

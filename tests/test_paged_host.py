@@ -149,7 +149,7 @@ def test_units_fit_every_split_of_tokens(shim):
 
 def cache(fp8=False, **kw):
     c = dict(K=FAKE, V=FAKE + GB, k_scale=FAKE + 2 * GB if fp8 else None, v_scale=FAKE + 3 * GB if fp8 else None,
-             page_table=FAKE + 4 * GB, lens=FAKE + 5 * GB, B=2, H_kv=2, d=64, num_pages=8, page_size=16, max_pages=4)
+             page_table=FAKE + 4 * GB, lens=FAKE + 5 * GB, B=2, H_kv=2, d=64, num_pages=8, page_size=16, max_pages=400)
     c.update(kw)
     return _lib.PagedCache(*(c[n] for n, _ in _lib.PagedCache._fields_))
 
@@ -276,12 +276,18 @@ def test_too_many_tiles_are_refused():
     assert paged(cache(B=4096, H_kv=2, max_pages=2 ** 22)) == _lib.FA_ERR_UNSUPPORTED
 
 
-def test_workspace_size_does_not_depend_on_lengths():
-    a = _lib.fa_paged_workspace_size(4, 8, 2, 1, 128, 0)
-    assert a > 0 and a % 256 == 0
-    assert _lib.fa_paged_workspace_size(4, 8, 3, 1, 128, 0) == 0
-    assert _lib.fa_paged_workspace_size(4, 8, 2, 9, 128, 0) == 0
-    assert _lib.fa_paged_workspace_size(0, 8, 2, 1, 128, 0) == 0
+def test_workspace_sizes():
+    size = lambda H=8, Nq=1, window=0, sinks=0, **kw: _lib.fa_paged_workspace_size(
+        cache(**dict(dict(max_pages=4096), **kw)), H, Nq, window, sinks)
+    assert size() > 0 and size(fp8=True) > 0
+    assert size(max_pages=4) == 0                     # short tables need none
+    assert size(window=100, sinks=4) == 0             # nor short windows
+    for bad in (dict(H=3), dict(Nq=9), dict(B=0), dict(d=96), dict(page_size=48), dict(window=-1), dict(H=0)):
+        assert size(**bad) == 0
+    assert _lib.fa_paged_workspace_size(None, 8, 1, 0, 0) == 0
+    q, kc = torch.empty(2, 8, 1, 64, dtype=torch.bfloat16), torch.empty(8, 2, 16, 64, dtype=torch.bfloat16)
+    assert api.paged_workspace_bytes(q, kc, torch.empty(2, 4096)) == size()
+    assert api.paged_workspace_bytes(q, kc.to(torch.uint8), torch.empty(2, 4096)) == size(fp8=True)
 
 
 @pytest.mark.parametrize("kw,code", [
