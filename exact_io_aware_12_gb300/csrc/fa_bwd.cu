@@ -184,7 +184,7 @@ struct BwdParams {
     uint8_t* plan;                  // block mask: the split plan's buffer (layout: split_layout)
     int plan_tiles;                 // its key tiles (BH * n_kv; sinks: those that hold them, per head), 0: no plan
     int plan_help;                  // its helper CTAs, launched first
-    int plan_chunks;                // sinks: chunks of each tile that holds sinks
+    int plan_chunks;                // sinks: chunks of each tile that holds sinks (persistent: its cells)
     size_t plan_part;               // sinks: the slots' offset in the buffer
 };
 
@@ -267,7 +267,7 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     static_assert(sizeof(BwdBarriers) <= L::kBytes - L::kBars, "barrier block overflows its slot");
     static_assert(NWG == 2 || NWG == 4, "two or four elementwise warpgroups");
     static_assert((D / NWG) % 16 == 0, "each warpgroup drains whole 16-column chunks");
-    static_assert(!PERSIST || MASK == kMaskNone, "the persistent kernel takes no mask");
+    static_assert(!PERSIST || MASK == kMaskNone || MASK == kMaskSinks, "the persistent kernel takes no such mask");
     constexpr int kProducerWarp = 4 * NWG, kMmaWarp = 4 * NWG + 1, kReducerWarp = 4 * NWG + 2;
     constexpr int kQC = 128 / NWG;      // query columns of P^T / dS^T per warpgroup
     constexpr int kDC = D / NWG;        // d-columns of dQ, dK, dV per warpgroup
@@ -347,7 +347,31 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     // head (heaviest first when causal): a snake that balances heavy and light
     // items without a shared counter.  (The head-grouped order measured slower
     // here: at these sizes the balance matters more than the L2 reuse.)
+    // Sinks, PERSIST: the tiles that hold them are much longer than the others.  The list is
+    // dealt in rounds of one cell per CTA: a sink tile fills plan_chunks cells of its CTA,
+    // the other tiles the cells left over, in order (the full rounds as a snake).
     auto item_at = [&](int k, int& ibh, int& ikv) -> bool {
+        if constexpr (PERSIST && MASK == kMaskSinks) {
+            const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+            const int n_long = p.BH * p.plan_tiles, full = n_long / G, rem = n_long - full * G;
+            int i;
+            if (k < full || (k == full && c < rem)) {
+                i = k * G + c;
+            } else {
+                const int rest = rem > 0 ? G - rem : 0;  // free cells of a round beside sink tiles
+                int r = k - full - (c < rem ? 1 : 0);
+                if (rem > 0 && c >= rem && r < p.plan_chunks) {
+                    i = n_long + r * rest + c - rem;
+                } else {
+                    if (rem > 0 && c >= rem) r -= p.plan_chunks;
+                    i = n_long + p.plan_chunks * rest + r * G + ((r & 1) ? G - 1 - c : c);
+                }
+                if (i >= p.items) return false;
+            }
+            ikv = i / p.BH;
+            ibh = i - ikv * p.BH;
+            return true;
+        }
         if constexpr (PERSIST) {
             const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
             const long long i = static_cast<long long>(k) * G + ((k & 1) ? G - 1 - c : c);
@@ -401,7 +425,11 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     }
     // an item's first query tile and step count (item 0: first and n_steps)
     auto first_of = [&](int ikv) { return PERSIST ? (CAUSAL ? ikv : 0) : first; };
-    auto steps_of = [&](int ikv) { return PERSIST ? n_q - (CAUSAL ? ikv : 0) : n_steps; };
+    auto steps_of = [&](int ikv) {
+        if (PERSIST && SINKS && ikv * kBK >= sinks)
+            return min(n_q - 1, (ikv * kBK + kBK - 1 + window - 1) / kBQ) - ikv + 1;
+        return PERSIST ? n_q - (CAUSAL ? ikv : 0) : n_steps;
+    };
 
     if (sbase & 1023u) {  // the swizzled tiles need 1024-byte alignment
         if (threadIdx.x == 0) atomicCAS(p.err, 0u, 1u | (0xAAu << 8));
@@ -1353,6 +1381,7 @@ int bwd_head_group(int BH, int N, int D, bool causal, int mask) {
 struct SinkPlan {
     int tiles = 0;    // key tiles that hold sinks, per head
     int chunks = 1;   // of each (1: no split)
+    int cells = 1;    // persistent: another tile's lengths that one of them takes
     size_t part = 0;  // offset of the partial slots in dQ
 };
 SinkPlan sink_plan(const BwdArgs& a, int n_kv, int D, int sms) {
@@ -1370,6 +1399,9 @@ SinkPlan sink_plan(const BwdArgs& a, int n_kv, int D, int sms) {
     const size_t room = s.part < dq_bytes ? (dq_bytes - s.part) / slot : 0;
     s.chunks = static_cast<int>(std::min<size_t>(s.chunks, room / (static_cast<size_t>(a.BH) * s.tiles)));
     if (s.chunks < 2) s.chunks = 1;
+    // (an item's set-up and epilogue count as kSplitCtaSteps steps)
+    const int other = window_steps + kSplitCtaSteps;
+    s.cells = std::max(1, (n_kv + kSplitCtaSteps + other / 2) / other);
     return s;
 }
 
@@ -1383,7 +1415,8 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
     // short d = 64 problems without a mask, with more work items than SMs: the
     // persistent kernel, so that one item's set-up, first loads and epilogue
     // overlap the next's
-    constexpr bool kCanPersist = D == 64 && MASK == kMaskNone;
+    // (windows with sinks at any length: their items are short)
+    constexpr bool kCanPersist = D == 64 && (MASK == kMaskNone || MASK == kMaskSinks);
     int sms = 0;
     if (kCanPersist || MASK == kMaskBlocks || MASK == kMaskSinks) {
         int dev = 0;
@@ -1442,9 +1475,10 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
             !make_tile_map(&tdv, a.dV, BF, 2, D, a.N, a.BH, 64, kBK))
             return cudaErrorInvalidValue;
         const long long items = static_cast<long long>(a.BH) * ((a.N + kBK - 1) / kBK);
-        const bool persist = kCanPersist && a.N <= kBwdPersistMaxN && items > sms;
+        const bool persist = kCanPersist && items > sms &&
+                             (MASK == kMaskSinks ? sp.chunks == 1 : a.N <= kBwdPersistMaxN);
         constexpr auto kern = &fa_bwd_main_kernel<D, CAUSAL, MASK, NWG, false, MASK == kMaskSinks>;
-        constexpr auto kern_p = &fa_bwd_main_kernel<D, CAUSAL, MASK, NWG, kCanPersist, MASK == kMaskSinks>;
+        constexpr auto kern_p = &fa_bwd_main_kernel<D, CAUSAL, MASK, NWG, kCanPersist, MASK == kMaskSinks && !kCanPersist>;
         constexpr auto kern_s =
             &fa_bwd_main_kernel<D, CAUSAL, MASK, NWG, false, MASK == kMaskBlocks || MASK == kMaskSinks>;
         const bool split = pa.base != nullptr || MASK == kMaskSinks;
@@ -1488,7 +1522,8 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
             p.plan_chunks = sp.chunks;
             p.plan_tiles = sp.tiles;
             p.plan_part = sp.part;
-            grid = dim3(static_cast<unsigned>(items + static_cast<long long>(a.BH) * sp.tiles * (sp.chunks - 1)));
+            if (persist) p.plan_chunks = sp.cells;
+            else grid = dim3(static_cast<unsigned>(items + static_cast<long long>(a.BH) * sp.tiles * (sp.chunks - 1)));
         }
         e = persist   ? launch_dependent(kern_p, grid, dim3(bwd_threads(NWG)), L::kBytesPersist, stream, tq, tk,
                                          tv, tdo, tacc, tdk, tdv, p)

@@ -51,8 +51,8 @@ constexpr int kBN = 128;  // keys per block
 // TILES = 2 (the default): two query tiles per CTA, 10 warps, all 512 tensor-
 // memory columns, one CTA per SM.  TILES = 1: one tile, 6 warps, 256 columns
 // and a smaller ring (5 slots at d = 64, 2 at d = 128), so two CTAs share an SM
-// and one's prologue and epilogue overlap the other's main loop: used for d = 64
-// block masks (d = 64 short sequences and d = 128 block masks have persistent
+// and one's prologue and epilogue overlap the other's main loop: used for windows
+// with sinks and d = 64 block masks (d = 64 short sequences and d = 128 block masks have persistent
 // kernels of their own, fa_fwd_short.cu and fa_fwd_sparse.cu).
 constexpr int threads_for(int tiles) { return tiles == 2 ? 320 : 192; }
 constexpr float kLn2 = 0.69314718055994531f;
@@ -160,18 +160,12 @@ __device__ __forceinline__ void issue_pv(uint32_t tmem_o, uint32_t tmem_p, uint3
 // diagonal when causal, and from the block holding key (first row - window + 1)
 // with a sliding window.  The two ranges overlap or touch, so the loaders walk
 // [jlo, jlo + nb) without gaps.  (A block mask recounts n_blk0, n_blk1 and nb.)
-// With sinks both tiles first take the ns key blocks that hold sinks and lie
-// before jlo: step u of the walk is block u for u < ns, then jlo + u - ns.  A
-// block jlo that itself holds sinks is taken by tile 1 too, whose window may
-// begin one block later.
+// With sinks (one tile) the key blocks that hold sinks and lie before the window's
+// first, win, stand in for the blocks just before it: the walk is still [lo0, hi0)
+// without a gap, and block(j) is the key block behind number j.
 struct FwdItem {
-    int bh, q_start0, q_start1, lo0, lo1, hi0, hi1, n_blk0, n_blk1, jlo, nb, ns;
-    // kMaskSinks: whether tile t (its block range [lo, hi)) takes step u, and u's key block
-    __device__ __forceinline__ int block(int u) const { return u < ns ? u : jlo + u - ns; }
-    __device__ __forceinline__ bool takes(int u, int lo, int hi) const {
-        const int j = jlo + u - ns;
-        return u < ns ? hi > 0 : (j >= lo && j < hi);
-    }
+    int bh, q_start0, q_start1, lo0, lo1, hi0, hi1, n_blk0, n_blk1, jlo, nb, win;
+    __device__ __forceinline__ int block(int j) const { return j < win ? j - jlo : j; }
 };
 
 template <bool CAUSAL, int TILES>
@@ -184,13 +178,12 @@ __device__ __forceinline__ FwdItem fwd_item(int bh, int pair, int N, int n_kv, i
     it.hi1 = it.q_start1 < N ? (CAUSAL ? min(n_kv, it.q_start1 / kBN + 1) : n_kv) : 0;
     it.lo0 = window > 0 ? max(0, it.q_start0 - window + 1) / kBN : 0;
     it.lo1 = window > 0 ? max(0, it.q_start1 - window + 1) / kBN : 0;
-    const int n_sink = (sinks + kBN - 1) / kBN;  // key blocks that hold sinks
+    it.win = it.lo0;
+    it.lo0 -= min((sinks + kBN - 1) / kBN, it.lo0);
+    it.n_blk0 = it.hi0 - it.lo0;
+    it.n_blk1 = it.hi1 > 0 ? it.hi1 - it.lo1 : 0;
     it.jlo = it.lo0;
-    it.ns = min(n_sink, it.jlo);
-    if (it.jlo < n_sink) it.lo1 = it.jlo;
-    it.n_blk0 = it.ns + it.hi0 - it.lo0;
-    it.n_blk1 = it.hi1 > 0 ? it.ns + it.hi1 - it.lo1 : 0;
-    it.nb = it.ns + max(it.hi0, it.hi1) - it.jlo;
+    it.nb = max(it.hi0, it.hi1) - it.jlo;
     return it;
 }
 
@@ -213,6 +206,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     // j + 1 is issued as soon as the softmax has read S of block j, and the
     // softmax runs from block to block without waiting for P V and the next S
     constexpr bool PIPE = D == 64 && MASK == kMaskNone;
+    static_assert(!SINKS || TILES == 1, "sinks: one tile per CTA");
     static_assert(!PERSIST || (TILES == 2 && !O32 && !SPARSE && (D == 128 || PIPE)),
                   "persistent: two-tile pairs with a bf16 O, no block mask");
     // the row sums as paired fp32 adds (bitwise the same sums): measured faster
@@ -403,7 +397,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                             break;
                         }
                         bool is_k = (ld & 1) == 0;
-                        int blk = SINKS ? it.block(ld >> 1) : it.jlo + (ld >> 1);
+                        int blk = SINKS ? it.block(it.jlo + (ld >> 1)) : it.jlo + (ld >> 1);
                         if constexpr (PIPE) {
                             // the MMA warp's order: K0 K1 V0 K2 V1 ... K(nb-1) V(nb-2) V(nb-1)
                             is_k = ld == 0 || ((ld & 1) && ld < 2 * it.nb - 1);
@@ -591,7 +585,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                         if (ok) {
                             tc_fence_after();
                             for (int t = 0; t < 2; ++t) {
-                                if (SINKS ? it.takes(0, lo[t], hi[t]) : lo[t] == it.jlo && hi[t] > it.jlo) {
+                                if (lo[t] == it.jlo && hi[t] > it.jlo) {
                                     issue_s<D>(tS[t], qlo[t], klo0 + s0 * kSlot);
                                     mma_commit_warp(bar_s + 8 * t);
                                 }
@@ -653,10 +647,8 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                                 if (k_ready) mma_commit_warp(bar_kv_empty + 8 * sk);
                             }
                         } else {
-                            // tile t takes blocks [lo[t], hi[t]) (with sinks: the steps that it.takes
-                            // says); S of a tile's first block may be issued while the other tile is
-                            // still in its leading blocks
-                            [[maybe_unused]] int cnt[2] = {0, 0};  // SINKS: P V products issued per tile
+                            // tile t takes blocks [lo[t], hi[t]); S of a tile's first block may
+                            // be issued while the other tile is still in its leading blocks
                             for (int u = 0; ok && u < it.nb; ++u) {
                                 const int j = it.jlo + u;  // key block
                                 const int lv = g0 + 2 * u + 1, lk = g0 + 2 * u + 2;
@@ -671,21 +663,19 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                                 // fully unrolled over the two tiles so the per-tile arrays stay in registers
 #pragma unroll
                                 for (int t = 0; t < 2; ++t) {
-                                    const int done = SINKS ? cnt[t] : j - lo[t];  // P V products of the item before this
-                                    if (ok && (SINKS ? it.takes(u, lo[t], hi[t]) : j >= lo[t] && j < hi[t])) {
-                                        if (done == 0) ok = o_free_wait(t);
+                                    if (ok && j >= lo[t] && j < hi[t]) {
+                                        if (j == lo[t]) ok = o_free_wait(t);
                                         if (ok)
                                             ok = __all_sync(0xffffffffu,
-                                                            mbar_wait(bar_p + 8 * t, (cb[t] + done) & 1, wd,
+                                                            mbar_wait(bar_p + 8 * t, (cb[t] + j - lo[t]) & 1, wd,
                                                                       kSiteMmaP));
                                         if (ok) {
                                             tc_fence_after();
-                                            issue_pv<D>(tO[t], tS[t], vlo0 + sv * kSlot, done > 0);
+                                            issue_pv<D>(tO[t], tS[t], vlo0 + sv * kSlot, j > lo[t]);
                                             mma_commit_warp(bar_o + 8 * t);
                                         }
-                                        if constexpr (SINKS) ++cnt[t];
                                     }
-                                    if (ok && (SINKS ? it.takes(u + 1, lo[t], hi[t]) : j + 1 >= lo[t] && j + 1 < hi[t])) {
+                                    if (ok && j + 1 >= lo[t] && j + 1 < hi[t]) {
                                         if (!k_ready) {
                                             ok = __all_sync(0xffffffffu,
                                                             mbar_wait(bar_kv_full + 8 * sk, (lk / L::kStages) & 1,
@@ -741,7 +731,7 @@ fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             int jsp = -1;  // block mask: the last key block visited
             for (int jj = 0; jj < nbt; ++jj) {
                 int j = lot + jj;  // key block
-                if constexpr (SINKS) j = jj < it.ns ? jj : lot + jj - it.ns;
+                if constexpr (SINKS) j = it.block(j);
                 if constexpr (SPARSE) {
                     jsp = next_set_bit(sh.use[t], nullptr, jsp + 1, n_kv);
                     j = jsp;
@@ -1120,10 +1110,11 @@ cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t stream) {
     }
     if (a.causal && !a.o32 && window_hides(a.N, a.window, a.sinks)) {
         if (a.sinks > 0)
-            // d = 64: one tile per CTA, two CTAs per SM (1-17% faster than pairs from 1k to
-            // 4k tokens: a window leaves a pair few key blocks to overlap its ends with)
-            return a.d == 64 ? launch_fwd_t<64, true, false, kMaskSinks, 1>(a, stream)
-                             : launch_fwd_t<128, true, false, kMaskSinks>(a, stream);
+            // d = 128: one tile per CTA, two CTAs per SM: against pairs 2-23% faster (16
+            // heads of 16k, window 4096: 388 -> 381 us; 5001 keys, window 1000: 59 -> 51
+            // us), 3% slower on two heads of 16k.  A window leaves a pair few key blocks
+            // to overlap its ends with, and pairs fill the SMs unevenly.
+            return a.d == 64 ? launch_fwd_short(a, stream) : launch_fwd_t<128, true, false, kMaskSinks, 1>(a, stream);
         return a.d == 64 ? launch_fwd_t<64, true, false, kMaskWindow>(a, stream)
                          : launch_fwd_t<128, true, false, kMaskWindow>(a, stream);
     }

@@ -1,4 +1,5 @@
-// Persistent forward for short d = 64 problems (N <= 2048, GPT-2-sized).
+// Persistent forward for short d = 64 problems (N <= 2048, GPT-2-sized), and for d = 64
+// windows with sinks at any length, whose query tiles have few key blocks too.
 //
 // The method is the forward of fa_fwd.cu ("Atencao eficiente - FlashAttention,
 // sparse e hibrida", "Insight 1 - Tiling" and "Insight 2 - Online softmax";
@@ -50,6 +51,7 @@ constexpr float kRescaleThreshold = 8.0f;     // log2 units: P stays <= 2^8
 struct ShortParams {
     float* LSE;
     int N, BH, n_q, items;
+    int window, sinks;  // SINKS
     float scale_log2;
     unsigned int* err;
     unsigned long long wait_limit_ns;
@@ -81,12 +83,25 @@ __device__ __forceinline__ int item_of(int k, int c, int G, int items) {
     return idx < items ? idx : -1;
 }
 
-template <bool CAUSAL>
-__device__ __forceinline__ int blocks_of(int qt, int n_kv) {
-    return CAUSAL ? min(n_kv, qt + 1) : n_kv;
+// The key blocks of query tile qt, in order: nb of them, number j being block(j).  With
+// SINKS first the blocks that hold sinks and lie before the window's first, win.
+struct Walk {
+    int nb, ns, win;
+    __device__ __forceinline__ int block(int j) const { return j < ns ? j : win + j - ns; }
+};
+template <bool CAUSAL, bool SINKS>
+__device__ __forceinline__ Walk walk_of(int qt, int n_kv, const ShortParams& p) {
+    Walk w{CAUSAL ? min(n_kv, qt + 1) : n_kv, 0, 0};
+    if constexpr (SINKS) {
+        w.win = max(0, qt * kBM - p.window + 1) / kBN;
+        w.ns = min((p.sinks + kBN - 1) / kBN, w.win);
+        w.nb += w.ns - w.win;
+    }
+    return w;
 }
 
-template <bool CAUSAL>
+// SINKS (with CAUSAL): a window of p.window keys beside the first p.sinks.
+template <bool CAUSAL, bool SINKS>
 __global__ void __launch_bounds__(kThreads, 2)
 fa_fwd_short_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -155,7 +170,8 @@ fa_fwd_short_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                 const int idx = item_of(k, c, G, p.items);
                 if (idx < 0) break;
                 const int qt = p.n_q - 1 - idx / p.BH, bh = idx % p.BH;
-                const int nb = blocks_of<CAUSAL>(qt, n_kv);
+                const Walk walk = walk_of<CAUSAL, SINKS>(qt, n_kv, p);
+                const int nb = walk.nb;
                 const int qb = k & 1;
                 // Q buffer qb held item k - 2's staged O until its store read it
                 if (k >= 2 && !mbar_wait(bar_qe + 8 * qb, ((k >> 1) - 1) & 1, wd, kSiteQFree)) break;
@@ -173,7 +189,7 @@ fa_fwd_short_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                     const int blk = is_k ? (ld + 1) / 2 : (ld == 2 * nb - 1 ? nb - 1 : ld / 2 - 1);
                     mbar_arrive_expect_tx(bar_kvf + 8 * slot, kTile);
                     tma_load_3d(sbase + kRing + slot * kTile, is_k ? &tmK : &tmV, bar_kvf + 8 * slot, 0,
-                                blk * kBN, bh);
+                                (SINKS ? walk.block(blk) : blk) * kBN, bh);
                 }
                 if (!ok) break;
                 lbase += 2 * nb;
@@ -194,7 +210,7 @@ fa_fwd_short_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             const int idx = item_of(k, c, G, p.items);
             if (idx < 0) break;
             const int qt = p.n_q - 1 - idx / p.BH;
-            const int nb = blocks_of<CAUSAL>(qt, n_kv);
+            const int nb = walk_of<CAUSAL, SINKS>(qt, n_kv, p).nb;
             const int qb = k & 1;
             const uint32_t qlo = sw128_desc_lo(sbase + kQ + qb * kTile, 16);
             if (!__all_sync(0xffffffffu, mbar_wait(bar_qf + 8 * qb, (k >> 1) & 1, wd, kSiteMmaQ))) break;
@@ -253,7 +269,8 @@ fa_fwd_short_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             const int idx = item_of(k, c, G, p.items);
             if (idx < 0) break;
             const int qt = p.n_q - 1 - idx / p.BH, bh = idx % p.BH;
-            const int nb = blocks_of<CAUSAL>(qt, n_kv);
+            const Walk walk = walk_of<CAUSAL, SINKS>(qt, n_kv, p);
+            const int nb = walk.nb;
             const int qb = k & 1;
             const int q_start = qt * kBM, row = q_start + r;
             float m_used = -INFINITY;
@@ -277,8 +294,17 @@ fa_fwd_short_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                 tc_fence_before();
                 mbar_arrive(bar_sf);  // S's columns may take the next block's scores now
 
-                const int kbase = jj * kBN;
-                if ((CAUSAL && kbase + kBN - 1 > q_start) || (kbase + kBN > N)) {
+                const int kbase = (SINKS ? walk.block(jj) : jj) * kBN;
+                // SINKS: some row's window begins behind this block's first key, and not all
+                // of the block is sinks
+                const bool edge = SINKS && kbase <= q_start + kBM - 1 - p.window && kbase + kBN > p.sinks;
+                if (edge) {
+                    const int last = min(row, N - 1), first = row - p.window + 1;
+#pragma unroll
+                    for (int cc = 0; cc < 128; ++cc)
+                        if (kbase + cc > last || (kbase + cc < first && kbase + cc >= p.sinks))
+                            s[cc >> 5][cc & 31] = f2u(-INFINITY);
+                } else if ((CAUSAL && kbase + kBN - 1 > q_start) || (kbase + kBN > N)) {
                     const int last = CAUSAL ? min(row, N - 1) : N - 1;  // last visible key
 #pragma unroll
                     for (int cc = 0; cc < 128; ++cc)
@@ -416,7 +442,7 @@ fa_fwd_short_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     }
 }
 
-template <bool CAUSAL>
+template <bool CAUSAL, bool SINKS = false>
 cudaError_t launch_short_t(const FwdArgs& a, cudaStream_t stream) {
     CUtensorMap tq, tk, tv, to;
     const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -425,7 +451,7 @@ cudaError_t launch_short_t(const FwdArgs& a, cudaStream_t stream) {
         !make_tile_map(&tv, a.V, BF, 2, kD, a.N, a.BH, 64, kBN) ||
         !make_tile_map(&to, a.O, BF, 2, kD, a.N, a.BH, 64, kBM))
         return cudaErrorInvalidValue;
-    constexpr auto kern = &fa_fwd_short_kernel<CAUSAL>;
+    constexpr auto kern = &fa_fwd_short_kernel<CAUSAL, SINKS>;
     cudaError_t e = set_max_dyn_smem_once<kern>(kDynSmem);
     if (e != cudaSuccess) return e;
     int dev = 0, sms = 0;
@@ -440,12 +466,14 @@ cudaError_t launch_short_t(const FwdArgs& a, cudaStream_t stream) {
     const long long items = static_cast<long long>(a.BH) * p.n_q;
     if (items > (1ll << 30)) return cudaErrorInvalidValue;
     p.items = static_cast<int>(items);
+    p.window = a.window;
+    p.sinks = a.sinks;
     p.scale_log2 = a.tau * kLog2e;
     p.err = a.err;
     p.wait_limit_ns = a.wait_limit_ns;
     const int grid = static_cast<int>(std::min<long long>(items, 2ll * sms));
     if (a.ev_start) cudaEventRecord(a.ev_start, stream);
-    fa_fwd_short_kernel<CAUSAL><<<grid, kThreads, kDynSmem, stream>>>(tq, tk, tv, to, p);
+    fa_fwd_short_kernel<CAUSAL, SINKS><<<grid, kThreads, kDynSmem, stream>>>(tq, tk, tv, to, p);
     e = cudaGetLastError();
     if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
     return e;
@@ -454,6 +482,7 @@ cudaError_t launch_short_t(const FwdArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_fwd_short(const FwdArgs& a, cudaStream_t stream) {
+    if (a.sinks > 0) return launch_short_t<true, true>(a, stream);
     return a.causal ? launch_short_t<true>(a, stream) : launch_short_t<false>(a, stream);
 }
 

@@ -100,6 +100,19 @@ def test_paged_matches_plain(H, Hkv, Nq, page, d, fp8):
     assert api.last_device_error() == _lib.FA_OK
 
 
+# tables short enough for a block per segment, with rows that need one, two and four warps; more rows
+# than one group of warps takes
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H,Hkv,Nq,d,page,longest", [(3, 3, 1, 64, 16, 600), (8, 2, 1, 128, 32, 640), (4, 1, 3, 128, 16, 300),
+                                                     (8, 2, 8, 64, 64, 256), (24, 3, 8, 128, 16, 160), (40, 1, 3, 64, 16, 100),
+                                                     (12, 1, 8, 128, 32, 1500), (1, 1, 8, 64, 16, 17), (2, 1, 1, 128, 16, 1)])
+def test_short_tables_and_many_rows(H, Hkv, Nq, d, page, longest, fp8):
+    lens = [longest] + [n for n in LENS if n < longest]
+    s = build(lens, H, Hkv, Nq, d, page, fp8, seed=H + Nq + longest)
+    check(s)
+    check(s, 37, 6)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 3), (16, 16), (64, 0), (100, 17), (128, 200), (5000, 4)])
 def test_window_and_sinks(window, sinks, fp8):
