@@ -232,6 +232,11 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8, WHOLE>::kCtas
     extern __shared__ __align__(1024) uint8_t smem[];
     PagedShared& sh = *reinterpret_cast<PagedShared*>(smem + kPagedWarps * L::kWarpRing);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    // Launched as a dependent of the kernel before it: its start-up overlaps that kernel's
+    // end.  Every thread waits here before it reads anything, so this grid ends after that
+    // one, whatever its blocks have to do.
+    griddep_launch_dependents();
+    griddep_wait();
     const uint32_t ring = smem_addr(smem) + warp * L::kWarpRing;
     if ((smem_addr(smem) & 255u) != 0u) {  // (the XOR orders count on tiles at multiples of 256 bytes)
         if (tid == 0) atomicCAS(p.err, 0u, 1u | (kSitePagedSmem << 8));
@@ -250,7 +255,6 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8, WHOLE>::kCtas
         rw = warp % p.rwarps;
         turn = warp / p.rwarps;
     } else {
-        griddep_launch_dependents();
         // ---- this warp's share of the tiles ----
         const int per = (p.B + kThreads - 1) / kThreads;
         int mine = 0;
@@ -986,16 +990,14 @@ cudaError_t launch_paged_t(const PagedArgs& a, const PagedPlan& pl, PagedParams&
     if (e != cudaSuccess) return e;
     if (pl.whole) {
         if (a.ev_start) cudaEventRecord(a.ev_start, stream);
-        kern_w<<<static_cast<unsigned>(pl.segs), kThreads, LW::kBytes, stream>>>(p);
-        e = cudaGetLastError();
+        e = launch_dependent(kern_w, dim3(static_cast<unsigned>(pl.segs)), dim3(kThreads), LW::kBytes, stream, p);
         if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
         return e;
     }
     if (a.ev_start) cudaEventRecord(a.ev_start, stream);
     // (no more CTAs than a full table gives kMinTiles per warp)
     const int ctas = static_cast<int>(std::min<long long>(pl.ctas, pl.tiles * pl.rwarps / (kMinTiles * kPagedWarps) + 1));
-    kern<<<static_cast<unsigned>(ctas), kThreads, L::kBytes, stream>>>(p);
-    e = cudaGetLastError();
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), L::kBytes, stream, p);
     // pieces of an average segment: few, a block with a warp per row; many, a block per row
     const long long pieces = static_cast<long long>(ctas) * kPagedWarps / (pl.segs * pl.rwarps) + 1;
     const long long rows = std::min(p.G * p.Nq, 8 * NT * pl.rwarps);
