@@ -3,8 +3,9 @@
 PyTorch only supplies device memory and the current stream; the tensors'
 data pointers go straight to ``fa_fwd`` / ``fa_bwd``.  Inputs must be CUDA
 bf16 tensors, contiguous, shaped [B, H, N, d].  The paged entry points
-(``kv_append``, ``fwd_paged``) check and call in a small extension module
-(csrc/torch_binding.cpp), for their kernels take little longer than a call.
+(``kv_append``, ``fwd_paged``) and windows with sinks check and call in a small
+extension module (csrc/torch_binding.cpp), for their kernels can take less time
+than a call from Python.
 """
 from __future__ import annotations
 
@@ -70,6 +71,8 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool,
         raise ValueError("a window needs causal=True and a bf16 O")
     if blocks is not None and (o_fp32 or window is not None):
         raise ValueError("a block mask needs a bf16 O and no window")
+    if sinks:
+        return _lib.binding().fwd_sinks(q, k, v, tau, window, sinks, out, lse)
     B, H, N, d = _check_inputs(q, k, v)
     tau = 1.0 / math.sqrt(d) if tau is None else float(tau)
     o_dtype = torch.float32 if o_fp32 else torch.bfloat16
@@ -83,12 +86,6 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool,
                                   lse.data_ptr(), B, H, N, d, tau, int(bool(causal)),
                                   blocks.data_ptr(), heads, _stream_handle(q.device))
         _lib.check(code, "fa_fwd_blocks")
-        return out, lse
-    if sinks:
-        code = _lib.fa_fwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                 lse.data_ptr(), B, H, N, d, tau, int(window), int(sinks),
-                                 _stream_handle(q.device))
-        _lib.check(code, "fa_fwd_sinks")
         return out, lse
     if window is not None:
         code = _lib.fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -114,8 +111,12 @@ def bwd(q, k, v, o, do, lse, causal: bool, tau: Optional[float] = None,
     """Backward pass.  Returns (dQ, dK, dV), bf16.  ``workspace`` (a byte
     tensor of at least ``workspace_bytes`` bytes) is allocated with torch when
     not given, so the library itself allocates nothing."""
-    if sinks and window is None:
-        raise ValueError("sinks need a window")
+    if sinks:
+        if window is None:
+            raise ValueError("sinks need a window")
+        if not causal or blocks is not None:
+            raise ValueError("a window needs causal=True and no block mask")
+        return _lib.binding().bwd_sinks(q, k, v, o, do, lse, tau, window, sinks, dq, dk, dv, workspace)
     B, H, N, d = _check_inputs(q, k, v, o, do)
     if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (B, H, N):
         raise ValueError("lse must be contiguous fp32 [B, H, N]")
@@ -140,13 +141,6 @@ def bwd(q, k, v, o, do, lse, causal: bool, tau: Optional[float] = None,
     if window is not None:
         if not causal:
             raise ValueError("a window needs causal=True")
-        if sinks:
-            code = _lib.fa_bwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
-                                     do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
-                                     dv.data_ptr(), workspace.data_ptr(), workspace.numel(), B, H,
-                                     N, d, tau, int(window), int(sinks), _stream_handle(q.device))
-            _lib.check(code, "fa_bwd_sinks")
-            return dq, dk, dv
         code = _lib.fa_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                   do.data_ptr(), lse.data_ptr(), dq.data_ptr(), dk.data_ptr(),
                                   dv.data_ptr(), workspace.data_ptr(), workspace.numel(), B, H, N,

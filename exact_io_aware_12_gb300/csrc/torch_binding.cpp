@@ -1,6 +1,7 @@
-// The paged entry points for torch tensors, as a Python extension module.
+// The paged entry points and windows with sinks for torch tensors, as a Python extension
+// module.
 //
-// Their kernels take a few microseconds, less than a ctypes call with its checks and
+// Their kernels can take a few microseconds, less than a ctypes call with its checks and
 // allocations takes in Python, so checks, output allocation and the call itself run here:
 // the C ABI is unchanged and holds all of the computation.  The module finds the library's
 // functions by name (load), so it links only against torch.
@@ -19,6 +20,7 @@
 #include <optional>
 #include <stdexcept>
 #include <string>
+#include <utility>
 
 #include "../../include/fa.h"
 
@@ -27,6 +29,9 @@ namespace {
 decltype(&fa_kv_append) g_append[2];  // bf16, e4m3
 decltype(&fa_fwd_paged) g_paged[2];
 decltype(&fa_paged_workspace_size) g_workspace;
+decltype(&fa_fwd_sinks) g_fwd_sinks;
+decltype(&fa_bwd_sinks) g_bwd_sinks;
+decltype(&fa_bwd_workspace_size) g_bwd_workspace;
 PyObject* g_error = nullptr;  // FAError(code, where)
 PyObject* g_oom = nullptr;    // torch.OutOfMemoryError
 
@@ -113,6 +118,29 @@ void check_status(int code, const char* where) {
         Py_DECREF(e);
     }
     throw PyErr{};
+}
+
+float scale_of(PyObject* o, int64_t d) {
+    if (o == Py_None) return static_cast<float>(1.0 / std::sqrt(static_cast<double>(d)));
+    const double tau = PyFloat_AsDouble(o);
+    if (tau == -1.0 && PyErr_Occurred()) throw PyErr{};
+    return static_cast<float>(tau);
+}
+
+// A tuple of tensors, each wrapped, or the argument that it came as.
+PyObject* results(std::initializer_list<std::pair<const std::optional<at::Tensor>*, PyObject*>> rs) {
+    PyObject* all = PyTuple_New(static_cast<Py_ssize_t>(rs.size()));
+    if (!all) throw PyErr{};
+    Py_ssize_t i = 0;
+    for (const auto& [made, given] : rs) {
+        PyObject* o = *made ? THPVariable_Wrap(**made) : Py_NewRef(given);
+        if (!o) {
+            Py_DECREF(all);
+            throw PyErr{};
+        }
+        PyTuple_SET_ITEM(all, i++, o);
+    }
+    return all;
 }
 
 // Every Python function's frame: no C++ exception passes into the interpreter.
@@ -209,11 +237,7 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
             window = to_int(integer(a[6]));
             require(window >= 1, "a window holds at least one key");
         }
-        double tau = 1.0 / std::sqrt(static_cast<double>(c.c.d));
-        if (a[5] != Py_None) {
-            tau = PyFloat_AsDouble(a[5]);
-            if (tau == -1.0 && PyErr_Occurred()) throw PyErr{};
-        }
+        const float tau = scale_of(a[5], c.c.d);
         const int64_t H = q.size(1), Nq = q.size(2);
         check_rows(q, {c.c.B, H, Nq, c.c.d}, c, "q");
         const c10::cuda::OptionalCUDAGuard guard(c.dev);
@@ -235,20 +259,82 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         check_status(g_paged[c.fp8](&c.c, q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), out->data_ptr(),
                                     out->stride(0), out->stride(1), out->stride(2), static_cast<float*>(lse->data_ptr()),
-                                    to_int(H), to_int(Nq), static_cast<float>(tau), window, sinks, ws ? ws->data_ptr() : nullptr, bytes,
+                                    to_int(H), to_int(Nq), tau, window, sinks, ws ? ws->data_ptr() : nullptr, bytes,
                                     c10::cuda::getCurrentCUDAStream(c.dev.index()).stream()),
                      c.fp8 ? "fa_fwd_paged_fp8" : "fa_fwd_paged");
-        PyObject* o = made_out ? THPVariable_Wrap(*made_out) : Py_NewRef(a[10]);
-        PyObject* l = made_lse ? THPVariable_Wrap(*made_lse) : Py_NewRef(a[11]);
-        PyObject* both = o && l ? PyTuple_New(2) : nullptr;
-        if (!both) {
-            Py_XDECREF(o);
-            Py_XDECREF(l);
-            throw PyErr{};
+        return results({{&made_out, a[10]}, {&made_lse, a[11]}});
+    });
+}
+
+// Contiguous bf16 [B, H, N, d] tensors of one shape and CUDA device, as fa_fwd takes them.
+void check_attention(std::initializer_list<const at::Tensor*> ts) {
+    const at::Tensor& ref = **ts.begin();
+    require(ref.dim() == 4, "expected [B, H, N, d] tensors");
+    for (const at::Tensor* t : ts) {
+        require(t->is_cuda() && t->scalar_type() == at::kBFloat16 && t->is_contiguous(),
+                "inputs must be contiguous CUDA bf16 tensors");
+        require(t->sizes() == ref.sizes() && t->device() == ref.device(), "inputs must share shape and device");
+    }
+}
+void check_lse(const at::Tensor& lse, const at::Tensor& q) {
+    require(lse.scalar_type() == at::kFloat && lse.is_contiguous() && lse.device() == q.device() &&
+                lse.sizes() == q.sizes().slice(0, 3),
+            "lse must be contiguous fp32 [B, H, N]");
+}
+// fwd_sinks(q, k, v, tau, window, sinks, out, lse) -> (O, LSE)
+PyObject* fwd_sinks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 8, [&]() -> PyObject* {
+        const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+        const at::Tensor *out = tensor_or_none(a[6], "out"), *lse = tensor_or_none(a[7], "lse");
+        check_attention({&q, &k, &v});
+        const int B = to_int(q.size(0)), H = to_int(q.size(1)), N = to_int(q.size(2)), d = to_int(q.size(3));
+        const int window = to_int(integer(a[4])), sinks = to_int(integer(a[5]));
+        const float tau = scale_of(a[3], d);
+        const c10::cuda::OptionalCUDAGuard guard(q.device());
+        std::optional<at::Tensor> made_out, made_lse;
+        if (out) check_attention({&q, out});
+        else out = &made_out.emplace(at::empty(q.sizes(), q.options()));
+        if (lse) check_lse(*lse, q);
+        else lse = &made_lse.emplace(at::empty(q.sizes().slice(0, 3), q.options().dtype(at::kFloat)));
+        check_status(g_fwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), out->data_ptr(),
+                                 static_cast<float*>(lse->data_ptr()), B, H, N, d, tau, window, sinks,
+                                 c10::cuda::getCurrentCUDAStream(q.device().index()).stream()),
+                     "fa_fwd_sinks");
+        return results({{&made_out, a[6]}, {&made_lse, a[7]}});
+    });
+}
+
+// bwd_sinks(q, k, v, o, do, lse, tau, window, sinks, dq, dk, dv, workspace) -> (dQ, dK, dV)
+PyObject* bwd_sinks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 13, [&]() -> PyObject* {
+        const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &o = tensor(a[3], "o");
+        const at::Tensor &go = tensor(a[4], "do"), &lse = tensor(a[5], "lse");
+        check_attention({&q, &k, &v, &o, &go});
+        check_lse(lse, q);
+        const int B = to_int(q.size(0)), H = to_int(q.size(1)), N = to_int(q.size(2)), d = to_int(q.size(3));
+        const int window = to_int(integer(a[7])), sinks = to_int(integer(a[8]));
+        const float tau = scale_of(a[6], d);
+        const c10::cuda::OptionalCUDAGuard guard(q.device());
+        std::optional<at::Tensor> made[3], made_ws;
+        void* grads[3];
+        for (int i = 0; i < 3; ++i) {
+            const at::Tensor* g = tensor_or_none(a[9 + i], "a gradient");
+            if (g) check_attention({&q, g});
+            else g = &made[i].emplace(at::empty(q.sizes(), q.options()));
+            grads[i] = g->data_ptr();
         }
-        PyTuple_SET_ITEM(both, 0, o);
-        PyTuple_SET_ITEM(both, 1, l);
-        return both;
+        const at::Tensor* ws = tensor_or_none(a[12], "workspace");
+        if (ws) require(ws->device() == q.device() && ws->is_contiguous(), "workspace must be contiguous, on the inputs' device");
+        else {
+            const size_t need = g_bwd_workspace(B, H, N, d);
+            ws = &made_ws.emplace(at::empty({static_cast<int64_t>(need ? need : 1)}, q.options().dtype(at::kByte)));
+        }
+        check_status(g_bwd_sinks(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), go.data_ptr(),
+                                 static_cast<const float*>(lse.data_ptr()), grads[0], grads[1], grads[2], ws->data_ptr(),
+                                 ws->nbytes(), B, H, N, d, tau, window, sinks,
+                                 c10::cuda::getCurrentCUDAStream(q.device().index()).stream()),
+                     "fa_bwd_sinks");
+        return results({{&made[0], a[9]}, {&made[1], a[10]}, {&made[2], a[11]}});
     });
 }
 
@@ -269,6 +355,9 @@ PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
         g_paged[0] = reinterpret_cast<decltype(&fa_fwd_paged)>(find("fa_fwd_paged"));
         g_paged[1] = reinterpret_cast<decltype(&fa_fwd_paged)>(find("fa_fwd_paged_fp8"));
         g_workspace = reinterpret_cast<decltype(&fa_paged_workspace_size)>(find("fa_paged_workspace_size"));
+        g_fwd_sinks = reinterpret_cast<decltype(&fa_fwd_sinks)>(find("fa_fwd_sinks"));
+        g_bwd_sinks = reinterpret_cast<decltype(&fa_bwd_sinks)>(find("fa_bwd_sinks"));
+        g_bwd_workspace = reinterpret_cast<decltype(&fa_bwd_workspace_size)>(find("fa_bwd_workspace_size"));
         Py_XDECREF(g_error);
         Py_XDECREF(g_oom);
         g_error = Py_NewRef(a[1]);
@@ -282,7 +371,8 @@ PyMethodDef method(const char* name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef g_methods[] = {method<kv_append>("kv_append"), method<fwd_paged>("fwd_paged"), method<load>("load"),
+PyMethodDef g_methods[] = {method<kv_append>("kv_append"), method<fwd_paged>("fwd_paged"),
+                           method<fwd_sinks>("fwd_sinks"), method<bwd_sinks>("bwd_sinks"), method<load>("load"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "fa_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -311,6 +311,16 @@ def test_python_checks():
         api.fwd(x, x, x, True, sinks=4)
     with pytest.raises(ValueError, match="sinks need a window"):
         api.bwd(x, x, x, x, x, x, True, sinks=4)
+    with pytest.raises(ValueError, match="causal"):
+        api.fwd(x, x, x, False, window=8, sinks=4)
+    with pytest.raises(ValueError, match="causal"):
+        api.bwd(x, x, x, x, x, x, False, window=8, sinks=4)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.fwd(x, x, x, True, window=8, sinks=4)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.bwd(x, x, x, x, x, x, True, window=8, sinks=4)
+    with pytest.raises(TypeError):
+        api.fwd(x, x, None, True, window=8, sinks=4)
     kc = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
     tb, ln = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
     q = torch.zeros(2, 4, 1, 64, dtype=torch.bfloat16)
