@@ -622,6 +622,7 @@ static fa_status append_common(const fa_paged_cache* c, bool fp8, const void* k,
     fa_status s = check_cache(c, fp8, &a.cache, &cache_bytes);
     if (s != FA_OK) return s;
     if (T < 0 || H < 0 || rot < 0 || (interleaved != 0 && interleaved != 1)) return FA_ERR_INVALID_ARG;
+    if (c->H_kv == 0 && H > 0) return FA_ERR_INVALID_ARG;
     if (c->B == 0 || c->H_kv == 0 || T == 0) return FA_OK;
     if (rot > c->d || rot % 16 != 0) return FA_ERR_INVALID_ARG;
     if ((rot > 0) != (inv_freq != nullptr) || (reinterpret_cast<uintptr_t>(inv_freq) & 7u) != 0) return FA_ERR_INVALID_ARG;
@@ -639,6 +640,7 @@ static fa_status append_common(const fa_paged_cache* c, bool fp8, const void* k,
     };
     const long long ks = span(nk, k_st, k_sh), vs = span(nk, v_st, v_sh);
     if (ks < 0 || vs < 0) return FA_ERR_INVALID_ARG;
+    size_t q_bytes = 0;  // of q_out
     const void* caches[] = {c->K, c->V};
     for (const void* x : caches)
         if (overlaps(x, cache_bytes, k, ks * 2) || overlaps(x, cache_bytes, v, vs * 2)) return FA_ERR_INVALID_ARG;
@@ -654,12 +656,27 @@ static fa_status append_common(const fa_paged_cache* c, bool fp8, const void* k,
         if (!in_place && (overlaps(q_out, os * 2, q, qs * 2) || overlaps(q_out, os * 2, k, ks * 2) ||
                           overlaps(q_out, os * 2, v, vs * 2)))
             return FA_ERR_INVALID_ARG;
+        q_bytes = static_cast<size_t>(os) * 2;
         a.q_st = q_st;
         a.q_sh = q_sh;
         a.o_st = qo_st;
         a.o_sh = qo_sh;
     } else {
         a.q_st = a.q_sh = a.o_st = a.o_sh = 0;
+    }
+    // what the kernels read as indices and angles lies apart from all that they write
+    const size_t sb = fp8 ? static_cast<size_t>(c->num_pages) * c->H_kv * 4 : 0;
+    const void* ins[] = {c->page_table, c->lens, cu_new, inv_freq};
+    const size_t in_bytes[] = {static_cast<size_t>(c->B) * c->max_pages * 4, static_cast<size_t>(c->B) * 4,
+                               cu_new ? (static_cast<size_t>(c->B) + 1) * 4 : 0, static_cast<size_t>(rot) * 4};
+    const void* outs[] = {c->K, c->V, q_out, c->k_scale, c->v_scale};
+    const size_t out_bytes[] = {cache_bytes, cache_bytes, q_bytes, sb, sb};
+    for (int o = 0; o < 5; ++o) {
+        if (out_bytes[o] == 0) continue;
+        for (int i = 0; i < 4; ++i)
+            if (in_bytes[i] > 0 && overlaps(outs[o], out_bytes[o], ins[i], in_bytes[i])) return FA_ERR_INVALID_ARG;
+        for (int o2 = 3; o2 < 5; ++o2)
+            if (sb > 0 && o2 != o && overlaps(outs[o], out_bytes[o], outs[o2], sb)) return FA_ERR_INVALID_ARG;
     }
     DeviceInfo* di = current_device(&s);
     if (!di) return s;
@@ -726,8 +743,8 @@ static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, 
     if (s != FA_OK) return s;
     if (H < 0 || Nq < 0 || window < 0 || sinks < 0 || (sinks > 0 && window == 0)) return FA_ERR_INVALID_ARG;
     if (!(std::isfinite(tau) && tau > 0.f)) return FA_ERR_INVALID_ARG;
-    if (c->B == 0 || c->H_kv == 0 || H == 0 || Nq == 0) return FA_OK;
-    if (H % c->H_kv != 0) return FA_ERR_INVALID_ARG;
+    if (c->B == 0 || H == 0 || Nq == 0) return FA_OK;
+    if (c->H_kv == 0 || H % c->H_kv != 0) return FA_ERR_INVALID_ARG;
     if (Nq > 8 || H / c->H_kv > (1 << 20)) return FA_ERR_UNSUPPORTED;
     if (paged_max_tiles(c->B, H, c->H_kv, Nq, c->max_pages, a.cache.shift) > INT_MAX) return FA_ERR_UNSUPPORTED;
     if (Q == nullptr || O == nullptr || LSE == nullptr) return FA_ERR_INVALID_ARG;

@@ -59,7 +59,7 @@ __device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0
 __device__ __forceinline__ void page_error(unsigned int* err) { atomicCAS(err, 0u, kErrPage); }
 
 __device__ __forceinline__ int cu_of(const AppendParams& p, int b) {
-    return p.cu ? __ldg(p.cu + b) : b * (p.T / p.B);
+    return p.cu ? p.cu[b] : b * (p.T / p.B);
 }
 
 // The largest b in [0, B) with key(b) <= x (0 if none), key non-decreasing: 32 probes at a
@@ -182,12 +182,12 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, RowShared<D>&
             const int tt = t_first + lane;
             if (b == b0 + 32)  // (32 sequences begin at or before the token: go on one by one)
                 while (b + 1 < p.B && cu_of(p, b + 1) <= tt) ++b;
-            const int c0 = cu_of(p, b), c1 = cu_of(p, b + 1), past = __ldg(p.lens + b);
+            const int c0 = cu_of(p, b), c1 = cu_of(p, b + 1), past = p.lens[b];
             const long long pos = static_cast<long long>(past) + (tt - c0);
             const bool live = tt < p.T && tt >= c0 && tt < c1;
             int pg = -1;
             if (live && h1 > p.H) {
-                if (past >= 0)
+                if (past >= 0 && c0 >= 0 && c1 <= p.T)
                     pg = page_of(p.table + static_cast<long long>(b) * p.max_pages, p.max_pages, p.num_pages, p.shift, pos);
                 if (pg < 0) page_error(p.err);
             }
@@ -203,7 +203,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, RowShared<D>&
         for (int idx = tid; idx < TOK * half; idx += kAppendThreads) {
             const int i = idx / half, c = idx - i * half;
             reinterpret_cast<float2*>(&sh.turn[i][c % 8 / 2][c / 8])[c & 1] =
-                turn_at(turn_fraction(__ldg(p.inv_freq + c)), sh.pos[i]);
+                turn_at(turn_fraction(p.inv_freq[c]), sh.pos[i]);
         }
         __syncthreads();
     }
@@ -226,8 +226,8 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, RowShared<D>&
                 const __nv_bfloat16* src = h < p.H            ? qrow + h * p.q_sh
                                            : h < p.H + p.H_kv ? krow + h * p.k_sh
                                                               : vrow + h * p.v_sh;
-                wa[i] = __ldg(reinterpret_cast<const uint4*>(src) + a);
-                wb[i] = __ldg(reinterpret_cast<const uint4*>(src) + c);
+                wa[i] = reinterpret_cast<const uint4*>(src)[a];
+                wb[i] = reinterpret_cast<const uint4*>(src)[c];
             }
         }
 #pragma unroll
@@ -257,8 +257,9 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, RowShared<D>&
 }
 
 // Both kernels are launched as dependents of the kernel before them, so that their start-up
-// overlaps its end; every thread waits for it before it reads anything.  (Calls in a row on
-// one stream: 6.2 -> 3.7 us each for one token of 64 sequences, 8.2 -> 5.6 us in 8 bits.)
+// overlaps its end; every thread waits for it before it reads anything (by plain loads: the
+// inputs may still be written while this grid is being set up).  Calls in a row on one
+// stream: 6.2 -> 3.7 us each for one token of 64 sequences, 8.2 -> 5.6 us in 8 bits.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const AppendParams p) {
     __shared__ RowShared<D> sh;
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_fp8_kernel(con
         else __syncthreads();
     };
     if (p.rot > 0) {
-        for (int i = threadIdx.x; i < p.rot / 2; i += kAppendThreads) sh.page.freq[i] = turn_fraction(__ldg(p.inv_freq + i));
+        for (int i = threadIdx.x; i < p.rot / 2; i += kAppendThreads) sh.page.freq[i] = turn_fraction(p.inv_freq[i]);
         __syncthreads();
     }
     uint32_t* amax_s = sh.page.amax[team];
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_fp8_kernel(con
     // this team's sequence and page
     const int unit = bx * TEAMS + team;
     const int b = last_not_above(p.B, unit, [&](int i) { return first_unit(cu_of(p, i), i, p.shift); });
-    const int c0 = cu_of(p, b), c1 = cu_of(p, b + 1), past = __ldg(p.lens + b);
+    const int c0 = cu_of(p, b), c1 = cu_of(p, b + 1), past = p.lens[b];
     const int i = static_cast<int>(unit - first_unit(c0, b, p.shift));
     if (c0 < 0 || c1 > p.T || c1 <= c0 || past < 0 || i < 0) {
         if (c1 != c0 && tid == 0) page_error(p.err);
@@ -374,8 +375,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_fp8_kernel(con
             const int rr = (ib + k) / nh, h = h0 + (ib + k) - rr * nh;
             if (rr < n_rows) {
                 const uint4* src = row_of(h, r0 + tr + rr * ROWS);
-                wa[k] = __ldg(src + a);
-                wb[k] = __ldg(src + c);
+                wa[k] = src[a];
+                wb[k] = src[c];
             }
         }
 #pragma unroll
@@ -425,8 +426,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_fp8_kernel(con
     uint4 wa, wb;
     if (n_items > 0) {
         const uint4* src = row_of(h0, r0 + tr);
-        wa = __ldg(src + a);
-        wb = __ldg(src + c);
+        wa = src[a];
+        wb = src[c];
     }
     int h = h0, r = r0 + tr;
     for (int it = 0; it < n_items; ++it) {
@@ -434,8 +435,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_fp8_kernel(con
         const int hn = h + 1 < h1 ? h + 1 : h0, rn = h + 1 < h1 ? r : r + ROWS;
         if (it + 1 < n_items) {
             const uint4* src = row_of(hn, rn);
-            wa = __ldg(src + a);
-            wb = __ldg(src + c);
+            wa = src[a];
+            wb = src[c];
         }
         if (turns && h == h0 && h0 < p.H_kv) {  // a new row
 #pragma unroll

@@ -1399,6 +1399,8 @@ SinkPlan sink_plan(const BwdArgs& a, int n_kv, int D, int sms) {
     const size_t room = s.part < dq_bytes ? (dq_bytes - s.part) / slot : 0;
     s.chunks = static_cast<int>(std::min<size_t>(s.chunks, room / (static_cast<size_t>(a.BH) * s.tiles)));
     if (s.chunks < 2) s.chunks = 1;
+    // (a slot is as large as four bf16 tiles of dQ, so tiles * chunks <= n_kv / 4 and every
+    // chunk of every such tile has query tiles)
     // (an item's set-up and epilogue count as kSplitCtaSteps steps)
     const int other = window_steps + kSplitCtaSteps;
     s.cells = std::max(1, (n_kv + kSplitCtaSteps + other / 2) / other);

@@ -75,8 +75,6 @@ struct PagedLayout {
     static constexpr int kWarpRing = kStages * kSlot;
     static constexpr int kBytes = kPagedWarps * kWarpRing + 2048;  // + PagedShared
 };
-constexpr int kMinTiles = 2;  // per warp: below, its start and end cost more than they save
-constexpr int kMaxResults = 512;  // pieces of a segment: more cost the combine kernel more than they save
 
 struct PagedParams {
     const __nv_bfloat16* Q;
@@ -196,7 +194,7 @@ __device__ __forceinline__ float sum_over_g(float x) {
 }
 
 __device__ __forceinline__ int clamp_len(const PagedParams& p, int b) {
-    const int len = __ldg(p.lens + b);
+    const int len = p.lens[b];
     const long long cap = static_cast<long long>(p.max_pages) << p.shift;
     if (len < 0 || len > cap) {
         atomicCAS(p.err, 0u, kErrPage);
@@ -233,8 +231,8 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8, WHOLE>::kCtas
     PagedShared& sh = *reinterpret_cast<PagedShared*>(smem + kPagedWarps * L::kWarpRing);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     // Launched as a dependent of the kernel before it: its start-up overlaps that kernel's
-    // end.  Every thread waits here before it reads anything, so this grid ends after that
-    // one, whatever its blocks have to do.
+    // end.  Every thread waits here before it reads anything (by plain loads: the inputs may
+    // still be written until then), so this grid ends after that one.
     griddep_launch_dependents();
     griddep_wait();
     const uint32_t ring = smem_addr(smem) + warp * L::kWarpRing;
@@ -278,8 +276,8 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8, WHOLE>::kCtas
         }
         const uint32_t total = static_cast<uint32_t>(total_b) * segs_per_b, segs = static_cast<uint32_t>(p.B) * segs_per_b;
         const int per_cta = kPagedWarps / p.rwarps;  // shares of a CTA
-        // (no share is empty: with few tiles the last warps have none)
-        const uint32_t shares = max(1u, min(min(gridDim.x * per_cta, total / kMinTiles), segs * kMaxResults));
+        // (with few tiles the last warps have none)
+        const uint32_t shares = share_count(gridDim.x * per_cta, total, segs);
         cut = Shares(total, shares);
         for (int w = 0; w < per_cta; ++w) {
             const uint32_t c = blockIdx.x * per_cta + w;
@@ -353,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8, WHOLE>::kCtas
                 if constexpr (F8) {
                     if (page >= 0) {
                         const long long ph = static_cast<long long>(page) * p.H_kv + hk;
-                        k_s = __ldg(p.k_scale + ph);
-                        v_s = __ldg(p.v_scale + ph);
+                        k_s = p.k_scale[ph];
+                        v_s = p.v_scale[ph];
                     }
                 }
             }
@@ -430,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8, WHOLE>::kCtas
 #pragma unroll
                 for (int c = 0; c < kChunksK; ++c) {
                     uint4 w = make_uint4(0u, 0u, 0u, 0u);
-                    if (in) w = __ldg(reinterpret_cast<const uint4*>(src) + t4 + 4 * c);
+                    if (in) w = reinterpret_cast<const uint4*>(src)[t4 + 4 * c];
                     q[nt][2 * c][0] = w.x;
                     q[nt][2 * c][1] = w.y;
                     q[nt][2 * c + 1][0] = w.z;
@@ -444,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8, WHOLE>::kCtas
 #pragma unroll
                 for (int c = 0; c < 2 * kChunksK; ++c) {
                     w[c] = make_uint4(0u, 0u, 0u, 0u);
-                    if (in) w[c] = __ldg(reinterpret_cast<const uint4*>(src) + 2 * (t4 + 4 * (c >> 1)) + (c & 1));
+                    if (in) w[c] = reinterpret_cast<const uint4*>(src)[2 * (t4 + 4 * (c >> 1)) + (c & 1)];
                     const uint32_t e[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -1018,7 +1016,7 @@ size_t paged_workspace(const PagedCache& c, int H, int Nq, int window, int sinks
 
 long long paged_max_tiles(int B, int H, int H_kv, int Nq, int max_pages, int shift) {
     const long long groups = (static_cast<long long>(H / H_kv) * Nq + 63) / 64;
-    return groups * H_kv * B * ((static_cast<long long>(max_pages) << shift) / kPagedTile + 1);
+    return groups * H_kv * B * ((static_cast<long long>(max_pages) << shift) / kPagedTile + kSegmentTiles);
 }
 
 cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream) {

@@ -70,6 +70,16 @@ struct Shares {
     }
 };
 
+constexpr int kMinTiles = 2;      // per share: below, its start and end cost more than they save
+constexpr int kMaxResults = 512;  // pieces of a segment: more cost the combine kernel more than they save
+// Shares that `total` tiles of `segs` segments are cut into, for `warps` takers: at least
+// one, none of them empty.  (Past 2^20 segments the last bound is beyond any number of takers.)
+FA_HD uint32_t share_count(uint32_t warps, uint32_t total, uint32_t segs) {
+    const uint32_t few = total / kMinTiles, most = segs < (1u << 20) ? segs * kMaxResults : ~0u;
+    const uint32_t n = warps < few ? warps : few;
+    return n > most ? most : n > 0 ? n : 1u;
+}
+
 // A frequency (radians per position, the bits of a double) as turns per position: the
 // fractional part in units of 2^-64, so that position * result mod 2^64 is the angle's
 // exact place on the circle however far the position.  Integer arithmetic throughout

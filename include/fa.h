@@ -256,9 +256,9 @@ FA_API fa_status fa_fwd_decode(const void* Q, const void* K, const void* V, void
  * d 64 or 128 (else FA_ERR_UNSUPPORTED).  Table and lengths are device data, read on the stream, so a
  * captured call can be replayed while they change.  Entries behind a sequence's
  * pages are not read.  A length below 0 or above max_pages * page_size, a page number
- * outside [0, num_pages) that is needed, and token counts that do not ascend within
- * [0, T] are not followed: fa_last_device_error then returns FA_ERR_PAGE, and each
- * entry point says what it did instead.  The description itself is host memory and
+ * outside [0, num_pages) that is needed, and a sequence's token counts that do not
+ * ascend within [0, T] are not followed: fa_last_device_error then returns FA_ERR_PAGE,
+ * and each entry point says what it did instead.  The description itself is host memory and
  * only read during the call; the caller owns all buffers.
  */
 typedef struct fa_paged_cache {
@@ -289,8 +289,10 @@ typedef struct fa_paged_cache {
  * (x cos a - y sin a, y cos a + x sin a), a = p * inv_freq[c] (device double
  * [rot / 2], radians per position), exact at any position and rounded once to bf16.
  * rot = 0 with inv_freq NULL (and no q): nothing turns.
- * A token whose position or page is out of bounds is not stored (FA_ERR_PAGE); its
- * query is rotated all the same.  No two sequences may append to the same page.
+ * A token whose position, page or sequence's counts are out of bounds is not stored
+ * (FA_ERR_PAGE); its query is rotated all the same.  No two sequences may append to the
+ * same page.  K, V, the scales and q_out must not overlap what else the call reads or
+ * writes (q_out = q aside).
  */
 FA_API fa_status fa_kv_append(const fa_paged_cache* cache, const void* k, long long k_st,
                               long long k_sh, const void* v, long long v_st, long long v_sh, int T,
@@ -329,7 +331,9 @@ FA_API fa_status fa_kv_append_fp8(const fa_paged_cache* cache, const void* k, lo
  * strides in elements, columns contiguous, 16-byte aligned, strides multiples of 8 and not negative; O's
  * rows must not overlap.  LSE: fp32 [B][H][Nq] contiguous.  window = 0: none;
  * sinks > 0 needs a window.  Rows of a page behind a sequence's end, and keys hidden
- * from every row of the call, are never read.
+ * from every row of the call, are never read.  (A value that one row sees and another
+ * does not must be finite, as in the other entry points: the other row's weight is 0,
+ * and 0 times infinity is NaN.)
  * workspace: fa_paged_workspace_size bytes (from the sizes alone, not the lengths; 0 for
  * small tables); NULL: taken with cudaMallocAsync and given back.  Two calls that may run at the same time
  * need two workspaces.  A length out of bounds is cut to the table's, and keys on a

@@ -285,6 +285,19 @@ def test_bad_token_counts_store_nothing(fp8):
     api.last_device_error()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_counts_past_the_tokens_store_nothing_of_their_sequence(fp8):
+    s = build([4, 10], [3, 10], 2, 2, 64, 16, fp8, seed=802)
+    want = run(s, freqs(64), False)
+    q, got = run(dict(s, cu=torch.tensor([0, 3, 14], dtype=torch.int32)), freqs(64), False)
+    assert api.last_device_error() == _lib.FA_ERR_PAGE
+    assert torch.equal(q, want[0])
+    pages = s["table"][1].long()
+    for n in ("kc", "vc"):
+        assert torch.equal(got[n][pages], s[n][pages])
+        assert torch.equal(got[n][int(s["table"][0, 0])], want[1][n][int(s["table"][0, 0])])
+
+
 def test_replayed_graph_follows_lengths_and_values():
     page, d, Hkv, H = 16, 128, 2, 4
     s = build([15, 3], [30, 30], Hkv, H, d, page, False, seed=900)

@@ -282,6 +282,108 @@ def test_bad_pages_are_hidden_and_reported(fp8):
     check(s, got=(o, lse), seqs=[2, 3])
 
 
+def test_errors_of_the_library_are_raised():
+    s = build([100], 2, 1, 1, 64, 16, False, seed=40)
+    q = s["q"].to(DEV).expand(1, 2, 9, 64).contiguous()
+    with pytest.raises(_lib.FAError) as e:
+        api.fwd_paged(q, *(s[n].to(DEV) for n in ("kc", "vc", "table", "lens")))
+    assert e.value.code == _lib.FA_ERR_UNSUPPORTED
+    with pytest.raises(_lib.FAError) as e:
+        api.fwd_paged(s["q"].to(DEV), *(s[n].to(DEV) for n in ("kc", "vc", "table", "lens")), tau=-1.0)
+    assert e.value.code == _lib.FA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("longest", [200, 3000])
+def test_calls_in_a_row_wait_for_one_another(fp8, longest):
+    """Each call's inputs are written by the kernel right before it, without a pause between: the same
+    bits as with one after each."""
+    H, Hkv, d, page = 8, 2, 128, 64
+    lens = [longest, 1, longest // 2]
+    s = build(lens, H, Hkv, 1, d, page, fp8, seed=41, one_scale=True)
+    room = (longest + 30) // page + 1
+    P = 3 * room
+    table = torch.arange(P, dtype=torch.int32).reshape(3, room).to(DEV)
+    x0 = torch.randn(3, H + 2 * Hkv, d, generator=torch.Generator().manual_seed(42)).to(torch.bfloat16).to(DEV)
+    f = (10000.0 ** (-torch.arange(d // 2, dtype=torch.float64) * 2 / d)).to(DEV)
+    outs = []
+    for pause in (True, False):
+        kc, vc = (torch.zeros(P, Hkv, page, d, dtype=torch.uint8 if fp8 else torch.bfloat16, device=DEV) for _ in "kv")
+        ks, vs = ((torch.full((P, Hkv), 2.0 ** -7, device=DEV) for _ in "kv") if fp8 else (None, None))
+        ln, x, o = torch.tensor(lens, dtype=torch.int32, device=DEV), x0.clone(), None
+        q = torch.empty(3, H, d, dtype=torch.bfloat16, device=DEV)
+        out = torch.empty(3, H, 1, d, dtype=torch.bfloat16, device=DEV)
+        torch.cuda.synchronize()
+        for i in range(25):
+            x.mul_(0.9375).add_(x.roll(1, 2), alpha=0.5)
+            for step in (lambda: api.kv_append(x[:, H:H + Hkv], x[:, H + Hkv:], kc, vc, table, ln, q=x[:, :H],
+                                               inv_freq=f, k_scale=ks, v_scale=vs, q_out=q),
+                         lambda: ln.add_(1),
+                         lambda: api.fwd_paged(q.unsqueeze(2), kc, vc, table, ln, k_scale=ks, v_scale=vs, out=out),
+                         lambda: x[:, :H].copy_(out.squeeze(2))):
+                step()
+                if pause:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        outs.append((x.cpu(), kc.cpu(), vc.cpu(), out.cpu()))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+    assert bool(torch.isfinite(outs[0][3].float()).all()) and api.last_device_error() == _lib.FA_OK
+
+
+@pytest.mark.parametrize("longest", [200, 3000])
+def test_captured_behind_a_copy_and_a_join(longest):
+    """A graph in which the calls follow a copy, a fork and a join of streams, and two graphs with buffers
+    of their own that run at the same time."""
+    H, Hkv, d, page = 8, 2, 64, 16
+    s = build([longest - 1, 77], H, Hkv, 1, d, page, False, seed=43, poison=False)
+    dev = {n: s[n].to(DEV) for n in ("kc", "vc", "table", "lens")}
+    g = torch.Generator().manual_seed(44)
+    xs = [torch.randn(2, H + 2 * Hkv, d, generator=g).to(torch.bfloat16).to(DEV) for _ in range(3)]
+    f = (10000.0 ** (-torch.arange(d // 2, dtype=torch.float64) * 2 / d)).to(DEV)
+
+    def step(st, fork):
+        st["x"].copy_(st["src"])
+        main = torch.cuda.current_stream()
+        fork.wait_stream(main)
+        with torch.cuda.stream(fork):
+            st["ln"].copy_(dev["lens"])
+            st["ln1"].copy_(dev["lens"]).add_(1)
+        st["x"].mul_(2.0)
+        main.wait_stream(fork)
+        q = api.kv_append(st["x"][:, H:H + Hkv], st["x"][:, H + Hkv:], st["kc"], st["vc"], dev["table"], st["ln"],
+                          q=st["x"][:, :H], inv_freq=f)
+        o, lse = api.fwd_paged(q.unsqueeze(2), st["kc"], st["vc"], dev["table"], st["ln1"])
+        st["o"].copy_(o)
+
+    def state():
+        return dict(src=xs[0].clone(), x=torch.zeros_like(xs[0]), kc=dev["kc"].clone(), vc=dev["vc"].clone(),
+                    ln=torch.zeros_like(dev["lens"]), ln1=torch.zeros_like(dev["lens"]),
+                    o=torch.zeros(2, H, 1, d, dtype=torch.bfloat16, device=DEV))
+    fork, sides = torch.cuda.Stream(), [torch.cuda.Stream(), torch.cuda.Stream()]
+    want, ref = [], state()
+    for x in xs:
+        ref["src"].copy_(x)
+        step(ref, fork)
+        torch.cuda.synchronize()
+        want.append(ref["o"].clone())
+    states, graphs = [state(), state()], [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for st, gr in zip(states, graphs):
+        with torch.cuda.graph(gr):
+            step(st, fork)
+    for i in range(6):
+        for k in range(2):
+            states[k]["src"].copy_(xs[(i + k) % 3])
+        torch.cuda.synchronize()
+        for side, gr in zip(sides, graphs):
+            with torch.cuda.stream(side):
+                gr.replay()
+        torch.cuda.synchronize()
+        for k in range(2):
+            assert torch.equal(states[k]["o"], want[(i + k) % 3])
+    assert api.last_device_error() == _lib.FA_OK
+
+
 def test_two_streams_two_workspaces():
     a, b = build([3000, 10, 500], 8, 2, 1, 128, 64, False, seed=16), build([2500], 8, 2, 2, 128, 64, True, seed=17)
     dev = [{n: (t.to(DEV) if t is not None else None) for n, t in s.items()} for s in (a, b)]

@@ -28,6 +28,7 @@ void t_range(int len, int nq, int w, int s, int* o) {
 int t_key0(int len, int nq, int w, int s, int i) { return paged_range(len, nq, w, s).key0(i); }
 long long t_start(long long c, long long t, long long s) { return Shares(t, s).start(c); }
 long long t_share(long long x, long long t, long long s) { return Shares(t, s).of(x); }
+uint32_t t_count(uint32_t w, uint32_t t, uint32_t s) { return share_count(w, t, s); }
 uint64_t t_turn(uint64_t b) { return turn_fraction(b); }
 int t_exp(uint32_t b) { return page_scale_exp(b); }
 int t_reached(long long p, int n, int sh) { return pages_reached(p, n, sh); }
@@ -53,6 +54,7 @@ def shim(tmp_path_factory):
     L.t_exp.argtypes = [ctypes.c_uint32]
     L.t_reached.argtypes = [LL, I, I]
     L.t_unit.argtypes = [LL, I, I]
+    L.t_count.argtypes, L.t_count.restype = [ctypes.c_uint32] * 3, ctypes.c_uint32
     return L
 
 
@@ -101,6 +103,15 @@ def test_shares_cover_every_step_once(shim, total, shares):
         assert a < b
         for x in {a, (a + b) // 2, b - 1}:
             assert shim.t_share(x, total, shares) == c
+
+
+def test_share_counts(shim):
+    assert shim.t_count(608, 10 ** 6, 8) == 608
+    assert shim.t_count(608, 100, 8) == 50            # two tiles each
+    assert shim.t_count(608, 1, 1) == 1               # never none
+    assert shim.t_count(1824, 10 ** 6, 1) == 512      # pieces of one segment
+    for segs in (2 ** 20 - 1, 2 ** 20, 2 ** 23, 2 ** 29, 2 ** 31 - 1):   # beyond 32 bits times that
+        assert shim.t_count(1824, 2 ** 31 - 1, segs) == 1824
 
 
 def test_turns_are_exact_far_out(shim):
@@ -214,12 +225,31 @@ NO_Q = dict(q=None, q_out=None, H=0)
     (dict(q_out=FAKE + 11 * GB, qo_st=512), _lib.FA_ERR_INVALID_ARG),
     (dict(qo_st=0), _lib.FA_ERR_INVALID_ARG),     # rows on top of each other
     (dict(q_out=FAKE + 8 * GB), _lib.FA_ERR_INVALID_ARG),       # over k
+    (dict(q_out=FAKE + 5 * GB), _lib.FA_ERR_INVALID_ARG),       # over lens
+    (dict(q_out=FAKE + 4 * GB + 16), _lib.FA_ERR_INVALID_ARG),  # over the page table
+    (dict(inv_freq=FAKE + 128), _lib.FA_ERR_INVALID_ARG),       # inside the cache
+    (dict(cu_new=FAKE + GB), _lib.FA_ERR_INVALID_ARG),
     (dict(T=0), _lib.FA_OK),
     (dict(T=0, k=None, v=None, **NO_Q), _lib.FA_OK),
 ])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_append_refuses(kw, code, fp8):
     assert append(cache(fp8), fp8, **kw) == code
+
+
+def test_a_cache_over_its_own_table_or_scales_is_refused():
+    assert append(cache(page_table=FAKE + 64)) == _lib.FA_ERR_INVALID_ARG
+    assert append(cache(lens=FAKE + GB)) == _lib.FA_ERR_INVALID_ARG
+    assert append(cache(True, k_scale=FAKE + 64), True) == _lib.FA_ERR_INVALID_ARG
+    assert append(cache(True, k_scale=FAKE + 3 * GB + 4), True) == _lib.FA_ERR_INVALID_ARG
+    assert append(cache(True, v_scale=FAKE + 5 * GB), True) == _lib.FA_ERR_INVALID_ARG
+
+
+def test_queries_without_key_heads_are_refused():
+    assert append(cache(H_kv=0)) == _lib.FA_ERR_INVALID_ARG
+    assert append(cache(H_kv=0), **NO_Q) == _lib.FA_OK
+    assert paged(cache(H_kv=0)) == _lib.FA_ERR_INVALID_ARG
+    assert paged(cache(H_kv=0), H=0) == _lib.FA_OK
 
 
 def test_a_cache_of_the_other_kind_is_refused():
@@ -274,6 +304,8 @@ def test_paged_refuses(kw, code, fp8):
 
 def test_too_many_tiles_are_refused():
     assert paged(cache(B=4096, H_kv=2, max_pages=2 ** 22)) == _lib.FA_ERR_UNSUPPORTED
+    # a segment counts as three tiles more than its keys fill
+    assert paged(cache(B=2 ** 23, H_kv=2, max_pages=125), q_sb=512, o_sb=512) == _lib.FA_ERR_UNSUPPORTED
 
 
 def test_workspace_sizes():
