@@ -62,16 +62,19 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kGrow = 8.0f;  // log2 units: weights stay <= 2^8
 enum : uint32_t { kSitePagedSmem = 51 };
 
-// Ring slots per warp and CTAs per SM: about 128 KB in flight per SM, as much as the
-// copy bandwidth times the memory's latency asks for (45 GB/s x ~1.5 us per SM).
-template <int D, int NT, bool F8, bool WHOLE = false>
+// Ring slots per warp and CTAs per SM: 130 to 200 KB of slots per SM, and as many warps as
+// the registers allow, since a tile's chain of dependent instructions takes a warp as long
+// as its bytes take to come (12 warps of two slots against 8 of three: 96 sequences of up to
+// 12000 e4m3 keys 200 -> 193 us, 48 of up to 16384 bf16 keys 296 -> 291; 16 query rows at
+// d = 128 do not fit 168 registers and keep 8: spilled, 54 -> 56 us and e4m3 41 -> 52).
+template <int D, int NT, bool F8>
 struct PagedLayout {
     static constexpr int kRow = D * (F8 ? 1 : 2);       // bytes of a key row
     static constexpr int kTile = kPagedTile * kRow;     // K or V of one tile
     static constexpr int TP = kTile == 4096 ? 1 : 2;    // tiles per slot and loop iteration
     static constexpr int kSlot = 2 * TP * kTile;
-    static constexpr int kCtas = WHOLE && NT == 1 ? (kSlot == 8192 ? 3 : 4) : kSlot == 8192 ? 2 : 3;
-    static constexpr int kStages = WHOLE && NT == 1 ? (kSlot == 8192 ? 2 : 3) : kSlot == 8192 ? 3 : 4;
+    static constexpr int kCtas = kSlot == 8192 ? (NT == 1 || D == 64 ? 3 : 2) : NT == 1 ? 4 : 3;
+    static constexpr int kStages = kSlot == 8192 ? (kCtas == 3 ? 2 : 3) : NT == 1 ? 3 : 4;
     static constexpr int kWarpRing = kStages * kSlot;
     static constexpr int kBytes = kPagedWarps * kWarpRing + 2048;  // + PagedShared
 };
@@ -219,8 +222,8 @@ static_assert(sizeof(PagedShared) <= kSharedBytes, "the shared block fits its pl
 // WHOLE: a block takes one segment, its warps the tiles in turn, and joins their results
 // in shared memory: no partial results, no second kernel.  For short segments.
 template <int D, int NT, bool F8, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8, WHOLE>::kCtas) fa_paged_kernel(const PagedParams p) {
-    using L = PagedLayout<D, NT, F8, WHOLE>;
+__global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_paged_kernel(const PagedParams p) {
+    using L = PagedLayout<D, NT, F8>;
     constexpr int ROW = L::kRow, CH = ROW / 16, S = L::kStages, TP = L::TP;
     using W = Swizzle<ROW>;
     constexpr int R = 8 * NT;           // query rows of a segment
@@ -983,12 +986,11 @@ cudaError_t launch_paged_t(const PagedArgs& a, const PagedPlan& pl, PagedParams&
     using L = PagedLayout<D, NT, F8>;
     constexpr auto kern = &fa_paged_kernel<D, NT, F8, false>;
     constexpr auto kern_w = &fa_paged_kernel<D, NT, F8, true>;
-    using LW = PagedLayout<D, NT, F8, true>;
-    cudaError_t e = pl.whole ? set_max_dyn_smem_once<kern_w>(LW::kBytes) : set_max_dyn_smem_once<kern>(L::kBytes);
+    cudaError_t e = pl.whole ? set_max_dyn_smem_once<kern_w>(L::kBytes) : set_max_dyn_smem_once<kern>(L::kBytes);
     if (e != cudaSuccess) return e;
     if (pl.whole) {
         if (a.ev_start) cudaEventRecord(a.ev_start, stream);
-        e = launch_dependent(kern_w, dim3(static_cast<unsigned>(pl.segs)), dim3(kThreads), LW::kBytes, stream, p);
+        e = launch_dependent(kern_w, dim3(static_cast<unsigned>(pl.segs)), dim3(kThreads), L::kBytes, stream, p);
         if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
         return e;
     }
