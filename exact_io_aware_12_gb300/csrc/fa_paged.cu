@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
         }
         // ---- this piece's result ----
         const bool final_piece = u0 == 0 && u1 >= rg.n;
-        const long long slot = 2ll * (static_cast<long long>(blockIdx.x) * kPagedWarps + warp) + (u0 == 0 ? 1 : 0);
+        const long long slot = 2ll * (static_cast<long long>(share) * p.rwarps + rw) + (u0 == 0 ? 1 : 0);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -808,126 +808,160 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
     }
 }
 
-// Adds a segment's pieces: O = sum_s 2^(l_s - L) O_s, L = log2 sum_s 2^(l_s).  Block
-// (segment, y) takes the rows y, y + gridDim.y, ...  With few pieces a warp adds a row by
-// itself, its loads all in flight at once; with many, the block's warps take them in turn,
-// eight at a time, and are added in warp order.
+// Adds a segment's pieces: O = sum_s 2^(l_s - L) O_s, L = log2 sum_s 2^(l_s), in order.
+// With few pieces per segment (on average, over full tables) a warp adds a row by itself,
+// eight pieces' loads in flight at once; block (segment, y) takes the rows y, y + gridDim.y,
+// ...  With many, block (segment, row, z) takes D / gridDim.z columns of one row, each warp 32
+// of them and 32 pieces at a time: eight lanes to a piece's 128 bytes, eight loads in flight.
 constexpr int kFewPieces = 16;
+constexpr int kCombineWarps = 16;
 
-template <int D, int NT>
-__global__ void __launch_bounds__(1024) fa_paged_combine_kernel(const PagedParams p) {
+template <int D, int NT, bool MANY>
+__global__ void __launch_bounds__(32 * (MANY ? kCombineWarps : 8)) fa_paged_combine_kernel(const PagedParams p) {
     constexpr int R = 8 * NT, PER = D / 32, kBatch = 8;
-    __shared__ float red[32][D];
-    __shared__ float red_l[32];
     const int segs_per_b = p.H_kv * p.rgroups;
     const int b = static_cast<int>(blockIdx.x) / segs_per_b, in_b = static_cast<int>(blockIdx.x) - b * segs_per_b;
     const int hk = in_b / p.rgroups, row0 = (in_b - hk * p.rgroups) * p.rwarps * R;
     const int rows = min(p.rwarps * R, p.G * p.Nq - row0);
-    const int per_cta = kPagedWarps / p.rwarps, warps = static_cast<int>(blockDim.x >> 5);
+    const int warps = static_cast<int>(blockDim.x >> 5);
     const int warp = static_cast<int>(threadIdx.x >> 5), lane = threadIdx.x & 31;
     griddep_wait();
     const int2 sg = p.seg[blockIdx.x];
     const int n = sg.y;
     if (n <= 1) return;
-    const bool few = n <= kFewPieces;
-    const int rstep = static_cast<int>(gridDim.y) * (few ? warps : 1);
-    for (int row = static_cast<int>(blockIdx.y) + (few ? warp * static_cast<int>(gridDim.y) : 0); row < rows; row += rstep) {
+    const int row_step = MANY ? rows : static_cast<int>(gridDim.y) * warps;
+    for (int row = static_cast<int>(blockIdx.y) + (MANY ? 0 : warp * static_cast<int>(gridDim.y)); row < rows; row += row_step) {
         const int rw = row / R, r = row - rw * R;
         // piece 0 lies in its warp's second slot (it ends the share), the others in their first
         const auto at = [&](int s) {
-            const int share = sg.x + s;
-            const long long w = static_cast<long long>(share / per_cta) * kPagedWarps + share % per_cta * p.rwarps + rw;
+            const long long w = static_cast<long long>(sg.x + s) * p.rwarps + rw;
             return (2 * w + (s == 0 ? 1 : 0)) * R + r;
         };
-        float sum = 0.f, ref;
-        float acc[PER];
-#pragma unroll
-        for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-        // pieces s0 .. s0 + 7 (below n), their weights in w of lanes 0 .. 7
-        float v[kBatch][PER];
-        const auto load = [&](int s0) {
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                if (s0 + k < n) {
-                    const float* src = p.part_o + at(s0 + k) * D + lane * PER;
-                    if constexpr (PER == 4) {
-                        const float4 y = *reinterpret_cast<const float4*>(src);
-                        v[k][0] = y.x;
-                        v[k][1] = y.y;
-                        v[k][2] = y.z;
-                        v[k][3] = y.w;
-                    } else {
-                        const float2 y = *reinterpret_cast<const float2*>(src);
-                        v[k][0] = y.x;
-                        v[k][1] = y.y;
-                    }
-                }
-            }
-        };
-        const auto add = [&](int s0, float w) {
-#pragma unroll
-            for (int k = 0; k < kBatch; ++k) {
-                const float wk = __shfl_sync(0xffffffffu, w, k);
-                if (s0 + k < n) {
-#pragma unroll
-                    for (int e = 0; e < PER; ++e) acc[e] = fmaf(wk, v[k][e], acc[e]);
-                }
-            }
-        };
-        if (few) {
-            load(0);
-            const float l = lane < n ? p.part_l[at(lane)] : -INFINITY;
-            float m = l;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            ref = m == -INFINITY ? 0.f : m;
-            const float w = ex2(l - ref);
-            sum = w;
-            add(0, w);
-            if (n > kBatch) {
-                load(kBatch);
-                add(kBatch, __shfl_down_sync(0xffffffffu, w, kBatch));
-            }
-        } else {
+        const int hh = (row0 + row) / p.Nq, qi = (row0 + row) - hh * p.Nq, h = hk * p.G + hh;
+        __nv_bfloat16* dst = p.O + b * p.o_sb + static_cast<long long>(h) * p.o_sh + qi * p.o_sn;
+        float* lse = p.LSE + (static_cast<long long>(b) * p.H + h) * p.Nq + qi;
+        if constexpr (MANY) {
+            __shared__ float red[kCombineWarps][32], red_l[kCombineWarps], red_m[kCombineWarps];
+            const int cw = D / 32 / static_cast<int>(gridDim.z), cg = warp % cw;  // 32-column groups of the block
+            const int sub = lane >> 3, col = 32 * (static_cast<int>(blockIdx.z) * cw + cg) + 4 * (lane & 7);
+            const int group = warp / cw, groups = warps / cw;  // of pieces
             float m = -INFINITY;
             for (int s = threadIdx.x; s < n; s += blockDim.x) m = fmaxf(m, p.part_l[at(s)]);
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            __syncthreads();  // (the row before has been written)
-            if (lane == 0) red_l[warp] = m;
+            if (lane == 0) red_m[warp] = m;
             __syncthreads();
-            for (int k = 0; k < warps; ++k) m = fmaxf(m, red_l[k]);
-            __syncthreads();
-            ref = m == -INFINITY ? 0.f : m;
-            for (int s0 = warp * kBatch; s0 < n; s0 += warps * kBatch) {
-                load(s0);
-                const float w = lane < min(kBatch, n - s0) ? ex2(p.part_l[at(s0 + lane)] - ref) : 0.f;
-                sum += w;
-                add(s0, w);
+            for (int k = 0; k < warps; ++k) m = fmaxf(m, red_m[k]);
+            const float ref = m == -INFINITY ? 0.f : m;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            float sum = 0.f;
+            for (int s0 = group * 4 * kBatch; s0 < n; s0 += groups * 4 * kBatch) {
+                float4 v[kBatch];
+                float l[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int s = s0 + 4 * k + sub;
+                    if (s < n) {
+                        l[k] = p.part_l[at(s)];
+                        v[k] = *reinterpret_cast<const float4*>(p.part_o + at(s) * D + col);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    if (s0 + 4 * k + sub < n) {
+                        const float w = ex2(l[k] - ref);
+                        sum += w;
+                        acc.x = fmaf(w, v[k].x, acc.x);
+                        acc.y = fmaf(w, v[k].y, acc.y);
+                        acc.z = fmaf(w, v[k].z, acc.z);
+                        acc.w = fmaf(w, v[k].w, acc.w);
+                    }
+                }
             }
-        }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (!few) {
-#pragma unroll
-            for (int e = 0; e < PER; ++e) red[warp][lane * PER + e] = acc[e];
+            for (int o = 8; o < 32; o <<= 1) {
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+                acc.y += __shfl_xor_sync(0xffffffffu, acc.y, o);
+                acc.z += __shfl_xor_sync(0xffffffffu, acc.z, o);
+                acc.w += __shfl_xor_sync(0xffffffffu, acc.w, o);
+            }
+            if (sub == 0) *reinterpret_cast<float4*>(&red[warp][4 * (lane & 7)]) = acc;
             if (lane == 0) red_l[warp] = sum;
             __syncthreads();
-            if (warp > 0) continue;
-            for (int k = 1; k < warps; ++k) {
+            if (group > 0) return;
+            sum = 0.f;
+            float o = 0.f;
+            for (int k = cg; k < warps; k += cw) {
                 sum += red_l[k];
-#pragma unroll
-                for (int e = 0; e < PER; ++e) acc[e] += red[k][lane * PER + e];
+                o += red[k][lane];
             }
+            o = sum == 0.f ? 0.f : o / sum;  // (0: the row sees nothing)
+            const float o1 = __shfl_down_sync(0xffffffffu, o, 1);
+            if ((lane & 1) == 0) *reinterpret_cast<uint32_t*>(dst + col - 4 * (lane & 7) + lane) = pack_bf16(o, o1);
+            if (threadIdx.x == 0 && blockIdx.z == 0) *lse = (ref + lg2(sum)) * kLn2;
+        } else {
+            float acc[PER], v[kBatch][PER];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+            // pieces s0 .. s0 + 7 (below n)
+            const auto load = [&](int s0) {
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    if (s0 + k < n) {
+                        const float* src = p.part_o + at(s0 + k) * D + lane * PER;
+                        if constexpr (PER == 4) {
+                            const float4 y = *reinterpret_cast<const float4*>(src);
+                            v[k][0] = y.x;
+                            v[k][1] = y.y;
+                            v[k][2] = y.z;
+                            v[k][3] = y.w;
+                        } else {
+                            const float2 y = *reinterpret_cast<const float2*>(src);
+                            v[k][0] = y.x;
+                            v[k][1] = y.y;
+                        }
+                    }
+                }
+            };
+            // ... with the weights of lanes from on
+            const auto add = [&](int s0, float w, int from) {
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const float wk = __shfl_sync(0xffffffffu, w, from + k);
+                    if (s0 + k < n) {
+#pragma unroll
+                        for (int e = 0; e < PER; ++e) acc[e] = fmaf(wk, v[k][e], acc[e]);
+                    }
+                }
+            };
+            load(0);
+            const float l = lane < n ? p.part_l[at(lane)] : -INFINITY;
+            float m = l;
+            for (int s = lane + 32; s < n; s += 32) m = fmaxf(m, p.part_l[at(s)]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float ref = m == -INFINITY ? 0.f : m;
+            float w = ex2(l - ref), sum = w;
+            add(0, w, 0);
+            for (int s0 = kBatch; s0 < n; s0 += kBatch) {
+                load(s0);
+                if ((s0 & 31) == 0) {  // (the next 32 pieces' weights, one per lane)
+                    w = s0 + lane < n ? ex2(p.part_l[at(s0 + lane)] - ref) : 0.f;
+                    sum += w;
+                }
+                add(s0, w, s0 & 31);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (0: the row sees nothing)
+            if constexpr (PER == 4)
+                *reinterpret_cast<uint2*>(dst + lane * PER) =
+                    make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+            else
+                *reinterpret_cast<uint32_t*>(dst + lane * PER) = pack_bf16(acc[0] * inv, acc[1] * inv);
+            if (lane == 0) *lse = (ref + lg2(sum)) * kLn2;
         }
-        const int hh = (row0 + row) / p.Nq, qi = (row0 + row) - hh * p.Nq, h = hk * p.G + hh;
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (0: the row sees nothing)
-        __nv_bfloat16* dst = p.O + b * p.o_sb + static_cast<long long>(h) * p.o_sh + qi * p.o_sn + lane * PER;
-        if constexpr (PER == 4)
-            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-        else
-            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
-        if (lane == 0) p.LSE[(static_cast<long long>(b) * p.H + h) * p.Nq + qi] = (ref + lg2(sum)) * kLn2;
     }
 }
 
@@ -998,14 +1032,21 @@ cudaError_t launch_paged_t(const PagedArgs& a, const PagedPlan& pl, PagedParams&
     // (no more CTAs than a full table gives kMinTiles per warp)
     const int ctas = static_cast<int>(std::min<long long>(pl.ctas, pl.tiles * pl.rwarps / (kMinTiles * kPagedWarps) + 1));
     e = launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), L::kBytes, stream, p);
-    // pieces of an average segment: few, a block with a warp per row; many, a block per row
+    // pieces of an average segment of full tables
     const long long pieces = static_cast<long long>(ctas) * kPagedWarps / (pl.segs * pl.rwarps) + 1;
     const long long rows = std::min(p.G * p.Nq, 8 * NT * pl.rwarps);
-    const unsigned threads = pieces > 128 ? 1024 : pieces > kFewPieces ? 256 : static_cast<unsigned>(32 * std::min(8ll, rows));
-    const long long y = pieces > kFewPieces ? rows : (rows + 7) / 8;
-    if (e == cudaSuccess)
-        e = launch_dependent(fa_paged_combine_kernel<D, NT>, dim3(static_cast<unsigned>(pl.segs), static_cast<unsigned>(y)),
-                             dim3(threads), 0, stream, p);
+    const unsigned segs = static_cast<unsigned>(pl.segs);
+    if (e == cudaSuccess && pieces > kFewPieces) {
+        // (a row's columns in one block while that block's warps suffice for the pieces)
+        const long long groups = (std::min<long long>(pieces, kMaxResults) + 31) / 32;
+        const unsigned z = groups * (D / 32) > kCombineWarps ? D / 32 : 1;
+        const long long warps = std::min<long long>(kCombineWarps, groups * (D / 32 / z));
+        e = launch_dependent(fa_paged_combine_kernel<D, NT, true>, dim3(segs, static_cast<unsigned>(rows), z),
+                             dim3(static_cast<unsigned>(32 * warps)), 0, stream, p);
+    } else if (e == cudaSuccess) {
+        e = launch_dependent(fa_paged_combine_kernel<D, NT, false>, dim3(segs, static_cast<unsigned>((rows + 7) / 8)),
+                             dim3(static_cast<unsigned>(32 * std::min(8ll, rows))), 0, stream, p);
+    }
     if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
     return e;
 }

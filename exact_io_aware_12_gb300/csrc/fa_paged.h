@@ -71,7 +71,7 @@ struct Shares {
 };
 
 constexpr int kMinTiles = 2;      // per share: below, its start and end cost more than they save
-constexpr int kMaxResults = 512;  // pieces of a segment: more cost the combine kernel more than they save
+constexpr int kMaxResults = 1024; // pieces of a segment: more cost the combine kernel more than they save
 // Shares that `total` tiles of `segs` segments are cut into, for `warps` takers: at least
 // one, none of them empty.  (Past 2^20 segments the last bound is beyond any number of takers.)
 FA_HD uint32_t share_count(uint32_t warps, uint32_t total, uint32_t segs) {

@@ -109,7 +109,7 @@ def test_share_counts(shim):
     assert shim.t_count(608, 10 ** 6, 8) == 608
     assert shim.t_count(608, 100, 8) == 50            # two tiles each
     assert shim.t_count(608, 1, 1) == 1               # never none
-    assert shim.t_count(1824, 10 ** 6, 1) == 512      # pieces of one segment
+    assert shim.t_count(1824, 10 ** 6, 1) == 1024     # pieces of one segment
     for segs in (2 ** 20 - 1, 2 ** 20, 2 ** 23, 2 ** 29, 2 ** 31 - 1):   # beyond 32 bits times that
         assert shim.t_count(1824, 2 ** 31 - 1, segs) == 1824
 
