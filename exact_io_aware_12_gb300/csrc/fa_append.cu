@@ -16,13 +16,19 @@
 // (exactly, but for values that fall among the subnormals, which round to nearest even).
 //
 // Both kernels only move bytes: each input is read and each output written once (the
-// 8-bit kernel reads its rows twice, the second time from L1/L2).  A thread owns 16
+// 8-bit kernel reads its rows twice, the second time from L1/L2).  For 21k tokens of
+// prompts (32 query and 8 key heads of 128, 524 MB) the bf16 kernel takes 85 us, 6.2 TB/s
+// or 91% of the copy bandwidth; into e4m3 pages (481 MB) 83 us, 5.8 TB/s: there the pages'
+// blocks compute (scale, rotate, round) about as long as they load.  One token of 64
+// sequences takes 4.3 and 6.1 us, which is launch and the latency of four dependent loads
+// (counts, length, page, row).  A thread owns 16
 // columns of a token (two 16-byte pieces that rotate into each other) and walks heads;
 // what a token costs besides (its sequence, page, sines and cosines) is found once per
 // block or held in registers over the heads.
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "fa_internal.h"
 #include "fa_paged.h"
@@ -47,8 +53,8 @@ struct AppendParams {
     long long q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh;  // elements
     int T, B, H, H_kv, rot, interleaved, num_pages, max_pages, shift;
     int groups;               // head groups (bf16: grid y)
-    int kv_blocks, q_groups;  // 8-bit: kv_blocks * groups blocks for the pages, then q_groups
-                              // per block of rows for the queries
+    int q_groups;             // 8-bit: blocks per block of rows for the queries
+    int lead, kv_blocks;      // 8-bit: blocks for the pages, in all and before the first for queries
     unsigned int* err;
 };
 
@@ -271,11 +277,13 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const A
     append_rows<D>(p, sh, static_cast<int>(blockIdx.x) * RowShared<D>::kTokens, h0, min(n, h0 + per));
 }
 
-__device__ __forceinline__ float amax8(const uint4& w, float m) {
-    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+// The largest magnitude of 16 bf16 values, two at a time (NaN is passed over: m starts at 0).
+__device__ __forceinline__ float amax16(const uint4& a, const uint4& b) {
+    const uint32_t x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t m = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m = fmaxf(m, fmaxf(fabsf(lo_f(x[i])), fabsf(hi_f(x[i]))));  // (NaN is passed over)
-    return m;
+    for (int i = 0; i < 8; ++i) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x[i] & 0x7fff7fffu));
+    return fmaxf(lo_f(m), hi_f(m));
 }
 
 // Four e4m3 codes rescaled by r (rounded to nearest even).
@@ -286,6 +294,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
     return pack_e4m3x4(a.x * r, a.y * r, b.x * r, b.y * r);
 }
 
+constexpr int kGroupCost = 3;
 constexpr int kMaxGroupHeads = 16;  // heads (of the list [K | V]) that one team walks
 
 struct PageShared {
@@ -308,9 +317,15 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_fp8_kernel(con
     } sh;
     griddep_launch_dependents();
     griddep_wait();
+    // The blocks for the pages compute more and take longer, those for the queries wait for
+    // memory: one of each in turn while there are pages, so that both share the SMs, with
+    // the pages first where they are more (lead).
     int bx = static_cast<int>(blockIdx.x);
-    if (bx >= p.kv_blocks * p.groups) {
-        bx -= p.kv_blocks * p.groups;
+    const int turn = bx - p.lead, pairs = p.kv_blocks - p.lead;
+    if (turn < 0 || (turn < 2 * pairs && (turn & 1) == 0)) {
+        bx = turn < 0 ? bx : p.lead + turn / 2;
+    } else {
+        bx = turn < 2 * pairs ? turn / 2 : turn - pairs;
         const int rb = bx / p.q_groups, per = (p.H + p.q_groups - 1) / p.q_groups, h0 = (bx - rb * p.q_groups) * per;
         if (h0 < p.H) append_rows<D>(p, sh.row, rb * RowShared<D>::kTokens, h0, min(p.H, h0 + per));
         return;
@@ -368,24 +383,30 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_fp8_kernel(con
     // 1. the largest magnitude of each head's new rows; four items' loads in flight
     const int most = (r1 - r0 + ROWS - 1) / ROWS * nh;  // (the same for the whole team)
     constexpr int kBatch = 4;
+    int rr = 0, hh = 0;  // row and head of the item to load next (counted: a division per item is dear)
     for (int ib = 0; ib < most; ib += kBatch) {
         uint4 wa[kBatch], wb[kBatch];
+        int head[kBatch];
+        bool mine[kBatch];  // (not past this thread's rows)
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int rr = (ib + k) / nh, h = h0 + (ib + k) - rr * nh;
-            if (rr < n_rows) {
-                const uint4* src = row_of(h, r0 + tr + rr * ROWS);
+            head[k] = hh;
+            mine[k] = rr < n_rows;
+            if (mine[k]) {
+                const uint4* src = row_of(h0 + hh, r0 + tr + rr * ROWS);
                 wa[k] = src[a];
                 wb[k] = src[c];
             }
+            const bool wrap = hh + 1 == nh;
+            hh = wrap ? 0 : hh + 1;
+            rr += wrap;
         }
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            const int rr = (ib + k) / nh, h = (ib + k) - rr * nh;
-            const float m = rr < n_rows ? amax8(wb[k], amax8(wa[k], 0.f)) : 0.f;
+            const float m = mine[k] ? amax16(wa[k], wb[k]) : 0.f;
             // (non-negative: the bits keep the order)
             const uint32_t mw = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-            if ((threadIdx.x & 31) == 0 && mw != 0u) atomicMax(&amax_s[h], mw);
+            if ((threadIdx.x & 31) == 0 && mw != 0u) atomicMax(&amax_s[head[k]], mw);
         }
     }
     sync();
@@ -512,24 +533,36 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
         const int n = p.H + 2 * p.H_kv;
         p.groups = static_cast<int>(std::max(1ll, std::min<long long>((kWantBlocks + row_blocks - 1) / row_blocks,
                                                                       (n + kHeadGroups - 1) / kHeadGroups)));
-        p.kv_blocks = p.q_groups = 0;
+        p.q_groups = p.lead = p.kv_blocks = 0;
         const dim3 grid(static_cast<unsigned>(row_blocks), static_cast<unsigned>(p.groups));
         return launch_dependent(d == 64 ? fa_kv_append_kernel<64> : fa_kv_append_kernel<128>, grid, dim3(kAppendThreads), 0,
                                 stream, p);
     }
-    // a warp per page where the sequences bring a token or a few each, else a block
+    // a warp per page where the sequences bring a token or a few each, else a block (32
+    // sequences of 4 tokens: 5.8 us by warps, 6.6 by blocks; of 8: 7.7 and 6.9)
     const bool warps = static_cast<long long>(a.T) <= 4ll * p.B;
     const long long units = (static_cast<long long>(a.T) >> p.shift) + 2ll * p.B;
-    const long long kv_blocks = warps ? (units + kAppendThreads / 32 - 1) / (kAppendThreads / 32) : units;
+    long long kv_blocks = warps ? (units + kAppendThreads / 32 - 1) / (kAppendThreads / 32) : units;
     const int n = 2 * p.H_kv;
-    p.groups = static_cast<int>(std::max<long long>((n + kMaxGroupHeads - 1) / kMaxGroupHeads,
-                                                    std::min<long long>((kWantBlocks + kv_blocks - 1) / kv_blocks, n)));
+    // Heads per group: a block takes as long as its heads and kGroupCost more (angles, scales,
+    // barriers); the least of the resident blocks' mean load and one block's length together
+    // (21k tokens, 16 heads of K and V: four groups 40 us, two, a little over one round, 44).
+    long long best = LLONG_MAX;
+    for (int per = std::min(n, kMaxGroupHeads); per >= 1; --per) {
+        const long long groups = (n + per - 1) / per, cost = (kv_blocks * groups + kWantBlocks) * (per + kGroupCost);
+        if (cost < best) {
+            best = cost;
+            p.groups = static_cast<int>(groups);
+        }
+    }
     p.q_groups = static_cast<int>(std::max(1ll, std::min<long long>((kWantBlocks + row_blocks - 1) / row_blocks,
                                                                     (p.H + kHeadGroups - 1) / kHeadGroups)));
-    const long long blocks = kv_blocks * p.groups + (p.H > 0 ? row_blocks * p.q_groups : 0);
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+    const long long q_blocks = p.H > 0 ? row_blocks * p.q_groups : 0;
+    kv_blocks *= p.groups;
+    if (kv_blocks + q_blocks > 0x3fffffffll) return cudaErrorInvalidValue;
     p.kv_blocks = static_cast<int>(kv_blocks);
-    const dim3 grid(static_cast<unsigned>(blocks));
+    p.lead = static_cast<int>(std::max(0ll, kv_blocks - q_blocks));
+    const dim3 grid(static_cast<unsigned>(kv_blocks + q_blocks));
     return launch_dependent(d == 64 ? (warps ? fa_kv_append_fp8_kernel<64, 32> : fa_kv_append_fp8_kernel<64, 256>)
                                     : (warps ? fa_kv_append_fp8_kernel<128, 32> : fa_kv_append_fp8_kernel<128, 256>),
                             grid, dim3(kAppendThreads), 0, stream, p);

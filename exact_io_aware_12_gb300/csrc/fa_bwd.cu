@@ -281,7 +281,7 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     // With sinks dS is formed from P before its rounding to bf16 and rounded once,
     // where the other masks multiply two rounded factors (dQ, dK rel-L2 3.4e-3 ->
     // 2.5e-3): kept in fp32 at d = 64 (no slower), as fp16 pairs at d = 128, where fp32
-    // spills (10% slower; the pairs cost 1.7%).  P <= 1, so fp16 is off by 2^-12 of it,
+    // spills (10% slower; the pairs cost 1.7%).  P <= 1, so fp16 is off by 2^-11 of it,
     // or 2^-25 in all below 2^-14.
     constexpr bool DS_FP32 = SINKS && D == 64, DS_FP16 = SINKS && D == 128;
     static_assert(!DS_FP16 || kQC == 32, "one chunk per warpgroup");

@@ -53,7 +53,8 @@ FA_HD PagedRange paged_range(int len, int nq, int window, int sinks) {
 }
 
 // Tiles counted for a segment: its own and, behind them, kSegmentTiles that stand for the
-// time in which a warp changes segments (and make an empty sequence count too).
+// time in which a warp changes segments (and make an empty sequence count too).  (1 and 6
+// were slower on uneven batches.)
 constexpr int kSegmentTiles = 3;
 FA_HD int paged_tiles(const PagedRange& r) { return r.n + kSegmentTiles; }
 
@@ -70,8 +71,12 @@ struct Shares {
     }
 };
 
-constexpr int kMinTiles = 2;      // per share: below, its start and end cost more than they save
-constexpr int kMaxResults = 1024; // pieces of a segment: more cost the combine kernel more than they save
+// Tiles of a share, at least: below, its start and end cost more than they save (one
+// sequence of 1500 keys, 8 key heads: 1 tile 11.2 us, 2 9.6, 4 10.1).
+constexpr int kMinTiles = 2;
+// Pieces of a segment: more cost the combine kernel more than they save (one segment of
+// 131072 keys: 512 pieces 19.5 us, 1024 17.4, 2048 21.8).
+constexpr int kMaxResults = 1024;
 // Shares that `total` tiles of `segs` segments are cut into, for `warps` takers: at least
 // one, none of them empty.  (Past 2^20 segments the last bound is beyond any number of takers.)
 FA_HD uint32_t share_count(uint32_t warps, uint32_t total, uint32_t segs) {
