@@ -51,9 +51,10 @@ constexpr int kBN = 128;  // keys per block
 // TILES = 2 (the default): two query tiles per CTA, 10 warps, all 512 tensor-
 // memory columns, one CTA per SM.  TILES = 1: one tile, 6 warps, 256 columns
 // and a smaller ring (5 slots at d = 64, 2 at d = 128), so two CTAs share an SM
-// and one's prologue and epilogue overlap the other's main loop: used for windows
-// with sinks and d = 64 block masks (d = 64 short sequences and d = 128 block masks have persistent
-// kernels of their own, fa_fwd_short.cu and fa_fwd_sparse.cu).
+// and one's prologue and epilogue overlap the other's main loop: used for d = 128 windows
+// with sinks and d = 64 block masks (d = 64 short sequences, d = 64 windows with
+// sinks and d = 128 block masks have persistent kernels of their own,
+// fa_fwd_short.cu and fa_fwd_sparse.cu).
 constexpr int threads_for(int tiles) { return tiles == 2 ? 320 : 192; }
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
