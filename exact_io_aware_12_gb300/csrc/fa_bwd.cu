@@ -1417,7 +1417,7 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
     // short d = 64 problems without a mask, with more work items than SMs: the
     // persistent kernel, so that one item's set-up, first loads and epilogue
     // overlap the next's
-    // (windows with sinks at any length: their items are short)
+    // (windows with sinks at any length where they hide keys: their items are short)
     constexpr bool kCanPersist = D == 64 && (MASK == kMaskNone || MASK == kMaskSinks);
     int sms = 0;
     if (kCanPersist || MASK == kMaskBlocks || MASK == kMaskSinks) {
@@ -1478,7 +1478,8 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
             return cudaErrorInvalidValue;
         const long long items = static_cast<long long>(a.BH) * ((a.N + kBK - 1) / kBK);
         const bool persist = kCanPersist && items > sms &&
-                             (MASK == kMaskSinks ? sp.chunks == 1 : a.N <= kBwdPersistMaxN);
+                             (MASK == kMaskSinks && window_hides(a.N, a.window, a.sinks) ? sp.chunks == 1
+                                                                                         : a.N <= kBwdPersistMaxN);
         constexpr auto kern = &fa_bwd_main_kernel<D, CAUSAL, MASK, NWG, false, MASK == kMaskSinks>;
         constexpr auto kern_p = &fa_bwd_main_kernel<D, CAUSAL, MASK, NWG, kCanPersist, MASK == kMaskSinks && !kCanPersist>;
         constexpr auto kern_s =
@@ -1495,7 +1496,7 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
         p.n_kv = n_kv;
         p.scale_log2 = a.tau * kLog2e;
         p.tau = a.tau;
-        p.window = (a.window > 0 && a.window < a.N) ? a.window : 0;
+        p.window = (a.window > 0 && a.window < a.N) ? a.window : MASK == kMaskSinks ? a.N : 0;
         p.sinks = a.sinks;
         p.blocks = a.blocks;
         p.blocks_head_stride = a.blocks_head_stride;
@@ -1557,13 +1558,13 @@ cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t stream) {
         return a.causal ? launch_bwd_t<128, true, kMaskBlocks>(a, stream)
                         : launch_bwd_t<128, false, kMaskBlocks>(a, stream);
     }
-    if (a.causal && window_hides(a.N, a.window, a.sinks)) {
-        if (a.sinks > 0)
-            return a.d == 64 ? launch_bwd_t<64, true, kMaskSinks>(a, stream)
-                             : launch_bwd_t<128, true, kMaskSinks>(a, stream);
+    // (also where the window hides nothing: dS has one precision for every call with sinks)
+    if (a.causal && a.sinks > 0)
+        return a.d == 64 ? launch_bwd_t<64, true, kMaskSinks>(a, stream)
+                         : launch_bwd_t<128, true, kMaskSinks>(a, stream);
+    if (a.causal && a.window > 0 && a.window < a.N)
         return a.d == 64 ? launch_bwd_t<64, true, kMaskWindow>(a, stream)
                          : launch_bwd_t<128, true, kMaskWindow>(a, stream);
-    }
     if (a.d == 64) return a.causal ? launch_bwd_t<64, true>(a, stream) : launch_bwd_t<64, false>(a, stream);
     return a.causal ? launch_bwd_t<128, true>(a, stream) : launch_bwd_t<128, false>(a, stream);
 }

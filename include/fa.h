@@ -22,6 +22,8 @@
  *   - causal = 1 hides key j from query i when j > i (query and key lengths
  *     are equal, so top-left and bottom-right alignment coincide); 0 = no mask.
  *   - tau is the score scale, finite and > 0 (usually 1/sqrt(d)).
+ *   - Inputs are finite.  A masked key's weight is 0, and 0 times an infinity or NaN
+ *     in its V is NaN; only what an entry point says it never reads may hold one.
  *   - Every pointer is a device pointer (cudaMalloc / PyTorch CUDA memory)
  *     aligned to 16 bytes, except the host buffers of fa_host_pipeline_step.
  *     The caller owns every buffer; apart from a host pipeline object's
@@ -163,7 +165,7 @@ FA_API fa_status fa_bwd_window(const void* Q, const void* K, const void* V, cons
  * and conventions as fa_fwd_window; key blocks that hold neither a sink nor a key
  * of some row's window are never loaded.  window >= 1 and sinks >= 0 (else
  * FA_ERR_INVALID_ARG); sinks = 0 is fa_fwd_window, and window + sinks >= N plain
- * causal attention.
+ * causal attention (fa_fwd's bits).
  */
 FA_API fa_status fa_fwd_sinks(const void* Q, const void* K, const void* V, void* O, float* LSE,
                               int B, int H, int N, int d, float tau, int window, int sinks,
@@ -253,9 +255,10 @@ FA_API fa_status fa_fwd_decode(const void* Q, const void* K, const void* V, void
  *                   code * scale of its page and head.  NULL for a bf16 cache.
  *   page_table      int [B][max_pages]; lens: int [B] (4-byte aligned)
  * page_size is a power of two from 16 to 256, max_pages * page_size at most 2^30 and
- * d 64 or 128 (else FA_ERR_UNSUPPORTED).  Table and lengths are device data, read on the stream, so a
- * captured call can be replayed while they change.  Entries behind a sequence's
- * pages are not read.  A length below 0 or above max_pages * page_size, a page number
+ * d 64 or 128 (else FA_ERR_UNSUPPORTED).  Table and lengths are device data, read on the
+ * stream, so a captured call can be replayed after they have changed.  Entries behind a
+ * sequence's pages are not read; sequences may share pages that none of them appends to.
+ * A length below 0 or above max_pages * page_size, a page number
  * outside [0, num_pages) that is needed, and a sequence's token counts that do not
  * ascend within [0, T] are not followed: fa_last_device_error then returns FA_ERR_PAGE,
  * and each entry point says what it did instead.  The description itself is host memory and
@@ -328,16 +331,14 @@ FA_API fa_status fa_kv_append_fp8(const fa_paged_cache* cache, const void* k, lo
  * Query head h reads key head h / (H / H_kv); H is a multiple of H_kv.  A row that
  * sees no key (lens[b] < Nq, or 0) is the empty sum: O = 0 and LSE = -inf.
  * Q, O: bf16 [B][H][Nq][d] with the given sequence (_sb), head (_sh) and row (_sn)
- * strides in elements, columns contiguous, 16-byte aligned, strides multiples of 8 and not negative; O's
- * rows must not overlap.  LSE: fp32 [B][H][Nq] contiguous.  window = 0: none;
- * sinks > 0 needs a window.  Rows of a page behind a sequence's end, and keys hidden
- * from every row of the call, are never read.  (A value that one row sees and another
- * does not must be finite, as in the other entry points: the other row's weight is 0,
- * and 0 times infinity is NaN.)
+ * strides in elements, columns contiguous, 16-byte aligned, strides multiples of 8 and
+ * not negative; O's rows must not overlap.  LSE: fp32 [B][H][Nq] contiguous.
+ * window = 0: none; sinks > 0 needs a window.  Rows of a page behind a sequence's end,
+ * and keys hidden from every row of the call, are never read.
  * workspace: fa_paged_workspace_size bytes (from the sizes alone, not the lengths; 0 for
- * small tables); NULL: taken with cudaMallocAsync and given back.  Two calls that may run at the same time
- * need two workspaces.  A length out of bounds is cut to the table's, and keys on a
- * page out of bounds are hidden (FA_ERR_PAGE).  More than 2^31 16-key tiles in full
+ * small tables); NULL: taken with cudaMallocAsync and given back.  Two calls that may run
+ * at the same time need two workspaces.  A length out of bounds is cut to the table's,
+ * and keys on a page out of bounds are hidden (FA_ERR_PAGE).  More than 2^31 16-key tiles in full
  * tables (of all sequences, key heads and 64 query rows) are FA_ERR_UNSUPPORTED.
  */
 FA_API size_t fa_paged_workspace_size(const fa_paged_cache* cache, int H, int Nq, int window,

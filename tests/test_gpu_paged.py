@@ -282,6 +282,17 @@ def test_bad_pages_are_hidden_and_reported(fp8):
     check(s, got=(o, lse), seqs=[2, 3])
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("longest", [300, 2000])
+def test_pages_shared_by_sequences_and_named_twice(fp8, longest):
+    s = build([longest, longest - 40, 90], 8, 2, 2, 64, 16, fp8, seed=39, poison=False)
+    s["table"][1, :5] = s["table"][0, :5]      # a common beginning
+    s["table"][2, :4] = s["table"][0, 1:5]
+    s["table"][0, 7] = s["table"][0, 2]        # one page twice
+    check(s)
+    check(s, 50, 20)
+
+
 def test_errors_of_the_library_are_raised():
     s = build([100], 2, 1, 1, 64, 16, False, seed=40)
     q = s["q"].to(DEV).expand(1, 2, 9, 64).contiguous()
