@@ -296,9 +296,17 @@ fa_fwd_short_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 
                 const int kbase = (SINKS ? walk.block(jj) : jj) * kBN;
                 // SINKS: some row's window begins behind this block's first key, and not all
-                // of the block is sinks
+                // of the block is sinks.  Wholly before the diagonal, what lies between the
+                // sinks and the row's window is hidden: one unsigned compare per score (8 x 12
+                // heads of 1024, window 256: 23.4 -> 22.1 us).
                 const bool edge = SINKS && kbase <= q_start + kBM - 1 - p.window && kbase + kBN > p.sinks;
-                if (edge) {
+                if (edge && kbase + kBN - 1 <= q_start) {
+                    const int from = p.sinks - kbase;
+                    const uint32_t n = static_cast<uint32_t>(max(0, row - p.window + 1 - p.sinks));
+#pragma unroll
+                    for (int cc = 0; cc < 128; ++cc)
+                        if (static_cast<uint32_t>(cc - from) < n) s[cc >> 5][cc & 31] = f2u(-INFINITY);
+                } else if (edge) {
                     const int last = min(row, N - 1), first = row - p.window + 1;
 #pragma unroll
                     for (int cc = 0; cc < 128; ++cc)
