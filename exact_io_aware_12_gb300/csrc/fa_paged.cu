@@ -106,6 +106,7 @@ struct PagedParams {
     long long q_sb, q_sh, q_sn, o_sb, o_sh, o_sn;
     int B, H, H_kv, G, Nq, num_pages, max_pages, shift, window, sinks;
     int rwarps;        // warps that share a share, 8 NT query rows each (1, 2 or 4)
+    int shares;        // at most
     int rgroups;       // segments per (sequence, key head): rwarps * 8 NT query rows each
     float scale_log2;  // tau * log2(e)
     unsigned int* err;
@@ -839,7 +840,8 @@ __global__ void __launch_bounds__(32 * (MANY ? kCombineWarps : 8)) fa_paged_comb
     griddep_wait();
     const int2 sg = p.seg[blockIdx.x];
     const int n = sg.y;
-    if (n <= 1) return;
+    // (the bound holds unless the first kernel gave up before it wrote its headers)
+    if (n <= 1 || sg.x < 0 || sg.x > p.shares - n) return;
     const int row_step = MANY ? rows : static_cast<int>(gridDim.y) * warps;
     for (int row = static_cast<int>(blockIdx.y) + (MANY ? 0 : warp * static_cast<int>(gridDim.y)); row < rows; row += row_step) {
         const int rw = row / R, r = row - rw * R;
@@ -1044,6 +1046,7 @@ cudaError_t launch_paged_t(const PagedArgs& a, const PagedPlan& pl, PagedParams&
     if (a.ev_start) cudaEventRecord(a.ev_start, stream);
     // (no more CTAs than a full table gives kMinTiles per warp)
     const int ctas = static_cast<int>(std::min<long long>(pl.ctas, pl.tiles * pl.rwarps / (kMinTiles * kPagedWarps) + 1));
+    p.shares = ctas * (kPagedWarps / pl.rwarps);
     e = launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), L::kBytes, stream, p);
     // pieces of an average segment of full tables
     const long long pieces = static_cast<long long>(ctas) * kPagedWarps / (pl.segs * pl.rwarps) + 1;
@@ -1104,6 +1107,7 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream) {
     p.G = a.H / a.cache.H_kv;
     p.Nq = a.Nq;
     p.rwarps = pl.rwarps;
+    p.shares = 0;
     p.rgroups = pl.rgroups;
     p.num_pages = a.cache.num_pages;
     p.max_pages = a.cache.max_pages;
