@@ -32,8 +32,8 @@
 //     accumulator's layout to the operand's with movmatrix.
 //   - The running max is moved only when some score passes it by 2^8 (one vote per
 //     tile); row sums stay per thread until the segment ends.
-//   - Short tables (kWholeTiles) take a block per segment instead: its warps take the tiles
-//     in turn and join their sums in shared memory, and no second kernel runs.
+//   - Short tables (kWholeTiles) take a block per segment instead: its four or eight warps
+//     take the tiles in turn and join their sums in shared memory, and no second kernel runs.
 //   - e4m3 keys and values are widened to fp16, which holds every code exactly; queries
 //     enter as fp16 with a power of two per row, so bf16's 8 bits stay exact down to
 //     2^-31 of the row's largest.  The page's K scale multiplies the scores in fp32; its
@@ -87,7 +87,6 @@ struct PagedLayout {
     static constexpr int kCtas = kSlot == 8192 ? (NT == 1 || D == 64 ? 3 : 2) : NT == 1 ? 4 : 3;
     static constexpr int kStages = kSlot == 8192 ? (kCtas == 3 ? 2 : 3) : NT == 1 ? 3 : 4;
     static constexpr int kWarpRing = kStages * kSlot;
-    static constexpr int kBytes = kPagedWarps * kWarpRing + 2048;  // + PagedShared
 };
 
 struct PagedParams {
@@ -218,23 +217,27 @@ __device__ __forceinline__ int clamp_len(const PagedParams& p, int b) {
     return len;
 }
 
+template <int WARPS>
 struct PagedShared {
     // per ring slot: first key of the tile (a bad page: past every row); 8-bit: the page's scales
     struct __align__(16) Slot {
         int key0;
         float ks, vs, pad;
-    } slot[kPagedWarps][4][2];  // [warp][ring slot][tile]
-    int scan[kPagedWarps];
-    int at_b[kPagedWarps], at_before[kPagedWarps];  // a share's first sequence, tiles of those before it
-    float m[kPagedWarps][16], l[kPagedWarps][16];   // WHOLE: each warp's running max and sum
+    } slot[WARPS][4][2];  // [warp][ring slot][tile]
+    int scan[WARPS];
+    int at_b[WARPS], at_before[WARPS];  // a share's first sequence, tiles of those before it
+    float m[WARPS][16], l[WARPS][16];   // WHOLE: each warp's running max and sum
 };
-constexpr int kSharedBytes = 2048;
-static_assert(sizeof(PagedShared) <= kSharedBytes, "the shared block fits its place");
+template <int D, int NT, bool F8, int WARPS>
+constexpr int kPagedBytes = WARPS * PagedLayout<D, NT, F8>::kWarpRing + static_cast<int>(sizeof(PagedShared<WARPS>));
 
-// WHOLE: a block takes one segment, its warps the tiles in turn, and joins their results
-// in shared memory: no partial results, no second kernel.  For short segments.
-template <int D, int NT, bool F8, bool WHOLE>
-__global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_paged_kernel(const PagedParams p) {
+// WW > 0: a block of WW warps takes one segment, its warps the tiles in turn, and joins their
+// results in shared memory: no partial results, no second kernel.  For short segments.
+template <int D, int NT, bool F8, int WW>
+__global__ void __launch_bounds__(WW > 0 ? 32 * WW : kThreads, WW > kPagedWarps ? 1 : PagedLayout<D, NT, F8>::kCtas)
+fa_paged_kernel(const PagedParams p) {
+    constexpr bool WHOLE = WW > 0;
+    constexpr int WARPS = WHOLE ? WW : kPagedWarps;
     using L = PagedLayout<D, NT, F8>;
     constexpr int ROW = L::kRow, CH = ROW / 16, S = L::kStages, TP = L::TP;
     using W = Swizzle<ROW>;
@@ -243,7 +246,8 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
     constexpr int KS = D / 16;          // 16-element steps of q.k
     constexpr int kChunksK = D / (F8 ? 64 : 32);  // 16-byte pieces of a key row per thread
     extern __shared__ __align__(1024) uint8_t smem[];
-    PagedShared& sh = *reinterpret_cast<PagedShared*>(smem + kPagedWarps * L::kWarpRing);
+    using Shared = PagedShared<WARPS>;
+    Shared& sh = *reinterpret_cast<Shared*>(smem + WARPS * L::kWarpRing);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     // Launched as a dependent of the kernel before it: its start-up overlaps that kernel's
     // end.  Every thread waits here before it reads anything (by plain loads: the inputs may
@@ -264,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
     Shares cut(1u, 1u);
     if constexpr (WHOLE) {
         b = static_cast<int>(blockIdx.x) / segs_per_b;
-        iw = kPagedWarps / p.rwarps;
+        iw = WARPS / p.rwarps;
         rw = warp % p.rwarps;
         turn = warp / p.rwarps;
     } else {
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
                 const int key0 = rg.key0(entry(i));
                 const int page = __shfl_sync(0xffffffffu, pg, i & 31);  // (-1 behind the piece's last tile, too)
                 const uint32_t dst = ring + in_slot * L::kSlot + tp * 2 * L::kTile;
-                typename PagedShared::Slot sl;
+                typename Shared::Slot sl;
                 sl.key0 = page < 0 ? 0x7fffff00 : key0;
                 if constexpr (F8) {
                     sl.ks = __shfl_sync(0xffffffffu, ks, i & 31);
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, PagedLayout<D, NT, F8>::kCtas) fa_pa
             issue(u + S - 1);
             cp_commit();
             const uint32_t ks_at = ring + slot_at * L::kSlot + k_src, vs_at = ring + slot_at * L::kSlot + L::kTile + v_src;
-            typename PagedShared::Slot sl[TP];
+            typename Shared::Slot sl[TP];
 #pragma unroll
             for (int tp = 0; tp < TP; ++tp) sl[tp] = sh.slot[warp][slot_at][tp];
             slot_at = slot_at + 1 == S ? 0 : slot_at + 1;
@@ -994,16 +998,21 @@ int ctas_for(int d, int nt, bool fp8) {
 }
 
 // Whole segments up to this many tiles (of a full table, within the window; the row warps
-// share a block's four): ten per warp.  (640 keys, 40 tiles: 12 heads 6.7 us whole and 8.4
-// split, 64 sequences of 8 key heads 34.3 and 34.6; 1000 keys: 8 key heads 11.5 and 9.0, 64
-// sequences 49.8 and 46.3.)
-constexpr int kWholeTiles = 40;
+// share a block's): ten per warp, of four warps, or where every segment has an SM to itself
+// and more than two tiles per warp (kNarrowTiles) of eight.  With several row warps eight
+// warps pay for fewer tiles.
+//   four warps: 640 keys of 64 sequences, 8 key heads, 34.3 us whole and 34.6 split; 1000
+//     keys 49.8 and 46.3;
+//   eight: 12 heads, 128 keys 4.6 us by eight and 3.9 by four, 517 keys 6.2 and 6.8, 1000 keys
+//     7.1 and 8.8 split, 1280 7.9 and 9.0; 64 segments, 1280 keys 10.5 and 12.6, 2000 14.1 and
+//     13.1; 8 segments of 32 rows (two row warps), 320 keys 9.9 and 12.3, 640 13.4 and 10.2.
+constexpr int kWholeTiles = 40, kWideTiles = 80, kWideRowTiles = 53, kNarrowTiles = 8;
 
 // Workspace: segment headers, then the pieces' sums and outputs, each 256-aligned; none
 // for whole segments.
 struct PagedPlan {
     int nt, rwarps, rgroups, ctas;
-    bool whole;
+    bool whole, wide;  // whole segments, by eight warps
     long long segs, tiles;  // tiles: of a full table, all segments
     size_t part_l, part_o, bytes;
 };
@@ -1022,7 +1031,8 @@ PagedPlan paged_plan(const PagedCache& c, int H, int Nq, int window, int sinks, 
     if (window > 0)
         most = std::min(most, (static_cast<long long>(window) + Nq) / kPagedTile + 2 + (sinks + kPagedTile - 1ll) / kPagedTile);
     pl.tiles = pl.segs * most;
-    pl.whole = most * pl.rwarps <= kWholeTiles;
+    pl.wide = pl.segs <= kSms && most * pl.rwarps > kNarrowTiles;
+    pl.whole = most * pl.rwarps <= (!pl.wide ? kWholeTiles : pl.rwarps == 1 ? kWideTiles : kWideRowTiles);
     const size_t part_rows = pl.whole ? 0 : static_cast<size_t>(2) * kPagedWarps * pl.ctas * 8 * pl.nt;
     pl.part_l = pl.whole ? 0 : up(static_cast<size_t>(pl.segs) * sizeof(int2));
     pl.part_o = pl.part_l + up(part_rows * sizeof(float));
@@ -1032,14 +1042,19 @@ PagedPlan paged_plan(const PagedCache& c, int H, int Nq, int window, int sinks, 
 
 template <int D, int NT, bool F8>
 cudaError_t launch_paged_t(const PagedArgs& a, const PagedPlan& pl, PagedParams& p, cudaStream_t stream) {
-    using L = PagedLayout<D, NT, F8>;
-    constexpr auto kern = &fa_paged_kernel<D, NT, F8, false>;
-    constexpr auto kern_w = &fa_paged_kernel<D, NT, F8, true>;
-    cudaError_t e = pl.whole ? set_max_dyn_smem_once<kern_w>(L::kBytes) : set_max_dyn_smem_once<kern>(L::kBytes);
+    constexpr auto kern = &fa_paged_kernel<D, NT, F8, 0>;
+    constexpr auto kern_w = &fa_paged_kernel<D, NT, F8, kPagedWarps>;
+    constexpr auto kern_w2 = &fa_paged_kernel<D, NT, F8, 2 * kPagedWarps>;
+    constexpr int bytes = kPagedBytes<D, NT, F8, kPagedWarps>, bytes2 = kPagedBytes<D, NT, F8, 2 * kPagedWarps>;
+    cudaError_t e = !pl.whole  ? set_max_dyn_smem_once<kern>(bytes)
+                    : pl.wide ? set_max_dyn_smem_once<kern_w2>(bytes2)
+                              : set_max_dyn_smem_once<kern_w>(bytes);
     if (e != cudaSuccess) return e;
     if (pl.whole) {
+        const dim3 grid(static_cast<unsigned>(pl.segs));
         if (a.ev_start) cudaEventRecord(a.ev_start, stream);
-        e = launch_dependent(kern_w, dim3(static_cast<unsigned>(pl.segs)), dim3(kThreads), L::kBytes, stream, p);
+        e = pl.wide ? launch_dependent(kern_w2, grid, dim3(2 * kThreads), bytes2, stream, p)
+                    : launch_dependent(kern_w, grid, dim3(kThreads), bytes, stream, p);
         if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
         return e;
     }
@@ -1047,7 +1062,7 @@ cudaError_t launch_paged_t(const PagedArgs& a, const PagedPlan& pl, PagedParams&
     // (no more CTAs than a full table gives kMinTiles per warp)
     const int ctas = static_cast<int>(std::min<long long>(pl.ctas, pl.tiles * pl.rwarps / (kMinTiles * kPagedWarps) + 1));
     p.shares = ctas * (kPagedWarps / pl.rwarps);
-    e = launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), L::kBytes, stream, p);
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), bytes, stream, p);
     // pieces of an average segment of full tables
     const long long pieces = static_cast<long long>(ctas) * kPagedWarps / (pl.segs * pl.rwarps) + 1;
     const long long rows = std::min(p.G * p.Nq, 8 * NT * pl.rwarps);

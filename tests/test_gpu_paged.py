@@ -113,6 +113,15 @@ def test_short_tables_and_many_rows(H, Hkv, Nq, d, page, longest, fp8):
     check(s, 37, 6)
 
 
+# more short segments than SMs: four warps to a block (eight above, where each has an SM to itself)
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("H,Hkv,Nq,d,longest", [(8, 4, 1, 128, 600), (24, 3, 8, 128, 150), (12, 3, 5, 64, 300), (4, 4, 1, 64, 100)])
+def test_many_short_segments(H, Hkv, Nq, d, longest, fp8):
+    s = build([longest] + [(7 * i) % longest for i in range(59)], H, Hkv, Nq, d, 16, fp8, seed=H + longest)
+    check(s)
+    check(s, 37, 6)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (5, 3), (16, 16), (64, 0), (100, 17), (128, 200), (5000, 4)])
 def test_window_and_sinks(window, sinks, fp8):
