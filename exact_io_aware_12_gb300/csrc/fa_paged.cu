@@ -32,8 +32,9 @@
 //     accumulator's layout to the operand's with movmatrix.
 //   - The running max is moved only when some score passes it by 2^8 (one vote per
 //     tile); row sums stay per thread until the segment ends.
-//   - Short tables (kWholeTiles) take a block per segment instead: its four or eight warps
-//     take the tiles in turn and join their sums in shared memory, and no second kernel runs.
+//   - Short tables (kWholeTiles) take a block, or a cluster of blocks, per segment instead:
+//     its warps take the tiles in turn and join their sums in shared memory (a cluster's
+//     blocks in one another's), and no second kernel runs.
 //   - e4m3 keys and values are widened to fp16, which holds every code exactly; queries
 //     enter as fp16 with a power of two per row, so bf16's 8 bits stay exact down to
 //     2^-31 of the row's largest.  The page's K scale multiplies the scores in fp32; its
@@ -106,6 +107,7 @@ struct PagedParams {
     int B, H, H_kv, G, Nq, num_pages, max_pages, shift, window, sinks;
     int rwarps;        // warps that share a share, 8 NT query rows each (1, 2 or 4)
     int shares;        // at most
+    int cluster_log2;  // WW = 8: of the blocks that share a segment
     int rgroups;       // segments per (sequence, key head): rwarps * 8 NT query rows each
     float scale_log2;  // tau * log2(e)
     unsigned int* err;
@@ -195,6 +197,27 @@ struct Swizzle {
     static __device__ __forceinline__ uint32_t v_row1(uint32_t a) { return ROW >= 128 ? a + ROW : a ^ 64; }
 };
 
+// Distributed shared memory: the address of another block's copy of a place in this one's,
+// loads from there, and a barrier over the cluster.
+__device__ __forceinline__ uint32_t map_block(uint32_t a, int block) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(block));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t a) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // max over the lanes that share lane % 4
 __device__ __forceinline__ float max_over_g(float x) {
 #pragma unroll
@@ -227,6 +250,7 @@ struct PagedShared {
     int scan[WARPS];
     int at_b[WARPS], at_before[WARPS];  // a share's first sequence, tiles of those before it
     float m[WARPS][16], l[WARPS][16];   // WHOLE: each warp's running max and sum
+    float lse[WARPS > kPagedWarps ? 64 : 1];  // of a cluster's block: log2 of its rows' sums
 };
 template <int D, int NT, bool F8, int WARPS>
 constexpr int kPagedBytes = WARPS * PagedLayout<D, NT, F8>::kWarpRing + static_cast<int>(sizeof(PagedShared<WARPS>));
@@ -265,12 +289,18 @@ fa_paged_kernel(const PagedParams p) {
     // every iw-th tile of one segment, from `turn` on; rows of row warp rw
     uint32_t share = 0, x = 0, x_end = 0, b_first = 0;
     int b = 0, rw = 0, turn = 0, iw = 1;
+    [[maybe_unused]] int seg = static_cast<int>(blockIdx.x), cn = 1;  // WHOLE: the segment, and its blocks
     Shares cut(1u, 1u);
     if constexpr (WHOLE) {
-        b = static_cast<int>(blockIdx.x) / segs_per_b;
+        if constexpr (WW > kPagedWarps) {
+            cn = 1 << p.cluster_log2;
+            seg = static_cast<int>(blockIdx.x) >> p.cluster_log2;
+        }
+        b = seg / segs_per_b;
         iw = WARPS / p.rwarps;
         rw = warp % p.rwarps;
-        turn = warp / p.rwarps;
+        turn = warp / p.rwarps + (static_cast<int>(blockIdx.x) - seg * cn) * iw;
+        iw *= cn;
     } else {
         // ---- this warp's share of the tiles ----
         const int per = (p.B + kThreads - 1) / kThreads;
@@ -329,7 +359,7 @@ fa_paged_kernel(const PagedParams p) {
 
     while (true) {
         // ---- one piece: tiles [u0, u1) of segment (b, hk, rb group) ----
-        const int in_b = WHOLE ? static_cast<int>(blockIdx.x) - b * segs_per_b : static_cast<int>((x - b_first) / tiles);
+        const int in_b = WHOLE ? seg - b * segs_per_b : static_cast<int>((x - b_first) / tiles);
         [[maybe_unused]] const uint32_t seg_first = b_first + in_b * tiles;
         const int hk = in_b / p.rgroups;
         const int u0 = WHOLE ? 0 : static_cast<int>(x - seg_first);
@@ -729,19 +759,22 @@ fa_paged_kernel(const PagedParams p) {
                 }
             __syncthreads();  // (and every warp is done with its ring)
             float* red = reinterpret_cast<float*>(smem);  // [warp][R][D]
+            const int liw = WARPS / p.rwarps, lturn = warp / p.rwarps;  // of this block
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int r = nt * 8 + 2 * t4 + e;
                     float m = -INFINITY, l = 0.f;
-                    for (int k = 0; k < iw; ++k) m = fmaxf(m, sh.m[k * p.rwarps + rw][r]);
+                    for (int k = 0; k < liw; ++k) m = fmaxf(m, sh.m[k * p.rwarps + rw][r]);
                     const float ref = m == -INFINITY ? 0.f : m;
-                    for (int k = 0; k < iw; ++k) l += sh.l[k * p.rwarps + rw][r] * ex2(sh.m[k * p.rwarps + rw][r] - ref);
+                    for (int k = 0; k < liw; ++k) l += sh.l[k * p.rwarps + rw][r] * ex2(sh.m[k * p.rwarps + rw][r] - ref);
                     // (a row that sees nothing: l = 0 and O = 0, LSE = -inf; NaN where a score was)
-                    for (int k = 0; m == -INFINITY && k < iw; ++k) l += sh.l[k * p.rwarps + rw][r];
+                    for (int k = 0; m == -INFINITY && k < liw; ++k) l += sh.l[k * p.rwarps + rw][r];
                     f[nt][e] = l == 0.f ? 0.f : ex2((F8 ? mv_run[nt][e] : m_run[nt][e]) - ref) / l;
-                    if (turn == 0 && g == 0 && r < rows) {
+                    if (WW > kPagedWarps && cn > 1) {
+                        if (lturn == 0 && g == 0) sh.lse[rw * R + r] = ref + lg2(l);
+                    } else if (turn == 0 && g == 0 && r < rows) {
                         const int hh = (row0 + r) / p.Nq, qi = (row0 + r) - hh * p.Nq, h = hk * p.G + hh;
                         p.LSE[(static_cast<long long>(b) * p.H + h) * p.Nq + qi] = (ref + lg2(l)) * kLn2;
                     }
@@ -757,19 +790,51 @@ fa_paged_kernel(const PagedParams p) {
                 }
             __syncthreads();
             // the iw warps of row warp rw write its rows
-            for (int i = turn * 32 + lane; i < rows * (D / 4); i += iw * 32) {
+            for (int i = lturn * 32 + lane; i < rows * (D / 4); i += liw * 32) {
                 const int r = i / (D / 4), col = i % (D / 4) * 4;
                 float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int k = 0; k < iw; ++k) {
+                for (int k = 0; k < liw; ++k) {
                     const float4 y = *reinterpret_cast<const float4*>(red + ((k * p.rwarps + rw) * R + r) * D + col);
                     o.x += y.x;
                     o.y += y.y;
                     o.z += y.z;
                     o.w += y.w;
                 }
+                if (WW > kPagedWarps && cn > 1) {  // (over row warp 0's part, which only this thread has read)
+                    *reinterpret_cast<float4*>(red + (rw * R + r) * D + col) = o;
+                    continue;
+                }
                 const int hh = (row0 + r) / p.Nq, qi = (row0 + r) - hh * p.Nq, h = hk * p.G + hh;
                 *reinterpret_cast<uint2*>(p.O + b * p.o_sb + static_cast<long long>(h) * p.o_sh + qi * p.o_sn + col) =
                     make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+            }
+            if constexpr (WW > kPagedWarps) {
+                if (cn == 1) return;
+                // the blocks of the cluster: O = sum_c 2^(l_c - L) O_c, each block a part of the rows
+                cluster_barrier();
+                for (int i = turn * 32 + lane; i < rows * (D / 4); i += iw * 32) {
+                    const int r = i / (D / 4), col = i % (D / 4) * 4;
+                    const uint32_t l_at = smem_addr(&sh.lse[rw * R + r]), o_at = smem_addr(red + (rw * R + r) * D + col);
+                    float m = -INFINITY, sum = 0.f;
+                    for (int k = 0; k < cn; ++k) m = fmaxf(m, ld_cluster(map_block(l_at, k)));
+                    const float ref = m == -INFINITY ? 0.f : m;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int k = 0; k < cn; ++k) {
+                        const float w = ex2(ld_cluster(map_block(l_at, k)) - ref);
+                        const float4 y = ld_cluster4(map_block(o_at, k));
+                        sum += w;
+                        o.x = fmaf(w, y.x, o.x);
+                        o.y = fmaf(w, y.y, o.y);
+                        o.z = fmaf(w, y.z, o.z);
+                        o.w = fmaf(w, y.w, o.w);
+                    }
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // (0: the row sees nothing)
+                    const int hh = (row0 + r) / p.Nq, qi = (row0 + r) - hh * p.Nq, h = hk * p.G + hh;
+                    *reinterpret_cast<uint2*>(p.O + b * p.o_sb + static_cast<long long>(h) * p.o_sh + qi * p.o_sn + col) =
+                        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+                    if (col == 0) p.LSE[(static_cast<long long>(b) * p.H + h) * p.Nq + qi] = (ref + lg2(sum)) * kLn2;
+                }
+                cluster_barrier();  // (no block ends while others read its memory)
             }
             return;
         }
@@ -999,20 +1064,25 @@ int ctas_for(int d, int nt, bool fp8) {
 
 // Whole segments up to this many tiles (of a full table, within the window; the row warps
 // share a block's): ten per warp, of four warps, or where every segment has an SM to itself
-// and more than two tiles per warp (kNarrowTiles) of eight.  With several row warps eight
-// warps pay for fewer tiles.
+// and more than two tiles per warp (kNarrowTiles) of eight; where SMs are left over, of a
+// cluster of up to eight such blocks, which keeps five tiles or fewer per warp while it can.
+// With several row warps eight warps pay for fewer tiles.
 //   four warps: 640 keys of 64 sequences, 8 key heads, 34.3 us whole and 34.6 split; 1000
 //     keys 49.8 and 46.3;
-//   eight: 12 heads, 128 keys 4.6 us by eight and 3.9 by four, 517 keys 6.2 and 6.8, 1000 keys
-//     7.1 and 8.8 split, 1280 7.9 and 9.0; 64 segments, 1280 keys 10.5 and 12.6, 2000 14.1 and
-//     13.1; 8 segments of 32 rows (two row warps), 320 keys 9.9 and 12.3, 640 13.4 and 10.2.
-constexpr int kWholeTiles = 40, kWideTiles = 80, kWideRowTiles = 53, kNarrowTiles = 8;
+//   eight: 12 heads, 128 keys 4.6 us by eight and 3.9 by four, 517 keys 6.2 and 6.8; 64
+//     segments, 1280 keys 10.5 and split 12.6, 2000 14.1 and 13.1; 8 segments of 32 rows (two
+//     row warps), 320 keys 9.9 and 12.3, 640 13.4 and 10.2;
+//   clusters: 8 segments, 1000 keys 8.2 us by two blocks and 8.9 by one, 3000 8.0 and split
+//     10.6, 9000 11.7 and 12.6; 32 segments, 2000 8.5 and 11.5; 64, 3000 17.0 and 17.4; one
+//     segment, 8000 keys 10.9 and 9.6.
+constexpr int kWholeTiles = 40, kWideTiles = 80, kWideRowTiles = 53, kNarrowTiles = 8, kMaxCluster = 8, kFewBlocks = 32;
 
 // Workspace: segment headers, then the pieces' sums and outputs, each 256-aligned; none
 // for whole segments.
 struct PagedPlan {
     int nt, rwarps, rgroups, ctas;
     bool whole, wide;  // whole segments, by eight warps
+    int cluster_log2;  // wide: of the blocks per segment
     long long segs, tiles;  // tiles: of a full table, all segments
     size_t part_l, part_o, bytes;
 };
@@ -1031,8 +1101,16 @@ PagedPlan paged_plan(const PagedCache& c, int H, int Nq, int window, int sinks, 
     if (window > 0)
         most = std::min(most, (static_cast<long long>(window) + Nq) / kPagedTile + 2 + (sinks + kPagedTile - 1ll) / kPagedTile);
     pl.tiles = pl.segs * most;
-    pl.wide = pl.segs <= kSms && most * pl.rwarps > kNarrowTiles;
-    pl.whole = most * pl.rwarps <= (!pl.wide ? kWholeTiles : pl.rwarps == 1 ? kWideTiles : kWideRowTiles);
+    const long long work = most * pl.rwarps, per_block = pl.rwarps == 1 ? kWideTiles : kWideRowTiles;
+    pl.wide = pl.segs <= kSms && work > kNarrowTiles;
+    pl.cluster_log2 = 0;
+    if (pl.wide)
+        while ((1 << pl.cluster_log2) < kMaxCluster && work > (per_block << pl.cluster_log2) / 2 &&
+               pl.segs << (pl.cluster_log2 + 1) <= kSms)
+            ++pl.cluster_log2;
+    // (where even clusters fill few SMs, a split takes over at half the length)
+    const bool few = pl.wide && pl.segs << pl.cluster_log2 < kFewBlocks;
+    pl.whole = work <= (pl.wide ? (per_block << pl.cluster_log2) / (few ? 2 : 1) : kWholeTiles);
     const size_t part_rows = pl.whole ? 0 : static_cast<size_t>(2) * kPagedWarps * pl.ctas * 8 * pl.nt;
     pl.part_l = pl.whole ? 0 : up(static_cast<size_t>(pl.segs) * sizeof(int2));
     pl.part_o = pl.part_l + up(part_rows * sizeof(float));
@@ -1051,9 +1129,9 @@ cudaError_t launch_paged_t(const PagedArgs& a, const PagedPlan& pl, PagedParams&
                               : set_max_dyn_smem_once<kern_w>(bytes);
     if (e != cudaSuccess) return e;
     if (pl.whole) {
-        const dim3 grid(static_cast<unsigned>(pl.segs));
+        const dim3 grid(static_cast<unsigned>(pl.segs << pl.cluster_log2));
         if (a.ev_start) cudaEventRecord(a.ev_start, stream);
-        e = pl.wide ? launch_dependent(kern_w2, grid, dim3(2 * kThreads), bytes2, stream, p)
+        e = pl.wide ? launch_dependent_clusters(kern_w2, 1u << pl.cluster_log2, grid, dim3(2 * kThreads), bytes2, stream, p)
                     : launch_dependent(kern_w, grid, dim3(kThreads), bytes, stream, p);
         if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
         return e;
@@ -1123,6 +1201,7 @@ cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream) {
     p.Nq = a.Nq;
     p.rwarps = pl.rwarps;
     p.shares = 0;
+    p.cluster_log2 = pl.cluster_log2;
     p.rgroups = pl.rgroups;
     p.num_pages = a.cache.num_pages;
     p.max_pages = a.cache.max_pages;

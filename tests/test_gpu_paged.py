@@ -113,6 +113,18 @@ def test_short_tables_and_many_rows(H, Hkv, Nq, d, page, longest, fp8):
     check(s, 37, 6)
 
 
+# tables too long for whole segments, split over all warps: every number of row warps and groups, short
+# and empty sequences among long ones, shares that cut a segment many times and segments that share one
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hkv,Nq,page", [(2, 2, 1, 64), (8, 1, 1, 16), (4, 2, 5, 64), (8, 2, 8, 128), (7, 1, 8, 32), (12, 1, 8, 64)])
+def test_long_tables_are_split(H, Hkv, Nq, page, d, fp8):
+    s = build([11111, 0, 3, 4097, 700, 1, 90], H, Hkv, Nq, d, page, fp8, seed=7 * H + Nq + d)
+    assert api.paged_workspace_bytes(s["q"], s["kc"], s["table"]) > 0
+    check(s)
+    check(s, 10500, 40)
+
+
 # more short segments than SMs: four warps to a block (eight above, where each has an SM to itself)
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("H,Hkv,Nq,d,longest", [(8, 4, 1, 128, 600), (24, 3, 8, 128, 150), (12, 3, 5, 64, 300), (4, 4, 1, 64, 100)])
@@ -221,7 +233,8 @@ def test_strides_orders_and_given_buffers(fp8):
 
 
 def test_workspace_given_or_taken_by_the_library():
-    s = build([900, 5], 4, 2, 1, 64, 16, False, seed=11)
+    s = build([14000, 5], 4, 2, 1, 64, 16, False, seed=11)   # (too long for whole segments)
+    assert api.paged_workspace_bytes(s["q"], s["kc"], s["table"]) > 0
     want = run(s)
     dev = {n: t.to(DEV) for n, t in s.items() if t is not None}
     P, Hkv, page, d = dev["kc"].shape
@@ -314,7 +327,7 @@ def test_errors_of_the_library_are_raised():
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("longest", [200, 3000])
+@pytest.mark.parametrize("longest", [200, 2900, 12000])
 def test_calls_in_a_row_wait_for_one_another(fp8, longest):
     """Each call's inputs are written by the kernel right before it, without a pause between: the same
     bits as with one after each."""
@@ -351,7 +364,7 @@ def test_calls_in_a_row_wait_for_one_another(fp8, longest):
     assert bool(torch.isfinite(outs[0][3].float()).all()) and api.last_device_error() == _lib.FA_OK
 
 
-@pytest.mark.parametrize("longest", [200, 3000])
+@pytest.mark.parametrize("longest", [200, 3000, 11000])
 def test_captured_behind_a_copy_and_a_join(longest):
     """A graph in which the calls follow a copy, a fork and a join of streams, and two graphs with buffers
     of their own that run at the same time."""
@@ -405,7 +418,7 @@ def test_captured_behind_a_copy_and_a_join(longest):
 
 
 def test_two_streams_two_workspaces():
-    a, b = build([3000, 10, 500], 8, 2, 1, 128, 64, False, seed=16), build([2500], 8, 2, 2, 128, 64, True, seed=17)
+    a, b = build([12000, 10, 500], 8, 2, 1, 128, 64, False, seed=16), build([11500], 8, 2, 2, 128, 64, True, seed=17)
     dev = [{n: (t.to(DEV) if t is not None else None) for n, t in s.items()} for s in (a, b)]
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     torch.cuda.synchronize()
@@ -422,8 +435,9 @@ def test_two_streams_two_workspaces():
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-def test_runs_are_bitwise_alike(fp8):
-    s = build([5000, 1, 777, 64], 8, 2, 3, 128, 64, fp8, seed=18)
+@pytest.mark.parametrize("longest", [5000, 13000])
+def test_runs_are_bitwise_alike(fp8, longest):
+    s = build([longest, 1, 777, 64], 8, 2, 3, 128, 64, fp8, seed=18)
     a = run(s)
     for _ in range(3):
         b = run(s)

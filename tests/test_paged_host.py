@@ -160,7 +160,7 @@ def test_units_fit_every_split_of_tokens(shim):
 
 def cache(fp8=False, **kw):
     c = dict(K=FAKE, V=FAKE + GB, k_scale=FAKE + 2 * GB if fp8 else None, v_scale=FAKE + 3 * GB if fp8 else None,
-             page_table=FAKE + 4 * GB, lens=FAKE + 5 * GB, B=2, H_kv=2, d=64, num_pages=8, page_size=16, max_pages=400)
+             page_table=FAKE + 4 * GB, lens=FAKE + 5 * GB, B=2, H_kv=2, d=64, num_pages=8, page_size=16, max_pages=4000)
     c.update(kw)
     return _lib.PagedCache(*(c[n] for n, _ in _lib.PagedCache._fields_))
 
