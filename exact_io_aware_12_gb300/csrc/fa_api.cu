@@ -11,6 +11,7 @@
 #include "../../include/fa.h"
 #include "fa_internal.h"
 #include "fa_paged.h"
+#include "fa_window.h"
 #include "ptx.cuh"
 
 // One error word per device (each device holds its own copy of this
@@ -161,8 +162,10 @@ fa_status fwd_common(const void* Q, const void* K, const void* V, void* O, float
     a.d = d;
     a.tau = tau;
     a.causal = causal != 0;
-    a.window = window;
-    a.sinks = sinks;
+    // (where the window hides nothing the kernels without one run)
+    const bool hides = window_hides(N, window, sinks);
+    a.window = hides ? window : 0;
+    a.sinks = hides ? sinks : 0;
     a.blocks = blocks;
     a.blocks_head_stride = mask_stride;
     a.o32 = o32;
@@ -348,8 +351,9 @@ static fa_status bwd_common(const void* Q, const void* K, const void* V, const v
     a.d = d;
     a.tau = tau;
     a.causal = causal != 0;
-    a.window = window;
-    a.sinks = sinks;
+    const WindowCut cut = cut_window(N, window, sinks);
+    a.window = cut.window;
+    a.sinks = cut.sinks;
     a.blocks = blocks;
     a.blocks_head_stride = mask_stride;
     a.err = di->err_word;

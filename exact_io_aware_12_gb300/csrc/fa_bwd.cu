@@ -47,6 +47,7 @@
 #include <type_traits>
 
 #include "fa_internal.h"
+#include "fa_window.h"
 #include "ptx.cuh"
 
 namespace fa {

@@ -41,6 +41,7 @@
 #include <cmath>
 
 #include "fa_internal.h"
+#include "fa_window.h"
 #include "ptx.cuh"
 
 namespace fa {
@@ -180,7 +181,7 @@ __device__ __forceinline__ FwdItem fwd_item(int bh, int pair, int N, int n_kv, i
     it.lo0 = window > 0 ? max(0, it.q_start0 - window + 1) / kBN : 0;
     it.lo1 = window > 0 ? max(0, it.q_start1 - window + 1) / kBN : 0;
     it.win = it.lo0;
-    it.lo0 -= min((sinks + kBN - 1) / kBN, it.lo0);
+    it.lo0 -= sink_blocks(sinks, it.lo0, kBN);
     it.n_blk0 = it.hi0 - it.lo0;
     it.n_blk1 = it.hi1 > 0 ? it.hi1 - it.lo1 : 0;
     it.jlo = it.lo0;
@@ -1081,7 +1082,7 @@ cudaError_t launch_fwd_t(const FwdArgs& a, cudaStream_t stream) {
     p.BH = a.BH;
     p.items = static_cast<int>(items);
     p.N = a.N;
-    p.window = (a.window > 0 && a.window < a.N) ? a.window : 0;
+    p.window = a.window;
     p.sinks = a.sinks;
     p.blocks = a.blocks;
     p.blocks_head_stride = a.blocks_head_stride;
@@ -1109,7 +1110,7 @@ cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t stream) {
                             : launch_fwd_t<64, false, false, kMaskBlocks, 1>(a, stream);
         return launch_fwd_sparse(a, stream);  // persistent, fa_fwd_sparse.cu
     }
-    if (a.causal && !a.o32 && window_hides(a.N, a.window, a.sinks)) {
+    if (a.causal && !a.o32 && a.window > 0) {
         if (a.sinks > 0)
             // d = 128: one tile per CTA, two CTAs per SM: against pairs 2-23% faster (16
             // heads of 16k, window 4096: 388 -> 381 us; 5001 keys, window 1000: 59 -> 51

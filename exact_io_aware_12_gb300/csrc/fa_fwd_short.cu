@@ -28,6 +28,7 @@
 #include <cmath>
 
 #include "fa_internal.h"
+#include "fa_window.h"
 #include "ptx.cuh"
 
 namespace fa {
@@ -94,7 +95,7 @@ __device__ __forceinline__ Walk walk_of(int qt, int n_kv, const ShortParams& p) 
     Walk w{CAUSAL ? min(n_kv, qt + 1) : n_kv, 0, 0};
     if constexpr (SINKS) {
         w.win = max(0, qt * kBM - p.window + 1) / kBN;
-        w.ns = min((p.sinks + kBN - 1) / kBN, w.win);
+        w.ns = sink_blocks(p.sinks, w.win, kBN);
         w.nb += w.ns - w.win;
     }
     return w;

@@ -25,8 +25,8 @@ struct FwdArgs {
     int BH, N, d;
     float tau;
     bool causal;
-    int window;       // causal sliding window in keys (0 = none)
-    int sinks = 0;    // keys [0, sinks) that stay visible behind the window
+    int window;       // causal sliding window in keys (0: none, or it hides nothing)
+    int sinks = 0;    // keys [0, sinks) that stay visible behind the window (0 without one)
     const uint8_t* blocks = nullptr;  // block mask [heads][nb][nb] (device) or null
     long long blocks_head_stride = 0;  // bytes between heads' masks (0: one mask)
     bool o32;
@@ -52,8 +52,8 @@ struct BwdArgs {
     int BH, N, d;
     float tau;
     bool causal;
-    int window;     // causal sliding window in keys (0 = none)
-    int sinks = 0;  // keys [0, sinks) that stay visible behind the window
+    int window;     // causal sliding window in keys, at most N (0 = none)
+    int sinks = 0;  // keys [0, sinks), at most N, that stay visible behind the window
     const uint8_t* blocks = nullptr;  // block mask [heads][nb][nb] (device) or null
     long long blocks_head_stride = 0;  // bytes between heads' masks (0: one mask)
     unsigned int* err;
@@ -147,14 +147,6 @@ struct PagedArgs {
 size_t paged_workspace(const PagedCache& c, int H, int Nq, int window, int sinks, bool fp8);
 // 16-key tiles that full tables hold, which 32-bit counts must not pass.
 long long paged_max_tiles(int B, int H, int H_kv, int Nq, int max_pages, int shift);
-
-// Whether a causal window of `window` keys (0: none) beside `sinks` first keys hides
-// anything that the causal mask shows: the last query, N - 1, sees neither the keys
-// from `sinks` on nor those within its window.  Where it hides nothing the kernels
-// without a window run.
-inline bool window_hides(int N, int window, int sinks) {
-    return window > 0 && static_cast<long long>(window) + sinks < N;
-}
 
 // How the decode forward cuts the KV cache: `splits` chunks of `chunk` keys
 // (a multiple of 64).  Depends only on its arguments.

@@ -222,3 +222,18 @@ def test_captured_step_replays_on_new_values_and_another_stream():
             assert torch.equal(outs[i], want[i])
         assert rel_l2(outs[2], want[2]) <= 1e-3
     assert api.last_device_error() == _lib.FA_OK
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N", [300, 2049])
+def test_all_keys_as_the_largest_number(N, d):
+    """sinks and window up to the largest int: plain causal attention, bit by bit."""
+    x = draw(1, 2, N, d, seed=101)
+    q, k, v = (x[n].to(DEV) for n in ("q", "k", "v"))
+    tau, most = 1 / math.sqrt(d), 2 ** 31 - 1
+    want = api.fwd(q, k, v, True, tau)
+    for w, s in ((1, most), (most, 1), (most, most), (7, most - 126), (7, N - 7)):
+        got = api.fwd(q, k, v, True, tau, window=w, sinks=s)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    check(x, tau, 1, most)
+    check(x, tau, most, most)
