@@ -348,7 +348,10 @@ FA_API fa_status fa_fwd_paged(const fa_paged_cache* cache, const void* Q, long l
                               long long o_sn, float* LSE, int H, int Nq, float tau, int window,
                               int sinks, void* workspace, size_t workspace_bytes, void* stream);
 
-/* fa_fwd_paged over an e4m3 cache. */
+/*
+ * fa_fwd_paged over an e4m3 cache.  A weight (times its page's V scale) is held to 2^-11 of
+ * itself down to 2^-28 of a row's largest, below that to 2^-39 of the largest.
+ */
 FA_API fa_status fa_fwd_paged_fp8(const fa_paged_cache* cache, const void* Q, long long q_sb,
                                   long long q_sh, long long q_sn, void* O, long long o_sb,
                                   long long o_sh, long long o_sn, float* LSE, int H, int Nq,

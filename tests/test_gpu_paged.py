@@ -558,3 +558,26 @@ def test_offsets_past_32_bits(fp8):
     check(s, got=(o.cpu(), lse.cpu()))
     if not fp8:
         assert torch.equal(_plain.gather(s["vc"], s["table"][0], 700).float(), x[:, Hkv:].cpu().transpose(0, 1).float())
+
+
+# Weights of 8-bit pages are rounded to fp16.  One key of value zero (a sink) that outweighs the others
+# leaves O to weights far below the running max: they keep fp16's 2^-11 down to 2^-28 of it (e^-19.4).
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Nq,lens", [(4, 1, [300, 17]), (4, 4, [300, 3]), (4, 1, [700] * 60), (4, 1, [2900]),
+                                       (4, 8, [2900]), (4, 1, [14000, 900]), (4, 8, [14000])])
+def test_8_bit_weights_far_below_a_dominant_key(H, Nq, lens, d):
+    page = 16
+    s = build(lens, H, 1, Nq, d, page, True, seed=50 + d, poison=False)
+    k = s["kc"].view(torch.uint8)
+    k.zero_()
+    s["k_scale"].fill_(2.0 ** -8)
+    s["v_scale"].fill_(2.0 ** -8)
+    for b in range(len(lens)):
+        at = (int(s["table"][b, 0]), 0, 0)
+        k[at] = torch.full((d,), 256.0).to(torch.float8_e4m3fn).view(torch.uint8)   # key 0: ones
+        s["vc"].view(torch.uint8)[at] = 0
+    # its score: 0, 12, 17 and 19 above the others', by head (some rows of a warp each)
+    for h, gap in enumerate((0.0, 12.0, 17.0, 19.0)):
+        s["q"][:, h] = gap / math.sqrt(d)
+    o, _ = check(s)
+    assert float(o[0, 3].abs().max()) > 0
