@@ -30,20 +30,20 @@
 //     takes the 16 bytes of a key row that it can load at once, so K needs no transposing
 //     load.  V^T pairs neighbouring keys with a byte permute; P^T changes from the
 //     accumulator's layout to the operand's with movmatrix.
-//   - The running max is moved only when some score passes it by 2^8 (8-bit pages: 2; one
-//     vote per tile); row sums stay per thread until the segment ends.
+//   - Weights are taken relative to a running reference, which moves to the max (8-bit pages:
+//     2^14 below it) only when some weight passes 2^8 (2^15; one vote per tile); row sums stay
+//     per thread until the segment ends.
 //   - Short tables (kWholeTiles) take a block, or a cluster of blocks, per segment instead:
 //     its warps take the tiles in turn and join their sums in shared memory (a cluster's
 //     blocks in one another's), and no second kernel runs.
 //   - e4m3 keys and values are widened to fp16, which holds every code exactly; queries
 //     enter as fp16 with a power of two per row, so bf16's 8 bits stay exact down to
 //     2^-31 of the row's largest.  The page's K scale multiplies the scores in fp32; its
-//     V scale enters the weights, which keep a running max of their own (log2 P + log2
-//     scale), and are held 2^14 times as large.
+//     V scale enters the weights, which keep a reference of their own (log2 P + log2 scale).
 //   - P is rounded for the second product, as O is in the end; statistics, scores and sums
 //     stay in fp32.  bf16: relative error at most 2^-8 per weight.  8-bit pages, fp16: 2^-11
-//     for weights (times their page's scale) down to 2^-28 of the running max of these;
-//     below, fp16's subnormals, 2^-39 of that max in all, so beside a key of value zero that
+//     for weights (times their page's scale) down to 2^-28 of the largest of these;
+//     below, fp16's subnormals, 2^-39 of the largest in all, so beside a key of value zero that
 //     outweighs them by e^19 the other keys' weights still have 11 bits.
 //   - Rows past a sequence's end are never read: the copy fills them with zeros, so what
 //     a page holds there, NaN included, does not matter; the same goes for keys hidden
@@ -73,12 +73,12 @@ constexpr int kSms = 152;  // of a GB300
 constexpr int kThreads = 32 * kPagedWarps;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
-// How far, in log2 units, a score may pass the running max before that moves: weights stay
-// <= 2^kGrow.  8-bit pages hold weights in fp16, 2^kLift8 times the weight, so that the
-// largest fill its range (kGrow8 + kLift8 = 15) and its 11 bits reach as far down as they
-// can.  (8 and 0 against 1 and 14: 16 sequences of 16384 keys, 32 rows per key head 163.3
-// and 164.7 us; 8 of up to 32768 and 96 of up to 12000, alike.)
-constexpr float kGrow = 8.0f, kGrow8 = 1.0f, kLift8 = 14.0f;
+// How far, in log2 units, scores may pass the running reference before that moves, and how
+// far below the largest score it then lies: weights stay <= 2^kGrow.  8-bit pages hold
+// weights in fp16, whose 11 bits reach as far down as they can when the largest lie at the
+// top of its range.  (kLift8 14 and kGrow8 15 against 0 and 8: 16 sequences of 16384 keys, 32
+// rows per key head 163.2 and 162.9 us; 8 of up to 32768 and 96 of up to 12000, alike.)
+constexpr float kGrow = 8.0f, kLift8 = 14.0f, kGrow8 = 15.0f;
 enum : uint32_t { kSitePagedSmem = 51 };
 
 // Ring slots per warp and CTAs per SM: 130 to 200 KB of slots per SM, and as many warps as
@@ -256,7 +256,7 @@ struct PagedShared {
     } slot[WARPS][4][2];  // [warp][ring slot][tile]
     int scan[WARPS];
     int at_b[WARPS], at_before[WARPS];  // a share's first sequence, tiles of those before it
-    float m[WARPS][16], l[WARPS][16];   // WHOLE: each warp's running max and sum
+    float m[WARPS][16], l[WARPS][16];   // WHOLE: each warp's reference and sum
     float lse[WARPS > kPagedWarps ? 64 : 1];  // of a cluster's block: log2 of its rows' sums
 };
 template <int D, int NT, bool F8, int WARPS>
@@ -276,7 +276,7 @@ fa_paged_kernel(const PagedParams p) {
     constexpr int MT = D / 16;          // 16-column tiles of V^T
     constexpr int KS = D / 16;          // 16-element steps of q.k
     constexpr int kChunksK = D / (F8 ? 64 : 32);  // 16-byte pieces of a key row per thread
-    constexpr float kSlack = F8 ? kGrow8 : kGrow;
+    constexpr float kSlack = F8 ? kGrow8 : kGrow, kLift = F8 ? kLift8 : 0.f;
     extern __shared__ __align__(1024) uint8_t smem[];
     using Shared = PagedShared<WARPS>;
     Shared& sh = *reinterpret_cast<Shared*>(smem + WARPS * L::kWarpRing);
@@ -535,7 +535,7 @@ fa_paged_kernel(const PagedParams p) {
             }
 
         float acc[NT][MT][4];
-        float m_run[NT][2], l_run[NT][2], mv_run[NT][2], fac[NT][2];  // fac: 2^(m - mv + kLift8)
+        float m_run[NT][2], l_run[NT][2], mv_run[NT][2], fac[NT][2];  // fac: 2^(m - mv)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -597,7 +597,7 @@ fa_paged_kernel(const PagedParams p) {
                 }
             }
 
-            // scale, mask; s becomes the score less the running max (log2 units)
+            // scale, mask; s becomes the score less the running reference (log2 units)
             bool grow = false;
             float vsc[TP], lvs[TP];
 #pragma unroll
@@ -617,7 +617,7 @@ fa_paged_kernel(const PagedParams p) {
                         const float m = m_run[nt][e];  // -inf until the row has seen a key
                         scale[e] = F8 ? rs[nt][e] * ksc : rs[nt][e];
                         ref[e] = m == -INFINITY ? 0.f : m;
-                        // the largest that the running maxima allow (8-bit: that of P vs, too)
+                        // the largest that the references allow (8-bit: that of P vs, too)
                         most[e] = F8 ? kSlack + fminf(0.f, mv_run[nt][e] - lvs[tp] - m) : kSlack;
                         if (m == -INFINITY) most[e] = -INFINITY;
                     }
@@ -636,7 +636,7 @@ fa_paged_kernel(const PagedParams p) {
                 }
             }
             if (__any_sync(0xffffffffu, grow)) {
-                // (rare: on a piece's first tiles, and where scores rise by more than 2^kSlack)
+                // (rare: on a piece's first tiles, and where scores rise by more than the slack)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -646,7 +646,7 @@ fa_paged_kernel(const PagedParams p) {
 #pragma unroll
                         for (int tp = 0; tp < TP; ++tp) {
                             mx[tp] = ref + max_over_g(fmaxf(s[tp][nt][e], s[tp][nt][e + 2]));
-                            m_new = fmaxf(m_new, mx[tp]);
+                            m_new = fmaxf(m_new, mx[tp] - kLift);
                         }
                         const float alpha = m == -INFINITY ? 1.f : ex2(m - m_new);
                         const float down = m_new == -INFINITY ? 0.f : m_new - ref;
@@ -656,10 +656,10 @@ fa_paged_kernel(const PagedParams p) {
                         if constexpr (F8) {
                             float mv_new = mv_run[nt][e];
 #pragma unroll
-                            for (int tp = 0; tp < TP; ++tp) mv_new = fmaxf(mv_new, mx[tp] + lvs[tp]);
+                            for (int tp = 0; tp < TP; ++tp) mv_new = fmaxf(mv_new, mx[tp] + lvs[tp] - kLift);
                             beta = mv_new == -INFINITY ? 1.f : ex2(mv_run[nt][e] - mv_new);
                             mv_run[nt][e] = mv_new;
-                            fac[nt][e] = mv_new == -INFINITY ? 0.f : ex2(m_new - mv_new + kLift8);
+                            fac[nt][e] = mv_new == -INFINITY ? 0.f : ex2(fminf(m_new - mv_new, 127.f));
                         }
 #pragma unroll
                         for (int tp = 0; tp < TP; ++tp) {
@@ -686,7 +686,8 @@ fa_paged_kernel(const PagedParams p) {
                     l_run[nt][0] += w[0] + w[2];
                     l_run[nt][1] += w[1] + w[3];
                     if constexpr (F8) {
-                        const float f0 = fac[nt][0] * vsc[tp], f1 = fac[nt][1] * vsc[tp];
+                        // (cut: with scales 2^100 apart the factor passes fp32, and a weight of 0 stays 0)
+                        const float f0 = fminf(fac[nt][0] * vsc[tp], 0x1p112f), f1 = fminf(fac[nt][1] * vsc[tp], 0x1p112f);
                         pb[nt][0] = movmatrix(pack_f16(w[0] * f0, w[1] * f1));
                         pb[nt][1] = movmatrix(pack_f16(w[2] * f0, w[3] * f1));
                     } else {
@@ -779,7 +780,7 @@ fa_paged_kernel(const PagedParams p) {
                     for (int k = 0; k < liw; ++k) l += sh.l[k * p.rwarps + rw][r] * ex2(sh.m[k * p.rwarps + rw][r] - ref);
                     // (a row that sees nothing: l = 0 and O = 0, LSE = -inf; NaN where a score was)
                     for (int k = 0; m == -INFINITY && k < liw; ++k) l += sh.l[k * p.rwarps + rw][r];
-                    f[nt][e] = l == 0.f ? 0.f : ex2((F8 ? mv_run[nt][e] - kLift8 : m_run[nt][e]) - ref) / l;
+                    f[nt][e] = l == 0.f ? 0.f : ex2((F8 ? mv_run[nt][e] : m_run[nt][e]) - ref) / l;
                     if (WW > kPagedWarps && cn > 1) {
                         if (lturn == 0 && g == 0) sh.lse[rw * R + r] = ref + lg2(l);
                     } else if (turn == 0 && g == 0 && r < rows) {
@@ -857,7 +858,7 @@ fa_paged_kernel(const PagedParams p) {
                 const float l = sum_over_g(l_run[nt][e]), m = m_run[nt][e];
                 // (a row that sees nothing: l = 0 and O = 0, LSE = -inf; NaN where a score was)
                 float f = l == 0.f ? 0.f : 1.f / l;
-                if (F8 && l != 0.f) f *= ex2(mv_run[nt][e] - kLift8 - m);
+                if (F8 && l != 0.f) f *= ex2(mv_run[nt][e] - m);
                 const float ls = (m == -INFINITY ? 0.f : m) + lg2(l);
                 if (r >= rows) continue;
                 constexpr int RUN = F8 ? D / 8 : 8;  // columns that lie together

@@ -251,8 +251,9 @@ FA_API fa_status fa_fwd_decode(const void* Q, const void* K, const void* V, void
  * token a token": the cache that each decode step reads and extends).
  *   K, V            [num_pages][H_kv][page_size][d], bf16, or e4m3 bytes for the
  *                   _fp8 entry points; 16-byte aligned, contiguous
- *   k_scale,v_scale fp32 [num_pages][H_kv], finite and > 0: the value of a code is
- *                   code * scale of its page and head.  NULL for a bf16 cache.
+ *   k_scale,v_scale fp32 [num_pages][H_kv], from 2^-110 to 2^125 (appending sets 2^-100
+ *                   to 2^121): the value of a code is code * scale of its page and
+ *                   head.  NULL for a bf16 cache.
  *   page_table      int [B][max_pages]; lens: int [B] (4-byte aligned)
  * page_size is a power of two from 16 to 256, max_pages * page_size at most 2^30 and
  * d 64 or 128 (else FA_ERR_UNSUPPORTED).  Table and lengths are device data, read on the

@@ -581,3 +581,31 @@ def test_8_bit_weights_far_below_a_dominant_key(H, Nq, lens, d):
         s["q"][:, h] = gap / math.sqrt(d)
     o, _ = check(s)
     assert float(o[0, 3].abs().max()) > 0
+
+
+def test_8_bit_scales_as_far_apart_as_they_come():
+    """A page of zero values (scale 2^-100) that holds the dominant key, the others at 2^60: the factor
+    between the two references passes fp32, and weights of zero stay zero."""
+    for length in (40, 14000):
+        s = build([length], 2, 1, 1, 64, 16, True, seed=51, poison=False)
+        k, v = (s[n].view(torch.uint8) for n in ("kc", "vc"))
+        k.zero_()
+        page = int(s["table"][0, 0])
+        v[page] = 0
+        k[page, 0, 0] = torch.full((64,), 256.0).to(torch.float8_e4m3fn).view(torch.uint8)
+        s["k_scale"].fill_(2.0 ** -8)
+        s["v_scale"].fill_(2.0 ** 60)
+        s["v_scale"][page] = 2.0 ** -100
+        s["q"].fill_(200.0 / 8 * math.log(2.0))      # the others lie 2^-200 below
+        o, lse = run(s)
+        # (17.25 in bf16: 2^-199.1) |O| <= 2^-199 * length * 448 * 2^60
+        assert bool((o.double().abs() <= 2.0 ** -115).all()) and bool(torch.isfinite(lse).all())
+    # one scale for all, at the ends of their range
+    for e in (-110, -100, 100, 125):
+        s = build([300], 2, 1, 1, 64, 16, True, seed=53, poison=False)
+        s["k_scale"].fill_(2.0 ** -8)
+        s["v_scale"].fill_(2.0 ** e)
+        s["vc"] = (torch.rand(s["vc"].shape, generator=torch.Generator().manual_seed(54)) < 0.5).float().to(torch.float8_e4m3fn)
+        o, _ = run(s)
+        s["v_scale"].fill_(1.0)
+        check(s, got=((o.double() * 2.0 ** -e).to(torch.float32), run(s)[1]))
