@@ -59,6 +59,7 @@ constexpr int kBK = 128;  // keys per CTA
 // reducer warps.
 constexpr int bwd_threads(int nwg) { return 32 * (4 * nwg + 3); }
 constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLiftP = 15.f, kUnliftP = 0x1p-15f;  // d = 128 with sinks: P as fp16 of 2^15 P
 // Which query tiles a key tile visits beyond causality.
 enum : int { kMaskNone = 0, kMaskWindow = 1, kMaskBlocks = 2, kMaskSinks = 3 };
 constexpr int kMaskWords = kMaxMaskBlocks / 32;
@@ -282,8 +283,9 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
     // With sinks dS is formed from P before its rounding to bf16 and rounded once,
     // where the other masks multiply two rounded factors (dQ, dK rel-L2 3.4e-3 ->
     // 2.5e-3): kept in fp32 at d = 64 (no slower), as fp16 pairs at d = 128, where fp32
-    // spills (10% slower; the pairs cost 1.7%).  P <= 1, so fp16 is off by 2^-11 of it,
-    // or 2^-25 in all below 2^-14.
+    // spills (10% slower; the pairs cost 1.7%).  P <= 1, so it is formed 2^15 times as large
+    // (kLiftP, added to -log2e LSE): fp16 is then off by 2^-11 of it down to P = 2^-29, far
+    // below a row's mean weight at any length.  dQ, dK and dV take the factor off.
     constexpr bool DS_FP32 = SINKS && D == 64, DS_FP16 = SINKS && D == 128;
     static_assert(!DS_FP16 || kQC == 32, "one chunk per warpgroup");
     // sinks with their key tiles split
@@ -588,6 +590,7 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                 for (int e = 0; e < 4; ++e) {
                     const int q = q_start + lane * 4 + e;
                     lv[e] = q < N ? -p.LSE[row0 + q] * kLog2e : -INFINITY;
+                    if constexpr (DS_FP16) lv[e] += kLiftP;
                     dv[e] = q < N ? -p.Dvec[row0 + q] : 0.f;
                 }
                 // the two halves of the stage are refilled as each is freed: dO (whose
@@ -1063,7 +1066,7 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
 #pragma unroll
                 for (int which = 0; which < 2; ++which) {
                     uint8_t* dst = smem + (PERSIST ? L::kStageKV + (which ? L::kTile : 0) : (which ? L::kK : L::kV));
-                    const float scale = which ? p.tau : 1.f;
+                    const float scale = (which ? p.tau : 1.f) * (DS_FP16 ? kUnliftP : 1.f);
                     const uint32_t src = which ? tDK : tDV;
 #pragma unroll
                     for (int cc = 0; cc < kDC; cc += 16) {
@@ -1544,14 +1547,15 @@ cudaError_t launch_bwd_t(const BwdArgs& a, cudaStream_t stream) {
         if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
         if (e != cudaSuccess) return e;
     }
-    // 3. dQ = tau * accumulator
+    // 3. dQ = tau * accumulator (d = 128 with sinks: less P's factor)
     {
         const int64_t n8 = rows * D / 8;
         int64_t blocks = (n8 + 255) / 256;
         if (blocks > 152 * 64) blocks = 152 * 64;
         return launch_dependent(fa_bwd_post_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
                                 stream, static_cast<const float*>(a.dQacc),
-                                static_cast<__nv_bfloat16*>(a.dQ), a.tau, n8);
+                                static_cast<__nv_bfloat16*>(a.dQ),
+                                a.tau * (MASK == kMaskSinks && D == 128 ? kUnliftP : 1.f), n8);
     }
 }
 

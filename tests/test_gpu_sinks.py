@@ -237,3 +237,61 @@ def test_all_keys_as_the_largest_number(N, d):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     check(x, tau, 1, most)
     check(x, tau, most, most)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_ds_of_weights_far_below_a_dominant_sink(d):
+    """Key 0 outweighs the others by e^17 in every row: their dS = P (dP - D) is a product with P near
+    2^-25, and their dK a sum of products with it.  One rounding of dS and one of the result, as above."""
+    N, w, s = 700, 200, 5
+    tau = 1 / math.sqrt(d)
+    x = draw(1, 4, N, d, seed=99)
+    x = {n: t.clone() for n, t in x.items()}
+    for n in "qk":
+        x[n][..., 0] = 0
+        x[n] *= 0.5
+    x["q"][..., 0] = 8.0
+    x["k"][:, :, 0] = 0
+    x["k"][:, :, 0, 0] = 17.0 / (8.0 * tau)
+    x["v"][:, :, 0] *= 0.0625
+    _, _, g = gpu(x, tau, w, s)
+    see = _plain.visible(N, N, w, s)
+    ref = _plain.attention_bwd(x["q"], x["k"], x["v"], x["do"], tau, see)
+    # (all but the last rows of the sequence have hundreds of summands)
+    for got, want in zip(g[1:], ref[1:]):
+        assert rel_l2(got[:, :, s:500], want[:, :, s:500].numpy()) <= 2.65e-3
+
+
+def test_ds_of_a_long_flat_window():
+    """Keys of zero: every row's weights are 1 over the number of keys that it sees, about 2^-17 behind
+    the window, so prefix sums give O and single keys' gradients.  151827 + 3 visible keys: in steps of
+    2^-24 that weight would be 110.5 steps, 0.45% from a whole number of them."""
+    N, d, w, s = 180000, 128, 151827, 3
+    tau = 1 / math.sqrt(d)
+    x = draw(1, 1, N, d, seed=100)
+    x = {n: t.clone() for n, t in x.items()}
+    x["k"].zero_()
+    o, lse, (dq, dk, dv) = gpu(x, tau, w, s)
+    q, v, do = (x[n][0, 0].double() for n in ("q", "v", "do"))
+    i = torch.arange(N)
+    first = (i - w + 1).clamp(min=s)          # first key of the window behind the sinks
+    seen = torch.where(i < s, i + 1, s + i + 1 - first)
+    run = torch.cat((torch.zeros(1, d, dtype=torch.float64), v.cumsum(0)))
+    ref_o = torch.where((i < s)[:, None], run[i + 1], run[s] + run[i + 1] - run[first]) / seen[:, None]
+    check_o(o[0, 0], ref_o.numpy())
+    check_lse(lse[0, 0], seen.double().log().numpy())
+    D = (do * ref_o).sum(1)
+    for keys in (torch.arange(s), torch.arange(90000, 90032), torch.arange(20000, 20032)):
+        ref_k, ref_v = [], []
+        for j in keys.tolist():
+            rows = slice(j, N if j < s else min(N, j + w))
+            p = 1.0 / seen[rows].double()
+            ref_v.append(p @ do[rows])
+            ref_k.append(tau * ((p * (do[rows] @ v[j] - D[rows])) @ q[rows]))
+        # The sinks' dK is mostly of the first rows, P = 1 / n for the n keys that they see, and there D, taken
+        # from O in bf16 (off by about 2^-8 / sqrt(6) of |O| = |V| / sqrt(n)), adds to the two roundings:
+        # relative to dP - D, of norm sqrt(1 - 1 / n), in all 2^-8 / sqrt(6) times the root of
+        # sum n^-3 / sum (n^-2 - n^-3) = 1.202 / 0.443: 2.6e-3, with the 2.3e-3 3.5e-3.
+        assert rel_l2(dk[0, 0][keys.to(DEV)], torch.stack(ref_k).numpy()) <= (4e-3 if int(keys[0]) < s else 2.65e-3)
+        assert rel_l2(dv[0, 0][keys.to(DEV)], torch.stack(ref_v).numpy()) <= 2.65e-3
+    assert float(dq.abs().max()) == 0.0
