@@ -849,7 +849,7 @@ fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constan
                     // bounds in one unsigned compare: 1k tokens, window 256 66 -> 62 us, 5001
                     // keys 152 -> 146)
                     const int hi = (LOCAL && wedge && (!SINKS || kg >= sinks)) ? kg + window - qh : (1 << 30);
-                    [[maybe_unused]] const uint32_t seen = hi > lo ? static_cast<uint32_t>(hi - lo) : 0u;
+                    [[maybe_unused]] const uint32_t seen = span(lo, hi);
 #pragma unroll
                     for (int c = 0; c < kQC / 32; ++c) {
                         uint32_t sv[32];

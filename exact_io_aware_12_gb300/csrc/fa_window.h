@@ -3,6 +3,8 @@
 // also runs on the host, where the tests call it.
 #pragma once
 
+#include <cstdint>
+
 #if defined(__CUDACC__)
 #define FA_WIN_HD __host__ __device__ __forceinline__
 #else
@@ -33,6 +35,12 @@ FA_WIN_HD WindowCut cut_window(int N, int window, int sinks) {
 FA_WIN_HD int sink_blocks(int sinks, int win, int block) {
     const int n = (sinks + block - 1) / block;
     return n < win ? n : win;
+}
+
+// Numbers x with lo <= x < hi, for bounds up to 2^30 either side of 0: one unsigned compare,
+// x - lo < span, tells whether x is among them.  (2^30 - -2^30 passes an int.)
+FA_WIN_HD uint32_t span(int lo, int hi) {
+    return hi > lo ? static_cast<uint32_t>(hi) - static_cast<uint32_t>(lo) : 0u;
 }
 
 }  // namespace fa

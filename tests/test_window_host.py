@@ -19,6 +19,7 @@ int t_hides(int n, int w, int s) { return window_hides(n, w, s); }
 int t_window(int n, int w, int s) { return cut_window(n, w, s).window; }
 int t_sinks(int n, int w, int s) { return cut_window(n, w, s).sinks; }
 int t_blocks(int s, int win, int block) { return sink_blocks(s, win, block); }
+uint32_t t_span(int lo, int hi) { return span(lo, hi); }
 }
 '''
 
@@ -31,7 +32,9 @@ def shim(tmp_path_factory):
     subprocess.run(["g++", "-O1", "-std=c++17", "-shared", "-fPIC", "-fsanitize=undefined",
                     "-fno-sanitize-recover=undefined", "-static-libubsan",
                     "-I", os.path.join(ROOT, "exact_io_aware_12_gb300", "csrc"), str(src), "-o", str(lib)], check=True)
-    return ctypes.CDLL(str(lib))
+    L = ctypes.CDLL(str(lib))
+    L.t_span.restype = ctypes.c_uint32
+    return L
 
 
 SIZES = (1, 2, 7, 29, 30, 31, 60, MOST - 126, MOST)
@@ -57,3 +60,14 @@ def test_sink_blocks_hold_the_sinks_before_the_window(shim):
                 for win in (0, 1, 3, (N - 1) // 128):
                     n = shim.t_blocks(sinks, win, 128)
                     assert n == min(-(-sinks // 128), win) and 0 <= n <= win
+
+
+def test_spans_up_to_their_widest(shim):
+    """Also the whole range of a sink's queries, 2^31 wide: no signed overflow."""
+    ends = (-2 ** 30, -2 ** 30 + 1, -200, -1, 0, 1, 127, 2 ** 30 - 1, 2 ** 30)
+    for lo in ends:
+        for hi in ends:
+            n = shim.t_span(lo, hi)
+            assert n == max(0, hi - lo)
+            for x in (0, 1, 64, 127):   # (the kernel's compare of columns of a tile)
+                assert ((x - lo) % 2 ** 32 < n) == (lo <= x < hi)
