@@ -353,10 +353,11 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_fp8_kernel(con
     const int b = last_not_above(p.B, unit, [&](int i) { return first_unit(cu_of(p, i), i, p.shift); });
     const int c0 = cu_of(p, b), c1 = cu_of(p, b + 1), past = p.lens[b];
     const int i = static_cast<int>(unit - first_unit(c0, b, p.shift));
-    if (c0 < 0 || c1 > p.T || c1 <= c0 || past < 0 || i < 0) {
+    if (c0 < 0 || c1 > p.T || c1 <= c0 || past < 0) {
         if (c1 != c0 && tid == 0) page_error(p.err);
         return;
     }
+    if (i < 0) return;  // rows before the first sequence's: no one's
     if (i >= pages_reached(past, c1 - c0, p.shift)) return;
     const int page = 1 << p.shift;
     const long long page0 = ((static_cast<long long>(past) >> p.shift) + i) << p.shift;  // position of the page's row 0

@@ -281,8 +281,8 @@ typedef struct fa_paged_cache {
  * Sequence b brings the rows cu_new[b] <= t < cu_new[b + 1] (device int [B + 1],
  * ascending; NULL: T / B rows each, T a multiple of B); row t stands at position
  * p = lens[b] + t - cu_new[b], where lens[b] keys are in the cache already (the
- * caller adds the new tokens to lens afterwards).  Rows from cu_new[B] on are
- * ignored: nothing of them is written, q_out included.
+ * caller adds the new tokens to lens afterwards).  Rows before cu_new[0] and from
+ * cu_new[B] on belong to no sequence: nothing of them is written, q_out included.
  *
  * k, v: bf16 [T][H_kv][d] and q, q_out: bf16 [T][H][d] with the given token (_st) and
  * head (_sh) strides in elements, columns contiguous, 16-byte aligned, strides multiples

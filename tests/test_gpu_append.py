@@ -331,3 +331,20 @@ def test_replayed_graph_follows_lengths_and_values():
     within(dev["vc"].cpu(), rv)
     within(torch.stack(qs, 1).flatten(0, 1), rq)
     assert api.last_device_error() == _lib.FA_OK
+
+
+# Rows that belong to no sequence, before the first one's; as many as pages hold and more
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("page,before", [(16, 3), (16, 16), (16, 100), (64, 64), (64, 200)])
+def test_counts_that_begin_behind_row_zero(page, before, fp8):
+    """A part of a batch: cu_new[0] > 0 is no error, and the rows before it are left alone."""
+    s = build([4, 20, 0], [30, 5, 70], 2, 4, 64, page, fp8, seed=803)
+    want, ref = run(s, freqs(64), False)
+    pad = lambda x: torch.cat((torch.full((before,) + x.shape[1:], 9.0, dtype=x.dtype), x))
+    s2 = dict(s, q=pad(s["q"]), k=pad(s["k"]), v=pad(s["v"]), cu=s["cu"] + before)
+    out = torch.full((before + 105, 4, 64), 7.0, dtype=torch.bfloat16, device=DEV)
+    q, got = run(s2, freqs(64), False, q_out=out)
+    assert api.last_device_error() == _lib.FA_OK
+    assert bool((q[:before] == 7).all()) and torch.equal(q[before:], want)
+    for n in ("kc", "vc", "ks", "vs"):
+        assert got[n] is None or torch.equal(got[n], ref[n])
