@@ -37,6 +37,8 @@
 namespace fa {
 namespace {
 
+constexpr int kAppendThreads = 256;
+
 struct AppendParams {
     const __nv_bfloat16* q;   // [T][H][d] by strides, or null
     const __nv_bfloat16* k;   // [T][H_kv][d] by strides
@@ -66,6 +68,16 @@ __device__ __forceinline__ void page_error(unsigned int* err) { atomicCAS(err, 0
 
 __device__ __forceinline__ int cu_of(const AppendParams& p, int b) {
     return p.cu ? p.cu[b] : b * (p.T / p.B);
+}
+
+// Reports token counts that do not ascend within [0, T], whether or not a row or page leads
+// to their sequence.  For one block: its threads [from, kAppendThreads).
+__device__ __forceinline__ void check_counts(const AppendParams& p, int from) {
+    if (p.cu == nullptr) return;
+    for (int b = static_cast<int>(threadIdx.x) - from; b < p.B; b += kAppendThreads - from) {
+        const int c0 = p.cu[b], c1 = p.cu[b + 1];
+        if (c0 < 0 || c1 < c0 || c1 > p.T) page_error(p.err);
+    }
 }
 
 // The largest b in [0, B) with key(b) <= x (0 if none), key non-decreasing: 32 probes at a
@@ -150,7 +162,6 @@ __device__ __forceinline__ uint4 pack8(const float* x) {
     return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-constexpr int kAppendThreads = 256;
 constexpr int kHeadGroups = 4;  // of a block: threads that share a token's angles
 constexpr int kMaxRot = 128;
 constexpr long long kWantBlocks = 4 * 152;  // as many as are resident
@@ -201,6 +212,8 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, RowShared<D>&
             sh.page[lane] = pg;
             sh.live[lane] = live;
         }
+    } else if (t_first == 0 && h0 == 0) {
+        check_counts(p, 32);  // (while the first warp looks for the tokens' places)
     }
     __syncthreads();
     const int half = p.rot / 2;
@@ -328,6 +341,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_fp8_kernel(con
         bx = turn < 2 * pairs ? turn / 2 : turn - pairs;
         const int rb = bx / p.q_groups, per = (p.H + p.q_groups - 1) / p.q_groups, h0 = (bx - rb * p.q_groups) * per;
         if (h0 < p.H) append_rows<D>(p, sh.row, rb * RowShared<D>::kTokens, h0, min(p.H, h0 + per));
+        else if (p.H == 0) check_counts(p, 0);  // (the one block that a call without queries has here)
         return;
     }
     const int group = bx % p.groups;
@@ -353,11 +367,11 @@ __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_fp8_kernel(con
     const int b = last_not_above(p.B, unit, [&](int i) { return first_unit(cu_of(p, i), i, p.shift); });
     const int c0 = cu_of(p, b), c1 = cu_of(p, b + 1), past = p.lens[b];
     const int i = static_cast<int>(unit - first_unit(c0, b, p.shift));
-    if (c0 < 0 || c1 > p.T || c1 <= c0 || past < 0) {
-        if (c1 != c0 && tid == 0) page_error(p.err);
+    // (nothing new, counts that check_counts reports, or rows before the first sequence's)
+    if (c1 <= c0 || c0 < 0 || c1 > p.T || i < 0 || past < 0) {
+        if (past < 0 && c1 > c0 && tid == 0) page_error(p.err);
         return;
     }
-    if (i < 0) return;  // rows before the first sequence's: no one's
     if (i >= pages_reached(past, c1 - c0, p.shift)) return;
     const int page = 1 << p.shift;
     const long long page0 = ((static_cast<long long>(past) >> p.shift) + i) << p.shift;  // position of the page's row 0
@@ -558,7 +572,7 @@ cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream) {
     }
     p.q_groups = static_cast<int>(std::max(1ll, std::min<long long>((kWantBlocks + row_blocks - 1) / row_blocks,
                                                                     (p.H + kHeadGroups - 1) / kHeadGroups)));
-    const long long q_blocks = p.H > 0 ? row_blocks * p.q_groups : 0;
+    const long long q_blocks = p.H > 0 ? row_blocks * p.q_groups : 1;
     kv_blocks *= p.groups;
     if (kv_blocks + q_blocks > 0x3fffffffll) return cudaErrorInvalidValue;
     p.kv_blocks = static_cast<int>(kv_blocks);

@@ -294,8 +294,10 @@ typedef struct fa_paged_cache {
  * [rot / 2], radians per position), exact at any position and rounded once to bf16.
  * rot = 0 with inv_freq NULL (and no q): nothing turns.
  * A token whose position, page or sequence's counts are out of bounds is not stored
- * (FA_ERR_PAGE); its query is rotated all the same.  No two sequences may append to the
- * same page.  K, V, the scales and q_out must not overlap what else the call reads or
+ * (FA_ERR_PAGE); its query is rotated all the same.  Counts that descend give FA_ERR_PAGE
+ * too: rows that they leave to no sequence are left alone, rows that they give to two are
+ * unspecified.  No page may be appended to twice in a call, by two sequences or by one
+ * whose table names it twice.  K, V, the scales and q_out must not overlap what else the call reads or
  * writes (q_out = q aside).
  */
 FA_API fa_status fa_kv_append(const fa_paged_cache* cache, const void* k, long long k_st,

@@ -348,3 +348,46 @@ def test_counts_that_begin_behind_row_zero(page, before, fp8):
     assert bool((q[:before] == 7).all()) and torch.equal(q[before:], want)
     for n in ("kc", "vc", "ks", "vs"):
         assert got[n] is None or torch.equal(got[n], ref[n])
+
+
+# counts of three sequences and 40 rows, and which sequences they refuse
+BAD_COUNTS = [([0, 5, 3, 9], [1]), ([0, 30, 3, 40], [1]), ([0, 41, 41, 41], [0, 1, 2]), ([-1, 10, 20, 30], [0]),
+              ([0, 10, 20, 45], [2]), ([5, 3, 3, 40], [0]), ([0, 0, -4, 0], [1, 2]), ([39, 0, 0, 0], [0])]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("cu,refused", BAD_COUNTS)
+def test_bad_token_counts_are_reported_and_the_others_stored(cu, refused, fp8):
+    page = 16
+    s = build([4, 10, 7], [40, 45, 45], 2, 2, 64, page, fp8, seed=804)
+    s = dict(s, cu=torch.tensor(cu, dtype=torch.int32), **{n: s[n][:40] for n in "qkv"})
+    _, got = run(s, freqs(64), False)
+    assert api.last_device_error() == _lib.FA_ERR_PAGE
+    assert api.last_device_error() == _lib.FA_OK
+    for b in range(3):
+        pages = s["table"][b].long()
+        pages = pages[pages >= 0]
+        if b in refused or cu[b] == cu[b + 1]:
+            for n in ("kc", "vc", "ks", "vs"):
+                assert got[n] is None or torch.equal(got[n][pages], s[n][pages])
+            continue
+        # alone, with good counts
+        one = dict(s, table=s["table"][b:b + 1], lens=s["lens"][b:b + 1], cu=torch.tensor(cu[b:b + 2], dtype=torch.int32))
+        _, want = run(one, freqs(64), False)
+        if all(b == c or not (cu[c] < cu[b + 1] and cu[b] < cu[c + 1]) for c in range(3)):   # (its rows are only its own)
+            for n in ("kc", "vc", "ks", "vs"):
+                assert got[n] is None or torch.equal(got[n][pages], want[n][pages])
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_counts_are_all_looked_at(fp8):
+    """One descending pair among 1000 sequences, wherever it stands, also where no row leads to it."""
+    B = 1000
+    s = build([3] * B, [1] * B, 1, 1, 64, 16, fp8, seed=805)
+    for at in (None, 1, 400, 999):
+        cu = s["cu"].clone()
+        if at is not None:
+            cu[at] = cu[at + 1] + 1
+        for q in (True, False):
+            run(dict(s, cu=cu), freqs(64), False, q=q)
+            assert api.last_device_error() == (_lib.FA_OK if at is None else _lib.FA_ERR_PAGE)
