@@ -660,6 +660,13 @@ static fa_status append_common(const fa_paged_cache* c, bool fp8, const void* k,
         if (!in_place && (overlaps(q_out, os * 2, q, qs * 2) || overlaps(q_out, os * 2, k, ks * 2) ||
                           overlaps(q_out, os * 2, v, vs * 2)))
             return FA_ERR_INVALID_ARG;
+        if (in_place) {
+            // (rows: q, k and v may be slices of one tensor, but no key is a query's place)
+            const auto at = [](const void* x) { return static_cast<long long>(reinterpret_cast<uintptr_t>(x) / 2); };
+            const RowSet rows{at(q_out), qo_st, qo_sh, T, H};
+            if (rows_meet(rows, {at(k), k_st, k_sh, T, c->H_kv}, c->d) || rows_meet(rows, {at(v), v_st, v_sh, T, c->H_kv}, c->d))
+                return FA_ERR_INVALID_ARG;
+        }
         q_bytes = static_cast<size_t>(os) * 2;
         a.q_st = q_st;
         a.q_sh = q_sh;

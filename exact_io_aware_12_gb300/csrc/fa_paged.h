@@ -124,4 +124,37 @@ FA_HD int pages_reached(long long past, int n, int shift) {
 }
 FA_HD long long first_unit(long long cu_b, int b, int shift) { return (cu_b >> shift) + 2ll * b; }
 
+// Rows of d elements at [T][H] strides, first at `at`, all in elements of one address space.
+struct RowSet {
+    long long at, st, sh;
+    int T, H;
+    FA_HD long long span(int d) const { return (T - 1) * st + (H - 1) * sh + d; }
+};
+// Whether a row of `a` and one of `b` (as many tokens, strides not negative) share an element:
+// slices of one projection's output may lie between one another.  Where the spans overlap and
+// the token strides differ, or heads' strides do and pairs of heads are many, yes without a
+// closer look.
+FA_HD bool rows_meet(const RowSet& a, const RowSet& b, int d) {
+    const long long delta = b.at - a.at;
+    if (delta >= a.span(d) || -delta >= b.span(d)) return false;
+    const long long st = a.T > 1 ? a.st : 0, last = a.T - 1;
+    if (a.T > 1 && a.st != b.st) return true;
+    const bool alike = a.sh == b.sh;
+    if (!alike && static_cast<long long>(a.H) * b.H > (1 << 16)) return true;
+    // (alike: only the difference of the heads counts)
+    for (int ha = 0; ha < a.H; ++ha)
+        for (int hb = 0; hb < (alike && ha > 0 ? 1 : b.H); ++hb) {
+            // rows of tokens t and t + m are off + m st apart
+            const long long off = delta + hb * b.sh - ha * a.sh;
+            long long m = st > 0 ? -off / st : 0;  // the nearest, or next to it
+            m = m < -last ? -last : m > last ? last : m;
+            for (long long k = m - 1; k <= m + 1; ++k) {
+                if (k < -last || k > last) continue;
+                const long long gap = off + k * st;
+                if (gap < d && -gap < d) return true;
+            }
+        }
+    return false;
+}
+
 }  // namespace fa

@@ -391,3 +391,18 @@ def test_many_counts_are_all_looked_at(fp8):
         for q in (True, False):
             run(dict(s, cu=cu), freqs(64), False, q=q)
             assert api.last_device_error() == (_lib.FA_OK if at is None else _lib.FA_ERR_PAGE)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_heads_that_lie_between_one_another(fp8):
+    """One head's query, key and value side by side (head stride 3 d), queries turned in place."""
+    s = build([3, 40], [20, 1], 4, 4, 64, 16, fp8, seed=806)
+    want, ref = check(s, freqs(64), False, 16)
+    dev = {n: (t.to(DEV) if t is not None else None) for n, t in s.items()}
+    x = torch.stack((s["q"], s["k"], s["v"]), dim=2).to(DEV)   # [T, H, 3, d]
+    rest = x[:, :, 1:].clone()
+    q = x[:, :, 0]
+    assert api.kv_append(x[:, :, 1], x[:, :, 2], dev["kc"], dev["vc"], dev["table"], dev["lens"], cu_new=dev["cu"], q=q,
+                         inv_freq=freqs(64).to(DEV), k_scale=dev["ks"], v_scale=dev["vs"], q_out=q) is q
+    assert torch.equal(q.cpu(), want) and torch.equal(x[:, :, 1:], rest)
+    assert torch.equal(dev["kc"].cpu(), ref["kc"]) and torch.equal(dev["vc"].cpu(), ref["vc"])

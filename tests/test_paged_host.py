@@ -33,6 +33,9 @@ uint64_t t_turn(uint64_t b) { return turn_fraction(b); }
 int t_exp(uint32_t b) { return page_scale_exp(b); }
 int t_reached(long long p, int n, int sh) { return pages_reached(p, n, sh); }
 long long t_unit(long long c, int b, int sh) { return first_unit(c, b, sh); }
+int t_meet(const long long* a, const long long* b, int t, int ha, int hb, int d) {
+    return rows_meet({a[0], a[1], a[2], t, ha}, {b[0], b[1], b[2], t, hb}, d);
+}
 }
 '''
 
@@ -372,3 +375,39 @@ def test_python_checks():
             api.fwd_paged(*args, **kw)
     with pytest.raises(ValueError, match="CUDA"):
         api.kv_append(new, new, kc, kc, tb, ln)
+
+
+def test_rows_that_meet(shim):
+    """Against sets of elements: slices of one tensor in every order, rows that touch, tokens' strides
+    smaller than a token's heads, single tokens."""
+    g = torch.Generator().manual_seed(5)
+    r = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=g))
+    d, seen = 4, set()
+
+    def rows(x, t, h):
+        return {x[0] + i * x[1] + j * x[2] + e for i in range(t) for j in range(h) for e in range(d)}
+    for _ in range(6000):
+        t, ha, hb = r(1, 4), r(1, 4), r(1, 3)
+        a = [0, r(0, 40), r(0, 14)]
+        b = [r(-70, 70), a[1] if r(0, 4) else r(0, 40), a[2] if r(0, 1) else r(0, 14)]
+        want = bool(rows(a, t, ha) & rows(b, t, hb))
+        LL3 = ctypes.c_longlong * 3
+        got = bool(shim.t_meet(LL3(*a), LL3(*b), t, ha, hb, d))
+        assert got == want or (got and t > 1 and a[1] != b[1]), (a, b, t, ha, hb)
+        seen.add((got, want, a[2] == b[2]))
+    assert len(seen) >= 5
+    LL3 = ctypes.c_longlong * 3
+    x = lambda at, st=3 * 64 * 32, sh=64: LL3(at, st, sh)
+    assert not shim.t_meet(x(0), x(32 * 64), 2 ** 21, 32, 32, 64)          # [T][q heads | k heads | v heads]
+    assert not shim.t_meet(x(0, sh=192), x(64, sh=192), 2 ** 21, 32, 32, 64)   # [T][head][q, k, v]
+    assert shim.t_meet(x(0), x(31 * 64), 2 ** 21, 32, 32, 64)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_queries_turned_in_place_over_the_keys_are_refused(fp8):
+    q = dict(q=FAKE + 8 * GB, q_out=FAKE + 8 * GB, q_st=256, qo_st=256, H=2)
+    assert append(cache(fp8), fp8, k_st=256, **q) == _lib.FA_ERR_INVALID_ARG                       # k itself
+    assert append(cache(fp8), fp8, k=FAKE + 8 * GB + 128, k_st=256, **q) == _lib.FA_ERR_INVALID_ARG  # its second head
+    q["q"] = q["q_out"] = FAKE + 9 * GB
+    assert append(cache(fp8), fp8, v_st=256, **q) == _lib.FA_ERR_INVALID_ARG
+    assert append(cache(fp8), fp8, v=FAKE + 9 * GB + 256, v_st=384, **q) == _lib.FA_ERR_INVALID_ARG  # other token strides
