@@ -645,12 +645,14 @@ static fa_status append_common(const fa_paged_cache* c, bool fp8, const void* k,
     const long long ks = span(nk, k_st, k_sh), vs = span(nk, v_st, v_sh);
     if (ks < 0 || vs < 0) return FA_ERR_INVALID_ARG;
     size_t q_bytes = 0;  // of q_out
+    long long q_span = 0;
     const void* caches[] = {c->K, c->V};
     for (const void* x : caches)
         if (overlaps(x, cache_bytes, k, ks * 2) || overlaps(x, cache_bytes, v, vs * 2)) return FA_ERR_INVALID_ARG;
     if (has_q) {
         const long long qs = span(nq, q_st, q_sh), os = span(nq, qo_st, qo_sh);
         if (qs < 0 || os < 0) return FA_ERR_INVALID_ARG;
+        q_span = qs;
         const long long o3[3] = {qo_st, qo_sh, 0};
         if (!strided_distinct(nq, o3, c->d)) return FA_ERR_INVALID_ARG;
         // in place (the same rows) or apart from everything else
@@ -675,8 +677,13 @@ static fa_status append_common(const fa_paged_cache* c, bool fp8, const void* k,
     } else {
         a.q_st = a.q_sh = a.o_st = a.o_sh = 0;
     }
-    // what the kernels read as indices and angles lies apart from all that they write
+    // what the kernels read as indices and angles lies apart from all that they write, the new
+    // rows apart from the scales
     const size_t sb = fp8 ? static_cast<size_t>(c->num_pages) * c->H_kv * 4 : 0;
+    const void* scales[] = {c->k_scale, c->v_scale};
+    for (const void* x : scales)
+        if (fp8 && (overlaps(x, sb, k, ks * 2) || overlaps(x, sb, v, vs * 2) || (has_q && overlaps(x, sb, q, q_span * 2))))
+            return FA_ERR_INVALID_ARG;
     const void* ins[] = {c->page_table, c->lens, cu_new, inv_freq};
     const size_t in_bytes[] = {static_cast<size_t>(c->B) * c->max_pages * 4, static_cast<size_t>(c->B) * 4,
                                cu_new ? (static_cast<size_t>(c->B) + 1) * 4 : 0, static_cast<size_t>(rot) * 4};

@@ -411,3 +411,9 @@ def test_queries_turned_in_place_over_the_keys_are_refused(fp8):
     q["q"] = q["q_out"] = FAKE + 9 * GB
     assert append(cache(fp8), fp8, v_st=256, **q) == _lib.FA_ERR_INVALID_ARG
     assert append(cache(fp8), fp8, v=FAKE + 9 * GB + 256, v_st=384, **q) == _lib.FA_ERR_INVALID_ARG  # other token strides
+
+
+@pytest.mark.parametrize("scale", ["k_scale", "v_scale"])
+def test_scales_over_the_new_rows_are_refused(scale):
+    for at in (FAKE + 8 * GB, FAKE + 9 * GB + 64, FAKE + 11 * GB + 4):   # k, v and q
+        assert append(cache(True, **{scale: at}), True) == _lib.FA_ERR_INVALID_ARG
