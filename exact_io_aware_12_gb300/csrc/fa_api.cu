@@ -14,9 +14,9 @@
 #include "fa_window.h"
 #include "ptx.cuh"
 
-// One error word per device (each device holds its own copy of this
-// variable; host code must look its address up per device).
-__device__ unsigned int g_fa_error_word;
+// Two error words per device, of timeouts and of pages (each device holds its own copy of
+// this variable; host code must look its address up per device).
+__device__ unsigned int g_fa_error_word[2];
 
 namespace fa {
 namespace {
@@ -49,7 +49,7 @@ constexpr int kMaxDevices = 64;
 struct DeviceInfo {
     std::once_flag once;
     bool supported = false;
-    unsigned int* err_word = nullptr;  // device address of g_fa_error_word
+    unsigned int* err_word = nullptr;  // device address of g_fa_error_word[0]
 };
 DeviceInfo g_dev[kMaxDevices];
 
@@ -855,18 +855,19 @@ fa_status fa_last_device_error(void* stream) {
         cudaGetLastError();
         return FA_ERR_CUDA;
     }
-    unsigned int word = 0;
-    if (cudaMemcpy(&word, di->err_word, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) {
+    unsigned int words[2] = {0, 0};
+    if (cudaMemcpy(words, di->err_word, sizeof(words), cudaMemcpyDeviceToHost) != cudaSuccess) {
         cudaGetLastError();
         return FA_ERR_CUDA;
     }
-    if (word != 0) {
+    for (int i = 0; i < 2; ++i) {
+        if (words[i] == 0) continue;
         const unsigned int zero = 0;
-        if (cudaMemcpy(di->err_word, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) {
+        if (cudaMemcpy(di->err_word + i, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) {
             cudaGetLastError();
             return FA_ERR_CUDA;
         }
-        return (word & 1u) != 0 ? FA_ERR_TIMEOUT : FA_ERR_PAGE;
+        return i == 0 ? FA_ERR_TIMEOUT : FA_ERR_PAGE;
     }
     return FA_OK;
 }

@@ -63,9 +63,6 @@ struct AppendParams {
 __device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-// Records a length, token count or page number out of bounds.
-__device__ __forceinline__ void page_error(unsigned int* err) { atomicCAS(err, 0u, kErrPage); }
-
 __device__ __forceinline__ int cu_of(const AppendParams& p, int b) {
     return p.cu ? p.cu[b] : b * (p.T / p.B);
 }

@@ -109,9 +109,10 @@ struct PagedCache {
     int B, H_kv, d, num_pages, max_pages, shift;
 };
 
-// Error-word value of a length, token count or page number out of bounds (bit 0 is a
-// timeout's).
-constexpr unsigned int kErrPage = 2u;
+// Records a length, token count or page number out of bounds: in the second error word, so
+// that it never stands before a timeout (the first: 1 | site << 8 of the first wait that ran
+// out).
+__device__ __forceinline__ void page_error(unsigned int* err) { *reinterpret_cast<volatile unsigned int*>(err + 1) = 1u; }
 
 // Arguments of one append.  Strides in elements: token, head.
 struct AppendArgs {

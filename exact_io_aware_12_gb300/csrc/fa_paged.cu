@@ -241,7 +241,7 @@ __device__ __forceinline__ int clamp_len(const PagedParams& p, int b) {
     const int len = p.lens[b];
     const long long cap = static_cast<long long>(p.max_pages) << p.shift;
     if (len < 0 || len > cap) {
-        atomicCAS(p.err, 0u, kErrPage);
+        page_error(p.err);
         return len < 0 ? 0 : static_cast<int>(cap);
     }
     return len;
@@ -404,7 +404,7 @@ fa_paged_kernel(const PagedParams p) {
             page = -1;
             if (i < nv) {
                 page = page_of(table, p.max_pages, p.num_pages, p.shift, rg.key0(entry(i)));
-                if (page < 0) atomicCAS(p.err, 0u, kErrPage);
+                if (page < 0) page_error(p.err);
                 if constexpr (F8) {
                     if (page >= 0) {
                         const long long ph = static_cast<long long>(page) * p.H_kv + hk;

@@ -112,10 +112,11 @@ FA_API const char* fa_status_string(fa_status s);
 
 /*
  * Synchronises `stream`, then reads and clears the library's device error
- * word for the current device.  FA_ERR_TIMEOUT if some kernel launched since
+ * words for the current device.  FA_ERR_TIMEOUT if some kernel launched since
  * the last call gave up on a bounded wait, FA_ERR_PAGE if one met a cache
  * length, token count or page number out of bounds (see fa_paged_cache),
- * FA_ERR_CUDA if the stream reports an error, else FA_OK.
+ * FA_ERR_CUDA if the stream reports an error, else FA_OK.  Where both happened, the
+ * timeout first and the page at the next call.
  */
 FA_API fa_status fa_last_device_error(void* stream);
 

@@ -609,3 +609,15 @@ def test_8_bit_scales_as_far_apart_as_they_come():
         o, _ = run(s)
         s["v_scale"].fill_(1.0)
         check(s, got=((o.double() * 2.0 ** -e).to(torch.float32), run(s)[1]))
+
+
+def test_a_bad_page_does_not_hide_a_timeout():
+    s = build([100], 2, 1, 1, 64, 16, False, seed=52)
+    s["table"][0, 2] = -1
+    run(s)
+    st = torch.cuda.current_stream().cuda_stream
+    assert _lib.fa_watchdog_selftest(50_000_000, st) == _lib.FA_OK
+    run(s)
+    assert api.last_device_error() == _lib.FA_ERR_TIMEOUT
+    assert api.last_device_error() == _lib.FA_ERR_PAGE
+    assert api.last_device_error() == _lib.FA_OK
