@@ -1084,7 +1084,12 @@ int ctas_for(int d, int nt, bool fp8) {
 //   clusters: 8 segments, 1000 keys 8.2 us by two blocks and 8.9 by one, 3000 8.0 and split
 //     10.6, 9000 11.7 and 12.6; 32 segments, 2000 8.5 and 11.5; 64, 3000 17.0 and 17.4; one
 //     segment, 8000 keys 10.9 and 9.6.
-constexpr int kWholeTiles = 40, kWideTiles = 80, kWideRowTiles = 53, kNarrowTiles = 8, kMaxCluster = 8, kFewBlocks = 32;
+constexpr int kWholeTiles = 40, kWideTiles = 80, kWideRowTiles = 53, kNarrowTiles = 8, kMaxClusterLog2 = 3, kFewBlocks = 32;
+// Clusters of 1, 2, 4 and 8 blocks, one to an SM, that run at a time: a cluster's SMs lie in
+// one processing cluster, some of which hold an odd number (cudaOccupancyMaxActiveClusters,
+// alike on two chips).  More would take a second round: 16 segments of 3000 keys by eight
+// blocks 13.8 us, by four 9.2; 37 of 2000 by four 14.4, by two 10.3.
+constexpr int kClusters[kMaxClusterLog2 + 1] = {kSms, 76, 36, 15};
 
 // Workspace: segment headers, then the pieces' sums and outputs, each 256-aligned; none
 // for whole segments.
@@ -1114,8 +1119,8 @@ PagedPlan paged_plan(const PagedCache& c, int H, int Nq, int window, int sinks, 
     pl.wide = pl.segs <= kSms && work > kNarrowTiles;
     pl.cluster_log2 = 0;
     if (pl.wide)
-        while ((1 << pl.cluster_log2) < kMaxCluster && work > (per_block << pl.cluster_log2) / 2 &&
-               pl.segs << (pl.cluster_log2 + 1) <= kSms)
+        while (pl.cluster_log2 < kMaxClusterLog2 && work > (per_block << pl.cluster_log2) / 2 &&
+               pl.segs <= kClusters[pl.cluster_log2 + 1])
             ++pl.cluster_log2;
     // (where even clusters fill few SMs, a split takes over at half the length)
     const bool few = pl.wide && pl.segs << pl.cluster_log2 < kFewBlocks;

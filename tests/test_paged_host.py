@@ -417,3 +417,10 @@ def test_queries_turned_in_place_over_the_keys_are_refused(fp8):
 def test_scales_over_the_new_rows_are_refused(scale):
     for at in (FAKE + 8 * GB, FAKE + 9 * GB + 64, FAKE + 11 * GB + 4):   # k, v and q
         assert append(cache(True, **{scale: at}), True) == _lib.FA_ERR_INVALID_ARG
+
+
+def test_clusters_that_run_at_a_time():
+    """3000 keys: whole segments by clusters of four blocks up to the 36 that the machine holds at a
+    time, split from there on (two blocks are too few)."""
+    size = lambda B: _lib.fa_paged_workspace_size(cache(B=B, H_kv=1, d=128, page_size=64, max_pages=47), 4, 1, 0, 0)
+    assert [size(B) > 0 for B in (8, 15, 16, 19, 36, 37, 38, 39)] == [False] * 5 + [True] * 3
