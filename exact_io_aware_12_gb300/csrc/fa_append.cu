@@ -20,9 +20,9 @@
 // prompts (32 query and 8 key heads of 128, 524 MB) the bf16 kernel takes 85 us, 6.2 TB/s
 // or 91% of the copy bandwidth; into e4m3 pages (481 MB) 83 us, 5.8 TB/s: there the pages'
 // blocks compute (scale, rotate, round) about as long as they load.  One token of 64
-// sequences takes 4.3 and 6.1 us, which is launch and the latency of four dependent loads
-// (counts, length, page, row).  A thread owns 16
-// columns of a token (two 16-byte pieces that rotate into each other) and walks heads;
+// sequences, inputs out of L2, takes 5.3 to 6.1 and 5.7 to 6.5 us, which is launch and the
+// latency of four dependent loads (counts, length, page, row).  A thread owns 16 columns of
+// a token (two 16-byte pieces that rotate into each other) and walks heads;
 // what a token costs besides (its sequence, page, sines and cosines) is found once per
 // block or held in registers over the heads.
 #include <cuda_bf16.h>
@@ -274,8 +274,9 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, RowShared<D>&
 
 // Both kernels are launched as dependents of the kernel before them, so that their start-up
 // overlaps its end; every thread waits for it before it reads anything (by plain loads: the
-// inputs may still be written while this grid is being set up).  Calls in a row on one
-// stream: 6.2 -> 3.7 us each for one token of 64 sequences, 8.2 -> 5.6 us in 8 bits.
+// inputs may still be written while this grid is being set up).  One token of 64 sequences,
+// calls in a row launched one by one (inputs in L2): 6.2 us without and 3.7 with, in 8 bits
+// 8.2 and 5.6; from a captured graph, where a launch costs little, 3.7 and 3.9, 5.2 and 5.1.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads, 4) fa_kv_append_kernel(const AppendParams p) {
     __shared__ RowShared<D> sh;

@@ -50,8 +50,8 @@
 //     from all of the step's rows.
 //
 // Measured (d = 128, pages of 64): 48 sequences of up to 16384 keys, 8 key heads of 4
-// query heads, bf16, 2.0 GB: 290 us, 6.9 TB/s, 1.02 of the copy bandwidth (which reads and
-// writes; 83% of the DRAM's cycles); 96 of up to 12000, e4m3, 1.24 GB: 193 us, 6.4 TB/s, 0.95;
+// query heads, bf16, 2.0 GB: 288 to 292 us, 6.9 TB/s, 1.02 of the copy bandwidth (which reads
+// and writes; 86% of the DRAM's cycles); 96 of up to 12000, e4m3, 1.24 GB: 193 us, 6.4 TB/s, 0.95;
 // 8 of up to 32768, 16 heads, e4m3, 0.53 GB: 86 us, 6.1 TB/s, 0.90.  A split call's fixed
 // part is about 10 us: launch, the lengths' scan (2 us), table and first tiles (3 to 6 us,
 // all rings filling at once), the slowest warp's tail, the combine kernel (3 us).  With 16
