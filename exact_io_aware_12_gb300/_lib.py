@@ -34,10 +34,19 @@ class PagedCache(ctypes.Structure):
                 ("page_size", _I), ("max_pages", _I)]
 
 
+class Score(ctypes.Structure):
+    """fa_score."""
+    _fields_ = [("softcap", _F), ("slopes", _P), ("bias", _P), ("buckets", _P), ("bias_f32", _I),
+                ("num_buckets", _I), ("max_distance", _I), ("docs", _P), ("prefix", _P),
+                ("window", _I)]
+
+
 _C = ctypes.POINTER(PagedCache)
+_S = ctypes.POINTER(Score)
 _LL = ctypes.c_longlong
 _APPEND = [_C, _P, _LL, _LL, _P, _LL, _LL, _I, _P, _P, _LL, _LL, _P, _LL, _LL, _I, _P, _I, _I, _P]
 _PAGED = [_C, _P, _LL, _LL, _LL, _P, _LL, _LL, _LL, _P, _I, _I, _F, _I, _I, _P, _SZ, _P]
+_PAGED_SCORE = _PAGED[:15] + [_S] + _PAGED[15:]
 SIGNATURES = {
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P]),
     "fa_fwd_o32": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P]),
@@ -62,6 +71,13 @@ SIGNATURES = {
     "fa_paged_workspace_size": (_SZ, [_C, _I, _I, _I, _I]),
     "fa_fwd_paged": (_I, _PAGED),
     "fa_fwd_paged_fp8": (_I, _PAGED),
+    "fa_fwd_paged_score": (_I, _PAGED_SCORE),
+    "fa_fwd_paged_score_fp8": (_I, _PAGED_SCORE),
+    "fa_fwd_score_workspace_size": (_SZ, [_I, _I, _S]),
+    "fa_fwd_score": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _S, _P, _SZ, _P]),
+    "fa_bwd_score_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _S]),
+    "fa_bwd_score": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _S,
+                          _P, _SZ, _P]),
     "fa_fwd_blocks": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P, _I, _P]),
     "fa_bwd_blocks": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _I, _I, _I, _I, _F, _I,
                            _P, _I, _P]),
@@ -75,6 +91,10 @@ SIGNATURES = {
 # Block-mask geometry (FA_BLOCK_MASK_EDGE, FA_BLOCK_MASK_MAX_N).
 BLOCK_MASK_EDGE = 128
 BLOCK_MASK_MAX_N = 131072
+
+# Most buckets of a learned bias, and the farthest distance with an entry of its own.
+SCORE_MAX_BUCKETS = 1024
+SCORE_MAX_DISTANCE = 1024
 
 # Size of the fixed scratch array fa_bwd_noalloc uses (FA_NOALLOC_SCRATCH_BYTES).
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -211,6 +231,38 @@ def fa_fwd_paged_fp8(cache, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq
                      sinks, workspace, workspace_bytes, stream) -> int:
     return _call("fa_fwd_paged_fp8", cache, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq,
                  tau, window, sinks, workspace, workspace_bytes, stream)
+
+
+def fa_fwd_paged_score(cache, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq, tau, window,
+                       sinks, score, workspace, workspace_bytes, stream) -> int:
+    return _call("fa_fwd_paged_score", cache, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq,
+                 tau, window, sinks, score, workspace, workspace_bytes, stream)
+
+
+def fa_fwd_paged_score_fp8(cache, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq, tau, window,
+                           sinks, score, workspace, workspace_bytes, stream) -> int:
+    return _call("fa_fwd_paged_score_fp8", cache, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H,
+                 Nq, tau, window, sinks, score, workspace, workspace_bytes, stream)
+
+
+def fa_fwd_score_workspace_size(B, N, score) -> int:
+    return int(_call("fa_fwd_score_workspace_size", B, N, score))
+
+
+def fa_fwd_score(Q, K, V, O, LSE, B, H, H_kv, N, d, tau, causal, score, workspace, workspace_bytes,
+                 stream) -> int:
+    return _call("fa_fwd_score", Q, K, V, O, LSE, B, H, H_kv, N, d, tau, causal, score, workspace,
+                 workspace_bytes, stream)
+
+
+def fa_bwd_score_workspace_size(B, H, N, d, causal, score) -> int:
+    return int(_call("fa_bwd_score_workspace_size", B, H, N, d, causal, score))
+
+
+def fa_bwd_score(Q, K, V, O, dO, LSE, dQ, dK, dV, dBias, B, H, H_kv, N, d, tau, causal, score,
+                 workspace, workspace_bytes, stream) -> int:
+    return _call("fa_bwd_score", Q, K, V, O, dO, LSE, dQ, dK, dV, dBias, B, H, H_kv, N, d, tau,
+                 causal, score, workspace, workspace_bytes, stream)
 
 
 def fa_fwd_blocks(Q, K, V, O, LSE, B, H, N, d, tau, causal, block_mask, mask_heads, stream) -> int:

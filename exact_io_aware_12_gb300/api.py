@@ -3,9 +3,10 @@
 PyTorch only supplies device memory and the current stream; the tensors'
 data pointers go straight to ``fa_fwd`` / ``fa_bwd``.  Inputs must be CUDA
 bf16 tensors, contiguous, shaped [B, H, N, d].  The paged entry points
-(``kv_append``, ``fwd_paged``) and windows with sinks check and call in a small
-extension module (csrc/torch_binding.cpp), for their kernels can take less time
-than a call from Python.
+(``kv_append``, ``fwd_paged``), windows with sinks and attention with capped,
+biased or masked scores check and call in a small extension module
+(csrc/torch_binding.cpp), for their kernels can take less time than a call from
+Python.
 """
 from __future__ import annotations
 
@@ -56,15 +57,79 @@ def _check_blocks(blocks: torch.Tensor, ref: torch.Tensor) -> int:
     return heads
 
 
+def _scored(*options) -> bool:
+    """Whether any option of attention with changed scores is given."""
+    return any(x is not None for x in options)
+
+
+def distance_buckets(num_buckets: int, max_distance: int, bidirectional: bool = False,
+                     device=None) -> torch.Tensor:
+    """The ``buckets`` of a learned relative position bias whose buckets widen with
+    the distance: int32 [2 L + 1] on ``device``, entry L + i - j the bucket of a
+    query at i and a key at j.  The first half of the buckets holds one distance
+    each, the others grow evenly over the logarithm up to ``max_distance``, and the
+    last holds all beyond.  ``bidirectional``: half of the buckets (num_buckets even)
+    for keys at or before the query, half for keys behind it; else these share bucket 0.
+    The borders are exact (whole numbers compared, no rounded logarithm).  L is the
+    first distance of the last bucket."""
+    n = num_buckets // 2 if bidirectional else num_buckets
+    exact = n // 2
+    if num_buckets < 2 or exact < 1 or max_distance <= exact or (bidirectional and num_buckets % 2):
+        raise ValueError("need at least two buckets a side, evenly split, and max_distance beyond the exact ones")
+    if num_buckets > _lib.SCORE_MAX_BUCKETS or max_distance > _lib.SCORE_MAX_DISTANCE:
+        raise ValueError(f"at most {_lib.SCORE_MAX_BUCKETS} buckets and max_distance {_lib.SCORE_MAX_DISTANCE}")
+    log_n = n - exact  # bucket exact + k begins at the first x with (x / exact)^log_n >= (max_distance / exact)^k
+    past, b = [], 0
+    while not past or past[-1] < n - 1:
+        x = len(past)
+        if x <= exact:
+            b = x
+        else:
+            while b + 1 < n and (x ** log_n * exact ** (b + 1 - exact)
+                                 >= max_distance ** (b + 1 - exact) * exact ** log_n):
+                b += 1
+        past.append(min(b, n - 1))
+    if len(past) == 1:  # (one bucket a side)
+        past.append(past[0])
+    future = [n + x for x in past[:0:-1]] if bidirectional else [0] * (len(past) - 1)
+    return torch.tensor(future + past, dtype=torch.int32, device=device)
+
+
 def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool,
         tau: Optional[float] = None, out: Optional[torch.Tensor] = None,
         lse: Optional[torch.Tensor] = None, o_fp32: bool = False, window: Optional[int] = None,
-        blocks: Optional[torch.Tensor] = None, sinks: int = 0):
+        blocks: Optional[torch.Tensor] = None, sinks: int = 0, softcap: Optional[float] = None,
+        slopes: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+        buckets: Optional[torch.Tensor] = None, docs: Optional[torch.Tensor] = None,
+        prefix: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
     """Forward pass.  Returns (O, LSE): O bf16 (fp32 with ``o_fp32``) and LSE
     fp32 [B, H, N].  ``window`` (with ``causal``): each query sees only its
     ``window`` most recent keys (fa_fwd_window), and with ``sinks`` also the
     first ``sinks`` keys of the sequence (fa_fwd_sinks).  ``blocks``: a block
-    mask over 128 x 128 blocks (fa_fwd_blocks)."""
+    mask over 128 x 128 blocks (fa_fwd_blocks).
+
+    Any of the following changes the scores or hides keys (fa_fwd_score); k and v
+    may then have fewer heads, [B, H_kv, N, d]: query head h reads key head
+    h // (H // H_kv).  A bf16 O, no sinks and no block mask go with them.
+      softcap  scores become softcap * tanh(score / softcap)
+      slopes   fp32 [H]: scores fall by slopes[h] for each position between
+               query and key
+      bias     bf16 or fp32 [num_buckets, H] with ``buckets``, int32
+               [2 * max_distance + 1]: bias[buckets[max_distance + i - j], h] is
+               added, the distance cut to +-max_distance (see distance_buckets;
+               an entry outside [0, num_buckets) adds nothing)
+      docs     int32 [B, N]: tokens see their own run of equal numbers only; a
+               number below 0 is padding, which sees nothing and nothing sees
+      prefix   int32 [B], with ``causal``: the first prefix[b] positions are
+               visible from before them, too
+    The workspace (only documents take one) is allocated with torch when not given."""
+    if _scored(softcap, slopes, bias, buckets, docs, prefix):
+        if o_fp32 or sinks or blocks is not None:
+            raise ValueError("capped, biased or masked scores go with a bf16 O, no sinks and no block mask")
+        return _lib.binding().fwd_score(q, k, v, causal, tau, softcap, slopes, bias, buckets, docs,
+                                        prefix, window, out, lse, workspace)
+    if workspace is not None:
+        raise ValueError("this forward takes no workspace")
     if sinks and window is None:
         raise ValueError("sinks need a window")
     if window is not None and (not causal or o_fp32):
@@ -104,13 +169,48 @@ def workspace_bytes(B: int, H: int, N: int, d: int) -> int:
     return _lib.fa_bwd_workspace_size(B, H, N, d)
 
 
+def score_workspace_bytes(q: torch.Tensor, causal: bool, bias: Optional[torch.Tensor] = None,
+                          buckets: Optional[torch.Tensor] = None, docs: Optional[torch.Tensor] = None,
+                          prefix: Optional[torch.Tensor] = None, backward: bool = True) -> int:
+    """Bytes of workspace that ``bwd`` (or ``fwd``) takes for queries of this size with
+    these options."""
+    B, H, N, d = q.shape
+    at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    s = _lib.Score(0.0, None, at(bias), at(buckets), int(bias is not None and bias.dtype == torch.float32),
+                   0 if bias is None else bias.shape[0], 0 if buckets is None else buckets.shape[0] // 2,
+                   at(docs), at(prefix), 0)
+    if backward:
+        return _lib.fa_bwd_score_workspace_size(B, H, N, d, int(bool(causal)), s)
+    return _lib.fa_fwd_score_workspace_size(B, N, s)
+
+
 def bwd(q, k, v, o, do, lse, causal: bool, tau: Optional[float] = None,
         dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
         dv: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-        window: Optional[int] = None, blocks: Optional[torch.Tensor] = None, sinks: int = 0):
+        window: Optional[int] = None, blocks: Optional[torch.Tensor] = None, sinks: int = 0,
+        softcap: Optional[float] = None, slopes: Optional[torch.Tensor] = None,
+        bias: Optional[torch.Tensor] = None, buckets: Optional[torch.Tensor] = None,
+        docs: Optional[torch.Tensor] = None, prefix: Optional[torch.Tensor] = None,
+        dbias: Optional[torch.Tensor] = None, bias_grad: bool = True):
     """Backward pass.  Returns (dQ, dK, dV), bf16.  ``workspace`` (a byte
     tensor of at least ``workspace_bytes`` bytes) is allocated with torch when
-    not given, so the library itself allocates nothing."""
+    not given, so the library itself allocates nothing.
+
+    ``softcap`` to ``prefix`` as in ``fwd`` (fa_bwd_score; the workspace is then of
+    ``score_workspace_bytes``): dK and dV have k's heads, summed over the query
+    heads that share them.  With a ``bias`` its gradient, of its shape and type,
+    comes fourth (in ``dbias`` where given), unless ``bias_grad`` is false."""
+    if _scored(softcap, slopes, bias, buckets, docs, prefix):
+        if sinks or blocks is not None:
+            raise ValueError("capped, biased or masked scores go with no sinks and no block mask")
+        if not bias_grad and dbias is not None:
+            raise ValueError("dbias without bias_grad")
+        grads = _lib.binding().bwd_score(q, k, v, o, do, lse, causal, tau, softcap, slopes, bias, buckets,
+                                         docs, prefix, window, dq, dk, dv, dbias if bias_grad else False,
+                                         workspace)
+        return grads if bias is not None and bias_grad else grads[:3]
+    if dbias is not None:
+        raise ValueError("dbias without a bias")
     if sinks:
         if window is None:
             raise ValueError("sinks need a window")
@@ -251,14 +351,21 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
               page_table: torch.Tensor, lens: torch.Tensor, tau: Optional[float] = None,
               window: Optional[int] = None, sinks: int = 0, k_scale: Optional[torch.Tensor] = None,
               v_scale: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
-              lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+              lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              softcap: Optional[float] = None, slopes: Optional[torch.Tensor] = None,
+              bias: Optional[torch.Tensor] = None, buckets: Optional[torch.Tensor] = None):
     """Attention of a decode step over a paged cache (fa_fwd_paged; with scales
     the cache is e4m3: fa_fwd_paged_fp8).  q [B, H, Nq, d] (1 <= Nq <= 8, any
     strides that are multiples of 8) holds each sequence's last Nq positions,
     which ``lens`` counts; query head h reads key head h // (H // H_kv).
     ``window`` and ``sinks`` as in ``fwd``.  Returns (O bf16 [B, H, Nq, d], LSE
     fp32 [B, H, Nq]); a row without keys gives 0 and -inf.  The workspace is
-    allocated with torch when not given."""
+    allocated with torch when not given.  ``softcap``, ``slopes``, ``bias`` and
+    ``buckets`` as in ``fwd`` (fa_fwd_paged_score): distances are between positions
+    of the sequence."""
+    if _scored(softcap, slopes, bias, buckets):
+        return _lib.binding().fwd_paged(q, k_cache, v_cache, page_table, lens, tau, window, sinks, k_scale,
+                                        v_scale, out, lse, workspace, softcap, slopes, bias, buckets)
     return _lib.binding().fwd_paged(q, k_cache, v_cache, page_table, lens, tau, window, sinks, k_scale,
                                     v_scale, out, lse, workspace)
 
@@ -284,10 +391,42 @@ class _Attention(torch.autograd.Function):
         return dq, dk, dv, None, None, None, None
 
 
+class _ScoredAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, bias, causal, tau, window, softcap, slopes, buckets, docs, prefix):
+        o, lse = fwd(q, k, v, causal, tau, window=window, softcap=softcap, slopes=slopes, bias=bias,
+                     buckets=buckets, docs=docs, prefix=prefix)
+        ctx.save_for_backward(q, k, v, o, lse, bias, slopes, buckets, docs, prefix)
+        ctx.how = causal, tau, window, softcap
+        return o
+
+    @staticmethod
+    def backward(ctx, do):
+        q, k, v, o, lse, bias, slopes, buckets, docs, prefix = ctx.saved_tensors
+        causal, tau, window, softcap = ctx.how
+        grads = bwd(q, k, v, o, do.contiguous(), lse, causal, tau, window=window, softcap=softcap,
+                    slopes=slopes, bias=bias, buckets=buckets, docs=docs, prefix=prefix,
+                    bias_grad=ctx.needs_input_grad[3])
+        dbias = grads[3] if len(grads) > 3 else None
+        return (*grads[:3], dbias, None, None, None, None, None, None, None, None)
+
+
 def attention(q, k, v, causal: bool = False, tau: Optional[float] = None,
-              window: Optional[int] = None, sinks: int = 0) -> torch.Tensor:
+              window: Optional[int] = None, sinks: int = 0, softcap: Optional[float] = None,
+              slopes: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None,
+              buckets: Optional[torch.Tensor] = None, docs: Optional[torch.Tensor] = None,
+              prefix: Optional[torch.Tensor] = None) -> torch.Tensor:
     """O = softmax(tau Q K^T [causal]) V with autograd support; ``window`` and
-    ``sinks`` as in ``fwd``."""
+    ``sinks``, and ``softcap`` to ``prefix``, as in ``fwd``.  Gradients flow to q, k, v and
+    ``bias`` (not to ``slopes``).  A backward pass may be captured in a CUDA graph while no
+    eager graph of the same leaves lives (torch ties a leaf to the stream that it was first
+    used on)."""
+    if _scored(softcap, slopes, bias, buckets, docs, prefix):
+        if sinks:
+            raise ValueError("capped, biased or masked scores go with no sinks")
+        if slopes is not None and slopes.requires_grad:
+            raise ValueError("slopes take no gradient")
+        return _ScoredAttention.apply(q, k, v, bias, causal, tau, window, softcap, slopes, buckets, docs, prefix)
     return _Attention.apply(q, k, v, causal, tau, window, sinks)
 
 

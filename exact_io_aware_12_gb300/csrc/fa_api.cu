@@ -11,6 +11,7 @@
 #include "../../include/fa.h"
 #include "fa_internal.h"
 #include "fa_paged.h"
+#include "fa_score.h"
 #include "fa_window.h"
 #include "ptx.cuh"
 
@@ -751,10 +752,46 @@ size_t fa_paged_workspace_size(const fa_paged_cache* cache, int H, int Nq, int w
     return paged_workspace(c, H, Nq, cut_keys(window), cut_keys(sinks), cache->k_scale != nullptr);
 }
 
+// Bytes of what a fa_score names.
+struct ScoreBytes {
+    size_t slopes, table, buckets, docs, prefix;
+};
+// Checks a fa_score for B sequences of N tokens (N = 0: of a cache, without documents or prefix)
+// and H query heads, and fills the internal form (its window aside).
+static fa_status check_score(const fa_score* f, int B, int H, int N, ScoreMod* m, ScoreBytes* bytes) {
+    if (!(f->softcap == 0.f || (f->softcap >= 0x1p-20f && f->softcap <= 0x1p60f))) return FA_ERR_INVALID_ARG;
+    if (f->bias_f32 != 0 && f->bias_f32 != 1) return FA_ERR_INVALID_ARG;
+    if (f->window < 0) return FA_ERR_INVALID_ARG;
+    if ((f->bias != nullptr) != (f->buckets != nullptr) || (f->bias != nullptr && f->slopes != nullptr)) return FA_ERR_INVALID_ARG;
+    if (f->bias != nullptr) {
+        if (f->num_buckets < 1 || f->max_distance < 1) return FA_ERR_INVALID_ARG;
+        if (f->num_buckets > kScoreMaxBuckets || f->max_distance > kScoreMaxFar) return FA_ERR_UNSUPPORTED;
+        if ((reinterpret_cast<uintptr_t>(f->bias) & (f->bias_f32 ? 3u : 1u)) != 0) return FA_ERR_INVALID_ARG;
+        m->num_buckets = f->num_buckets;
+        m->far = f->max_distance;
+        m->table_f32 = f->bias_f32 != 0;
+    }
+    if (!aligned4(f->slopes) || !aligned4(f->buckets) || !aligned4(f->docs) || !aligned4(f->prefix)) return FA_ERR_INVALID_ARG;
+    if (N == 0 && B == 0 && (f->docs != nullptr || f->prefix != nullptr)) return FA_ERR_INVALID_ARG;
+    m->softcap = f->softcap;
+    m->slopes = f->slopes;
+    m->table = f->bias;
+    m->buckets = f->buckets;
+    m->docs = f->docs;
+    m->prefix = f->prefix;
+    bytes->slopes = f->slopes ? static_cast<size_t>(H) * 4 : 0;
+    bytes->table = f->bias ? static_cast<size_t>(f->num_buckets) * H * (f->bias_f32 ? 4 : 2) : 0;
+    bytes->buckets = f->bias ? (2 * static_cast<size_t>(f->max_distance) + 1) * 4 : 0;
+    bytes->docs = f->docs ? static_cast<size_t>(B) * N * 4 : 0;
+    bytes->prefix = f->prefix ? static_cast<size_t>(B) * 4 : 0;
+    return FA_OK;
+}
+
 static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, long long q_sb,
                               long long q_sh, long long q_sn, void* O, long long o_sb, long long o_sh,
                               long long o_sn, float* LSE, int H, int Nq, float tau, int window, int sinks,
-                              void* workspace, size_t workspace_bytes, void* stream) {
+                              void* workspace, size_t workspace_bytes, void* stream,
+                              const fa_score* score = nullptr) {
     PagedArgs a;
     size_t cache_bytes = 0;
     fa_status s = check_cache(c, fp8, &a.cache, &cache_bytes);
@@ -775,14 +812,20 @@ static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, 
     if (workspace != nullptr && workspace_bytes < need) return FA_ERR_WORKSPACE;
     const size_t lb = static_cast<size_t>(c->B) * H * Nq * 4, tb = static_cast<size_t>(c->B) * c->max_pages * 4;
     const size_t sb = fp8 ? static_cast<size_t>(c->num_pages) * c->H_kv * 4 : 0;
-    const void* ins[] = {Q, c->K, c->V, c->page_table, c->lens, c->k_scale, c->v_scale};
-    const size_t in_bytes[] = {static_cast<size_t>(qs) * 2, cache_bytes, cache_bytes, tb,
-                               static_cast<size_t>(c->B) * 4, sb, sb};
+    ScoreBytes mod{};
+    if (score != nullptr) {
+        s = check_score(score, 0, H, 0, &a.mod, &mod);
+        if (s != FA_OK) return s;
+    }
+    const void* ins[] = {Q, c->K, c->V, c->page_table, c->lens, a.mod.slopes, a.mod.table, a.mod.buckets, c->k_scale,
+                         c->v_scale};
+    const size_t in_bytes[] = {static_cast<size_t>(qs) * 2, cache_bytes, cache_bytes, tb, static_cast<size_t>(c->B) * 4,
+                               mod.slopes, mod.table, mod.buckets, sb, sb};
     const void* outs[] = {O, LSE, workspace};
     const size_t out_bytes[] = {static_cast<size_t>(os) * 2, lb, need};
     for (int o = 0; o < (workspace && need > 0 ? 3 : 2); ++o) {
-        for (int i = 0; i < (fp8 ? 7 : 5); ++i)
-            if (overlaps(outs[o], out_bytes[o], ins[i], in_bytes[i])) return FA_ERR_INVALID_ARG;
+        for (int i = 0; i < 10; ++i)
+            if (ins[i] != nullptr && overlaps(outs[o], out_bytes[o], ins[i], in_bytes[i])) return FA_ERR_INVALID_ARG;
         for (int o2 = 0; o2 < o; ++o2)
             if (overlaps(outs[o], out_bytes[o], outs[o2], out_bytes[o2])) return FA_ERR_INVALID_ARG;
     }
@@ -813,7 +856,7 @@ static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, 
     a.err = di->err_word;
     a.ev_start = t_ev_start;
     a.ev_stop = t_ev_stop;
-    const cudaError_t e = launch_fwd_paged(a, st);
+    const cudaError_t e = score != nullptr ? launch_fwd_paged_score(a, st) : launch_fwd_paged(a, st);
     if (own) cudaFreeAsync(ws, st);
     return map_cuda(e);
 }
@@ -832,6 +875,176 @@ fa_status fa_fwd_paged_fp8(const fa_paged_cache* cache, const void* Q, long long
                        size_t workspace_bytes, void* stream) {
     return paged_common(cache, true, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq, tau, window,
                         sinks, workspace, workspace_bytes, stream);
+}
+
+fa_status fa_fwd_paged_score(const fa_paged_cache* cache, const void* Q, long long q_sb, long long q_sh,
+                             long long q_sn, void* O, long long o_sb, long long o_sh, long long o_sn,
+                             float* LSE, int H, int Nq, float tau, int window, int sinks,
+                             const fa_score* score, void* workspace, size_t workspace_bytes, void* stream) {
+    if (score == nullptr || score->window != 0) return FA_ERR_INVALID_ARG;
+    return paged_common(cache, false, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq, tau, window,
+                        sinks, workspace, workspace_bytes, stream, score);
+}
+
+fa_status fa_fwd_paged_score_fp8(const fa_paged_cache* cache, const void* Q, long long q_sb,
+                                 long long q_sh, long long q_sn, void* O, long long o_sb, long long o_sh,
+                                 long long o_sn, float* LSE, int H, int Nq, float tau, int window,
+                                 int sinks, const fa_score* score, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+    if (score == nullptr || score->window != 0) return FA_ERR_INVALID_ARG;
+    return paged_common(cache, true, Q, q_sb, q_sh, q_sn, O, o_sb, o_sh, o_sn, LSE, H, Nq, tau, window,
+                        sinks, workspace, workspace_bytes, stream, score);
+}
+
+// A list of device buffers, for the checks that what a call writes lies apart from all else.
+struct Buffer {
+    const void* p;
+    size_t n;
+};
+// Whether every one of the first n_out buffers lies apart from all others (null: none).
+static bool apart(const Buffer* bs, int n_out, int n) {
+    for (int o = 0; o < n_out; ++o)
+        for (int i = o + 1; i < n; ++i)
+            if (bs[o].p != nullptr && bs[i].p != nullptr && overlaps(bs[o].p, bs[o].n, bs[i].p, bs[i].n)) return false;
+    return true;
+}
+
+// Checks that the forward and the backward share; *empty: no rows.  Fills the arguments'
+// sizes and scores.
+static fa_status score_shape(int B, int H, int H_kv, int N, int d, float tau, int causal, const fa_score* score,
+                             ScoreArgs* a, ScoreBytes* mod, bool* empty) {
+    if (score == nullptr || H_kv < 0) return FA_ERR_INVALID_ARG;
+    fa_status s = check_shape(B, H, N, d, tau, causal, empty);
+    if (s != FA_OK) return s;
+    if (H_kv == 0 ? H > 0 : H % H_kv != 0) return FA_ERR_INVALID_ARG;
+    s = check_score(score, B, H, N, &a->mod, mod);
+    if (s != FA_OK) return s;
+    if ((score->prefix != nullptr || score->window != 0) && !causal) return FA_ERR_INVALID_ARG;
+    if (*empty) return FA_OK;
+    // (the backward's grid, one block per key tile; window: cut to the N keys that there are)
+    if (static_cast<long long>(B) * H * ((static_cast<long long>(N) + 127) / 128) > INT_MAX) return FA_ERR_UNSUPPORTED;
+    a->mod.window = score->window < N ? score->window : 0;
+    a->B = B;
+    a->H = H;
+    a->H_kv = H_kv;
+    a->N = N;
+    a->d = d;
+    a->tau = tau;
+    a->causal = causal != 0;
+    return FA_OK;
+}
+
+size_t fa_fwd_score_workspace_size(int B, int N, const fa_score* score) {
+    if (score == nullptr || B <= 0 || N <= 0) return 0;
+    return score_fwd_workspace(B, N, score->docs != nullptr);
+}
+
+size_t fa_bwd_score_workspace_size(int B, int H, int N, int d, int causal, const fa_score* score) {
+    ScoreArgs a;
+    ScoreBytes mod;
+    bool empty = false;
+    if (score_shape(B, H, H, N, d, 1.f, causal, score, &a, &mod, &empty) != FA_OK || empty) return 0;
+    return score_bwd_workspace(a);
+}
+
+fa_status fa_fwd_score(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int H,
+                       int H_kv, int N, int d, float tau, int causal, const fa_score* score,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+    ScoreArgs a;
+    ScoreBytes mod;
+    bool empty = false;
+    fa_status s = score_shape(B, H, H_kv, N, d, tau, causal, score, &a, &mod, &empty);
+    if (s != FA_OK || empty) return s;
+    const void* ptrs[] = {Q, K, V, O, LSE};
+    for (const void* p : ptrs)
+        if (p == nullptr || !aligned16(p)) return FA_ERR_INVALID_ARG;
+    if (workspace != nullptr && !aligned16(workspace)) return FA_ERR_INVALID_ARG;
+    const size_t need = fa_fwd_score_workspace_size(B, N, score);
+    if (workspace != nullptr && workspace_bytes < need) return FA_ERR_WORKSPACE;
+    const size_t rows = static_cast<size_t>(B) * H * N, tb = rows * d * 2, kb = tb / H * H_kv;
+    const Buffer bs[] = {{O, tb}, {LSE, rows * 4}, {need > 0 ? workspace : nullptr, need}, {Q, tb}, {K, kb}, {V, kb},
+                         {a.mod.slopes, mod.slopes}, {a.mod.table, mod.table}, {a.mod.buckets, mod.buckets},
+                         {a.mod.docs, mod.docs}, {a.mod.prefix, mod.prefix}};
+    if (!apart(bs, 3, 11)) return FA_ERR_INVALID_ARG;
+    DeviceInfo* di = current_device(&s);
+    if (!di) return s;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    void* ws = need > 0 ? workspace : nullptr;
+    const bool own = need > 0 && workspace == nullptr;
+    if (own && cudaMallocAsync(&ws, need, st) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_CUDA;
+    }
+    a.Q = Q;
+    a.K = K;
+    a.V = V;
+    a.O = O;
+    a.LSE = LSE;
+    a.workspace = static_cast<uint8_t*>(ws);
+    a.err = di->err_word;
+    a.wait_limit_ns = g_wait_limit_ns.load();
+    a.ev_start = t_ev_start;
+    a.ev_stop = t_ev_stop;
+    const cudaError_t e = launch_score_fwd(a, st);
+    if (own) cudaFreeAsync(ws, st);
+    return map_cuda(e);
+}
+
+fa_status fa_bwd_score(const void* Q, const void* K, const void* V, const void* O, const void* dO,
+                       const float* LSE, void* dQ, void* dK, void* dV, void* dBias, int B, int H, int H_kv,
+                       int N, int d, float tau, int causal, const fa_score* score, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    ScoreArgs a;
+    ScoreBytes mod;
+    bool empty = false;
+    fa_status s = score_shape(B, H, H_kv, N, d, tau, causal, score, &a, &mod, &empty);
+    if (s != FA_OK) return s;
+    if (dBias != nullptr && a.mod.table == nullptr) return FA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(dBias) & (a.mod.table_f32 ? 3u : 1u)) != 0) return FA_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (empty) {  // (no pair: a gradient of zeros)
+        if (dBias == nullptr || mod.table == 0) return FA_OK;
+        const Buffer bs[] = {{dBias, mod.table}, {a.mod.table, mod.table}, {a.mod.buckets, mod.buckets}};
+        if (!apart(bs, 1, 3)) return FA_ERR_INVALID_ARG;
+        if (!current_device(&s)) return s;
+        return map_cuda(cudaMemsetAsync(dBias, 0, mod.table, st));
+    }
+    const void* ptrs[] = {Q, K, V, O, dO, LSE, dQ, dK, dV};
+    for (const void* p : ptrs)
+        if (p == nullptr || !aligned16(p)) return FA_ERR_INVALID_ARG;
+    if (workspace != nullptr && !aligned16(workspace)) return FA_ERR_INVALID_ARG;
+    const size_t need = score_bwd_workspace(a);
+    if (workspace != nullptr && workspace_bytes < need) return FA_ERR_WORKSPACE;
+    const size_t rows = static_cast<size_t>(B) * H * N, tb = rows * d * 2, kb = tb / H * H_kv;
+    const Buffer bs[] = {{dQ, tb}, {dK, kb}, {dV, kb}, {dBias, mod.table}, {workspace, need}, {Q, tb}, {K, kb}, {V, kb},
+                         {O, tb}, {dO, tb}, {LSE, rows * 4}, {a.mod.slopes, mod.slopes}, {a.mod.table, mod.table},
+                         {a.mod.buckets, mod.buckets}, {a.mod.docs, mod.docs}, {a.mod.prefix, mod.prefix}};
+    if (!apart(bs, 5, 16)) return FA_ERR_INVALID_ARG;
+    DeviceInfo* di = current_device(&s);
+    if (!di) return s;
+    void* ws = workspace;
+    if (workspace == nullptr && cudaMallocAsync(&ws, need, st) != cudaSuccess) {
+        cudaGetLastError();
+        return FA_ERR_CUDA;
+    }
+    a.Q = Q;
+    a.K = K;
+    a.V = V;
+    a.O = const_cast<void*>(O);
+    a.dO = dO;
+    a.LSE = const_cast<float*>(LSE);
+    a.dQ = dQ;
+    a.dK = dK;
+    a.dV = dV;
+    a.dTable = dBias;
+    a.workspace = static_cast<uint8_t*>(ws);
+    a.err = di->err_word;
+    a.wait_limit_ns = g_wait_limit_ns.load();
+    a.ev_start = t_ev_start;
+    a.ev_stop = t_ev_stop;
+    const cudaError_t e = launch_score_bwd(a, st);
+    if (workspace == nullptr) cudaFreeAsync(ws, st);
+    return map_cuda(e);
 }
 
 const char* fa_status_string(fa_status s) {

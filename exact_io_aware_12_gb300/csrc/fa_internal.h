@@ -128,6 +128,20 @@ struct AppendArgs {
     unsigned int* err;
 };
 
+// What changes the scores of an attention call, and which are hidden (fa_score in
+// include/fa.h; device pointers, validated by the caller).
+struct ScoreMod {
+    float softcap = 0.f;            // 0: none
+    const float* slopes = nullptr;  // [H]
+    const void* table = nullptr;    // [num_buckets][H], bf16 or fp32 (table_f32)
+    const int* buckets = nullptr;   // [2 far + 1]
+    bool table_f32 = false;
+    int num_buckets = 0, far = 0;
+    const int* docs = nullptr;      // [B][N]
+    const int* prefix = nullptr;    // [B]
+    int window = 0;                 // causal sliding window, at most N (0: none)
+};
+
 // Arguments of one attention step over a paged cache.  Strides in elements: sequence,
 // head, row.
 struct PagedArgs {
@@ -139,6 +153,7 @@ struct PagedArgs {
     long long q_sb, q_sh, q_sn, o_sb, o_sh, o_sn;
     int H, Nq, window, sinks;
     float tau;
+    ScoreMod mod;      // (launch_fwd_paged_score; no documents, prefix or window of its own)
     unsigned int* err;
     cudaEvent_t ev_start;  // optional: recorded around the two kernels
     cudaEvent_t ev_stop;
@@ -148,6 +163,31 @@ struct PagedArgs {
 size_t paged_workspace(const PagedCache& c, int H, int Nq, int window, int sinks, bool fp8);
 // 16-key tiles that full tables hold, which 32-bit counts must not pass.
 long long paged_max_tiles(int B, int H, int H_kv, int Nq, int max_pages, int shift);
+
+// Arguments of attention with such scores, forward and backward.
+struct ScoreArgs {
+    const void* Q;   // bf16 [B][H][N][d]; K, V [B][H_kv][N][d]
+    const void* K;
+    const void* V;
+    void* O;         // (the backward does not need it)
+    float* LSE;      // (backward: read)
+    const void* dO = nullptr;
+    void* dQ = nullptr;
+    void* dK = nullptr;
+    void* dV = nullptr;
+    void* dTable = nullptr;  // [num_buckets][H], of the table's type
+    uint8_t* workspace;
+    int B, H, H_kv, N, d;
+    float tau;
+    bool causal;
+    ScoreMod mod;
+    unsigned int* err;
+    unsigned long long wait_limit_ns;
+    cudaEvent_t ev_start;  // optional: recorded around the main kernel
+    cudaEvent_t ev_stop;
+};
+size_t score_fwd_workspace(int B, int N, bool docs);
+size_t score_bwd_workspace(const ScoreArgs& a);
 
 // How the decode forward cuts the KV cache: `splits` chunks of `chunk` keys
 // (a multiple of 64).  Depends only on its arguments.
@@ -211,9 +251,17 @@ cudaError_t launch_fwd_short(const FwdArgs& a, cudaStream_t stream);
 // d = 128 with a block mask, bf16 O: the persistent block-sparse forward
 cudaError_t launch_fwd_sparse(const FwdArgs& a, cudaStream_t stream);
 cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t stream);
+cudaError_t launch_score_fwd(const ScoreArgs& a, cudaStream_t stream);
+cudaError_t launch_score_bwd(const ScoreArgs& a, cudaStream_t stream);
+// D_i = sum_j P_ij dP_ij and a zeroed dQ accumulator (spans and bias2: of the workspace, or null)
+cudaError_t launch_score_rows(const ScoreArgs& a, float* dvec, float* acc, const void* spans, const float* bias2,
+                              cudaStream_t stream);
+// documents' ids [B][N] -> each token's document as [first, end) (int2 [B][N])
+cudaError_t launch_score_spans(const int* docs, void* spans, int B, int N, cudaStream_t stream);
 cudaError_t launch_decode(const DecArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream);
+cudaError_t launch_fwd_paged_score(const PagedArgs& a, cudaStream_t stream);
 cudaError_t launch_fwd_fp8(const Fp8Args& a, cudaStream_t stream);
 cudaError_t launch_watchdog_selftest(unsigned int* err, unsigned long long limit_ns,
                                      cudaStream_t stream);

@@ -1,0 +1,955 @@
+// Backward of attention whose scores are capped, biased by distance or masked (forward:
+// fa_score_fwd.cu), with grouped heads and the gradient of a learned bias, for sm_103a.
+//
+// Mathematics: with x = tau q_i.k_j and y = cap tanh(x / cap) + b(h, i - j) (or x + b),
+//   P = exp(y - LSE_i),  D_i = sum_j P_ij dP_ij,  dP = dO V^T,  dY = P o (dP - D),
+//   dX = dY (1 - tanh^2(x / cap)),  dV = P^T dO,  dK = tau dX^T Q,  dQ = tau dX K,
+// summed over the query heads that share a key head; the bias's gradient is the sum of dY
+// over the pairs of each bucket.
+//
+// Kernels:
+//   spans     documents' ranges (with documents)
+//   expand    the table's biases by distance (with a table; log2 units)
+//   rows      D_i and a zeroed fp32 dQ accumulator (fa_score_rows.cu)
+//   main      one CTA per (128-key tile, key head).  It keeps K and V and walks the query
+//             tiles that see its keys, head by head of the group, summing dK and dV in
+//             tensor memory over all of them: shared heads need no sum afterwards.  Per step
+//             S^T = K Q^T and dP^T = V dO^T (tcgen05), P^T and dX^T by elementwise warps (a
+//             key row per thread, P^T to tensor memory, dX^T to shared memory), dV += P^T dO,
+//             dQ = dX K (read out and added to the accumulator by TMA reductions), dK += dX^T Q.
+//   post      dQ = bf16(tau * accumulator)
+//   buckets, table   the bias's gradient (below), with a table
+//
+// dX enters the products as bf16, rounded once from fp32: P (1 - tanh^2) waits for dP^T as
+// fp16 of 2^15 times its value, which is off by 2^-11 of it down to 2^-29; dQ, dK, dV
+// take the factor off.
+//
+// The bias's gradient: pairs at one distance lie on a diagonal.  A tile pair all of whose
+// distances are `far` or more (most of them in a long sequence: the last bucket begins near)
+// has one bucket, and its dY are summed in fp32 registers over the steps.  In the near ones
+// each warp sums a 32 x 32 block's 63 diagonals: it turns column q's 32 values by q lanes (one
+// shuffle), so that lane m holds the value at distance m or m - 32 of the block's.
+// The sums go to memory, 64 per block, and two small kernels add them in a fixed order: no
+// atomics.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "fa_score.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kBQ = 128, kBK = 128;
+constexpr int threads_for(int nwg) { return 32 * (4 * nwg + 3); }
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLiftP = 15.f, kUnliftP = 0x1p-15f;
+
+template <int D>
+struct ScoreBwdLayout {
+    static constexpr int kTile = kBK * D * 2;  // one bf16 [128 x D] tile
+    static constexpr int kBox = 128 * 128;     // [128 rows x 64 bf16] or [128 x 32 fp32]
+    static constexpr int kBoxes = D / 64;
+    static constexpr int kK = 0;
+    static constexpr int kV = kTile;
+    static constexpr int kStage0 = 2 * kTile;    // stage s: Q at +0, dO at +kTile
+    static constexpr int kStageBytes = 2 * kTile;
+    static constexpr int kDS = kStage0 + 2 * kStageBytes;  // dX^T [128 keys x 128 queries] bf16
+    static constexpr int kVec = kDS + 128 * 128 * 2;       // lse2[2][128], dvec[2][128]
+    static constexpr int kBars = kVec + 4 * 128 * 4;
+    static constexpr int kBytes = kBars + 256;
+    // tensor-memory columns: dV, dK (D each), S^T, dP^T; dQ over dP^T at d = 128, its own at 64
+    static constexpr uint32_t kTmDV = 0, kTmDK = D, kTmS = 2 * D, kTmDP = 2 * D + 128;
+    static constexpr bool kDQAliasDP = D == 128;
+    // dK's A operand: dX^T from tensor memory (beside P^T) at d = 128, from shared memory at 64
+    static constexpr bool kDSInTmem = D == 128;
+    static constexpr uint32_t kTmDQ = kDQAliasDP ? kTmDP : 2 * D + 256;
+};
+
+struct ScoreBwdShared {
+    uint64_t kv_full;
+    uint64_t q_full[2];    // Q tile (and the LSE / D vectors) of stage s loaded
+    uint64_t do_full[2];
+    uint64_t q_empty[2];   // stage s's Q half free: MMAs done, staged dQ half read
+    uint64_t do_empty[2];
+    uint64_t s_full, dp_full, p_ready, ds_ready, dq_full, dq_drained;
+    uint64_t dq_staged_q;   // dQ columns [0, D/2) staged over Q
+    uint64_t dq_staged_do;  // dQ columns [D/2, D) staged over dO
+    uint64_t dk_done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+// The table gradient's partial sums, in the workspace.
+constexpr int kNearFloats = 1024;  // of a near tile pair: 16 blocks of 64
+constexpr int kFarFloats = 2;      // of a warp: the sum over far keys behind the query, and before it
+
+struct ScoreBwdParams {
+    const float* LSE;
+    const float* Dvec;
+    int H, H_kv, G, n_kv, head_group;
+    ScoreMask mask;
+    float scale_log2, tau;
+    float x_scale, cap_log2;
+    const float* slopes;
+    const float* bias2;  // [H][2 far + 1], log2 units
+    int far;
+    float* near_part;    // [B H][n_kv][near_n][kNearFloats], or null
+    float* far_part;     // [B H][n_kv][4 NWG][kFarFloats]
+    int near_lo, near_n;  // near tile pairs: query tile - key tile from near_lo on
+    unsigned int* err;
+    unsigned long long wait_limit_ns;
+};
+
+enum : uint32_t {
+    kSiteProd = 71, kSiteMmaKV = 72, kSiteMmaQ = 73, kSiteMmaP = 74, kSiteMmaDS = 75, kSiteMmaDrain = 76,
+    kSiteDsS = 77, kSiteDsQ = 78, kSiteDsDP = 79, kSiteDsDQ = 80, kSiteDrain = 81, kSiteReduce = 82
+};
+
+__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
+
+constexpr uint32_t kDescHi = sw128_desc_hi(1024);
+constexpr uint32_t kLboMN = 128 * 128;
+
+// D = A B^T, both K-major tiles of 128 rows x Dk.
+template <int Dk>
+__device__ __forceinline__ void mma_rows_rows(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo) {
+    constexpr uint32_t id = idesc_bf16(128, 128, false, false);
+#pragma unroll
+    for (int k = 0; k < Dk / 16; ++k) {
+        const uint32_t off = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;
+        if (k == 0) mma_ss_warp<0>(tmem_d, a_lo + off, b_lo + off, kDescHi, id);
+        else mma_ss_warp<1>(tmem_d, a_lo + off, b_lo + off, kDescHi, id);
+    }
+}
+// D (+)= A_tmem[128 x 128] B, B an MN-major tile; each warpgroup's QC columns of A lie packed over
+// the first half of its QC fp32 columns.
+template <int Dn, int QC>
+__device__ __forceinline__ void mma_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo, bool accumulate) {
+    constexpr uint32_t id = idesc_bf16(128, Dn, false, true);
+    if (accumulate) mma_ts_warp<1>(tmem_d, tmem_a, b_lo, kDescHi, id);
+    else mma_ts_warp<0>(tmem_d, tmem_a, b_lo, kDescHi, id);
+#pragma unroll
+    for (int k = 1; k < 128 / 16; ++k)
+        mma_ts_warp<1>(tmem_d, tmem_a + (16 * k / QC) * QC + (16 * k % QC) / 2, b_lo + ((k * 2048) >> 4), kDescHi, id);
+}
+// D (+)= A B, A a K-major tile [128 x 128], B MN-major.
+template <int Dn>
+__device__ __forceinline__ void mma_rows_mn(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo, bool accumulate) {
+    constexpr uint32_t id = idesc_bf16(128, Dn, false, true);
+    if (accumulate) mma_ss_warp<1>(tmem_d, a_lo, b_lo, kDescHi, id);
+    else mma_ss_warp<0>(tmem_d, a_lo, b_lo, kDescHi, id);
+#pragma unroll
+    for (int k = 1; k < 128 / 16; ++k)
+        mma_ss_warp<1>(tmem_d, a_lo + (((k / 4) * (128 * 128) + (k % 4) * 32) >> 4), b_lo + ((k * 2048) >> 4), kDescHi, id);
+}
+// D = A B, both MN-major.
+template <int Dn>
+__device__ __forceinline__ void mma_mn_mn(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo) {
+    constexpr uint32_t id = idesc_bf16(128, Dn, true, true);
+    mma_ss_warp<0>(tmem_d, a_lo, b_lo, kDescHi, id);
+#pragma unroll
+    for (int k = 1; k < 128 / 16; ++k) mma_ss_warp<1>(tmem_d, a_lo + ((k * 2048) >> 4), b_lo + ((k * 2048) >> 4), kDescHi, id);
+}
+
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+template <int D, bool CAP, int BIAS>
+__global__ void __launch_bounds__(threads_for(D == 128 ? 4 : 2), 1)
+fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
+                    const __grid_constant__ CUtensorMap tmdQacc, const __grid_constant__ CUtensorMap tmdK,
+                    const __grid_constant__ CUtensorMap tmdV, const ScoreBwdParams p) {
+    using L = ScoreBwdLayout<D>;
+    constexpr int NWG = D == 128 ? 4 : 2;  // elementwise warpgroups: a share of the query and d columns each
+    static_assert(sizeof(ScoreBwdShared) <= L::kBytes - L::kBars, "barrier block overflows its slot");
+    constexpr int kProducerWarp = 4 * NWG, kMmaWarp = 4 * NWG + 1, kReducerWarp = 4 * NWG + 2;
+    constexpr int kQC = 128 / NWG;      // query columns of P^T / dX^T per warpgroup
+    constexpr int kDC = D / NWG;        // d-columns of dQ, dK, dV per warpgroup
+    constexpr int kEW = 128 * NWG;
+    constexpr int kChunks = kQC / 32;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_addr(smem);
+    ScoreBwdShared& sh = *reinterpret_cast<ScoreBwdShared*>(smem + L::kBars);
+    float* lse2_s = reinterpret_cast<float*>(smem + L::kVec);        // [2][128]
+    float* dvec_s = reinterpret_cast<float*>(smem + L::kVec + 1024);  // [2][128]
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int N = p.mask.N;
+    // launch order: groups of head_group key heads, whose Q, dO and accumulator stay in L2; in a
+    // group the key tiles in order (when causal the longest first), its heads interleaved
+    int ikv, bkv;
+    {
+        const long long i = blockIdx.x, per_group = static_cast<long long>(p.head_group) * p.n_kv;
+        const int BHkv = static_cast<int>(gridDim.x) / p.n_kv;
+        const int g = static_cast<int>(i / per_group), j = static_cast<int>(i - g * per_group);
+        const int heads = min(p.head_group, BHkv - g * p.head_group);
+        ikv = j / heads;
+        bkv = g * p.head_group + (j - ikv * heads);
+    }
+    const int b = bkv / p.H_kv, hkv = bkv - b * p.H_kv;
+    const int kvs = ikv * kBK;
+    if (sbase & 1023u) {  // the swizzled tiles need 1024-byte alignment
+        if (threadIdx.x == 0) atomicCAS(p.err, 0u, 1u | (0xAAu << 8));
+        return;
+    }
+
+    const uint32_t bar_kv = smem_addr(&sh.kv_full);
+    const uint32_t bar_qf = smem_addr(&sh.q_full[0]);
+    const uint32_t bar_df = smem_addr(&sh.do_full[0]);
+    const uint32_t bar_qe = smem_addr(&sh.q_empty[0]);
+    const uint32_t bar_de = smem_addr(&sh.do_empty[0]);
+    const uint32_t bar_s = smem_addr(&sh.s_full);
+    const uint32_t bar_dp = smem_addr(&sh.dp_full);
+    const uint32_t bar_p = smem_addr(&sh.p_ready);
+    const uint32_t bar_ds = smem_addr(&sh.ds_ready);
+    const uint32_t bar_dq = smem_addr(&sh.dq_full);
+    const uint32_t bar_dr = smem_addr(&sh.dq_drained);
+    const uint32_t bar_sgq = smem_addr(&sh.dq_staged_q);
+    const uint32_t bar_sgd = smem_addr(&sh.dq_staged_do);
+    const uint32_t bar_dk = smem_addr(&sh.dk_done);
+    if (threadIdx.x == 0) {
+        sh.abort_flag = 0;
+        mbar_init(bar_kv, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar_qf + 8 * s, 32);
+            mbar_init(bar_df + 8 * s, 1);
+            mbar_init(bar_qe + 8 * s, 2);  // MMA commit + the reducer warp
+            mbar_init(bar_de + 8 * s, 2);
+        }
+        mbar_init(bar_s, 1);
+        mbar_init(bar_dp, 1);
+        mbar_init(bar_p, kEW);
+        mbar_init(bar_ds, kEW);
+        mbar_init(bar_dq, 1);
+        mbar_init(bar_dr, kEW);
+        mbar_init(bar_sgq, kEW / 2);
+        mbar_init(bar_sgd, kEW / 2);
+        mbar_init(bar_dk, 1);
+        mbar_init_fence();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_addr(&sh.tmem_base), 512);
+        tmem_relinquish();
+    }
+    if (warp == kProducerWarp && lane == 0) {
+        tma_prefetch_map(&tmQ);
+        tma_prefetch_map(&tmK);
+        tma_prefetch_map(&tmV);
+        tma_prefetch_map(&tmdO);
+        tma_prefetch_map(&tmdQacc);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    griddep_launch_dependents();
+    griddep_wait();  // D, the accumulator and the spans come from the kernels before
+    const uint32_t tmem = sh.tmem_base;
+    const Watchdog wd{p.err, &sh.abort_flag, p.wait_limit_ns};
+    constexpr uint32_t FULL = 0xffffffffu;
+
+    // query tiles [first, first + per_head) see this key tile, in each of the G heads; the rows in
+    // [clear_lo, clear_hi) see all of its keys.  A tile of keys that nothing sees has a step all the same
+    // (its sums are 0).
+    const int prefix = prefix_of(p.mask, b);
+    const ScoreRange left = queries_of(p.mask, b, kvs, prefix);
+    const ScoreRange right = queries_of(p.mask, b, min(kvs + kBK, N) - 1, prefix);
+    const ScoreRange tiles = blocks_of(left.lo, right.hi, kBQ);
+    const int clear_lo = right.lo, clear_hi = kvs + kBK > N ? 0 : left.hi;
+    const int first = tiles.lo, per_head = tiles.hi - tiles.lo;
+    const int steps = per_head * p.G;
+    const int bh0 = b * p.H + hkv * p.G;  // the group's first query head
+
+    if (warp == kProducerWarp) {
+        // ------------------------------------------------------------ producer --
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar_kv, 2 * L::kTile);
+            for (int x = 0; x < L::kBoxes; ++x) {
+                tma_load_3d(sbase + L::kK + x * L::kBox, &tmK, bar_kv, x * 64, kvs, bkv);
+                tma_load_3d(sbase + L::kV + x * L::kBox, &tmV, bar_kv, x * 64, kvs, bkv);
+            }
+        }
+        int bh = bh0, qt = first;
+        for (int s = 0; s < steps; ++s) {
+            const int st = s & 1;
+            const int q_start = qt * kBQ;
+            const int64_t row0 = static_cast<int64_t>(bh) * N;
+            // LSE and D into registers first: their latency overlaps the wait for the stage (negated,
+            // for paired adds)
+            float lv[4], dv[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int q = q_start + lane * 4 + e;
+                lv[e] = q < N ? kLiftP - p.LSE[row0 + q] * kLog2e : -INFINITY;
+                dv[e] = q < N ? -p.Dvec[row0 + q] : 0.f;
+            }
+            const uint32_t stage = sbase + L::kStage0 + st * L::kStageBytes;
+            if (s >= 2 && !mbar_wait(bar_de + 8 * st, ((s >> 1) - 1) & 1, wd, kSiteProd)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar_df + 8 * st, L::kTile);
+                for (int x = 0; x < L::kBoxes; ++x)
+                    tma_load_3d(stage + L::kTile + x * L::kBox, &tmdO, bar_df + 8 * st, x * 64, q_start, bh);
+            }
+            if (s >= 2 && !mbar_wait(bar_qe + 8 * st, ((s >> 1) - 1) & 1, wd, kSiteProd)) break;
+            if (lane == 0) {
+                mbar_expect_tx(bar_qf + 8 * st, L::kTile);
+                for (int x = 0; x < L::kBoxes; ++x)
+                    tma_load_3d(stage + x * L::kBox, &tmQ, bar_qf + 8 * st, x * 64, q_start, bh);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                lse2_s[st * 128 + lane * 4 + e] = lv[e];
+                dvec_s[st * 128 + lane * 4 + e] = dv[e];
+            }
+            mbar_arrive(bar_qf + 8 * st);  // 32 arrivals; the phase also waits for the copy
+            if (++qt == first + per_head) {
+                qt = first;
+                ++bh;
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        // ----------------------------------------------------------------- MMA --
+        const uint32_t k_lo = sw128_desc_lo(sbase + L::kK, 16), k_mn = sw128_desc_lo(sbase + L::kK, kLboMN);
+        const uint32_t v_lo = sw128_desc_lo(sbase + L::kV, 16);
+        const uint32_t ds_mn = sw128_desc_lo(sbase + L::kDS, kLboMN), ds_lo = sw128_desc_lo(sbase + L::kDS, 16);
+        const uint32_t q_lo0 = sw128_desc_lo(sbase + L::kStage0, 16);
+        const uint32_t q_mn0 = sw128_desc_lo(sbase + L::kStage0, kLboMN);
+        const uint32_t do_lo0 = sw128_desc_lo(sbase + L::kStage0 + L::kTile, 16);
+        const uint32_t do_mn0 = sw128_desc_lo(sbase + L::kStage0 + L::kTile, kLboMN);
+        constexpr uint32_t kStageStep = L::kStageBytes >> 4;
+        bool ok = __all_sync(FULL, mbar_wait(bar_kv, 0, wd, kSiteMmaKV) && mbar_wait(bar_qf, 0, wd, kSiteMmaQ));
+        if (ok) {
+            tc_fence_after();
+            mma_rows_rows<D>(tmem + L::kTmS, k_lo, q_lo0);     // S^T
+            mma_commit_warp(bar_s);
+            ok = __all_sync(FULL, mbar_wait(bar_df, 0, wd, kSiteMmaQ));
+            if (ok) {
+                tc_fence_after();
+                mma_rows_rows<D>(tmem + L::kTmDP, v_lo, do_lo0);   // dP^T
+                mma_commit_warp(bar_dp);
+            }
+        }
+        for (int s = 0; ok && s < steps; ++s) {
+            const int st = s & 1;
+            const uint32_t so = st * kStageStep;
+            if (!(ok = __all_sync(FULL, mbar_wait(bar_p, s & 1, wd, kSiteMmaP)))) break;
+            tc_fence_after();
+            mma_tmem_a<D, kQC>(tmem + L::kTmDV, tmem + L::kTmS, do_mn0 + so, s > 0);   // dV
+            mma_commit_warp(bar_de + 8 * st);  // the last MMA that reads this dO
+            if (!(ok = __all_sync(FULL, mbar_wait(bar_ds, s & 1, wd, kSiteMmaDS)))) break;
+            tc_fence_after();
+            // d = 64: the dQ columns are reused every step
+            if (!L::kDQAliasDP && s > 0) {
+                if (!(ok = __all_sync(FULL, mbar_wait(bar_dr, (s - 1) & 1, wd, kSiteMmaDrain)))) break;
+                tc_fence_after();
+            }
+            // dQ first: its drain is on the elementwise warps' path; dK and the next S^T run beside it
+            mma_mn_mn<D>(tmem + L::kTmDQ, ds_mn, k_mn);                                // dQ
+            mma_commit_warp(bar_dq);
+            if constexpr (L::kDSInTmem)
+                mma_tmem_a<D, kQC>(tmem + L::kTmDK, tmem + L::kTmS + kQC / 2, q_mn0 + so, s > 0);  // dK
+            else
+                mma_rows_mn<D>(tmem + L::kTmDK, ds_lo, q_mn0 + so, s > 0);
+            mma_commit_warp(bar_dk);           // d = 64: also, the dX^T tile is free again
+            mma_commit_warp(bar_qe + 8 * st);
+            if (s + 1 < steps) {
+                const int st1 = (s + 1) & 1;
+                const uint32_t so1 = st1 * kStageStep;
+                if (!(ok = __all_sync(FULL, mbar_wait(bar_qf + 8 * st1, ((s + 1) >> 1) & 1, wd, kSiteMmaQ)))) break;
+                tc_fence_after();
+                // S^T over P^T and dX^T, which only the MMAs above read (they run in issue order)
+                mma_rows_rows<D>(tmem + L::kTmS, k_lo, q_lo0 + so1);
+                mma_commit_warp(bar_s);
+                // d = 128: dP^T over the dQ tile, once it has been read out
+                if (L::kDQAliasDP) {
+                    if (!(ok = __all_sync(FULL, mbar_wait(bar_dr, s & 1, wd, kSiteMmaDrain)))) break;
+                    tc_fence_after();
+                }
+                if (!(ok = __all_sync(FULL, mbar_wait(bar_df + 8 * st1, ((s + 1) >> 1) & 1, wd, kSiteMmaQ)))) break;
+                tc_fence_after();
+                mma_rows_rows<D>(tmem + L::kTmDP, v_lo, do_lo0 + so1);
+                mma_commit_warp(bar_dp);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kReducerWarp) {
+        // ------------------------------------------------------------- reducer --
+        // adds each step's staged fp32 dQ tiles into the accumulator and hands the stage back
+        if (lane == 0) {
+            bool ok = true;
+            int bh = bh0, qt = first;
+            for (int s = 0; s < steps; ++s) {
+                const int st = s & 1;
+                const uint32_t src = sbase + L::kStage0 + st * L::kStageBytes;
+                const int q_start = qt * kBQ;
+                // dQ columns [D/2, D) were staged over dO (first), [0, D/2) over Q (once dK is done)
+                if (ok) ok = mbar_wait(bar_sgd, s & 1, wd, kSiteReduce);
+                if (ok) {
+                    for (int x = D / 64; x < D / 32; ++x) tma_reduce_add_3d(&tmdQacc, src + x * L::kBox, x * 32, q_start, bh);
+                    bulk_commit();
+                }
+                if (ok) ok = mbar_wait(bar_sgq, s & 1, wd, kSiteReduce);
+                if (ok) {
+                    for (int x = 0; x < D / 64; ++x) tma_reduce_add_3d(&tmdQacc, src + x * L::kBox, x * 32, q_start, bh);
+                    bulk_commit();
+                    bulk_wait_read<1>();
+                }
+                mbar_arrive(bar_de + 8 * st);
+                if (ok) bulk_wait_read<0>();
+                mbar_arrive(bar_qe + 8 * st);
+                if (++qt == first + per_head) {
+                    qt = first;
+                    ++bh;
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------ elementwise warpgroups 0 .. NWG - 1 --
+        // A failed wait poisons the rest of the work (ok = false) but every thread still reaches every
+        // barrier.
+        const int hw = warp >> 2;
+        const int r = threadIdx.x & 127;  // key row (P^T, dX^T, dK, dV) / query row (dQ)
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_off + L::kTmS + kQC * hw;
+        const uint32_t tDP = tmem + lane_off + L::kTmDP + kQC * hw;
+        const uint32_t tDQ = tmem + lane_off + L::kTmDQ + kDC * hw;
+        uint8_t* ds_row = smem + L::kDS + (kQC * hw / 64) * (128 * 128) + r * 128;
+        const int ds_chunk0 = (kQC * hw % 64) / 8;
+        constexpr int kDrainChunks = kDC / 16;
+        const int kg = kvs + r;
+        // the queries that see this row's key (none past a ragged end)
+        const ScoreRange mine = kg < N ? queries_of(p.mask, b, kg, prefix) : ScoreRange{0, 0};
+        const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
+        [[maybe_unused]] const uint64_t k2 = f2_pack(p.x_scale, p.x_scale), cap2 = f2_pack(p.cap_log2, p.cap_log2);
+        // the table gradient's sums of far pairs, kept while steps stay on one side
+        [[maybe_unused]] uint64_t fsum = 0;
+        [[maybe_unused]] int fside = 0;
+        const bool grad = BIAS == kBiasTable && p.near_part != nullptr;
+        [[maybe_unused]] const auto flush = [&](int bh) {
+            const float2 f = f2_unpack(fsum);
+            const float fs = warp_sum(f.x + f.y);
+            if (lane == 0)
+                p.far_part[((static_cast<long long>(bh) * p.n_kv + ikv) * (4 * NWG) + warp) * kFarFloats + (fside > 0)] = fs;
+            fsum = 0;
+        };
+        bool ok = true;
+        int s = 0;
+        for (int g = 0; g < p.G; ++g) {
+            const int bh = bh0 + g;
+            [[maybe_unused]] float slope2 = 0.f;
+            [[maybe_unused]] const float* bias2 = nullptr;
+            if constexpr (BIAS == kBiasSlopes) slope2 = p.slopes[hkv * p.G + g] * kLog2e;
+            if constexpr (BIAS == kBiasTable) bias2 = p.bias2 + static_cast<long long>(hkv * p.G + g) * (2 * p.far + 1);
+            if (grad) {
+                // what no step of this head writes is zero
+                const long long at = static_cast<long long>(bh) * p.n_kv + ikv;
+                if (lane < kFarFloats) p.far_part[(at * (4 * NWG) + warp) * kFarFloats + lane] = 0.f;
+                __syncwarp();
+                for (int x = 0; x < p.near_n; ++x) {
+                    const int qt = ikv + p.near_lo + x;
+                    if (qt >= 0 && qt < p.n_kv && (qt < first || qt >= first + per_head))
+                        for (int i = threadIdx.x; i < kNearFloats; i += kEW)
+                            p.near_part[(at * p.near_n + x) * kNearFloats + i] = 0.f;
+                }
+                fside = 0;
+            }
+            for (int t = 0; t < per_head; ++t, ++s) {
+                const int st = s & 1;
+                const int q_start = (first + t) * kBQ;
+                const ulonglong2* nl4 = reinterpret_cast<const ulonglong2*>(lse2_s + st * 128 + kQC * hw);
+                uint32_t keep[kChunks][16];  // P (1 - tanh^2), fp16 pairs
+                if (ok) ok = __all_sync(FULL, mbar_wait_sleep(bar_qf + 8 * st, (s >> 1) & 1, wd, kSiteDsQ));
+                if (ok) ok = __all_sync(FULL, mbar_wait_sleep(bar_s, s & 1, wd, kSiteDsS));
+                [[maybe_unused]] const int side = far_side(q_start, kvs, kBQ, BIAS == kBiasTable ? p.far : 0);
+                if (ok) {
+                    tc_fence_after();
+                    const int qh = q_start + kQC * hw;
+                    const bool masked = q_start < clear_lo || q_start + kBQ > clear_hi;
+                    const int from = mine.lo - qh;
+                    const uint32_t seen = static_cast<uint32_t>(mine.hi - mine.lo);
+                    [[maybe_unused]] uint64_t far_bias = 0;
+                    if constexpr (BIAS == kBiasTable) {
+                        if (side != 0) {
+                            const float v = bias2[side > 0 ? 2 * p.far : 0];
+                            far_bias = f2_pack(v, v);
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        uint32_t sv[32], pk[16];
+                        tmem_ld32(tS + 32 * c, sv);
+                        tmem_ld_wait(sv);
+                        // a pair of queries: weights from y0 = score before the bias (log2 units)
+                        const auto weights = [&](int i, uint64_t y0, uint64_t turn) {
+                            const int q = 32 * c + 2 * i;
+                            const ulonglong2 nl = nl4[8 * c + (i >> 1)];
+                            uint64_t add = (i & 1) ? nl.y : nl.x;
+                            if constexpr (BIAS == kBiasSlopes) {
+                                const float d0 = static_cast<float>(qh - kg);
+                                const float2 a = f2_unpack(add);
+                                add = f2_pack(fmaf(-slope2, fabsf(d0 + q), a.x), fmaf(-slope2, fabsf(d0 + (q + 1)), a.y));
+                            }
+                            if constexpr (BIAS == kBiasTable) {
+                                if (side != 0) {
+                                    add = fadd2(add, far_bias);
+                                } else {
+                                    const int at = qh - kg + q + p.far, top = 2 * p.far;
+                                    add = fadd2(add, f2_pack(bias2[max(0, min(top, at))], bias2[max(0, min(top, at + 1))]));
+                                }
+                            }
+                            const float2 x = f2_unpack(CAP ? fadd2(y0, add) : ffma2(y0, c2, add));
+                            float p0 = ex2(x.x), p1 = ex2(x.y);
+                            if (masked) {
+                                if (static_cast<uint32_t>(q - from) >= seen) p0 = 0.f;
+                                if (static_cast<uint32_t>(q + 1 - from) >= seen) p1 = 0.f;
+                            }
+                            pk[i] = pack_bf16(p0, p1);
+                            if constexpr (CAP) {
+                                const float2 k = f2_unpack(fmul2(f2_pack(p0, p1), turn));
+                                keep[c][i] = pack_f16(k.x, k.y);
+                            } else {
+                                keep[c][i] = pack_f16(p0, p1);
+                            }
+                        };
+                        if constexpr (CAP) {
+                            float mx0 = 0.f, mx1 = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                mx0 = fmax3(mx0, fabsf(u2f(sv[i])), fabsf(u2f(sv[i + 1])));
+                                mx1 = fmax3(mx1, fabsf(u2f(sv[i + 2])), fabsf(u2f(sv[i + 3])));
+                            }
+                            const float mx = fmaxf(mx0, mx1) * p.x_scale;
+                            const auto all = [&](auto how) {
+                                constexpr int HOW = decltype(how)::value;
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const uint64_t th = tanh2<HOW>(fmul2(f2_pack(u2f(sv[2 * i]), u2f(sv[2 * i + 1])), k2));
+                                    weights(i, fmul2(th, cap2), ffma2(fmul2(th, f2_pack(-1.f, -1.f)), th, f2_pack(1.f, 1.f)));
+                                }
+                            };
+                            if (!__any_sync(FULL, !(mx <= kTanhNear))) all(std::integral_constant<int, kTanhPoly3>{});
+                            else if (!__any_sync(FULL, !(mx <= kTanhMid))) all(std::integral_constant<int, kTanhPoly5>{});
+                            else all(std::integral_constant<int, kTanhExp>{});
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) weights(i, f2_pack(u2f(sv[2 * i]), u2f(sv[2 * i + 1])), 0);
+                        }
+                        tmem_st16(tS + 16 * c, pk);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                }
+                mbar_arrive(bar_p);
+
+                const ulonglong2* nd4 = reinterpret_cast<const ulonglong2*>(dvec_s + st * 128 + kQC * hw);
+                if (ok)
+                    ok = __all_sync(FULL, mbar_wait_sleep(bar_dp, s & 1, wd, kSiteDsDP) &&
+                                              (s == 0 || mbar_wait_sleep(L::kDSInTmem ? bar_dq : bar_dk, (s - 1) & 1, wd,
+                                                                         kSiteDsDQ)));
+                if (ok) {
+                    tc_fence_after();
+                    if (grad && side != fside) {
+                        if (fside != 0) flush(bh);
+                        fside = side;
+                    }
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        uint32_t dp[32], ds[16];
+                        tmem_ld32(tDP + 32 * c, dp);
+                        [[maybe_unused]] uint32_t pw[16];  // CAP: P itself
+                        if constexpr (CAP && BIAS == kBiasTable) {
+                            tmem_ld16(tS + 16 * c, pw);
+                            tmem_ld_wait(pw);
+                        }
+                        tmem_ld_wait(dp);
+                        [[maybe_unused]] float ahead = 0.f, behind = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const ulonglong2 nd = nd4[8 * c + (i >> 1)];
+                            const uint64_t t2 = fadd2(f2_pack(u2f(dp[2 * i]), u2f(dp[2 * i + 1])), (i & 1) ? nd.y : nd.x);
+                            const float2 kk = unpack_f16(keep[c][i]);
+                            const uint64_t k2w = f2_pack(kk.x, kk.y);
+                            const uint64_t d2 = fmul2(k2w, t2);
+                            const float2 dx = f2_unpack(d2);
+                            ds[i] = pack_bf16(dx.x, dx.y);
+                            if constexpr (BIAS == kBiasTable) {
+                                if (grad) {
+                                    uint64_t dy = d2;
+                                    if constexpr (CAP) dy = fmul2(f2_pack(u2f(pw[i] << 16), u2f(pw[i] & 0xffff0000u)), t2);
+                                    if (side != 0) {
+                                        fsum = fadd2(fsum, dy);
+                                    } else {
+                                        // column q's value of key row l to lane (q - l) mod 32
+                                        const float2 y = f2_unpack(dy);
+                                        const float y0 = __shfl_sync(FULL, y.x, 2 * i - lane);
+                                        const float y1 = __shfl_sync(FULL, y.y, 2 * i + 1 - lane);
+                                        if (lane <= 2 * i) ahead += y0;
+                                        else behind += y0;
+                                        if (lane <= 2 * i + 1) ahead += y1;
+                                        else behind += y1;
+                                    }
+                                }
+                            }
+                        }
+                        if constexpr (BIAS == kBiasTable) {
+                            if (grad && side == 0) {
+                                // block (query block, key block) of 32: lane m holds distance m, and m - 32
+                                const long long at = (static_cast<long long>(bh) * p.n_kv + ikv) * p.near_n + (first + t - ikv - p.near_lo);
+                                float* dst = p.near_part + at * kNearFloats + ((kChunks * hw + c) * 4 + (warp & 3)) * 64;
+                                dst[lane] = ahead;
+                                dst[32 + lane] = behind;
+                            }
+                        }
+                        if constexpr (L::kDSInTmem) tmem_st16(tS + kQC / 2 + 16 * c, ds);
+#pragma unroll
+                        for (int q4 = 0; q4 < 4; ++q4) {
+                            const int chunk = ds_chunk0 + 4 * c + q4;
+                            *reinterpret_cast<uint4*>(ds_row + ((chunk ^ (r & 7)) << 4)) =
+                                make_uint4(ds[4 * q4], ds[4 * q4 + 1], ds[4 * q4 + 2], ds[4 * q4 + 3]);
+                        }
+                    }
+                    fence_async_shared();
+                    if constexpr (L::kDSInTmem) tmem_st_wait();
+                    tc_fence_before();
+                }
+                mbar_arrive(bar_ds);
+
+                // dQ drain: this warpgroup's columns -> fp32 tiles -> bulk reduce-add
+                if (ok) ok = __all_sync(FULL, mbar_wait_sleep(bar_dq, s & 1, wd, kSiteDrain));
+                uint8_t* stage = smem + L::kStage0 + st * L::kStageBytes;
+                uint32_t acc[kDrainChunks][16];
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int x = 0; x < kDrainChunks; ++x) tmem_ld16(tDQ + 16 * x, acc[x]);
+#pragma unroll
+                    for (int x = 0; x < kDrainChunks; ++x) tmem_ld_wait(acc[x]);
+                    tc_fence_before();
+                    mbar_arrive(bar_dr);
+                    // staged over dO (free: dV and dP^T come before dQ) and over Q (free once dK is done)
+                    if (hw < NWG / 2) ok = __all_sync(FULL, mbar_wait_sleep(bar_dk, s & 1, wd, kSiteDrain));
+                } else {
+                    mbar_arrive(bar_dr);
+                }
+                if (ok) {
+#pragma unroll
+                    for (int x = 0; x < kDrainChunks; ++x) {
+                        const int col = hw * kDC + 16 * x;
+                        uint8_t* box = stage + (col / 32) * L::kBox + r * 128;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            *reinterpret_cast<uint4*>(box + ((((col % 32) / 4 + j) ^ (r & 7)) << 4)) =
+                                make_uint4(acc[x][4 * j], acc[x][4 * j + 1], acc[x][4 * j + 2], acc[x][4 * j + 3]);
+                    }
+                    fence_async_shared();
+                }
+                mbar_arrive(hw >= NWG / 2 ? bar_sgd : bar_sgq);
+            }
+            if (grad && fside != 0) flush(bh);
+        }
+        // dK = tau * dK_acc and dV, staged over the K and V tiles once the last dK is done (its commit
+        // covers every MMA of this CTA)
+        if (ok) ok = __all_sync(FULL, mbar_wait_sleep(bar_dk, (steps - 1) & 1, wd, kSiteDrain));
+        if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                uint8_t* dst = smem + (which ? L::kK : L::kV);
+                const float scale = (which ? p.tau : 1.f) * kUnliftP;
+                const uint32_t src = tmem + lane_off + (which ? L::kTmDK : L::kTmDV);
+#pragma unroll
+                for (int cc = 0; cc < kDC; cc += 16) {
+                    const int c0 = hw * kDC + cc;
+                    uint32_t o[16];
+                    tmem_ld16(src + c0, o);
+                    tmem_ld_wait(o);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int chunk = (c0 % 64) / 8 + q;
+                        uint4 v;
+                        v.x = pack_bf16(u2f(o[8 * q + 0]) * scale, u2f(o[8 * q + 1]) * scale);
+                        v.y = pack_bf16(u2f(o[8 * q + 2]) * scale, u2f(o[8 * q + 3]) * scale);
+                        v.z = pack_bf16(u2f(o[8 * q + 4]) * scale, u2f(o[8 * q + 5]) * scale);
+                        v.w = pack_bf16(u2f(o[8 * q + 6]) * scale, u2f(o[8 * q + 7]) * scale);
+                        *reinterpret_cast<uint4*>(dst + (c0 / 64) * L::kBox + r * 128 + ((chunk ^ (r & 7)) << 4)) = v;
+                    }
+                }
+            }
+            fence_async_shared();
+        }
+        // (all warps reach this barrier, also after a failed wait, and agree)
+        if (!named_bar_or(4, kEW, !ok) && threadIdx.x == 0) {
+            for (int x = 0; x < L::kBoxes; ++x) {
+                tma_store_3d(&tmdV, sbase + L::kV + x * L::kBox, x * 64, kvs, bkv);
+                tma_store_3d(&tmdK, sbase + L::kK + x * L::kBox, x * 64, kvs, bkv);
+            }
+            bulk_commit();
+            bulk_wait_read<0>();
+        }
+    }
+
+    // -------------------------------------------------------------- teardown --
+    if (sh.abort_flag) drain_after_abort();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// The table's biases by distance, [H][2 far + 1] in log2 units.
+__global__ void __launch_bounds__(256) fa_score_expand_kernel(const void* table, int f32, const int* buckets, int num_buckets, int H,
+                                                              int far, float* bias2) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int n = 2 * far + 1, i = static_cast<int>(blockIdx.x) * 256 + threadIdx.x;
+    if (i < n * H) bias2[i] = kLog2e * table_bias(table, f32, buckets, num_buckets, H, i / n, i % n);
+}
+
+// dQ = bf16(scale * acc), 8 elements per thread, grid-stride.
+__global__ void __launch_bounds__(256) fa_score_post_kernel(const float* acc, __nv_bfloat16* dQ, float scale, int64_t n8) {
+    griddep_launch_dependents();
+    griddep_wait();
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n8; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const float4 a = reinterpret_cast<const float4*>(acc)[2 * i];
+        const float4 b = reinterpret_cast<const float4*>(acc)[2 * i + 1];
+        uint4 o;
+        o.x = pack_bf16(a.x * scale, a.y * scale);
+        o.y = pack_bf16(a.z * scale, a.w * scale);
+        o.z = pack_bf16(b.x * scale, b.y * scale);
+        o.w = pack_bf16(b.z * scale, b.w * scale);
+        reinterpret_cast<uint4*>(dQ)[i] = o;
+    }
+}
+
+struct TableGradParams {
+    const float* near_part;
+    const float* far_part;
+    float* red;       // [near_n][H][num_buckets] sums per bucket; then [H][2] of the far parts
+    const int* buckets;
+    void* out;        // [num_buckets][H]
+    int B, H, n_kv, near_lo, near_n, far_warps, far, num_buckets, out_f32;
+};
+
+// Block (x, head): x < near_n adds the diagonals of all tile pairs at offset near_lo + x, over the
+// batch and the key tiles in order, and then, bucket by bucket, the diagonals of each; x = near_n
+// adds the far parts.
+__global__ void __launch_bounds__(1024) fa_score_buckets_kernel(const TableGradParams p) {
+    __shared__ float val[kNearFloats];
+    __shared__ int of[kNearFloats];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int x = static_cast<int>(blockIdx.x), h = static_cast<int>(blockIdx.y);
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    if (x == p.near_n) {
+        const long long parts = static_cast<long long>(p.n_kv) * p.far_warps;
+        float sum = 0.f;
+        for (int b = 0; b < p.B; ++b) {
+            const float* src = p.far_part + (static_cast<long long>(b) * p.H + h) * parts * kFarFloats;
+            for (long long i = t >> 1; i < parts; i += 512) sum += src[i * kFarFloats + (t & 1)];
+        }
+        val[t] = sum;
+        __syncthreads();
+        if (warp < 2) {
+            float s = 0.f;
+            for (int i = lane; i < 512; i += 32) s += val[2 * i + warp];
+            s = warp_sum(s);
+            if (lane == 0) p.red[static_cast<long long>(p.near_n) * p.H * p.num_buckets + h * 2 + warp] = s;
+        }
+        return;
+    }
+    const int off = p.near_lo + x;  // query tile - key tile
+    const int k0 = max(0, -off), k1 = min(p.n_kv, p.n_kv - off);
+    float sum = 0.f;
+    for (int b = 0; b < p.B; ++b) {
+        const long long at = (static_cast<long long>(b) * p.H + h) * p.n_kv;
+#pragma unroll 8
+        for (int k = k0; k < k1; ++k) sum += p.near_part[((at + k) * p.near_n + x) * kNearFloats + t];
+    }
+    const int blk = t >> 6, m = t & 63;
+    const int dist = off * 128 + 32 * (blk / 4 - blk % 4) + (m < 32 ? m : m - 64);
+    val[t] = sum;
+    of[t] = p.buckets[max(0, min(2 * p.far, dist + p.far))];
+    __syncthreads();
+    float* dst = p.red + (static_cast<long long>(x) * p.H + h) * p.num_buckets;
+    for (int e = warp; e < p.num_buckets; e += 32) {
+        float s = 0.f;
+        for (int i = lane; i < kNearFloats; i += 32)
+            if (of[i] == e) s += val[i];
+        s = warp_sum(s);
+        if (lane == 0) dst[e] = s;
+    }
+}
+
+// Block h: the gradient of head h's biases.
+__global__ void __launch_bounds__(256) fa_score_table_kernel(const TableGradParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int h = static_cast<int>(blockIdx.x), nb = p.num_buckets;
+    const long long step = static_cast<long long>(p.H) * nb;
+    const float* red = p.red + static_cast<long long>(h) * nb;
+    const float* far = p.red + p.near_n * step + h * 2;  // far keys behind the query's tiles, and before
+    const int low = p.buckets[0], high = p.buckets[2 * p.far];
+    for (int e = threadIdx.x; e < nb; e += 256) {
+        float s = 0.f;
+        for (int x = 0; x < p.near_n; ++x) s += red[x * step + e];
+        if (e == low) s += far[0];
+        if (e == high) s += far[1];
+        s *= kUnliftP;
+        if (p.out_f32) static_cast<float*>(p.out)[static_cast<long long>(e) * p.H + h] = s;
+        else static_cast<__nv_bfloat16*>(p.out)[static_cast<long long>(e) * p.H + h] = __float2bfloat16_rn(s);
+    }
+}
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+// The workspace's parts, each 256-aligned.
+struct BwdPlan {
+    int near_lo = 0, near_n = 0, warps = 0;
+    size_t dvec = 0, acc = 0, spans = 0, bias2 = 0, near = 0, far = 0, red = 0, bytes = 0;
+};
+BwdPlan plan_of(const ScoreArgs& a) {
+    BwdPlan pl;
+    const size_t rows = static_cast<size_t>(a.B) * a.H * a.N;
+    const int n_kv = (a.N + kBK - 1) / kBK;
+    pl.acc = up(rows * sizeof(float));
+    pl.spans = pl.acc + up(rows * a.d * sizeof(float));
+    pl.bias2 = pl.spans + up(score_fwd_workspace(a.B, a.N, a.mod.docs != nullptr));
+    pl.near = pl.far = pl.red = pl.bytes = pl.bias2;
+    if (!a.mod.table) return pl;
+    // (offsets that tiles have; behind the query only where a prefix, or no mask, shows such keys)
+    const int n = std::min(near_tiles(a.mod.far, kBQ), n_kv - 1);
+    pl.near_lo = a.causal && !a.mod.prefix ? 0 : -n;
+    pl.near_n = n - pl.near_lo + 1;
+    pl.warps = a.d == 128 ? 16 : 8;
+    const size_t tiles = static_cast<size_t>(a.B) * a.H * n_kv;
+    pl.near = pl.bias2 + up(static_cast<size_t>(a.H) * (2 * a.mod.far + 1) * sizeof(float));
+    pl.far = pl.near + tiles * pl.near_n * kNearFloats * sizeof(float);
+    pl.red = pl.far + up(tiles * pl.warps * kFarFloats * sizeof(float));
+    pl.bytes = pl.red + up((static_cast<size_t>(pl.near_n) * a.H * a.mod.num_buckets + a.H * 2) * sizeof(float));
+    return pl;
+}
+
+// Key heads per launch-order group: what the resident CTAs read (K, V, and of each query head of the
+// group Q, dO and the accumulator) within L2, as the backward without biases was measured.
+int head_group(const ScoreArgs& a) {
+    const double budget = (a.causal ? 128.0 : 48.0) * 1024 * 1024;
+    const double per_head = static_cast<double>(a.N) * a.d * (4.0 + 8.0 * a.H / a.H_kv);
+    int g = 1;
+    while (g < 16 && 2.0 * g * per_head <= budget) g *= 2;
+    return std::max(1, std::min(a.B * a.H_kv, g));
+}
+
+template <int D, bool CAP, int BIAS>
+cudaError_t launch_main(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t stream) {
+    using L = ScoreBwdLayout<D>;
+    CUtensorMap tq, tk, tv, tdo, tacc, tdk, tdv;
+    const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int BH = a.B * a.H, BHkv = a.B * a.H_kv;
+    float* acc = reinterpret_cast<float*>(a.workspace + pl.acc);
+    if (!make_tile_map(&tq, a.Q, BF, 2, D, a.N, BH, 64, kBQ) || !make_tile_map(&tk, a.K, BF, 2, D, a.N, BHkv, 64, kBK) ||
+        !make_tile_map(&tv, a.V, BF, 2, D, a.N, BHkv, 64, kBK) || !make_tile_map(&tdo, a.dO, BF, 2, D, a.N, BH, 64, kBQ) ||
+        !make_tile_map(&tacc, acc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, D, a.N, BH, 32, kBQ) ||
+        !make_tile_map(&tdk, a.dK, BF, 2, D, a.N, BHkv, 64, kBK) || !make_tile_map(&tdv, a.dV, BF, 2, D, a.N, BHkv, 64, kBK))
+        return cudaErrorInvalidValue;
+    constexpr auto kern = &fa_score_bwd_kernel<D, CAP, BIAS>;
+    cudaError_t e = set_max_dyn_smem_once<kern>(L::kBytes);
+    if (e != cudaSuccess) return e;
+    ScoreBwdParams p;
+    p.LSE = a.LSE;
+    p.Dvec = reinterpret_cast<const float*>(a.workspace + pl.dvec);
+    p.H = a.H;
+    p.H_kv = a.H_kv;
+    p.G = a.H / a.H_kv;
+    p.n_kv = (a.N + kBK - 1) / kBK;
+    p.head_group = head_group(a);
+    p.mask.spans = a.mod.docs ? reinterpret_cast<const int2*>(a.workspace + pl.spans) : nullptr;
+    p.mask.prefix = a.mod.prefix;
+    p.mask.N = a.N;
+    p.mask.window = a.mod.window;
+    p.mask.causal = a.causal;
+    p.scale_log2 = a.tau * kLog2e;
+    p.tau = a.tau;
+    p.x_scale = CAP ? a.tau / a.mod.softcap : 0.f;
+    p.cap_log2 = a.mod.softcap * kLog2e;
+    p.slopes = a.mod.slopes;
+    p.bias2 = reinterpret_cast<const float*>(a.workspace + pl.bias2);
+    p.far = a.mod.far;
+    p.near_part = a.dTable ? reinterpret_cast<float*>(a.workspace + pl.near) : nullptr;
+    p.far_part = reinterpret_cast<float*>(a.workspace + pl.far);
+    p.near_lo = pl.near_lo;
+    p.near_n = pl.near_n;
+    p.err = a.err;
+    p.wait_limit_ns = a.wait_limit_ns;
+    if (a.ev_start) cudaEventRecord(a.ev_start, stream);
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(BHkv) * static_cast<unsigned>(p.n_kv)),
+                         dim3(threads_for(D == 128 ? 4 : 2)), L::kBytes, stream, tq, tk, tv, tdo, tacc, tdk, tdv, p);
+    if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
+    return e;
+}
+
+template <int D>
+cudaError_t launch_d(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t stream) {
+    const int64_t rows = static_cast<int64_t>(a.B) * a.H * a.N;
+    float* bias2 = reinterpret_cast<float*>(a.workspace + pl.bias2);
+    float* acc = reinterpret_cast<float*>(a.workspace + pl.acc);
+    cudaError_t e = cudaSuccess;
+    if (a.mod.table) {
+        const int n = a.H * (2 * a.mod.far + 1);
+        e = launch_dependent(fa_score_expand_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream, a.mod.table,
+                             static_cast<int>(a.mod.table_f32), a.mod.buckets, a.mod.num_buckets, a.H, a.mod.far, bias2);
+        if (e != cudaSuccess) return e;
+    }
+    e = launch_score_rows(a, reinterpret_cast<float*>(a.workspace + pl.dvec), acc, a.mod.docs ? a.workspace + pl.spans : nullptr,
+                          bias2, stream);
+    if (e != cudaSuccess) return e;
+    const bool cap = a.mod.softcap > 0.f;
+    if (a.mod.slopes) e = cap ? launch_main<D, true, kBiasSlopes>(a, pl, stream) : launch_main<D, false, kBiasSlopes>(a, pl, stream);
+    else if (a.mod.table) e = cap ? launch_main<D, true, kBiasTable>(a, pl, stream) : launch_main<D, false, kBiasTable>(a, pl, stream);
+    else e = cap ? launch_main<D, true, kBiasNone>(a, pl, stream) : launch_main<D, false, kBiasNone>(a, pl, stream);
+    if (e != cudaSuccess) return e;
+    const int64_t n8 = rows * D / 8;
+    return launch_dependent(fa_score_post_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((n8 + 255) / 256, 152 * 64))),
+                            dim3(256), 0, stream, static_cast<const float*>(acc), static_cast<__nv_bfloat16*>(a.dQ),
+                            a.tau * kUnliftP, n8);
+}
+
+}  // namespace
+
+size_t score_bwd_workspace(const ScoreArgs& a) { return plan_of(a).bytes; }
+
+cudaError_t launch_score_bwd(const ScoreArgs& a, cudaStream_t stream) {
+    const BwdPlan pl = plan_of(a);
+    cudaError_t e = cudaSuccess;
+    if (a.mod.docs) e = launch_score_spans(a.mod.docs, a.workspace + pl.spans, a.B, a.N, stream);
+    if (e == cudaSuccess) e = a.d == 64 ? launch_d<64>(a, pl, stream) : launch_d<128>(a, pl, stream);
+    if (e != cudaSuccess || !a.dTable) return e;
+    TableGradParams t;
+    t.near_part = reinterpret_cast<const float*>(a.workspace + pl.near);
+    t.far_part = reinterpret_cast<const float*>(a.workspace + pl.far);
+    t.red = reinterpret_cast<float*>(a.workspace + pl.red);
+    t.buckets = a.mod.buckets;
+    t.out = a.dTable;
+    t.B = a.B;
+    t.H = a.H;
+    t.n_kv = (a.N + kBK - 1) / kBK;
+    t.near_lo = pl.near_lo;
+    t.near_n = pl.near_n;
+    t.far_warps = pl.warps;
+    t.far = a.mod.far;
+    t.num_buckets = a.mod.num_buckets;
+    t.out_f32 = a.mod.table_f32;
+    e = launch_dependent(fa_score_buckets_kernel, dim3(static_cast<unsigned>(t.near_n + 1), static_cast<unsigned>(t.H)), dim3(1024),
+                         0, stream, t);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(fa_score_table_kernel, dim3(static_cast<unsigned>(t.H)), dim3(256), 0, stream, t);
+}
+
+}  // namespace fa

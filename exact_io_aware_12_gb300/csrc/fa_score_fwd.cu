@@ -1,0 +1,536 @@
+// Forward of attention whose scores are capped by a tanh, biased by distance or masked by
+// documents, a prefix or a window, with grouped heads, for sm_103a.
+//
+// Mathematics: with x = tau q_i.k_j, the score of a visible pair is
+//   y = cap tanh(x / cap) (or x) + b(h, i - j),
+// b a slope times the distance or an entry of a learned table by bucket of distance;
+// O = sum_j softmax_j(y) v_j by the online recurrence, LSE = ln sum_j exp(y_ij).  Which keys
+// a query sees is one range of positions (fa_score.h), so a tile's mask is one unsigned
+// compare per score, and needed only where a tile is not wholly visible.
+//
+// Design: one CTA per 128-row query tile and query head, two CTAs to an SM (256 of its 512
+// tensor-memory columns each), so that one's loads, S and P V products and epilogue run
+// beside the other's softmax, which bounds these kernels: per score the mask, the cap (6
+// to 8 operations on the fp32 pipe; see tanh2), the bias, one exponential and two sums,
+// against the 2 x 128 x 128 x d products of a tile pair.
+//   - warp 4 streams Q, K_j and V_j by TMA through a ring of slots; warp 5 issues
+//     S = Q K_j^T and O += P V_j (tcgen05, P read from tensor memory); warps 0-3 own a row
+//     per thread.  At d = 64, P has columns of its own and the next S is issued as soon as the
+//     softmax has read the last; at d = 128 it is written over S.
+//   - The query heads that share a key head are neighbours in launch order, so that its
+//     keys are read from L2; longest tiles first when causal.
+//   - Slopes: the distance is counted up in fp32, exactly, two columns at a time.
+//   - Table: the head's biases by distance, 2 far + 1 of them, lie in shared memory; a
+//     tile all of whose pairs are at `far` or more has one bias.
+//   - A row that sees nothing keeps its reference at -inf: its weights and its sum stay 0,
+//     O = 0 and LSE = -inf.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "fa_score.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kBM = 128, kBN = 128;
+constexpr int kThreads = 192;
+constexpr int kProducerWarp = 4, kMmaWarp = 5;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8
+
+template <int D>
+struct ScoreFwdLayout {
+    static constexpr int kTile = kBM * D * 2;    // one bf16 tile
+    static constexpr int kBox = 128 * 128;       // one [128 rows x 64 columns] TMA box
+    static constexpr int kBoxes = D / 64;
+    static constexpr int kStages = D == 64 ? 4 : 2;
+    static constexpr int kRing = kTile;
+    static constexpr int kTable = kRing + kStages * kTile;
+    static constexpr int kDynSmem = kTable + 1024;  // + alignment slack; + the table's biases
+    static constexpr uint32_t kTmS = 0, kTmO = 128, kTmCols = 256;
+    static constexpr bool kPipe = D == 64;       // P in columns of its own
+    static constexpr uint32_t kTmP = kPipe ? 192 : 0;
+};
+
+struct ScoreFwdParams {
+    float* LSE;
+    int H, G, n_q;  // query heads, those to a key head, query tiles
+    ScoreMask mask;
+    float scale_log2;        // tau * log2(e)
+    float x_scale, cap_log2;  // cap: tau / cap, cap * log2(e)
+    const float* slopes;
+    const void* table;
+    const int* buckets;
+    int table_f32, num_buckets, far;
+    unsigned int* err;
+    unsigned long long wait_limit_ns;
+};
+
+struct ScoreFwdShared {
+    uint64_t q_full;
+    uint64_t kv_full[4];
+    uint64_t kv_empty[4];
+    uint64_t s_full, s_free, p_ready, o_done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+enum : uint32_t {
+    kSiteProd = 61, kSiteMmaQ = 62, kSiteMmaKV = 63, kSiteMmaS = 64, kSiteMmaP = 65,
+    kSiteSoftS = 66, kSiteSoftO = 67, kSiteEpi = 68
+};
+
+__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
+__device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
+
+constexpr uint32_t kDescHi = sw128_desc_hi(1024);
+
+// The 128 scores of a row, in registers, two at a time: f(column, pair) -> pair.
+template <typename F>
+__device__ __forceinline__ void each_pair(uint32_t (&s)[4][32], F&& f) {
+#pragma unroll
+    for (int c = 0; c < 128; c += 2) {
+        uint32_t &a = s[c >> 5][c & 31], &b = s[c >> 5][(c & 31) + 1];
+        const float2 y = f2_unpack(f(c, f2_pack(u2f(a), u2f(b))));
+        a = f2u(y.x);
+        b = f2u(y.y);
+    }
+}
+
+template <int D, bool CAP, int BIAS>
+__global__ void __launch_bounds__(kThreads, 2)
+fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
+                    const ScoreFwdParams p) {
+    using L = ScoreFwdLayout<D>;
+    constexpr bool PIPE = L::kPipe;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ ScoreFwdShared sh;
+    const uint32_t raw = smem_addr(smem_raw);
+    const uint32_t pad = ((raw + 1023u) & ~1023u) - raw;
+    uint8_t* smem = smem_raw + pad;
+    const uint32_t sbase = raw + pad;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int N = p.mask.N;
+    const int bh = static_cast<int>(blockIdx.x);
+    const int b = bh / p.H, h = bh - b * p.H;
+    const int bkv = b * (p.H / p.G) + h / p.G;
+    const int q_start = (p.n_q - 1 - static_cast<int>(blockIdx.y)) * kBM;
+
+    const uint32_t bar_q = smem_addr(&sh.q_full);
+    const uint32_t bar_kvf = smem_addr(&sh.kv_full[0]);
+    const uint32_t bar_kve = smem_addr(&sh.kv_empty[0]);
+    const uint32_t bar_s = smem_addr(&sh.s_full);
+    const uint32_t bar_sf = smem_addr(&sh.s_free);
+    const uint32_t bar_p = smem_addr(&sh.p_ready);
+    const uint32_t bar_o = smem_addr(&sh.o_done);
+    if (threadIdx.x == 0) {
+        sh.abort_flag = 0;
+        mbar_init(bar_q, 1);
+        for (int s = 0; s < L::kStages; ++s) {
+            mbar_init(bar_kvf + 8 * s, 1);
+            mbar_init(bar_kve + 8 * s, 1);
+        }
+        mbar_init(bar_s, 1);
+        mbar_init(bar_sf, 128);
+        mbar_init(bar_p, 128);
+        mbar_init(bar_o, 1);
+        mbar_init_fence();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_addr(&sh.tmem_base), L::kTmCols);
+        tmem_relinquish();
+    }
+    if (warp == kProducerWarp && lane == 0) {
+        tma_prefetch_map(&tmQ);
+        tma_prefetch_map(&tmK);
+        tma_prefetch_map(&tmV);
+        tma_prefetch_map(&tmO);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // launched as a dependent of the kernel before it: its start-up overlaps that kernel's end
+    griddep_launch_dependents();
+    griddep_wait();
+    const uint32_t tmem = sh.tmem_base;
+    const Watchdog wd{p.err, &sh.abort_flag, p.wait_limit_ns};
+
+    // key blocks [jlo, jlo + nb); those within [clear_lo, clear_hi) every row sees
+    const int prefix = prefix_of(p.mask, b);
+    const ScoreRange top = keys_of(p.mask, b, q_start, prefix);
+    const ScoreRange bottom = keys_of(p.mask, b, min(q_start + kBM, N) - 1, prefix);
+    const ScoreRange blocks = blocks_of(top.lo, bottom.hi, kBN);
+    const int clear_lo = bottom.lo, clear_hi = top.hi;
+    const int jlo = blocks.lo, nb = blocks.hi - blocks.lo;
+
+    if (warp == kProducerWarp) {
+        // ------------------------------------------------------------ producer --
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar_q, L::kTile);
+            for (int x = 0; x < L::kBoxes; ++x) tma_load_3d(sbase + x * L::kBox, &tmQ, bar_q, x * 64, q_start, bh);
+            for (int ld = 0; ld < 2 * nb; ++ld) {
+                const int slot = ld % L::kStages;
+                if (ld >= L::kStages && !mbar_wait(bar_kve + 8 * slot, ((ld / L::kStages) - 1) & 1, wd, kSiteProd)) break;
+                bool is_k = (ld & 1) == 0;
+                int blk = ld >> 1;
+                if constexpr (PIPE) {  // the MMA warp's order: K0 K1 V0 K2 V1 ... K(nb-1) V(nb-2) V(nb-1)
+                    is_k = ld == 0 || ((ld & 1) && ld < 2 * nb - 1);
+                    blk = is_k ? (ld + 1) / 2 : (ld == 2 * nb - 1 ? nb - 1 : ld / 2 - 1);
+                }
+                mbar_arrive_expect_tx(bar_kvf + 8 * slot, L::kTile);
+                for (int x = 0; x < L::kBoxes; ++x)
+                    tma_load_3d(sbase + L::kRing + slot * L::kTile + x * L::kBox, is_k ? &tmK : &tmV, bar_kvf + 8 * slot,
+                                x * 64, (jlo + blk) * kBN, bkv);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ----------------------------------------------------------------- MMA --
+        const uint32_t tS = tmem + L::kTmS, tO = tmem + L::kTmO, tP = tmem + L::kTmP;
+        const uint32_t qlo = sw128_desc_lo(sbase, 16);
+        const uint32_t klo0 = sw128_desc_lo(sbase + L::kRing, 16);          // K: K-major
+        const uint32_t vlo0 = sw128_desc_lo(sbase + L::kRing, 128 * 128);   // V: MN-major
+        constexpr uint32_t kSlot = L::kTile >> 4;
+        constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);
+        constexpr uint32_t id_pv = idesc_bf16(128, D, false, true);
+        const auto issue_s = [&](int slot) {
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const uint32_t off = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;
+                if (k == 0) mma_ss_warp<0>(tS, qlo + off, klo0 + slot * kSlot + off, kDescHi, id_s);
+                else mma_ss_warp<1>(tS, qlo + off, klo0 + slot * kSlot + off, kDescHi, id_s);
+            }
+            mma_commit_warp(bar_s);
+            mma_commit_warp(bar_kve + 8 * slot);
+        };
+        const auto issue_pv = [&](int slot, bool accumulate) {
+            if (accumulate) mma_ts_warp<1>(tO, tP, vlo0 + slot * kSlot, kDescHi, id_pv);
+            else mma_ts_warp<0>(tO, tP, vlo0 + slot * kSlot, kDescHi, id_pv);
+#pragma unroll
+            for (int k = 1; k < kBN / 16; ++k)
+                mma_ts_warp<1>(tO, tP + k * 8, vlo0 + slot * kSlot + ((k * 2048) >> 4), kDescHi, id_pv);
+            mma_commit_warp(bar_o);
+            mma_commit_warp(bar_kve + 8 * slot);
+        };
+        const auto kv_in = [&](int ld) { return mbar_wait(bar_kvf + 8 * (ld % L::kStages), (ld / L::kStages) & 1, wd, kSiteMmaKV); };
+        bool ok = __all_sync(0xffffffffu, mbar_wait(bar_q, 0, wd, kSiteMmaQ));
+        for (int j = 0; ok && j <= nb; ++j) {
+            if (PIPE && j < nb) {  // S of block j, once the softmax has read S of j - 1
+                const int ld = j == 0 ? 0 : 2 * j - 1;
+                ok = __all_sync(0xffffffffu, kv_in(ld) && (j == 0 || mbar_wait(bar_sf, (j - 1) & 1, wd, kSiteMmaS)));
+                if (!ok) break;
+                tc_fence_after();
+                issue_s(ld % L::kStages);
+            }
+            if (j > 0) {  // P V of block j - 1
+                const int ld = !PIPE ? 2 * j - 1 : min(2 * j, 2 * nb - 1);
+                ok = __all_sync(0xffffffffu, kv_in(ld) && mbar_wait(bar_p, (j - 1) & 1, wd, kSiteMmaP));
+                if (!ok) break;
+                tc_fence_after();
+                issue_pv(ld % L::kStages, j > 1);
+            }
+            if (!PIPE && j < nb) {  // S of block j, over P, which the P V just issued reads first: they run in order
+                ok = __all_sync(0xffffffffu, kv_in(2 * j));
+                if (!ok) break;
+                tc_fence_after();
+                issue_s((2 * j) % L::kStages);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------- softmax --
+        const int r = threadIdx.x & 127;
+        const int row = q_start + r;
+        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lane_off + L::kTmS, tO = tmem + lane_off + L::kTmO;
+        const uint32_t tP = tmem + lane_off + L::kTmP;
+        const float sl2 = p.scale_log2;
+        const uint64_t c2 = f2_pack(sl2, sl2);
+        const ScoreRange mine = keys_of(p.mask, b, min(row, N - 1), prefix);
+        [[maybe_unused]] float* bias_s = reinterpret_cast<float*>(smem + L::kTable);
+        [[maybe_unused]] float slope2 = 0.f;
+        if constexpr (BIAS == kBiasSlopes) slope2 = p.slopes[h] * kLog2e;
+        if constexpr (BIAS == kBiasTable) {
+            for (int i = r; i <= 2 * p.far; i += 128)
+                bias_s[i] = kLog2e * table_bias(p.table, p.table_f32, p.buckets, p.num_buckets, p.H, h, i);
+            named_bar_sync(1, 128);
+        }
+        constexpr bool SCALED = CAP || BIAS != kBiasNone;  // y in log2 units before the max is taken
+        float m_used = -INFINITY;
+        float l = 0.f, l_mma = 0.f;
+        bool ok = true;
+        for (int j = 0; j < nb; ++j) {
+            if (!__all_sync(0xffffffffu, mbar_wait(bar_s, j & 1, wd, kSiteSoftS))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t s[4][32];
+            tmem_ld32(tS + 0, s[0]);
+            tmem_ld32(tS + 32, s[1]);
+            tmem_ld32(tS + 64, s[2]);
+            tmem_ld32(tS + 96, s[3]);
+            tmem_ld_wait(s[0]);
+            tmem_ld_wait(s[1]);
+            tmem_ld_wait(s[2]);
+            tmem_ld_wait(s[3]);
+            if constexpr (PIPE) {
+                tc_fence_before();
+                mbar_arrive(bar_sf);  // S's columns may take the next block's scores now
+            }
+            const int kbase = (jlo + j) * kBN;
+            if constexpr (CAP) {
+                // y = cap log2(e) tanh(s tau / cap), by the largest |s| of the warp's rows
+                float mx0 = 0.f, mx1 = 0.f;
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    mx0 = fmax3(mx0, fabsf(u2f(s[0][c])), fabsf(u2f(s[0][c + 1])));
+                    mx1 = fmax3(mx1, fabsf(u2f(s[1][c])), fabsf(u2f(s[1][c + 1])));
+                    mx0 = fmax3(mx0, fabsf(u2f(s[2][c])), fabsf(u2f(s[2][c + 1])));
+                    mx1 = fmax3(mx1, fabsf(u2f(s[3][c])), fabsf(u2f(s[3][c + 1])));
+                }
+                const float mx = fmaxf(mx0, mx1) * p.x_scale;
+                const uint64_t k2 = f2_pack(p.x_scale, p.x_scale), cap2 = f2_pack(p.cap_log2, p.cap_log2);
+                if (!__any_sync(0xffffffffu, !(mx <= kTanhNear)))
+                    each_pair(s, [&](int, uint64_t v) { return fmul2(tanh2<kTanhPoly3>(fmul2(v, k2)), cap2); });
+                else if (!__any_sync(0xffffffffu, !(mx <= kTanhMid)))
+                    each_pair(s, [&](int, uint64_t v) { return fmul2(tanh2<kTanhPoly5>(fmul2(v, k2)), cap2); });
+                else
+                    each_pair(s, [&](int, uint64_t v) { return fmul2(tanh2<kTanhExp>(fmul2(v, k2)), cap2); });
+            }
+            if constexpr (BIAS == kBiasSlopes) {
+                const float d0 = static_cast<float>(kbase - row);  // j - i at column 0, exact below 2^24
+                const int side = far_side(q_start, kbase, kBM, 0);
+                if (side != 0) {
+                    // all keys before (or behind) all queries: y - slope |i - j| with the sign in the slope
+                    const uint64_t sl = f2_pack(side * slope2, side * slope2), two = f2_pack(2.f, 2.f);
+                    uint64_t dist[4];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) dist[g] = f2_pack(d0 + 32 * g, d0 + 32 * g + 1);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 2)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            uint64_t v = f2_pack(u2f(s[g][c]), u2f(s[g][c + 1]));
+                            if constexpr (!CAP) v = fmul2(v, c2);
+                            const float2 y = f2_unpack(ffma2(dist[g], sl, v));
+                            s[g][c] = f2u(y.x);
+                            s[g][c + 1] = f2u(y.y);
+                            dist[g] = fadd2(dist[g], two);
+                        }
+                } else {
+                    each_pair(s, [&](int c, uint64_t v) {
+                        float2 y = f2_unpack(CAP ? v : fmul2(v, c2));
+                        y.x = fmaf(-slope2, fabsf(d0 + c), y.x);
+                        y.y = fmaf(-slope2, fabsf(d0 + c + 1), y.y);
+                        return f2_pack(y.x, y.y);
+                    });
+                }
+            }
+            if constexpr (BIAS == kBiasTable) {
+                const int side = far_side(q_start, kbase, kBM, p.far);
+                if (side != 0) {
+                    const float bf = bias_s[side > 0 ? 2 * p.far : 0];
+                    const uint64_t b2 = f2_pack(bf, bf);
+                    each_pair(s, [&](int, uint64_t v) { return CAP ? fadd2(v, b2) : ffma2(v, c2, b2); });
+                } else {
+                    const int i0 = row - kbase + p.far, top_i = 2 * p.far;
+                    each_pair(s, [&](int c, uint64_t v) {
+                        const uint64_t b2 = f2_pack(bias_s[max(0, min(top_i, i0 - c))], bias_s[max(0, min(top_i, i0 - c - 1))]);
+                        return CAP ? fadd2(v, b2) : ffma2(v, c2, b2);
+                    });
+                }
+            }
+            if (kbase < clear_lo || kbase + kBN > clear_hi) {
+                const int from = mine.lo - kbase;
+                const uint32_t n = static_cast<uint32_t>(mine.hi - mine.lo);
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                    if (static_cast<uint32_t>(c - from) >= n) s[c >> 5][c & 31] = f2u(-INFINITY);
+            }
+            float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 32; c += 2) {
+                mx0 = fmax3(mx0, u2f(s[0][c]), u2f(s[0][c + 1]));
+                mx1 = fmax3(mx1, u2f(s[1][c]), u2f(s[1][c + 1]));
+                mx2 = fmax3(mx2, u2f(s[2][c]), u2f(s[2][c + 1]));
+                mx3 = fmax3(mx3, u2f(s[3][c]), u2f(s[3][c + 1]));
+            }
+            float m_cand = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+            if constexpr (!SCALED) m_cand *= sl2;
+            const bool grow = m_cand > m_used + kRescaleThreshold;
+            float alpha = 1.f;
+            if (grow) {
+                alpha = ex2(m_used - m_cand);  // 0 on the first block (m_used = -inf)
+                m_used = m_cand;
+            }
+            l *= alpha;
+            l_mma *= alpha;
+            const float neg_m = (m_used == -INFINITY) ? 0.f : -m_used;
+            // l_mma sums the bf16 weights that the P V product takes (it normalises O), l the
+            // fp32 ones (it gives LSE)
+            const uint64_t nm2 = f2_pack(neg_m, neg_m);
+            uint64_t ls2 = 0;
+            float lr0 = 0.f, lr1 = 0.f;
+            constexpr int kPC = D == 128 ? 16 : 32;  // packed columns per tensor-memory store
+#pragma unroll
+            for (int hh = 0; hh < 64 / kPC; ++hh) {
+                uint32_t pk[kPC];
+#pragma unroll
+                for (int i = 0; i < kPC; ++i) {
+                    const int c = hh * 2 * kPC + 2 * i;
+                    const uint64_t v = f2_pack(u2f(s[c >> 5][c & 31]), u2f(s[c >> 5][(c & 31) + 1]));
+                    const float2 x = f2_unpack(SCALED ? fadd2(v, nm2) : ffma2(v, c2, nm2));
+                    const float p0 = ex2(x.x), p1 = ex2(x.y);
+                    pk[i] = pack_bf16(p0, p1);
+                    ls2 = fadd2(ls2, f2_pack(p0, p1));
+                    add_bf16x2_f32(pk[i], lr0, lr1);
+                }
+                if (PIPE && hh == 0 && j > 0) {
+                    // P's columns are free once the previous P V has read them
+                    if (!__all_sync(0xffffffffu, mbar_wait(bar_o, (j - 1) & 1, wd, kSiteSoftO))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                }
+                if constexpr (kPC == 16) tmem_st16(tP + hh * 16, pk);
+                else tmem_st32(tP + hh * 32, pk);
+            }
+            if (!ok) break;
+            const float2 a2 = f2_unpack(ls2);
+            l += a2.x + a2.y;
+            l_mma += lr0 + lr1;
+            if (j > 0 && __any_sync(0xffffffffu, grow)) {
+                // rescale this warp's rows of O once the previous P V has landed
+                if (!__all_sync(0xffffffffu, mbar_wait(bar_o, (j - 1) & 1, wd, kSiteSoftO))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int c0 = 0; c0 < D; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(tO + c0, o);
+                    tmem_ld_wait(o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * alpha);
+                    tmem_st32(tO + c0, o);
+                }
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(bar_p);
+        }
+        // ----------------------------------------------------------- epilogue --
+        // O / l_mma -> bf16, staged over Q (every S has read it), one TMA store
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_o, (nb - 1) & 1, wd, kSiteEpi));
+        if (ok) {
+            tc_fence_after();
+            const float inv_l = l_mma > 0.f ? 1.f / l_mma : 0.f;
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 32) {
+                uint32_t o[32];
+                tmem_ld32(tO + c0, o);
+                tmem_ld_wait(o);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int chunk = (c0 % 64) / 8 + q;
+                    uint4 v;
+                    v.x = pack_bf16(u2f(o[8 * q + 0]) * inv_l, u2f(o[8 * q + 1]) * inv_l);
+                    v.y = pack_bf16(u2f(o[8 * q + 2]) * inv_l, u2f(o[8 * q + 3]) * inv_l);
+                    v.z = pack_bf16(u2f(o[8 * q + 4]) * inv_l, u2f(o[8 * q + 5]) * inv_l);
+                    v.w = pack_bf16(u2f(o[8 * q + 6]) * inv_l, u2f(o[8 * q + 7]) * inv_l);
+                    *reinterpret_cast<uint4*>(smem + (c0 / 64) * L::kBox + r * 128 + ((chunk ^ (r & 7)) << 4)) = v;
+                }
+            }
+            fence_async_shared();
+            if (row < N) p.LSE[static_cast<int64_t>(bh) * N + row] = (m_used + __log2f(l)) * kLn2;
+        }
+        // (all four warps reach this barrier, also after a failed wait, and agree)
+        if (!named_bar_or(1, 128, !ok) && r == 0) {
+            for (int x = 0; x < L::kBoxes; ++x) tma_store_3d(&tmO, sbase + x * L::kBox, x * 64, q_start, bh);
+            bulk_commit();
+            bulk_wait_read<0>();
+        }
+    }
+
+    // -------------------------------------------------------------- teardown --
+    if (sh.abort_flag) drain_after_abort();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, L::kTmCols);
+    }
+}
+
+template <int D, bool CAP, int BIAS>
+cudaError_t launch_t(const ScoreArgs& a, cudaStream_t stream) {
+    using L = ScoreFwdLayout<D>;
+    CUtensorMap tq, tk, tv, to;
+    const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int BH = a.B * a.H, BHkv = a.B * a.H_kv;
+    if (!make_tile_map(&tq, a.Q, BF, 2, D, a.N, BH, 64, kBM) || !make_tile_map(&tk, a.K, BF, 2, D, a.N, BHkv, 64, kBN) ||
+        !make_tile_map(&tv, a.V, BF, 2, D, a.N, BHkv, 64, kBN) || !make_tile_map(&to, a.O, BF, 2, D, a.N, BH, 64, kBM))
+        return cudaErrorInvalidValue;
+    constexpr auto kern = &fa_score_fwd_kernel<D, CAP, BIAS>;
+    // (the limit is set for the largest table, so that it is set once)
+    constexpr int kTableMax = BIAS == kBiasTable ? (2 * kScoreMaxFar + 1) * 4 : 0;
+    cudaError_t e = set_max_dyn_smem_once<kern>(L::kDynSmem + kTableMax);
+    if (e != cudaSuccess) return e;
+    const int bytes = L::kDynSmem + (BIAS == kBiasTable ? (2 * a.mod.far + 1) * 4 : 0);
+    ScoreFwdParams p;
+    p.LSE = a.LSE;
+    p.H = a.H;
+    p.G = a.H / a.H_kv;
+    p.n_q = (a.N + kBM - 1) / kBM;
+    p.mask.spans = a.mod.docs ? reinterpret_cast<const int2*>(a.workspace) : nullptr;
+    p.mask.prefix = a.mod.prefix;
+    p.mask.N = a.N;
+    p.mask.window = a.mod.window;
+    p.mask.causal = a.causal;
+    p.scale_log2 = a.tau * kLog2e;
+    p.x_scale = CAP ? a.tau / a.mod.softcap : 0.f;
+    p.cap_log2 = a.mod.softcap * kLog2e;
+    p.slopes = a.mod.slopes;
+    p.table = a.mod.table;
+    p.buckets = a.mod.buckets;
+    p.table_f32 = a.mod.table_f32;
+    p.num_buckets = a.mod.num_buckets;
+    p.far = a.mod.far;
+    p.err = a.err;
+    p.wait_limit_ns = a.wait_limit_ns;
+    if (a.ev_start) cudaEventRecord(a.ev_start, stream);
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(BH), static_cast<unsigned>(p.n_q)), dim3(kThreads),
+                         static_cast<size_t>(bytes), stream, tq, tk, tv, to, p);
+    if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
+    return e;
+}
+
+template <int D>
+cudaError_t launch_d(const ScoreArgs& a, cudaStream_t stream) {
+    const bool cap = a.mod.softcap > 0.f;
+    if (a.mod.slopes) return cap ? launch_t<D, true, kBiasSlopes>(a, stream) : launch_t<D, false, kBiasSlopes>(a, stream);
+    if (a.mod.table) return cap ? launch_t<D, true, kBiasTable>(a, stream) : launch_t<D, false, kBiasTable>(a, stream);
+    return cap ? launch_t<D, true, kBiasNone>(a, stream) : launch_t<D, false, kBiasNone>(a, stream);
+}
+
+}  // namespace
+
+size_t score_fwd_workspace(int B, int N, bool docs) { return docs ? static_cast<size_t>(B) * N * sizeof(int2) : 0; }
+
+cudaError_t launch_score_fwd(const ScoreArgs& a, cudaStream_t stream) {
+    if (a.mod.docs) {
+        const cudaError_t e = launch_score_spans(a.mod.docs, a.workspace, a.B, a.N, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return a.d == 64 ? launch_d<64>(a, stream) : launch_d<128>(a, stream);
+}
+
+}  // namespace fa

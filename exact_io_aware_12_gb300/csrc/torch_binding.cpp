@@ -1,5 +1,5 @@
-// The paged entry points and windows with sinks for torch tensors, as a Python extension
-// module.
+// The paged entry points, windows with sinks and attention with capped, biased or masked scores
+// for torch tensors, as a Python extension module.
 //
 // Their kernels can take a few microseconds, less than a ctypes call with its checks and
 // allocations takes in Python, so checks, output allocation and the call itself run here:
@@ -32,6 +32,11 @@ decltype(&fa_paged_workspace_size) g_workspace;
 decltype(&fa_fwd_sinks) g_fwd_sinks;
 decltype(&fa_bwd_sinks) g_bwd_sinks;
 decltype(&fa_bwd_workspace_size) g_bwd_workspace;
+decltype(&fa_fwd_score) g_fwd_score;
+decltype(&fa_bwd_score) g_bwd_score;
+decltype(&fa_fwd_score_workspace_size) g_fwd_score_workspace;
+decltype(&fa_bwd_score_workspace_size) g_bwd_score_workspace;
+decltype(&fa_fwd_paged_score) g_paged_score[2];
 PyObject* g_error = nullptr;  // FAError(code, where)
 PyObject* g_oom = nullptr;    // torch.OutOfMemoryError
 
@@ -218,10 +223,45 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// A fa_score from Python's arguments softcap, slopes, bias and buckets, for H heads on a device.
+fa_score check_score(PyObject* const* a, int64_t H, const at::Device& dev) {
+    fa_score s{};
+    if (a[0] != Py_None) {
+        const double cap = PyFloat_AsDouble(a[0]);
+        if (cap == -1.0 && PyErr_Occurred()) throw PyErr{};
+        s.softcap = static_cast<float>(cap);
+        require(s.softcap > 0.f, "softcap must be above 0");
+    }
+    const at::Tensor *slopes = tensor_or_none(a[1], "slopes"), *bias = tensor_or_none(a[2], "bias");
+    const at::Tensor* buckets = tensor_or_none(a[3], "buckets");
+    require((bias != nullptr) == (buckets != nullptr), "a bias needs buckets, and buckets a bias");
+    require(!bias || !slopes, "slopes or a bias, not both");
+    if (slopes) {
+        require(slopes->dim() == 1 && slopes->size(0) == H && slopes->scalar_type() == at::kFloat && slopes->device() == dev &&
+                    slopes->is_contiguous(),
+                "slopes must be contiguous fp32 [H] on the queries' device");
+        s.slopes = static_cast<const float*>(slopes->data_ptr());
+    }
+    if (bias) {
+        require(bias->dim() == 2 && bias->size(1) == H && bias->device() == dev && bias->is_contiguous() &&
+                    (bias->scalar_type() == at::kFloat || bias->scalar_type() == at::kBFloat16),
+                "bias must be contiguous fp32 or bf16 [num_buckets, H] on the queries' device");
+        require(buckets->dim() == 1 && buckets->size(0) % 2 == 1 && buckets->scalar_type() == at::kInt &&
+                    buckets->device() == dev && buckets->is_contiguous(),
+                "buckets must be contiguous int32 [2 * max_distance + 1] on the queries' device");
+        s.bias = bias->data_ptr();
+        s.buckets = static_cast<const int*>(buckets->data_ptr());
+        s.bias_f32 = bias->scalar_type() == at::kFloat;
+        s.num_buckets = to_int(bias->size(0));
+        s.max_distance = to_int(buckets->size(0) / 2);
+    }
+    return s;
+}
+
 // fwd_paged(q, k_cache, v_cache, page_table, lens, tau, window, sinks, k_scale, v_scale,
-//           out, lse, workspace) -> (O, LSE)
+//           out, lse, workspace[, softcap, slopes, bias, buckets]) -> (O, LSE)
 PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 13, [&]() -> PyObject* {
+    return guarded(n, n == 13 ? 13 : 17, [&]() -> PyObject* {
         const at::Tensor& q = tensor(a[0], "q");
         const Cache c = check_cache(tensor(a[1], "k_cache"), tensor(a[2], "v_cache"), tensor(a[3], "page_table"),
                                     tensor(a[4], "lens"), tensor_or_none(a[8], "k_scale"),
@@ -240,6 +280,8 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const float tau = scale_of(a[5], c.c.d);
         const int64_t H = q.size(1), Nq = q.size(2);
         check_rows(q, {c.c.B, H, Nq, c.c.d}, c, "q");
+        fa_score score{};
+        if (n > 13) score = check_score(a + 13, H, c.dev);
         const c10::cuda::OptionalCUDAGuard guard(c.dev);
         std::optional<at::Tensor> made_out, made_lse, made_ws;
         if (out) check_rows(*out, q.sizes(), c, "out");
@@ -257,11 +299,17 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
             bytes = g_workspace(&c.c, to_int(H), to_int(Nq), window, sinks);
             if (bytes) ws = &made_ws.emplace(at::empty({static_cast<int64_t>(bytes)}, q.options().dtype(at::kByte)));
         }
-        check_status(g_paged[c.fp8](&c.c, q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), out->data_ptr(),
-                                    out->stride(0), out->stride(1), out->stride(2), static_cast<float*>(lse->data_ptr()),
-                                    to_int(H), to_int(Nq), tau, window, sinks, ws ? ws->data_ptr() : nullptr, bytes,
-                                    c10::cuda::getCurrentCUDAStream(c.dev.index()).stream()),
-                     c.fp8 ? "fa_fwd_paged_fp8" : "fa_fwd_paged");
+        const auto call = [&](auto f, auto... more) {
+            return f(&c.c, q.data_ptr(), q.stride(0), q.stride(1), q.stride(2), out->data_ptr(), out->stride(0),
+                     out->stride(1), out->stride(2), static_cast<float*>(lse->data_ptr()), to_int(H), to_int(Nq), tau,
+                     window, sinks, more..., ws ? ws->data_ptr() : nullptr, bytes,
+                     c10::cuda::getCurrentCUDAStream(c.dev.index()).stream());
+        };
+        if (n > 13)
+            check_status(call(g_paged_score[c.fp8], static_cast<const fa_score*>(&score)),
+                         c.fp8 ? "fa_fwd_paged_score_fp8" : "fa_fwd_paged_score");
+        else
+            check_status(call(g_paged[c.fp8]), c.fp8 ? "fa_fwd_paged_fp8" : "fa_fwd_paged");
         return results({{&made_out, a[10]}, {&made_lse, a[11]}});
     });
 }
@@ -338,6 +386,119 @@ PyObject* bwd_sinks(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
+// Queries [B, H, N, d] and keys and values [B, H_kv, N, d] of attention with changed scores, and the
+// rest of its fa_score: documents, prefixes and window.
+struct Scored {
+    int B, H, H_kv, N, d;
+    fa_score f;
+};
+Scored check_scored(const at::Tensor& q, const at::Tensor& k, const at::Tensor& v, PyObject* const* a, int causal) {
+    check_attention({&q});
+    check_attention({&k, &v});
+    require(k.device() == q.device() && k.size(0) == q.size(0) && k.size(2) == q.size(2) && k.size(3) == q.size(3),
+            "keys and values must be [B, H_kv, N, d] on the queries' device");
+    Scored s{to_int(q.size(0)), to_int(q.size(1)), to_int(k.size(1)), to_int(q.size(2)), to_int(q.size(3)),
+             check_score(a, q.size(1), q.device())};
+    require(s.H_kv == 0 ? s.H == 0 : s.H % s.H_kv == 0, "the query heads must be a multiple of the key heads");
+    const at::Tensor *docs = tensor_or_none(a[4], "docs"), *prefix = tensor_or_none(a[5], "prefix");
+    if (docs) {
+        require(docs->dim() == 2 && docs->size(0) == s.B && docs->size(1) == s.N && docs->scalar_type() == at::kInt &&
+                    docs->device() == q.device() && docs->is_contiguous(),
+                "docs must be contiguous int32 [B, N] on the queries' device");
+        s.f.docs = static_cast<const int*>(docs->data_ptr());
+    }
+    if (prefix) {
+        require(causal, "a prefix needs causal=True");
+        require(prefix->dim() == 1 && prefix->size(0) == s.B && prefix->scalar_type() == at::kInt &&
+                    prefix->device() == q.device() && prefix->is_contiguous(),
+                "prefix must be contiguous int32 [B] on the queries' device");
+        s.f.prefix = static_cast<const int*>(prefix->data_ptr());
+    }
+    if (a[6] != Py_None) {
+        require(causal, "a window needs causal=True");
+        s.f.window = to_int(integer(a[6]));
+        require(s.f.window >= 1, "a window holds at least one key");
+    }
+    return s;
+}
+// A workspace as given, or one of `need` bytes.
+const at::Tensor* workspace_of(PyObject* o, size_t need, const at::Tensor& q, std::optional<at::Tensor>& made) {
+    const at::Tensor* ws = tensor_or_none(o, "workspace");
+    if (ws) require(ws->device() == q.device() && ws->is_contiguous(), "workspace must be contiguous, on the inputs' device");
+    else if (need) ws = &made.emplace(at::empty({static_cast<int64_t>(need)}, q.options().dtype(at::kByte)));
+    return ws;
+}
+int truth(PyObject* o) {
+    const int t = PyObject_IsTrue(o);
+    if (t < 0) throw PyErr{};
+    return t;
+}
+
+// fwd_score(q, k, v, causal, tau, softcap, slopes, bias, buckets, docs, prefix, window, out, lse,
+//           workspace) -> (O, LSE)
+PyObject* fwd_score(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 15, [&]() -> PyObject* {
+        const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+        const at::Tensor *out = tensor_or_none(a[12], "out"), *lse = tensor_or_none(a[13], "lse");
+        const int causal = truth(a[3]);
+        const Scored s = check_scored(q, k, v, a + 5, causal);
+        const float tau = scale_of(a[4], s.d);
+        const c10::cuda::OptionalCUDAGuard guard(q.device());
+        std::optional<at::Tensor> made_out, made_lse, made_ws;
+        if (out) check_attention({&q, out});
+        else out = &made_out.emplace(at::empty(q.sizes(), q.options()));
+        if (lse) check_lse(*lse, q);
+        else lse = &made_lse.emplace(at::empty(q.sizes().slice(0, 3), q.options().dtype(at::kFloat)));
+        const at::Tensor* ws = workspace_of(a[14], g_fwd_score_workspace(s.B, s.N, &s.f), q, made_ws);
+        check_status(g_fwd_score(q.data_ptr(), k.data_ptr(), v.data_ptr(), out->data_ptr(), static_cast<float*>(lse->data_ptr()),
+                                 s.B, s.H, s.H_kv, s.N, s.d, tau, causal, &s.f, ws ? ws->data_ptr() : nullptr,
+                                 ws ? ws->nbytes() : 0, c10::cuda::getCurrentCUDAStream(q.device().index()).stream()),
+                     "fa_fwd_score");
+        return results({{&made_out, a[12]}, {&made_lse, a[13]}});
+    });
+}
+
+// bwd_score(q, k, v, o, do, lse, causal, tau, softcap, slopes, bias, buckets, docs, prefix, window,
+//           dq, dk, dv, dbias, workspace) -> (dQ, dK, dV, dBias); dbias False: not computed, None back
+PyObject* bwd_score(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return guarded(n, 20, [&]() -> PyObject* {
+        const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &o = tensor(a[3], "o");
+        const at::Tensor &go = tensor(a[4], "do"), &lse = tensor(a[5], "lse");
+        const int causal = truth(a[6]);
+        const Scored s = check_scored(q, k, v, a + 8, causal);
+        check_attention({&q, &o, &go});
+        check_lse(lse, q);
+        const float tau = scale_of(a[7], s.d);
+        const c10::cuda::OptionalCUDAGuard guard(q.device());
+        std::optional<at::Tensor> made[4], made_ws;
+        void* grads[4] = {nullptr, nullptr, nullptr, nullptr};
+        for (int i = 0; i < 3; ++i) {
+            const at::Tensor* g = tensor_or_none(a[15 + i], "a gradient");
+            const at::Tensor& of = i == 0 ? q : k;
+            if (g) check_attention({&of, g});
+            else g = &made[i].emplace(at::empty(of.sizes(), of.options()));
+            grads[i] = g->data_ptr();
+        }
+        const bool wanted = s.f.bias && a[18] != Py_False;
+        if (wanted) {
+            const at::Tensor *g = tensor_or_none(a[18], "dbias"), &bias = tensor(a[10], "bias");
+            if (g)
+                require(g->sizes() == bias.sizes() && g->scalar_type() == bias.scalar_type() && g->device() == q.device() &&
+                            g->is_contiguous(),
+                        "dbias must be contiguous and like bias");
+            else g = &made[3].emplace(at::empty(bias.sizes(), bias.options()));
+            grads[3] = g->data_ptr();
+        }
+        const at::Tensor* ws = workspace_of(a[19], g_bwd_score_workspace(s.B, s.H, s.N, s.d, causal, &s.f), q, made_ws);
+        check_status(g_bwd_score(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), go.data_ptr(),
+                                 static_cast<const float*>(lse.data_ptr()), grads[0], grads[1], grads[2], grads[3], s.B, s.H,
+                                 s.H_kv, s.N, s.d, tau, causal, &s.f, ws ? ws->data_ptr() : nullptr, ws ? ws->nbytes() : 0,
+                                 c10::cuda::getCurrentCUDAStream(q.device().index()).stream()),
+                     "fa_bwd_score");
+        return results({{&made[0], a[15]}, {&made[1], a[16]}, {&made[2], a[17]}, {&made[3], wanted ? a[18] : Py_None}});
+    });
+}
+
 // load(path of the library, FAError, torch.OutOfMemoryError)
 PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return guarded(n, 3, [&]() -> PyObject* {
@@ -358,6 +519,12 @@ PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
         g_fwd_sinks = reinterpret_cast<decltype(&fa_fwd_sinks)>(find("fa_fwd_sinks"));
         g_bwd_sinks = reinterpret_cast<decltype(&fa_bwd_sinks)>(find("fa_bwd_sinks"));
         g_bwd_workspace = reinterpret_cast<decltype(&fa_bwd_workspace_size)>(find("fa_bwd_workspace_size"));
+        g_fwd_score = reinterpret_cast<decltype(&fa_fwd_score)>(find("fa_fwd_score"));
+        g_bwd_score = reinterpret_cast<decltype(&fa_bwd_score)>(find("fa_bwd_score"));
+        g_fwd_score_workspace = reinterpret_cast<decltype(&fa_fwd_score_workspace_size)>(find("fa_fwd_score_workspace_size"));
+        g_bwd_score_workspace = reinterpret_cast<decltype(&fa_bwd_score_workspace_size)>(find("fa_bwd_score_workspace_size"));
+        g_paged_score[0] = reinterpret_cast<decltype(&fa_fwd_paged_score)>(find("fa_fwd_paged_score"));
+        g_paged_score[1] = reinterpret_cast<decltype(&fa_fwd_paged_score)>(find("fa_fwd_paged_score_fp8"));
         Py_XDECREF(g_error);
         Py_XDECREF(g_oom);
         g_error = Py_NewRef(a[1]);
@@ -372,7 +539,8 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {method<kv_append>("kv_append"), method<fwd_paged>("fwd_paged"),
-                           method<fwd_sinks>("fwd_sinks"), method<bwd_sinks>("bwd_sinks"), method<load>("load"),
+                           method<fwd_sinks>("fwd_sinks"), method<bwd_sinks>("bwd_sinks"),
+                           method<fwd_score>("fwd_score"), method<bwd_score>("bwd_score"), method<load>("load"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "fa_binding", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

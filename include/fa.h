@@ -222,6 +222,72 @@ FA_API fa_status fa_bwd_blocks(const void* Q, const void* K, const void* V, cons
                                int mask_heads, void* stream);
 
 /*
+ * What changes the scores of fa_fwd_score and the entry points beside it, and which keys they
+ * hide.  Fields left 0 or NULL change nothing; device pointers.
+ *   softcap       x = tau q.k becomes softcap * tanh(x / softcap).  0, or 2^-20 to 2^60.
+ *   slopes        fp32 [H]: then - slopes[h] |i - j| is added, i the query's position and j the
+ *                 key's.
+ *   bias, buckets a learned bias by buckets of distance: bias[e][h] is added, e =
+ *                 buckets[max_distance + cut(i - j)], cut to +-max_distance; bias is
+ *                 [num_buckets][H], bf16 or (bias_f32 = 1) fp32, buckets int
+ *                 [2 max_distance + 1].  An entry outside [0, num_buckets) adds nothing.
+ *                 num_buckets and max_distance from 1 to 1024 (above: FA_ERR_UNSUPPORTED).  Not
+ *                 together with slopes.  The cap comes first, then the bias.
+ *   docs          int [B][N]: a document is a run of equal numbers, and tokens see their own
+ *                 document only; a token whose number is below 0 is in none (padding): it sees
+ *                 nothing, O = 0 and LSE = -inf, and nothing sees it.
+ *   prefix        int [B], with causal: the first prefix[b] positions (cut to [0, N]) are
+ *                 visible from before them, too: j <= i or j < prefix[b].
+ *   window        with causal: j > i - window only (>= 1; 0: none).
+ * What hides a key hides it, whatever else shows it.  Values are finite.
+ */
+typedef struct fa_score {
+    float softcap;
+    const float* slopes;
+    const void* bias;
+    const int* buckets;
+    int bias_f32, num_buckets, max_distance;
+    const int* docs;
+    const int* prefix;
+    int window;
+} fa_score;
+
+/*
+ * Attention with such scores, forward ("Atencao eficiente - FlashAttention, sparse e hibrida",
+ * section "Sparse e hibrida": which tokens a token attends to; the scores' cap and bias have no
+ * counterpart in the pages).  Q, O: bf16 [B][H][N][d] and K, V: bf16 [B][H_kv][N][d], H a
+ * multiple of H_kv: query head h reads key head h / (H / H_kv).  LSE: fp32 [B][H][N], of the
+ * changed scores; a row that sees nothing gives 0 and -inf.  Key blocks that no row of a
+ * tile sees are not loaded.  score may not be NULL (all fields 0: plain attention with grouped
+ * heads); it is host memory, only read during the call.  workspace:
+ * fa_fwd_score_workspace_size bytes (0 without docs); NULL: taken with cudaMallocAsync and
+ * given back.  Two calls that may run at the same time need two workspaces.  Other buffers and
+ * conventions as fa_fwd.
+ */
+FA_API size_t fa_fwd_score_workspace_size(int B, int N, const fa_score* score);
+FA_API fa_status fa_fwd_score(const void* Q, const void* K, const void* V, void* O, float* LSE,
+                              int B, int H, int H_kv, int N, int d, float tau, int causal,
+                              const fa_score* score, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/*
+ * Backward of fa_fwd_score (LSE as it wrote it for the same inputs; O is checked but not read: its
+ * product with dO is summed anew from the weights, unrounded): dQ [B][H][N][d], dK,
+ * dV [B][H_kv][N][d], summed over the query heads that share a key head; every element is
+ * written.  dBias: with a bias its gradient [num_buckets][H], of its type (every element
+ * written; buckets of no visible pair get 0), or NULL: not computed.  It is summed in fp32 in a
+ * fixed order and rounded once.  (dQ's order of summation is not fixed, as in fa_bwd.)
+ * workspace: fa_bwd_score_workspace_size bytes; NULL as in fa_fwd_score.
+ */
+FA_API size_t fa_bwd_score_workspace_size(int B, int H, int N, int d, int causal,
+                                          const fa_score* score);
+FA_API fa_status fa_bwd_score(const void* Q, const void* K, const void* V, const void* O,
+                              const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
+                              void* dBias, int B, int H, int H_kv, int N, int d, float tau,
+                              int causal, const fa_score* score, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
  * Decode forward: Nq new query rows per (batch, head) against a KV cache of Nk
  * keys ("Atencao eficiente - FlashAttention, sparse e hibrida", box
  * "FlashAttention nao acelera o decode token a token": each decode step brings
@@ -361,6 +427,23 @@ FA_API fa_status fa_fwd_paged_fp8(const fa_paged_cache* cache, const void* Q, lo
                                   long long o_sh, long long o_sn, float* LSE, int H, int Nq,
                                   float tau, int window, int sinks, void* workspace,
                                   size_t workspace_bytes, void* stream);
+
+/*
+ * fa_fwd_paged and fa_fwd_paged_fp8 with capped or biased scores: softcap, slopes, bias and
+ * buckets of score; its docs, prefix and window must be unset (sequences are apart in the
+ * cache, and window is an argument).  i - j counts positions of the sequence.  Same
+ * workspace.
+ */
+FA_API fa_status fa_fwd_paged_score(const fa_paged_cache* cache, const void* Q, long long q_sb,
+                                    long long q_sh, long long q_sn, void* O, long long o_sb,
+                                    long long o_sh, long long o_sn, float* LSE, int H, int Nq,
+                                    float tau, int window, int sinks, const fa_score* score,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+FA_API fa_status fa_fwd_paged_score_fp8(const fa_paged_cache* cache, const void* Q, long long q_sb,
+                                        long long q_sh, long long q_sn, void* O, long long o_sb,
+                                        long long o_sh, long long o_sn, float* LSE, int H, int Nq,
+                                        float tau, int window, int sinks, const fa_score* score,
+                                        void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * FP8 forward ("Atencao eficiente - FlashAttention, sparse e hibrida", the
