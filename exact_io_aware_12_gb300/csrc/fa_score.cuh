@@ -1,6 +1,8 @@
 // Device parts that the kernels of attention with capped, biased or masked scores share.
 #pragma once
 
+#include <cstring>
+
 #include "fa_internal.h"
 #include "fa_score.h"
 #include "ptx.cuh"
@@ -76,6 +78,50 @@ __device__ __forceinline__ uint64_t tanh2(uint64_t x) {
         }
         p = ffma2(u, p, c(1.f));
         return fmul2(x, p);
+    }
+}
+
+// Scores capped, in log2 units: what cap log2(e) tanh(s tau / cap) takes.
+struct CapScale {
+    float k, k_exp, cap2;
+    uint64_t k_2, cap_2, cap_m2, near[4], mid[6];  // pairs: a paired instruction takes them as they come
+    __host__ __device__ CapScale() {}
+    static uint64_t pair(float v) {
+        uint32_t x;
+        std::memcpy(&x, &v, 4);
+        return static_cast<uint64_t>(x) << 32 | x;
+    }
+    CapScale(float tau, float cap) {
+        const float log2e = 1.44269504088896341f, lin = tau * log2e;
+        k = tau / cap;
+        k_exp = 2.f * log2e * k;
+        cap2 = cap * log2e;
+        k_2 = pair(k);
+        cap_2 = pair(cap2);
+        cap_m2 = pair(-2.f * cap2);
+        // the fits of tanh2, times tau log2(e): y = s p((k s)^2) needs no products beside p's
+        const float n[4] = {1.f, -0.3333296477794647f, 0.1331268697977066f, -0.05022904649376869f};
+        const float m[6] = {1.f, -0.33332979679107666f, 0.13325688242912292f, -0.053358446806669235f, 0.019611310213804245f,
+                            -0.004736414644867182f};
+        for (int i = 0; i < 4; ++i) near[i] = pair(lin * n[i]);
+        for (int i = 0; i < 6; ++i) mid[i] = pair(lin * m[i]);
+    }
+};
+// Two capped scores plus `add`.
+template <int HOW>
+__device__ __forceinline__ uint64_t cap_score2(const CapScale& c, uint64_t s, uint64_t add) {
+    if constexpr (HOW == kTanhExp) {
+        const float2 v = f2_unpack(s);
+        const uint64_t r = f2_pack(rcp(1.f + ex2(c.k_exp * v.x)), rcp(1.f + ex2(c.k_exp * v.y)));
+        return ffma2(c.cap_m2, r, fadd2(c.cap_2, add));
+    } else {
+        constexpr int n = HOW == kTanhPoly3 ? 4 : 6;
+        const uint64_t* q = HOW == kTanhPoly3 ? c.near : c.mid;
+        const uint64_t t = fmul2(s, c.k_2), u = fmul2(t, t);
+        uint64_t p = q[n - 1];
+#pragma unroll
+        for (int i = n - 2; i >= 0; --i) p = ffma2(u, p, q[i]);
+        return ffma2(s, p, add);
     }
 }
 

@@ -35,6 +35,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "fa_score.cuh"
 
@@ -159,14 +160,18 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
+// Elementwise warpgroups: four at d = 128 (32 query columns each); at d = 64 two, but four where the
+// elementwise work is more than the products hide.
+constexpr int warpgroups(int D, bool cap, int bias) { return D == 128 || cap || bias == kBiasTable ? 4 : 2; }
+
 template <int D, bool CAP, int BIAS>
-__global__ void __launch_bounds__(threads_for(D == 128 ? 4 : 2), 1)
+__global__ void __launch_bounds__(threads_for(warpgroups(D, CAP, BIAS)), 1)
 fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
                     const __grid_constant__ CUtensorMap tmdQacc, const __grid_constant__ CUtensorMap tmdK,
                     const __grid_constant__ CUtensorMap tmdV, const ScoreBwdParams p) {
     using L = ScoreBwdLayout<D>;
-    constexpr int NWG = D == 128 ? 4 : 2;  // elementwise warpgroups: a share of the query and d columns each
+    constexpr int NWG = warpgroups(D, CAP, BIAS);  // elementwise warpgroups: a share of the query and d columns each
     static_assert(sizeof(ScoreBwdShared) <= L::kBytes - L::kBars, "barrier block overflows its slot");
     constexpr int kProducerWarp = 4 * NWG, kMmaWarp = 4 * NWG + 1, kReducerWarp = 4 * NWG + 2;
     constexpr int kQC = 128 / NWG;      // query columns of P^T / dX^T per warpgroup
@@ -470,7 +475,8 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                 if (ok) {
                     tc_fence_after();
                     const int qh = q_start + kQC * hw;
-                    const bool masked = q_start < clear_lo || q_start + kBQ > clear_hi;
+                    const bool general = q_start < clear_lo || q_start + kBQ > clear_hi || (BIAS != kBiasNone && side == 0);
+                    [[maybe_unused]] const uint64_t sl = f2_pack(-side * slope2, -side * slope2);  // (of i - j)
                     const int from = mine.lo - qh;
                     const uint32_t seen = static_cast<uint32_t>(mine.hi - mine.lo);
                     [[maybe_unused]] uint64_t far_bias = 0;
@@ -485,38 +491,60 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                         uint32_t sv[32], pk[16];
                         tmem_ld32(tS + 32 * c, sv);
                         tmem_ld_wait(sv);
-                        // a pair of queries: weights from y0 = score before the bias (log2 units)
-                        const auto weights = [&](int i, uint64_t y0, uint64_t turn) {
+                        // a pair of queries, s as it comes.  GENERAL: any mask, any bias; else all are visible and
+                        // the bias is the same or, of slopes, on one side.
+                        const float d0 = static_cast<float>(qh + 32 * c - kg);  // i - j at the chunk's first query
+                        [[maybe_unused]] uint64_t dist = f2_pack(d0, d0 + 1.f);
+                        const auto weights = [&](auto how, auto general_, int i) {
+                            constexpr bool GENERAL = decltype(general_)::value;
                             const int q = 32 * c + 2 * i;
                             const ulonglong2 nl = nl4[8 * c + (i >> 1)];
                             uint64_t add = (i & 1) ? nl.y : nl.x;
                             if constexpr (BIAS == kBiasSlopes) {
-                                const float d0 = static_cast<float>(qh - kg);
-                                const float2 a = f2_unpack(add);
-                                add = f2_pack(fmaf(-slope2, fabsf(d0 + q), a.x), fmaf(-slope2, fabsf(d0 + (q + 1)), a.y));
+                                if constexpr (GENERAL) {
+                                    const float2 a = f2_unpack(add), y = f2_unpack(dist);
+                                    add = f2_pack(fmaf(-slope2, fabsf(y.x), a.x), fmaf(-slope2, fabsf(y.y), a.y));
+                                } else {
+                                    add = ffma2(dist, sl, add);
+                                }
+                                dist = fadd2(dist, f2_pack(2.f, 2.f));
                             }
                             if constexpr (BIAS == kBiasTable) {
-                                if (side != 0) {
-                                    add = fadd2(add, far_bias);
-                                } else {
+                                if constexpr (GENERAL) {
                                     const int at = qh - kg + q + p.far, top = 2 * p.far;
                                     add = fadd2(add, f2_pack(bias2[max(0, min(top, at))], bias2[max(0, min(top, at + 1))]));
+                                } else {
+                                    add = fadd2(add, far_bias);
                                 }
                             }
-                            const float2 x = f2_unpack(CAP ? fadd2(y0, add) : ffma2(y0, c2, add));
+                            const uint64_t v = f2_pack(u2f(sv[2 * i]), u2f(sv[2 * i + 1]));
+                            [[maybe_unused]] uint64_t th = 0;
+                            float2 x;
+                            if constexpr (CAP) {
+                                th = tanh2<decltype(how)::value>(fmul2(v, k2));
+                                x = f2_unpack(ffma2(th, cap2, add));
+                            } else {
+                                x = f2_unpack(ffma2(v, c2, add));
+                            }
                             float p0 = ex2(x.x), p1 = ex2(x.y);
-                            if (masked) {
+                            if constexpr (GENERAL) {
                                 if (static_cast<uint32_t>(q - from) >= seen) p0 = 0.f;
                                 if (static_cast<uint32_t>(q + 1 - from) >= seen) p1 = 0.f;
                             }
                             pk[i] = pack_bf16(p0, p1);
-                            if constexpr (CAP) {
-                                const float2 k = f2_unpack(fmul2(f2_pack(p0, p1), turn));
+                            if constexpr (CAP) {  // (tanh^2 - 1: dX, dK and dQ come with their sign turned)
+                                const float2 k = f2_unpack(fmul2(f2_pack(p0, p1), ffma2(th, th, f2_pack(-1.f, -1.f))));
                                 keep[c][i] = pack_f16(k.x, k.y);
                             } else {
                                 keep[c][i] = pack_f16(p0, p1);
                             }
                         };
+                        const auto all = [&](auto how, auto general_) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) weights(how, general_, i);
+                        };
+                        using Poly5 = std::integral_constant<int, kTanhPoly5>;
+                        using Exp = std::integral_constant<int, kTanhExp>;
                         if constexpr (CAP) {
                             float mx0 = 0.f, mx1 = 0.f;
 #pragma unroll
@@ -524,21 +552,18 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                                 mx0 = fmax3(mx0, fabsf(u2f(sv[i])), fabsf(u2f(sv[i + 1])));
                                 mx1 = fmax3(mx1, fabsf(u2f(sv[i + 2])), fabsf(u2f(sv[i + 3])));
                             }
+                            // (the few tiles at the edges: two forms)
                             const float mx = fmaxf(mx0, mx1) * p.x_scale;
-                            const auto all = [&](auto how) {
-                                constexpr int HOW = decltype(how)::value;
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const uint64_t th = tanh2<HOW>(fmul2(f2_pack(u2f(sv[2 * i]), u2f(sv[2 * i + 1])), k2));
-                                    weights(i, fmul2(th, cap2), ffma2(fmul2(th, f2_pack(-1.f, -1.f)), th, f2_pack(1.f, 1.f)));
-                                }
-                            };
-                            if (!__any_sync(FULL, !(mx <= kTanhNear))) all(std::integral_constant<int, kTanhPoly3>{});
-                            else if (!__any_sync(FULL, !(mx <= kTanhMid))) all(std::integral_constant<int, kTanhPoly5>{});
-                            else all(std::integral_constant<int, kTanhExp>{});
+                            const bool near = !__any_sync(FULL, !(mx <= kTanhNear)), mid = !__any_sync(FULL, !(mx <= kTanhMid));
+                            if (general && mid) all(Poly5{}, std::true_type{});
+                            else if (general) all(Exp{}, std::true_type{});
+                            else if (near) all(std::integral_constant<int, kTanhPoly3>{}, std::false_type{});
+                            else if (mid) all(Poly5{}, std::false_type{});
+                            else all(Exp{}, std::false_type{});
+                        } else if (general) {
+                            all(Exp{}, std::true_type{});
                         } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) weights(i, f2_pack(u2f(sv[2 * i]), u2f(sv[2 * i + 1])), 0);
+                            all(Exp{}, std::false_type{});
                         }
                         tmem_st16(tS + 16 * c, pk);
                     }
@@ -569,20 +594,21 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                         }
                         tmem_ld_wait(dp);
                         [[maybe_unused]] float ahead = 0.f, behind = 0.f;
+                        // SUMS: of the table's gradient, for far (1) or near (2) pairs
+                        const auto products = [&](auto sums) {
+                            constexpr int SUMS = decltype(sums)::value;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const ulonglong2 nd = nd4[8 * c + (i >> 1)];
-                            const uint64_t t2 = fadd2(f2_pack(u2f(dp[2 * i]), u2f(dp[2 * i + 1])), (i & 1) ? nd.y : nd.x);
-                            const float2 kk = unpack_f16(keep[c][i]);
-                            const uint64_t k2w = f2_pack(kk.x, kk.y);
-                            const uint64_t d2 = fmul2(k2w, t2);
-                            const float2 dx = f2_unpack(d2);
-                            ds[i] = pack_bf16(dx.x, dx.y);
-                            if constexpr (BIAS == kBiasTable) {
-                                if (grad) {
+                            for (int i = 0; i < 16; ++i) {
+                                const ulonglong2 nd = nd4[8 * c + (i >> 1)];
+                                const uint64_t t2 = fadd2(f2_pack(u2f(dp[2 * i]), u2f(dp[2 * i + 1])), (i & 1) ? nd.y : nd.x);
+                                const float2 kk = unpack_f16(keep[c][i]);
+                                const uint64_t d2 = fmul2(f2_pack(kk.x, kk.y), t2);
+                                const float2 dx = f2_unpack(d2);
+                                ds[i] = pack_bf16(dx.x, dx.y);
+                                if constexpr (SUMS != 0) {
                                     uint64_t dy = d2;
                                     if constexpr (CAP) dy = fmul2(f2_pack(u2f(pw[i] << 16), u2f(pw[i] & 0xffff0000u)), t2);
-                                    if (side != 0) {
+                                    if constexpr (SUMS == 1) {
                                         fsum = fadd2(fsum, dy);
                                     } else {
                                         // column q's value of key row l to lane (q - l) mod 32
@@ -596,7 +622,10 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                                     }
                                 }
                             }
-                        }
+                        };
+                        if (BIAS == kBiasTable && grad && side != 0) products(std::integral_constant<int, BIAS == kBiasTable>{});
+                        else if (BIAS == kBiasTable && grad) products(std::integral_constant<int, BIAS == kBiasTable ? 2 : 0>{});
+                        else products(std::integral_constant<int, 0>{});
                         if constexpr (BIAS == kBiasTable) {
                             if (grad && side == 0) {
                                 // block (query block, key block) of 32: lane m holds distance m, and m - 32
@@ -661,7 +690,7 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 #pragma unroll
             for (int which = 0; which < 2; ++which) {
                 uint8_t* dst = smem + (which ? L::kK : L::kV);
-                const float scale = (which ? p.tau : 1.f) * kUnliftP;
+                const float scale = (which ? (CAP ? -p.tau : p.tau) : 1.f) * kUnliftP;
                 const uint32_t src = tmem + lane_off + (which ? L::kTmDK : L::kTmDV);
 #pragma unroll
                 for (int cc = 0; cc < kDC; cc += 16) {
@@ -828,7 +857,7 @@ BwdPlan plan_of(const ScoreArgs& a) {
     const int n = std::min(near_tiles(a.mod.far, kBQ), n_kv - 1);
     pl.near_lo = a.causal && !a.mod.prefix ? 0 : -n;
     pl.near_n = n - pl.near_lo + 1;
-    pl.warps = a.d == 128 ? 16 : 8;
+    pl.warps = 4 * warpgroups(a.d, a.mod.softcap > 0.f, kBiasTable);
     const size_t tiles = static_cast<size_t>(a.B) * a.H * n_kv;
     pl.near = pl.bias2 + up(static_cast<size_t>(a.H) * (2 * a.mod.far + 1) * sizeof(float));
     pl.far = pl.near + tiles * pl.near_n * kNearFloats * sizeof(float);
@@ -890,7 +919,7 @@ cudaError_t launch_main(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t stre
     p.wait_limit_ns = a.wait_limit_ns;
     if (a.ev_start) cudaEventRecord(a.ev_start, stream);
     e = launch_dependent(kern, dim3(static_cast<unsigned>(BHkv) * static_cast<unsigned>(p.n_kv)),
-                         dim3(threads_for(D == 128 ? 4 : 2)), L::kBytes, stream, tq, tk, tv, tdo, tacc, tdk, tdv, p);
+                         dim3(threads_for(warpgroups(D, CAP, BIAS))), L::kBytes, stream, tq, tk, tv, tdo, tacc, tdk, tdv, p);
     if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
     return e;
 }
@@ -918,7 +947,7 @@ cudaError_t launch_d(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t stream)
     const int64_t n8 = rows * D / 8;
     return launch_dependent(fa_score_post_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((n8 + 255) / 256, 152 * 64))),
                             dim3(256), 0, stream, static_cast<const float*>(acc), static_cast<__nv_bfloat16*>(a.dQ),
-                            a.tau * kUnliftP, n8);
+                            (cap ? -a.tau : a.tau) * kUnliftP, n8);
 }
 
 }  // namespace

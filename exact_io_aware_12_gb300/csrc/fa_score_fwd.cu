@@ -19,7 +19,11 @@
 //     softmax has read the last; at d = 128 it is written over S.
 //   - The query heads that share a key head are neighbours in launch order, so that its
 //     keys are read from L2; longest tiles first when causal.
-//   - Slopes: the distance is counted up in fp32, exactly, two columns at a time.
+//   - Capped scores without a bias: the maximum is found before the cap, which keeps the order,
+//     and the cap's last multiply-add takes the reference off.
+//   - Slopes: a tile on one side of its queries adds slope * column, the same for all rows, from
+//     shared memory; what is left, slope times the distance of the first column, goes into
+//     the row's reference.
 //   - Table: the head's biases by distance, 2 far + 1 of them, lie in shared memory; a
 //     tile all of whose pairs are at `far` or more has one bias.
 //   - A row that sees nothing keeps its reference at -inf: its weights and its sum stay 0,
@@ -59,8 +63,8 @@ struct ScoreFwdParams {
     float* LSE;
     int H, G, n_q;  // query heads, those to a key head, query tiles
     ScoreMask mask;
-    float scale_log2;        // tau * log2(e)
-    float x_scale, cap_log2;  // cap: tau / cap, cap * log2(e)
+    float scale_log2;  // tau * log2(e)
+    CapScale cap;
     const float* slopes;
     const void* table;
     const int* buckets;
@@ -74,6 +78,7 @@ struct ScoreFwdShared {
     uint64_t kv_full[4];
     uint64_t kv_empty[4];
     uint64_t s_full, s_free, p_ready, o_done;
+    __align__(16) float ramp[2][128];  // slopes: +-slope log2(e) times the column
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -87,6 +92,13 @@ __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 __device__ __forceinline__ uint32_t f2u(float x) { return __float_as_uint(x); }
 
 constexpr uint32_t kDescHi = sw128_desc_hi(1024);
+
+// (volatile: loads of the whole ramp ahead of its use would take the scores' registers)
+__device__ __forceinline__ ulonglong2 lds_2x64(uint32_t a) {
+    ulonglong2 v;
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(v.x), "=l"(v.y) : "r"(a));
+    return v;
+}
 
 // The 128 scores of a row, in registers, two at a time: f(column, pair) -> pair.
 template <typename F>
@@ -254,7 +266,12 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         const ScoreRange mine = keys_of(p.mask, b, min(row, N - 1), prefix);
         [[maybe_unused]] float* bias_s = reinterpret_cast<float*>(smem + L::kTable);
         [[maybe_unused]] float slope2 = 0.f;
-        if constexpr (BIAS == kBiasSlopes) slope2 = p.slopes[h] * kLog2e;
+        if constexpr (BIAS == kBiasSlopes) {
+            slope2 = p.slopes[h] * kLog2e;
+            sh.ramp[0][r] = slope2 * r;
+            sh.ramp[1][r] = -slope2 * r;
+            named_bar_sync(1, 128);
+        }
         if constexpr (BIAS == kBiasTable) {
             for (int i = r; i <= 2 * p.far; i += 128)
                 bias_s[i] = kLog2e * table_bias(p.table, p.table_f32, p.buckets, p.num_buckets, p.H, h, i);
@@ -284,45 +301,60 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                 mbar_arrive(bar_sf);  // S's columns may take the next block's scores now
             }
             const int kbase = (jlo + j) * kBN;
+            const bool masked = kbase < clear_lo || kbase + kBN > clear_hi;
+            [[maybe_unused]] int how = kTanhExp;  // CAP: form of the tanh
+            [[maybe_unused]] bool late = false;   // CAP: the cap is yet to come
+            [[maybe_unused]] float base = 0.f;    // slopes: what the scores below lack, the same for the row
+            float m_cand = -INFINITY;
             if constexpr (CAP) {
-                // y = cap log2(e) tanh(s tau / cap), by the largest |s| of the warp's rows
-                float mx0 = 0.f, mx1 = 0.f;
+                float hi0 = -INFINITY, hi1 = -INFINITY, lo0 = INFINITY, lo1 = INFINITY;
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                    mx0 = fmax3(mx0, fabsf(u2f(s[0][c])), fabsf(u2f(s[0][c + 1])));
-                    mx1 = fmax3(mx1, fabsf(u2f(s[1][c])), fabsf(u2f(s[1][c + 1])));
-                    mx0 = fmax3(mx0, fabsf(u2f(s[2][c])), fabsf(u2f(s[2][c + 1])));
-                    mx1 = fmax3(mx1, fabsf(u2f(s[3][c])), fabsf(u2f(s[3][c + 1])));
+                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4) {
+                        hi0 = fmax3(hi0, u2f(s[g][c]), u2f(s[g][c + 1]));
+                        hi1 = fmax3(hi1, u2f(s[g][c + 2]), u2f(s[g][c + 3]));
+                        lo0 = fmin3(lo0, u2f(s[g][c]), u2f(s[g][c + 1]));
+                        lo1 = fmin3(lo1, u2f(s[g][c + 2]), u2f(s[g][c + 3]));
+                    }
+                const float hi = fmaxf(hi0, hi1);
+                const float mx = fmaxf(hi, -fminf(lo0, lo1)) * p.cap.k;  // of the warp's rows: the tanh's form
+                how = !__any_sync(0xffffffffu, !(mx <= kTanhNear))  ? kTanhPoly3
+                      : !__any_sync(0xffffffffu, !(mx <= kTanhMid)) ? kTanhPoly5
+                                                                    : kTanhExp;
+                if (BIAS == kBiasNone && !masked) {
+                    late = true;
+                    const uint64_t v = f2_pack(hi, hi);
+                    m_cand = f2_unpack(how == kTanhPoly3   ? cap_score2<kTanhPoly3>(p.cap, v, 0)
+                                       : how == kTanhPoly5 ? cap_score2<kTanhPoly5>(p.cap, v, 0)
+                                                           : cap_score2<kTanhExp>(p.cap, v, 0)).x;
+                } else if (how == kTanhPoly3) {
+                    each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhPoly3>(p.cap, v, 0); });
+                } else if (how == kTanhPoly5) {
+                    each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhPoly5>(p.cap, v, 0); });
+                } else {
+                    each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhExp>(p.cap, v, 0); });
                 }
-                const float mx = fmaxf(mx0, mx1) * p.x_scale;
-                const uint64_t k2 = f2_pack(p.x_scale, p.x_scale), cap2 = f2_pack(p.cap_log2, p.cap_log2);
-                if (!__any_sync(0xffffffffu, !(mx <= kTanhNear)))
-                    each_pair(s, [&](int, uint64_t v) { return fmul2(tanh2<kTanhPoly3>(fmul2(v, k2)), cap2); });
-                else if (!__any_sync(0xffffffffu, !(mx <= kTanhMid)))
-                    each_pair(s, [&](int, uint64_t v) { return fmul2(tanh2<kTanhPoly5>(fmul2(v, k2)), cap2); });
-                else
-                    each_pair(s, [&](int, uint64_t v) { return fmul2(tanh2<kTanhExp>(fmul2(v, k2)), cap2); });
             }
             if constexpr (BIAS == kBiasSlopes) {
                 const float d0 = static_cast<float>(kbase - row);  // j - i at column 0, exact below 2^24
                 const int side = far_side(q_start, kbase, kBM, 0);
                 if (side != 0) {
                     // all keys before (or behind) all queries: y - slope |i - j| with the sign in the slope
-                    const uint64_t sl = f2_pack(side * slope2, side * slope2), two = f2_pack(2.f, 2.f);
-                    uint64_t dist[4];
+                    base = side * slope2 * d0;
+                    const uint32_t ramp = smem_addr(sh.ramp[side < 0]);
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) dist[g] = f2_pack(d0 + 32 * g, d0 + 32 * g + 1);
+                    for (int c = 0; c < 128; c += 4) {
+                        const ulonglong2 w = lds_2x64(ramp + 4 * c);
 #pragma unroll
-                    for (int c = 0; c < 32; c += 2)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            uint64_t v = f2_pack(u2f(s[g][c]), u2f(s[g][c + 1]));
-                            if constexpr (!CAP) v = fmul2(v, c2);
-                            const float2 y = f2_unpack(ffma2(dist[g], sl, v));
-                            s[g][c] = f2u(y.x);
-                            s[g][c + 1] = f2u(y.y);
-                            dist[g] = fadd2(dist[g], two);
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t &a = s[c >> 5][(c & 31) + 2 * e], &bb = s[c >> 5][(c & 31) + 2 * e + 1];
+                            const uint64_t v = f2_pack(u2f(a), u2f(bb)), add = e ? w.y : w.x;
+                            const float2 y = f2_unpack(CAP ? fadd2(v, add) : ffma2(v, c2, add));
+                            a = f2u(y.x);
+                            bb = f2u(y.y);
                         }
+                    }
                 } else {
                     each_pair(s, [&](int c, uint64_t v) {
                         float2 y = f2_unpack(CAP ? v : fmul2(v, c2));
@@ -346,23 +378,26 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                     });
                 }
             }
-            if (kbase < clear_lo || kbase + kBN > clear_hi) {
+            if (masked) {
                 const int from = mine.lo - kbase;
                 const uint32_t n = static_cast<uint32_t>(mine.hi - mine.lo);
 #pragma unroll
                 for (int c = 0; c < 128; ++c)
                     if (static_cast<uint32_t>(c - from) >= n) s[c >> 5][c & 31] = f2u(-INFINITY);
             }
-            float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+            if (!late) {
+                float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-                mx0 = fmax3(mx0, u2f(s[0][c]), u2f(s[0][c + 1]));
-                mx1 = fmax3(mx1, u2f(s[1][c]), u2f(s[1][c + 1]));
-                mx2 = fmax3(mx2, u2f(s[2][c]), u2f(s[2][c + 1]));
-                mx3 = fmax3(mx3, u2f(s[3][c]), u2f(s[3][c + 1]));
+                for (int c = 0; c < 32; c += 2) {
+                    mx0 = fmax3(mx0, u2f(s[0][c]), u2f(s[0][c + 1]));
+                    mx1 = fmax3(mx1, u2f(s[1][c]), u2f(s[1][c + 1]));
+                    mx2 = fmax3(mx2, u2f(s[2][c]), u2f(s[2][c + 1]));
+                    mx3 = fmax3(mx3, u2f(s[3][c]), u2f(s[3][c + 1]));
+                }
+                m_cand = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
+                if constexpr (!SCALED) m_cand *= sl2;
+                if constexpr (BIAS == kBiasSlopes) m_cand += base;
             }
-            float m_cand = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
-            if constexpr (!SCALED) m_cand *= sl2;
             const bool grow = m_cand > m_used + kRescaleThreshold;
             float alpha = 1.f;
             if (grow) {
@@ -371,38 +406,45 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             }
             l *= alpha;
             l_mma *= alpha;
-            const float neg_m = (m_used == -INFINITY) ? 0.f : -m_used;
+            const float neg_m = (m_used == -INFINITY ? 0.f : -m_used) + base;
             // l_mma sums the bf16 weights that the P V product takes (it normalises O), l the
             // fp32 ones (it gives LSE)
             const uint64_t nm2 = f2_pack(neg_m, neg_m);
             uint64_t ls2 = 0;
             float lr0 = 0.f, lr1 = 0.f;
             constexpr int kPC = D == 128 ? 16 : 32;  // packed columns per tensor-memory store
-#pragma unroll
-            for (int hh = 0; hh < 64 / kPC; ++hh) {
-                uint32_t pk[kPC];
-#pragma unroll
-                for (int i = 0; i < kPC; ++i) {
-                    const int c = hh * 2 * kPC + 2 * i;
-                    const uint64_t v = f2_pack(u2f(s[c >> 5][c & 31]), u2f(s[c >> 5][(c & 31) + 1]));
-                    const float2 x = f2_unpack(SCALED ? fadd2(v, nm2) : ffma2(v, c2, nm2));
-                    const float p0 = ex2(x.x), p1 = ex2(x.y);
-                    pk[i] = pack_bf16(p0, p1);
-                    ls2 = fadd2(ls2, f2_pack(p0, p1));
-                    add_bf16x2_f32(pk[i], lr0, lr1);
+            if (PIPE && j > 0) {
+                // P's columns are free once the previous P V has read them
+                if (!__all_sync(0xffffffffu, mbar_wait(bar_o, (j - 1) & 1, wd, kSiteSoftO))) {
+                    ok = false;
+                    break;
                 }
-                if (PIPE && hh == 0 && j > 0) {
-                    // P's columns are free once the previous P V has read them
-                    if (!__all_sync(0xffffffffu, mbar_wait(bar_o, (j - 1) & 1, wd, kSiteSoftO))) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                }
-                if constexpr (kPC == 16) tmem_st16(tP + hh * 16, pk);
-                else tmem_st32(tP + hh * 32, pk);
+                tc_fence_after();
             }
-            if (!ok) break;
+            const auto weights = [&](auto&& exponent) {  // of a pair
+#pragma unroll
+                for (int hh = 0; hh < 64 / kPC; ++hh) {
+                    uint32_t pk[kPC];
+#pragma unroll
+                    for (int i = 0; i < kPC; ++i) {
+                        const int c = hh * 2 * kPC + 2 * i;
+                        const float2 x = f2_unpack(exponent(f2_pack(u2f(s[c >> 5][c & 31]), u2f(s[c >> 5][(c & 31) + 1]))));
+                        const float p0 = ex2(x.x), p1 = ex2(x.y);
+                        pk[i] = pack_bf16(p0, p1);
+                        ls2 = fadd2(ls2, f2_pack(p0, p1));
+                        add_bf16x2_f32(pk[i], lr0, lr1);
+                    }
+                    if constexpr (kPC == 16) tmem_st16(tP + hh * 16, pk);
+                    else tmem_st32(tP + hh * 32, pk);
+                }
+            };
+            if (CAP && late) {
+                if (how == kTanhPoly3) weights([&](uint64_t v) { return cap_score2<kTanhPoly3>(p.cap, v, nm2); });
+                else if (how == kTanhPoly5) weights([&](uint64_t v) { return cap_score2<kTanhPoly5>(p.cap, v, nm2); });
+                else weights([&](uint64_t v) { return cap_score2<kTanhExp>(p.cap, v, nm2); });
+            } else {
+                weights([&](uint64_t v) { return SCALED ? fadd2(v, nm2) : ffma2(v, c2, nm2); });
+            }
             const float2 a2 = f2_unpack(ls2);
             l += a2.x + a2.y;
             l_mma += lr0 + lr1;
@@ -496,8 +538,7 @@ cudaError_t launch_t(const ScoreArgs& a, cudaStream_t stream) {
     p.mask.window = a.mod.window;
     p.mask.causal = a.causal;
     p.scale_log2 = a.tau * kLog2e;
-    p.x_scale = CAP ? a.tau / a.mod.softcap : 0.f;
-    p.cap_log2 = a.mod.softcap * kLog2e;
+    if (CAP) p.cap = CapScale(a.tau, a.mod.softcap);
     p.slopes = a.mod.slopes;
     p.table = a.mod.table;
     p.buckets = a.mod.buckets;

@@ -18,6 +18,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "fa_score.cuh"
 
@@ -46,7 +47,8 @@ struct RowsParams {
     float* dQacc;
     int H, G, n_pairs;
     ScoreMask mask;
-    float scale_log2, x_scale, cap_log2;
+    float scale_log2;
+    CapScale cap;
     const float* slopes;
     const float* bias2;  // [H][2 far + 1], log2 units
     int far;
@@ -189,11 +191,12 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                 if (!ok) continue;
                 tc_fence_after();
                 product(tmem + 256 * t, a0 + 2 * t * kStep, ring0 + sk * kStep);                 // S
+                // (K goes back as soon as both tiles' S have read it: its slot is the next V's, wanted a tile's products later)
+                if (t == 1 || j >= hi[1] || j < lo[1]) mma_commit_warp(bar_kve + 8 * sk);
                 product(tmem + 256 * t + 128, a0 + (2 * t + 1) * kStep, ring0 + sv * kStep);     // dP
                 mma_commit_warp(bar_full + 8 * t);
             }
             if (!ok) break;
-            mma_commit_warp(bar_kve + 8 * sk);
             mma_commit_warp(bar_kve + 8 * sv);
         }
         __syncwarp();
@@ -214,7 +217,6 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         // (a row that sees nothing: LSE = -inf, every weight masked to 0)
         const float nl = row < N ? -p.LSE[at] * kLog2e : -INFINITY;
         const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2), nl2 = f2_pack(nl, nl);
-        [[maybe_unused]] const uint64_t k2 = f2_pack(p.x_scale, p.x_scale), cap2 = f2_pack(p.cap_log2, p.cap_log2);
         [[maybe_unused]] float slope2 = 0.f;
         [[maybe_unused]] const float* bias2 = nullptr;
         if constexpr (BIAS == kBiasSlopes) slope2 = p.slopes[h] * kLog2e;
@@ -230,8 +232,9 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             }
             tc_fence_after();
             const int kbase = (jt + jj) * kBN;
-            const bool masked = kbase < c_lo || kbase + kBN > c_hi;
-            [[maybe_unused]] const int side = far_side(q_start, kbase, kBM, BIAS == kBiasTable ? p.far : 0);
+            const int side = far_side(q_start, kbase, kBM, BIAS == kBiasTable ? p.far : 0);
+            const bool general = kbase < c_lo || kbase + kBN > c_hi || (BIAS != kBiasNone && side == 0);
+            [[maybe_unused]] const uint64_t sl = f2_pack(side * slope2, side * slope2);  // (of j - i)
             [[maybe_unused]] uint64_t add0 = nl2;
             if constexpr (BIAS == kBiasTable) {
                 if (side != 0) {
@@ -253,27 +256,42 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                 const int col0 = kbase + 64 * side_half + 32 * c;  // the chunk's first key
                 const int from = mine.lo - col0;
                 const uint32_t n = static_cast<uint32_t>(mine.hi - mine.lo);
-                // a pair of keys: y0 = score before the bias (log2 units, or CAP false: unscaled)
-                const auto one = [&](int i, uint64_t y0) {
+                // a pair of keys, s as it comes.  GENERAL: any mask, any bias; else all are visible and the
+                // bias is the same or, of slopes, on one side.
+                [[maybe_unused]] uint64_t dist = f2_pack(static_cast<float>(col0 - row), static_cast<float>(col0 - row + 1));
+                const auto one = [&](auto how, auto general, int i) {
+                    constexpr bool GENERAL = decltype(general)::value;
                     uint64_t add = add0;
                     if constexpr (BIAS == kBiasSlopes) {
-                        const float d0 = static_cast<float>(col0 - row);
-                        add = f2_pack(fmaf(-slope2, fabsf(d0 + 2 * i), nl), fmaf(-slope2, fabsf(d0 + (2 * i + 1)), nl));
-                    }
-                    if constexpr (BIAS == kBiasTable) {
-                        if (side == 0) {
-                            const int x = row - col0 - 2 * i + p.far, top = 2 * p.far;
-                            add = fadd2(nl2, f2_pack(bias2[max(0, min(top, x))], bias2[max(0, min(top, x - 1))]));
+                        if constexpr (GENERAL) {
+                            const float2 y = f2_unpack(dist);
+                            add = f2_pack(fmaf(-slope2, fabsf(y.x), nl), fmaf(-slope2, fabsf(y.y), nl));
+                        } else {
+                            add = ffma2(dist, sl, add0);
                         }
+                        dist = fadd2(dist, f2_pack(2.f, 2.f));
                     }
-                    const float2 x = f2_unpack(CAP ? fadd2(y0, add) : ffma2(y0, c2, add));
+                    if constexpr (BIAS == kBiasTable && GENERAL) {
+                        const int x = row - col0 - 2 * i + p.far, top = 2 * p.far;
+                        add = fadd2(nl2, f2_pack(bias2[max(0, min(top, x))], bias2[max(0, min(top, x - 1))]));
+                    }
+                    const uint64_t v = f2_pack(u2f(s[2 * i]), u2f(s[2 * i + 1]));
+                    float2 x;
+                    if constexpr (CAP) x = f2_unpack(cap_score2<decltype(how)::value>(p.cap, v, add));
+                    else x = f2_unpack(ffma2(v, c2, add));
                     float p0 = ex2(x.x), p1 = ex2(x.y);
-                    if (masked) {
+                    if constexpr (GENERAL) {
                         if (static_cast<uint32_t>(2 * i - from) >= n) p0 = 0.f;
                         if (static_cast<uint32_t>(2 * i + 1 - from) >= n) p1 = 0.f;
                     }
                     sum[i & 1] = ffma2(f2_pack(p0, p1), f2_pack(u2f(dp[2 * i]), u2f(dp[2 * i + 1])), sum[i & 1]);
                 };
+                const auto all = [&](auto how, auto general_) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) one(how, general_, i);
+                };
+                using Poly5 = std::integral_constant<int, kTanhPoly5>;
+                using Exp = std::integral_constant<int, kTanhExp>;
                 if constexpr (CAP) {
                     float mx0 = 0.f, mx1 = 0.f;
 #pragma unroll
@@ -281,18 +299,18 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                         mx0 = fmax3(mx0, fabsf(u2f(s[i])), fabsf(u2f(s[i + 1])));
                         mx1 = fmax3(mx1, fabsf(u2f(s[i + 2])), fabsf(u2f(s[i + 3])));
                     }
-                    const float mx = fmaxf(mx0, mx1) * p.x_scale;
-                    const auto all = [&](auto how) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            one(i, fmul2(tanh2<decltype(how)::value>(fmul2(f2_pack(u2f(s[2 * i]), u2f(s[2 * i + 1])), k2)), cap2));
-                    };
-                    if (!__any_sync(0xffffffffu, !(mx <= kTanhNear))) all(std::integral_constant<int, kTanhPoly3>{});
-                    else if (!__any_sync(0xffffffffu, !(mx <= kTanhMid))) all(std::integral_constant<int, kTanhPoly5>{});
-                    else all(std::integral_constant<int, kTanhExp>{});
+                    // (the few tiles at the edges: two forms)
+                    const float mx = fmaxf(mx0, mx1) * p.cap.k;
+                    const bool near = !__any_sync(0xffffffffu, !(mx <= kTanhNear)), mid = !__any_sync(0xffffffffu, !(mx <= kTanhMid));
+                    if (general && mid) all(Poly5{}, std::true_type{});
+                    else if (general) all(Exp{}, std::true_type{});
+                    else if (near) all(std::integral_constant<int, kTanhPoly3>{}, std::false_type{});
+                    else if (mid) all(Poly5{}, std::false_type{});
+                    else all(Exp{}, std::false_type{});
+                } else if (general) {
+                    all(Exp{}, std::true_type{});
                 } else {
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) one(i, f2_pack(u2f(s[2 * i]), u2f(s[2 * i + 1])));
+                    all(Exp{}, std::false_type{});
                 }
             }
         }
@@ -337,8 +355,7 @@ cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, const void* sp
     p.mask.window = a.mod.window;
     p.mask.causal = a.causal;
     p.scale_log2 = a.tau * kLog2e;
-    p.x_scale = CAP ? a.tau / a.mod.softcap : 0.f;
-    p.cap_log2 = a.mod.softcap * kLog2e;
+    if (CAP) p.cap = CapScale(a.tau, a.mod.softcap);
     p.slopes = a.mod.slopes;
     p.bias2 = bias2;
     p.far = a.mod.far;

@@ -638,6 +638,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
     return d;
 }
 
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+    float d;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Smallest index j in [from, n) whose bit is set in a | b (b may be null), or n.
 // Bits at or past n must be clear.
 __device__ __forceinline__ int next_set_bit(const uint32_t* a, const uint32_t* b, int from, int n) {
