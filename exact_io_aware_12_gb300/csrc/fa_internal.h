@@ -186,6 +186,12 @@ struct ScoreArgs {
     cudaEvent_t ev_start;  // optional: recorded around the main kernel
     cudaEvent_t ev_stop;
 };
+// Orders in which tiles are taken, each [B][tiles], or null: of 128 queries, of 256, of 128 keys.
+struct ScoreOrder {
+    int* queries = nullptr;
+    int* pairs = nullptr;
+    int* keys = nullptr;
+};
 size_t score_fwd_workspace(int B, int N, bool docs);
 size_t score_bwd_workspace(const ScoreArgs& a);
 
@@ -253,11 +259,12 @@ cudaError_t launch_fwd_sparse(const FwdArgs& a, cudaStream_t stream);
 cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t stream);
 cudaError_t launch_score_fwd(const ScoreArgs& a, cudaStream_t stream);
 cudaError_t launch_score_bwd(const ScoreArgs& a, cudaStream_t stream);
-// D_i = sum_j P_ij dP_ij and a zeroed dQ accumulator (spans and bias2: of the workspace, or null)
-cudaError_t launch_score_rows(const ScoreArgs& a, float* dvec, float* acc, const void* spans, const float* bias2,
-                              cudaStream_t stream);
-// documents' ids [B][N] -> each token's document as [first, end) (int2 [B][N])
-cudaError_t launch_score_spans(const int* docs, void* spans, int B, int N, cudaStream_t stream);
+// D_i = sum_j P_ij dP_ij and a zeroed dQ accumulator (spans, order of pairs and bias2: of the workspace, or null)
+cudaError_t launch_score_rows(const ScoreArgs& a, float* dvec, float* acc, const void* spans, const int* order,
+                              const float* bias2, cudaStream_t stream);
+// documents' ids -> each token's document as [first, end) (int2 [B][N]), and tiles' orders
+cudaError_t launch_score_spans(const ScoreArgs& a, void* spans, const ScoreOrder& order, cudaStream_t stream);
+size_t score_spans_bytes(int B, int N);
 cudaError_t launch_decode(const DecArgs& a, cudaStream_t stream);
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_fwd_paged(const PagedArgs& a, cudaStream_t stream);

@@ -258,7 +258,7 @@ __device__ __forceinline__ int clamp_len(const PagedParams& p, int b) {
     return len;
 }
 
-template <int WARPS>
+template <int WARPS, bool MOD>
 struct PagedShared {
     // per ring slot: first key of the tile (a bad page: past every row); 8-bit: the page's scales
     struct __align__(16) Slot {
@@ -269,9 +269,10 @@ struct PagedShared {
     int at_b[WARPS], at_before[WARPS];  // a share's first sequence, tiles of those before it
     float m[WARPS][16], l[WARPS][16];   // WHOLE: each warp's reference and sum
     float lse[WARPS > kPagedWarps ? 64 : 1];  // of a cluster's block: log2 of its rows' sums
+    short bucket[MOD ? kScoreMaxFar + 1 : 1];  // a bias's bucket at distances 0 .. far (-1: none)
 };
-template <int D, int NT, bool F8, int WARPS>
-constexpr int kPagedBytes = WARPS * PagedLayout<D, NT, F8>::kWarpRing + static_cast<int>(sizeof(PagedShared<WARPS>));
+template <int D, int NT, bool F8, int WARPS, bool MOD>
+constexpr int kPagedBytes = WARPS * PagedLayout<D, NT, F8>::kWarpRing + static_cast<int>(sizeof(PagedShared<WARPS, MOD>));
 
 // WW > 0: a block of WW warps takes one segment, its warps the tiles in turn, and joins their
 // results in shared memory: no partial results, no second kernel.  For short segments.
@@ -289,7 +290,7 @@ fa_paged_kernel(const PagedParams p) {
     constexpr int kChunksK = D / (F8 ? 64 : 32);  // 16-byte pieces of a key row per thread
     constexpr float kSlack = F8 ? kGrow8 : kGrow, kLift = F8 ? kLift8 : 0.f;
     extern __shared__ __align__(1024) uint8_t smem[];
-    using Shared = PagedShared<WARPS>;
+    using Shared = PagedShared<WARPS, MOD>;
     Shared& sh = *reinterpret_cast<Shared*>(smem + WARPS * L::kWarpRing);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     // Launched as a dependent of the kernel before it: its start-up overlaps that kernel's
@@ -301,6 +302,23 @@ fa_paged_kernel(const PagedParams p) {
     if ((smem_addr(smem) & 255u) != 0u) {  // (the XOR orders count on tiles at multiples of 256 bytes)
         if (tid == 0) atomicCAS(p.err, 0u, 1u | (kSitePagedSmem << 8));
         return;
+    }
+    // (the buckets' map once per block: two loads in a row for each near tile took as long as several tiles)
+    [[maybe_unused]] const auto bias_at = [&](int h, int dist) {
+        const int e = sh.bucket[MOD ? max(0, min(p.far, dist)) : 0];
+        const long long at = static_cast<long long>(max(e, 0)) * p.H + h;  // (a load for all, no branch)
+        const float y = p.bias_f32 ? static_cast<const float*>(p.bias)[at]
+                                   : __uint_as_float(static_cast<uint32_t>(static_cast<const unsigned short*>(p.bias)[at]) << 16);
+        return e < 0 ? 0.f : kLog2e * y;
+    };
+    if constexpr (MOD) {
+        if (p.bias) {
+            for (int i = tid; i <= p.far; i += static_cast<int>(blockDim.x)) {
+                const int e = p.buckets[p.far + i];
+                sh.bucket[i] = static_cast<short>(static_cast<unsigned>(e) < static_cast<unsigned>(p.num_buckets) ? e : -1);
+            }
+            __syncthreads();
+        }
     }
     const uint32_t k_dst = W::k_dst(lane), v_dst = W::v_dst(lane), k_src = W::k_src(g, t4), v_src = W::v_src(g, t4);
     const int segs_per_b = p.H_kv * p.rgroups;
@@ -558,8 +576,7 @@ fa_paged_kernel(const PagedParams p) {
                     mod_h[nt][e] = h;
                     mod_f[nt][e] = 0.f;
                     if (rows > 0 && p.slopes) mod_f[nt][e] = kLog2e * p.slopes[h];
-                    if (rows > 0 && p.bias)
-                        mod_f[nt][e] = kLog2e * table_bias(p.bias, p.bias_f32, p.buckets, p.num_buckets, p.H, h, 2 * p.far);
+                    if (rows > 0 && p.bias) mod_f[nt][e] = bias_at(h, p.far);
                 }
         }
 
@@ -589,6 +606,27 @@ fa_paged_kernel(const PagedParams p) {
 #pragma unroll
             for (int tp = 0; tp < TP; ++tp) sl[tp] = sh.slot[warp][slot_at][tp];
             slot_at = slot_at + 1 == S ? 0 : slot_at + 1;
+
+            // a bias of near keys is fetched while the products below run (tiles all of whose keys are far from every
+            // row have one bias per row)
+            [[maybe_unused]] float bias_y[TP][NT][4];
+            if constexpr (MOD) {
+                if (p.bias) {
+#pragma unroll
+                    for (int tp = 0; tp < TP; ++tp) {
+                        const int key0 = sl[tp].key0;
+                        const bool near = len - p.Nq - (key0 + kPagedTile - 1) < p.far;
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                bias_y[tp][nt][e] = mod_f[nt][e & 1];
+                                if (near)  // (keys behind the row are hidden below)
+                                    bias_y[tp][nt][e] = bias_at(mod_h[nt][e & 1], last[nt][e & 1] - (key0 + g + (e & 2 ? 8 : 0)));
+                            }
+                    }
+                }
+            }
 
             // S^T = K Q^T
             float s[TP][NT][4];
@@ -673,18 +711,8 @@ fa_paged_kernel(const PagedParams p) {
                                 x[e + 2] = fmaf(mod_f[nt][e], k1 - la, x[e + 2]);
                             }
                         } else if (p.bias) {
-                            // (tiles all of whose keys are far from every row: one bias per row)
-                            const bool near = len - p.Nq - (key0 + kPagedTile - 1) < p.far;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float y = mod_f[nt][e & 1];
-                                if (near) {
-                                    const int dist = last[nt][e & 1] - (key0 + g + (e & 2 ? 8 : 0));
-                                    y = kLog2e * table_bias(p.bias, p.bias_f32, p.buckets, p.num_buckets, p.H, mod_h[nt][e & 1],
-                                                            max(0, min(2 * p.far, dist + p.far)));
-                                }
-                                x[e] += y;
-                            }
+                            for (int e = 0; e < 4; ++e) x[e] += bias_y[tp][nt][e];
                         }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) x[e] -= ref[e & 1];
@@ -1203,7 +1231,7 @@ cudaError_t launch_paged_t(const PagedArgs& a, const PagedPlan& pl, PagedParams&
     constexpr auto kern = &fa_paged_kernel<D, NT, F8, 0, MOD>;
     constexpr auto kern_w = &fa_paged_kernel<D, NT, F8, kPagedWarps, MOD>;
     constexpr auto kern_w2 = &fa_paged_kernel<D, NT, F8, 2 * kPagedWarps, MOD>;
-    constexpr int bytes = kPagedBytes<D, NT, F8, kPagedWarps>, bytes2 = kPagedBytes<D, NT, F8, 2 * kPagedWarps>;
+    constexpr int bytes = kPagedBytes<D, NT, F8, kPagedWarps, MOD>, bytes2 = kPagedBytes<D, NT, F8, 2 * kPagedWarps, MOD>;
     cudaError_t e = !pl.whole  ? set_max_dyn_smem_once<kern>(bytes)
                     : pl.wide ? set_max_dyn_smem_once<kern_w2>(bytes2)
                               : set_max_dyn_smem_once<kern_w>(bytes);

@@ -90,6 +90,7 @@ struct ScoreBwdParams {
     const float* LSE;
     const float* Dvec;
     int H, H_kv, G, n_kv, head_group;
+    const int* order;  // [B][n_kv], or null: as they come
     ScoreMask mask;
     float scale_log2, tau;
     float x_scale, cap_log2;
@@ -198,7 +199,6 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         bkv = g * p.head_group + (j - ikv * heads);
     }
     const int b = bkv / p.H_kv, hkv = bkv - b * p.H_kv;
-    const int kvs = ikv * kBK;
     if (sbase & 1023u) {  // the swizzled tiles need 1024-byte alignment
         if (threadIdx.x == 0) atomicCAS(p.err, 0u, 1u | (0xAAu << 8));
         return;
@@ -258,6 +258,8 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const Watchdog wd{p.err, &sh.abort_flag, p.wait_limit_ns};
     constexpr uint32_t FULL = 0xffffffffu;
 
+    if (p.order) ikv = p.order[static_cast<long long>(b) * p.n_kv + ikv];
+    const int kvs = ikv * kBK;
     // query tiles [first, first + per_head) see this key tile, in each of the G heads; the rows in
     // [clear_lo, clear_hi) see all of its keys.  A tile of keys that nothing sees has a step all the same
     // (its sums are 0).
@@ -842,7 +844,7 @@ size_t up(size_t x) { return (x + 255) / 256 * 256; }
 // The workspace's parts, each 256-aligned.
 struct BwdPlan {
     int near_lo = 0, near_n = 0, warps = 0;
-    size_t dvec = 0, acc = 0, spans = 0, bias2 = 0, near = 0, far = 0, red = 0, bytes = 0;
+    size_t dvec = 0, acc = 0, spans = 0, order = 0, bias2 = 0, near = 0, far = 0, red = 0, bytes = 0;
 };
 BwdPlan plan_of(const ScoreArgs& a) {
     BwdPlan pl;
@@ -850,7 +852,8 @@ BwdPlan plan_of(const ScoreArgs& a) {
     const int n_kv = (a.N + kBK - 1) / kBK;
     pl.acc = up(rows * sizeof(float));
     pl.spans = pl.acc + up(rows * a.d * sizeof(float));
-    pl.bias2 = pl.spans + up(score_fwd_workspace(a.B, a.N, a.mod.docs != nullptr));
+    pl.order = pl.spans + (a.mod.docs ? score_spans_bytes(a.B, a.N) : 0);  // of pairs, then of key tiles
+    pl.bias2 = pl.order + (a.mod.docs ? up(static_cast<size_t>(a.B) * (n_kv + (n_kv + 1) / 2) * sizeof(int)) : 0);
     pl.near = pl.far = pl.red = pl.bytes = pl.bias2;
     if (!a.mod.table) return pl;
     // (offsets that tiles have; behind the query only where a prefix, or no mask, shows such keys)
@@ -899,6 +902,7 @@ cudaError_t launch_main(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t stre
     p.G = a.H / a.H_kv;
     p.n_kv = (a.N + kBK - 1) / kBK;
     p.head_group = head_group(a);
+    p.order = a.mod.docs ? reinterpret_cast<const int*>(a.workspace + pl.order) + static_cast<size_t>(a.B) * ((p.n_kv + 1) / 2) : nullptr;
     p.mask.spans = a.mod.docs ? reinterpret_cast<const int2*>(a.workspace + pl.spans) : nullptr;
     p.mask.prefix = a.mod.prefix;
     p.mask.N = a.N;
@@ -937,7 +941,7 @@ cudaError_t launch_d(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t stream)
         if (e != cudaSuccess) return e;
     }
     e = launch_score_rows(a, reinterpret_cast<float*>(a.workspace + pl.dvec), acc, a.mod.docs ? a.workspace + pl.spans : nullptr,
-                          bias2, stream);
+                          a.mod.docs ? reinterpret_cast<const int*>(a.workspace + pl.order) : nullptr, bias2, stream);
     if (e != cudaSuccess) return e;
     const bool cap = a.mod.softcap > 0.f;
     if (a.mod.slopes) e = cap ? launch_main<D, true, kBiasSlopes>(a, pl, stream) : launch_main<D, false, kBiasSlopes>(a, pl, stream);
@@ -957,7 +961,12 @@ size_t score_bwd_workspace(const ScoreArgs& a) { return plan_of(a).bytes; }
 cudaError_t launch_score_bwd(const ScoreArgs& a, cudaStream_t stream) {
     const BwdPlan pl = plan_of(a);
     cudaError_t e = cudaSuccess;
-    if (a.mod.docs) e = launch_score_spans(a.mod.docs, a.workspace + pl.spans, a.B, a.N, stream);
+    if (a.mod.docs) {
+        ScoreOrder order;
+        order.pairs = reinterpret_cast<int*>(a.workspace + pl.order);
+        order.keys = order.pairs + static_cast<size_t>(a.B) * ((a.N + 2 * kBQ - 1) / (2 * kBQ));
+        e = launch_score_spans(a, a.workspace + pl.spans, order, stream);
+    }
     if (e == cudaSuccess) e = a.d == 64 ? launch_d<64>(a, pl, stream) : launch_d<128>(a, pl, stream);
     if (e != cudaSuccess || !a.dTable) return e;
     TableGradParams t;

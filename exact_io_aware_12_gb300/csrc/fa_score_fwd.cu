@@ -62,6 +62,7 @@ struct ScoreFwdLayout {
 struct ScoreFwdParams {
     float* LSE;
     int H, G, n_q;  // query heads, those to a key head, query tiles
+    const int* order;  // [B][n_q], or null: from the last
     ScoreMask mask;
     float scale_log2;  // tau * log2(e)
     CapScale cap;
@@ -131,7 +132,6 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const int bh = static_cast<int>(blockIdx.x);
     const int b = bh / p.H, h = bh - b * p.H;
     const int bkv = b * (p.H / p.G) + h / p.G;
-    const int q_start = (p.n_q - 1 - static_cast<int>(blockIdx.y)) * kBM;
 
     const uint32_t bar_q = smem_addr(&sh.q_full);
     const uint32_t bar_kvf = smem_addr(&sh.kv_full[0]);
@@ -171,6 +171,8 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     griddep_wait();
     const uint32_t tmem = sh.tmem_base;
     const Watchdog wd{p.err, &sh.abort_flag, p.wait_limit_ns};
+    const int rank = static_cast<int>(blockIdx.y);
+    const int q_start = (p.order ? p.order[static_cast<long long>(b) * p.n_q + rank] : p.n_q - 1 - rank) * kBM;
 
     // key blocks [jlo, jlo + nb); those within [clear_lo, clear_hi) every row sees
     const int prefix = prefix_of(p.mask, b);
@@ -533,6 +535,7 @@ cudaError_t launch_t(const ScoreArgs& a, cudaStream_t stream) {
     p.G = a.H / a.H_kv;
     p.n_q = (a.N + kBM - 1) / kBM;
     p.mask.spans = a.mod.docs ? reinterpret_cast<const int2*>(a.workspace) : nullptr;
+    p.order = a.mod.docs ? reinterpret_cast<const int*>(a.workspace + score_spans_bytes(a.B, a.N)) : nullptr;
     p.mask.prefix = a.mod.prefix;
     p.mask.N = a.N;
     p.mask.window = a.mod.window;
@@ -564,11 +567,15 @@ cudaError_t launch_d(const ScoreArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-size_t score_fwd_workspace(int B, int N, bool docs) { return docs ? static_cast<size_t>(B) * N * sizeof(int2) : 0; }
+size_t score_fwd_workspace(int B, int N, bool docs) {
+    return docs ? score_spans_bytes(B, N) + static_cast<size_t>(B) * ((static_cast<size_t>(N) + kBM - 1) / kBM) * sizeof(int) : 0;
+}
 
 cudaError_t launch_score_fwd(const ScoreArgs& a, cudaStream_t stream) {
     if (a.mod.docs) {
-        const cudaError_t e = launch_score_spans(a.mod.docs, a.workspace, a.B, a.N, stream);
+        ScoreOrder order;
+        order.queries = reinterpret_cast<int*>(a.workspace + score_spans_bytes(a.B, a.N));
+        const cudaError_t e = launch_score_spans(a, a.workspace, order, stream);
         if (e != cudaSuccess) return e;
     }
     return a.d == 64 ? launch_d<64>(a, stream) : launch_d<128>(a, stream);

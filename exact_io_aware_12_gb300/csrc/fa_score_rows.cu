@@ -46,6 +46,7 @@ struct RowsParams {
     float* Dvec;
     float* dQacc;
     int H, G, n_pairs;
+    const int* order;  // [B][n_pairs], or null: from the last
     ScoreMask mask;
     float scale_log2;
     CapScale cap;
@@ -88,8 +89,6 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     const int bh = static_cast<int>(blockIdx.x);
     const int b = bh / p.H, h = bh - b * p.H;
     const int bkv = b * (p.H / p.G) + h / p.G;
-    const int q0 = (p.n_pairs - 1 - static_cast<int>(blockIdx.y)) * 2 * kBM;
-    const bool two = q0 + kBM < N;
 
     const uint32_t bar_q = smem_addr(&sh.q_full);
     const uint32_t bar_kvf = smem_addr(&sh.kv_full[0]);
@@ -126,6 +125,9 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     griddep_wait();
     const uint32_t tmem = sh.tmem_base;
     const Watchdog wd{p.err, &sh.abort_flag, p.wait_limit_ns};
+    const int rank = static_cast<int>(blockIdx.y);
+    const int q0 = (p.order ? p.order[static_cast<long long>(b) * p.n_pairs + rank] : p.n_pairs - 1 - rank) * 2 * kBM;
+    const bool two = q0 + kBM < N;
 
     // tile t takes key blocks [lo[t], hi[t]); the two ranges overlap or touch (a tile's own block is
     // in its range or beside it), so the loaders walk [jlo, jhi)
@@ -331,7 +333,7 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 }
 
 template <int D, bool CAP, int BIAS>
-cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, const void* spans, const float* bias2, cudaStream_t stream) {
+cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, const void* spans, const int* order, const float* bias2, cudaStream_t stream) {
     using L = RowsLayout<D>;
     CUtensorMap tq, tk, tv, tdo;
     const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -350,6 +352,7 @@ cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, const void* sp
     p.G = a.H / a.H_kv;
     p.n_pairs = (a.N + 2 * kBM - 1) / (2 * kBM);
     p.mask.spans = static_cast<const int2*>(spans);
+    p.order = order;
     p.mask.prefix = a.mod.prefix;
     p.mask.N = a.N;
     p.mask.window = a.mod.window;
@@ -366,23 +369,23 @@ cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, const void* sp
 }
 
 template <int D>
-cudaError_t launch_d(const ScoreArgs& a, float* dvec, float* acc, const void* spans, const float* bias2, cudaStream_t stream) {
+cudaError_t launch_d(const ScoreArgs& a, float* dvec, float* acc, const void* spans, const int* order, const float* bias2, cudaStream_t stream) {
     const bool cap = a.mod.softcap > 0.f;
     if (a.mod.slopes)
-        return cap ? launch_t<D, true, kBiasSlopes>(a, dvec, acc, spans, bias2, stream)
-                   : launch_t<D, false, kBiasSlopes>(a, dvec, acc, spans, bias2, stream);
+        return cap ? launch_t<D, true, kBiasSlopes>(a, dvec, acc, spans, order, bias2, stream)
+                   : launch_t<D, false, kBiasSlopes>(a, dvec, acc, spans, order, bias2, stream);
     if (a.mod.table)
-        return cap ? launch_t<D, true, kBiasTable>(a, dvec, acc, spans, bias2, stream)
-                   : launch_t<D, false, kBiasTable>(a, dvec, acc, spans, bias2, stream);
-    return cap ? launch_t<D, true, kBiasNone>(a, dvec, acc, spans, bias2, stream)
-               : launch_t<D, false, kBiasNone>(a, dvec, acc, spans, bias2, stream);
+        return cap ? launch_t<D, true, kBiasTable>(a, dvec, acc, spans, order, bias2, stream)
+                   : launch_t<D, false, kBiasTable>(a, dvec, acc, spans, order, bias2, stream);
+    return cap ? launch_t<D, true, kBiasNone>(a, dvec, acc, spans, order, bias2, stream)
+               : launch_t<D, false, kBiasNone>(a, dvec, acc, spans, order, bias2, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_score_rows(const ScoreArgs& a, float* dvec, float* acc, const void* spans, const float* bias2,
-                              cudaStream_t stream) {
-    return a.d == 64 ? launch_d<64>(a, dvec, acc, spans, bias2, stream) : launch_d<128>(a, dvec, acc, spans, bias2, stream);
+cudaError_t launch_score_rows(const ScoreArgs& a, float* dvec, float* acc, const void* spans, const int* order,
+                              const float* bias2, cudaStream_t stream) {
+    return a.d == 64 ? launch_d<64>(a, dvec, acc, spans, order, bias2, stream) : launch_d<128>(a, dvec, acc, spans, order, bias2, stream);
 }
 
 }  // namespace fa
