@@ -57,11 +57,6 @@ def _check_blocks(blocks: torch.Tensor, ref: torch.Tensor) -> int:
     return heads
 
 
-def _scored(*options) -> bool:
-    """Whether any option of attention with changed scores is given."""
-    return any(x is not None for x in options)
-
-
 def distance_buckets(num_buckets: int, max_distance: int, bidirectional: bool = False,
                      device=None) -> torch.Tensor:
     """The ``buckets`` of a learned relative position bias whose buckets widen with
@@ -123,7 +118,8 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool,
       prefix   int32 [B], with ``causal``: the first prefix[b] positions are
                visible from before them, too
     The workspace (only documents take one) is allocated with torch when not given."""
-    if _scored(softcap, slopes, bias, buckets, docs, prefix):
+    if (softcap is not None or slopes is not None or bias is not None or buckets is not None
+            or docs is not None or prefix is not None):
         if o_fp32 or sinks or blocks is not None:
             raise ValueError("capped, biased or masked scores go with a bf16 O, no sinks and no block mask")
         return _lib.binding().fwd_score(q, k, v, causal, tau, softcap, slopes, bias, buckets, docs,
@@ -200,7 +196,8 @@ def bwd(q, k, v, o, do, lse, causal: bool, tau: Optional[float] = None,
     ``score_workspace_bytes``): dK and dV have k's heads, summed over the query
     heads that share them.  With a ``bias`` its gradient, of its shape and type,
     comes fourth (in ``dbias`` where given), unless ``bias_grad`` is false."""
-    if _scored(softcap, slopes, bias, buckets, docs, prefix):
+    if (softcap is not None or slopes is not None or bias is not None or buckets is not None
+            or docs is not None or prefix is not None):
         if sinks or blocks is not None:
             raise ValueError("capped, biased or masked scores go with no sinks and no block mask")
         if not bias_grad and dbias is not None:
@@ -363,7 +360,7 @@ def fwd_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     allocated with torch when not given.  ``softcap``, ``slopes``, ``bias`` and
     ``buckets`` as in ``fwd`` (fa_fwd_paged_score): distances are between positions
     of the sequence."""
-    if _scored(softcap, slopes, bias, buckets):
+    if softcap is not None or slopes is not None or bias is not None or buckets is not None:
         return _lib.binding().fwd_paged(q, k_cache, v_cache, page_table, lens, tau, window, sinks, k_scale,
                                         v_scale, out, lse, workspace, softcap, slopes, bias, buckets)
     return _lib.binding().fwd_paged(q, k_cache, v_cache, page_table, lens, tau, window, sinks, k_scale,
@@ -421,7 +418,8 @@ def attention(q, k, v, causal: bool = False, tau: Optional[float] = None,
     ``bias`` (not to ``slopes``).  A backward pass may be captured in a CUDA graph while no
     eager graph of the same leaves lives (torch ties a leaf to the stream that it was first
     used on)."""
-    if _scored(softcap, slopes, bias, buckets, docs, prefix):
+    if (softcap is not None or slopes is not None or bias is not None or buckets is not None
+            or docs is not None or prefix is not None):
         if sinks:
             raise ValueError("capped, biased or masked scores go with no sinks")
         if slopes is not None and slopes.requires_grad:

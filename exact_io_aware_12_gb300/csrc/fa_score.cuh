@@ -50,12 +50,13 @@ __device__ __forceinline__ float rcp(float x) {
 }
 
 // tanh(x) for |x| <= kTanhNear, by x p(x^2): p of degree 3 fitted to least largest error
-// (6e-9), degree 5 up to kTanhMid (4e-8); beyond, 1 - 2 / (1 + e^2x) with the
+// (6e-9), degree 4 up to kTanhMid (1.4e-8); beyond, 1 - 2 / (1 + e^2x) with the
 // hardware's exponential and reciprocal (two of them per score, which a polynomial on the
-// fp32 pipe beats while it is short).  tanh.approx is off by 2^-11 of its value: 0.02 of a
-// score capped at 50.
-constexpr float kTanhNear = 0.3f, kTanhMid = 0.75f;
-enum : int { kTanhPoly3 = 0, kTanhPoly5 = 1, kTanhExp = 2 };
+// fp32 pipe beats while it is short: forward of 16 heads of 8192 tokens, window 4096, 231 us by
+// the first, 292 by the last).  tanh.approx is off by 2^-11 of its value: 0.02 of a score
+// capped at 50.
+constexpr float kTanhNear = 0.3f, kTanhMid = 0.5f;
+enum : int { kTanhPoly3 = 0, kTanhPoly4 = 1, kTanhExp = 2 };
 // Two values of tanh(x) at once, |x| within the bound of HOW.
 template <int HOW>
 __device__ __forceinline__ uint64_t tanh2(uint64_t x) {
@@ -71,10 +72,9 @@ __device__ __forceinline__ uint64_t tanh2(uint64_t x) {
             p = ffma2(u, c(-0.05022904649376869f), c(0.1331268697977066f));
             p = ffma2(u, p, c(-0.3333296477794647f));
         } else {
-            p = ffma2(u, c(-0.004736414644867182f), c(0.019611310213804245f));
-            p = ffma2(u, p, c(-0.053358446806669235f));
-            p = ffma2(u, p, c(0.13325688242912292f));
-            p = ffma2(u, p, c(-0.33332979679107666f));
+            p = ffma2(u, c(0.017151299864053726f), c(-0.05299423262476921f));
+            p = ffma2(u, p, c(0.13324907422065735f));
+            p = ffma2(u, p, c(-0.33333075046539307f));
         }
         p = ffma2(u, p, c(1.f));
         return fmul2(x, p);
@@ -84,7 +84,7 @@ __device__ __forceinline__ uint64_t tanh2(uint64_t x) {
 // Scores capped, in log2 units: what cap log2(e) tanh(s tau / cap) takes.
 struct CapScale {
     float k, k_exp, cap2;
-    uint64_t k_2, cap_2, cap_m2, near[4], mid[6];  // pairs: a paired instruction takes them as they come
+    uint64_t k_2, cap_2, cap_m2, near[4], mid[5];  // pairs: a paired instruction takes them as they come
     __host__ __device__ CapScale() {}
     static uint64_t pair(float v) {
         uint32_t x;
@@ -101,10 +101,9 @@ struct CapScale {
         cap_m2 = pair(-2.f * cap2);
         // the fits of tanh2, times tau log2(e): y = s p((k s)^2) needs no products beside p's
         const float n[4] = {1.f, -0.3333296477794647f, 0.1331268697977066f, -0.05022904649376869f};
-        const float m[6] = {1.f, -0.33332979679107666f, 0.13325688242912292f, -0.053358446806669235f, 0.019611310213804245f,
-                            -0.004736414644867182f};
+        const float m[5] = {1.f, -0.33333075046539307f, 0.13324907422065735f, -0.05299423262476921f, 0.017151299864053726f};
         for (int i = 0; i < 4; ++i) near[i] = pair(lin * n[i]);
-        for (int i = 0; i < 6; ++i) mid[i] = pair(lin * m[i]);
+        for (int i = 0; i < 5; ++i) mid[i] = pair(lin * m[i]);
     }
 };
 // Two capped scores plus `add`.
@@ -115,7 +114,7 @@ __device__ __forceinline__ uint64_t cap_score2(const CapScale& c, uint64_t s, ui
         const uint64_t r = f2_pack(rcp(1.f + ex2(c.k_exp * v.x)), rcp(1.f + ex2(c.k_exp * v.y)));
         return ffma2(c.cap_m2, r, fadd2(c.cap_2, add));
     } else {
-        constexpr int n = HOW == kTanhPoly3 ? 4 : 6;
+        constexpr int n = HOW == kTanhPoly3 ? 4 : 5;
         const uint64_t* q = HOW == kTanhPoly3 ? c.near : c.mid;
         const uint64_t t = fmul2(s, c.k_2), u = fmul2(t, t);
         uint64_t p = q[n - 1];

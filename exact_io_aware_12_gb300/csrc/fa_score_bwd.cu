@@ -545,7 +545,7 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
 #pragma unroll
                             for (int i = 0; i < 16; ++i) weights(how, general_, i);
                         };
-                        using Poly5 = std::integral_constant<int, kTanhPoly5>;
+                        using Poly4 = std::integral_constant<int, kTanhPoly4>;
                         using Exp = std::integral_constant<int, kTanhExp>;
                         if constexpr (CAP) {
                             float mx0 = 0.f, mx1 = 0.f;
@@ -557,10 +557,10 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                             // (the few tiles at the edges: two forms)
                             const float mx = fmaxf(mx0, mx1) * p.x_scale;
                             const bool near = !__any_sync(FULL, !(mx <= kTanhNear)), mid = !__any_sync(FULL, !(mx <= kTanhMid));
-                            if (general && mid) all(Poly5{}, std::true_type{});
+                            if (general && mid) all(Poly4{}, std::true_type{});
                             else if (general) all(Exp{}, std::true_type{});
                             else if (near) all(std::integral_constant<int, kTanhPoly3>{}, std::false_type{});
-                            else if (mid) all(Poly5{}, std::false_type{});
+                            else if (mid) all(Poly4{}, std::false_type{});
                             else all(Exp{}, std::false_type{});
                         } else if (general) {
                             all(Exp{}, std::true_type{});

@@ -43,6 +43,7 @@ constexpr int kThreads = 192;
 constexpr int kProducerWarp = 4, kMmaWarp = 5;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kCapExact = 1024.f;        // log2 units: 2^-24 of it is 6e-5 of a score
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8
 
 template <int D>
@@ -82,6 +83,7 @@ struct ScoreFwdShared {
     __align__(16) float ramp[2][128];  // slopes: +-slope log2(e) times the column
     uint32_t tmem_base;
     int abort_flag;
+    int how;  // the farthest form of the tanh that a tile has needed
 };
 
 enum : uint32_t {
@@ -142,6 +144,7 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const uint32_t bar_o = smem_addr(&sh.o_done);
     if (threadIdx.x == 0) {
         sh.abort_flag = 0;
+        sh.how = 0;
         mbar_init(bar_q, 1);
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(bar_kvf + 8 * s, 1);
@@ -322,18 +325,24 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                 const float hi = fmaxf(hi0, hi1);
                 const float mx = fmaxf(hi, -fminf(lo0, lo1)) * p.cap.k;  // of the warp's rows: the tanh's form
                 how = !__any_sync(0xffffffffu, !(mx <= kTanhNear))  ? kTanhPoly3
-                      : !__any_sync(0xffffffffu, !(mx <= kTanhMid)) ? kTanhPoly5
+                      : !__any_sync(0xffffffffu, !(mx <= kTanhMid)) ? kTanhPoly4
                                                                     : kTanhExp;
+                // (once one of the CTA's tiles has needed a farther form, all take it: warps that go to and
+                // fro between the forms wait for instructions, 292 -> 351 us where a third of the tiles passed a bound.
+                // The last form's error is 2^-24 of the cap, whatever the score: not where caps are in the thousands.)
+                const int most = *const_cast<volatile int*>(&sh.how);
+                if (how > most) *const_cast<volatile int*>(&sh.how) = how;
+                else if (most == kTanhPoly4 || p.cap.cap2 <= kCapExact) how = most;
                 if (BIAS == kBiasNone && !masked) {
                     late = true;
                     const uint64_t v = f2_pack(hi, hi);
                     m_cand = f2_unpack(how == kTanhPoly3   ? cap_score2<kTanhPoly3>(p.cap, v, 0)
-                                       : how == kTanhPoly5 ? cap_score2<kTanhPoly5>(p.cap, v, 0)
+                                       : how == kTanhPoly4 ? cap_score2<kTanhPoly4>(p.cap, v, 0)
                                                            : cap_score2<kTanhExp>(p.cap, v, 0)).x;
                 } else if (how == kTanhPoly3) {
                     each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhPoly3>(p.cap, v, 0); });
-                } else if (how == kTanhPoly5) {
-                    each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhPoly5>(p.cap, v, 0); });
+                } else if (how == kTanhPoly4) {
+                    each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhPoly4>(p.cap, v, 0); });
                 } else {
                     each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhExp>(p.cap, v, 0); });
                 }
@@ -442,7 +451,7 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             };
             if (CAP && late) {
                 if (how == kTanhPoly3) weights([&](uint64_t v) { return cap_score2<kTanhPoly3>(p.cap, v, nm2); });
-                else if (how == kTanhPoly5) weights([&](uint64_t v) { return cap_score2<kTanhPoly5>(p.cap, v, nm2); });
+                else if (how == kTanhPoly4) weights([&](uint64_t v) { return cap_score2<kTanhPoly4>(p.cap, v, nm2); });
                 else weights([&](uint64_t v) { return cap_score2<kTanhExp>(p.cap, v, nm2); });
             } else {
                 weights([&](uint64_t v) { return SCALED ? fadd2(v, nm2) : ffma2(v, c2, nm2); });

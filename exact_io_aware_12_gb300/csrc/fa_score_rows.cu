@@ -292,7 +292,7 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 #pragma unroll
                     for (int i = 0; i < 16; ++i) one(how, general_, i);
                 };
-                using Poly5 = std::integral_constant<int, kTanhPoly5>;
+                using Poly4 = std::integral_constant<int, kTanhPoly4>;
                 using Exp = std::integral_constant<int, kTanhExp>;
                 if constexpr (CAP) {
                     float mx0 = 0.f, mx1 = 0.f;
@@ -304,10 +304,10 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                     // (the few tiles at the edges: two forms)
                     const float mx = fmaxf(mx0, mx1) * p.cap.k;
                     const bool near = !__any_sync(0xffffffffu, !(mx <= kTanhNear)), mid = !__any_sync(0xffffffffu, !(mx <= kTanhMid));
-                    if (general && mid) all(Poly5{}, std::true_type{});
+                    if (general && mid) all(Poly4{}, std::true_type{});
                     else if (general) all(Exp{}, std::true_type{});
                     else if (near) all(std::integral_constant<int, kTanhPoly3>{}, std::false_type{});
-                    else if (mid) all(Poly5{}, std::false_type{});
+                    else if (mid) all(Poly4{}, std::false_type{});
                     else all(Exp{}, std::false_type{});
                 } else if (general) {
                     all(Exp{}, std::true_type{});
