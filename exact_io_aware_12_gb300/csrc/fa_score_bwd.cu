@@ -763,15 +763,16 @@ __global__ void __launch_bounds__(256) fa_score_post_kernel(const float* acc, __
 struct TableGradParams {
     const float* near_part;
     const float* far_part;
-    float* red;       // [near_n][H][num_buckets] sums per bucket; then [H][2] of the far parts
+    float* red;       // [near_n kParts][H][num_buckets] sums per bucket; then [H][2] of the far parts
     const int* buckets;
     void* out;        // [num_buckets][H]
     int B, H, n_kv, near_lo, near_n, far_warps, far, num_buckets, out_f32;
 };
 
-// Block (x, head): x < near_n adds the diagonals of all tile pairs at offset near_lo + x, over the
-// batch and the key tiles in order, and then, bucket by bucket, the diagonals of each; x = near_n
-// adds the far parts.
+// Block (x, head): x < near_n kParts adds the diagonals of the tile pairs at offset near_lo + x / kParts, of a part of
+// the batch and the key tiles, in order, and then, bucket by bucket, the diagonals of each; the last
+// block adds the far parts.  (One block for all of an offset's tiles read 256 KB by itself, 24 us.)
+constexpr int kParts = 8;
 __global__ void __launch_bounds__(1024) fa_score_buckets_kernel(const TableGradParams p) {
     __shared__ float val[kNearFloats];
     __shared__ int of[kNearFloats];
@@ -779,7 +780,7 @@ __global__ void __launch_bounds__(1024) fa_score_buckets_kernel(const TableGradP
     griddep_wait();
     const int x = static_cast<int>(blockIdx.x), h = static_cast<int>(blockIdx.y);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-    if (x == p.near_n) {
+    if (x == p.near_n * kParts) {
         const long long parts = static_cast<long long>(p.n_kv) * p.far_warps;
         float sum = 0.f;
         for (int b = 0; b < p.B; ++b) {
@@ -792,17 +793,23 @@ __global__ void __launch_bounds__(1024) fa_score_buckets_kernel(const TableGradP
             float s = 0.f;
             for (int i = lane; i < 512; i += 32) s += val[2 * i + warp];
             s = warp_sum(s);
-            if (lane == 0) p.red[static_cast<long long>(p.near_n) * p.H * p.num_buckets + h * 2 + warp] = s;
+            if (lane == 0) p.red[static_cast<long long>(p.near_n) * kParts * p.H * p.num_buckets + h * 2 + warp] = s;
         }
         return;
     }
-    const int off = p.near_lo + x;  // query tile - key tile
-    const int k0 = max(0, -off), k1 = min(p.n_kv, p.n_kv - off);
+    const int off = p.near_lo + x / kParts;  // query tile - key tile
+    const int k0 = max(0, -off), nk = min(p.n_kv, p.n_kv - off) - k0;  // key tiles of each sequence
+    const long long all = static_cast<long long>(p.B) * nk;
+    const int i0 = static_cast<int>(all * (x % kParts) / kParts), i1 = static_cast<int>(all * (x % kParts + 1) / kParts);
     float sum = 0.f;
-    for (int b = 0; b < p.B; ++b) {
-        const long long at = (static_cast<long long>(b) * p.H + h) * p.n_kv;
+    int b = nk > 0 ? i0 / nk : 0, k = i0 - b * nk;
 #pragma unroll 8
-        for (int k = k0; k < k1; ++k) sum += p.near_part[((at + k) * p.near_n + x) * kNearFloats + t];
+    for (int i = i0; i < i1; ++i) {
+        sum += p.near_part[(((static_cast<long long>(b) * p.H + h) * p.n_kv + k + k0) * p.near_n + x / kParts) * kNearFloats + t];
+        if (++k == nk) {
+            k = 0;
+            ++b;
+        }
     }
     const int blk = t >> 6, m = t & 63;
     const int dist = off * 128 + 32 * (blk / 4 - blk % 4) + (m < 32 ? m : m - 64);
@@ -826,11 +833,13 @@ __global__ void __launch_bounds__(256) fa_score_table_kernel(const TableGradPara
     const int h = static_cast<int>(blockIdx.x), nb = p.num_buckets;
     const long long step = static_cast<long long>(p.H) * nb;
     const float* red = p.red + static_cast<long long>(h) * nb;
-    const float* far = p.red + p.near_n * step + h * 2;  // far keys behind the query's tiles, and before
+    const int parts = p.near_n * kParts;
+    const float* far = p.red + parts * step + h * 2;  // far keys behind the query's tiles, and before
     const int low = p.buckets[0], high = p.buckets[2 * p.far];
     for (int e = threadIdx.x; e < nb; e += 256) {
         float s = 0.f;
-        for (int x = 0; x < p.near_n; ++x) s += red[x * step + e];
+#pragma unroll 8
+        for (int x = 0; x < parts; ++x) s += red[x * step + e];
         if (e == low) s += far[0];
         if (e == high) s += far[1];
         s *= kUnliftP;
@@ -865,7 +874,7 @@ BwdPlan plan_of(const ScoreArgs& a) {
     pl.near = pl.bias2 + up(static_cast<size_t>(a.H) * (2 * a.mod.far + 1) * sizeof(float));
     pl.far = pl.near + tiles * pl.near_n * kNearFloats * sizeof(float);
     pl.red = pl.far + up(tiles * pl.warps * kFarFloats * sizeof(float));
-    pl.bytes = pl.red + up((static_cast<size_t>(pl.near_n) * a.H * a.mod.num_buckets + a.H * 2) * sizeof(float));
+    pl.bytes = pl.red + up((static_cast<size_t>(pl.near_n) * kParts * a.H * a.mod.num_buckets + a.H * 2) * sizeof(float));
     return pl;
 }
 
@@ -984,7 +993,7 @@ cudaError_t launch_score_bwd(const ScoreArgs& a, cudaStream_t stream) {
     t.far = a.mod.far;
     t.num_buckets = a.mod.num_buckets;
     t.out_f32 = a.mod.table_f32;
-    e = launch_dependent(fa_score_buckets_kernel, dim3(static_cast<unsigned>(t.near_n + 1), static_cast<unsigned>(t.H)), dim3(1024),
+    e = launch_dependent(fa_score_buckets_kernel, dim3(static_cast<unsigned>(t.near_n * kParts + 1), static_cast<unsigned>(t.H)), dim3(1024),
                          0, stream, t);
     if (e != cudaSuccess) return e;
     return launch_dependent(fa_score_table_kernel, dim3(static_cast<unsigned>(t.H)), dim3(256), 0, stream, t);

@@ -38,9 +38,13 @@
 namespace fa {
 namespace {
 
+constexpr int kSms = 152;  // of a GB300
 constexpr int kBM = 128, kBN = 128;
-constexpr int kThreads = 192;
-constexpr int kProducerWarp = 4, kMmaWarp = 5;
+// Softmax warpgroups: one (a thread per row), with two CTAs to an SM; or two (two threads per row, half of a
+// block's keys each), with one, where there are at most two CTAs for each SM, and the chain of steps of the longest
+// sets the time (16 heads, d = 64: 901 tokens with slopes 15.0 us by one and 12.6 by two, 2000
+// capped 41.3 and 30.9, 4096 capped 84 and 108).
+constexpr int threads_for(int wgs) { return 128 * wgs + 64; }
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kCapExact = 1024.f;        // log2 units: 2^-24 of it is 6e-5 of a score
@@ -81,9 +85,10 @@ struct ScoreFwdShared {
     uint64_t kv_empty[4];
     uint64_t s_full, s_free, p_ready, o_done;
     __align__(16) float ramp[2][128];  // slopes: +-slope log2(e) times the column
+    float top[2][2][128];  // two warpgroups: [block's parity][warpgroup][row], largest score
+    float sum[2][2][128];  // [l, l_mma][warpgroup][row], at the end
     uint32_t tmem_base;
     int abort_flag;
-    int how;  // the farthest form of the tanh that a tile has needed
 };
 
 enum : uint32_t {
@@ -103,11 +108,11 @@ __device__ __forceinline__ ulonglong2 lds_2x64(uint32_t a) {
     return v;
 }
 
-// The 128 scores of a row, in registers, two at a time: f(column, pair) -> pair.
-template <typename F>
-__device__ __forceinline__ void each_pair(uint32_t (&s)[4][32], F&& f) {
+// A thread's scores, in registers, two at a time: f(column, pair) -> pair.
+template <int N, typename F>
+__device__ __forceinline__ void each_pair(uint32_t (&s)[N][32], F&& f) {
 #pragma unroll
-    for (int c = 0; c < 128; c += 2) {
+    for (int c = 0; c < 32 * N; c += 2) {
         uint32_t &a = s[c >> 5][c & 31], &b = s[c >> 5][(c & 31) + 1];
         const float2 y = f2_unpack(f(c, f2_pack(u2f(a), u2f(b))));
         a = f2u(y.x);
@@ -115,13 +120,15 @@ __device__ __forceinline__ void each_pair(uint32_t (&s)[4][32], F&& f) {
     }
 }
 
-template <int D, bool CAP, int BIAS>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int D, bool CAP, int BIAS, int WGS>
+__global__ void __launch_bounds__(threads_for(WGS), WGS == 1 ? 2 : 1)
 fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                     const ScoreFwdParams p) {
     using L = ScoreFwdLayout<D>;
     constexpr bool PIPE = L::kPipe;
+    constexpr int kProducerWarp = 4 * WGS, kMmaWarp = 4 * WGS + 1;
+    constexpr int kSoftmax = 128 * WGS, kCols = 128 / WGS, kParts = kCols / 32;  // threads; keys of a block per thread
     extern __shared__ uint8_t smem_raw[];
     __shared__ ScoreFwdShared sh;
     const uint32_t raw = smem_addr(smem_raw);
@@ -144,15 +151,14 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     const uint32_t bar_o = smem_addr(&sh.o_done);
     if (threadIdx.x == 0) {
         sh.abort_flag = 0;
-        sh.how = 0;
         mbar_init(bar_q, 1);
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(bar_kvf + 8 * s, 1);
             mbar_init(bar_kve + 8 * s, 1);
         }
         mbar_init(bar_s, 1);
-        mbar_init(bar_sf, 128);
-        mbar_init(bar_p, 128);
+        mbar_init(bar_sf, kSoftmax);
+        mbar_init(bar_p, kSoftmax);
         mbar_init(bar_o, 1);
         mbar_init_fence();
     }
@@ -230,7 +236,7 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             else mma_ts_warp<0>(tO, tP, vlo0 + slot * kSlot, kDescHi, id_pv);
 #pragma unroll
             for (int k = 1; k < kBN / 16; ++k)
-                mma_ts_warp<1>(tO, tP + k * 8, vlo0 + slot * kSlot + ((k * 2048) >> 4), kDescHi, id_pv);
+                mma_ts_warp<1>(tO, tP + (PIPE || WGS == 1 ? k * 8 : (k / 4) * kCols + (k % 4) * 8), vlo0 + slot * kSlot + ((k * 2048) >> 4), kDescHi, id_pv);
             mma_commit_warp(bar_o);
             mma_commit_warp(bar_kve + 8 * slot);
         };
@@ -261,11 +267,13 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         __syncwarp();
     } else {
         // ------------------------------------------------------------- softmax --
-        const int r = threadIdx.x & 127;
+        // A failed wait poisons the rest (ok = false); two warpgroups agree on it at the block's barrier, which every
+        // warp reaches.
+        const int wg = WGS == 1 ? 0 : warp >> 2, r = threadIdx.x & 127;
         const int row = q_start + r;
-        const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t tS = tmem + lane_off + L::kTmS, tO = tmem + lane_off + L::kTmO;
-        const uint32_t tP = tmem + lane_off + L::kTmP;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t tS = lanes + L::kTmS + kCols * wg, tO = lanes + L::kTmO + D / WGS * wg;
+        const uint32_t tP = lanes + L::kTmP + (PIPE ? kCols / 2 : kCols) * wg;  // (d = 128: over this thread's S)
         const float sl2 = p.scale_log2;
         const uint64_t c2 = f2_pack(sl2, sl2);
         const ScoreRange mine = keys_of(p.mask, b, min(row, N - 1), prefix);
@@ -275,139 +283,144 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             slope2 = p.slopes[h] * kLog2e;
             sh.ramp[0][r] = slope2 * r;
             sh.ramp[1][r] = -slope2 * r;
-            named_bar_sync(1, 128);
+            named_bar_sync(1, kSoftmax);
         }
         if constexpr (BIAS == kBiasTable) {
-            for (int i = r; i <= 2 * p.far; i += 128)
+            for (int i = threadIdx.x; i <= 2 * p.far; i += kSoftmax)
                 bias_s[i] = kLog2e * table_bias(p.table, p.table_f32, p.buckets, p.num_buckets, p.H, h, i);
-            named_bar_sync(1, 128);
+            named_bar_sync(1, kSoftmax);
         }
         constexpr bool SCALED = CAP || BIAS != kBiasNone;  // y in log2 units before the max is taken
         float m_used = -INFINITY;
         float l = 0.f, l_mma = 0.f;
+        [[maybe_unused]] int most = kTanhPoly3;  // CAP: the farthest form of the tanh so far
         bool ok = true;
         for (int j = 0; j < nb; ++j) {
-            if (!__all_sync(0xffffffffu, mbar_wait(bar_s, j & 1, wd, kSiteSoftS))) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            uint32_t s[4][32];
-            tmem_ld32(tS + 0, s[0]);
-            tmem_ld32(tS + 32, s[1]);
-            tmem_ld32(tS + 64, s[2]);
-            tmem_ld32(tS + 96, s[3]);
-            tmem_ld_wait(s[0]);
-            tmem_ld_wait(s[1]);
-            tmem_ld_wait(s[2]);
-            tmem_ld_wait(s[3]);
-            if constexpr (PIPE) {
-                tc_fence_before();
-                mbar_arrive(bar_sf);  // S's columns may take the next block's scores now
-            }
-            const int kbase = (jlo + j) * kBN;
-            const bool masked = kbase < clear_lo || kbase + kBN > clear_hi;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_s, j & 1, wd, kSiteSoftS));
+            if (WGS == 1 && !ok) break;
+            uint32_t s[kParts][32];
+            const int kb0 = (jlo + j) * kBN, kbase = kb0 + kCols * wg;
+            const bool masked = kb0 < clear_lo || kb0 + kBN > clear_hi;
             [[maybe_unused]] int how = kTanhExp;  // CAP: form of the tanh
             [[maybe_unused]] bool late = false;   // CAP: the cap is yet to come
             [[maybe_unused]] float base = 0.f;    // slopes: what the scores below lack, the same for the row
             float m_cand = -INFINITY;
-            if constexpr (CAP) {
-                float hi0 = -INFINITY, hi1 = -INFINITY, lo0 = INFINITY, lo1 = INFINITY;
+            if (ok) {
+                tc_fence_after();
 #pragma unroll
-                for (int g = 0; g < 4; ++g)
+                for (int g = 0; g < kParts; ++g) tmem_ld32(tS + 32 * g, s[g]);
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        hi0 = fmax3(hi0, u2f(s[g][c]), u2f(s[g][c + 1]));
-                        hi1 = fmax3(hi1, u2f(s[g][c + 2]), u2f(s[g][c + 3]));
-                        lo0 = fmin3(lo0, u2f(s[g][c]), u2f(s[g][c + 1]));
-                        lo1 = fmin3(lo1, u2f(s[g][c + 2]), u2f(s[g][c + 3]));
-                    }
-                const float hi = fmaxf(hi0, hi1);
-                const float mx = fmaxf(hi, -fminf(lo0, lo1)) * p.cap.k;  // of the warp's rows: the tanh's form
-                how = !__any_sync(0xffffffffu, !(mx <= kTanhNear))  ? kTanhPoly3
-                      : !__any_sync(0xffffffffu, !(mx <= kTanhMid)) ? kTanhPoly4
-                                                                    : kTanhExp;
-                // (once one of the CTA's tiles has needed a farther form, all take it: warps that go to and
-                // fro between the forms wait for instructions, 292 -> 351 us where a third of the tiles passed a bound.
-                // The last form's error is 2^-24 of the cap, whatever the score: not where caps are in the thousands.)
-                const int most = *const_cast<volatile int*>(&sh.how);
-                if (how > most) *const_cast<volatile int*>(&sh.how) = how;
-                else if (most == kTanhPoly4 || p.cap.cap2 <= kCapExact) how = most;
-                if (BIAS == kBiasNone && !masked) {
-                    late = true;
-                    const uint64_t v = f2_pack(hi, hi);
-                    m_cand = f2_unpack(how == kTanhPoly3   ? cap_score2<kTanhPoly3>(p.cap, v, 0)
-                                       : how == kTanhPoly4 ? cap_score2<kTanhPoly4>(p.cap, v, 0)
-                                                           : cap_score2<kTanhExp>(p.cap, v, 0)).x;
-                } else if (how == kTanhPoly3) {
-                    each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhPoly3>(p.cap, v, 0); });
-                } else if (how == kTanhPoly4) {
-                    each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhPoly4>(p.cap, v, 0); });
-                } else {
-                    each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhExp>(p.cap, v, 0); });
+                for (int g = 0; g < kParts; ++g) tmem_ld_wait(s[g]);
+                if constexpr (PIPE) {
+                    tc_fence_before();
+                    mbar_arrive(bar_sf);  // S's columns may take the next block's scores now
                 }
-            }
-            if constexpr (BIAS == kBiasSlopes) {
-                const float d0 = static_cast<float>(kbase - row);  // j - i at column 0, exact below 2^24
-                const int side = far_side(q_start, kbase, kBM, 0);
-                if (side != 0) {
-                    // all keys before (or behind) all queries: y - slope |i - j| with the sign in the slope
-                    base = side * slope2 * d0;
-                    const uint32_t ramp = smem_addr(sh.ramp[side < 0]);
+                if constexpr (CAP) {
+                    float hi0 = -INFINITY, hi1 = -INFINITY, lo0 = INFINITY, lo1 = INFINITY;
 #pragma unroll
-                    for (int c = 0; c < 128; c += 4) {
-                        const ulonglong2 w = lds_2x64(ramp + 4 * c);
+                    for (int g = 0; g < kParts; ++g)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            uint32_t &a = s[c >> 5][(c & 31) + 2 * e], &bb = s[c >> 5][(c & 31) + 2 * e + 1];
-                            const uint64_t v = f2_pack(u2f(a), u2f(bb)), add = e ? w.y : w.x;
-                            const float2 y = f2_unpack(CAP ? fadd2(v, add) : ffma2(v, c2, add));
-                            a = f2u(y.x);
-                            bb = f2u(y.y);
+                        for (int c = 0; c < 32; c += 4) {
+                            hi0 = fmax3(hi0, u2f(s[g][c]), u2f(s[g][c + 1]));
+                            hi1 = fmax3(hi1, u2f(s[g][c + 2]), u2f(s[g][c + 3]));
+                            lo0 = fmin3(lo0, u2f(s[g][c]), u2f(s[g][c + 1]));
+                            lo1 = fmin3(lo1, u2f(s[g][c + 2]), u2f(s[g][c + 3]));
                         }
+                    const float hi = fmaxf(hi0, hi1);
+                    const float mx = fmaxf(hi, -fminf(lo0, lo1)) * p.cap.k;  // of the warp's rows: the tanh's form
+                    how = !__any_sync(0xffffffffu, !(mx <= kTanhNear))  ? kTanhPoly3
+                          : !__any_sync(0xffffffffu, !(mx <= kTanhMid)) ? kTanhPoly4
+                                                                        : kTanhExp;
+                    // (once one of a warp's blocks has needed a farther form, those behind it take it, too: warps that go
+                    // to and fro between the forms wait for instructions, 292 -> 351 us where a third of the blocks
+                    // passed a bound.  The last form's error is 2^-24 of the cap, whatever the score: not where caps are
+                    // in the thousands.)
+                    if (how > most) most = how;
+                    else if (most == kTanhPoly4 || p.cap.cap2 <= kCapExact) how = most;
+                    if (BIAS == kBiasNone && !masked) {
+                        late = true;
+                        const uint64_t v = f2_pack(hi, hi);
+                        m_cand = f2_unpack(how == kTanhPoly3   ? cap_score2<kTanhPoly3>(p.cap, v, 0)
+                                           : how == kTanhPoly4 ? cap_score2<kTanhPoly4>(p.cap, v, 0)
+                                                               : cap_score2<kTanhExp>(p.cap, v, 0)).x;
+                    } else if (how == kTanhPoly3) {
+                        each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhPoly3>(p.cap, v, 0); });
+                    } else if (how == kTanhPoly4) {
+                        each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhPoly4>(p.cap, v, 0); });
+                    } else {
+                        each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhExp>(p.cap, v, 0); });
                     }
-                } else {
-                    each_pair(s, [&](int c, uint64_t v) {
-                        float2 y = f2_unpack(CAP ? v : fmul2(v, c2));
-                        y.x = fmaf(-slope2, fabsf(d0 + c), y.x);
-                        y.y = fmaf(-slope2, fabsf(d0 + c + 1), y.y);
-                        return f2_pack(y.x, y.y);
-                    });
                 }
-            }
-            if constexpr (BIAS == kBiasTable) {
-                const int side = far_side(q_start, kbase, kBM, p.far);
-                if (side != 0) {
-                    const float bf = bias_s[side > 0 ? 2 * p.far : 0];
-                    const uint64_t b2 = f2_pack(bf, bf);
-                    each_pair(s, [&](int, uint64_t v) { return CAP ? fadd2(v, b2) : ffma2(v, c2, b2); });
-                } else {
-                    const int i0 = row - kbase + p.far, top_i = 2 * p.far;
-                    each_pair(s, [&](int c, uint64_t v) {
-                        const uint64_t b2 = f2_pack(bias_s[max(0, min(top_i, i0 - c))], bias_s[max(0, min(top_i, i0 - c - 1))]);
-                        return CAP ? fadd2(v, b2) : ffma2(v, c2, b2);
-                    });
-                }
-            }
-            if (masked) {
-                const int from = mine.lo - kbase;
-                const uint32_t n = static_cast<uint32_t>(mine.hi - mine.lo);
+                if constexpr (BIAS == kBiasSlopes) {
+                    const float d0 = static_cast<float>(kbase - row);  // j - i at column 0, exact below 2^24
+                    const int side = far_side(q_start, kb0, kBM, 0);
+                    if (side != 0) {
+                        // all keys before (or behind) all queries: y - slope |i - j| with the sign in the slope
+                        base = side * slope2 * d0;
+                        const uint32_t ramp = smem_addr(sh.ramp[side < 0]);
 #pragma unroll
-                for (int c = 0; c < 128; ++c)
-                    if (static_cast<uint32_t>(c - from) >= n) s[c >> 5][c & 31] = f2u(-INFINITY);
-            }
-            if (!late) {
-                float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
+                        for (int c = 0; c < kCols; c += 4) {
+                            const ulonglong2 w = lds_2x64(ramp + 4 * c);
 #pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                    mx0 = fmax3(mx0, u2f(s[0][c]), u2f(s[0][c + 1]));
-                    mx1 = fmax3(mx1, u2f(s[1][c]), u2f(s[1][c + 1]));
-                    mx2 = fmax3(mx2, u2f(s[2][c]), u2f(s[2][c + 1]));
-                    mx3 = fmax3(mx3, u2f(s[3][c]), u2f(s[3][c + 1]));
+                            for (int e = 0; e < 2; ++e) {
+                                uint32_t &a = s[c >> 5][(c & 31) + 2 * e], &bb = s[c >> 5][(c & 31) + 2 * e + 1];
+                                const uint64_t v = f2_pack(u2f(a), u2f(bb)), add = e ? w.y : w.x;
+                                const float2 y = f2_unpack(CAP ? fadd2(v, add) : ffma2(v, c2, add));
+                                a = f2u(y.x);
+                                bb = f2u(y.y);
+                            }
+                        }
+                    } else {
+                        each_pair(s, [&](int c, uint64_t v) {
+                            float2 y = f2_unpack(CAP ? v : fmul2(v, c2));
+                            y.x = fmaf(-slope2, fabsf(d0 + c), y.x);
+                            y.y = fmaf(-slope2, fabsf(d0 + c + 1), y.y);
+                            return f2_pack(y.x, y.y);
+                        });
+                    }
                 }
-                m_cand = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3));
-                if constexpr (!SCALED) m_cand *= sl2;
-                if constexpr (BIAS == kBiasSlopes) m_cand += base;
+                if constexpr (BIAS == kBiasTable) {
+                    const int side = far_side(q_start, kb0, kBM, p.far);
+                    if (side != 0) {
+                        const float bf = bias_s[side > 0 ? 2 * p.far : 0];
+                        const uint64_t b2 = f2_pack(bf, bf);
+                        each_pair(s, [&](int, uint64_t v) { return CAP ? fadd2(v, b2) : ffma2(v, c2, b2); });
+                    } else {
+                        const int i0 = row - kbase + p.far, top_i = 2 * p.far;
+                        each_pair(s, [&](int c, uint64_t v) {
+                            const uint64_t b2 = f2_pack(bias_s[max(0, min(top_i, i0 - c))], bias_s[max(0, min(top_i, i0 - c - 1))]);
+                            return CAP ? fadd2(v, b2) : ffma2(v, c2, b2);
+                        });
+                    }
+                }
+                if (masked) {
+                    const int from = mine.lo - kbase;
+                    const uint32_t n = static_cast<uint32_t>(mine.hi - mine.lo);
+#pragma unroll
+                    for (int c = 0; c < kCols; ++c)
+                        if (static_cast<uint32_t>(c - from) >= n) s[c >> 5][c & 31] = f2u(-INFINITY);
+                }
+                if (!late) {
+                    float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+                    for (int g = 0; g < kParts; ++g)
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            mx0 = fmax3(mx0, u2f(s[g][c]), u2f(s[g][c + 1]));
+                            mx1 = fmax3(mx1, u2f(s[g][c + 2]), u2f(s[g][c + 3]));
+                        }
+                    m_cand = fmaxf(mx0, mx1);
+                    if constexpr (!SCALED) m_cand *= sl2;
+                    if constexpr (BIAS == kBiasSlopes) m_cand += base;
+                }
+            }
+            if constexpr (WGS == 2) {
+                sh.top[j & 1][wg][r] = m_cand;
+                if (named_bar_or(1, kSoftmax, !ok)) {
+                    ok = false;
+                    break;
+                }
+                m_cand = fmaxf(m_cand, sh.top[j & 1][wg ^ 1][r]);
             }
             const bool grow = m_cand > m_used + kRescaleThreshold;
             float alpha = 1.f;
@@ -423,18 +436,16 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             const uint64_t nm2 = f2_pack(neg_m, neg_m);
             uint64_t ls2 = 0;
             float lr0 = 0.f, lr1 = 0.f;
-            constexpr int kPC = D == 128 ? 16 : 32;  // packed columns per tensor-memory store
+            constexpr int kPC = D == 128 || WGS == 2 ? 16 : 32;  // packed columns per tensor-memory store
             if (PIPE && j > 0) {
                 // P's columns are free once the previous P V has read them
-                if (!__all_sync(0xffffffffu, mbar_wait(bar_o, (j - 1) & 1, wd, kSiteSoftO))) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(0xffffffffu, mbar_wait(bar_o, (j - 1) & 1, wd, kSiteSoftO));
+                if (!ok && WGS == 1) break;
                 tc_fence_after();
             }
             const auto weights = [&](auto&& exponent) {  // of a pair
 #pragma unroll
-                for (int hh = 0; hh < 64 / kPC; ++hh) {
+                for (int hh = 0; hh < kCols / 2 / kPC; ++hh) {
                     uint32_t pk[kPC];
 #pragma unroll
                     for (int i = 0; i < kPC; ++i) {
@@ -449,7 +460,8 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                     else tmem_st32(tP + hh * 32, pk);
                 }
             };
-            if (CAP && late) {
+            if (!ok) {
+            } else if (CAP && late) {
                 if (how == kTanhPoly3) weights([&](uint64_t v) { return cap_score2<kTanhPoly3>(p.cap, v, nm2); });
                 else if (how == kTanhPoly4) weights([&](uint64_t v) { return cap_score2<kTanhPoly4>(p.cap, v, nm2); });
                 else weights([&](uint64_t v) { return cap_score2<kTanhExp>(p.cap, v, nm2); });
@@ -459,54 +471,64 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             const float2 a2 = f2_unpack(ls2);
             l += a2.x + a2.y;
             l_mma += lr0 + lr1;
-            if (j > 0 && __any_sync(0xffffffffu, grow)) {
-                // rescale this warp's rows of O once the previous P V has landed
-                if (!__all_sync(0xffffffffu, mbar_wait(bar_o, (j - 1) & 1, wd, kSiteSoftO))) {
-                    ok = false;
-                    break;
-                }
+            if (ok && j > 0 && __any_sync(0xffffffffu, grow)) {
+                // rescale this thread's part of O once the previous P V has landed
+                ok = __all_sync(0xffffffffu, mbar_wait(bar_o, (j - 1) & 1, wd, kSiteSoftO));
+                if (!ok && WGS == 1) break;
                 tc_fence_after();
+                if (ok) {
 #pragma unroll
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    uint32_t o[32];
-                    tmem_ld32(tO + c0, o);
-                    tmem_ld_wait(o);
+                    for (int c0 = 0; c0 < D / WGS; c0 += 32) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + c0, o);
+                        tmem_ld_wait(o);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * alpha);
-                    tmem_st32(tO + c0, o);
+                        for (int i = 0; i < 32; ++i) o[i] = f2u(u2f(o[i]) * alpha);
+                        tmem_st32(tO + c0, o);
+                    }
                 }
             }
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(bar_p);
+            if (ok) {
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(bar_p);
+            }
         }
         // ----------------------------------------------------------- epilogue --
         // O / l_mma -> bf16, staged over Q (every S has read it), one TMA store
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_o, (nb - 1) & 1, wd, kSiteEpi));
+        if constexpr (WGS == 2) {
+            sh.sum[0][wg][r] = l;
+            sh.sum[1][wg][r] = l_mma;
+            ok = !named_bar_or(1, kSoftmax, !ok);
+            l += sh.sum[0][wg ^ 1][r];
+            l_mma += sh.sum[1][wg ^ 1][r];
+        }
         if (ok) {
             tc_fence_after();
             const float inv_l = l_mma > 0.f ? 1.f / l_mma : 0.f;
 #pragma unroll
-            for (int c0 = 0; c0 < D; c0 += 32) {
+            for (int c0 = 0; c0 < D / WGS; c0 += 32) {
                 uint32_t o[32];
                 tmem_ld32(tO + c0, o);
                 tmem_ld_wait(o);
+                const int col = D / WGS * wg + c0;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int chunk = (c0 % 64) / 8 + q;
+                    const int chunk = (col % 64) / 8 + q;
                     uint4 v;
                     v.x = pack_bf16(u2f(o[8 * q + 0]) * inv_l, u2f(o[8 * q + 1]) * inv_l);
                     v.y = pack_bf16(u2f(o[8 * q + 2]) * inv_l, u2f(o[8 * q + 3]) * inv_l);
                     v.z = pack_bf16(u2f(o[8 * q + 4]) * inv_l, u2f(o[8 * q + 5]) * inv_l);
                     v.w = pack_bf16(u2f(o[8 * q + 6]) * inv_l, u2f(o[8 * q + 7]) * inv_l);
-                    *reinterpret_cast<uint4*>(smem + (c0 / 64) * L::kBox + r * 128 + ((chunk ^ (r & 7)) << 4)) = v;
+                    *reinterpret_cast<uint4*>(smem + (col / 64) * L::kBox + r * 128 + ((chunk ^ (r & 7)) << 4)) = v;
                 }
             }
             fence_async_shared();
-            if (row < N) p.LSE[static_cast<int64_t>(bh) * N + row] = (m_used + __log2f(l)) * kLn2;
+            if (wg == 0 && row < N) p.LSE[static_cast<int64_t>(bh) * N + row] = (m_used + __log2f(l)) * kLn2;
         }
-        // (all four warps reach this barrier, also after a failed wait, and agree)
-        if (!named_bar_or(1, 128, !ok) && r == 0) {
+        // (every warp reaches this barrier, also after a failed wait, and all agree)
+        if (!named_bar_or(1, kSoftmax, !ok) && threadIdx.x == 0) {
             for (int x = 0; x < L::kBoxes; ++x) tma_store_3d(&tmO, sbase + x * L::kBox, x * 64, q_start, bh);
             bulk_commit();
             bulk_wait_read<0>();
@@ -523,8 +545,8 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     }
 }
 
-template <int D, bool CAP, int BIAS>
-cudaError_t launch_t(const ScoreArgs& a, cudaStream_t stream) {
+template <int D, bool CAP, int BIAS, int WGS>
+cudaError_t launch_w(const ScoreArgs& a, cudaStream_t stream) {
     using L = ScoreFwdLayout<D>;
     CUtensorMap tq, tk, tv, to;
     const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -532,7 +554,7 @@ cudaError_t launch_t(const ScoreArgs& a, cudaStream_t stream) {
     if (!make_tile_map(&tq, a.Q, BF, 2, D, a.N, BH, 64, kBM) || !make_tile_map(&tk, a.K, BF, 2, D, a.N, BHkv, 64, kBN) ||
         !make_tile_map(&tv, a.V, BF, 2, D, a.N, BHkv, 64, kBN) || !make_tile_map(&to, a.O, BF, 2, D, a.N, BH, 64, kBM))
         return cudaErrorInvalidValue;
-    constexpr auto kern = &fa_score_fwd_kernel<D, CAP, BIAS>;
+    constexpr auto kern = &fa_score_fwd_kernel<D, CAP, BIAS, WGS>;
     // (the limit is set for the largest table, so that it is set once)
     constexpr int kTableMax = BIAS == kBiasTable ? (2 * kScoreMaxFar + 1) * 4 : 0;
     cudaError_t e = set_max_dyn_smem_once<kern>(L::kDynSmem + kTableMax);
@@ -560,10 +582,16 @@ cudaError_t launch_t(const ScoreArgs& a, cudaStream_t stream) {
     p.err = a.err;
     p.wait_limit_ns = a.wait_limit_ns;
     if (a.ev_start) cudaEventRecord(a.ev_start, stream);
-    e = launch_dependent(kern, dim3(static_cast<unsigned>(BH), static_cast<unsigned>(p.n_q)), dim3(kThreads),
+    e = launch_dependent(kern, dim3(static_cast<unsigned>(BH), static_cast<unsigned>(p.n_q)), dim3(threads_for(WGS)),
                          static_cast<size_t>(bytes), stream, tq, tk, tv, to, p);
     if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
     return e;
+}
+
+template <int D, bool CAP, int BIAS>
+cudaError_t launch_t(const ScoreArgs& a, cudaStream_t stream) {
+    const long long ctas = static_cast<long long>(a.B) * a.H * ((a.N + kBM - 1) / kBM);
+    return ctas <= 2 * kSms ? launch_w<D, CAP, BIAS, 2>(a, stream) : launch_w<D, CAP, BIAS, 1>(a, stream);
 }
 
 template <int D>
