@@ -270,6 +270,72 @@ def test_bias_gradient_is_as_exact_at_length(causal):
     assert off <= 1.25 * e.s_dbias and off <= 2.0 ** -10 * float(e.dbias.norm())
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kw", [
+    dict(prefix=True), dict(softcap=50.0), dict(softcap=3.0), dict(slopes=True, docs=True), dict(softcap=6.0, slopes=True),
+    dict(table=(32, 128, False)), dict(softcap=20.0, table=(32, 40, True), docs=True), dict(window=200, softcap=8.0)],
+    ids=lambda kw: "-".join(kw))
+def test_more_tiles_than_the_sms_hold(kw, d):
+    """52 heads of 6 tiles, more than two for each SM, which one softmax warpgroup per tile takes."""
+    B, H, N = 2, 26, 700
+    kw = dict(kw)
+    if kw.get("slopes"):
+        kw["slopes"] = slopes_of(H)
+    if "table" in kw:
+        nb, far, both = kw.pop("table")
+        kw.update(table_of(H, nb, far, both, 5))
+    if kw.get("docs"):
+        kw["docs"] = docs_of(B, N, 6)
+    if kw.get("prefix"):
+        kw["prefix"] = torch.tensor([N // 3, N - 1], dtype=torch.int32)
+    x = inputs(B, H, 13, N, d, N + d)
+    check(x, True, backward=False, **kw)
+    a, b = gpu(x, True, backward=False, **kw), gpu(x, True, backward=False, **kw)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("lengths", [[300, 33000, 31, 1, 700, 128, 35000, 577], [66000, 2], [65536, 65536, 500]], ids=str)
+def test_documents_of_long_sequences(lengths, causal):
+    """Runs longer than the tokens that are looked at together, across their limits and up to them, each against
+    the formula in 64 bits.  Where a row sees many keys of like weight, the 2^-8 / sqrt(3) of its
+    weights' roundings and of the result's give an O, dQ, dK and dV within sqrt(2/3) 2^-8; 1.25 as above."""
+    d, gap = 64, 70  # (padding behind each)
+    N = sum(lengths) + gap * len(lengths)
+    ids = torch.full((1, N), -1, dtype=torch.int32)
+    at = 0
+    for i, n in enumerate(lengths):
+        ids[0, at:at + n] = i % 2
+        at += n + gap
+    x = inputs(1, 1, 1, N, d, 51)
+    o, lse, (dq, dk, dv) = gpu(x, causal, docs=ids)
+    none = ids[0] < 0
+    for t in (o, dq, dk, dv):
+        assert not t[0, 0].cpu()[none].any()
+    assert bool((lse[0, 0].cpu()[none] == -math.inf).all())
+    at = 0
+    for n in lengths:
+        q, k, v, do = (x[i][0, 0, at:at + n].to(DEV).double() for i in ("q", "k", "v", "do"))
+        eo, el, eq, ek, ev = torch.empty_like(q), torch.empty_like(q[:, 0]), torch.empty_like(q), torch.zeros_like(k), torch.zeros_like(v)
+        for r in range(0, n, 4096):
+            z = slice(r, min(n, r + 4096))
+            y = q[z] @ k.T * d ** -0.5
+            if causal:
+                y.masked_fill_(torch.arange(n, device=DEV)[None, :] > torch.arange(r, z.stop, device=DEV)[:, None], -math.inf)
+            el[z] = torch.logsumexp(y, -1)
+            w = (y - el[z, None]).exp_()
+            eo[z] = w @ v
+            ev += w.T @ do[z]
+            w *= do[z] @ v.T - (do[z] * eo[z]).sum(-1, keepdim=True)
+            eq[z] = w @ k * d ** -0.5
+            ek += w.T @ q[z] * d ** -0.5
+        assert float((lse[0, 0, at:at + n] - el).abs().max()) < 1e-4
+        if n >= 64:
+            for got, want in ((o, eo), (dq, eq), (dk, ek), (dv, ev)):
+                assert rel_l2(got[0, 0, at:at + n], want) <= 1.25 * math.sqrt(2 / 3) * 2.0 ** -8
+        at += n + gap
+
+
 # --------------------------------------------------------------------- behaviour ----
 def test_without_options_it_is_plain_attention():
     """All fields 0: the forward and backward of grouped heads."""
