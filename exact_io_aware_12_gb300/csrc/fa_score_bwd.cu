@@ -20,9 +20,11 @@
 //   post      dQ = bf16(tau * accumulator)
 //   buckets, table   the bias's gradient (below), with a table
 //
-// dX enters the products as bf16, rounded once from fp32: P (1 - tanh^2) waits for dP^T as
-// fp16 of 2^15 times its value, which is off by 2^-11 of it down to 2^-29; dQ, dK, dV
-// take the factor off.
+// (d = 64: the same in fa_score_bwd64.cu, with steps that overlap.)
+//
+// dX enters the products as bf16, rounded once from fp32; where registers are short, P (1 - tanh^2) waits for
+// dP^T as fp16 of 2^15 times its value, which is off by 2^-11 of it down to 2^-29; dQ, dK, dV take
+// the factor off.
 //
 // The bias's gradient: pairs at one distance lie on a diagonal.  A tile pair all of whose
 // distances are `far` or more (most of them in a long sequence: the last bucket begins near)
@@ -35,19 +37,14 @@
 
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
-#include "fa_score.cuh"
+#include "fa_score_bwd.cuh"
 
 namespace fa {
 namespace {
 
-constexpr int kBQ = 128, kBK = 128;
-constexpr int threads_for(int nwg) { return 32 * (4 * nwg + 3); }
-constexpr float kLog2e = 1.44269504088896341f;
-constexpr float kLiftP = 15.f, kUnliftP = 0x1p-15f;
+constexpr int D = 128;
 
-template <int D>
 struct ScoreBwdLayout {
     static constexpr int kTile = kBK * D * 2;  // one bf16 [128 x D] tile
     static constexpr int kBox = 128 * 128;     // [128 rows x 64 bf16] or [128 x 32 fp32]
@@ -60,12 +57,8 @@ struct ScoreBwdLayout {
     static constexpr int kVec = kDS + 128 * 128 * 2;       // lse2[2][128], dvec[2][128]
     static constexpr int kBars = kVec + 4 * 128 * 4;
     static constexpr int kBytes = kBars + 256;
-    // tensor-memory columns: dV, dK (D each), S^T, dP^T; dQ over dP^T at d = 128, its own at 64
-    static constexpr uint32_t kTmDV = 0, kTmDK = D, kTmS = 2 * D, kTmDP = 2 * D + 128;
-    static constexpr bool kDQAliasDP = D == 128;
-    // dK's A operand: dX^T from tensor memory (beside P^T) at d = 128, from shared memory at 64
-    static constexpr bool kDSInTmem = D == 128;
-    static constexpr uint32_t kTmDQ = kDQAliasDP ? kTmDP : 2 * D + 256;
+    // tensor-memory columns; dQ over dP^T, P^T and (dK's A operand) dX^T over S^T
+    static constexpr uint32_t kTmDV = 0, kTmDK = D, kTmS = 2 * D, kTmDP = 2 * D + 128, kTmDQ = kTmDP;
 };
 
 struct ScoreBwdShared {
@@ -82,103 +75,22 @@ struct ScoreBwdShared {
     int abort_flag;
 };
 
-// The table gradient's partial sums, in the workspace.
-constexpr int kNearFloats = 1024;  // of a near tile pair: 16 blocks of 64
-constexpr int kFarFloats = 2;      // of a warp: the sum over far keys behind the query, and before it
-
-struct ScoreBwdParams {
-    const float* LSE;
-    const float* Dvec;
-    int H, H_kv, G, n_kv, head_group;
-    const int* order;  // [B][n_kv], or null: as they come
-    ScoreMask mask;
-    float scale_log2, tau;
-    float x_scale, cap_log2;
-    const float* slopes;
-    const float* bias2;  // [H][2 far + 1], log2 units
-    int far;
-    float* near_part;    // [B H][n_kv][near_n][kNearFloats], or null
-    float* far_part;     // [B H][n_kv][4 NWG][kFarFloats]
-    int near_lo, near_n;  // near tile pairs: query tile - key tile from near_lo on
-    unsigned int* err;
-    unsigned long long wait_limit_ns;
-};
-
 enum : uint32_t {
     kSiteProd = 71, kSiteMmaKV = 72, kSiteMmaQ = 73, kSiteMmaP = 74, kSiteMmaDS = 75, kSiteMmaDrain = 76,
     kSiteDsS = 77, kSiteDsQ = 78, kSiteDsDP = 79, kSiteDsDQ = 80, kSiteDrain = 81, kSiteReduce = 82
 };
 
-__device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
-
-constexpr uint32_t kDescHi = sw128_desc_hi(1024);
-constexpr uint32_t kLboMN = 128 * 128;
-
-// D = A B^T, both K-major tiles of 128 rows x Dk.
-template <int Dk>
-__device__ __forceinline__ void mma_rows_rows(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo) {
-    constexpr uint32_t id = idesc_bf16(128, 128, false, false);
-#pragma unroll
-    for (int k = 0; k < Dk / 16; ++k) {
-        const uint32_t off = ((k / 4) * (128 * 128) + (k % 4) * 32) >> 4;
-        if (k == 0) mma_ss_warp<0>(tmem_d, a_lo + off, b_lo + off, kDescHi, id);
-        else mma_ss_warp<1>(tmem_d, a_lo + off, b_lo + off, kDescHi, id);
-    }
-}
-// D (+)= A_tmem[128 x 128] B, B an MN-major tile; each warpgroup's QC columns of A lie packed over
-// the first half of its QC fp32 columns.
-template <int Dn, int QC>
-__device__ __forceinline__ void mma_tmem_a(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo, bool accumulate) {
-    constexpr uint32_t id = idesc_bf16(128, Dn, false, true);
-    if (accumulate) mma_ts_warp<1>(tmem_d, tmem_a, b_lo, kDescHi, id);
-    else mma_ts_warp<0>(tmem_d, tmem_a, b_lo, kDescHi, id);
-#pragma unroll
-    for (int k = 1; k < 128 / 16; ++k)
-        mma_ts_warp<1>(tmem_d, tmem_a + (16 * k / QC) * QC + (16 * k % QC) / 2, b_lo + ((k * 2048) >> 4), kDescHi, id);
-}
-// D (+)= A B, A a K-major tile [128 x 128], B MN-major.
-template <int Dn>
-__device__ __forceinline__ void mma_rows_mn(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo, bool accumulate) {
-    constexpr uint32_t id = idesc_bf16(128, Dn, false, true);
-    if (accumulate) mma_ss_warp<1>(tmem_d, a_lo, b_lo, kDescHi, id);
-    else mma_ss_warp<0>(tmem_d, a_lo, b_lo, kDescHi, id);
-#pragma unroll
-    for (int k = 1; k < 128 / 16; ++k)
-        mma_ss_warp<1>(tmem_d, a_lo + (((k / 4) * (128 * 128) + (k % 4) * 32) >> 4), b_lo + ((k * 2048) >> 4), kDescHi, id);
-}
-// D = A B, both MN-major.
-template <int Dn>
-__device__ __forceinline__ void mma_mn_mn(uint32_t tmem_d, uint32_t a_lo, uint32_t b_lo) {
-    constexpr uint32_t id = idesc_bf16(128, Dn, true, true);
-    mma_ss_warp<0>(tmem_d, a_lo, b_lo, kDescHi, id);
-#pragma unroll
-    for (int k = 1; k < 128 / 16; ++k) mma_ss_warp<1>(tmem_d, a_lo + ((k * 2048) >> 4), b_lo + ((k * 2048) >> 4), kDescHi, id);
-}
-
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
-
-// Elementwise warpgroups: four at d = 128 (32 query columns each); at d = 64 two, but four where the
-// elementwise work is more than the products hide.
-constexpr int warpgroups(int D, bool cap, int bias) { return D == 128 || cap || bias == kBiasTable ? 4 : 2; }
-
-template <int D, bool CAP, int BIAS>
-__global__ void __launch_bounds__(threads_for(warpgroups(D, CAP, BIAS)), 1)
+template <bool CAP, int BIAS>
+__global__ void __launch_bounds__(kThreads, 1)
 fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
                     const __grid_constant__ CUtensorMap tmdQacc, const __grid_constant__ CUtensorMap tmdK,
                     const __grid_constant__ CUtensorMap tmdV, const ScoreBwdParams p) {
-    using L = ScoreBwdLayout<D>;
-    constexpr int NWG = warpgroups(D, CAP, BIAS);  // elementwise warpgroups: a share of the query and d columns each
+    using L = ScoreBwdLayout;
     static_assert(sizeof(ScoreBwdShared) <= L::kBytes - L::kBars, "barrier block overflows its slot");
-    constexpr int kProducerWarp = 4 * NWG, kMmaWarp = 4 * NWG + 1, kReducerWarp = 4 * NWG + 2;
-    constexpr int kQC = 128 / NWG;      // query columns of P^T / dX^T per warpgroup
-    constexpr int kDC = D / NWG;        // d-columns of dQ, dK, dV per warpgroup
-    constexpr int kEW = 128 * NWG;
-    constexpr int kChunks = kQC / 32;
+    constexpr int kProducerWarp = 4 * kNWG, kMmaWarp = 4 * kNWG + 1, kReducerWarp = 4 * kNWG + 2;
+    constexpr int kDC = D / kNWG;        // d-columns of dQ, dK, dV per warpgroup
+    constexpr int kEW = 128 * kNWG;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_addr(smem);
     ScoreBwdShared& sh = *reinterpret_cast<ScoreBwdShared*>(smem + L::kBars);
@@ -350,19 +262,11 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             mma_commit_warp(bar_de + 8 * st);  // the last MMA that reads this dO
             if (!(ok = __all_sync(FULL, mbar_wait(bar_ds, s & 1, wd, kSiteMmaDS)))) break;
             tc_fence_after();
-            // d = 64: the dQ columns are reused every step
-            if (!L::kDQAliasDP && s > 0) {
-                if (!(ok = __all_sync(FULL, mbar_wait(bar_dr, (s - 1) & 1, wd, kSiteMmaDrain)))) break;
-                tc_fence_after();
-            }
             // dQ first: its drain is on the elementwise warps' path; dK and the next S^T run beside it
             mma_mn_mn<D>(tmem + L::kTmDQ, ds_mn, k_mn);                                // dQ
             mma_commit_warp(bar_dq);
-            if constexpr (L::kDSInTmem)
-                mma_tmem_a<D, kQC>(tmem + L::kTmDK, tmem + L::kTmS + kQC / 2, q_mn0 + so, s > 0);  // dK
-            else
-                mma_rows_mn<D>(tmem + L::kTmDK, ds_lo, q_mn0 + so, s > 0);
-            mma_commit_warp(bar_dk);           // d = 64: also, the dX^T tile is free again
+            mma_tmem_a<D, kQC>(tmem + L::kTmDK, tmem + L::kTmS + kQC / 2, q_mn0 + so, s > 0);  // dK
+            mma_commit_warp(bar_dk);
             mma_commit_warp(bar_qe + 8 * st);
             if (s + 1 < steps) {
                 const int st1 = (s + 1) & 1;
@@ -372,11 +276,9 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                 // S^T over P^T and dX^T, which only the MMAs above read (they run in issue order)
                 mma_rows_rows<D>(tmem + L::kTmS, k_lo, q_lo0 + so1);
                 mma_commit_warp(bar_s);
-                // d = 128: dP^T over the dQ tile, once it has been read out
-                if (L::kDQAliasDP) {
-                    if (!(ok = __all_sync(FULL, mbar_wait(bar_dr, s & 1, wd, kSiteMmaDrain)))) break;
-                    tc_fence_after();
-                }
+                // dP^T over the dQ tile, once it has been read out
+                if (!(ok = __all_sync(FULL, mbar_wait(bar_dr, s & 1, wd, kSiteMmaDrain)))) break;
+                tc_fence_after();
                 if (!(ok = __all_sync(FULL, mbar_wait(bar_df + 8 * st1, ((s + 1) >> 1) & 1, wd, kSiteMmaQ)))) break;
                 tc_fence_after();
                 mma_rows_rows<D>(tmem + L::kTmDP, v_lo, do_lo0 + so1);
@@ -417,7 +319,7 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         }
         __syncwarp();
     } else {
-        // ------------------------------------------ elementwise warpgroups 0 .. NWG - 1 --
+        // ------------------------------------------ elementwise warpgroups 0 .. kNWG - 1 --
         // A failed wait poisons the rest of the work (ok = false) but every thread still reaches every
         // barrier.
         const int hw = warp >> 2;
@@ -432,8 +334,6 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         const int kg = kvs + r;
         // the queries that see this row's key (none past a ragged end)
         const ScoreRange mine = kg < N ? queries_of(p.mask, b, kg, prefix) : ScoreRange{0, 0};
-        const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
-        [[maybe_unused]] const uint64_t k2 = f2_pack(p.x_scale, p.x_scale), cap2 = f2_pack(p.cap_log2, p.cap_log2);
         // the table gradient's sums of far pairs, kept while steps stay on one side
         [[maybe_unused]] uint64_t fsum = 0;
         [[maybe_unused]] int fside = 0;
@@ -442,7 +342,7 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             const float2 f = f2_unpack(fsum);
             const float fs = warp_sum(f.x + f.y);
             if (lane == 0)
-                p.far_part[((static_cast<long long>(bh) * p.n_kv + ikv) * (4 * NWG) + warp) * kFarFloats + (fside > 0)] = fs;
+                p.far_part[((static_cast<long long>(bh) * p.n_kv + ikv) * (4 * kNWG) + warp) * kFarFloats + (fside > 0)] = fs;
             fsum = 0;
         };
         bool ok = true;
@@ -456,7 +356,7 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             if (grad) {
                 // what no step of this head writes is zero
                 const long long at = static_cast<long long>(bh) * p.n_kv + ikv;
-                if (lane < kFarFloats) p.far_part[(at * (4 * NWG) + warp) * kFarFloats + lane] = 0.f;
+                if (lane < kFarFloats) p.far_part[(at * (4 * kNWG) + warp) * kFarFloats + lane] = 0.f;
                 __syncwarp();
                 for (int x = 0; x < p.near_n; ++x) {
                     const int qt = ikv + p.near_lo + x;
@@ -470,105 +370,28 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                 const int st = s & 1;
                 const int q_start = (first + t) * kBQ;
                 const ulonglong2* nl4 = reinterpret_cast<const ulonglong2*>(lse2_s + st * 128 + kQC * hw);
-                uint32_t keep[kChunks][16];  // P (1 - tanh^2), fp16 pairs
-                if (ok) ok = __all_sync(FULL, mbar_wait_sleep(bar_qf + 8 * st, (s >> 1) & 1, wd, kSiteDsQ));
-                if (ok) ok = __all_sync(FULL, mbar_wait_sleep(bar_s, s & 1, wd, kSiteDsS));
+                uint32_t keep[keep_regs(CAP, BIAS)];  // P (1 - tanh^2)
                 [[maybe_unused]] const int side = far_side(q_start, kvs, kBQ, BIAS == kBiasTable ? p.far : 0);
+                [[maybe_unused]] uint64_t far_bias = 0;
+                if constexpr (BIAS == kBiasTable) {
+                    if (side != 0) {
+                        const float v = bias2[side > 0 ? 2 * p.far : 0];
+                        far_bias = f2_pack(v, v);
+                    }
+                }
+                if (ok)
+                    ok = __all_sync(FULL, mbar_wait_sleep(bar_qf + 8 * st, (s >> 1) & 1, wd, kSiteDsQ) &&
+                                              mbar_wait_sleep(bar_s, s & 1, wd, kSiteDsS));
                 if (ok) {
                     tc_fence_after();
                     const int qh = q_start + kQC * hw;
                     const bool general = q_start < clear_lo || q_start + kBQ > clear_hi || (BIAS != kBiasNone && side == 0);
-                    [[maybe_unused]] const uint64_t sl = f2_pack(-side * slope2, -side * slope2);  // (of i - j)
-                    const int from = mine.lo - qh;
-                    const uint32_t seen = static_cast<uint32_t>(mine.hi - mine.lo);
-                    [[maybe_unused]] uint64_t far_bias = 0;
-                    if constexpr (BIAS == kBiasTable) {
-                        if (side != 0) {
-                            const float v = bias2[side > 0 ? 2 * p.far : 0];
-                            far_bias = f2_pack(v, v);
-                        }
-                    }
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        uint32_t sv[32], pk[16];
-                        tmem_ld32(tS + 32 * c, sv);
-                        tmem_ld_wait(sv);
-                        // a pair of queries, s as it comes.  GENERAL: any mask, any bias; else all are visible and
-                        // the bias is the same or, of slopes, on one side.
-                        const float d0 = static_cast<float>(qh + 32 * c - kg);  // i - j at the chunk's first query
-                        [[maybe_unused]] uint64_t dist = f2_pack(d0, d0 + 1.f);
-                        const auto weights = [&](auto how, auto general_, int i) {
-                            constexpr bool GENERAL = decltype(general_)::value;
-                            const int q = 32 * c + 2 * i;
-                            const ulonglong2 nl = nl4[8 * c + (i >> 1)];
-                            uint64_t add = (i & 1) ? nl.y : nl.x;
-                            if constexpr (BIAS == kBiasSlopes) {
-                                if constexpr (GENERAL) {
-                                    const float2 a = f2_unpack(add), y = f2_unpack(dist);
-                                    add = f2_pack(fmaf(-slope2, fabsf(y.x), a.x), fmaf(-slope2, fabsf(y.y), a.y));
-                                } else {
-                                    add = ffma2(dist, sl, add);
-                                }
-                                dist = fadd2(dist, f2_pack(2.f, 2.f));
-                            }
-                            if constexpr (BIAS == kBiasTable) {
-                                if constexpr (GENERAL) {
-                                    const int at = qh - kg + q + p.far, top = 2 * p.far;
-                                    add = fadd2(add, f2_pack(bias2[max(0, min(top, at))], bias2[max(0, min(top, at + 1))]));
-                                } else {
-                                    add = fadd2(add, far_bias);
-                                }
-                            }
-                            const uint64_t v = f2_pack(u2f(sv[2 * i]), u2f(sv[2 * i + 1]));
-                            [[maybe_unused]] uint64_t th = 0;
-                            float2 x;
-                            if constexpr (CAP) {
-                                th = tanh2<decltype(how)::value>(fmul2(v, k2));
-                                x = f2_unpack(ffma2(th, cap2, add));
-                            } else {
-                                x = f2_unpack(ffma2(v, c2, add));
-                            }
-                            float p0 = ex2(x.x), p1 = ex2(x.y);
-                            if constexpr (GENERAL) {
-                                if (static_cast<uint32_t>(q - from) >= seen) p0 = 0.f;
-                                if (static_cast<uint32_t>(q + 1 - from) >= seen) p1 = 0.f;
-                            }
-                            pk[i] = pack_bf16(p0, p1);
-                            if constexpr (CAP) {  // (tanh^2 - 1: dX, dK and dQ come with their sign turned)
-                                const float2 k = f2_unpack(fmul2(f2_pack(p0, p1), ffma2(th, th, f2_pack(-1.f, -1.f))));
-                                keep[c][i] = pack_f16(k.x, k.y);
-                            } else {
-                                keep[c][i] = pack_f16(p0, p1);
-                            }
-                        };
-                        const auto all = [&](auto how, auto general_) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) weights(how, general_, i);
-                        };
-                        using Poly4 = std::integral_constant<int, kTanhPoly4>;
-                        using Exp = std::integral_constant<int, kTanhExp>;
-                        if constexpr (CAP) {
-                            float mx0 = 0.f, mx1 = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 32; i += 4) {
-                                mx0 = fmax3(mx0, fabsf(u2f(sv[i])), fabsf(u2f(sv[i + 1])));
-                                mx1 = fmax3(mx1, fabsf(u2f(sv[i + 2])), fabsf(u2f(sv[i + 3])));
-                            }
-                            // (the few tiles at the edges: two forms)
-                            const float mx = fmaxf(mx0, mx1) * p.x_scale;
-                            const bool near = !__any_sync(FULL, !(mx <= kTanhNear)), mid = !__any_sync(FULL, !(mx <= kTanhMid));
-                            if (general && mid) all(Poly4{}, std::true_type{});
-                            else if (general) all(Exp{}, std::true_type{});
-                            else if (near) all(std::integral_constant<int, kTanhPoly3>{}, std::false_type{});
-                            else if (mid) all(Poly4{}, std::false_type{});
-                            else all(Exp{}, std::false_type{});
-                        } else if (general) {
-                            all(Exp{}, std::true_type{});
-                        } else {
-                            all(Exp{}, std::false_type{});
-                        }
-                        tmem_st16(tS + 16 * c, pk);
-                    }
+                    const BwdRow row{kg, mine.lo, static_cast<uint32_t>(mine.hi - mine.lo), general, side, slope2, bias2, far_bias};
+                    uint32_t sv[32], pk[16];
+                    tmem_ld32(tS, sv);
+                    tmem_ld_wait(sv);
+                    bwd_weights<CAP, BIAS>(p, row, sv, nl4, qh, pk, keep);
+                    tmem_st16(tS, pk);
                     tmem_st_wait();
                     tc_fence_before();
                 }
@@ -577,76 +400,46 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                 const ulonglong2* nd4 = reinterpret_cast<const ulonglong2*>(dvec_s + st * 128 + kQC * hw);
                 if (ok)
                     ok = __all_sync(FULL, mbar_wait_sleep(bar_dp, s & 1, wd, kSiteDsDP) &&
-                                              (s == 0 || mbar_wait_sleep(L::kDSInTmem ? bar_dq : bar_dk, (s - 1) & 1, wd,
-                                                                         kSiteDsDQ)));
+                                              (s == 0 || mbar_wait_sleep(bar_dq, (s - 1) & 1, wd, kSiteDsDQ)));
                 if (ok) {
                     tc_fence_after();
                     if (grad && side != fside) {
                         if (fside != 0) flush(bh);
                         fside = side;
                     }
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        uint32_t dp[32], ds[16];
-                        tmem_ld32(tDP + 32 * c, dp);
-                        [[maybe_unused]] uint32_t pw[16];  // CAP: P itself
-                        if constexpr (CAP && BIAS == kBiasTable) {
-                            tmem_ld16(tS + 16 * c, pw);
-                            tmem_ld_wait(pw);
-                        }
-                        tmem_ld_wait(dp);
-                        [[maybe_unused]] float ahead = 0.f, behind = 0.f;
-                        // SUMS: of the table's gradient, for far (1) or near (2) pairs
-                        const auto products = [&](auto sums) {
-                            constexpr int SUMS = decltype(sums)::value;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const ulonglong2 nd = nd4[8 * c + (i >> 1)];
-                                const uint64_t t2 = fadd2(f2_pack(u2f(dp[2 * i]), u2f(dp[2 * i + 1])), (i & 1) ? nd.y : nd.x);
-                                const float2 kk = unpack_f16(keep[c][i]);
-                                const uint64_t d2 = fmul2(f2_pack(kk.x, kk.y), t2);
-                                const float2 dx = f2_unpack(d2);
-                                ds[i] = pack_bf16(dx.x, dx.y);
-                                if constexpr (SUMS != 0) {
-                                    uint64_t dy = d2;
-                                    if constexpr (CAP) dy = fmul2(f2_pack(u2f(pw[i] << 16), u2f(pw[i] & 0xffff0000u)), t2);
-                                    if constexpr (SUMS == 1) {
-                                        fsum = fadd2(fsum, dy);
-                                    } else {
-                                        // column q's value of key row l to lane (q - l) mod 32
-                                        const float2 y = f2_unpack(dy);
-                                        const float y0 = __shfl_sync(FULL, y.x, 2 * i - lane);
-                                        const float y1 = __shfl_sync(FULL, y.y, 2 * i + 1 - lane);
-                                        if (lane <= 2 * i) ahead += y0;
-                                        else behind += y0;
-                                        if (lane <= 2 * i + 1) ahead += y1;
-                                        else behind += y1;
-                                    }
-                                }
-                            }
-                        };
-                        if (BIAS == kBiasTable && grad && side != 0) products(std::integral_constant<int, BIAS == kBiasTable>{});
-                        else if (BIAS == kBiasTable && grad) products(std::integral_constant<int, BIAS == kBiasTable ? 2 : 0>{});
-                        else products(std::integral_constant<int, 0>{});
-                        if constexpr (BIAS == kBiasTable) {
-                            if (grad && side == 0) {
-                                // block (query block, key block) of 32: lane m holds distance m, and m - 32
-                                const long long at = (static_cast<long long>(bh) * p.n_kv + ikv) * p.near_n + (first + t - ikv - p.near_lo);
-                                float* dst = p.near_part + at * kNearFloats + ((kChunks * hw + c) * 4 + (warp & 3)) * 64;
-                                dst[lane] = ahead;
-                                dst[32 + lane] = behind;
-                            }
-                        }
-                        if constexpr (L::kDSInTmem) tmem_st16(tS + kQC / 2 + 16 * c, ds);
-#pragma unroll
-                        for (int q4 = 0; q4 < 4; ++q4) {
-                            const int chunk = ds_chunk0 + 4 * c + q4;
-                            *reinterpret_cast<uint4*>(ds_row + ((chunk ^ (r & 7)) << 4)) =
-                                make_uint4(ds[4 * q4], ds[4 * q4 + 1], ds[4 * q4 + 2], ds[4 * q4 + 3]);
+                    uint32_t dp[32], ds[16];
+                    tmem_ld32(tDP, dp);
+                    [[maybe_unused]] uint32_t pw[16];  // CAP: P itself
+                    if constexpr (CAP && BIAS == kBiasTable) {
+                        tmem_ld16(tS, pw);
+                        tmem_ld_wait(pw);
+                    }
+                    tmem_ld_wait(dp);
+                    [[maybe_unused]] float ahead = 0.f, behind = 0.f;
+                    if (BIAS == kBiasTable && grad && side != 0)
+                        bwd_products<CAP, BIAS == kBiasTable>(dp, keep, pw, nd4, lane, ds, fsum, ahead, behind);
+                    else if (BIAS == kBiasTable && grad)
+                        bwd_products<CAP, BIAS == kBiasTable ? 2 : 0>(dp, keep, pw, nd4, lane, ds, fsum, ahead, behind);
+                    else
+                        bwd_products<CAP, 0>(dp, keep, pw, nd4, lane, ds, fsum, ahead, behind);
+                    if constexpr (BIAS == kBiasTable) {
+                        if (grad && side == 0) {
+                            // block (query block, key block) of 32: lane m holds distance m, and m - 32
+                            const long long at = (static_cast<long long>(bh) * p.n_kv + ikv) * p.near_n + (first + t - ikv - p.near_lo);
+                            float* dst = p.near_part + at * kNearFloats + (hw * 4 + (warp & 3)) * 64;
+                            dst[lane] = ahead;
+                            dst[32 + lane] = behind;
                         }
                     }
+                    tmem_st16(tS + kQC / 2, ds);
+#pragma unroll
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const int chunk = ds_chunk0 + q4;
+                        *reinterpret_cast<uint4*>(ds_row + ((chunk ^ (r & 7)) << 4)) =
+                            make_uint4(ds[4 * q4], ds[4 * q4 + 1], ds[4 * q4 + 2], ds[4 * q4 + 3]);
+                    }
                     fence_async_shared();
-                    if constexpr (L::kDSInTmem) tmem_st_wait();
+                    tmem_st_wait();
                     tc_fence_before();
                 }
                 mbar_arrive(bar_ds);
@@ -664,7 +457,7 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                     tc_fence_before();
                     mbar_arrive(bar_dr);
                     // staged over dO (free: dV and dP^T come before dQ) and over Q (free once dK is done)
-                    if (hw < NWG / 2) ok = __all_sync(FULL, mbar_wait_sleep(bar_dk, s & 1, wd, kSiteDrain));
+                    if (hw < kNWG / 2) ok = __all_sync(FULL, mbar_wait_sleep(bar_dk, s & 1, wd, kSiteDrain));
                 } else {
                     mbar_arrive(bar_dr);
                 }
@@ -680,7 +473,7 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                     }
                     fence_async_shared();
                 }
-                mbar_arrive(hw >= NWG / 2 ? bar_sgd : bar_sgq);
+                mbar_arrive(hw >= kNWG / 2 ? bar_sgd : bar_sgq);
             }
             if (grad && fside != 0) flush(bh);
         }
@@ -850,17 +643,13 @@ __global__ void __launch_bounds__(256) fa_score_table_kernel(const TableGradPara
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-// The workspace's parts, each 256-aligned.
-struct BwdPlan {
-    int near_lo = 0, near_n = 0, warps = 0;
-    size_t dvec = 0, acc = 0, spans = 0, order = 0, bias2 = 0, near = 0, far = 0, red = 0, bytes = 0;
-};
 BwdPlan plan_of(const ScoreArgs& a) {
     BwdPlan pl;
     const size_t rows = static_cast<size_t>(a.B) * a.H * a.N;
     const int n_kv = (a.N + kBK - 1) / kBK;
     pl.acc = up(rows * sizeof(float));
-    pl.spans = pl.acc + up(rows * a.d * sizeof(float));
+    pl.next = pl.acc + up(rows * a.d * sizeof(float));
+    pl.spans = pl.next + up(sizeof(int));
     pl.order = pl.spans + (a.mod.docs ? score_spans_bytes(a.B, a.N) : 0);  // of pairs, then of key tiles
     pl.bias2 = pl.order + (a.mod.docs ? up(static_cast<size_t>(a.B) * (n_kv + (n_kv + 1) / 2) * sizeof(int)) : 0);
     pl.near = pl.far = pl.red = pl.bytes = pl.bias2;
@@ -869,7 +658,7 @@ BwdPlan plan_of(const ScoreArgs& a) {
     const int n = std::min(near_tiles(a.mod.far, kBQ), n_kv - 1);
     pl.near_lo = a.causal && !a.mod.prefix ? 0 : -n;
     pl.near_n = n - pl.near_lo + 1;
-    pl.warps = 4 * warpgroups(a.d, a.mod.softcap > 0.f, kBiasTable);
+    pl.warps = 4 * kNWG;
     const size_t tiles = static_cast<size_t>(a.B) * a.H * n_kv;
     pl.near = pl.bias2 + up(static_cast<size_t>(a.H) * (2 * a.mod.far + 1) * sizeof(float));
     pl.far = pl.near + tiles * pl.near_n * kNearFloats * sizeof(float);
@@ -888,26 +677,14 @@ int head_group(const ScoreArgs& a) {
     return std::max(1, std::min(a.B * a.H_kv, g));
 }
 
-template <int D, bool CAP, int BIAS>
-cudaError_t launch_main(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t stream) {
-    using L = ScoreBwdLayout<D>;
-    CUtensorMap tq, tk, tv, tdo, tacc, tdk, tdv;
-    const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const int BH = a.B * a.H, BHkv = a.B * a.H_kv;
-    float* acc = reinterpret_cast<float*>(a.workspace + pl.acc);
-    if (!make_tile_map(&tq, a.Q, BF, 2, D, a.N, BH, 64, kBQ) || !make_tile_map(&tk, a.K, BF, 2, D, a.N, BHkv, 64, kBK) ||
-        !make_tile_map(&tv, a.V, BF, 2, D, a.N, BHkv, 64, kBK) || !make_tile_map(&tdo, a.dO, BF, 2, D, a.N, BH, 64, kBQ) ||
-        !make_tile_map(&tacc, acc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, D, a.N, BH, 32, kBQ) ||
-        !make_tile_map(&tdk, a.dK, BF, 2, D, a.N, BHkv, 64, kBK) || !make_tile_map(&tdv, a.dV, BF, 2, D, a.N, BHkv, 64, kBK))
-        return cudaErrorInvalidValue;
-    constexpr auto kern = &fa_score_bwd_kernel<D, CAP, BIAS>;
-    cudaError_t e = set_max_dyn_smem_once<kern>(L::kBytes);
-    if (e != cudaSuccess) return e;
+ScoreBwdParams params_of(const ScoreArgs& a, const BwdPlan& pl) {
+    const bool cap = a.mod.softcap > 0.f;
     ScoreBwdParams p;
     p.LSE = a.LSE;
     p.Dvec = reinterpret_cast<const float*>(a.workspace + pl.dvec);
     p.H = a.H;
     p.H_kv = a.H_kv;
+    p.BHkv = a.B * a.H_kv;
     p.G = a.H / a.H_kv;
     p.n_kv = (a.N + kBK - 1) / kBK;
     p.head_group = head_group(a);
@@ -919,7 +696,7 @@ cudaError_t launch_main(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t stre
     p.mask.causal = a.causal;
     p.scale_log2 = a.tau * kLog2e;
     p.tau = a.tau;
-    p.x_scale = CAP ? a.tau / a.mod.softcap : 0.f;
+    p.x_scale = cap ? a.tau / a.mod.softcap : 0.f;
     p.cap_log2 = a.mod.softcap * kLog2e;
     p.slopes = a.mod.slopes;
     p.bias2 = reinterpret_cast<const float*>(a.workspace + pl.bias2);
@@ -928,18 +705,36 @@ cudaError_t launch_main(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t stre
     p.far_part = reinterpret_cast<float*>(a.workspace + pl.far);
     p.near_lo = pl.near_lo;
     p.near_n = pl.near_n;
+    p.next = reinterpret_cast<int*>(a.workspace + pl.next);
     p.err = a.err;
     p.wait_limit_ns = a.wait_limit_ns;
+    return p;
+}
+
+template <bool CAP, int BIAS>
+cudaError_t launch_main(const ScoreArgs& a, const ScoreBwdParams& p, float* acc, cudaStream_t stream) {
+    using L = ScoreBwdLayout;
+    CUtensorMap tq, tk, tv, tdo, tacc, tdk, tdv;
+    const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int BH = a.B * a.H, BHkv = p.BHkv;
+    if (!make_tile_map(&tq, a.Q, BF, 2, D, a.N, BH, 64, kBQ) || !make_tile_map(&tk, a.K, BF, 2, D, a.N, BHkv, 64, kBK) ||
+        !make_tile_map(&tv, a.V, BF, 2, D, a.N, BHkv, 64, kBK) || !make_tile_map(&tdo, a.dO, BF, 2, D, a.N, BH, 64, kBQ) ||
+        !make_tile_map(&tacc, acc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, D, a.N, BH, 32, kBQ) ||
+        !make_tile_map(&tdk, a.dK, BF, 2, D, a.N, BHkv, 64, kBK) || !make_tile_map(&tdv, a.dV, BF, 2, D, a.N, BHkv, 64, kBK))
+        return cudaErrorInvalidValue;
+    constexpr auto kern = &fa_score_bwd_kernel<CAP, BIAS>;
+    cudaError_t e = set_max_dyn_smem_once<kern>(L::kBytes);
+    if (e != cudaSuccess) return e;
     if (a.ev_start) cudaEventRecord(a.ev_start, stream);
     e = launch_dependent(kern, dim3(static_cast<unsigned>(BHkv) * static_cast<unsigned>(p.n_kv)),
-                         dim3(threads_for(warpgroups(D, CAP, BIAS))), L::kBytes, stream, tq, tk, tv, tdo, tacc, tdk, tdv, p);
+                         dim3(kThreads), L::kBytes, stream, tq, tk, tv, tdo, tacc, tdk, tdv, p);
     if (e == cudaSuccess && a.ev_stop) e = cudaEventRecord(a.ev_stop, stream);
     return e;
 }
 
-template <int D>
-cudaError_t launch_d(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t stream) {
+cudaError_t launch_all(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(a.B) * a.H * a.N;
+    const ScoreBwdParams p = params_of(a, pl);
     float* bias2 = reinterpret_cast<float*>(a.workspace + pl.bias2);
     float* acc = reinterpret_cast<float*>(a.workspace + pl.acc);
     cudaError_t e = cudaSuccess;
@@ -949,15 +744,16 @@ cudaError_t launch_d(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t stream)
                              static_cast<int>(a.mod.table_f32), a.mod.buckets, a.mod.num_buckets, a.H, a.mod.far, bias2);
         if (e != cudaSuccess) return e;
     }
-    e = launch_score_rows(a, reinterpret_cast<float*>(a.workspace + pl.dvec), acc, a.mod.docs ? a.workspace + pl.spans : nullptr,
+    e = launch_score_rows(a, reinterpret_cast<float*>(a.workspace + pl.dvec), acc, p.next, a.mod.docs ? a.workspace + pl.spans : nullptr,
                           a.mod.docs ? reinterpret_cast<const int*>(a.workspace + pl.order) : nullptr, bias2, stream);
     if (e != cudaSuccess) return e;
     const bool cap = a.mod.softcap > 0.f;
-    if (a.mod.slopes) e = cap ? launch_main<D, true, kBiasSlopes>(a, pl, stream) : launch_main<D, false, kBiasSlopes>(a, pl, stream);
-    else if (a.mod.table) e = cap ? launch_main<D, true, kBiasTable>(a, pl, stream) : launch_main<D, false, kBiasTable>(a, pl, stream);
-    else e = cap ? launch_main<D, true, kBiasNone>(a, pl, stream) : launch_main<D, false, kBiasNone>(a, pl, stream);
+    if (a.d == 64) e = launch_score_bwd64(a, p, acc, stream);
+    else if (a.mod.slopes) e = cap ? launch_main<true, kBiasSlopes>(a, p, acc, stream) : launch_main<false, kBiasSlopes>(a, p, acc, stream);
+    else if (a.mod.table) e = cap ? launch_main<true, kBiasTable>(a, p, acc, stream) : launch_main<false, kBiasTable>(a, p, acc, stream);
+    else e = cap ? launch_main<true, kBiasNone>(a, p, acc, stream) : launch_main<false, kBiasNone>(a, p, acc, stream);
     if (e != cudaSuccess) return e;
-    const int64_t n8 = rows * D / 8;
+    const int64_t n8 = rows * a.d / 8;
     return launch_dependent(fa_score_post_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((n8 + 255) / 256, 152 * 64))),
                             dim3(256), 0, stream, static_cast<const float*>(acc), static_cast<__nv_bfloat16*>(a.dQ),
                             (cap ? -a.tau : a.tau) * kUnliftP, n8);
@@ -976,7 +772,7 @@ cudaError_t launch_score_bwd(const ScoreArgs& a, cudaStream_t stream) {
         order.keys = order.pairs + static_cast<size_t>(a.B) * ((a.N + 2 * kBQ - 1) / (2 * kBQ));
         e = launch_score_spans(a, a.workspace + pl.spans, order, stream);
     }
-    if (e == cudaSuccess) e = a.d == 64 ? launch_d<64>(a, pl, stream) : launch_d<128>(a, pl, stream);
+    if (e == cudaSuccess) e = launch_all(a, pl, stream);
     if (e != cudaSuccess || !a.dTable) return e;
     TableGradParams t;
     t.near_part = reinterpret_cast<const float*>(a.workspace + pl.near);

@@ -1,5 +1,5 @@
 // Row sums of the backward of attention with capped, biased or masked scores, for sm_103a:
-// D_i = sum_j P_ij dP_ij, and a zeroed fp32 dQ accumulator.
+// D_i = sum_j P_ij dP_ij, and a zeroed fp32 dQ accumulator and tile counter.
 //
 // Mathematics: D_i = dO_i . O_i as well, which costs nothing but reads O as the forward rounded it, from
 // weights that it rounded too: off by 2^-8 of |dO| |O|, while dY = P (dP - D) is a small
@@ -45,6 +45,7 @@ struct RowsParams {
     const float* LSE;
     float* Dvec;
     float* dQacc;
+    int* next;  // zeroed, too
     int H, G, n_pairs;
     const int* order;  // [B][n_pairs], or null: from the last
     ScoreMask mask;
@@ -123,6 +124,7 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     tc_fence_after();
     griddep_launch_dependents();
     griddep_wait();
+    if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.y == 0) *p.next = 0;
     const uint32_t tmem = sh.tmem_base;
     const Watchdog wd{p.err, &sh.abort_flag, p.wait_limit_ns};
     const int rank = static_cast<int>(blockIdx.y);
@@ -333,7 +335,8 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 }
 
 template <int D, bool CAP, int BIAS>
-cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, const void* spans, const int* order, const float* bias2, cudaStream_t stream) {
+cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, int* next, const void* spans, const int* order,
+                     const float* bias2, cudaStream_t stream) {
     using L = RowsLayout<D>;
     CUtensorMap tq, tk, tv, tdo;
     const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -348,6 +351,7 @@ cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, const void* sp
     p.LSE = a.LSE;
     p.Dvec = dvec;
     p.dQacc = acc;
+    p.next = next;
     p.H = a.H;
     p.G = a.H / a.H_kv;
     p.n_pairs = (a.N + 2 * kBM - 1) / (2 * kBM);
@@ -369,23 +373,25 @@ cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, const void* sp
 }
 
 template <int D>
-cudaError_t launch_d(const ScoreArgs& a, float* dvec, float* acc, const void* spans, const int* order, const float* bias2, cudaStream_t stream) {
+cudaError_t launch_d(const ScoreArgs& a, float* dvec, float* acc, int* next, const void* spans, const int* order,
+                     const float* bias2, cudaStream_t stream) {
     const bool cap = a.mod.softcap > 0.f;
     if (a.mod.slopes)
-        return cap ? launch_t<D, true, kBiasSlopes>(a, dvec, acc, spans, order, bias2, stream)
-                   : launch_t<D, false, kBiasSlopes>(a, dvec, acc, spans, order, bias2, stream);
+        return cap ? launch_t<D, true, kBiasSlopes>(a, dvec, acc, next, spans, order, bias2, stream)
+                   : launch_t<D, false, kBiasSlopes>(a, dvec, acc, next, spans, order, bias2, stream);
     if (a.mod.table)
-        return cap ? launch_t<D, true, kBiasTable>(a, dvec, acc, spans, order, bias2, stream)
-                   : launch_t<D, false, kBiasTable>(a, dvec, acc, spans, order, bias2, stream);
-    return cap ? launch_t<D, true, kBiasNone>(a, dvec, acc, spans, order, bias2, stream)
-               : launch_t<D, false, kBiasNone>(a, dvec, acc, spans, order, bias2, stream);
+        return cap ? launch_t<D, true, kBiasTable>(a, dvec, acc, next, spans, order, bias2, stream)
+                   : launch_t<D, false, kBiasTable>(a, dvec, acc, next, spans, order, bias2, stream);
+    return cap ? launch_t<D, true, kBiasNone>(a, dvec, acc, next, spans, order, bias2, stream)
+               : launch_t<D, false, kBiasNone>(a, dvec, acc, next, spans, order, bias2, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_score_rows(const ScoreArgs& a, float* dvec, float* acc, const void* spans, const int* order,
+cudaError_t launch_score_rows(const ScoreArgs& a, float* dvec, float* acc, int* next, const void* spans, const int* order,
                               const float* bias2, cudaStream_t stream) {
-    return a.d == 64 ? launch_d<64>(a, dvec, acc, spans, order, bias2, stream) : launch_d<128>(a, dvec, acc, spans, order, bias2, stream);
+    return a.d == 64 ? launch_d<64>(a, dvec, acc, next, spans, order, bias2, stream)
+                     : launch_d<128>(a, dvec, acc, next, spans, order, bias2, stream);
 }
 
 }  // namespace fa
