@@ -34,8 +34,9 @@ __device__ void sort_tiles(const ScoreMask& m, int b, int prefix, int rows, int 
         return kBins - min(kBins, r.hi - r.lo);
     };
     bins[t] = 0;
+    const int own = t < n ? bin_of(t) : 0;  // of a thread's first tile, mostly its only one
     __syncthreads();
-    for (int i = t; i < n; i += kSpanThreads) atomicAdd(&bins[bin_of(i)], 1);
+    for (int i = t; i < n; i += kSpanThreads) atomicAdd(&bins[i == t ? own : bin_of(i)], 1);
     __syncthreads();
     const int mine = bins[t];
     int incl = mine;
@@ -50,7 +51,7 @@ __device__ void sort_tiles(const ScoreMask& m, int b, int prefix, int rows, int 
     for (int w = 0; w < warp; ++w) at += sums[w];
     bins[t] = at;
     __syncthreads();
-    for (int i = t; i < n; i += kSpanThreads) order[static_cast<long long>(b) * n + atomicAdd(&bins[bin_of(i)], 1)] = i;
+    for (int i = t; i < n; i += kSpanThreads) order[static_cast<long long>(b) * n + atomicAdd(&bins[i == t ? own : bin_of(i)], 1)] = i;
     __syncthreads();
 }
 
@@ -72,7 +73,7 @@ __global__ void __launch_bounds__(kSpanThreads) fa_score_spans_kernel(const int*
     const auto chunk = [&](int c0, bool starts, bool ends, int& carry_start, int& carry_end) {
         const int words = (min(kChunk, N - c0) + 31) / 32;
 #pragma unroll 8
-        for (int k = 0; k < kChunk / kSpanThreads; ++k) {
+        for (int k = 0; k < (words + 31) / 32; ++k) {
             const int w = k * 32 + warp, i = c0 + 32 * w + lane;
             int v = 0, prev = 0;
             if (i < N) {
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kSpanThreads) fa_score_spans_kernel(const int*
         word_end[t] = min(end, carry_end);
         __syncthreads();
 #pragma unroll 4
-        for (int k = 0; k < kChunk / kSpanThreads; ++k) {
+        for (int k = 0; k < (words + 31) / 32; ++k) {
             const int w = k * 32 + warp, i = c0 + 32 * w + lane;
             if (i >= N) break;
             const uint32_t upto = (2u << lane) - 1u, b = start_bits[w];
