@@ -260,7 +260,7 @@ cudaError_t launch_bwd(const BwdArgs& a, cudaStream_t stream);
 cudaError_t launch_score_fwd(const ScoreArgs& a, cudaStream_t stream);
 cudaError_t launch_score_bwd(const ScoreArgs& a, cudaStream_t stream);
 // D_i = sum_j P_ij dP_ij and a zeroed dQ accumulator (spans, order of pairs and bias2: of the workspace, or null)
-cudaError_t launch_score_rows(const ScoreArgs& a, float* dvec, float* acc, int* next, const void* spans, const int* order,
+cudaError_t launch_score_rows(const ScoreArgs& a, float* dvec, float* acc, unsigned* next, const void* spans, const int* order,
                               const float* bias2, cudaStream_t stream);
 // documents' ids -> each token's document as [first, end) (int2 [B][N]), and tiles' orders
 cudaError_t launch_score_spans(const ScoreArgs& a, void* spans, const ScoreOrder& order, cudaStream_t stream);

@@ -533,8 +533,8 @@ __global__ void __launch_bounds__(256) fa_score_expand_kernel(const void* table,
                                                               int far, float* bias2) {
     griddep_launch_dependents();
     griddep_wait();
-    const int n = 2 * far + 1, i = static_cast<int>(blockIdx.x) * 256 + threadIdx.x;
-    if (i < n * H) bias2[i] = kLog2e * table_bias(table, f32, buckets, num_buckets, H, i / n, i % n);
+    const int n = 2 * far + 1, h = static_cast<int>(blockIdx.x), i = static_cast<int>(blockIdx.y) * 256 + threadIdx.x;
+    if (i < n) bias2[static_cast<long long>(h) * n + i] = kLog2e * table_bias(table, f32, buckets, num_buckets, H, h, i);
 }
 
 // dQ = bf16(scale * acc), 8 elements per thread, grid-stride.
@@ -562,7 +562,7 @@ struct TableGradParams {
     int B, H, n_kv, near_lo, near_n, far_warps, far, num_buckets, out_f32;
 };
 
-// Block (x, head): x < near_n kParts adds the diagonals of the tile pairs at offset near_lo + x / kParts, of a part of
+// Block (head, x): x < near_n kParts adds the diagonals of the tile pairs at offset near_lo + x / kParts, of a part of
 // the batch and the key tiles, in order, and then, bucket by bucket, the diagonals of each; the last
 // block adds the far parts.  (One block for all of an offset's tiles read 256 KB by itself, 24 us.)
 constexpr int kParts = 8;
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(1024) fa_score_buckets_kernel(const TableGradP
     __shared__ int of[kNearFloats];
     griddep_launch_dependents();
     griddep_wait();
-    const int x = static_cast<int>(blockIdx.x), h = static_cast<int>(blockIdx.y);
+    const int x = static_cast<int>(blockIdx.y), h = static_cast<int>(blockIdx.x);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     if (x == p.near_n * kParts) {
         const long long parts = static_cast<long long>(p.n_kv) * p.far_warps;
@@ -705,7 +705,7 @@ ScoreBwdParams params_of(const ScoreArgs& a, const BwdPlan& pl) {
     p.far_part = reinterpret_cast<float*>(a.workspace + pl.far);
     p.near_lo = pl.near_lo;
     p.near_n = pl.near_n;
-    p.next = reinterpret_cast<int*>(a.workspace + pl.next);
+    p.next = reinterpret_cast<unsigned*>(a.workspace + pl.next);
     p.err = a.err;
     p.wait_limit_ns = a.wait_limit_ns;
     return p;
@@ -739,8 +739,8 @@ cudaError_t launch_all(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t strea
     float* acc = reinterpret_cast<float*>(a.workspace + pl.acc);
     cudaError_t e = cudaSuccess;
     if (a.mod.table) {
-        const int n = a.H * (2 * a.mod.far + 1);
-        e = launch_dependent(fa_score_expand_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, stream, a.mod.table,
+        const dim3 grid(static_cast<unsigned>(a.H), static_cast<unsigned>((2 * a.mod.far + 256) / 256));
+        e = launch_dependent(fa_score_expand_kernel, grid, dim3(256), 0, stream, a.mod.table,
                              static_cast<int>(a.mod.table_f32), a.mod.buckets, a.mod.num_buckets, a.H, a.mod.far, bias2);
         if (e != cudaSuccess) return e;
     }
@@ -789,7 +789,7 @@ cudaError_t launch_score_bwd(const ScoreArgs& a, cudaStream_t stream) {
     t.far = a.mod.far;
     t.num_buckets = a.mod.num_buckets;
     t.out_f32 = a.mod.table_f32;
-    e = launch_dependent(fa_score_buckets_kernel, dim3(static_cast<unsigned>(t.near_n * kParts + 1), static_cast<unsigned>(t.H)), dim3(1024),
+    e = launch_dependent(fa_score_buckets_kernel, dim3(static_cast<unsigned>(t.H), static_cast<unsigned>(t.near_n * kParts + 1)), dim3(1024),
                          0, stream, t);
     if (e != cudaSuccess) return e;
     return launch_dependent(fa_score_table_kernel, dim3(static_cast<unsigned>(t.H)), dim3(256), 0, stream, t);

@@ -25,7 +25,7 @@ struct ScoreBwdParams {
     float* near_part;    // [B H][n_kv][near_n][kNearFloats], or null
     float* far_part;     // [B H][n_kv][4 NWG][kFarFloats]
     int near_lo, near_n;  // near tile pairs: query tile - key tile from near_lo on
-    int* next;  // d = 64: tiles taken, behind the first of every CTA
+    unsigned* next;  // d = 64: tiles taken, behind the first of every CTA
     unsigned int* err;
     unsigned long long wait_limit_ns;
 };

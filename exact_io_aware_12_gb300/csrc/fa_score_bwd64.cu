@@ -156,8 +156,9 @@ fa_score_bwd64_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
 
     if (warp == kProducerWarp) {
         // ------------------------------------------------------------ producer --
-        const int tiles = p.BHkv * p.n_kv;
-        int next = static_cast<int>(blockIdx.x), s = 0;
+        const unsigned tiles = static_cast<unsigned>(p.BHkv) * p.n_kv;
+        unsigned next = blockIdx.x;
+        int s = 0;
         bool ok = true;
         for (int t = 0; ok; ++t) {
             const int buf = t & 1;
@@ -168,8 +169,8 @@ fa_score_bwd64_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                 mbar_arrive(bar);
                 break;
             }
-            int after = 0;
-            if (lane == 0) after = static_cast<int>(gridDim.x) + atomicAdd(p.next, 1);
+            unsigned after = 0;
+            if (lane == 0) after = gridDim.x + atomicAdd(p.next, 1u);
             // order: groups of head_group key heads, whose Q, dO and accumulator stay in L2; in a group
             // the key tiles in order (when causal the longest first), its heads interleaved
             const long long per_group = static_cast<long long>(p.head_group) * p.n_kv;

@@ -10,13 +10,16 @@
 //
 // Design: one CTA per 128-row query tile and query head, two CTAs to an SM (256 of its 512
 // tensor-memory columns each), so that one's loads, S and P V products and epilogue run
-// beside the other's softmax, which bounds these kernels: per score the mask, the cap (6
-// to 8 operations on the fp32 pipe; see tanh2), the bias, one exponential and two sums,
-// against the 2 x 128 x 128 x d products of a tile pair.
-//   - warp 4 streams Q, K_j and V_j by TMA through a ring of slots; warp 5 issues
-//     S = Q K_j^T and O += P V_j (tcgen05, P read from tensor memory); warps 0-3 own a row
-//     per thread.  At d = 64, P has columns of its own and the next S is issued as soon as the
-//     softmax has read the last; at d = 128 it is written over S.
+// beside the other's softmax: per score the mask, the cap (6 to 8 operations on the fp32 pipe; see
+// tanh2), the bias, one exponential and two sums, against the 2 x 128 x 128 x d products of a tile pair.
+// What bounds it is each CTA's chain S -> softmax -> P V -> S at d = 128 (16 heads of 16384 tokens, window 4096:
+// 367 us without a cap, 535 with, and no less where a sum or the exponential is left out), the
+// fp32 and exponential pipes at d = 64.
+//   - Softmax warpgroups (WGS): one, a row per thread; or two, half of a row's keys each, with one CTA to an
+//     SM, where tiles are few (launch_t).  The next warp streams Q, K_j and V_j by TMA through a ring of
+//     slots, the last issues S = Q K_j^T and O += P V_j (tcgen05, P read from tensor memory).  At d = 64,
+//     P has columns of its own and the next S is issued as soon as the softmax has read the last; at d = 128
+//     it is written over S.
 //   - The query heads that share a key head are neighbours in launch order, so that its
 //     keys are read from L2; longest tiles first when causal.
 //   - Capped scores without a bias: the maximum is found before the cap, which keeps the order,
@@ -40,10 +43,6 @@ namespace {
 
 constexpr int kSms = 152;  // of a GB300
 constexpr int kBM = 128, kBN = 128;
-// Softmax warpgroups: one (a thread per row), with two CTAs to an SM; or two (two threads per row, half of a
-// block's keys each), with one, where there are at most two CTAs for each SM, and the chain of steps of the longest
-// sets the time (16 heads, d = 64: 901 tokens with slopes 15.0 us by one and 12.6 by two, 2000
-// capped 41.3 and 30.9, 4096 capped 84 and 108).
 constexpr int threads_for(int wgs) { return 128 * wgs + 64; }
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
@@ -588,6 +587,9 @@ cudaError_t launch_w(const ScoreArgs& a, cudaStream_t stream) {
     return e;
 }
 
+// Two softmax warpgroups where there are at most two tiles for each SM, and the chain of steps of the longest sets the
+// time (16 heads, d = 64: 901 tokens with slopes 15.0 us by one and 12.6 by two, 2000 capped 41.3 and 30.9, 4096
+// capped 84 and 108).
 template <int D, bool CAP, int BIAS>
 cudaError_t launch_t(const ScoreArgs& a, cudaStream_t stream) {
     const long long ctas = static_cast<long long>(a.B) * a.H * ((a.N + kBM - 1) / kBM);

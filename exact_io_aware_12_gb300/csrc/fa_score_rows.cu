@@ -45,7 +45,7 @@ struct RowsParams {
     const float* LSE;
     float* Dvec;
     float* dQacc;
-    int* next;  // zeroed, too
+    unsigned* next;  // zeroed, too
     int H, G, n_pairs;
     const int* order;  // [B][n_pairs], or null: from the last
     ScoreMask mask;
@@ -335,7 +335,7 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
 }
 
 template <int D, bool CAP, int BIAS>
-cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, int* next, const void* spans, const int* order,
+cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, unsigned* next, const void* spans, const int* order,
                      const float* bias2, cudaStream_t stream) {
     using L = RowsLayout<D>;
     CUtensorMap tq, tk, tv, tdo;
@@ -373,7 +373,7 @@ cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, int* next, con
 }
 
 template <int D>
-cudaError_t launch_d(const ScoreArgs& a, float* dvec, float* acc, int* next, const void* spans, const int* order,
+cudaError_t launch_d(const ScoreArgs& a, float* dvec, float* acc, unsigned* next, const void* spans, const int* order,
                      const float* bias2, cudaStream_t stream) {
     const bool cap = a.mod.softcap > 0.f;
     if (a.mod.slopes)
@@ -388,7 +388,7 @@ cudaError_t launch_d(const ScoreArgs& a, float* dvec, float* acc, int* next, con
 
 }  // namespace
 
-cudaError_t launch_score_rows(const ScoreArgs& a, float* dvec, float* acc, int* next, const void* spans, const int* order,
+cudaError_t launch_score_rows(const ScoreArgs& a, float* dvec, float* acc, unsigned* next, const void* spans, const int* order,
                               const float* bias2, cudaStream_t stream) {
     return a.d == 64 ? launch_d<64>(a, dvec, acc, next, spans, order, bias2, stream)
                      : launch_d<128>(a, dvec, acc, next, spans, order, bias2, stream);

@@ -181,6 +181,13 @@ def test_maps_of_any_kind(d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+def test_more_heads_than_a_grid_dimension_holds(d):
+    H = 70000
+    check(inputs(1, H, H, 2, d, 3), True, **table_of(H, 4, 3, False, 4))
+    check(inputs(1, H, 7, 1, d, 3), False, slopes=torch.linspace(0, 1, H))
+
+
+@pytest.mark.parametrize("d", [64, 128])
 def test_large_biases(d):
     """Biases and slopes that leave most weights at 0."""
     N, H = 333, 2
