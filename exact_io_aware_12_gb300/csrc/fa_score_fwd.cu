@@ -13,8 +13,8 @@
 // beside the other's softmax: per score the mask, the cap (6 to 8 operations on the fp32 pipe; see
 // tanh2), the bias, one exponential and two sums, against the 2 x 128 x 128 x d products of a tile pair.
 // What bounds it is each CTA's chain S -> softmax -> P V -> S at d = 128 (16 heads of 16384 tokens, window 4096:
-// 367 us without a cap, 535 with, and no less where a sum or the exponential is left out), the
-// fp32 and exponential pipes at d = 64.
+// 367 us without a cap, 535 with, and no less where a sum or the exponential is left out), a score's
+// instructions at d = 64 (half of the issue slots, with the waits of the same chain).
 //   - Softmax warpgroups (WGS): one, a row per thread; or two, half of a row's keys each, with one CTA to an
 //     SM, where tiles are few (launch_t).  The next warp streams Q, K_j and V_j by TMA through a ring of
 //     slots, the last issues S = Q K_j^T and O += P V_j (tcgen05, P read from tensor memory).  At d = 64,

