@@ -63,6 +63,17 @@ DeviceInfo* current_device(fa_status* why) {
         *why = FA_ERR_CUDA;
         return nullptr;
     }
+    // A thread that has made no call of the runtime that needs one (autograd's workers are such) has no current
+    // context, without which descriptors cannot be encoded.
+    static thread_local int bound = -1;
+    if (bound != dev) {
+        if (cudaSetDevice(dev) != cudaSuccess) {
+            cudaGetLastError();
+            *why = FA_ERR_CUDA;
+            return nullptr;
+        }
+        bound = dev;
+    }
     DeviceInfo& di = g_dev[dev];
     std::call_once(di.once, [&di, dev] {
         int major = 0, minor = 0;

@@ -2,6 +2,9 @@
 plain 64-bit form, element by element within the bounds that its roundings give
 (_plain_score.py), and how its calls behave: streams, graphs, workspaces, autograd."""
 import math
+import pathlib
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -510,6 +513,22 @@ def test_autograd_captured():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+
+
+@pytest.mark.parametrize("kw", ["softcap=4.0", "slopes=torch.ones(2, device='cuda')", "prefix=torch.ones(1, dtype=torch.int32, device='cuda')"])
+def test_first_backward_of_a_process(kw):
+    """Autograd's thread has no CUDA context until something binds one; the call's descriptors need it."""
+    code = f"""
+import torch
+from exact_io_aware_12_gb300 import api
+q, k, v = (torch.randn(1, 2, 150, 64, device="cuda").bfloat16().requires_grad_() for _ in range(3))
+grads = torch.autograd.grad(api.attention(q, k, v, True, {kw}), (q, k, v), q.detach().clone())
+torch.cuda.synchronize()
+assert all(bool(t.isfinite().all()) for t in grads)
+"""
+    root = pathlib.Path(__file__).resolve().parent.parent
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 def test_python_refusals_on_the_device():
