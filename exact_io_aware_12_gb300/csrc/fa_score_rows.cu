@@ -27,9 +27,14 @@ namespace fa {
 namespace {
 
 constexpr int kBM = 128, kBN = 128;
-constexpr int kThreads = 576;
 constexpr int kProducerWarp = 16, kMmaWarp = 17;
 constexpr float kLog2e = 1.44269504088896341f;
+
+// Warps that issue products: at d = 128 one for each tile, since one's issue (16 in each block and tile, at 110 cycles
+// each beside busy warps) bounds the kernel (16 heads of 16384 tokens, window 4096: 389 us by one, 325 by two); at
+// d = 64, where it does not, the second costs more (129 us, 148).
+constexpr int mma_warps(int D) { return D == 128 ? 2 : 1; }
+constexpr int threads_for(int D) { return 32 * (kMmaWarp + mma_warps(D)); }
 
 template <int D>
 struct RowsLayout {
@@ -77,7 +82,7 @@ __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 constexpr uint32_t kDescHi = sw128_desc_hi(1024);
 
 template <int D, bool CAP, int BIAS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads_for(D), 1)
 fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO, const RowsParams p) {
     using L = RowsLayout<D>;
@@ -102,7 +107,7 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         mbar_init(bar_q, 1);
         for (int s = 0; s < L::kStages; ++s) {
             mbar_init(bar_kvf + 8 * s, 1);
-            mbar_init(bar_kve + 8 * s, 1);
+            mbar_init(bar_kve + 8 * s, mma_warps(D));
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(bar_full + 8 * t, 1);
@@ -171,7 +176,7 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
             }
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp >= kMmaWarp) {
         // ----------------------------------------------------------------- MMA --
         constexpr uint32_t id = idesc_bf16(128, 128, false, false);
         constexpr uint32_t kStep = L::kTile >> 4;
@@ -186,23 +191,52 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
         };
         const auto kv_in = [&](int ld) { return mbar_wait(bar_kvf + 8 * (ld % L::kStages), (ld / L::kStages) & 1, wd, kSiteMmaKV); };
         bool ok = __all_sync(0xffffffffu, mbar_wait(bar_q, 0, wd, kSiteMmaQ));
-        for (int j = jlo; ok && j < jhi; ++j) {
-            const int lk = 2 * (j - jlo), lv = lk + 1, sk = lk % L::kStages, sv = lv % L::kStages;
-            ok = __all_sync(0xffffffffu, kv_in(lk) && kv_in(lv));
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (!ok || j < lo[t] || j >= hi[t]) continue;
-                if (j > lo[t]) ok = __all_sync(0xffffffffu, mbar_wait(bar_free + 8 * t, (j - lo[t] - 1) & 1, wd, kSiteMmaFree));
-                if (!ok) continue;
+        if constexpr (mma_warps(D) == 2) {
+            const int t = warp - kMmaWarp;
+            const int j0 = t ? lo[1] : lo[0], j1 = t ? hi[1] : hi[0];
+            for (int j = jlo; ok && j < jhi; ++j) {
+                const int lk = 2 * (j - jlo), lv = lk + 1, sk = lk % L::kStages, sv = lv % L::kStages;
+                ok = __all_sync(0xffffffffu, kv_in(lk));
+                if (!ok) break;
+                if (j < j0 || j >= j1) {  // not of this tile
+                    ok = __all_sync(0xffffffffu, kv_in(lv));
+                    if (ok && lane == 0) {
+                        mbar_arrive(bar_kve + 8 * sk);
+                        mbar_arrive(bar_kve + 8 * sv);
+                    }
+                    continue;
+                }
+                if (j > j0) ok = __all_sync(0xffffffffu, mbar_wait(bar_free + 8 * t, (j - j0 - 1) & 1, wd, kSiteMmaFree));
+                if (!ok) break;
                 tc_fence_after();
                 product(tmem + 256 * t, a0 + 2 * t * kStep, ring0 + sk * kStep);                 // S
-                // (K goes back as soon as both tiles' S have read it: its slot is the next V's, wanted a tile's products later)
-                if (t == 1 || j >= hi[1] || j < lo[1]) mma_commit_warp(bar_kve + 8 * sk);
+                mma_commit_warp(bar_kve + 8 * sk);  // (its slot is the next V's, wanted a tile's products later)
+                ok = __all_sync(0xffffffffu, kv_in(lv));
+                if (!ok) break;
+                tc_fence_after();
                 product(tmem + 256 * t + 128, a0 + (2 * t + 1) * kStep, ring0 + sv * kStep);     // dP
                 mma_commit_warp(bar_full + 8 * t);
+                mma_commit_warp(bar_kve + 8 * sv);
             }
-            if (!ok) break;
-            mma_commit_warp(bar_kve + 8 * sv);
+        } else {
+            for (int j = jlo; ok && j < jhi; ++j) {
+                const int lk = 2 * (j - jlo), lv = lk + 1, sk = lk % L::kStages, sv = lv % L::kStages;
+                ok = __all_sync(0xffffffffu, kv_in(lk) && kv_in(lv));
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (!ok || j < lo[t] || j >= hi[t]) continue;
+                    if (j > lo[t]) ok = __all_sync(0xffffffffu, mbar_wait(bar_free + 8 * t, (j - lo[t] - 1) & 1, wd, kSiteMmaFree));
+                    if (!ok) continue;
+                    tc_fence_after();
+                    product(tmem + 256 * t, a0 + 2 * t * kStep, ring0 + sk * kStep);                 // S
+                    // (K goes back as soon as both tiles' S have read it: its slot is the next V's, wanted a tile's products later)
+                    if (t == 1 || j >= hi[1] || j < lo[1]) mma_commit_warp(bar_kve + 8 * sk);
+                    product(tmem + 256 * t + 128, a0 + (2 * t + 1) * kStep, ring0 + sv * kStep);     // dP
+                    mma_commit_warp(bar_full + 8 * t);
+                }
+                if (!ok) break;
+                mma_commit_warp(bar_kve + 8 * sv);
+            }
         }
         __syncwarp();
     } else {
@@ -369,7 +403,7 @@ cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, unsigned* next
     p.far = a.mod.far;
     p.err = a.err;
     p.wait_limit_ns = a.wait_limit_ns;
-    return launch_dependent(kern, dim3(static_cast<unsigned>(BH), static_cast<unsigned>(p.n_pairs)), dim3(kThreads), L::kDynSmem,
+    return launch_dependent(kern, dim3(static_cast<unsigned>(BH), static_cast<unsigned>(p.n_pairs)), dim3(threads_for(D)), L::kDynSmem,
                             stream, tq, tk, tv, tdo, p);
 }
 
