@@ -304,6 +304,30 @@ def test_more_tiles_than_the_sms_hold(kw, d):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,H,Hkv", [(300, 52, 52), (100, 170, 170), (260, 120, 40)])
+@pytest.mark.parametrize("kw", [
+    dict(softcap=5.0), dict(slopes=True, docs=True), dict(table=(32, 128, False)), dict(softcap=20.0, table=(8, 40, True), docs=True),
+    dict(prefix=True, window=90)], ids=lambda kw: "-".join(kw))
+def test_backward_of_more_tiles_than_sms(kw, N, H, Hkv, d):
+    """Two sequences whose key tiles are 240 and more, of one step and of several: an SM takes two or three."""
+    B = 2
+    kw = dict(kw)
+    if kw.get("slopes"):
+        kw["slopes"] = slopes_of(H)
+    if "table" in kw:
+        nb, far, both = kw.pop("table")
+        kw.update(table_of(H, nb, far, both, 5))
+    if kw.get("docs"):
+        kw["docs"] = docs_of(B, N, 6)
+    if kw.get("prefix"):
+        kw["prefix"] = torch.tensor([N // 3, N - 1], dtype=torch.int32)
+    x = inputs(B, H, Hkv, N, d, N + d)
+    check(x, True, **kw)
+    a, b = gpu(x, True, **kw), gpu(x, True, **kw)
+    assert all(torch.equal(p, q) for p, q in zip(a[2][1:], b[2][1:]))
+
+
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("lengths", [[300, 33000, 31, 1, 700, 128, 35000, 577], [66000, 2], [65536, 65536, 500]], ids=str)
 def test_documents_of_long_sequences(lengths, causal):
