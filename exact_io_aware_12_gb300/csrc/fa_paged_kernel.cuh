@@ -697,7 +697,8 @@ fa_paged_kernel(const PagedParams p) {
                         if (p.cap_log2 > 0.f) {
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const float2 th = f2_unpack(tanh2<kTanhExp>(f2_pack(x[e] * p.cap_inv, x[e + 2] * p.cap_inv)));
+                                const uint64_t u = f2_pack(x[e] * p.cap_inv, x[e + 2] * p.cap_inv);
+                                const float2 th = f2_unpack(p.cap_log2 > kCapExact ? tanh2<kTanhSafe>(u) : tanh2<kTanhExp>(u));
                                 x[e] = th.x * p.cap_log2;
                                 x[e + 2] = th.y * p.cap_log2;
                             }

@@ -52,15 +52,30 @@ __device__ __forceinline__ float rcp(float x) {
 // tanh(x) for |x| <= kTanhNear, by x p(x^2): p of degree 3 fitted to least largest error
 // (6e-9), degree 4 up to kTanhMid (1.4e-8); beyond, 1 - 2 / (1 + e^2x) with the
 // hardware's exponential and reciprocal (two of them per score, which a polynomial on the
-// fp32 pipe beats while it is short: forward of 16 heads of 8192 tokens, window 4096, 231 us by
-// the first, 292 by the last).  tanh.approx is off by 2^-11 of its value: 0.02 of a score
+// fp32 pipe beats while it is short: forward of 16 heads of 8192 tokens, window 4096, 229 us by
+// the first, 294 by the last).  tanh.approx is off by 2^-11 of its value: 0.02 of a score
 // capped at 50.
+//
+// The last form is off by up to 2^-23 whatever x, that is, by 2^-23 of the cap: 6e-5 of a score where the cap is
+// kCapExact, but for larger ones too much beside small scores.  There kTanhSafe takes, score by score, the
+// polynomial up to kTanhMid, and is off by 2^-22 of its own value.
 constexpr float kTanhNear = 0.3f, kTanhMid = 0.5f;
-enum : int { kTanhPoly3 = 0, kTanhPoly4 = 1, kTanhExp = 2 };
+constexpr float kCapExact = 1024.f;  // log2 units
+enum : int { kTanhPoly3 = 0, kTanhPoly4 = 1, kTanhExp = 2, kTanhSafe = 3 };
+// A kernel's cap: none, one up to kCapExact, a larger one (kernels of their own: another form in the same ones cost
+// 5 to 10% of those with a common cap).
+enum : int { kCapNone = 0, kCapCommon = 1, kCapLarge = 2 };
+__host__ __device__ constexpr int far_form(int cap) { return cap == kCapLarge ? kTanhSafe : kTanhExp; }
+inline int cap_of(float softcap) {
+    return softcap <= 0.f ? kCapNone : softcap * 1.44269504088896341f > kCapExact ? kCapLarge : kCapCommon;
+}
 // Two values of tanh(x) at once, |x| within the bound of HOW.
 template <int HOW>
 __device__ __forceinline__ uint64_t tanh2(uint64_t x) {
-    if constexpr (HOW == kTanhExp) {
+    if constexpr (HOW == kTanhSafe) {
+        const float2 v = f2_unpack(x), p = f2_unpack(tanh2<kTanhPoly4>(x)), e = f2_unpack(tanh2<kTanhExp>(x));
+        return f2_pack(fabsf(v.x) <= kTanhMid ? p.x : e.x, fabsf(v.y) <= kTanhMid ? p.y : e.y);
+    } else if constexpr (HOW == kTanhExp) {
         constexpr float k = 2.f * 1.44269504088896341f;
         const float2 v = f2_unpack(x);
         return f2_pack(fmaf(-2.f, rcp(1.f + ex2(k * v.x)), 1.f), fmaf(-2.f, rcp(1.f + ex2(k * v.y)), 1.f));
@@ -109,7 +124,9 @@ struct CapScale {
 // Two capped scores plus `add`.
 template <int HOW>
 __device__ __forceinline__ uint64_t cap_score2(const CapScale& c, uint64_t s, uint64_t add) {
-    if constexpr (HOW == kTanhExp) {
+    if constexpr (HOW == kTanhSafe) {
+        return ffma2(tanh2<kTanhSafe>(fmul2(s, c.k_2)), c.cap_2, add);
+    } else if constexpr (HOW == kTanhExp) {
         const float2 v = f2_unpack(s);
         const uint64_t r = f2_pack(rcp(1.f + ex2(c.k_exp * v.x)), rcp(1.f + ex2(c.k_exp * v.y)));
         return ffma2(c.cap_m2, r, fadd2(c.cap_2, add));

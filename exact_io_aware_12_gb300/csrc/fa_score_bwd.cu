@@ -80,7 +80,7 @@ enum : uint32_t {
     kSiteDsS = 77, kSiteDsQ = 78, kSiteDsDP = 79, kSiteDsDQ = 80, kSiteDrain = 81, kSiteReduce = 82
 };
 
-template <bool CAP, int BIAS>
+template <int CAP, int BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
 fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -711,7 +711,7 @@ ScoreBwdParams params_of(const ScoreArgs& a, const BwdPlan& pl) {
     return p;
 }
 
-template <bool CAP, int BIAS>
+template <int CAP, int BIAS>
 cudaError_t launch_main(const ScoreArgs& a, const ScoreBwdParams& p, float* acc, cudaStream_t stream) {
     using L = ScoreBwdLayout;
     CUtensorMap tq, tk, tv, tdo, tacc, tdk, tdv;
@@ -732,6 +732,13 @@ cudaError_t launch_main(const ScoreArgs& a, const ScoreBwdParams& p, float* acc,
     return e;
 }
 
+template <int CAP>
+cudaError_t launch_c(const ScoreArgs& a, const ScoreBwdParams& p, float* acc, cudaStream_t stream) {
+    return a.mod.slopes  ? launch_main<CAP, kBiasSlopes>(a, p, acc, stream)
+           : a.mod.table ? launch_main<CAP, kBiasTable>(a, p, acc, stream)
+                         : launch_main<CAP, kBiasNone>(a, p, acc, stream);
+}
+
 cudaError_t launch_all(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(a.B) * a.H * a.N;
     const ScoreBwdParams p = params_of(a, pl);
@@ -749,9 +756,9 @@ cudaError_t launch_all(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t strea
     if (e != cudaSuccess) return e;
     const bool cap = a.mod.softcap > 0.f;
     if (a.d == 64) e = launch_score_bwd64(a, p, acc, stream);
-    else if (a.mod.slopes) e = cap ? launch_main<true, kBiasSlopes>(a, p, acc, stream) : launch_main<false, kBiasSlopes>(a, p, acc, stream);
-    else if (a.mod.table) e = cap ? launch_main<true, kBiasTable>(a, p, acc, stream) : launch_main<false, kBiasTable>(a, p, acc, stream);
-    else e = cap ? launch_main<true, kBiasNone>(a, p, acc, stream) : launch_main<false, kBiasNone>(a, p, acc, stream);
+    else if (cap_of(a.mod.softcap) == kCapNone) e = launch_c<kCapNone>(a, p, acc, stream);
+    else if (cap_of(a.mod.softcap) == kCapCommon) e = launch_c<kCapCommon>(a, p, acc, stream);
+    else e = launch_c<kCapLarge>(a, p, acc, stream);
     if (e != cudaSuccess) return e;
     const int64_t n8 = rows * a.d / 8;
     return launch_dependent(fa_score_post_kernel, dim3(static_cast<unsigned>(std::min<int64_t>((n8 + 255) / 256, 152 * 64))),

@@ -101,7 +101,7 @@ constexpr int kThreads = 32 * (4 * kNWG + 3);
 // P (1 - tanh^2) waits for dP as fp32, or as fp16 (off by 2^-11 of it down to 2^-29, being lifted by 2^15) where a cap and
 // a bias leave no registers: 16 of 96 a thread.  (fp32 saves the conversions: 16 heads of 8192 tokens, window 4096, d = 128
 // 636 -> 628 us, slopes at d = 64 448 -> 427.)
-constexpr int keep_regs(bool cap, int bias) { return cap && bias != kBiasNone ? 16 : 32; }
+constexpr int keep_regs(int cap, int bias) { return cap != kCapNone && bias != kBiasNone ? 16 : 32; }
 
 // What a thread knows of a step: its key, the side of the pair of tiles, its bias there.
 struct BwdRow {
@@ -117,7 +117,7 @@ struct BwdRow {
 
 // Of one row's scores with queries [q0, q0 + 32): P as bf16 pairs (pk), and P (1 - tanh^2), what dP is to
 // be multiplied by, as fp16 pairs (keep).  nl4: the queries' 15 - LSE log2(e).
-template <bool CAP, int BIAS>
+template <int CAP, int BIAS>
 __device__ __forceinline__ void bwd_weights(const ScoreBwdParams& p, const BwdRow& r, const uint32_t (&sv)[32], const ulonglong2* nl4,
                                             int q0, uint32_t (&pk)[16], uint32_t (&keep)[keep_regs(CAP, BIAS)]) {
     constexpr uint32_t FULL = 0xffffffffu;
@@ -181,7 +181,7 @@ __device__ __forceinline__ void bwd_weights(const ScoreBwdParams& p, const BwdRo
         for (int i = 0; i < 16; ++i) weights(how, general_, i);
     };
     using Poly4 = std::integral_constant<int, kTanhPoly4>;
-    using Exp = std::integral_constant<int, kTanhExp>;
+    using Exp = std::integral_constant<int, far_form(CAP)>;
     if constexpr (CAP) {
         float mx0 = 0.f, mx1 = 0.f;
 #pragma unroll
@@ -206,7 +206,7 @@ __device__ __forceinline__ void bwd_weights(const ScoreBwdParams& p, const BwdRo
 
 // Of the same pairs: dX as bf16 pairs (ds) from dP.  nd4: the queries' -D.  pw: with a cap and SUMS, P.  SUMS: of
 // the table's gradient, for far (1) or near (2) pairs.
-template <bool CAP, int SUMS, int KEEP>
+template <int CAP, int SUMS, int KEEP>
 __device__ __forceinline__ void bwd_products(const uint32_t (&dp)[32], const uint32_t (&keep)[KEEP], [[maybe_unused]] const uint32_t (&pw)[16],
                                              const ulonglong2* nd4, [[maybe_unused]] int lane, uint32_t (&ds)[16],
                                              [[maybe_unused]] uint64_t& fsum, [[maybe_unused]] float& ahead,

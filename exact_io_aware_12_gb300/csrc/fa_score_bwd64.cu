@@ -74,7 +74,7 @@ enum : uint32_t {
     kSiteEwS = 107, kSiteEwDP = 108, kSiteDrain = 109, kSiteReduce = 110
 };
 
-template <bool CAP, int BIAS>
+template <int CAP, int BIAS>
 __global__ void __launch_bounds__(kThreads, 1)
 fa_score_bwd64_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
@@ -541,7 +541,7 @@ fa_score_bwd64_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
     }
 }
 
-template <bool CAP, int BIAS>
+template <int CAP, int BIAS>
 cudaError_t launch_t(const ScoreArgs& a, const ScoreBwdParams& p, float* acc, cudaStream_t stream) {
     CUtensorMap tq, tk, tv, tdo, tacc, tdk, tdv;
     const auto BF = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -562,13 +562,21 @@ cudaError_t launch_t(const ScoreArgs& a, const ScoreBwdParams& p, float* acc, cu
     return e;
 }
 
+template <int CAP>
+cudaError_t launch_c(const ScoreArgs& a, const ScoreBwdParams& p, float* acc, cudaStream_t stream) {
+    return a.mod.slopes  ? launch_t<CAP, kBiasSlopes>(a, p, acc, stream)
+           : a.mod.table ? launch_t<CAP, kBiasTable>(a, p, acc, stream)
+                         : launch_t<CAP, kBiasNone>(a, p, acc, stream);
+}
+
 }  // namespace
 
 cudaError_t launch_score_bwd64(const ScoreArgs& a, const ScoreBwdParams& p, float* acc, cudaStream_t stream) {
-    const bool cap = a.mod.softcap > 0.f;
-    if (a.mod.slopes) return cap ? launch_t<true, kBiasSlopes>(a, p, acc, stream) : launch_t<false, kBiasSlopes>(a, p, acc, stream);
-    if (a.mod.table) return cap ? launch_t<true, kBiasTable>(a, p, acc, stream) : launch_t<false, kBiasTable>(a, p, acc, stream);
-    return cap ? launch_t<true, kBiasNone>(a, p, acc, stream) : launch_t<false, kBiasNone>(a, p, acc, stream);
+    switch (cap_of(a.mod.softcap)) {
+        case kCapNone: return launch_c<kCapNone>(a, p, acc, stream);
+        case kCapCommon: return launch_c<kCapCommon>(a, p, acc, stream);
+        default: return launch_c<kCapLarge>(a, p, acc, stream);
+    }
 }
 
 }  // namespace fa

@@ -46,7 +46,6 @@ constexpr int kBM = 128, kBN = 128;
 constexpr int threads_for(int wgs) { return 128 * wgs + 64; }
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
-constexpr float kCapExact = 1024.f;        // log2 units: 2^-24 of it is 6e-5 of a score
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays <= 2^8
 
 template <int D>
@@ -119,12 +118,13 @@ __device__ __forceinline__ void each_pair(uint32_t (&s)[N][32], F&& f) {
     }
 }
 
-template <int D, bool CAP, int BIAS, int WGS>
+template <int D, int CAP, int BIAS, int WGS>
 __global__ void __launch_bounds__(threads_for(WGS), WGS == 1 ? 2 : 1)
 fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
                     const ScoreFwdParams p) {
     using L = ScoreFwdLayout<D>;
+    [[maybe_unused]] constexpr int kFar = far_form(CAP);
     constexpr bool PIPE = L::kPipe;
     constexpr int kProducerWarp = 4 * WGS, kMmaWarp = 4 * WGS + 1;
     constexpr int kSoftmax = 128 * WGS, kCols = 128 / WGS, kParts = kCols / 32;  // threads; keys of a block per thread
@@ -335,19 +335,19 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                     // passed a bound.  The last form's error is 2^-24 of the cap, whatever the score: not where caps are
                     // in the thousands.)
                     if (how > most) most = how;
-                    else if (most == kTanhPoly4 || p.cap.cap2 <= kCapExact) how = most;
+                    else if (most == kTanhPoly4 || CAP == kCapCommon) how = most;
                     if (BIAS == kBiasNone && !masked) {
                         late = true;
                         const uint64_t v = f2_pack(hi, hi);
                         m_cand = f2_unpack(how == kTanhPoly3   ? cap_score2<kTanhPoly3>(p.cap, v, 0)
                                            : how == kTanhPoly4 ? cap_score2<kTanhPoly4>(p.cap, v, 0)
-                                                               : cap_score2<kTanhExp>(p.cap, v, 0)).x;
+                                                               : cap_score2<kFar>(p.cap, v, 0)).x;
                     } else if (how == kTanhPoly3) {
                         each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhPoly3>(p.cap, v, 0); });
                     } else if (how == kTanhPoly4) {
                         each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhPoly4>(p.cap, v, 0); });
                     } else {
-                        each_pair(s, [&](int, uint64_t v) { return cap_score2<kTanhExp>(p.cap, v, 0); });
+                        each_pair(s, [&](int, uint64_t v) { return cap_score2<kFar>(p.cap, v, 0); });
                     }
                 }
                 if constexpr (BIAS == kBiasSlopes) {
@@ -463,7 +463,7 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
             } else if (CAP && late) {
                 if (how == kTanhPoly3) weights([&](uint64_t v) { return cap_score2<kTanhPoly3>(p.cap, v, nm2); });
                 else if (how == kTanhPoly4) weights([&](uint64_t v) { return cap_score2<kTanhPoly4>(p.cap, v, nm2); });
-                else weights([&](uint64_t v) { return cap_score2<kTanhExp>(p.cap, v, nm2); });
+                else weights([&](uint64_t v) { return cap_score2<kFar>(p.cap, v, nm2); });
             } else {
                 weights([&](uint64_t v) { return SCALED ? fadd2(v, nm2) : ffma2(v, c2, nm2); });
             }
@@ -544,7 +544,7 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
     }
 }
 
-template <int D, bool CAP, int BIAS, int WGS>
+template <int D, int CAP, int BIAS, int WGS>
 cudaError_t launch_w(const ScoreArgs& a, cudaStream_t stream) {
     using L = ScoreFwdLayout<D>;
     CUtensorMap tq, tk, tv, to;
@@ -590,18 +590,27 @@ cudaError_t launch_w(const ScoreArgs& a, cudaStream_t stream) {
 // Two softmax warpgroups where there are at most two tiles for each SM, and the chain of steps of the longest sets the
 // time (16 heads, d = 64: 901 tokens with slopes 15.0 us by one and 12.6 by two, 2000 capped 41.3 and 30.9, 4096
 // capped 84 and 108).
-template <int D, bool CAP, int BIAS>
+template <int D, int CAP, int BIAS>
 cudaError_t launch_t(const ScoreArgs& a, cudaStream_t stream) {
     const long long ctas = static_cast<long long>(a.B) * a.H * ((a.N + kBM - 1) / kBM);
-    return ctas <= 2 * kSms ? launch_w<D, CAP, BIAS, 2>(a, stream) : launch_w<D, CAP, BIAS, 1>(a, stream);
+    if constexpr (CAP == kCapLarge) return launch_w<D, CAP, BIAS, 1>(a, stream);  // (rare: one form)
+    else return ctas <= 2 * kSms ? launch_w<D, CAP, BIAS, 2>(a, stream) : launch_w<D, CAP, BIAS, 1>(a, stream);
+}
+
+template <int D, int CAP>
+cudaError_t launch_c(const ScoreArgs& a, cudaStream_t stream) {
+    return a.mod.slopes  ? launch_t<D, CAP, kBiasSlopes>(a, stream)
+           : a.mod.table ? launch_t<D, CAP, kBiasTable>(a, stream)
+                         : launch_t<D, CAP, kBiasNone>(a, stream);
 }
 
 template <int D>
 cudaError_t launch_d(const ScoreArgs& a, cudaStream_t stream) {
-    const bool cap = a.mod.softcap > 0.f;
-    if (a.mod.slopes) return cap ? launch_t<D, true, kBiasSlopes>(a, stream) : launch_t<D, false, kBiasSlopes>(a, stream);
-    if (a.mod.table) return cap ? launch_t<D, true, kBiasTable>(a, stream) : launch_t<D, false, kBiasTable>(a, stream);
-    return cap ? launch_t<D, true, kBiasNone>(a, stream) : launch_t<D, false, kBiasNone>(a, stream);
+    switch (cap_of(a.mod.softcap)) {
+        case kCapNone: return launch_c<D, kCapNone>(a, stream);
+        case kCapCommon: return launch_c<D, kCapCommon>(a, stream);
+        default: return launch_c<D, kCapLarge>(a, stream);
+    }
 }
 
 }  // namespace

@@ -81,7 +81,7 @@ __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 
 constexpr uint32_t kDescHi = sw128_desc_hi(1024);
 
-template <int D, bool CAP, int BIAS>
+template <int D, int CAP, int BIAS>
 __global__ void __launch_bounds__(threads_for(D), 1)
 fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO, const RowsParams p) {
@@ -330,7 +330,7 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
                     for (int i = 0; i < 16; ++i) one(how, general_, i);
                 };
                 using Poly4 = std::integral_constant<int, kTanhPoly4>;
-                using Exp = std::integral_constant<int, kTanhExp>;
+                using Exp = std::integral_constant<int, far_form(CAP)>;
                 if constexpr (CAP) {
                     float mx0 = 0.f, mx1 = 0.f;
 #pragma unroll
@@ -369,7 +369,7 @@ fa_score_rows_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_const
     }
 }
 
-template <int D, bool CAP, int BIAS>
+template <int D, int CAP, int BIAS>
 cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, unsigned* next, const void* spans, const int* order,
                      const float* bias2, cudaStream_t stream) {
     using L = RowsLayout<D>;
@@ -407,18 +407,22 @@ cudaError_t launch_t(const ScoreArgs& a, float* dvec, float* acc, unsigned* next
                             stream, tq, tk, tv, tdo, p);
 }
 
+template <int D, int CAP>
+cudaError_t launch_c(const ScoreArgs& a, float* dvec, float* acc, unsigned* next, const void* spans, const int* order,
+                     const float* bias2, cudaStream_t stream) {
+    return a.mod.slopes  ? launch_t<D, CAP, kBiasSlopes>(a, dvec, acc, next, spans, order, bias2, stream)
+           : a.mod.table ? launch_t<D, CAP, kBiasTable>(a, dvec, acc, next, spans, order, bias2, stream)
+                         : launch_t<D, CAP, kBiasNone>(a, dvec, acc, next, spans, order, bias2, stream);
+}
+
 template <int D>
 cudaError_t launch_d(const ScoreArgs& a, float* dvec, float* acc, unsigned* next, const void* spans, const int* order,
                      const float* bias2, cudaStream_t stream) {
-    const bool cap = a.mod.softcap > 0.f;
-    if (a.mod.slopes)
-        return cap ? launch_t<D, true, kBiasSlopes>(a, dvec, acc, next, spans, order, bias2, stream)
-                   : launch_t<D, false, kBiasSlopes>(a, dvec, acc, next, spans, order, bias2, stream);
-    if (a.mod.table)
-        return cap ? launch_t<D, true, kBiasTable>(a, dvec, acc, next, spans, order, bias2, stream)
-                   : launch_t<D, false, kBiasTable>(a, dvec, acc, next, spans, order, bias2, stream);
-    return cap ? launch_t<D, true, kBiasNone>(a, dvec, acc, next, spans, order, bias2, stream)
-               : launch_t<D, false, kBiasNone>(a, dvec, acc, next, spans, order, bias2, stream);
+    switch (cap_of(a.mod.softcap)) {
+        case kCapNone: return launch_c<D, kCapNone>(a, dvec, acc, next, spans, order, bias2, stream);
+        case kCapCommon: return launch_c<D, kCapCommon>(a, dvec, acc, next, spans, order, bias2, stream);
+        default: return launch_c<D, kCapLarge>(a, dvec, acc, next, spans, order, bias2, stream);
+    }
 }
 
 }  // namespace

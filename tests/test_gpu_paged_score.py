@@ -120,6 +120,22 @@ def test_windows_and_sinks(mod, fp8):
     check([3000, 100, 700], 4, 4, 1, 64, 16, fp8, window=1, **MODS[mod](4))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("cap", [2.0 ** 14, 2.0 ** 20, 2.0 ** 60])
+def test_large_caps_leave_scores_as_they_are(cap, fp8):
+    """x / cap below 2^-11: cap tanh(x / cap) is x within 2^-23 of it, as one fp32 rounding, of which the bounds
+    without a cap give q.k's own sum d."""
+    for lens, H, Hkv, Nq, d, page in (([130, 517, 33], 12, 12, 1, 64, 16), ([2500, 2500, 1700], 32, 2, 4, 128, 64)):
+        c = pool(lens, Hkv, page, d, 5, fp8)
+        q = torch.randn(len(lens), H, Nq, d, generator=c["gen"]).to(BF)
+        a = dev({n: t for n, t in c.items() if n != "gen"})
+        scales = {n: a[n] for n in ("k_scale", "v_scale") if n in a}
+        o, lse = api.fwd_paged(q.to(DEV), a["k"], a["v"], a["table"], a["lens"], softcap=cap, **scales)
+        eo, el, bo, bl = exact(c, q, d ** -0.5)
+        within(o, eo, bo, "O")
+        within(lse, el, bl, "LSE")
+
+
 def test_all_fields_unset_is_the_plain_step():
     c = pool([100, 900], 2, 16, 64, 3, False)
     q = torch.randn(2, 4, 1, 64, generator=c["gen"]).to(BF).to(DEV)

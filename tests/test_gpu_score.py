@@ -257,6 +257,27 @@ def test_random_calls():
             check(inputs(B, H, Hkv, N, d, 500 + i, 1 + r(0, 2) / 2), causal, **kw)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+def test_small_scores_beside_scores_of_a_large_cap(causal, d):
+    """Rows whose scores are of deviation one, between rows whose scores reach a cap of 2^20: 2^-23 of the
+    cap would be 0.1 of a score.  The weights of the former are flat, so that O and dQ of these rows are within
+    sqrt(2/3) 2^-8 (as above), and their LSE within what fp32 gives a score of one."""
+    N, cap = 300, 2.0 ** 20
+    x = inputs(2, 2, 1, N, d, 14)
+    # (powers of two, exact in bf16: sqrt(d) deviates q.k; 8 = 64^(1/2))
+    grow = torch.full((N, 1), 2.0 ** 8)
+    grow[::2] = 2.0 ** -11
+    x["q"], x["k"] = (x["q"].float() * grow).to(BF), (x["k"].float() * 2.0 ** 8).to(BF)
+    o, lse, (dq, dk, dv) = gpu(x, causal, 1.0, softcap=cap)
+    e = Exact(x["q"], x["k"], x["v"], causal, 1.0, x["do"], softcap=cap)
+    far = (x["q"].double() @ x["k"].double().mT).abs().amax(-1)
+    assert float(far[..., 1::2].amax()) > 0.6 * cap and float(far[..., ::2].amax()) < 100
+    for got, n in ((o, "o"), (dq, "dq")):
+        assert rel_l2(got[:, :, ::2], getattr(e, n)[:, :, ::2]) <= 1.25 * math.sqrt(2 / 3) * 2.0 ** -8, n
+    assert float((lse.cpu().double() - e.lse)[:, :, ::2].abs().max()) < 1e-4
+
+
 def test_other_scales_of_scores():
     x = inputs(1, 2, 2, 200, 64, 8)
     for tau in (1e-3, 1.0, 4.0):
