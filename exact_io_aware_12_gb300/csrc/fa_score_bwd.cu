@@ -235,7 +235,7 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
         // ----------------------------------------------------------------- MMA --
         const uint32_t k_lo = sw128_desc_lo(sbase + L::kK, 16), k_mn = sw128_desc_lo(sbase + L::kK, kLboMN);
         const uint32_t v_lo = sw128_desc_lo(sbase + L::kV, 16);
-        const uint32_t ds_mn = sw128_desc_lo(sbase + L::kDS, kLboMN), ds_lo = sw128_desc_lo(sbase + L::kDS, 16);
+        const uint32_t ds_mn = sw128_desc_lo(sbase + L::kDS, kLboMN);
         const uint32_t q_lo0 = sw128_desc_lo(sbase + L::kStage0, 16);
         const uint32_t q_mn0 = sw128_desc_lo(sbase + L::kStage0, kLboMN);
         const uint32_t do_lo0 = sw128_desc_lo(sbase + L::kStage0 + L::kTile, 16);
