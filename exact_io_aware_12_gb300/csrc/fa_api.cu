@@ -1013,12 +1013,21 @@ fa_status fa_bwd_score(const void* Q, const void* K, const void* V, const void* 
     if (dBias != nullptr && a.mod.table == nullptr) return FA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(dBias) & (a.mod.table_f32 ? 3u : 1u)) != 0) return FA_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (empty) {  // (no pair: a gradient of zeros)
-        if (dBias == nullptr || mod.table == 0) return FA_OK;
-        const Buffer bs[] = {{dBias, mod.table}, {a.mod.table, mod.table}, {a.mod.buckets, mod.buckets}};
-        if (!apart(bs, 1, 3)) return FA_ERR_INVALID_ARG;
+    if (empty) {  // (no pair: gradients of zeros, of a bias, or of keys that no query head reads)
+        bool none = false;
+        s = check_shape(B, H_kv, N, d, tau, causal, &none);
+        if (s != FA_OK) return s;
+        const size_t kb = none ? 0 : static_cast<size_t>(B) * H_kv * N * d * 2, tb = dBias ? mod.table : 0;
+        if (kb > 0 && (dK == nullptr || dV == nullptr || !aligned16(dK) || !aligned16(dV))) return FA_ERR_INVALID_ARG;
+        const auto of = [](const void* p, size_t n) { return Buffer{n > 0 ? p : nullptr, n}; };
+        const Buffer bs[] = {of(dK, kb), of(dV, kb), of(dBias, tb), of(K, kb), of(V, kb), of(a.mod.table, mod.table),
+                             of(a.mod.buckets, mod.buckets), of(a.mod.docs, mod.docs), of(a.mod.prefix, mod.prefix)};
+        if (!apart(bs, 3, 9)) return FA_ERR_INVALID_ARG;
+        if (kb == 0 && tb == 0) return FA_OK;
         if (!current_device(&s)) return s;
-        return map_cuda(cudaMemsetAsync(dBias, 0, mod.table, st));
+        for (int i = 0; i < 3; ++i)
+            if (bs[i].p != nullptr && cudaMemsetAsync(const_cast<void*>(bs[i].p), 0, bs[i].n, st) != cudaSuccess) return FA_ERR_CUDA;
+        return FA_OK;
     }
     const void* ptrs[] = {Q, K, V, O, dO, LSE, dQ, dK, dV};
     for (const void* p : ptrs)

@@ -274,7 +274,7 @@ FA_API fa_status fa_fwd_score(const void* Q, const void* K, const void* V, void*
  * Backward of fa_fwd_score (LSE as it wrote it for the same inputs; O is checked but not read: its
  * product with dO is summed anew from the weights, unrounded): dQ [B][H][N][d], dK,
  * dV [B][H_kv][N][d], summed over the query heads that share a key head; every element is
- * written.  dBias: with a bias its gradient [num_buckets][H], of its type (every element
+ * written (without query heads, H = 0, dK and dV are zeros).  dBias: with a bias its gradient [num_buckets][H], of its type (every element
  * written; buckets of no visible pair get 0), or NULL: not computed.  It is summed in fp32 in a
  * fixed order and rounded once.  (dQ's order of summation is not fixed, as in fa_bwd.)
  * workspace: fa_bwd_score_workspace_size bytes; NULL as in fa_fwd_score.

@@ -480,6 +480,16 @@ def test_no_rows():
         assert not g[3].any()
 
 
+def test_keys_that_no_query_head_reads():
+    """No query heads beside key heads: dK and dV are zeros."""
+    q, k = torch.empty(2, 0, 300, 64, dtype=BF, device=DEV), torch.ones(2, 3, 300, 64, dtype=BF, device=DEV)
+    for kw in (dict(softcap=5.0), dict(docs=torch.zeros(2, 300, dtype=torch.int32, device=DEV))):
+        o, lse = api.fwd(q, k, k, True, **kw)
+        dk, dv = torch.ones_like(k), torch.ones_like(k)
+        g = api.bwd(q, k, k, o, o, lse, True, dk=dk, dv=dv, **kw)
+        assert g[0].shape == q.shape and not g[1].any() and not g[2].any()
+
+
 def test_side_stream_and_device_argument():
     """Inputs made on another stream, the call on a stream of its own."""
     x = inputs(1, 4, 4, 900, 128, 33)

@@ -253,6 +253,15 @@ def test_refusals_of_one_side():
     assert calls(score(**dict(TABLE, bias_f32=1)), dBias=FAKE + 23 * GB + 2)[1] == BAD
 
 
+def test_keys_that_no_query_head_reads():
+    """H = 0 beside H_kv key heads: the backward still writes dK and dV, and checks them."""
+    for kw, code in [(dict(dK=None), BAD), (dict(dV=None), BAD), (dict(dK=FAKE + 7 * GB + 8), BAD), (dict(dV=FAKE + 7 * GB), BAD),
+                     (dict(dK=FAKE + GB), BAD), (dict(dV=FAKE + 2 * GB), BAD), (dict(d=96), UN), (dict(N=65535 * 128 + 1), UN)]:
+        assert calls(score(), H=0, **kw)[1] == code, kw
+    assert calls(score(docs=FAKE + 7 * GB), H=0)[1] == BAD
+    assert calls(score(), H=0, N=0, dK=None) == calls(score(), H=0, B=0, dV=None) == (OK, OK)
+
+
 def test_workspace_sizes():
     size = lambda B=2, H=4, N=300, d=64, causal=1, **f: _lib.fa_bwd_score_workspace_size(B, H, N, d, causal, score(**f))
     base = size()
