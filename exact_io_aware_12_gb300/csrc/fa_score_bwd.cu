@@ -387,11 +387,12 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                     const int qh = q_start + kQC * hw;
                     const bool general = q_start < clear_lo || q_start + kBQ > clear_hi || (BIAS != kBiasNone && side == 0);
                     const BwdRow row{kg, mine.lo, static_cast<uint32_t>(mine.hi - mine.lo), general, side, slope2, bias2, far_bias};
-                    uint32_t sv[32], pk[16];
+                    uint32_t sv[32], pk[16], pw[16];
                     tmem_ld32(tS, sv);
                     tmem_ld_wait(sv);
-                    bwd_weights<CAP, BIAS>(p, row, sv, nl4, qh, pk, keep);
+                    bwd_weights<CAP, BIAS>(p, row, sv, nl4, qh, pk, keep, pw);
                     tmem_st16(tS, pk);
+                    if constexpr (CAP && BIAS == kBiasTable) tmem_st16(tS + kQC / 2, pw);  // (until dX takes its columns)
                     tmem_st_wait();
                     tc_fence_before();
                 }
@@ -409,9 +410,9 @@ fa_score_bwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                     }
                     uint32_t dp[32], ds[16];
                     tmem_ld32(tDP, dp);
-                    [[maybe_unused]] uint32_t pw[16];  // CAP: P itself
+                    [[maybe_unused]] uint32_t pw[16];  // CAP: P itself, fp16
                     if constexpr (CAP && BIAS == kBiasTable) {
-                        tmem_ld16(tS, pw);
+                        tmem_ld16(tS + kQC / 2, pw);
                         tmem_ld_wait(pw);
                     }
                     tmem_ld_wait(dp);

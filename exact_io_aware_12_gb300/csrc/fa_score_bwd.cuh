@@ -116,10 +116,12 @@ struct BwdRow {
 };
 
 // Of one row's scores with queries [q0, q0 + 32): P as bf16 pairs (pk), and P (1 - tanh^2), what dP is to
-// be multiplied by, as fp16 pairs (keep).  nl4: the queries' 15 - LSE log2(e).
+// be multiplied by, as fp16 pairs (keep).  With a cap and a table, whose gradient takes P itself, P as fp16 pairs, too
+// (pw).  nl4: the queries' 15 - LSE log2(e).
 template <int CAP, int BIAS>
 __device__ __forceinline__ void bwd_weights(const ScoreBwdParams& p, const BwdRow& r, const uint32_t (&sv)[32], const ulonglong2* nl4,
-                                            int q0, uint32_t (&pk)[16], uint32_t (&keep)[keep_regs(CAP, BIAS)]) {
+                                            int q0, uint32_t (&pk)[16], uint32_t (&keep)[keep_regs(CAP, BIAS)],
+                                            [[maybe_unused]] uint32_t (&pw)[16]) {
     constexpr uint32_t FULL = 0xffffffffu;
     const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
     [[maybe_unused]] const uint64_t k2 = f2_pack(p.x_scale, p.x_scale), cap2 = f2_pack(p.cap_log2, p.cap_log2);
@@ -164,6 +166,7 @@ __device__ __forceinline__ void bwd_weights(const ScoreBwdParams& p, const BwdRo
             if (static_cast<uint32_t>(q + 1 - from) >= r.seen) p1 = 0.f;
         }
         pk[i] = pack_bf16(p0, p1);
+        if constexpr (CAP && BIAS == kBiasTable) pw[i] = pack_f16(p0, p1);
         if constexpr (CAP) {  // (tanh^2 - 1: dX, dK and dQ come with their sign turned)
             const float2 k = f2_unpack(fmul2(f2_pack(p0, p1), ffma2(th, th, f2_pack(-1.f, -1.f))));
             p0 = k.x;
@@ -205,7 +208,11 @@ __device__ __forceinline__ void bwd_weights(const ScoreBwdParams& p, const BwdRo
 }
 
 // Of the same pairs: dX as bf16 pairs (ds) from dP.  nd4: the queries' -D.  pw: with a cap and SUMS, P.  SUMS: of
-// the table's gradient, for far (1) or near (2) pairs.
+// the table's gradient, for far (1) or near (2) pairs: sums of dY = P (dP - D), in which a far bucket's pairs, almost
+// all of a row's weight, nearly cancel.  So P is not the product's bf16 one there: 32 buckets, cap 50, 2500 tokens, an fp32
+// gradient off by 1.7e-3 to 2.7e-3 with that, by 1.5e-4 to 3.9e-4 with fp16 of 2^15 times it (backward of 16 heads of 4096
+// tokens at d = 128 328 -> 335 us, 48 of 2048 both ways at d = 64 417 -> 436; packed only where the gradient is wanted, by a
+// branch, 395 and 500).
 template <int CAP, int SUMS, int KEEP>
 __device__ __forceinline__ void bwd_products(const uint32_t (&dp)[32], const uint32_t (&keep)[KEEP], [[maybe_unused]] const uint32_t (&pw)[16],
                                              const ulonglong2* nd4, [[maybe_unused]] int lane, uint32_t (&ds)[16],
@@ -222,7 +229,10 @@ __device__ __forceinline__ void bwd_products(const uint32_t (&dp)[32], const uin
         ds[i] = pack_bf16(dx.x, dx.y);
         if constexpr (SUMS != 0) {
             uint64_t dy = d2;
-            if constexpr (CAP) dy = fmul2(f2_pack(u2f(pw[i] << 16), u2f(pw[i] & 0xffff0000u)), t2);
+            if constexpr (CAP) {
+                const float2 w = unpack_f16(pw[i]);
+                dy = fmul2(f2_pack(w.x, w.y), t2);
+            }
             if constexpr (SUMS == 1) {
                 fsum = fadd2(fsum, dy);
             } else {

@@ -451,6 +451,7 @@ fa_score_bwd64_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                     for (int i = 0; i < tile.per_head; ++i, ++s) {
                         const int q_start = (tile.first + i) * kBQ, qh = q_start + kQC * hw;
                         const uint32_t tS = lanes + L::kTmS + 128 * (s & 1);
+                        [[maybe_unused]] const uint32_t tPW = tS + L::kTmDQ + kQC / 2 * hw;  // (until dQ takes its columns)
                         uint32_t keep[keep_regs(CAP, BIAS)];  // P (1 - tanh^2)
                         row.side = far_side(q_start, kvs, kBQ, BIAS == kBiasTable ? p.far : 0);
                         row.general = q_start < tile.clear_lo || q_start + kBQ > tile.clear_hi || (BIAS != kBiasNone && row.side == 0);
@@ -469,10 +470,11 @@ fa_score_bwd64_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                             __syncwarp();
                             if (lane == 0) mbar_arrive(bar_sr + 8 * (warp & 3));
                             const ulonglong2* nl4 = reinterpret_cast<const ulonglong2*>(lse2_s + s % 3 * 128 + kQC * hw);
-                            uint32_t pk[16];
-                            bwd_weights<CAP, BIAS>(p, row, sv, nl4, qh, pk, keep);
+                            uint32_t pk[16], pw[16];
+                            bwd_weights<CAP, BIAS>(p, row, sv, nl4, qh, pk, keep, pw);
                             if (!wait(bar_sr + 8 * (warp & 3), s, kSiteEwS)) return;
                             tmem_st16(tS + kQC / 2 * hw, pk);
+                            if constexpr (CAP && BIAS == kBiasTable) tmem_st16(tPW, pw);
                             tmem_st_wait();
                             tc_fence_before();
                             mbar_arrive(bar_p);
@@ -493,9 +495,9 @@ fa_score_bwd64_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_cons
                         }
                         uint32_t dp[32], ds[16];
                         tmem_ld32(tDP, dp);
-                        [[maybe_unused]] uint32_t pw[16];  // CAP: P itself
+                        [[maybe_unused]] uint32_t pw[16];  // CAP: P itself, fp16
                         if constexpr (CAP && BIAS == kBiasTable) {
-                            tmem_ld16(tS + kQC / 2 * hw, pw);
+                            tmem_ld16(tPW, pw);
                             tmem_ld_wait(pw);
                         }
                         tmem_ld_wait(dp);

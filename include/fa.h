@@ -276,7 +276,8 @@ FA_API fa_status fa_fwd_score(const void* Q, const void* K, const void* V, void*
  * dV [B][H_kv][N][d], summed over the query heads that share a key head; every element is
  * written (without query heads, H = 0, dK and dV are zeros).  dBias: with a bias its gradient [num_buckets][H], of its type (every element
  * written; buckets of no visible pair get 0), or NULL: not computed.  It is summed in fp32 in a
- * fixed order and rounded once.  (dQ's order of summation is not fixed, as in fa_bwd.)
+ * fixed order and rounded once, of weights in fp32 or, with a cap, off by at most 2^-11 of
+ * themselves down to 2^-29.  (dQ's order of summation is not fixed, as in fa_bwd.)
  * workspace: fa_bwd_score_workspace_size bytes; NULL as in fa_fwd_score.
  */
 FA_API size_t fa_bwd_score_workspace_size(int B, int H, int N, int d, int causal,

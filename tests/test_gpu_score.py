@@ -11,7 +11,7 @@ import torch
 
 from exact_io_aware_12_gb300 import api, _lib
 from tests import _plain_score
-from tests._plain_score import Exact, within
+from tests._plain_score import BF16_HALF, Exact, within
 from tests._parity import rel_l2
 
 pytestmark = pytest.mark.gpu
@@ -299,6 +299,36 @@ def test_bias_gradient_is_as_exact_at_length(causal):
     e = Exact(x["q"], x["k"], x["v"], causal, 0.125, x["do"], **t)
     off = float((grads[3].cpu().double() - e.dbias).norm())
     assert off <= 1.25 * e.s_dbias and off <= 2.0 ** -10 * float(e.dbias.norm())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+def test_capped_bias_gradient_is_as_exact_at_length(causal, d):
+    """The same with a cap.  P of the sums as fp16 leaves 2^-11 / sqrt(3) of each pair's dY, 4.2e-4 of the whole at
+    most on these inputs by the variances' sum (with bf16, 3.4e-3): below 2^-10 with twice that and fp32's part."""
+    x = inputs(1, 2, 2, 2500, d, 77)
+    t = table_of(2, 32, 128, not causal, 7, torch.float32)
+    *_, grads = gpu(x, causal, softcap=50.0, **t)
+    e = Exact(x["q"], x["k"], x["v"], causal, d ** -0.5, x["do"], softcap=50.0, **t)
+    assert float((grads[3].cpu().double() - e.dbias).norm()) <= 2.0 ** -10 * float(e.dbias.norm())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,nb,far,causal,cap", [(77, 4, 9, True, 3.0), (300, 32, 128, False, 8.0), (517, 32, 40, True, 50.0),
+                                                 (700, 8, 300, False, 2.0 ** 12)])
+def test_capped_bias_gradient_by_buckets(N, nb, far, causal, cap, d):
+    """Bucket by bucket: P off by 2^-11 of itself, as without a cap."""
+    x = inputs(2, 4, 2, N, d, N + d)
+    t = table_of(4, nb, far, not causal, 7, torch.float32)
+    *_, grads = gpu(x, causal, softcap=cap, **t)
+    e = Exact(x["q"], x["k"], x["v"], causal, d ** -0.5, x["do"], softcap=cap, **t)
+    do, v = x["do"].double(), x["v"].double().repeat_interleave(2, 1)
+    dy = e.p * (do @ v.mT - (do * e.o).sum(-1, keepdim=True))
+    L = t["buckets"].numel() // 2
+    dist = torch.arange(N)[:, None] - torch.arange(N)[None, :]
+    at = t["buckets"].long()[dist.clamp(-L, L) + L].flatten()
+    size = torch.zeros(nb, 4, dtype=torch.float64).index_add_(0, at, dy.abs().sum(0).flatten(1).T)
+    within(grads[3], e.dbias, e.b_dbias - BF16_HALF * size, "dbias")
 
 
 @pytest.mark.parametrize("d", [64, 128])
