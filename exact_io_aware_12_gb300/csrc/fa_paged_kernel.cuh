@@ -704,12 +704,12 @@ fa_paged_kernel(const PagedParams p) {
                             }
                         }
                         if (p.slopes) {
-                            const float k0 = static_cast<float>(key0 + g), k1 = static_cast<float>(key0 + g + 8);
+                            // (j - i as a whole number first: positions beyond 2^24 are not exact in fp32, near distances are)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
-                                const float la = static_cast<float>(last[nt][e]);
-                                x[e] = fmaf(mod_f[nt][e], k0 - la, x[e]);
-                                x[e + 2] = fmaf(mod_f[nt][e], k1 - la, x[e + 2]);
+                                const float dist = static_cast<float>(key0 + g - last[nt][e]);
+                                x[e] = fmaf(mod_f[nt][e], dist, x[e]);
+                                x[e + 2] = fmaf(mod_f[nt][e], dist + 8.f, x[e + 2]);
                             }
                         } else if (p.bias) {
 #pragma unroll

@@ -136,6 +136,26 @@ def test_large_caps_leave_scores_as_they_are(cap, fp8):
         within(lse, el, bl, "LSE")
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_slopes_of_positions_beyond_2_24(d, fp8):
+    """16778217 keys of 64 pages that take turns: positions that fp32 does not hold, distances that it does.  Keys
+    more than 8000 away weigh less than e^-380 of the rest (scores are below 10), so that the last 64 pages alone give
+    the same."""
+    page, pages, L = 128, 64, 2 ** 24 + 1001
+    c = pool([page * pages], 2, page, d, 3, fp8)
+    q = torch.randn(1, 4, 3, d, generator=c["gen"]).to(BF)
+    slopes = torch.tensor([1.0, 0.7, 0.25, 0.05])
+    c["table"] = (torch.arange(-(-L // page)) % pages).to(torch.int32)[None]
+    c["lens"] = torch.tensor([L], dtype=torch.int32)
+    o, lse = run(c, q, slopes=slopes)
+    c["table"] = c["table"][:, -pages:].contiguous()
+    c["lens"] = torch.tensor([(pages - 1) * page + L % page], dtype=torch.int32)
+    eo, el, bo, bl = exact(c, q, d ** -0.5, slopes=slopes)
+    within(o, eo, bo, "O")
+    within(lse, el, bl, "LSE")
+
+
 def test_all_fields_unset_is_the_plain_step():
     c = pool([100, 900], 2, 16, 64, 3, False)
     q = torch.randn(2, 4, 1, 64, generator=c["gen"]).to(BF).to(DEV)
