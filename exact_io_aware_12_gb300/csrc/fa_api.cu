@@ -32,17 +32,22 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+typedef CUresult (*CtxGetCurrentFn)(CUcontext*);
+
+// A function of the driver as of a CUDA version, or null.
+void* driver_fn(const char* name, unsigned version) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+        return nullptr;
+    return p;
+}
 EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
+    static const EncodeTiledFn fn = reinterpret_cast<EncodeTiledFn>(driver_fn("cuTensorMapEncodeTiled", 12000));
+    return fn;
+}
+CtxGetCurrentFn get_current_fn() {
+    static const CtxGetCurrentFn fn = reinterpret_cast<CtxGetCurrentFn>(driver_fn("cuCtxGetCurrent", 4000));
     return fn;
 }
 
@@ -64,15 +69,14 @@ DeviceInfo* current_device(fa_status* why) {
         return nullptr;
     }
     // A thread that has made no call of the runtime that needs one (autograd's workers are such) has no current
-    // context, without which descriptors cannot be encoded.
-    static thread_local int bound = -1;
-    if (bound != dev) {
-        if (cudaSetDevice(dev) != cudaSuccess) {
-            cudaGetLastError();
-            *why = FA_ERR_CUDA;
-            return nullptr;
-        }
-        bound = dev;
+    // context, without which descriptors cannot be encoded: it gets the device's primary one.  A context that the
+    // caller has made current stays.
+    CUcontext now = nullptr;
+    const CtxGetCurrentFn get_current = get_current_fn();
+    if (get_current == nullptr || get_current(&now) != CUDA_SUCCESS || (now == nullptr && cudaSetDevice(dev) != cudaSuccess)) {
+        cudaGetLastError();
+        *why = FA_ERR_CUDA;
+        return nullptr;
     }
     DeviceInfo& di = g_dev[dev];
     std::call_once(di.once, [&di, dev] {

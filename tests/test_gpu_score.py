@@ -1,10 +1,12 @@
 """GPU parity of attention with capped, biased or masked scores (fa_fwd_score, fa_bwd_score) against the
 plain 64-bit form, element by element within the bounds that its roundings give
 (_plain_score.py), and how its calls behave: streams, graphs, workspaces, autograd."""
+import ctypes
 import math
 import pathlib
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
@@ -614,6 +616,47 @@ assert all(bool(t.isfinite().all()) for t in grads)
     root = pathlib.Path(__file__).resolve().parent.parent
     done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_a_context_of_the_caller_stays():
+    """A context made and bound through the driver's interface is current after a call as before it."""
+    code = """
+import ctypes
+from exact_io_aware_12_gb300 import _lib
+cuda = ctypes.CDLL("libcuda.so.1")
+own, now = ctypes.c_void_p(), ctypes.c_void_p()
+assert cuda.cuInit(0) == 0 and cuda.cuCtxCreate_v2(ctypes.byref(own), 0, 0) == 0
+code = _lib.fa_last_device_error(None)
+assert cuda.cuCtxGetCurrent(ctypes.byref(now)) == 0
+assert cuda.cuCtxDestroy_v2(own) == 0
+assert code == _lib.FA_OK and now.value == own.value
+"""
+    root = pathlib.Path(__file__).resolve().parent.parent
+    done = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
+
+
+def test_a_thread_whose_context_is_taken_away():
+    """Two backward calls of a thread that drops its context behind each."""
+    x = {n: t.to(DEV) for n, t in inputs(1, 2, 2, 150, 64, 22).items()}
+    o, lse = api.fwd(x["q"], x["k"], x["v"], True, softcap=3.0)
+    want = api.bwd(x["q"], x["k"], x["v"], o, x["do"], lse, True, softcap=3.0)
+    g = [torch.empty_like(x["q"]) for _ in range(3)]
+    ws = torch.empty(api.score_workspace_bytes(x["q"], True), dtype=torch.uint8, device=DEV)
+    at = [t.data_ptr() for t in (x["q"], x["k"], x["v"], o, x["do"], lse, *g)]
+    torch.cuda.synchronize()
+    cuda, codes = ctypes.CDLL("libcuda.so.1"), []
+
+    def work():
+        for _ in range(2):
+            codes.append(_lib.fa_bwd_score(*at, None, 1, 2, 2, 150, 64, 0.125, 1, _lib.Score(softcap=3.0), ws.data_ptr(), ws.numel(), None))
+            codes.append(cuda.cuCtxSetCurrent(None))
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert codes == [0, 0, 0, 0]
+    assert torch.equal(g[1], want[1]) and torch.equal(g[2], want[2])
 
 
 def test_python_refusals_on_the_device():
