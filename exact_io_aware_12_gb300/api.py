@@ -372,6 +372,27 @@ def last_device_error(device: Optional[torch.device] = None) -> int:
     return _lib.fa_last_device_error(_stream_handle(device))
 
 
+class _Once(torch.autograd.Function):
+    """Gradients as they are, from what they depend on: differentiating them raises."""
+
+    @staticmethod
+    def forward(ctx, n, *ts):
+        return tuple(t.view_as(t) for t in ts[:n])
+
+    @staticmethod
+    def backward(ctx, *gs):
+        raise RuntimeError("attention's gradients have no derivative")
+
+
+def _once(grads, *inputs):
+    """With create_graph, gradients that the kernels wrote (autograd would take them for constants, and a second
+    derivative would lack them without a word; torch's once_differentiable leaves them so where only saved tensors,
+    not the incoming gradient, depend on the leaves)."""
+    if not torch.is_grad_enabled():
+        return grads
+    return _Once.apply(len(grads), *grads, *inputs)
+
+
 class _Attention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, causal, tau, window, sinks):
@@ -383,8 +404,8 @@ class _Attention(torch.autograd.Function):
     @staticmethod
     def backward(ctx, do):
         q, k, v, o, lse = ctx.saved_tensors
-        dq, dk, dv = bwd(q, k, v, o, do.contiguous(), lse, ctx.causal, ctx.tau, window=ctx.window,
-                         sinks=ctx.sinks)
+        dq, dk, dv = _once(bwd(q, k, v, o, do.contiguous(), lse, ctx.causal, ctx.tau, window=ctx.window,
+                               sinks=ctx.sinks), q, k, v, do)
         return dq, dk, dv, None, None, None, None
 
 
@@ -401,9 +422,9 @@ class _ScoredAttention(torch.autograd.Function):
     def backward(ctx, do):
         q, k, v, o, lse, bias, slopes, buckets, docs, prefix = ctx.saved_tensors
         causal, tau, window, softcap = ctx.how
-        grads = bwd(q, k, v, o, do.contiguous(), lse, causal, tau, window=window, softcap=softcap,
-                    slopes=slopes, bias=bias, buckets=buckets, docs=docs, prefix=prefix,
-                    bias_grad=ctx.needs_input_grad[3])
+        grads = _once(bwd(q, k, v, o, do.contiguous(), lse, causal, tau, window=window, softcap=softcap,
+                          slopes=slopes, bias=bias, buckets=buckets, docs=docs, prefix=prefix,
+                          bias_grad=ctx.needs_input_grad[3]), q, k, v, do, bias)
         dbias = grads[3] if len(grads) > 3 else None
         return (*grads[:3], dbias, None, None, None, None, None, None, None, None)
 
@@ -415,7 +436,8 @@ def attention(q, k, v, causal: bool = False, tau: Optional[float] = None,
               prefix: Optional[torch.Tensor] = None) -> torch.Tensor:
     """O = softmax(tau Q K^T [causal]) V with autograd support; ``window`` and
     ``sinks``, and ``softcap`` to ``prefix``, as in ``fwd``.  Gradients flow to q, k, v and
-    ``bias`` (not to ``slopes``).  A backward pass may be captured in a CUDA graph while no
+    ``bias`` (not to ``slopes``), and have none of their own: with ``create_graph`` a second
+    derivative through them raises RuntimeError.  A backward pass may be captured in a CUDA graph while no
     eager graph of the same leaves lives (torch ties a leaf to the stream that it was first
     used on)."""
     if (softcap is not None or slopes is not None or bias is not None or buckets is not None

@@ -491,6 +491,17 @@ def test_autograd():
     assert api.last_device_error() == _lib.FA_OK
 
 
+@pytest.mark.parametrize("kw", [{}, dict(softcap=4.0), dict(window=30, sinks=2)])
+def test_second_derivatives_raise(kw):
+    x = {n: t.to(DEV) for n, t in inputs(1, 2, 2, 150, 64, 61).items()}
+    q = x["q"].requires_grad_()
+    want, = torch.autograd.grad(api.attention(q, x["k"], x["v"], True, **kw), q, x["do"])
+    g, = torch.autograd.grad(api.attention(q, x["k"], x["v"], True, **kw), q, x["do"], create_graph=True)
+    assert rel_l2(g.detach().cpu(), want.cpu()) < 1e-3  # (dQ's order of summation is free)
+    with pytest.raises(RuntimeError, match="no derivative"):
+        torch.autograd.grad(g.float().pow(2).sum() + q.float().sum(), q)
+
+
 def test_bias_gradient_only_on_request():
     x = {n: t.to(DEV) for n, t in inputs(1, 2, 2, 150, 64, 22).items()}
     t = dev(table_of(2, 16, 64, False, 4))

@@ -319,3 +319,34 @@ def test_python_checks():
         api.attention(x, x, x, True, slopes=torch.ones(2, requires_grad=True))
     with pytest.raises(TypeError):
         api.fwd(x, x, None, True, softcap=1.0)
+
+
+@pytest.mark.parametrize("how", ["plain", "capped", "biased"])
+def test_second_derivatives_raise(how, monkeypatch):
+    """The kernels' gradients are no constants: whatever of q, k, v, the bias or the incoming gradient they are
+    differentiated to, also beside terms that have a derivative.  (Calls of the library replaced by tensors.)"""
+    x = [torch.randn(1, 2, 4, 8, requires_grad=True) for _ in range(4)]
+    bias = torch.randn(3, 2, requires_grad=True)
+    monkeypatch.setattr(api, "fwd", lambda q, *a, **kw: (q.detach().clone(), torch.zeros(1, 2, 4)))
+    monkeypatch.setattr(api, "bwd", lambda q, k, v, *a, bias=None, **kw:
+                        tuple(t.detach().clone() for t in (q, k, v) + (() if bias is None else (bias,))))
+    kw = {"plain": {}, "capped": dict(softcap=2.0), "biased": dict(bias=bias, buckets=torch.zeros(3, dtype=torch.int32))}[how]
+    leaves = x[:3] + ([bias] if how == "biased" else [])
+    o = api.attention(*x[:3], True, **kw)
+    first = torch.autograd.grad(o, leaves, torch.ones_like(o), retain_graph=True)
+    assert all(torch.equal(g, t) and not g.requires_grad for g, t in zip(first, leaves))
+    for do in (torch.ones_like(o), x[3] * 2):
+        grads = torch.autograd.grad(o, leaves, do, create_graph=True)
+        for g, t in zip(grads, leaves):
+            assert torch.equal(g, t)
+            with pytest.raises(RuntimeError, match="no derivative"):
+                torch.autograd.grad(g.sum() + x[0].sum() + x[3].sum(), [x[0]], retain_graph=True)
+    # frozen inputs, and gradients that are only used
+    o = api.attention(x[0].detach(), x[1], x[2].detach(), True, **kw)
+    g, = torch.autograd.grad(o, x[1], torch.ones_like(o), create_graph=True)
+    with pytest.raises(RuntimeError, match="no derivative"):
+        torch.autograd.grad((g * x[1]).sum(), x[1])
+    x[1].grad = None
+    o = api.attention(*x[:3], True, **kw)
+    o.sum().backward(create_graph=True)
+    assert torch.equal(x[1].grad, x[1])
