@@ -196,6 +196,8 @@ def bwd(q, k, v, o, do, lse, causal: bool, tau: Optional[float] = None,
     ``score_workspace_bytes``): dK and dV have k's heads, summed over the query
     heads that share them.  With a ``bias`` its gradient, of its shape and type,
     comes fourth (in ``dbias`` where given), unless ``bias_grad`` is false."""
+    if dbias is not None and bias is None:
+        raise ValueError("dbias without a bias")
     if (softcap is not None or slopes is not None or bias is not None or buckets is not None
             or docs is not None or prefix is not None):
         if sinks or blocks is not None:
@@ -206,8 +208,6 @@ def bwd(q, k, v, o, do, lse, causal: bool, tau: Optional[float] = None,
                                          docs, prefix, window, dq, dk, dv, dbias if bias_grad else False,
                                          workspace)
         return grads if bias is not None and bias_grad else grads[:3]
-    if dbias is not None:
-        raise ValueError("dbias without a bias")
     if sinks:
         if window is None:
             raise ValueError("sinks need a window")

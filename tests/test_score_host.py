@@ -321,6 +321,13 @@ def test_python_checks():
         api.fwd(x, x, None, True, softcap=1.0)
 
 
+def test_a_bias_gradient_needs_a_bias():
+    x, i = torch.zeros(1, 2, 128, 64, dtype=torch.bfloat16), torch.zeros(1, 128, dtype=torch.int32)
+    for kw in (dict(softcap=1.0), dict(slopes=torch.ones(2)), dict(docs=i), dict(prefix=i[0, :1])):
+        with pytest.raises(ValueError, match="dbias without a bias"):
+            api.bwd(x, x, x, x, x, x, True, dbias=x, **kw)
+
+
 @pytest.mark.parametrize("how", ["plain", "capped", "biased"])
 def test_second_derivatives_raise(how, monkeypatch):
     """The kernels' gradients are no constants: whatever of q, k, v, the bias or the incoming gradient they are
