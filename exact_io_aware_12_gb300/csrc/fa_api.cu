@@ -771,9 +771,9 @@ size_t fa_paged_workspace_size(const fa_paged_cache* cache, int H, int Nq, int w
 struct ScoreBytes {
     size_t slopes, table, buckets, docs, prefix;
 };
-// Checks a fa_score for B sequences of N tokens (N = 0: of a cache, without documents or prefix)
+// Checks a fa_score for B sequences of N tokens (of a cache: without documents or prefix)
 // and H query heads, and fills the internal form (its window aside).
-static fa_status check_score(const fa_score* f, int B, int H, int N, ScoreMod* m, ScoreBytes* bytes) {
+static fa_status check_score(const fa_score* f, int B, int H, int N, bool cache, ScoreMod* m, ScoreBytes* bytes) {
     if (!(f->softcap == 0.f || (f->softcap >= 0x1p-20f && f->softcap <= 0x1p60f))) return FA_ERR_INVALID_ARG;
     if (f->bias_f32 != 0 && f->bias_f32 != 1) return FA_ERR_INVALID_ARG;
     if (f->window < 0) return FA_ERR_INVALID_ARG;
@@ -787,7 +787,7 @@ static fa_status check_score(const fa_score* f, int B, int H, int N, ScoreMod* m
         m->table_f32 = f->bias_f32 != 0;
     }
     if (!aligned4(f->slopes) || !aligned4(f->buckets) || !aligned4(f->docs) || !aligned4(f->prefix)) return FA_ERR_INVALID_ARG;
-    if (N == 0 && B == 0 && (f->docs != nullptr || f->prefix != nullptr)) return FA_ERR_INVALID_ARG;
+    if (cache && (f->docs != nullptr || f->prefix != nullptr)) return FA_ERR_INVALID_ARG;
     m->softcap = f->softcap;
     m->slopes = f->slopes;
     m->table = f->bias;
@@ -829,7 +829,7 @@ static fa_status paged_common(const fa_paged_cache* c, bool fp8, const void* Q, 
     const size_t sb = fp8 ? static_cast<size_t>(c->num_pages) * c->H_kv * 4 : 0;
     ScoreBytes mod{};
     if (score != nullptr) {
-        s = check_score(score, 0, H, 0, &a.mod, &mod);
+        s = check_score(score, 0, H, 0, true, &a.mod, &mod);
         if (s != FA_OK) return s;
     }
     const void* ins[] = {Q, c->K, c->V, c->page_table, c->lens, a.mod.slopes, a.mod.table, a.mod.buckets, c->k_scale,
@@ -932,7 +932,7 @@ static fa_status score_shape(int B, int H, int H_kv, int N, int d, float tau, in
     fa_status s = check_shape(B, H, N, d, tau, causal, empty);
     if (s != FA_OK) return s;
     if (H_kv == 0 ? H > 0 : H % H_kv != 0) return FA_ERR_INVALID_ARG;
-    s = check_score(score, B, H, N, &a->mod, mod);
+    s = check_score(score, B, H, N, false, &a->mod, mod);
     if (s != FA_OK) return s;
     if ((score->prefix != nullptr || score->window != 0) && !causal) return FA_ERR_INVALID_ARG;
     if (*empty) return FA_OK;

@@ -262,6 +262,12 @@ def test_keys_that_no_query_head_reads():
     assert calls(score(), H=0, N=0, dK=None) == calls(score(), H=0, B=0, dV=None) == (OK, OK)
 
 
+def test_documents_of_nothing():
+    """No sequences of no tokens are as empty with documents or a prefix as without."""
+    for f in (dict(docs=FAKE + 22 * GB), dict(prefix=FAKE + 22 * GB), TABLE):
+        assert calls(score(**f), B=0, N=0) == (OK, OK)
+
+
 def test_workspace_sizes():
     size = lambda B=2, H=4, N=300, d=64, causal=1, **f: _lib.fa_bwd_score_workspace_size(B, H, N, d, causal, score(**f))
     base = size()
