@@ -255,6 +255,7 @@ fa_score check_score(PyObject* const* a, int64_t H, const at::Device& dev) {
         require(buckets->dim() == 1 && buckets->size(0) % 2 == 1 && buckets->scalar_type() == at::kInt &&
                     buckets->device() == dev && buckets->is_contiguous(),
                 "buckets must be contiguous int32 [2 * max_distance + 1] on the queries' device");
+        if (H == 0) return s;  // (biases of no heads have no address)
         s.bias = bias->data_ptr();
         s.buckets = static_cast<const int*>(buckets->data_ptr());
         s.bias_f32 = bias->scalar_type() == at::kFloat;
@@ -485,7 +486,7 @@ PyObject* bwd_score(PyObject*, PyObject* const* a, Py_ssize_t n) {
             else g = &made[i].emplace(make(of.sizes(), at::kBFloat16, q.device()));
             grads[i] = g->data_ptr();
         }
-        const bool wanted = s.f.bias && a[18] != Py_False;
+        const bool wanted = a[10] != Py_None && a[18] != Py_False;
         if (wanted) {
             const at::Tensor *g = tensor_or_none(a[18], "dbias"), &bias = tensor(a[10], "bias");
             if (g)
@@ -493,7 +494,7 @@ PyObject* bwd_score(PyObject*, PyObject* const* a, Py_ssize_t n) {
                             g->is_contiguous(),
                         "dbias must be contiguous and like bias");
             else g = &made[3].emplace(make(bias.sizes(), bias.scalar_type(), q.device()));
-            grads[3] = g->data_ptr();
+            if (s.f.bias) grads[3] = g->data_ptr();
         }
         const at::Tensor* ws = workspace_of(a[19], g_bwd_score_workspace(s.B, s.H, s.N, s.d, causal, &s.f), q, made_ws);
         check_status(g_bwd_score(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), go.data_ptr(),

@@ -533,6 +533,18 @@ def test_keys_that_no_query_head_reads():
         assert g[0].shape == q.shape and not g[1].any() and not g[2].any()
 
 
+def test_a_bias_of_no_heads():
+    """As empty as a call without one."""
+    q, m = torch.empty(2, 0, 300, 64, dtype=BF, device=DEV), api.distance_buckets(16, 64, device=DEV)
+    bias = torch.empty(16, 0, device=DEV)
+    o, lse = api.fwd(q, q, q, True, bias=bias, buckets=m)
+    assert o.shape == q.shape and lse.shape == q.shape[:3]
+    g = api.bwd(q, q, q, o, o, lse, True, bias=bias, buckets=m)
+    assert len(g) == 4 and g[3].shape == bias.shape and g[3].dtype == bias.dtype
+    given = torch.empty_like(bias)
+    assert api.bwd(q, q, q, o, o, lse, True, bias=bias, buckets=m, dbias=given)[3] is given
+
+
 def test_side_stream_and_device_argument():
     """Inputs made on another stream, the call on a stream of its own."""
     x = inputs(1, 4, 4, 900, 128, 33)
