@@ -76,6 +76,7 @@ SIGNATURES = {
     "fa_fwd_score_workspace_size": (_SZ, [_I, _I, _S]),
     "fa_fwd_score": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _S, _P, _SZ, _P]),
     "fa_bwd_score_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _S]),
+    "fa_bwd_score_frozen_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _S]),
     "fa_bwd_score": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _S,
                           _P, _SZ, _P]),
     "fa_fwd_blocks": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _I, _P, _I, _P]),
@@ -257,6 +258,10 @@ def fa_fwd_score(Q, K, V, O, LSE, B, H, H_kv, N, d, tau, causal, score, workspac
 
 def fa_bwd_score_workspace_size(B, H, N, d, causal, score) -> int:
     return int(_call("fa_bwd_score_workspace_size", B, H, N, d, causal, score))
+
+
+def fa_bwd_score_frozen_workspace_size(B, H, N, d, causal, score) -> int:
+    return int(_call("fa_bwd_score_frozen_workspace_size", B, H, N, d, causal, score))
 
 
 def fa_bwd_score(Q, K, V, O, dO, LSE, dQ, dK, dV, dBias, B, H, H_kv, N, d, tau, causal, score,

@@ -167,16 +167,18 @@ def workspace_bytes(B: int, H: int, N: int, d: int) -> int:
 
 def score_workspace_bytes(q: torch.Tensor, causal: bool, bias: Optional[torch.Tensor] = None,
                           buckets: Optional[torch.Tensor] = None, docs: Optional[torch.Tensor] = None,
-                          prefix: Optional[torch.Tensor] = None, backward: bool = True) -> int:
+                          prefix: Optional[torch.Tensor] = None, backward: bool = True,
+                          bias_grad: bool = True) -> int:
     """Bytes of workspace that ``bwd`` (or ``fwd``) takes for queries of this size with
-    these options."""
+    these options (``bias_grad`` as in ``bwd``)."""
     B, H, N, d = q.shape
     at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     s = _lib.Score(0.0, None, at(bias), at(buckets), int(bias is not None and bias.dtype == torch.float32),
                    0 if bias is None else bias.shape[0], 0 if buckets is None else buckets.shape[0] // 2,
                    at(docs), at(prefix), 0)
     if backward:
-        return _lib.fa_bwd_score_workspace_size(B, H, N, d, int(bool(causal)), s)
+        size = _lib.fa_bwd_score_workspace_size if bias_grad else _lib.fa_bwd_score_frozen_workspace_size
+        return size(B, H, N, d, int(bool(causal)), s)
     return _lib.fa_fwd_score_workspace_size(B, N, s)
 
 

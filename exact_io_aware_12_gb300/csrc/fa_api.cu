@@ -954,12 +954,20 @@ size_t fa_fwd_score_workspace_size(int B, int N, const fa_score* score) {
     return score_fwd_workspace(B, N, score->docs != nullptr);
 }
 
-size_t fa_bwd_score_workspace_size(int B, int H, int N, int d, int causal, const fa_score* score) {
+static size_t score_bwd_bytes(int B, int H, int N, int d, int causal, const fa_score* score, bool grad) {
     ScoreArgs a;
     ScoreBytes mod;
     bool empty = false;
     if (score_shape(B, H, H, N, d, 1.f, causal, score, &a, &mod, &empty) != FA_OK || empty) return 0;
-    return score_bwd_workspace(a);
+    return score_bwd_workspace(a, grad);
+}
+
+size_t fa_bwd_score_workspace_size(int B, int H, int N, int d, int causal, const fa_score* score) {
+    return score_bwd_bytes(B, H, N, d, causal, score, true);
+}
+
+size_t fa_bwd_score_frozen_workspace_size(int B, int H, int N, int d, int causal, const fa_score* score) {
+    return score_bwd_bytes(B, H, N, d, causal, score, false);
 }
 
 fa_status fa_fwd_score(const void* Q, const void* K, const void* V, void* O, float* LSE, int B, int H,
@@ -1037,7 +1045,7 @@ fa_status fa_bwd_score(const void* Q, const void* K, const void* V, const void* 
     for (const void* p : ptrs)
         if (p == nullptr || !aligned16(p)) return FA_ERR_INVALID_ARG;
     if (workspace != nullptr && !aligned16(workspace)) return FA_ERR_INVALID_ARG;
-    const size_t need = score_bwd_workspace(a);
+    const size_t need = score_bwd_workspace(a, dBias != nullptr);
     if (workspace != nullptr && workspace_bytes < need) return FA_ERR_WORKSPACE;
     const size_t rows = static_cast<size_t>(B) * H * N, tb = rows * d * 2, kb = tb / H * H_kv;
     const Buffer bs[] = {{dQ, tb}, {dK, kb}, {dV, kb}, {dBias, mod.table}, {workspace, need}, {Q, tb}, {K, kb}, {V, kb},

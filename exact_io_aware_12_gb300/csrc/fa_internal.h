@@ -193,7 +193,7 @@ struct ScoreOrder {
     int* keys = nullptr;
 };
 size_t score_fwd_workspace(int B, int N, bool docs);
-size_t score_bwd_workspace(const ScoreArgs& a);
+size_t score_bwd_workspace(const ScoreArgs& a, bool grad);  // grad: with the table's
 
 // How the decode forward cuts the KV cache: `splits` chunks of `chunk` keys
 // (a multiple of 64).  Depends only on its arguments.

@@ -644,7 +644,8 @@ __global__ void __launch_bounds__(256) fa_score_table_kernel(const TableGradPara
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
-BwdPlan plan_of(const ScoreArgs& a) {
+// grad: with the parts of the table's gradient (4 KB per near tile pair and head, most of what such a call takes).
+BwdPlan plan_of(const ScoreArgs& a, bool grad) {
     BwdPlan pl;
     const size_t rows = static_cast<size_t>(a.B) * a.H * a.N;
     const int n_kv = (a.N + kBK - 1) / kBK;
@@ -655,13 +656,15 @@ BwdPlan plan_of(const ScoreArgs& a) {
     pl.bias2 = pl.order + (a.mod.docs ? up(static_cast<size_t>(a.B) * (n_kv + (n_kv + 1) / 2) * sizeof(int)) : 0);
     pl.near = pl.far = pl.red = pl.bytes = pl.bias2;
     if (!a.mod.table) return pl;
+    pl.near = pl.bias2 + up(static_cast<size_t>(a.H) * (2 * a.mod.far + 1) * sizeof(float));
+    pl.far = pl.red = pl.bytes = pl.near;
+    if (!grad) return pl;
     // (offsets that tiles have; behind the query only where a prefix, or no mask, shows such keys)
     const int n = std::min(near_tiles(a.mod.far, kBQ), n_kv - 1);
     pl.near_lo = a.causal && !a.mod.prefix ? 0 : -n;
     pl.near_n = n - pl.near_lo + 1;
     pl.warps = 4 * kNWG;
     const size_t tiles = static_cast<size_t>(a.B) * a.H * n_kv;
-    pl.near = pl.bias2 + up(static_cast<size_t>(a.H) * (2 * a.mod.far + 1) * sizeof(float));
     pl.far = pl.near + tiles * pl.near_n * kNearFloats * sizeof(float);
     pl.red = pl.far + up(tiles * pl.warps * kFarFloats * sizeof(float));
     pl.bytes = pl.red + up((static_cast<size_t>(pl.near_n) * kParts * a.H * a.mod.num_buckets + a.H * 2) * sizeof(float));
@@ -769,10 +772,10 @@ cudaError_t launch_all(const ScoreArgs& a, const BwdPlan& pl, cudaStream_t strea
 
 }  // namespace
 
-size_t score_bwd_workspace(const ScoreArgs& a) { return plan_of(a).bytes; }
+size_t score_bwd_workspace(const ScoreArgs& a, bool grad) { return plan_of(a, grad).bytes; }
 
 cudaError_t launch_score_bwd(const ScoreArgs& a, cudaStream_t stream) {
-    const BwdPlan pl = plan_of(a);
+    const BwdPlan pl = plan_of(a, a.dTable != nullptr);
     cudaError_t e = cudaSuccess;
     if (a.mod.docs) {
         ScoreOrder order;

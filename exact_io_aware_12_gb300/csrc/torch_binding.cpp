@@ -35,7 +35,7 @@ decltype(&fa_bwd_workspace_size) g_bwd_workspace;
 decltype(&fa_fwd_score) g_fwd_score;
 decltype(&fa_bwd_score) g_bwd_score;
 decltype(&fa_fwd_score_workspace_size) g_fwd_score_workspace;
-decltype(&fa_bwd_score_workspace_size) g_bwd_score_workspace;
+decltype(&fa_bwd_score_workspace_size) g_bwd_score_workspace[2];  // [whether a bias's gradient is wanted]
 decltype(&fa_fwd_paged_score) g_paged_score[2];
 PyObject* g_error = nullptr;  // FAError(code, where)
 PyObject* g_oom = nullptr;    // torch.OutOfMemoryError
@@ -496,7 +496,7 @@ PyObject* bwd_score(PyObject*, PyObject* const* a, Py_ssize_t n) {
             else g = &made[3].emplace(make(bias.sizes(), bias.scalar_type(), q.device()));
             if (s.f.bias) grads[3] = g->data_ptr();
         }
-        const at::Tensor* ws = workspace_of(a[19], g_bwd_score_workspace(s.B, s.H, s.N, s.d, causal, &s.f), q, made_ws);
+        const at::Tensor* ws = workspace_of(a[19], g_bwd_score_workspace[grads[3] != nullptr](s.B, s.H, s.N, s.d, causal, &s.f), q, made_ws);
         check_status(g_bwd_score(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), go.data_ptr(),
                                  static_cast<const float*>(lse.data_ptr()), grads[0], grads[1], grads[2], grads[3], s.B, s.H,
                                  s.H_kv, s.N, s.d, tau, causal, &s.f, ws ? ws->data_ptr() : nullptr, ws ? ws->nbytes() : 0,
@@ -529,7 +529,9 @@ PyObject* load(PyObject*, PyObject* const* a, Py_ssize_t n) {
         g_fwd_score = reinterpret_cast<decltype(&fa_fwd_score)>(find("fa_fwd_score"));
         g_bwd_score = reinterpret_cast<decltype(&fa_bwd_score)>(find("fa_bwd_score"));
         g_fwd_score_workspace = reinterpret_cast<decltype(&fa_fwd_score_workspace_size)>(find("fa_fwd_score_workspace_size"));
-        g_bwd_score_workspace = reinterpret_cast<decltype(&fa_bwd_score_workspace_size)>(find("fa_bwd_score_workspace_size"));
+        g_bwd_score_workspace[0] =
+            reinterpret_cast<decltype(&fa_bwd_score_workspace_size)>(find("fa_bwd_score_frozen_workspace_size"));
+        g_bwd_score_workspace[1] = reinterpret_cast<decltype(&fa_bwd_score_workspace_size)>(find("fa_bwd_score_workspace_size"));
         g_paged_score[0] = reinterpret_cast<decltype(&fa_fwd_paged_score)>(find("fa_fwd_paged_score"));
         g_paged_score[1] = reinterpret_cast<decltype(&fa_fwd_paged_score)>(find("fa_fwd_paged_score_fp8"));
         Py_XDECREF(g_error);

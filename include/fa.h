@@ -278,10 +278,13 @@ FA_API fa_status fa_fwd_score(const void* Q, const void* K, const void* V, void*
  * written; buckets of no visible pair get 0), or NULL: not computed.  It is summed in fp32 in a
  * fixed order and rounded once, of weights in fp32 or, with a cap, off by at most 2^-11 of
  * themselves down to 2^-29.  (dQ's order of summation is not fixed, as in fa_bwd.)
- * workspace: fa_bwd_score_workspace_size bytes; NULL as in fa_fwd_score.
+ * workspace: fa_bwd_score_workspace_size bytes, or fa_bwd_score_frozen_workspace_size where
+ * dBias is NULL (the same without a bias); NULL as in fa_fwd_score.
  */
 FA_API size_t fa_bwd_score_workspace_size(int B, int H, int N, int d, int causal,
                                           const fa_score* score);
+FA_API size_t fa_bwd_score_frozen_workspace_size(int B, int H, int N, int d, int causal,
+                                                 const fa_score* score);
 FA_API fa_status fa_bwd_score(const void* Q, const void* K, const void* V, const void* O,
                               const void* dO, const float* LSE, void* dQ, void* dK, void* dV,
                               void* dBias, int B, int H, int H_kv, int N, int d, float tau,

@@ -491,6 +491,25 @@ def test_autograd():
     assert api.last_device_error() == _lib.FA_OK
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_frozen_bias_in_its_workspace(d):
+    """Without the gradient, in a workspace of that size with a border behind it: dK and dV bit for bit the same."""
+    x = {n: t.to(DEV) for n, t in inputs(2, 4, 2, 700, d, 23).items()}
+    t = dev(table_of(4, 32, 128, True, 4))
+    for kw in (dict(t), dict(t, softcap=20.0), dict(t, docs=docs_of(2, 700, 3).to(DEV))):
+        o, lse = api.fwd(x["q"], x["k"], x["v"], False, **kw)
+        all4 = api.bwd(x["q"], x["k"], x["v"], o, x["do"], lse, False, **kw)
+        size = api.score_workspace_bytes(x["q"], False, t["bias"], t["buckets"], kw.get("docs"), bias_grad=False)
+        space = torch.full((size + 4096,), 0xff, dtype=torch.uint8, device=DEV)
+        three = api.bwd(x["q"], x["k"], x["v"], o, x["do"], lse, False, bias_grad=False, workspace=space[:size], **kw)
+        assert bool((space[size:] == 0xff).all())
+        assert torch.equal(all4[1], three[1]) and torch.equal(all4[2], three[2])
+        assert rel_l2(three[0].cpu(), all4[0].cpu()) < 2.0 ** -8  # (dQ's order of summation is free)
+        with pytest.raises(_lib.FAError) as err:
+            api.bwd(x["q"], x["k"], x["v"], o, x["do"], lse, False, workspace=space[:size], **kw)
+        assert err.value.code == _lib.FA_ERR_WORKSPACE
+
+
 @pytest.mark.parametrize("kw", [{}, dict(softcap=4.0), dict(window=30, sinks=2)])
 def test_second_derivatives_raise(kw):
     x = {n: t.to(DEV) for n, t in inputs(1, 2, 2, 150, 64, 61).items()}

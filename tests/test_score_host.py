@@ -290,6 +290,26 @@ def test_workspace_sizes():
     assert api.score_workspace_bytes(q, True, torch.zeros(32, 4), m) == size(**dict(TABLE, max_distance=m.numel() // 2))
 
 
+def test_a_frozen_bias_takes_no_workspace_for_its_gradient():
+    """Without dBias the call takes what it takes without a bias, and the biases by distance."""
+    frozen = lambda **f: _lib.fa_bwd_score_frozen_workspace_size(2, 4, 3000, 64, 0, score(**f))
+    whole = lambda **f: _lib.fa_bwd_score_workspace_size(2, 4, 3000, 64, 0, score(**f))
+    assert frozen() == whole() and frozen(docs=FAKE) == whole(docs=FAKE)
+    t = dict(TABLE, max_distance=1024)
+    assert whole() < frozen(**t) <= whole() + 4 * 2049 * 4 + 512
+    assert whole(**t) > frozen(**t) + 2 * 4 * 24 * 17 * 4096
+    assert _lib.fa_bwd_score_frozen_workspace_size(2, 4, 300, 96, 1, score()) == 0
+    a = dict(B=2, H=4, H_kv=4, N=3000, d=64, causal=0)
+    n = frozen(**t)
+    assert calls(score(**t), ws_bytes=n - 1, **a)[1] == WS and calls(score(**t), ws_bytes=n, dBias=FAKE + 23 * GB, **a)[1] == WS
+    # (refused for its workspace's place, not for its size)
+    assert calls(score(**t), ws=FAKE + 6 * GB, ws_bytes=n, **a)[1] == BAD
+    q = torch.empty(2, 4, 3000, 64, dtype=torch.bfloat16)
+    m = torch.zeros(2049, dtype=torch.int32)
+    assert api.score_workspace_bytes(q, False, torch.zeros(32, 4), m, bias_grad=False) == n
+    assert api.score_workspace_bytes(q, False, torch.zeros(32, 4), m) == whole(**t)
+
+
 def test_paged_refusals():
     cache = _lib.PagedCache(FAKE, FAKE + GB, None, None, FAKE + 4 * GB, FAKE + 5 * GB, 2, 2, 64, 8, 16, 4)
 
