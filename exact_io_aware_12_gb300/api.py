@@ -84,8 +84,6 @@ def distance_buckets(num_buckets: int, max_distance: int, bidirectional: bool = 
                                  >= max_distance ** (b + 1 - exact) * exact ** log_n):
                 b += 1
         past.append(min(b, n - 1))
-    if len(past) == 1:  # (one bucket a side)
-        past.append(past[0])
     future = [n + x for x in past[:0:-1]] if bidirectional else [0] * (len(past) - 1)
     return torch.tensor(future + past, dtype=torch.int32, device=device)
 
