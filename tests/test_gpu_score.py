@@ -358,6 +358,24 @@ def test_more_tiles_than_the_sms_hold(kw, d):
 
 
 @pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N,scale,kw", [
+    (8200, 1.5, dict(softcap=50.0, window=4096)), (4200, 1.5, dict(softcap=50.0)), (4200, 1.0, dict(slopes=True)),
+    (4200, 1.0, dict(table=(32, 128, False))), (4200, 1.5, dict(softcap=30.0, prefix=True)), (4200, 1.0, dict(softcap=20.0, table=(32, 128, False)))],
+    ids=str)
+def test_long_sequences(N, scale, kw, d):
+    """Tens of blocks per tile, most of them wholly visible and far from the diagonal: element by element as the
+    short ones."""
+    kw, H = dict(kw), 1 if N > 5000 else 2
+    if kw.get("slopes"):
+        kw["slopes"] = slopes_of(H)
+    if "table" in kw:
+        kw.update(table_of(H, *kw.pop("table"), 5))
+    if kw.get("prefix"):
+        kw["prefix"] = torch.tensor([N // 3], dtype=torch.int32)
+    check(inputs(1, H, 1, N, d, N + d, scale), True, **kw)
+
+
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("N,H,Hkv", [(300, 52, 52), (100, 170, 170), (260, 120, 40)])
 @pytest.mark.parametrize("kw", [
     dict(softcap=5.0), dict(slopes=True, docs=True), dict(table=(32, 128, False)), dict(softcap=20.0, table=(8, 40, True), docs=True),
