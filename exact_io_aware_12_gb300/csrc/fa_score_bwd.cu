@@ -24,7 +24,8 @@
 //
 // dX enters the products as bf16, rounded once from fp32; where registers are short, P (1 - tanh^2) waits for
 // dP^T as fp16 of 2^15 times its value, which is off by 2^-11 of it down to 2^-29; dQ, dK, dV take
-// the factor off.
+// the factor off.  With a cap and a table P itself, which dY takes, waits in the same form in tensor memory, in the
+// columns that dX^T (d = 64: dQ) takes later.
 //
 // The bias's gradient: pairs at one distance lie on a diagonal.  A tile pair all of whose
 // distances are `far` or more (most of them in a long sequence: the last bucket begins near)

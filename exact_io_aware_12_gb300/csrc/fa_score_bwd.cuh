@@ -116,7 +116,7 @@ struct BwdRow {
 };
 
 // Of one row's scores with queries [q0, q0 + 32): P as bf16 pairs (pk), and P (1 - tanh^2), what dP is to
-// be multiplied by, as fp16 pairs (keep).  With a cap and a table, whose gradient takes P itself, P as fp16 pairs, too
+// be multiplied by, as fp32 or, where keep_regs gives half the registers, as fp16 pairs (keep).  With a cap and a table, whose gradient takes P itself, P as fp16 pairs, too
 // (pw).  nl4: the queries' 15 - LSE log2(e).
 template <int CAP, int BIAS>
 __device__ __forceinline__ void bwd_weights(const ScoreBwdParams& p, const BwdRow& r, const uint32_t (&sv)[32], const ulonglong2* nl4,

@@ -332,8 +332,8 @@ fa_score_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_consta
                                                                         : kTanhExp;
                     // (once one of a warp's blocks has needed a farther form, those behind it take it, too: warps that go
                     // to and fro between the forms wait for instructions, 292 -> 351 us where a third of the blocks
-                    // passed a bound.  The last form's error is 2^-24 of the cap, whatever the score: not where caps are
-                    // in the thousands.)
+                    // passed a bound.  The last form is off by a part of the cap, whatever the score (fa_score.cuh): not
+                    // where caps are in the thousands.)
                     if (how > most) most = how;
                     else if (most == kTanhPoly4 || CAP == kCapCommon) how = most;
                     if (BIAS == kBiasNone && !masked) {

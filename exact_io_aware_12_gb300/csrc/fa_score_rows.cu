@@ -10,10 +10,10 @@
 // the error is fp32's.
 //
 // Design: one CTA per pair of 128-row query tiles of a head.  Warp 16 streams K_j and V_j by TMA,
-// warp 17 issues S_t = Q_t K_j^T and dP_t = dO_t V_j^T (tcgen05; all 512 tensor-memory columns), and four
-// warpgroups, two to a tile with half of its columns each, add p * dP, a row per thread: no
-// maximum, no second product, LSE being known.  One tile's elementwise work runs beside the
-// other's products: 16 heads of 8192 tokens, window 4096 and 8 key heads at d = 128, capped, 185 us (tensor
+// warp 17 (d = 128: 17 for one tile, 18 for the other) issues S_t = Q_t K_j^T and dP_t = dO_t V_j^T (tcgen05; all 512
+// tensor-memory columns), and four warpgroups, two to a tile with half of its columns each, add
+// p * dP, a row per thread: no maximum, no second product, LSE being known.  One tile's
+// elementwise work runs beside the other's products: 16 heads of 8192 tokens, window 4096 and 8 key heads at d = 128, capped, 185 us (tensor
 // pipe 51%); 96 heads of 1024 tokens with slopes, d = 64, 33.
 #include <cuda_bf16.h>
 
