@@ -115,7 +115,8 @@ def fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool,
                number below 0 is padding, which sees nothing and nothing sees
       prefix   int32 [B], with ``causal``: the first prefix[b] positions are
                visible from before them, too
-    The workspace (only documents take one) is allocated with torch when not given."""
+    Values are finite, in padding and behind a mask, too.  The workspace (only
+    documents take one) is allocated with torch when not given."""
     if (softcap is not None or slopes is not None or bias is not None or buckets is not None
             or docs is not None or prefix is not None):
         if o_fp32 or sinks or blocks is not None:
