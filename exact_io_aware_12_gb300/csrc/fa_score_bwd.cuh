@@ -99,7 +99,8 @@ constexpr int kQC = 128 / kNWG;
 constexpr int kThreads = 32 * (4 * kNWG + 3);
 
 // P (1 - tanh^2) waits for dP as fp32, or as fp16 (off by 2^-11 of it down to 2^-29, being lifted by 2^15) where a cap and
-// a bias leave no registers: 16 of 96 a thread.  (fp32 saves the conversions: 16 heads of 8192 tokens, window 4096, d = 128
+// a bias leave no registers: 16 of 96 a thread.  (Cut to fp16's largest, a P of 2: beside scores of 2^21, which fp32 holds to
+// 2^-3, P comes out above 1, and infinite it made dQ and dK NaN.)  (fp32 saves the conversions: 16 heads of 8192 tokens, window 4096, d = 128
 // 636 -> 628 us, slopes at d = 64 448 -> 427.)
 constexpr int keep_regs(int cap, int bias) { return cap != kCapNone && bias != kBiasNone ? 16 : 32; }
 
@@ -166,7 +167,7 @@ __device__ __forceinline__ void bwd_weights(const ScoreBwdParams& p, const BwdRo
             if (static_cast<uint32_t>(q + 1 - from) >= r.seen) p1 = 0.f;
         }
         pk[i] = pack_bf16(p0, p1);
-        if constexpr (CAP && BIAS == kBiasTable) pw[i] = pack_f16(p0, p1);
+        if constexpr (CAP && BIAS == kBiasTable) pw[i] = pack_f16_sat(p0, p1);
         if constexpr (CAP) {  // (tanh^2 - 1: dX, dK and dQ come with their sign turned)
             const float2 k = f2_unpack(fmul2(f2_pack(p0, p1), ffma2(th, th, f2_pack(-1.f, -1.f))));
             p0 = k.x;
@@ -176,7 +177,7 @@ __device__ __forceinline__ void bwd_weights(const ScoreBwdParams& p, const BwdRo
             keep[2 * i] = __float_as_uint(p0);
             keep[2 * i + 1] = __float_as_uint(p1);
         } else {
-            keep[i] = pack_f16(p0, p1);
+            keep[i] = pack_f16_sat(p0, p1);
         }
     };
     const auto all = [&](auto how, auto general_) {

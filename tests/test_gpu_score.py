@@ -280,6 +280,20 @@ def test_small_scores_beside_scores_of_a_large_cap(causal, d):
     assert float((lse.cpu().double() - e.lse)[:, :, ::2].abs().max()) < 1e-4
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bias", ["none", "slopes", "table"])
+@pytest.mark.parametrize("grow", [2.0 ** 8, 2.0 ** 10, 2.0 ** 12])
+def test_scores_that_fp32_holds_coarsely(grow, bias, d):
+    """Scores of 2^19 to 2^23 under a larger cap: their fp32 steps are 2^-4 to 1, so weights may be off by as many
+    powers of e, but stay finite, and so do all gradients."""
+    x = inputs(1, 2, 2, 300, d, 14)
+    x["q"], x["k"] = (x["q"].float() * grow).to(BF), (x["k"].float() * 2.0 ** 8).to(BF)
+    kw = {"none": {}, "slopes": dict(slopes=slopes_of(2)), "table": table_of(2, 32, 128, False, 3, torch.float32)}[bias]
+    o, lse, grads = gpu(x, True, 1.0, softcap=2.0 ** 40, **kw)
+    for t in (o, lse, *grads):
+        assert bool(t.isfinite().all())
+
+
 def test_other_scales_of_scores():
     x = inputs(1, 2, 2, 200, 64, 8)
     for tau in (1e-3, 1.0, 4.0):
